@@ -438,6 +438,92 @@ int txl_rel_attn_table_path(int B, int L, int H, int D, int max_len,
                             const txl_view* out, txl_dtype dtype);
 
 /*
+ * Quantised K/V memory: the FIFO memory of txl_mem with its keys and values held as 4- or 8-bit
+ * codes (a service of this library; the pages hold the memory in the compute type).  The channels
+ * of a head are split into groups of 32 consecutive d (G = ceil(D/32); the last group is shorter
+ * when D is not a multiple of 32).  With n = 2^bits - 1, a group x of one position is held as
+ *     lo   = the largest bf16 that is not above min(x)
+ *     step = the smallest bf16 that is not below (max(x) - lo) / n
+ *     c_d  = the integer nearest to (x_d - lo) / step, ties to even (0 where step = 0)
+ * and stands for x'_d = lo + step * c_d, so |x'_d - x_d| <= step / 2.  These definitions are met
+ * exactly, whatever the input type.  A group with a NaN or an infinity, or one whose lo, step or
+ * max - lo is not finite, is held with step = lo = NaN and stands for NaN throughout.
+ *   k, v : device, 16-byte aligned, dense [B][H][M][G * 4 * bits] bytes.  The bytes of a row hold
+ *          the codes in the order of d (4 bits: byte t holds d = 2t in its low and d = 2t + 1 in
+ *          its high half); codes of d >= D in the last group are 0.
+ *   par  : device, 16-byte aligned, dense bf16 [B][H][M][G][4]: the k step, k lo, v step and v lo
+ *          of each group.
+ *   bits : 4 or 8.  D <= 128.
+ *   wp, valid : as in txl_mem (logical key j in slot (wp + j) mod M, valid iff j >= M - valid).
+ * Slots that are not valid are never read, so the arrays need no initial values.  M = 0 means no
+ * memory (the pointers may then be NULL).  Heads and batch entries are contiguous in M so that a
+ * head's keys stream from memory.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    void* par;
+    int B, M, H, D;
+    int bits;
+    int wp;
+    int valid;
+} txl_qmem;
+
+/* Bytes of each of the k and v arrays, and of the par array, of a quantised memory (0 for an empty
+ * or invalid shape). */
+size_t txl_qmem_code_bytes(int B, int M, int H, int D, int bits);
+size_t txl_qmem_par_bytes(int B, int M, int H, int D);
+
+/*
+ * txl_qmem_push -- txl_mem_push into a quantised memory: quantises k_new/v_new [B][L][H][D] (device
+ * views of dtype) into slots (wp + t) mod M for t = max(0, L-M) .. L-1, then updates mem->wp and
+ * mem->valid on the host at enqueue time.  Other slots are left as they were.  Any strides; rows
+ * that start on 16-byte boundaries are read 16 bytes at a time.
+ */
+txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v_new, int L,
+                         txl_dtype dtype, void* stream);
+
+/*
+ * txl_qmem_read -- what the memory stands for: logical positions j0 .. j0+n-1 (oldest first; all of
+ * them valid: M - valid <= j0, j0 + n <= M, TXL_ERR_INVALID_ARG otherwise) into views k_out, v_out
+ * of [B][n][H][D], dtype, each value rounded once to it.  Only d < D is written.
+ */
+txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_out,
+                         const txl_view* v_out, txl_dtype dtype, void* stream);
+
+/*
+ * txl_rel_attn_qmem -- txl_rel_attn_fwd with the memory's keys and values held in a txl_qmem: the
+ * same scores, mask, clamp and softmax over k'_j, v'_j = what the memory stands for, and the current
+ * segment's k_cur, v_cur as they are.  Arguments as txl_rel_attn_fwd (mem may be NULL), plus
+ *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_qmem_workspace_size(B, L,
+ *            H, D, mem, dtype) bytes (TXL_ERR_WORKSPACE otherwise; may be NULL when that is 0).
+ *            Calls that share a workspace must not overlap on the GPU.
+ * L <= 16 (generation): one launch, the codes expanded on chip; no workspace.  L > 16: the memory's
+ * valid positions are read back into the workspace once (in dtype) and txl_rel_attn_fwd's kernels
+ * run over it; err_flag is used by those.  Enqueues one launch, or two.
+ */
+txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len,
+                             const txl_view* q, const txl_qmem* mem,
+                             const txl_view* k_cur, const txl_view* v_cur,
+                             const float* u, const float* v_bias,
+                             const void* r, int64_t ld_r, int n_rows,
+                             float scale, const txl_view* out, txl_dtype dtype,
+                             void* workspace, size_t workspace_bytes,
+                             int* err_flag, void* stream);
+
+/* Bytes of device workspace txl_rel_attn_qmem needs: 0 for L <= 16 or without a memory, else the
+ * bytes of M positions of keys and values in dtype, D rounded up to a multiple of 8. */
+size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype);
+
+/* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the kernel that expands the
+ * codes on chip (L <= 16), 1 or 2 = the memory read back, then the kernel of txl_rel_attn_path, or a
+ * negative txl_status if the arguments are rejected.  Nothing is launched; the workspace is not
+ * checked. */
+int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem,
+                           const txl_view* k_cur, const txl_view* v_cur, const void* r,
+                           int64_t ld_r, const txl_view* out, txl_dtype dtype);
+
+/*
  * Checked build.  libtxl_checked.so is this library compiled with -DTXL_CHECKED (the package builds
  * it on request: transformer_xl_relative_gb300/_build.py --checked; the binding loads it when the
  * environment variable TXL_CHECKED is 1).  Its kernels range-check the indices they compute before

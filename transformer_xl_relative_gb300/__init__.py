@@ -7,8 +7,11 @@ Importing the package loads the library and fails loudly if it has not been buil
 from . import native
 from .api import (  # noqa: F401
     Memory,
+    QuantMemory,
     linear,
     mem_push,
+    qmem_push,
+    qmem_read,
     rel_attn_bwd,
     rel_attn_bwd_path,
     rel_attn_decode,
@@ -20,6 +23,9 @@ from .api import (  # noqa: F401
     rel_attn_layer_fused,
     rel_attn_layer_fused_workspace_size,
     rel_attn_path,
+    rel_attn_qmem,
+    rel_attn_qmem_path,
+    rel_attn_qmem_workspace_size,
     rel_attn_table_fwd,
     rel_attn_table_path,
     rel_pos_bwd,

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import native
-from .native import TxlMem, TxlView, check
+from .native import TxlMem, TxlQmem, TxlView, check
 
 _DTYPES = {torch.float32: native.TXL_F32, torch.bfloat16: native.TXL_BF16}
 
@@ -43,6 +43,22 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+class _on:
+    """Makes `device` current for a call when it is not (the library launches on the current device)."""
+
+    def __init__(self, device):
+        self._to = device.index
+
+    def __enter__(self):
+        self._from = torch.cuda.current_device()
+        if self._to is not None and self._to != self._from:
+            torch.cuda.set_device(self._to)
+
+    def __exit__(self, *exc):
+        if self._to is not None and self._to != self._from:
+            torch.cuda.set_device(self._from)
 
 
 class Memory:
@@ -387,6 +403,161 @@ def rel_attn_table_path(q, k, v, r_table, max_len: int, out, key_mask=None) -> i
     return _lib().txl_rel_attn_table_path(
         B, L, H, D, int(max_len), ctypes.byref(vq), ctypes.byref(vk), ctypes.byref(vv), r_table.data_ptr(),
         r_table.stride(1), key_mask.data_ptr() if key_mask is not None else None, ctypes.byref(vo), dtype_code(q))
+
+
+class QuantMemory:
+    """K/V memory of M positions per batch entry held as 4- or 8-bit codes (txl_qmem): groups of 32
+    channels of a head share a bf16 step and minimum.  ``k`` and ``v`` are uint8 [B, H, M, row bytes],
+    ``par`` bf16 [B, H, M, groups, 4]; ``wp``/``valid`` as in Memory.  Filled by qmem_push, read by
+    rel_attn_qmem and qmem_read."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, par: torch.Tensor, D: int, bits: int, wp: int = 0,
+                 valid: int = 0):
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
+        if not 1 <= D <= 128:
+            raise ValueError("D must be in 1..128")
+        if k.dim() != 4:
+            raise ValueError("k and v must be uint8 [B, H, M, row bytes]")
+        B, H, M, _ = k.shape
+        G = (D + 31) // 32
+        for t, shape, dtype in ((k, (B, H, M, 4 * G * bits), torch.uint8), (v, (B, H, M, 4 * G * bits), torch.uint8),
+                                (par, (B, H, M, G, 4), torch.bfloat16)):
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("a quantised memory holds contiguous uint8 k, v %s and bf16 par %s on one device"
+                                 % ((B, H, M, 4 * G * bits), (B, H, M, G, 4)))
+        if not k.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        self.k, self.v, self.par = k, v, par
+        self._c = TxlQmem(k.data_ptr() if M else None, v.data_ptr() if M else None, par.data_ptr() if M else None,
+                          B, M, H, D, bits, int(wp), int(valid))
+
+    @classmethod
+    def empty(cls, B, M, H, D, bits=4, device="cuda"):
+        G = (D + 31) // 32
+        code = [torch.zeros(B, H, M, 4 * G * bits, dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*code, torch.zeros(B, H, M, G, 4, dtype=torch.bfloat16, device=device), D, bits)
+
+    @property
+    def M(self) -> int:
+        return self._c.M
+
+    @property
+    def wp(self) -> int:
+        return self._c.wp
+
+    @property
+    def valid(self) -> int:
+        return self._c.valid
+
+    def state(self):
+        """Host ring state (wp, valid): with the buffers, everything needed to resume."""
+        return self._c.wp, self._c.valid
+
+    def restore(self, wp: int, valid: int) -> None:
+        self._c.wp, self._c.valid = int(wp), int(valid)
+
+    @property
+    def c_struct(self) -> TxlQmem:
+        return self._c
+
+
+def _qmem_kv(mem: QuantMemory, k: torch.Tensor, v: torch.Tensor, T: int) -> None:
+    c = mem.c_struct
+    for t in (k, v):
+        if t.shape != (c.B, T, c.H, c.D):
+            raise ValueError("expected [B, T, H, D] = %s, got %s" % ((c.B, T, c.H, c.D), tuple(t.shape)))
+        if t.device != mem.k.device:
+            raise ValueError("tensors must live on the memory's device")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share a dtype")
+
+
+def qmem_push(mem: QuantMemory, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> QuantMemory:
+    """Quantise k_new/v_new [B, L, H, D] into the FIFO memory (txl_qmem_push)."""
+    L = k_new.shape[1]
+    _qmem_kv(mem, k_new, v_new, L)
+    vk, vv = view(k_new), view(v_new)
+    with _on(k_new.device):
+        st = _lib().txl_qmem_push(ctypes.byref(mem.c_struct), ctypes.byref(vk), ctypes.byref(vv), L,
+                                  dtype_code(k_new), _stream(stream))
+    check(st, "txl_qmem_push")
+    return mem
+
+
+def qmem_read(mem: QuantMemory, j0: int, n: int, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
+    """What the memory's logical positions j0 .. j0+n-1 (oldest first, all valid) stand for, into
+    k_out/v_out [B, n, H, D] (txl_qmem_read)."""
+    _qmem_kv(mem, k_out, v_out, n)
+    vk, vv = view(k_out), view(v_out)
+    with _on(k_out.device):
+        st = _lib().txl_qmem_read(ctypes.byref(mem.c_struct), int(j0), int(n), ctypes.byref(vk), ctypes.byref(vv),
+                                  dtype_code(k_out), _stream(stream))
+    check(st, "txl_qmem_read")
+    return k_out, v_out
+
+
+def rel_attn_qmem_workspace_size(q: torch.Tensor, mem: QuantMemory | None) -> int:
+    """Bytes of workspace rel_attn_qmem needs (txl_rel_attn_qmem_workspace_size): 0 for up to 16 queries."""
+    B, L, H, D = q.shape
+    memc = ctypes.byref(mem.c_struct) if mem is not None else None
+    return int(_lib().txl_rel_attn_qmem_workspace_size(B, L, H, D, memc, dtype_code(q)))
+
+
+def _qattn_check(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out):
+    B, L, H, D = q.shape
+    dtype, device = q.dtype, q.device
+    for t in (k_cur, v_cur, out):
+        if t.shape != q.shape or t.dtype != dtype or t.device != device:
+            raise ValueError("q, k_cur, v_cur and out must share shape, dtype and device")
+    for t in (u, v_bias):
+        if t.dtype != torch.float32:
+            raise TypeError("u and v_bias are fp32 [H, D]")
+        if t.shape != (H, D) or not t.is_contiguous() or t.device != device:
+            raise ValueError("u and v_bias must be contiguous [H, D] on the queries' device")
+    if (r.dim() != 3 or r.dtype != dtype or r.device != device or r.shape[0] < n_rows or r.shape[1] != H
+            or r.shape[2] < D or r.stride(2) != 1 or (r.shape[0] > 1 and r.stride(0) != H * r.stride(1))):
+        raise ValueError("r must be [n_rows, H, ld_r] of the queries' dtype and device, rows H * ld_r apart")
+    if mem is not None and mem.k.device != device:
+        raise ValueError("tensors must live on the memory's device")
+
+
+def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor, v_cur: torch.Tensor,
+                  u: torch.Tensor, v_bias: torch.Tensor, r: torch.Tensor, n_rows: int, clamp_len: int,
+                  out: torch.Tensor, scale: float = 0.0, workspace: torch.Tensor | None = None,
+                  err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Relative attention over [quantised memory ++ current segment] (txl_rel_attn_qmem).  Without
+    `workspace`, a device buffer of the required size (none for up to 16 queries) is taken from
+    torch's allocator for the call."""
+    _qattn_check(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out)
+    B, L, H, D = q.shape
+    memc = ctypes.byref(mem.c_struct) if mem is not None else None
+    vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)
+    if workspace is None and L > 16:
+        # from the pool of the stream that will use it, so that it is not reused before it has been
+        with torch.cuda.stream(stream) if stream is not None else _on(q.device):
+            need = rel_attn_qmem_workspace_size(q, mem)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    wp, nbytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
+        else (None, 0)
+    with _on(q.device):
+        st = _lib().txl_rel_attn_qmem(
+            B, L, H, D, int(clamp_len), ctypes.byref(vq), memc, ctypes.byref(vk), ctypes.byref(vv),
+            u.data_ptr(), v_bias.data_ptr(), r.data_ptr(), r.stride(1), int(n_rows), float(scale),
+            ctypes.byref(vo), dtype_code(q), wp, nbytes,
+            err_flag.data_ptr() if err_flag is not None else None, _stream(stream))
+    check(st, "txl_rel_attn_qmem")
+    return out
+
+
+def rel_attn_qmem_path(q, mem, k_cur, v_cur, r, out) -> int:
+    """5 = the kernel that expands the codes on chip (up to 16 queries), 1 or 2 = the memory read back,
+    then the kernel of rel_attn_path (txl_rel_attn_qmem_path)."""
+    B, L, H, D = q.shape
+    memc = ctypes.byref(mem.c_struct) if mem is not None else None
+    vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)
+    return _lib().txl_rel_attn_qmem_path(B, L, H, D, ctypes.byref(vq), memc, ctypes.byref(vk), ctypes.byref(vv),
+                                         r.data_ptr(), r.stride(1), ctypes.byref(vo), dtype_code(q))
 
 
 def selftest_wait_timeout(err_flag: torch.Tensor, timeout_us: int, stream=None) -> None:

@@ -1024,6 +1024,200 @@ int txl_rel_attn_decode_path(int B, int L, int H, int D, const txl_view* q, cons
     return decode_takes_fused(B, L, H, D, q, mem, k_cur, v_cur, r, ld_r, dtype) ? 1 : 4;
 }
 
+namespace {
+
+// A quantised memory's shape, pointers and ring state.
+txl_status check_qmem(const txl_qmem* m)
+{
+    if (m->B < 0 || m->M < 0 || m->H <= 0 || m->D <= 0) return TXL_ERR_INVALID_ARG;
+    if (m->D > 128 || (m->bits != 4 && m->bits != 8)) return TXL_ERR_UNSUPPORTED;
+    if (m->M == 0) return m->valid == 0 ? TXL_OK : TXL_ERR_INVALID_ARG;
+    if (!m->k || !m->v || !m->par) return TXL_ERR_INVALID_ARG;
+    if (m->wp < 0 || m->wp >= m->M || m->valid < 0 || m->valid > m->M) return TXL_ERR_INVALID_ARG;
+    if (!a16(m->k) || !a16(m->v) || !a16(m->par)) return TXL_ERR_ALIGNMENT;
+    if (m->B > 65535 || m->H > 65535) return TXL_ERR_UNSUPPORTED;
+    return TXL_OK;
+}
+
+inline int q_groups(int D) { return (D + kQGroup - 1) / kQGroup; }
+
+QmemParams qmem_params(const txl_qmem* m, const txl_view* xk, const txl_view* xv, txl_dtype dtype)
+{
+    const int elem = dtype == TXL_F32 ? 4 : 2;
+    auto rows16 = [&](const txl_view* v) {
+        return a16(v->ptr) && s16(v->stride_b, elem) && s16(v->stride_t, elem) && s16(v->stride_h, elem);
+    };
+    QmemParams p{};
+    p.xk = xk->ptr; p.xk_sb = xk->stride_b; p.xk_st = xk->stride_t; p.xk_sh = xk->stride_h;
+    p.xv = xv->ptr; p.xv_sb = xv->stride_b; p.xv_st = xv->stride_t; p.xv_sh = xv->stride_h;
+    p.k = static_cast<uint8_t*>(m->k);
+    p.v = static_cast<uint8_t*>(m->v);
+    p.par = static_cast<uint16_t*>(m->par);
+    p.B = m->B; p.H = m->H; p.D = m->D; p.M = m->M; p.G = q_groups(m->D); p.bits = m->bits;
+    p.vec_k = rows16(xk);
+    p.vec_v = rows16(xv);
+    p.chk = range_counter();
+    return p;
+}
+
+// Slot of logical position j (0 <= j <= M) of the ring.
+inline int ring_slot(const txl_qmem* m, int j)
+{
+    return static_cast<int>((static_cast<int64_t>(m->wp) + j) % m->M);
+}
+
+// Shared argument checks of txl_rel_attn_qmem and its path query.
+txl_status check_qattn(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem, const txl_view* k_cur,
+                       const txl_view* v_cur, const void* r, int64_t ld_r, const txl_view* out, txl_dtype dtype)
+{
+    txl_status st = check_attn(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
+    if (st != TXL_OK || !mem) return st;
+    st = check_qmem(mem);
+    if (st != TXL_OK) return st;
+    if (mem->M > 0 && (mem->B != B || mem->H != H || mem->D != D)) return TXL_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(mem->M) + L > INT32_MAX) return TXL_ERR_UNSUPPORTED;
+    return TXL_OK;
+}
+
+// The memory's valid positions as read back into the workspace: head-major [B][H][valid][ld], oldest
+// first, ld = D rounded up to 8 so that rows start on 16-byte boundaries.
+txl_mem read_back_mem(int B, int H, int D, const txl_qmem* mem, txl_dtype dtype, void* workspace)
+{
+    const int64_t ld = (D + 7) / 8 * 8, n = mem->valid;
+    const int64_t elem = dtype == TXL_F32 ? 4 : 2;
+    txl_mem m{};
+    m.k = workspace;
+    m.v = static_cast<char*>(workspace) + B * H * n * ld * elem;
+    m.stride_b = H * n * ld;
+    m.stride_t = ld;
+    m.stride_h = n * ld;
+    m.B = B; m.M = mem->valid; m.H = H; m.D = D;
+    m.dtype = dtype;
+    m.wp = 0;
+    m.valid = mem->valid;
+    return m;
+}
+
+}  // namespace
+
+size_t txl_qmem_code_bytes(int B, int M, int H, int D, int bits)
+{
+    if (B <= 0 || M <= 0 || H <= 0 || D <= 0 || D > 128 || (bits != 4 && bits != 8)) return 0;
+    return static_cast<size_t>(B) * H * M * q_groups(D) * 4 * bits;
+}
+
+size_t txl_qmem_par_bytes(int B, int M, int H, int D)
+{
+    if (B <= 0 || M <= 0 || H <= 0 || D <= 0 || D > 128) return 0;
+    return static_cast<size_t>(B) * H * M * q_groups(D) * 8;
+}
+
+txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v_new, int L, txl_dtype dtype,
+                         void* stream)
+{
+    if (!mem || !view_ok(k_new) || !view_ok(v_new) || L < 0) return TXL_ERR_INVALID_ARG;
+    if (dtype != TXL_F32 && dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
+    txl_status st = check_qmem(mem);
+    if (st != TXL_OK) return st;
+    if (mem->M == 0 || L == 0) return TXL_OK;
+    QmemParams p = qmem_params(mem, k_new, v_new, dtype);
+    p.t0 = L > mem->M ? L - mem->M : 0;
+    p.n = L - p.t0;
+    p.slot0 = ring_slot(mem, p.t0 % mem->M);
+    if (mem->B > 0 && launch_qmem_push(p, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TXL_ERR_CUDA;
+    mem->wp = static_cast<int>((static_cast<int64_t>(mem->wp) + L) % mem->M);
+    mem->valid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(mem->valid) + L, mem->M));
+    return TXL_OK;
+}
+
+txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_out, const txl_view* v_out,
+                         txl_dtype dtype, void* stream)
+{
+    if (!mem || !view_ok(k_out) || !view_ok(v_out)) return TXL_ERR_INVALID_ARG;
+    if (dtype != TXL_F32 && dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
+    txl_status st = check_qmem(mem);
+    if (st != TXL_OK) return st;
+    if (n < 0 || j0 < mem->M - mem->valid || static_cast<int64_t>(j0) + n > mem->M) return TXL_ERR_INVALID_ARG;
+    if (n == 0 || mem->B == 0) return TXL_OK;
+    QmemParams p = qmem_params(mem, k_out, v_out, dtype);
+    p.n = n;
+    p.slot0 = ring_slot(mem, j0);
+    return launch_qmem_read(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
+size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype)
+{
+    if (B <= 0 || L <= kDecodeMaxL || H <= 0 || D <= 0 || D > 128 || !mem || mem->M <= 0) return 0;
+    return static_cast<size_t>(2) * B * mem->M * H * ((D + 7) / 8 * 8) * (dtype == TXL_F32 ? 4 : 2);
+}
+
+int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem, const txl_view* k_cur,
+                           const txl_view* v_cur, const void* r, int64_t ld_r, const txl_view* out, txl_dtype dtype)
+{
+    const txl_status st = check_qattn(B, L, H, D, q, mem, k_cur, v_cur, r, ld_r, out, dtype);
+    if (st != TXL_OK) return -static_cast<int>(st);
+    if (L <= kDecodeMaxL) return 5;
+    if (!mem || mem->valid == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
+    const txl_mem m = read_back_mem(B, H, D, mem, dtype, mem->k);   // an aligned address; nothing is read
+    return txl_rel_attn_path(B, L, H, D, q, &m, k_cur, v_cur, r, ld_r, out, dtype);
+}
+
+txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const txl_view* q, const txl_qmem* mem,
+                             const txl_view* k_cur, const txl_view* v_cur, const float* u, const float* v_bias,
+                             const void* r, int64_t ld_r, int n_rows, float scale, const txl_view* out,
+                             txl_dtype dtype, void* workspace, size_t workspace_bytes, int* err_flag, void* stream)
+{
+    txl_status st = check_qattn(B, L, H, D, q, mem, k_cur, v_cur, r, ld_r, out, dtype);
+    if (st != TXL_OK) return st;
+    if (clamp_len < 0 || !u || !v_bias) return TXL_ERR_INVALID_ARG;
+    const int M = mem ? mem->M : 0;
+    if (n_rows < std::min<int64_t>(static_cast<int64_t>(M) + L, static_cast<int64_t>(clamp_len) + 1))
+        return TXL_ERR_INVALID_ARG;
+    if (B == 0 || L == 0) return TXL_OK;
+    const int valid = M > 0 ? mem->valid : 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (L > kDecodeMaxL) {
+        const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
+        if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
+        if (valid == 0)
+            return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, nullptr, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale,
+                                    out, dtype, nullptr, 0, err_flag, stream);
+        const txl_mem m = read_back_mem(B, H, D, mem, dtype, workspace);
+        const txl_view kw{m.k, m.stride_b, m.stride_t, m.stride_h}, vw{m.v, m.stride_b, m.stride_t, m.stride_h};
+        st = txl_qmem_read(mem, M - valid, valid, &kw, &vw, dtype, stream);
+        if (st != TXL_OK) return st;
+        return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, &m, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale, out,
+                                dtype, nullptr, 0, err_flag, stream);
+    }
+    if (B > 65535 || H > 65535) return TXL_ERR_UNSUPPORTED;
+    if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
+    QattnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = q->ptr; p.q_sb = q->stride_b; p.q_st = q->stride_t; p.q_sh = q->stride_h;
+    p.kcur = k_cur->ptr; p.kc_sb = k_cur->stride_b; p.kc_st = k_cur->stride_t; p.kc_sh = k_cur->stride_h;
+    p.vcur = v_cur->ptr; p.vc_sb = v_cur->stride_b; p.vc_st = v_cur->stride_t; p.vc_sh = v_cur->stride_h;
+    p.out = out->ptr; p.o_sb = out->stride_b; p.o_st = out->stride_t; p.o_sh = out->stride_h;
+    if (valid > 0) {
+        p.k = static_cast<const uint8_t*>(mem->k);
+        p.v = static_cast<const uint8_t*>(mem->v);
+        p.par = static_cast<const uint16_t*>(mem->par);
+        p.bits = mem->bits;
+        p.wp = mem->wp;
+    }
+    p.u = u; p.vb = v_bias;
+    p.r = r; p.r_row = static_cast<int64_t>(H) * ld_r; p.r_head = ld_r;
+    p.f32 = dtype == TXL_F32;
+    p.B = B; p.L = L; p.H = H; p.D = D; p.M = M; p.G = q_groups(D); p.lo = M - valid; p.C = clamp_len;
+    p.n_rows = n_rows;
+    p.qscale = scale * 1.4426950408889634f;
+    const int elem = dtype == TXL_F32 ? 4 : 2;
+    p.vec_r = a16(r) && s16(ld_r, elem);
+    p.chk = range_counter();
+    const int sms = sm_count();
+    if (sms <= 0) return TXL_ERR_CUDA;
+    return launch_qattn(p, sms, s) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
 int txl_checked_build(void) { return kCheckedBuild ? 1 : 0; }
 
 txl_status txl_range_errors(int* count)

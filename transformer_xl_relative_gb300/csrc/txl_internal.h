@@ -263,6 +263,43 @@ struct MemPushParams {
 
 cudaError_t launch_mem_push(const MemPushParams& p, cudaStream_t s);
 
+// ---------------------------------------------------------------- quantised memory
+constexpr int kQGroup = 32;         // channels that share a step and a minimum
+
+// Push (positions t0 .. t0+n-1 of the segment into slots (slot0 + t) mod M) and read (n logical
+// positions from slot slot0 on into t = 0 .. n-1) of a quantised memory.  x_*: the k and v tensors
+// read by the push and written by the read.
+struct QmemParams {
+    void* xk; int64_t xk_sb, xk_st, xk_sh;
+    void* xv; int64_t xv_sb, xv_st, xv_sh;
+    uint8_t* k; uint8_t* v;             // [B][H][M][G * 4 * bits]
+    uint16_t* par;                      // bf16 [B][H][M][G][4]
+    int B, H, D, M, G, bits;
+    int slot0, t0, n;
+    int vec_k, vec_v;                   // every row of the tensor starts on a 16-byte boundary
+    int* chk;                           // range-check counter (checked build)
+};
+cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
+cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
+
+// Attention of 1 .. kDecodeMaxL queries over a quantised memory and the segment's own keys.
+struct QattnParams {
+    const void* q; int64_t q_sb, q_st, q_sh;
+    const void* kcur; int64_t kc_sb, kc_st, kc_sh;
+    const void* vcur; int64_t vc_sb, vc_st, vc_sh;
+    void* out; int64_t o_sb, o_st, o_sh;
+    const uint8_t* k; const uint8_t* v; const uint16_t* par;
+    const float* u; const float* vb;
+    const void* r; int64_t r_row, r_head;       // element strides of the r table
+    int f32;                                    // dtype: 1 = fp32, 0 = bf16
+    int B, L, H, D, M, G, bits, lo, wp, C;      // lo: first valid logical key
+    int n_rows;
+    float qscale;                               // scale * log2(e)
+    int vec_r;                                  // rows of r start on 16-byte boundaries
+    int* chk;                                   // range-check counter (checked build)
+};
+cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s);
+
 cudaError_t launch_selftest_wait(int* err_flag, unsigned timeout_us, cudaStream_t s);
 // One failing and one passing range check on the device (the checked build's counter gains one).
 cudaError_t launch_selftest_range(int* chk, cudaStream_t s);

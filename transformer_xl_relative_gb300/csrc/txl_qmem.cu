@@ -1,0 +1,308 @@
+// txl_qmem.cu -- the FIFO K/V memory held as 4- or 8-bit codes: quantised as it is written
+// (txl_qmem_push) and read back (txl_qmem_read).
+//
+// A group is 32 consecutive channels of one position and head; n = 2^bits - 1:
+//     lo = bf16 floor of min(x),  step = bf16 ceiling of (max(x) - lo) / n,
+//     c_d = nearest integer to (x_d - lo) / step (ties to even),  x'_d = lo + step c_d.
+// Rounding step up makes n step >= max - lo, so no code is clipped and |x' - x| <= step / 2; a bf16
+// minimum is its own floor, so bf16 inputs lose nothing in lo.  lo and step take 16 bits each: 4-bit
+// codes cost 5 bits per channel in all.  The definitions are met exactly: fp32 estimates are
+// corrected where the exact value could lie on the other side of a border (all comparisons below
+// are between exactly represented numbers).
+//
+// Both kernels are bound by HBM.  Four lanes share a group, eight channels each: 16-byte accesses to
+// bf16 rows, and consecutive threads walk the groups of a row, then the positions of one head, which
+// are contiguous in the code arrays.
+#include <cuda_bf16.h>
+
+#include "txl_internal.h"
+#include "txl_ptx.cuh"
+
+namespace txl {
+
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr float kTwo64 = 18446744073709551616.f;
+
+__device__ __forceinline__ float bf16_floor(float x)
+{
+    const uint32_t b = __float_as_uint(x), t = b & 0xffff0000u;
+    return __uint_as_float(t + (t != b && (b >> 31) ? 0x10000u : 0u));
+}
+
+// x >= 0, not NaN
+__device__ __forceinline__ float bf16_ceil_pos(float x)
+{
+    return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
+}
+
+// Eight channels d0 .. d0+7 of a row; channels at or past D read as `fill`.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, float fill, float* x)
+{
+    if (vec && d0 + 8 <= D) {
+        if constexpr (F32) {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + d0);
+            const float4 a = __ldg(q), b = __ldg(q + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + d0));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = fill;
+        if (d0 + e < D) {
+            if constexpr (F32) x[e] = __ldg(static_cast<const float*>(row) + d0 + e);
+            else x[e] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
+        }
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* row, int d0, int D, bool vec, const float* x)
+{
+    if (vec && d0 + 8 <= D) {
+        if constexpr (F32) {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(row) + d0);
+            q[0] = make_float4(x[0], x[1], x[2], x[3]);
+            q[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + d0) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (d0 + e < D) {
+            if constexpr (F32) static_cast<float*>(row)[d0 + e] = x[e];
+            else static_cast<__nv_bfloat16*>(row)[d0 + e] = __float2bfloat16_rn(x[e]);
+        }
+}
+
+// One lane's part (eight channels, `live` of them inside D) of quantising a group shared by four
+// consecutive lanes.  Returns the codes and the group's step and lo.
+template <int BITS>
+__device__ __forceinline__ void quantise8(const float* x, int live, uint32_t* code, float& step, float& lo)
+{
+    constexpr float n = static_cast<float>((1 << BITS) - 1);
+    float mn = INFINITY, mx = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < live) {
+            mn = fminf(mn, x[e]);
+            mx = fmaxf(mx, x[e]);
+            bad |= !(fabsf(x[e]) < INFINITY);
+        }
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        bad |= __shfl_xor_sync(0xffffffffu, bad ? 1 : 0, off) != 0;
+    }
+    lo = bf16_floor(mn);
+    // max - lo = span + err exactly
+    const float span = mx - lo;
+    const float bb = span - mx;
+    const float err = (mx - (span - bb)) + (-lo - bb);
+    auto below = [&](float s) {                        // s n < max - lo, exactly (s has 8 bits, n at most 8)
+        const float p = s * n;
+        return p < span || (p == span && err > 0.f);
+    };
+    step = bf16_ceil_pos(span * (1.f / n));
+    const float down = __uint_as_float(__float_as_uint(step) - (step > 0.f ? 0x10000u : 0u));
+    if (below(step)) step = __uint_as_float(__float_as_uint(step) + 0x10000u);
+    else if (!below(down)) step = down;
+    bad |= !(span < INFINITY) || !(lo > -INFINITY);    // (then step = span / n is finite too)
+    if (bad) step = lo = __uint_as_float(0x7fc00000u);
+
+    // quotients from the reciprocal (a tiny step scaled up first, so that it has one); within 1e-4 of
+    // the exact quotient, so only those near a half need the exact comparison with (c + 1/2) step
+    const float sc = step < 1e-30f ? kTwo64 : 1.f;
+    const float inv = step > 0.f ? 1.f / (step * sc) : 0.f;
+    uint32_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float d = x[e] - lo;
+        const float t = d * sc * inv;
+        float r = rintf(t);
+        if (fabsf(t - r) > 0.499f && e < live) {
+            const float base = floorf(t);
+            const float diff = d - (base + 0.5f) * step;           // exact: both sides agree to a factor of 2
+            const float b2 = d - x[e];
+            const float lost = (x[e] - (d - b2)) + (-lo - b2);     // x - lo = d + lost exactly
+            const bool up = diff > 0.f || (diff == 0.f && lost > 0.f);
+            const bool tie = diff == 0.f && lost == 0.f;
+            r = up ? base + 1.f : base;
+            if (tie) r = 2.f * rintf(0.5f * base) == base ? base : base + 1.f;
+        }
+        c[e] = e < live && !bad ? static_cast<uint32_t>(r) : 0u;
+    }
+    if constexpr (BITS == 4) {
+        code[0] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12 | c[4] << 16 | c[5] << 20 | c[6] << 24 | c[7] << 28;
+    } else {
+        code[0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+        code[1] = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+    }
+}
+
+// (step, lo) as the bf16 pair a parameter word holds; both are bf16 values already
+__device__ __forceinline__ uint32_t par_word(float step, float lo)
+{
+    return (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+}
+
+struct QPos {
+    int64_t row;          // row of the code and parameter arrays
+    int t, g, d0;         // position of the segment, group, first channel of the lane
+};
+
+// Grid: (ceil(n * G * 4 / kQThreads), H, B); consecutive threads take the lanes of a row's groups,
+// then the next position of the same head.
+template <int G>
+__device__ __forceinline__ bool q_pos(const QmemParams& p, int64_t i, QPos& o)
+{
+    const int64_t t = i / (4 * G);
+    const int rem = static_cast<int>(i - t * (4 * G));
+    o.t = static_cast<int>(t);
+    o.g = rem >> 2;
+    o.d0 = o.g * kQGroup + (rem & 3) * 8;
+    int64_t slot = p.slot0 + t;
+    if (slot >= p.M) slot -= p.M;
+    const bool live = t < p.n;
+    if (live && !in_range(slot, 0, p.M, p.chk)) slot = 0;
+    o.row = (static_cast<int64_t>(blockIdx.z) * p.H + blockIdx.y) * p.M + slot;
+    return live;
+}
+
+template <int BITS, int G, bool F32>
+__global__ void __launch_bounds__(kQThreads) qmem_push_kernel(const __grid_constant__ QmemParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    QPos o;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
+    const bool on = q_pos<G>(p, i, o);                 // the four lanes of a group are on or off together
+    constexpr int E = F32 ? 4 : 2;
+    float xk[8], xv[8];
+    const int live = on ? min(max(p.D - o.d0, 0), 8) : 0;
+    const int64_t t = p.t0 + o.t;
+    if (on) {
+        const char* rk = static_cast<const char*>(p.xk) + (blockIdx.z * p.xk_sb + t * p.xk_st + blockIdx.y * p.xk_sh) * E;
+        const char* rv = static_cast<const char*>(p.xv) + (blockIdx.z * p.xv_sb + t * p.xv_st + blockIdx.y * p.xv_sh) * E;
+        load8<F32>(rk, o.d0, p.D, p.vec_k, 0.f, xk);
+        load8<F32>(rv, o.d0, p.D, p.vec_v, 0.f, xv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xk[e] = xv[e] = 0.f;
+    }
+    uint32_t ck[2], cv[2];
+    float ks, kl, vs, vl;
+    quantise8<BITS>(xk, live, ck, ks, kl);
+    quantise8<BITS>(xv, live, cv, vs, vl);
+    if (!on) return;
+    const int64_t at = o.row * (4 * G * BITS) + o.d0 * BITS / 8;
+    if constexpr (BITS == 4) {
+        *reinterpret_cast<uint32_t*>(p.k + at) = ck[0];
+        *reinterpret_cast<uint32_t*>(p.v + at) = cv[0];
+    } else {
+        *reinterpret_cast<uint2*>(p.k + at) = make_uint2(ck[0], ck[1]);
+        *reinterpret_cast<uint2*>(p.v + at) = make_uint2(cv[0], cv[1]);
+    }
+    if ((o.d0 & (kQGroup - 1)) == 0)
+        *reinterpret_cast<uint2*>(p.par + (o.row * G + o.g) * 4) = make_uint2(par_word(ks, kl), par_word(vs, vl));
+}
+
+template <int BITS>
+__device__ __forceinline__ void expand8(const uint32_t* code, uint32_t par, float* x)
+{
+    const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xffff0000u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t c = BITS == 4 ? (code[0] >> (4 * e)) & 15u : (code[e >> 2] >> (8 * (e & 3))) & 255u;
+        x[e] = fmaf(step, static_cast<float>(c), lo);
+    }
+}
+
+template <int BITS, int G, bool F32>
+__global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_constant__ QmemParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    QPos o;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
+    if (!q_pos<G>(p, i, o)) return;
+    constexpr int E = F32 ? 4 : 2;
+    const int64_t at = o.row * (4 * G * BITS) + o.d0 * BITS / 8;
+    uint32_t ck[2], cv[2];
+    if constexpr (BITS == 4) {
+        ck[0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
+        cv[0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
+    } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at)), b = __ldg(reinterpret_cast<const uint2*>(p.v + at));
+        ck[0] = a.x; ck[1] = a.y; cv[0] = b.x; cv[1] = b.y;
+    }
+    const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (o.row * G + o.g) * 4));
+    float xk[8], xv[8];
+    expand8<BITS>(ck, par.x, xk);
+    expand8<BITS>(cv, par.y, xv);
+    const int64_t t = o.t;
+    char* rk = static_cast<char*>(p.xk) + (blockIdx.z * p.xk_sb + t * p.xk_st + blockIdx.y * p.xk_sh) * E;
+    char* rv = static_cast<char*>(p.xv) + (blockIdx.z * p.xv_sb + t * p.xv_st + blockIdx.y * p.xv_sh) * E;
+    store8<F32>(rk, o.d0, p.D, p.vec_k, xk);
+    store8<F32>(rv, o.d0, p.D, p.vec_v, xv);
+}
+
+template <int BITS, int G>
+cudaError_t launch(const QmemParams& p, bool f32, bool push, cudaStream_t s)
+{
+    const int64_t units = static_cast<int64_t>(p.n) * G * 4;
+    const int64_t blocks = (units + kQThreads - 1) / kQThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(blocks), p.H, p.B);
+    auto* kernel = push ? (f32 ? qmem_push_kernel<BITS, G, true> : qmem_push_kernel<BITS, G, false>)
+                        : (f32 ? qmem_read_kernel<BITS, G, true> : qmem_read_kernel<BITS, G, false>);
+    return launch_dependent(kernel, grid, dim3(kQThreads), 0, s, p);
+}
+
+cudaError_t launch_any(const QmemParams& p, txl_dtype dtype, bool push, cudaStream_t s)
+{
+    const bool f32 = dtype == TXL_F32;
+    switch (p.G * 16 + p.bits) {
+    case 1 * 16 + 4: return launch<4, 1>(p, f32, push, s);
+    case 2 * 16 + 4: return launch<4, 2>(p, f32, push, s);
+    case 3 * 16 + 4: return launch<4, 3>(p, f32, push, s);
+    case 4 * 16 + 4: return launch<4, 4>(p, f32, push, s);
+    case 1 * 16 + 8: return launch<8, 1>(p, f32, push, s);
+    case 2 * 16 + 8: return launch<8, 2>(p, f32, push, s);
+    case 3 * 16 + 8: return launch<8, 3>(p, f32, push, s);
+    case 4 * 16 + 8: return launch<8, 4>(p, f32, push, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t s)
+{
+    return launch_any(p, dtype, true, s);
+}
+
+cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s)
+{
+    return launch_any(p, dtype, false, s);
+}
+
+}  // namespace txl
