@@ -1,21 +1,72 @@
 // txl_qmem_attn.cu -- relative attention of 1 .. 16 queries over a quantised memory and the segment's
-// own keys: the generation step over a memory of 4- or 8-bit codes.
+// own keys: the generation step over a memory of 4- or 8-bit codes, in one launch.
 //
 //     s_ij = scale [ (q_i+u).k'_j + (q_i+v).r[min(M+i-j, C)] ],  out_i = softmax_j(s_ij) v'_j
-// with k'_jd = lo + step c_jd for memory keys and the segment's own k, v unquantised.
+// with k'_jd = lo_jG + step_jG c_jd in group G of 32 channels.  The codes never become k' or v':
+//     q.k'_j  = sum_G step_jG (sum_{d in G} q_d c_jd) + lo_jG (sum_{d in G} q_d)
+//     out_d   = sum_j (p_j step_jG) c_jd + sum_j p_j lo_jG
+// so the inner sums are products with the integer codes, and step and lo act once per key and group.
 //
-// One block per (query, head, batch entry): the keys in chunks of one per thread, the codes expanded
-// in registers, an online softmax over the chunks in fp32.
+// The work is bound by HBM (a byte of 4-bit codes carries four flops per query); what it must avoid is
+// spending instructions per code.  The inner sums run as mma.sync m16n8k16 with the codes as the A
+// operand: the bit pattern of a code in the low bits of an fp16 number is the subnormal c 2^-24, which the
+// tensor cores multiply exactly, so one AND per pair of codes makes an operand (a nibble at bits 4..7
+// is 16 c 2^-24; the 16 goes into q, or into the output).  ldmatrix delivers four codes of a row per
+// 16 bits; its transposed form pairs two keys of the same channel for P.V.  At 4 bits a pair of codes
+// costs 0.6 instructions for K and for V, where converting to floats took about three.  (tcgen05 would
+// want the codes expanded into shared memory first, and 128 rows of queries where there are 1 to 16.)
+//
+// Precision: q+u is held as two fp16 parts (scaled by a power of two per row; 22 bits) in two columns
+// of the B operand, p step likewise; the accumulators are fp32.  The eight columns of an MMA are four
+// slots x (hi, lo).  A slot is a query; with fewer than four queries the other slots take other tiles
+// of 16 keys ("streams": the B operand is zero outside the tile's own slots), so that the work per key
+// after the first product (scale, softmax, splitting p) falls on all 32 lanes whatever L is.
+//
+// The position term: the keys of a block and the queries meet at consecutive distances, so
+// e(i, rho) = (q_i+v).r is a band computed once per block of keys, on the tensor cores too (bf16 r rows,
+// q+v as two bf16 parts), for up to eight (batch entry, query) rows at once: a CTA covers NB batch
+// entries, which share every r row.  Distances at or past the clamp share one entry.
+//
+// One CTA: NB batch entries x one head x a range of keys; 8 / NB warps per entry, each with its own
+// ring of cp.async stages (no block barriers in the key loop).  The key ranges of a head are the ranks
+// of a cluster, merged through distributed shared memory.
+#include <algorithm>
+
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "txl_internal.h"
+#include "txl_mma.cuh"
 #include "txl_ptx.cuh"
 
 namespace txl {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
+constexpr int kMaxRows = 8;                    // (batch entry, query) rows of a CTA
+constexpr int kBandBytes = 16384;              // of position terms: 16384 / (4 rows) keys per block
+constexpr int kBandPad = 40;                   // floats after a row's keys: up to 22 more entries; rows 8 banks apart
+constexpr float kNoMax = -3e38f;               // running maximum before any key
+constexpr float kTwo24 = 16777216.f;
+constexpr float kMinUnit = 3.00926553e-36f;    // 2^-118 and 2^126: bounds of the weights' unit, so that a weight
+constexpr float kMaxUnit = 8.50705917e37f;     // (at most 2^8) over the unit stays finite
+
+// Keys of a stage: 64 where a key's codes are small, fewer where they are long.
+__host__ __device__ constexpr int stage_keys(int bits, int ng) { return bits * ng <= 8 ? 64 : 32; }
+__host__ __device__ constexpr int stage_bytes(int bits, int ng) { return stage_keys(bits, ng) * (8 * ng * bits + 8 * ng); }
+
+struct QSplit {               // how the host divides the work
+    int nb;                   // batch entries of a CTA (1, 2, 4, 8)
+    int lq;                   // queries of a CTA; blockIdx.x / ranks selects the group of queries
+    int ranks;                // CTAs of a cluster: key ranges
+    int range;                // keys of a range (a multiple of the stage)
+    int block;                // keys of a position band
+    int pitch;                // floats between band rows
+    int nc_mul;               // 65536 / (16-byte chunks of a code row) + 1
+};
 
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
 {
@@ -23,93 +74,645 @@ __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
                : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
 }
 
-// channel d of a code row
-__device__ __forceinline__ float code_at(const uint8_t* row, int d, int bits)
+// D += A B: m16n8k16, fp16 operands, fp32 accumulators
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
 {
-    return static_cast<float>(bits == 4 ? (row[d >> 1] >> (4 * (d & 1))) & 15 : row[d]);
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__ QattnParams p)
+// 8 x 8 transpose of 16-bit elements across a warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
-    __shared__ float qu[128], qv[128], ps[kThreads], red[kThreads / 32];
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
+
+// (hi, lo) fp16 parts of x in one word: hi = x rounded, lo = the rest rounded
+__device__ __forceinline__ uint32_t split_f16(float x)
+{
+    const __half hi = __float2half_rn(x);
+    return __half_as_ushort(hi) | half_bits(x - __half2float(hi)) << 16;
+}
+
+__device__ __forceinline__ void cp_async8(void* dst, const void* src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float ld_rank(const float* p, uint32_t rank)       // this address in another CTA of the cluster
+{
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
+// large at 4 bits).  `half` selects the upper byte (4 bits).
+template <int BITS>
+__device__ __forceinline__ uint32_t pair_even(uint32_t w) { return w & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu); }
+template <int BITS>
+__device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : (w >> 8) & 0x00ff00ffu; }
+
+template <int BITS, int NG, int QT>
+__global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSplit sp)
+{
+    constexpr int DP = NG * 32;                           // channels, padded
+    constexpr int NC = NG * BITS / 4;                     // 16-byte chunks of a code row
+    constexpr int KS = stage_keys(BITS, NG);
+    constexpr int kParOff = KS * 2 * NC * 16;             // of a stage: k chunks, v chunks, parameters
+    constexpr int kStageBytes = stage_bytes(BITS, NG);
+    constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per chunk and product
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* stages = smem;
+    float* band = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+    float* qu = band + kBandBytes / 4 + kMaxRows * kBandPad;    // [row][DP], scaled into fp16's range
+    float* qv = qu + kMaxRows * DP;                       // [row][DP], log2 units
+    float* norm = qv + kMaxRows * DP;                     // [row]: qu times this is in log2 units
+    float* mine = norm + kMaxRows;                        // [row][DP + 2]: this CTA's O, m, l
+    uint16_t* qvh = reinterpret_cast<uint16_t*>(mine + kMaxRows * (DP + 2));   // [2 row + part][DP] bf16 parts of qv
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
+    const int rank = blockIdx.x % sp.ranks, i0 = blockIdx.x / sp.ranks * sp.lq;
+    const int h = blockIdx.y, b0 = blockIdx.z * sp.nb;
+    const int Lq = min(sp.lq, p.L - i0), rows = sp.nb * Lq;
+    const int wpe = kWarps / sp.nb, bs = warp / wpe, sw = warp % wpe;          // this warp's batch entry and part
+    const int b = b0 + bs;
+    // slots of an MMA's columns: slot = stream * Lp + query
+    const int lp_log = Lq >= 3 ? 2 : Lq - 1, Lp = 1 << lp_log;
+    const int NS = min(4 >> lp_log, KS / 16);
     pdl_launch_dependents();
     pdl_wait();
-    const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    if (tid < p.D) {
-        const float q = ld_elem(p.q, b * p.q_sb + i * p.q_st + h * p.q_sh + tid, p.f32);
-        qu[tid] = (q + p.u[h * p.D + tid]) * p.qscale;
-        qv[tid] = (q + p.vb[h * p.D + tid]) * p.qscale;
-    }
-    __syncthreads();
-    const int K = p.M + i + 1;                     // keys this query sees
-    const int row_bytes = 4 * p.G * p.bits;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int j0 = p.lo; j0 < K; j0 += kThreads) {
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        if (j < K) {
-            s = 0.f;
-            const int64_t rr = static_cast<int64_t>(min(p.M + i - j, p.C)) * p.r_row + h * p.r_head;
-            if (j < p.M) {
-                const int slot = static_cast<int>((static_cast<int64_t>(p.wp) + j) % p.M);
-                const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.M + slot;
-                for (int d = 0; d < p.D; ++d) {
-                    const uint16_t* par = p.par + (row * p.G + d / kQGroup) * 4;
-                    const float step = __uint_as_float(static_cast<uint32_t>(par[0]) << 16);
-                    const float lo = __uint_as_float(static_cast<uint32_t>(par[1]) << 16);
-                    s = fmaf(qu[d], fmaf(step, code_at(p.k + row * row_bytes, d, p.bits), lo), s);
+
+    const int j_lo = static_cast<int>(min(static_cast<int64_t>(p.M), p.lo + static_cast<int64_t>(rank) * sp.range));
+    const int j_hi = static_cast<int>(min(static_cast<int64_t>(p.M), static_cast<int64_t>(j_lo) + sp.range));
+
+    // ---- this warp's copies: stage n covers keys j_lo + (n * wpe + sw) * KS ..
+    uint8_t* my_stages = stages + warp * kStages * kStageBytes;
+    const int n_stage = b < p.B ? max(0, (j_hi - j_lo - sw * KS + wpe * KS - 1) / (wpe * KS)) : 0;
+    const int64_t head_row = (static_cast<int64_t>(b) * p.H + h) * p.M;
+    const int nc = p.G * BITS / 4;
+    auto copy_stage = [&](int n) {
+        if (n < n_stage) {
+            uint8_t* st = my_stages + (n % kStages) * kStageBytes;
+            const int j = j_lo + (n * wpe + sw) * KS;
+            const int live = min(KS, j_hi - j);
+            int64_t slot0 = static_cast<int64_t>(p.wp) + j;
+            if (slot0 >= p.M) slot0 -= p.M;
+            auto row_of = [&](int r) {
+                int64_t s = slot0 + r;
+                if (s >= p.M) s -= p.M;
+                if (!in_range(r < live ? s : 0, 0, p.M, p.chk)) s = 0;
+                return r < live ? head_row + s : head_row;
+            };
+            for (int x = lane; x < KS * nc; x += 32) {
+                const int r = (x * sp.nc_mul) >> 16, c = x - r * nc;
+                const int64_t at = (row_of(r) * nc + c) * 16;
+                const uint32_t bytes = r < live ? 16u : 0u;
+                mma::cp_async16(st + (c * KS + r) * 16, p.k + at, bytes);
+                mma::cp_async16(st + ((NC + c) * KS + r) * 16, p.v + at, bytes);
+            }
+            if (p.G & 1) {
+                for (int x = lane; x < KS * p.G; x += 32) {
+                    const int r = p.G == 1 ? x : x / 3, c = x - r * p.G;
+                    cp_async8(st + kParOff + r * 8 * NG + 8 * c, p.par + (row_of(r) * p.G + c) * 4, r < live ? 8u : 0u);
                 }
             } else {
-                for (int d = 0; d < p.D; ++d)
-                    s = fmaf(qu[d], ld_elem(p.kcur, b * p.kc_sb + (j - p.M) * p.kc_st + h * p.kc_sh + d, p.f32), s);
-            }
-            for (int d = 0; d < p.D; ++d) s = fmaf(qv[d], ld_elem(p.r, rr + d, p.f32), s);
-        }
-        float x = s;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = x;
-        __syncthreads();
-        const float mn = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        ps[tid] = exp2f(s - mn);
-        __syncthreads();
-        const float w = exp2f(m - mn);
-        m = mn;
-        l *= w;
-        o *= w;
-        const int n = min(kThreads, K - j0);
-        for (int t = 0; t < n; ++t) {
-            const float pr = ps[t];
-            l += pr;
-            if (tid < p.D) {
-                const int jt = j0 + t;
-                float v;
-                if (jt < p.M) {
-                    const int slot = static_cast<int>((static_cast<int64_t>(p.wp) + jt) % p.M);
-                    const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.M + slot;
-                    const uint16_t* par = p.par + (row * p.G + tid / kQGroup) * 4;
-                    v = fmaf(__uint_as_float(static_cast<uint32_t>(par[2]) << 16), code_at(p.v + row * row_bytes, tid, p.bits),
-                             __uint_as_float(static_cast<uint32_t>(par[3]) << 16));
-                } else {
-                    v = ld_elem(p.vcur, b * p.vc_sb + (jt - p.M) * p.vc_st + h * p.vc_sh + tid, p.f32);
+                for (int x = lane; x < KS * (p.G >> 1); x += 32) {
+                    const int r = p.G == 2 ? x : x >> 1, c = p.G == 2 ? 0 : x & 1;
+                    mma::cp_async16(st + kParOff + r * 8 * NG + 16 * c, p.par + (row_of(r) * p.G + 2 * c) * 4,
+                                    r < live ? 16u : 0u);
                 }
-                o = fmaf(pr, v, o);
+            }
+        }
+        mma::cp_async_commit();
+    };
+    if (p.G != NG) {                                      // parameters of groups past G stay zero
+        for (int x = lane; x < kStages * KS * NG; x += 32) {
+            const int st = x / (KS * NG), rem = x % (KS * NG);
+            if (rem % NG >= p.G) *reinterpret_cast<uint2*>(my_stages + st * kStageBytes + kParOff + 8 * rem) = make_uint2(0, 0);
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int n = 0; n < kStages - 1; ++n) copy_stage(n);
+
+    // ---- queries: (q+u), (q+v) times scale log2 e; rows past the last batch entry are zero
+    for (int x = tid; x < kMaxRows * DP; x += kThreads) {
+        const int row = x / DP, d = x % DP;
+        const int be = b0 + row / Lq, i = i0 + row % Lq;
+        float a = 0.f, c = 0.f;
+        if (row < rows && be < p.B && d < p.D) {
+            const float q = ld_elem(p.q, be * p.q_sb + i * p.q_st + h * p.q_sh + d, p.f32);
+            a = (q + __ldg(p.u + h * p.D + d)) * p.qscale;
+            c = (q + __ldg(p.vb + h * p.D + d)) * p.qscale;
+        }
+        qu[x] = a;
+        qv[x] = c;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(c);
+        qvh[2 * row * DP + d] = __bfloat16_as_ushort(hi);
+        qvh[(2 * row + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
+    }
+    __syncthreads();
+    {
+        // each row of qu scaled by a power of two so that its largest entry lies in [2^11, 2^12)
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < NG; ++e) mx = fmaxf(mx, fabsf(qu[warp * DP + 32 * e + lane]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(11 - ex + 127) << 23);
+#pragma unroll
+        for (int e = 0; e < NG; ++e) qu[warp * DP + 32 * e + lane] *= up;
+        if (lane == 0) norm[warp] = __uint_as_float(static_cast<uint32_t>(ex - 11 + 127) << 23);
+    }
+    __syncthreads();
+
+    // ---- B operands of Q.K: column g = (slot g/2, part g%2); and per slot c4 the group sums of q
+    uint32_t bq[QT][NG * 2][2];
+    float qs[QT][NG], sc[QT];
+    const int my_stream = (g >> 1) >> lp_log;             // of the column this lane holds in B operands
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int il = min(((g >> 1) & (Lp - 1)) + 4 * t, Lq - 1);
+        const float* row = qu + (bs * Lq + il) * DP;
+        auto part = [&](int d, float f) {
+            const uint32_t w = split_f16(row[d] * f);
+            return g & 1 ? w >> 16 : w & 0xffffu;
+        };
+#pragma unroll
+        for (int ks = 0; ks < NG * 2; ++ks) {
+            if constexpr (BITS == 4) {
+                const int d = 32 * (ks >> 1) + 8 * c4 + 2 * (ks & 1);
+                bq[t][ks][0] = part(d, 1.f) | part(d + 4, 1.f) << 16;
+                bq[t][ks][1] = part(d + 1, 0.0625f) | part(d + 5, 0.0625f) << 16;
+            } else {
+                const int d = 16 * ks + 4 * c4;
+                bq[t][ks][0] = part(d, 1.f) | part(d + 2, 1.f) << 16;
+                bq[t][ks][1] = part(d + 1, 1.f) | part(d + 3, 1.f) << 16;
+            }
+        }
+        const int is = bs * Lq + min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
+        sc[t] = norm[is] * kTwo24;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+            float s = 0.f;
+            for (int d = 0; d < 32; ++d) s += qu[is * DP + 32 * G + d];
+            qs[t][G] = s * norm[is];
+        }
+    }
+
+    // ---- running state of slot c4: maximum, weight unit rf (O is in units of rf), sums
+    float o[QT][NG * 2][4], z[QT][NG], m[QT], l[QT], rf[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = kNoMax;
+        l[t] = 0.f;
+        rf[t] = kMinUnit;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) z[t][G] = 0.f;
+#pragma unroll
+        for (int x = 0; x < NG * 2; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
+    }
+
+    int n = 0;
+    for (int jb = j_lo; jb < j_hi; jb += sp.block) {
+        // ---- position band of keys jb .. jb + kb - 1: entry rho is distance top - rho
+        const int kb = min(sp.block, j_hi - jb);
+        const int top = p.M + i0 + Lq - 1 - jb;
+        const int n_rho = kb + Lq - 1;
+        const int rho_c = max(0, min(n_rho - 1, top - p.C));      // entries before this one equal it
+        if (jb != j_lo) __syncthreads();
+        if (!p.f32) {
+            const int n_ct = (rows + 3) >> 2;
+            for (int t16 = (rho_c >> 4) + warp; t16 * 16 < n_rho; t16 += kWarps) {
+                uint4 a[2][NG];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    int rr = max(0, min(top - (t16 * 16 + g + 8 * half), p.C));
+                    if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
+                    const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
+#pragma unroll
+                    for (int G = 0; G < NG; ++G) {
+                        const int d = 32 * G + 8 * c4;
+                        if (p.vec_r && d + 8 <= p.D) {
+                            a[half][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
+                        } else {
+                            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
+                            a[half][G] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                for (int ct = 0; ct < n_ct; ++ct) {
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int G = 0; G < NG; ++G) {
+                        const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
+                        mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
+                        mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
+                    }
+                    if (4 * ct + c4 < rows) {
+                        float* e = band + (4 * ct + c4) * sp.pitch + t16 * 16 + g;
+                        e[0] = acc[0] + acc[1];
+                        e[8] = acc[2] + acc[3];
+                    }
+                }
+            }
+        } else {
+            for (int x = tid; x < rows * n_rho; x += kThreads) {
+                const int row = x / n_rho, rho = x % n_rho;
+                if (rho < rho_c) continue;
+                int rr = max(0, min(top - rho, p.C));
+                if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
+                const float* src = static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head;
+                float s = 0.f;
+                for (int d = 0; d < p.D; ++d) s = fmaf(qv[row * DP + d], __ldg(src + d), s);
+                band[row * sp.pitch + rho] = s;
+            }
+        }
+        __syncthreads();
+
+        // ---- this warp's stages of the block
+        for (; n < n_stage; ++n) {
+            const int js = j_lo + (n * wpe + sw) * KS;
+            if (js >= jb + kb) break;
+            copy_stage(n + kStages - 1);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const uint8_t* st = my_stages + (n % kStages) * kStageBytes;
+            const uint32_t st_addr = smem_u32(st) + (((lane >> 4) * KS) + ((lane >> 3) & 1) * 8 + (lane & 7)) * 16;
+            for (int k0 = 0; k0 < KS; k0 += 16 * NS) {
+                if (js + k0 >= j_hi) break;
+                // Q.K: acc[t][G] = for slot c4, keys g and g+8 of its stream's tile, (hi, lo) parts
+                float acc[QT][NG][4];
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+#pragma unroll
+                    for (int G = 0; G < NG; ++G) acc[t][G][0] = acc[t][G][1] = acc[t][G][2] = acc[t][G][3] = 0.f;
+                for (int T = 0; T < NS; ++T) {
+                    const bool on = my_stream == T;
+#pragma unroll
+                    for (int c2 = 0; c2 < NC; c2 += 2) {
+                        uint32_t w[4];
+                        mma::ldsm_x4(st_addr + (c2 * KS + k0 + 16 * T) * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int c = c2 + half, G = c * 4 / BITS;
+#pragma unroll
+                            for (int s = 0; s < SUB; ++s) {
+                                const uint32_t x = w[2 * half] >> (8 * s), y = w[2 * half + 1] >> (8 * s);
+                                const int ks = c * SUB + s;
+#pragma unroll
+                                for (int t = 0; t < QT; ++t)
+                                    mma_f16(acc[t][G], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
+                                            pair_odd<BITS>(y), on ? bq[t][ks][0] : 0u, on ? bq[t][ks][1] : 0u);
+                            }
+                        }
+                    }
+                }
+                // scores, weights, and the P operands: two keys per lane
+                const int kk = k0 + 16 * (c4 >> lp_log) + g;          // key of the stage (and kk + 8)
+                const bool in_use = (c4 >> lp_log) < NS;              // slots past the streams hold no keys
+                uint2 par[2][NG];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int G = 0; G < NG; ++G)
+                        par[x][G] = in_use ? *reinterpret_cast<const uint2*>(st + kParOff + (kk + 8 * x) * 8 * NG + 8 * G)
+                                           : make_uint2(0, 0);
+                uint32_t bp[QT][NG][2];
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const int il = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
+                    const float* e = band + (bs * Lq + il) * sp.pitch;
+                    float s[2], pr[2], w[2][NG];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int key = js + kk + 8 * x;
+                        const bool live = in_use && key < j_hi;
+                        float a = live ? e[max(Lq - 1 - il + key - jb, rho_c)] : 0.f, d = 0.f;
+#pragma unroll
+                        for (int G = 0; G < NG; ++G) {
+                            d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], __uint_as_float(par[x][G].x << 16), d);
+                            a = fmaf(__uint_as_float(par[x][G].x & 0xffff0000u), qs[t][G], a);
+                        }
+                        s[x] = live ? fmaf(d, sc[t], a) : -INFINITY;
+                        pr[x] = ex2_approx(s[x] - m[t]);
+                    }
+                    const float f = 1.f / rf[t];                      // a power of two
+                    float big = fmaxf(pr[0], pr[1]) * 16.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int G = 0; G < NG; ++G) {
+                            w[x][G] = pr[x] * f * __uint_as_float(par[x][G].y << 16);
+                            big = fmaxf(big, w[x][G]);
+                        }
+                    if (__any_sync(0xffffffffu, big > 4096.f)) {
+                        // a weight grew past 2^8, or its product with a step past 2^12: new maximum and unit
+                        float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        const float mn = fmaxf(m[t], mx);
+                        const float dl = ex2_approx(m[t] - mn);
+                        float ref = 0.f;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            pr[x] = ex2_approx(s[x] - mn);
+#pragma unroll
+                            for (int G = 0; G < NG; ++G) ref = fmaxf(ref, pr[x] * __uint_as_float(par[x][G].y << 16));
+                        }
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+                        ref = fminf(fmaxf(fmaxf(ref, rf[t] * dl), kMinUnit), kMaxUnit);
+                        const float unit = __uint_as_float(__float_as_uint(ref) & 0x7f800000u);      // its power of two
+                        const float so = dl * rf[t] / unit;
+                        rf[t] = unit;
+                        m[t] = mn;
+                        l[t] *= dl;
+#pragma unroll
+                        for (int G = 0; G < NG; ++G) z[t][G] *= dl;
+#pragma unroll
+                        for (int x = 0; x < NG * 2; ++x) {
+                            o[t][x][0] *= so; o[t][x][1] *= so; o[t][x][2] *= so; o[t][x][3] *= so;
+                        }
+                        const float f2 = 1.f / unit;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int G = 0; G < NG; ++G) w[x][G] = pr[x] * f2 * __uint_as_float(par[x][G].y << 16);
+                    }
+                    l[t] += pr[0] + pr[1];
+#pragma unroll
+                    for (int G = 0; G < NG; ++G) {
+                        z[t][G] = fmaf(pr[0], __uint_as_float(par[0][G].y & 0xffff0000u),
+                                       fmaf(pr[1], __uint_as_float(par[1][G].y & 0xffff0000u), z[t][G]));
+                        // row = key, columns (2 slot, 2 slot + 1) -> rows = columns of B, pairs of keys
+                        bp[t][G][0] = transpose8(split_f16(w[0][G]));
+                        bp[t][G][1] = transpose8(split_f16(w[1][G]));
+                    }
+                }
+                // P.V: o[t][mt] = for slot c4, channels of row g and g+8 of the tile, (hi, lo) parts
+                for (int T = 0; T < NS; ++T) {
+                    const bool on = my_stream == T;
+#pragma unroll
+                    for (int c2 = 0; c2 < NC; c2 += 2) {
+                        uint32_t w[4];
+                        mma::ldsm_x4_t(st_addr + ((NC + c2) * KS + k0 + 16 * T) * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int c = c2 + half, G = c * 4 / BITS;
+#pragma unroll
+                            for (int s = 0; s < SUB; ++s) {
+                                const uint32_t x = w[2 * half] >> (8 * s), y = w[2 * half + 1] >> (8 * s);
+#pragma unroll
+                                for (int t = 0; t < QT; ++t)
+                                    mma_f16(o[t][c * SUB + s], pair_even<BITS>(x), pair_odd<BITS>(x), pair_even<BITS>(y),
+                                            pair_odd<BITS>(y), on ? bp[t][G][0] : 0u, on ? bp[t][G][1] : 0u);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();                                 // the stage may be overwritten
+        }
+    }
+    __syncthreads();
+
+    // ---- merge: the streams of a warp, its warps, the segment's own keys, the ranks
+    float* part = reinterpret_cast<float*>(stages);       // [warp][query][DP + 2]
+    float* own_part = part + kWarps * sp.lq * (DP + 2);   // [row][DP + 2] of the segment's own keys
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        float lt = l[t], zt[NG], ot[NG * 4];
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+            zt[G] = z[t][G];
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) zt[G] += __shfl_xor_sync(0xffffffffu, zt[G], off);
+        }
+        const float un = rf[t] * kTwo24;
+#pragma unroll
+        for (int x = 0; x < NG * 2; ++x) {
+            ot[2 * x] = fmaf(o[t][x][0] + o[t][x][1], un, zt[x >> 1]);
+            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (BITS == 4 ? 0.0625f : 1.f), un, zt[x >> 1]);
+        }
+        float mt = m[t];
+        for (int off = Lp; off <= 2; off <<= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, mt, off);
+            const float mn = fmaxf(mt, mo);
+            const float a = ex2_approx(mt - mn), c = ex2_approx(mo - mn);
+            mt = mn;
+            lt = lt * a + __shfl_xor_sync(0xffffffffu, lt, off) * c;
+#pragma unroll
+            for (int x = 0; x < NG * 4; ++x) ot[x] = ot[x] * a + __shfl_xor_sync(0xffffffffu, ot[x], off) * c;
+        }
+        const int il = c4 + 4 * t;
+        if (c4 < Lp && il < Lq) {
+            float* dst = part + (warp * sp.lq + il) * (DP + 2);
+#pragma unroll
+            for (int x = 0; x < NG * 2; ++x) {
+                const int d = BITS == 4 ? 32 * (x >> 1) + 4 * g + 2 * (x & 1) : 16 * x + 2 * g;
+                dst[d] = ot[2 * x];
+                dst[d + 1] = ot[2 * x + 1];
+            }
+            if (g == 0) {
+                dst[DP] = mt;
+                dst[DP + 1] = lt;
             }
         }
     }
-    if (tid < p.D) {
-        const int64_t at = b * p.o_sb + i * p.o_st + h * p.o_sh + tid;
-        if (p.f32) static_cast<float*>(p.out)[at] = o / l;
-        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o / l);
+    const bool has_own = rank == sp.ranks - 1;
+    if (has_own) {
+        for (int row = warp; row < rows; row += kWarps) {
+            const int be = b0 + row / Lq, i = i0 + row % Lq;
+            if (be >= p.B) continue;
+            float mo = kNoMax, lo = 0.f, oo[NG];
+#pragma unroll
+            for (int e = 0; e < NG; ++e) oo[e] = 0.f;
+            const float nm = norm[row];
+            for (int j = 0; j <= i; ++j) {
+                int rr = min(i - j, p.C);
+                if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < NG; ++e) {
+                    const int d = lane + 32 * e;
+                    if (d < p.D) {
+                        const float k = ld_elem(p.kcur, be * p.kc_sb + j * p.kc_st + h * p.kc_sh + d, p.f32);
+                        const float r = ld_elem(p.r, rr * p.r_row + h * p.r_head + d, p.f32);
+                        s = fmaf(qu[row * DP + d] * nm, k, fmaf(qv[row * DP + d], r, s));
+                    }
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+                const float mn = fmaxf(mo, s), a = ex2_approx(mo - mn), w = ex2_approx(s - mn);
+                mo = mn;
+                lo = lo * a + w;
+#pragma unroll
+                for (int e = 0; e < NG; ++e) {
+                    const int d = lane + 32 * e;
+                    const float v = d < p.D ? ld_elem(p.vcur, be * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
+                    oo[e] = oo[e] * a + w * v;
+                }
+            }
+            float* dst = own_part + row * (DP + 2);
+#pragma unroll
+            for (int e = 0; e < NG; ++e) dst[lane + 32 * e] = oo[e];
+            if (lane == 0) {
+                dst[DP] = mo;
+                dst[DP + 1] = lo;
+            }
+        }
     }
+    __syncthreads();
+    for (int x = tid; x < rows * DP; x += kThreads) {
+        const int row = x / DP, d = x % DP, wb = row / Lq * wpe, il = row % Lq;
+        const float* own = own_part + row * (DP + 2);
+        const bool use_own = has_own && b0 + row / Lq < p.B;
+        float mx = use_own ? own[DP] : kNoMax;
+        for (int w = 0; w < wpe; ++w) mx = fmaxf(mx, part[((wb + w) * sp.lq + il) * (DP + 2) + DP]);
+        float lt = 0.f, ot = 0.f;
+        for (int w = 0; w < wpe; ++w) {
+            const float* src = part + ((wb + w) * sp.lq + il) * (DP + 2);
+            const float a = ex2_approx(src[DP] - mx);
+            lt += src[DP + 1] * a;
+            ot += src[d] * a;
+        }
+        if (use_own) {
+            const float a = ex2_approx(own[DP] - mx);
+            lt += own[DP + 1] * a;
+            ot += own[d] * a;
+        }
+        mine[row * (DP + 2) + d] = ot;
+        if (d == 0) {
+            mine[row * (DP + 2) + DP] = mx;
+            mine[row * (DP + 2) + DP + 1] = lt;
+        }
+    }
+    __syncthreads();
+    if (sp.ranks > 1) cluster_sync_all();
+    for (int x = rank * kThreads + tid; x < rows * DP; x += sp.ranks * kThreads) {
+        const int row = x / DP, d = x % DP, be = b0 + row / Lq;
+        if (d >= p.D || be >= p.B) continue;
+        const float* src = mine + row * (DP + 2);
+        float lt, ot;
+        if (sp.ranks == 1) {
+            ot = src[d];
+            lt = src[DP + 1];
+        } else {
+            float mr[8], mx = kNoMax;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                mr[r] = r < sp.ranks ? ld_rank(src + DP, r) : kNoMax;
+                mx = fmaxf(mx, mr[r]);
+            }
+            lt = ot = 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < sp.ranks) {
+                    const float a = ex2_approx(mr[r] - mx);
+                    lt += ld_rank(src + DP + 1, r) * a;
+                    ot += ld_rank(src + d, r) * a;
+                }
+        }
+        const int64_t at = be * p.o_sb + (i0 + row % Lq) * p.o_st + h * p.o_sh + d;
+        if (p.f32) static_cast<float*>(p.out)[at] = ot / lt;
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(ot / lt);
+    }
+    __syncthreads();
+    if (sp.ranks > 1) cluster_sync_all();                 // no CTA leaves while its memory is read
+}
+
+template <int BITS, int NG, int QT>
+cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream_t s)
+{
+    constexpr int DP = NG * 32;
+    const size_t bytes = kWarps * kStages * stage_bytes(BITS, NG) + kBandBytes + kMaxRows * kBandPad * 4 +
+                         (2 * kMaxRows * DP + kMaxRows + kMaxRows * (DP + 2)) * 4 + 2 * kMaxRows * DP * 2;
+    static_assert(kWarps * kStages * stage_bytes(BITS, NG) >= (kWarps + 1) * kMaxRows * (DP + 2) * 4, "partial results fit");
+    auto* kernel = qattn_kernel<BITS, NG, QT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = sp.ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, sp);
+}
+
+template <int BITS, int NG>
+cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream_t s)
+{
+    return sp.lq <= 4 ? launch<BITS, NG, 1>(p, sp, grid, s) : launch<BITS, NG, 2>(p, sp, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_qattn(const QattnParams& p, int, cudaStream_t s)
+cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
 {
-    return launch_dependent(qattn_kernel, dim3(p.L, p.H, p.B), dim3(kThreads), 0, s, p);
+    const int ng = p.G <= 2 ? 2 : 4, bits = p.bits == 8 ? 8 : 4;
+    const int ks = stage_keys(bits, ng);
+    QSplit sp{};
+    const int groups = p.L > 8 ? 2 : 1;                   // queries: eight at most per CTA
+    sp.lq = (p.L + groups - 1) / groups;
+    // Batch entries of a CTA: as many as share a position band of eight rows, but no fewer CTAs than SMs
+    // when the keys are split eight ways.
+    const int64_t keys = p.M - p.lo;
+    sp.nb = 1;
+    while (2 * sp.nb * sp.lq <= kMaxRows && sp.nb < p.B) sp.nb *= 2;
+    auto blocks = [&](int nb) { return static_cast<int64_t>(p.H) * ((p.B + nb - 1) / nb) * groups; };
+    while (sp.nb > 1 && blocks(sp.nb) * 8 < sm_count) sp.nb /= 2;
+    // Key ranges: until two CTAs per SM, while each warp keeps two stages.
+    sp.ranks = 1;
+    while (sp.ranks < 8 && blocks(sp.nb) * sp.ranks < 2 * sm_count &&
+           keys > static_cast<int64_t>(sp.ranks) * 2 * ks * (kWarps / sp.nb))
+        sp.ranks *= 2;
+    const int64_t unit = static_cast<int64_t>(ks) * (kWarps / sp.nb);
+    sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + unit - 1) / unit * unit);
+    if (sp.range == 0) sp.range = static_cast<int>(unit);
+    // Position band: a multiple of the stages of one round of the warps
+    const int rows = sp.nb * sp.lq;
+    const int fit = kBandBytes / 4 / rows / static_cast<int>(unit) * static_cast<int>(unit);
+    sp.block = std::max(fit, static_cast<int>(unit));
+    if (sp.block > sp.range) sp.block = sp.range;
+    sp.pitch = sp.block + kBandPad;
+    sp.nc_mul = 65536 / (p.G * bits / 4) + 1;
+    const dim3 grid(sp.ranks * groups, p.H, (p.B + sp.nb - 1) / sp.nb);
+    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, grid, s) : launch_qt<4, 4>(p, sp, grid, s);
+    return ng == 2 ? launch_qt<8, 2>(p, sp, grid, s) : launch_qt<8, 4>(p, sp, grid, s);
 }
 
 }  // namespace txl
