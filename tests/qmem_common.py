@@ -129,9 +129,10 @@ def decode_tolerance(ref, size, vmax, dtype):
 
 
 def segment_tolerance(q, k, v, u, vb, r, C, ref):
-    """|out - ref| allowed of the bf16 tensor-core kernels over the memory read back, elementwise.  They
-    round c(q+u), c(q+v), k', the position term, the weights and v' to bf16, each by at most 2^-8 of its
-    value (uniform: a deviation of 2^-8 / sqrt(3)), independently.  Errors of a score's products add in
+    """|out - ref| allowed of the tensor-core kernels over the memory read back, elementwise.  They round
+    c(q+u), c(q+v), k', the position term, the weights and v' to 16 bits, each by at most bf16's 2^-8 of
+    its value (uniform: a deviation of 2^-8 / sqrt(3)), independently (in fp16, a bound eight times too
+    wide).  Errors of a score's products add in
     squares, s2 = scale^2 [2 sum (q+u)^2 k^2 + sum (q+v)^2 r^2 + ((q+v).r)^2]; a score's error moves the
     output by p_j (v_j - out), a weight's and a value's by p_j v_j each.  Six deviations of the sum, and
     half a step of the output's own rounding, 2^-8 of its value."""

@@ -213,6 +213,10 @@ def test_a_group_of_nan_reaches_only_what_it_should(txl):
 SEGMENT = [
     # B, H, D, L, M, valid, wp, C, dtype, expected path
     (2, 2, 64, 128, 128, 128, 0, 1000, "bf16", 1),
+    (2, 2, 41, 50, 90, 80, 7, 60, "bf16", 1),               # dense odd rows: copied for TMA
+    (1, 2, 24, 33, 700, 700, 650, 1000, "bf16", 1),
+    (1, 1, 96, 140, 1000, 990, 3, 500, "bf16", 1),
+    (40, 8, 64, 20, 30, 30, 29, 1000, "bf16", 1),           # more heads than multiprocessors
     (1, 3, 64, 200, 300, 250, 77, 150, "bf16", 1),          # a ring write pointer no tile divides
     (1, 2, 64, 17, 40, 40, 39, 1000, "bf16", 1),
     (2, 2, 128, 100, 130, 130, 7, 1000, "bf16", 1),
@@ -236,6 +240,47 @@ def test_segments_match_64_bits(txl, c, bits):
         check(call)
     else:
         check_segment(call)
+
+
+@pytest.mark.parametrize("factor", [1e-30, 1e-5, 1e5, 1e30])
+def test_segment_values_of_any_magnitude(txl, factor):
+    """V is held in fp16 in units taken from the data, so its size does not matter."""
+    call = Call(txl, 2, 2, 64, 40, 300, 300, 9, 1000, 4, "bf16")
+    call.vh = (call.vh * factor).to(torch.bfloat16)
+    call.v.mul_(factor)
+    call.mem.restore((9 - 300) % 300, 0)
+    txl.qmem_push(call.mem, call.kh.cuda(), call.vh.cuda())
+    call.run(txl)
+    torch.cuda.synchronize()
+    check_segment(call)
+
+
+@pytest.mark.parametrize("factor", [1e-30, 1e-5, 1e5, 1e30])
+def test_segment_keys_of_any_magnitude(txl, factor):
+    """K likewise, with queries that bring the scores back to size."""
+    call = Call(txl, 2, 2, 64, 40, 300, 300, 9, 1000, 8, "bf16")
+    call.kh = (call.kh * factor).to(torch.bfloat16)
+    call.k.mul_(factor)
+    call.q.div_(factor)
+    call.u.div_(factor)
+    call.vb.div_(factor)
+    call.r.mul_(factor)
+    call.mem.restore((9 - 300) % 300, 0)
+    txl.qmem_push(call.mem, call.kh.cuda(), call.vh.cuda())
+    call.run(txl)
+    torch.cuda.synchronize()
+    check_segment(call)
+
+
+def test_segment_with_an_unaligned_position_table(txl):
+    call = Call(txl, 1, 2, 64, 40, 100, 100, 9, 1000, 8, "bf16")
+    flat = torch.empty(call.r.numel() + 1, dtype=torch.bfloat16, device="cuda")
+    flat[1:].copy_(call.r.reshape(-1))
+    call.r = flat[1:].view(call.r.shape)
+    assert txl.rel_attn_qmem_path(call.q, call.mem, call.k, call.v, call.r, call.out) == 1
+    call.run(txl)
+    torch.cuda.synchronize()
+    check_segment(call)
 
 
 @pytest.mark.parametrize("bits", [4, 8])

@@ -128,12 +128,12 @@ def test_long_segments_need_their_workspace(native):
     lib, E = native.load(), native
     m = qmem(native)
     p = ctypes.byref
-    need = 2 * 2 * 128 * 4 * 64 * 2
+    need = ((2 * 128 + 3 * 17) * 2 + 128 + 17) * 4 * 64 * 2 + 2 * 4 * 16
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 1) == need
-    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 2 * need
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 2 * 128 * 2 * 4 * 64 * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 16, 4, 64, p(m), 1) == 0
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, None, 1) == 0
-    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 41, p(qmem(native, D=41)), 1) == need // 64 * 48
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 41, p(qmem(native, D=41)), 1) == (need - 128) // 64 * 48 + 128
     assert attn(native, L=17) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=17, ws=FAKE, ws_bytes=need - 1) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=17, ws=FAKE + 8, ws_bytes=need) == E.TXL_ERR_WORKSPACE
@@ -150,8 +150,8 @@ def test_path_selection(native):
     assert path(L=17) == 1                                             # read back, fused tcgen05 kernel
     assert path(L=200, m=qmem(native, M=300, wp=77, valid=250)) == 1   # whatever the ring's write pointer
     assert path(L=200, dtype=0) == 2                                   # fp32: CUDA cores
-    assert path(L=200, D=41, ld_r=48) == 2                             # dense 82-byte rows
-    assert path(L=200, ptr=FAKE + 2) == 2                              # misaligned queries
+    assert path(L=200, D=41, ld_r=48) == 1                             # dense 82-byte rows are copied
+    assert path(L=200, ptr=FAKE + 2) == 1                              # and so are misaligned ones
     assert path(L=200, m=qmem(native, valid=0)) == 1
 
 

@@ -243,7 +243,8 @@ namespace {
 txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_view* q, const txl_mem* mem,
                           const txl_view* k_cur, const txl_view* v_cur, const float* u, const float* v_bias,
                           const void* r, int64_t ld_r, int n_rows, float scale, const txl_view* out, int* err_flag,
-                          cudaStream_t s, int ring_slots, float* lse = nullptr, int lse_out = 0)
+                          cudaStream_t s, int ring_slots, float* lse = nullptr, int lse_out = 0,
+                          const float* units = nullptr)
 {
     const int M = (mem && mem->M > 0) ? mem->M : 0;
     const int valid = M > 0 ? mem->valid : 0;
@@ -294,6 +295,7 @@ txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_v
     p.err_flag = err_flag;
     p.lse = lse;
     p.lse_out = lse_out;
+    p.units = units;
     if (lse && p.n_atoms != 1) return TXL_ERR_UNSUPPORTED;
     if (p.n_atoms == 1) {
         if (static_cast<int64_t>(p.n_qt) * H * B > INT32_MAX) return TXL_ERR_UNSUPPORTED;
@@ -1148,7 +1150,10 @@ txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_o
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype)
 {
     if (B <= 0 || L <= kDecodeMaxL || H <= 0 || D <= 0 || D > 128 || !mem || mem->M <= 0) return 0;
-    return static_cast<size_t>(2) * B * mem->M * H * ((D + 7) / 8 * 8) * (dtype == TXL_F32 ? 4 : 2);
+    const size_t row = static_cast<size_t>(B) * H * ((D + 7) / 8 * 8);
+    if (dtype == TXL_F32) return 2 * row * mem->M * 4;
+    const size_t r_rows = static_cast<size_t>(H) * ((D + 7) / 8 * 8) * (static_cast<size_t>(mem->M) + L);
+    return (2 * row * mem->M + 3 * row * L + r_rows) * 2 + static_cast<size_t>(B) * H * 16;
 }
 
 int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem, const txl_view* k_cur,
@@ -1158,6 +1163,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
     if (st != TXL_OK) return -static_cast<int>(st);
     if (L <= kDecodeMaxL) return 5;
     if (!mem || mem->valid == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
+    if (dtype == TXL_BF16) return 1;
     const txl_mem m = read_back_mem(B, H, D, mem, dtype, mem->k);   // an aligned address; nothing is read
     return txl_rel_attn_path(B, L, H, D, q, &m, k_cur, v_cur, r, ld_r, out, dtype);
 }
@@ -1176,20 +1182,60 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     if (B == 0 || L == 0) return TXL_OK;
     const int valid = M > 0 ? mem->valid : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (B > 65535 || H > 65535) return TXL_ERR_UNSUPPORTED;
     if (L > kDecodeMaxL) {
         const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
         if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
         if (valid == 0)
             return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, nullptr, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale,
                                     out, dtype, nullptr, 0, err_flag, stream);
+        if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
         const txl_mem m = read_back_mem(B, H, D, mem, dtype, workspace);
+        if (dtype == TXL_BF16) {
+            const int ld = (D + 7) / 8 * 8;
+            const int64_t seg = static_cast<int64_t>(B) * H * L * ld;
+            QexpandParams e{};
+            e.k = static_cast<const uint8_t*>(mem->k);
+            e.v = static_cast<const uint8_t*>(mem->v);
+            e.par = static_cast<const uint16_t*>(mem->par);
+            e.B = B; e.H = H; e.D = D; e.M = M; e.G = q_groups(D); e.bits = mem->bits;
+            e.slot0 = ring_slot(mem, M - valid);
+            e.n = valid; e.L = L; e.ld = ld;
+            auto rows16 = [&](const txl_view* v) {
+                return a16(v->ptr) && s16(v->stride_b, 2) && s16(v->stride_t, 2) && s16(v->stride_h, 2);
+            };
+            e.vcur = v_cur->ptr; e.vc_sb = v_cur->stride_b; e.vc_st = v_cur->stride_t; e.vc_sh = v_cur->stride_h;
+            e.kcur = k_cur->ptr; e.kc_sb = k_cur->stride_b; e.kc_st = k_cur->stride_t; e.kc_sh = k_cur->stride_h;
+            e.q = q->ptr; e.q_sb = q->stride_b; e.q_st = q->stride_t; e.q_sh = q->stride_h;
+            e.r = static_cast<const uint16_t*>(r);
+            e.ld_r = ld_r;
+            e.n_r = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(valid) + L, static_cast<int64_t>(clamp_len) + 1));
+            e.vec_v = rows16(v_cur); e.vec_k = rows16(k_cur); e.vec_q = rows16(q); e.vec_r = a16(r) && s16(ld_r, 2);
+            e.k_mem = m.k;
+            e.v_mem = m.v;
+            uint16_t* at = static_cast<uint16_t*>(m.v) + static_cast<int64_t>(B) * H * valid * ld;
+            e.k_seg = at;
+            e.v_seg = at + seg;
+            const txl_view ks{e.k_seg, static_cast<int64_t>(H) * L * ld, ld, static_cast<int64_t>(L) * ld};
+            txl_view vs = ks, qs = ks;
+            vs.ptr = e.v_seg;
+            // q that TMA cannot address is copied to rows that it can
+            if (!view_tma_ok(q, L, H, B)) qs.ptr = e.q_seg = at + 2 * seg;
+            else qs = *q;
+            e.r16 = at + 3 * seg;
+            e.units = reinterpret_cast<float*>(at + 3 * seg + static_cast<int64_t>(e.n_r) * H * ld);
+            e.chk = range_counter();
+            const int sms = sm_count();
+            if (sms <= 0 || launch_qmem_expand(e, sms, s) != cudaSuccess) return TXL_ERR_CUDA;
+            return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
+                                  err_flag, s, 0, nullptr, 0, e.units);
+        }
         const txl_view kw{m.k, m.stride_b, m.stride_t, m.stride_h}, vw{m.v, m.stride_b, m.stride_t, m.stride_h};
         st = txl_qmem_read(mem, M - valid, valid, &kw, &vw, dtype, stream);
         if (st != TXL_OK) return st;
         return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, &m, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale, out,
                                 dtype, nullptr, 0, err_flag, stream);
     }
-    if (B > 65535 || H > 65535) return TXL_ERR_UNSUPPORTED;
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
     QattnParams p;
     std::memset(&p, 0, sizeof(p));

@@ -24,16 +24,17 @@ __device__ __forceinline__ void pair_bar(int li) { named_bar_sync(2 + (li >> 5),
 
 // ---------------------------------------------------------------------------------------------
 // Logits of one thread's 64 columns of a tile (log2 domain): s = AC + BD(remapped), in place,
-// returning their maximum.  The ring already carries the mask (-inf) and the clamp (the value of
+// returning their maximum.  kF16: the ring holds fp16 instead of bf16.  The ring already carries the mask (-inf) and the clamp (the value of
 // r[clamp_len]) in the positions concerned, so every tile runs this one branch-free loop.
+template <bool kF16 = false>
 __device__ __forceinline__ float logits_interior(float* s, const uint32_t* bdrow, int wbase)
 {
     float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
     for (int m = 0; m < 32; ++m) {
         const uint32_t w = bdrow[(wbase - m) & 127];
-        const float x0 = add_bf16hi_f32(w, s[2 * m]);
-        const float x1 = add_bf16lo_f32(w, s[2 * m + 1]);
+        const float x0 = kF16 ? add_f16hi_f32(w, s[2 * m]) : add_bf16hi_f32(w, s[2 * m]);
+        const float x1 = kF16 ? add_f16lo_f32(w, s[2 * m + 1]) : add_bf16lo_f32(w, s[2 * m + 1]);
         s[2 * m] = x0;
         s[2 * m + 1] = x1;
         switch (m & 3) {
@@ -46,10 +47,16 @@ __device__ __forceinline__ float logits_interior(float* s, const uint32_t* bdrow
     return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
 }
 
+// A pair of position terms as the ring holds them, and -inf in both halves of a word.
+template <bool kF16>
+__device__ __forceinline__ uint32_t ring_pair(float lo, float hi) { return kF16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi); }
+template <bool kF16> constexpr uint32_t kRingNegInf = kF16 ? 0xFC00FC00u : 0xFF80FF80u;
+
 // Copy this thread's half of a new BD chunk (64 fp32 columns, in registers) into the row's ring
-// as bf16.  Chunk column c lives at ring position (128*(t&1) + c + sh) mod 256 (two positions per
+// as bf16 (kF16: fp16).  Chunk column c lives at ring position (128*(t&1) + c + sh) mod 256 (two positions per
 // 32-bit word, the even one in the low half).  With sh = 1 the column pairs straddle words, so
 // the words shared with the other half, or with the other ring slot, are written per 16 bits.
+template <bool kF16 = false>
 __device__ __forceinline__ void ring_write_half(uint32_t* bdrow, uint32_t row_saddr, const uint32_t* v,
                                                 int t, int hf, int sh)
 {
@@ -62,24 +69,24 @@ __device__ __forceinline__ void ring_write_half(uint32_t* bdrow, uint32_t row_sa
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(v[8 * q4 + 2 * e]), __uint_as_float(v[8 * q4 + 2 * e + 1]));
+                w[e] = ring_pair<kF16>(__uint_as_float(v[8 * q4 + 2 * e]), __uint_as_float(v[8 * q4 + 2 * e + 1]));
             *reinterpret_cast<uint4*>(slot + 32 * hf + 4 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
         // word 32hf + k = (lo: column 64hf + 2k - 1, hi: column 64hf + 2k)
-        const uint16_t first = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[0])));
-        const uint16_t last = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[63])));
+        const uint32_t ends = ring_pair<kF16>(__uint_as_float(v[0]), __uint_as_float(v[63]));
+        const uint16_t first = static_cast<uint16_t>(ends), last = static_cast<uint16_t>(ends >> 16);
         sts_u16(slot_saddr + 4u * (32 * hf) + 2u, first);             // hi half of word 32hf
 #pragma unroll
         for (int k = 1; k < 4; ++k)
-            slot[32 * hf + k] = pack_bf16x2(__uint_as_float(v[2 * k - 1]), __uint_as_float(v[2 * k]));
+            slot[32 * hf + k] = ring_pair<kF16>(__uint_as_float(v[2 * k - 1]), __uint_as_float(v[2 * k]));
 #pragma unroll
         for (int q4 = 1; q4 < 8; ++q4) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 4 * q4 + e;
-                w[e] = pack_bf16x2(__uint_as_float(v[2 * k - 1]), __uint_as_float(v[2 * k]));
+                w[e] = ring_pair<kF16>(__uint_as_float(v[2 * k - 1]), __uint_as_float(v[2 * k]));
             }
             *reinterpret_cast<uint4*>(slot + 32 * hf + 4 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
         }

@@ -178,7 +178,10 @@ constexpr uint16_t kMaskedKeyBf16 = 0xF14A;
 
 // kLse = 1: the row statistics alone (log-sum-exp for the gradient kernels): no output is written.
 // kLse = 2: the forward output and, besides it, every row's log-sum-exp.
-template <bool kTab, bool kMask = false, int kLse = 0>
+// kF16 (operands read back from a quantised memory): K, V, r, c(q + u), c(q + v), the position ring and
+// P are fp16, K, V and r in units of powers of two per (b, h) (p.units).  Operands, the argument of the
+// exponential and P keep 11 bits instead of 8.
+template <bool kTab, bool kMask = false, int kLse = 0, bool kF16 = false>
 __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid_constant__ AttnTcParams p)
 {
     constexpr int NPV = 64;
@@ -320,7 +323,18 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 us[e] = in ? __ldg(p.u + static_cast<int64_t>(it.h) * p.D + d) * bs : 0.f;
                 vs[e] = in ? __ldg(p.vb + static_cast<int64_t>(it.h) * p.D + d) * bs : 0.f;
             }
-            const uint64_t sc2 = f2_pack(p.qscale, p.qscale);
+            uint64_t sc2 = f2_pack(p.qscale, p.qscale), sc2u = sc2;      // of Qv and Qu
+            if constexpr (kF16) {                           // times the units of r and K
+                const float* un = p.units + 4 * (static_cast<int64_t>(it.b) * p.H + it.h);
+                const float ku = __ldg(un), ru = __ldg(un + 2);
+                sc2u = f2_pack(p.qscale * ku, p.qscale * ku);
+                sc2 = f2_pack(p.qscale * ru, p.qscale * ru);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    us[e] *= ku;
+                    vs[e] *= ru;
+                }
+            }
             if (!(ok = warp_wait(&bar.qraw_full[qb], (n >> 1) & 1, wc, 40))) break;
             uint8_t* qu = smem + PSmem::qu(qb);
             uint8_t* qv = smem + PSmem::qv(qb);
@@ -336,10 +350,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                     // dims past D hold zeros in q and in the biases, so they stay zero
                     const uint64_t q2 = f2_pack(__uint_as_float(rw[e] << 16), __uint_as_float(rw[e] & 0xffff0000u));
                     float a0, a1, b0, b1;
-                    f2_unpack(f2_fma(q2, sc2, f2_pack(us[2 * e], us[2 * e + 1])), a0, a1);
+                    f2_unpack(f2_fma(q2, sc2u, f2_pack(us[2 * e], us[2 * e + 1])), a0, a1);
                     f2_unpack(f2_fma(q2, sc2, f2_pack(vs[2 * e], vs[2 * e + 1])), b0, b1);
-                    wu[e] = pack_bf16x2(a0, a1);
-                    wv[e] = pack_bf16x2(b0, b1);
+                    wu[e] = kF16 ? pack_f16x2_sat(a0, a1) : pack_bf16x2(a0, a1);
+                    wv[e] = kF16 ? pack_f16x2_sat(b0, b1) : pack_bf16x2(b0, b1);
                 }
                 *reinterpret_cast<uint4*>(qu + off) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
                 *reinterpret_cast<uint4*>(qv + off) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
     } else if (warp == kPMmaWarp) {
         // =========================================================== UMMA issuer: S and BD
         if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idesc_qk = kF16 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
             const uint64_t qu_d0 = sdesc_k_sw128(smem_u32(smem + PSmem::qu(0)));
             const uint64_t qv_d0 = sdesc_k_sw128(smem_u32(smem + PSmem::qv(0)));
             constexpr uint64_t kQBuf = (2 * kTile) >> 4;           // next (Qu, Qv) buffer
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
     } else if (warp == kPValueWarp) {
         // =========================================================== V tiles + P.V
         if (lane == 0) {
-            constexpr uint32_t idesc_pv = idesc_bf16(128, NPV, 0, 1);
+            constexpr uint32_t idesc_pv = kF16 ? idesc_f16(128, NPV, 0, 1) : idesc_bf16(128, NPV, 0, 1);
             const uint64_t v_d = sdesc_mn_sw128(smem_u32(smem + PSmem::V), kTile);
             constexpr uint64_t kStage = kTile >> 4;
             const uint32_t b_vempty = smem_u32(bar.v_empty), b_pvdone = smem_u32(bar.pv_done);
@@ -532,7 +546,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
             // keys (lj > pi) are never written before that tile, so those keys come out masked.
             {
                 uint4* w = reinterpret_cast<uint4*>(bdrow + 64 * hf);
-                const uint4 ninf = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+                constexpr uint32_t ni = kRingNegInf<kF16>;
+                const uint4 ninf = make_uint4(ni, ni, ni, ni);
 #pragma unroll
                 for (int q4 = 0; q4 < 16; ++q4) w[q4] = ninf;
             }
@@ -589,7 +604,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
 #pragma unroll
                             for (int k = 0; k < 64; ++k) bdv[k] = bdc_bits;
                         }
-                        ring_write_half(bdrow, row_saddr, bdv, t, hf, sh);
+                        ring_write_half<kF16>(bdrow, row_saddr, bdv, t, hf, sh);
                     }
                     uint32_t su[64];
                     tmem_ld64(scol, su);
@@ -632,12 +647,13 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                         const int hi_lj = min(lm, 64 * hf + 64);
 #pragma unroll 1
                         for (int lj = 64 * hf; lj < hi_lj; ++lj)
-                            sts_u16(row_saddr + 2u * ((128 * (t & 1) + pi - lj + sh) & 255), 0xFF80);
+                            sts_u16(row_saddr + 2u * ((128 * (t & 1) + pi - lj + sh) & 255),
+                                    static_cast<uint16_t>(kRingNegInf<kF16>));
                     }
                 }
                 float mloc = -INFINITY;
                 if (ok) {
-                    mloc = logits_interior(s, bdrow, wbase);
+                    mloc = logits_interior<kF16>(s, bdrow, wbase);
                     xchg[2 * (t & 1) + hf] = mloc;
                 }
                 pair_bar(li);                               // exchange the two halves' maxima
@@ -673,6 +689,17 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                     for (int k = 0; k < 32; ++k) {
                         float y0, y1;
                         f2_unpack(f2_add(f2_pack(s[2 * k], s[2 * k + 1]), negm), y0, y1);
+                        if constexpr (kF16) {
+                            pw[k] = ex2_f16x2(pack_f16x2(y0, y1));
+                            if (k & 1) {
+                                b0 = add_f16lo_f32(pw[k], b0);
+                                b1 = add_f16hi_f32(pw[k], b1);
+                            } else {
+                                a0 = add_f16lo_f32(pw[k], a0);
+                                a1 = add_f16hi_f32(pw[k], a1);
+                            }
+                            continue;
+                        }
                         pw[k] = ex2_bf16x2(pack_bf16x2(y0, y1));
                         if (k & 1) {
                             b0 = add_bf16lo_f32(pw[k], b0);
@@ -742,7 +769,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_if(bar.o_free, lane == 0);
-                const float inv_l = rcp_approx(l_half + xchg[2 * (it.n_t & 1) + (hf ^ 1)]);
+                float inv_l = rcp_approx(l_half + xchg[2 * (it.n_t & 1) + (hf ^ 1)]);
+                if constexpr (kF16) inv_l *= __ldg(p.units + 4 * (static_cast<int64_t>(it.b) * p.H + it.h) + 1);
                 if constexpr (kLse == 2) {
                     // the row sum of the bf16 P that P.V multiplied, the normaliser of out
                     const int i = it.i0 + pi;
@@ -831,10 +859,16 @@ cudaError_t launch_attn_persist(const AttnTcParams& p, int sm_count, cudaStream_
         e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 2>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
         if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
+        if (e != cudaSuccess) return e;
         attr_done = true;
     }
     const int64_t items = static_cast<int64_t>(p.n_qt) * p.H * p.B;
     const int grid = static_cast<int>(items < sm_count ? items : sm_count);
+    if (p.units)
+        return launch_dependent(attn_persist_kernel<false, false, 0, true>, dim3(grid), dim3(kPThreads), PSmem::Size,
+                                s, p);
     if (p.lse && !p.table && p.lse_out)
         return launch_dependent(attn_persist_kernel<false, false, 2>, dim3(grid), dim3(kPThreads), PSmem::Size,
                                 s, p);

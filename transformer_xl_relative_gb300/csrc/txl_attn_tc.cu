@@ -102,7 +102,8 @@ struct Plan {
     __device__ bool need_chunk(int t, int C) const { return 128 * t < C; }
 };
 
-template <int NA>
+// kF16: fp16 operands read back from a quantised memory, K, V and r in units of p.units per (b, h).
+template <int NA, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnTcParams p)
 {
     using S = AttnSmem<NA>;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if (!load_v(t)) break;
             } else {
                 // O += P_t V_t from the P buffer, V of tile t + 1 requested before P_t is awaited
-                constexpr uint32_t idesc_pv = idesc_bf16(128, NPV, 0, 1);
+                constexpr uint32_t idesc_pv = kF16 ? idesc_f16(128, NPV, 0, 1) : idesc_bf16(128, NPV, 0, 1);
                 const uint64_t v_d = sdesc_mn_sw128(smem_u32(smem + S::V), kTile);
                 constexpr uint64_t kStage = (NA * kTile) >> 4;
                 const uint32_t b_vempty = smem_u32(bar.v_empty), b_pvdone = smem_u32(bar.pv_done);
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp == kMmaWarp) {
         // =========================================================== UMMA issuer
         if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0);
-            constexpr uint32_t idesc_pv = idesc_bf16(128, NPV, 0, 1);
+            constexpr uint32_t idesc_qk = kF16 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idesc_pv = kF16 ? idesc_f16(128, NPV, 0, 1) : idesc_bf16(128, NPV, 0, 1);
             const uint32_t qu = smem_u32(smem + S::Qu), qv = smem_u32(smem + S::Qv);
             const int ksteps = p.k_steps;
             int rs = 0, bd_uses = 0;
@@ -407,6 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const int src = pi;
             const float* uh = uv;
             const float* vh = uv + 128;
+            float scu = p.qscale, scv = p.qscale;
+            if constexpr (kF16) {                           // times the units of K and r
+                const float* un = p.units + 4 * (static_cast<int64_t>(b) * p.H + h);
+                scu *= __ldg(un);
+                scv *= __ldg(un + 2);
+            }
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
 #pragma unroll
@@ -424,8 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         const bool z0 = d0 >= p.D, z1 = d0 + 1 >= p.D;
                         const float u0 = uh[d0], u1 = uh[d0 + 1];
                         const float v0 = vh[d0], v1 = vh[d0 + 1];
-                        wu[e] = pack_bf16x2(z0 ? 0.f : (q0 + u0) * p.qscale, z1 ? 0.f : (q1 + u1) * p.qscale);
-                        wv[e] = pack_bf16x2(z0 ? 0.f : (q0 + v0) * p.qscale, z1 ? 0.f : (q1 + v1) * p.qscale);
+                        const float x0 = z0 ? 0.f : (q0 + u0) * scu, x1 = z1 ? 0.f : (q1 + u1) * scu;
+                        const float y0 = z0 ? 0.f : (q0 + v0) * scv, y1 = z1 ? 0.f : (q1 + v1) * scv;
+                        wu[e] = kF16 ? pack_f16x2_sat(x0, x1) : pack_bf16x2(x0, x1);
+                        wv[e] = kF16 ? pack_f16x2_sat(y0, y1) : pack_bf16x2(y0, y1);
                     }
                     const int off = a * kTile + li * 128 + ((c ^ (li & 7)) << 4);
                     *reinterpret_cast<uint4*>(smem + S::Qu + off) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
@@ -450,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // (lj > pi) are never written before that tile, so those keys come out masked.
         {
             uint4* w = reinterpret_cast<uint4*>(bdrow + 64 * hf);
-            const uint4 ninf = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+            constexpr uint32_t ni = kRingNegInf<kF16>;
+            const uint4 ninf = make_uint4(ni, ni, ni, ni);
 #pragma unroll
             for (int q4 = 0; q4 < 16; ++q4) w[q4] = ninf;
         }
@@ -501,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
                         for (int k = 0; k < 64; ++k) bdv[k] = bdc_bits;
                     }
-                    ring_write_half(bdrow, row_saddr, bdv, t, hf, sh);
+                    ring_write_half<kF16>(bdrow, row_saddr, bdv, t, hf, sh);
                 }
                 uint32_t su[64];
                 tmem_ld64(scol, su);
@@ -525,11 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const int hi_lj = min(lm, 64 * hf + 64);
 #pragma unroll 1
                 for (int lj = 64 * hf; lj < hi_lj; ++lj)
-                    sts_u16(row_saddr + 2u * ((128 * (t & 1) + pi - lj + sh) & 255), 0xFF80);
+                    sts_u16(row_saddr + 2u * ((128 * (t & 1) + pi - lj + sh) & 255), static_cast<uint16_t>(kRingNegInf<kF16>));
             }
             float mloc = -INFINITY;
             if (ok) {
-                mloc = logits_interior(s, bdrow, wbase);
+                mloc = logits_interior<kF16>(s, bdrow, wbase);
                 xchg[2 * (t & 1) + hf] = mloc;
             }
             pair_bar(li);                               // exchange the two halves' maxima
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
                     if (k & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
                     else acc0 = f2_add(acc0, f2_pack(p0, p1));
-                    pw[k] = pack_bf16x2(p0, p1);
+                    pw[k] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                 }
                 float a0, a1, b0, b1;
                 f2_unpack(acc0, a0, a1);
@@ -607,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tc_fence_after();
             const float l_row = l_half + xchg[2 * (n_t & 1) + (hf ^ 1)];
             const int i = plan.i0 + pi;
-            const float inv_l = 1.f / l_row;
+            float inv_l = 1.f / l_row;
+            if constexpr (kF16) inv_l *= __ldg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h) + 1);
             __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_sb +
                                   static_cast<int64_t>(i) * p.o_st + h * p.o_sh;
             const bool vec = p.out_vec != 0;
@@ -644,18 +655,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
 }
 
-template <int NA>
+template <int NA, bool kF16>
 cudaError_t launch_na(const AttnTcParams& p, cudaStream_t s)
 {
     static bool attr_done = false;
     if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NA, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              AttnSmem<NA>::Size);
         if (e != cudaSuccess) return e;
         attr_done = true;
     }
     dim3 grid(p.n_qt, p.H, p.B);
-    attn_tc_kernel<NA><<<grid, kThreads, AttnSmem<NA>::Size, s>>>(p);
+    attn_tc_kernel<NA, kF16><<<grid, kThreads, AttnSmem<NA>::Size, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -667,7 +678,7 @@ cudaError_t launch_attn_tc(const AttnTcParams& p, cudaStream_t s)
 {
     if (p.B == 0 || p.L == 0 || p.H == 0) return cudaSuccess;
     if (p.n_atoms != 2) return cudaErrorInvalidValue;
-    return launch_na<2>(p, s);
+    return p.units ? launch_na<2, true>(p, s) : launch_na<2, false>(p, s);
 }
 
 }  // namespace txl

@@ -141,6 +141,10 @@ struct AttnTcParams {
     // lse_out is set, not otherwise
     float* lse;
     int lse_out;
+    // fp16 operands (units != null): k, v, r are fp16 in units of units[4 (b H + h) + 0, 1, 2]; c(q+u)
+    // times the K unit, c(q+v) times the r unit, the position term and P are taken in fp16, and the
+    // output is multiplied by the V unit
+    const float* units;
 };
 
 cudaError_t launch_attn_tc(const AttnTcParams& p, cudaStream_t s);
@@ -281,6 +285,26 @@ struct QmemParams {
 };
 cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
 cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
+
+// The fp16 operands of the fused attention over a quantised memory (positions slot0 .. of the ring,
+// n of them) and a segment of L: K, V and q head-major [B][H][rows][ld], ld = D rounded up to 8.
+struct QexpandParams {
+    const uint8_t* k; const uint8_t* v; const uint16_t* par;
+    int B, H, D, M, G, bits, slot0, n, L, ld;
+    const void* vcur; int64_t vc_sb, vc_st, vc_sh;
+    const void* kcur; int64_t kc_sb, kc_st, kc_sh;
+    const void* q; int64_t q_sb, q_st, q_sh;
+    const uint16_t* r; int64_t ld_r;    // bf16 [n_r][H][ld_r]
+    int vec_v, vec_k, vec_q, vec_r;     // rows of these start on 16-byte boundaries
+    int n_r;
+    void* k_mem; void* v_mem;           // n rows per head, in the units below
+    void* k_seg; void* v_seg;           // L rows per head, the same units
+    void* q_seg;                        // bf16 copy for TMA, or null where q serves as it is
+    void* r16;                          // [n_r][H][ld]
+    float* units;                       // [B][H][4], 16-byte aligned: powers of two of K, V and r
+    int* chk;
+};
+cudaError_t launch_qmem_expand(const QexpandParams& p, int sm_count, cudaStream_t s);
 
 // Attention of 1 .. kDecodeMaxL queries over a quantised memory and the segment's own keys.
 struct QattnParams {

@@ -186,6 +186,23 @@ __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, const 
     return ok;
 }
 
+// ------------------------------------------------------------------------------- clusters
+// Barrier of every thread of the cluster (whole warps arrive together), shared memory included.
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The float at this shared-memory address in another CTA of the cluster.
+__device__ __forceinline__ float ld_rank(const float* p, uint32_t rank)
+{
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // ------------------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map)
 {
@@ -446,6 +463,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
          | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same for fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
+{
+    return idesc_bf16(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10));
+}
+
 // Instruction descriptor of tcgen05.mma kind::tf32: tf32 A and B, fp32 accumulator, M x N tile.
 __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N, int a_mn, int b_mn)
 {
@@ -487,6 +510,37 @@ __device__ __forceinline__ float add_bf16lo_f32(uint32_t w, float c)
 {
     float r;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, lo, %2;\n\t}"
+        : "=f"(r) : "r"(w), "f"(c));
+    return r;
+}
+
+// The same two of an fp16 pair, and the packing, plain and with values past fp16's range held at its ends.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float add_f16hi_f32(uint32_t w, float c)
+{
+    float r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.f16 %0, hi, %2;\n\t}"
+        : "=f"(r) : "r"(w), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float add_f16lo_f32(uint32_t w, float c)
+{
+    float r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.f16 %0, lo, %2;\n\t}"
         : "=f"(r) : "r"(w), "f"(c));
     return r;
 }
@@ -544,6 +598,14 @@ __device__ __forceinline__ uint32_t ex2_bf16x2(uint32_t w)
 {
     uint32_t r;
     asm("ex2.approx.ftz.bf16x2 %0, %1;" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// 2^x of both fp16 halves of w.
+__device__ __forceinline__ uint32_t ex2_f16x2(uint32_t w)
+{
+    uint32_t r;
+    asm("ex2.approx.f16x2 %0, %1;" : "=r"(r) : "r"(w));
     return r;
 }
 

@@ -265,6 +265,189 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     store8<F32>(rv, o.d0, p.D, p.vec_v, xv);
 }
 
+// The operands of the fused attention kernels in fp16, which keeps 11 bits where bf16 keeps 8: K and V
+// of the memory and of the segment, and r.  Each takes its range from a power of two, the unit: the
+// largest |k| of a (b, h) comes into [1, 2) (its unit multiplies c(q+u)), the largest |v| into
+// [2^11, 2^12) (P of the attention goes up to 2^8), and the largest |r| of 64 rows of the head into [1, 2)
+// (rows of up to 2^15 times that size have room).  One cluster per (b, h); each CTA takes a share of the rows, first for
+// the largest values (a group's end points bound its values, so the parameters suffice for the memory),
+// then to write.  Rows are taken four at a time per thread, the loads first.
+constexpr int kXThreads = 256;
+constexpr int kXRows = 4;
+
+template <int BITS, int G>
+__global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int ranks)
+{
+    __shared__ float red[3][kXThreads / 32];
+    __shared__ float rank_max[2];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int64_t bh = static_cast<int64_t>(b) * p.H + h;
+    auto share = [](int64_t n, int64_t part, int64_t parts) { return static_cast<int>(n * part / parts); };
+    const int r0 = share(p.n, rank, ranks), r1 = share(p.n, rank + 1, ranks);
+    const int s0 = share(p.L, rank, ranks), s1 = share(p.L, rank + 1, ranks);
+    auto slot_row = [&](int t) {
+        int64_t s = static_cast<int64_t>(p.slot0) + t;
+        if (s >= p.M) s -= p.M;
+        if (!in_range(s, 0, p.M, p.chk)) s = 0;
+        return bh * p.M + s;
+    };
+    auto seg = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int t) {
+        return static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh;
+    };
+    constexpr int LPR = 4 * G;                            // lanes of a row, eight channels each
+    constexpr int RPP = kXThreads / LPR;                  // rows of a pass
+    const int lr = tid / LPR, c = tid % LPR, d0 = 8 * c;
+    const bool lane_on = lr < RPP && d0 < p.D;
+
+    float mx[3] = {0.f, 0.f, 0.f};                        // k, v, r; values that are not finite do not count
+    auto see = [&](int which, float a) {
+        if (a < INFINITY) mx[which] = fmaxf(mx[which], a);
+    };
+    const int64_t x1 = static_cast<int64_t>(r1) * G;
+#pragma unroll 4
+    for (int64_t x = static_cast<int64_t>(r0) * G + tid; x < x1; x += kXThreads) {
+        const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + (slot_row(t) * G + g) * 4));
+        const uint32_t kv[2] = {w.x, w.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float step = __uint_as_float(kv[i] << 16), lo = __uint_as_float(kv[i] & 0xffff0000u);
+            see(i, fmaxf(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo))));
+        }
+    }
+    if (lane_on)
+#pragma unroll 2
+        for (int t = s0 + lr; t < s1; t += RPP) {
+            float xk[8], xv[8];
+            load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, t), d0, p.D, p.vec_k, 0.f, xk);
+            load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, t), d0, p.D, p.vec_v, 0.f, xv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                see(0, fabsf(xk[e]));
+                see(1, fabsf(xv[e]));
+            }
+        }
+    const int samples = min(p.n_r, 64);                   // the same rows in every CTA of the head
+    if (lane_on)
+        for (int i = lr; i < samples; i += RPP) {
+            const int64_t row = static_cast<int64_t>(share(p.n_r - 1, i, max(samples - 1, 1))) * p.H + h;
+            float x[8];
+            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) see(2, fabsf(x[e]));
+        }
+    float inv[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+        if ((tid & 31) == 0) red[i][tid >> 5] = mx[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+        for (int w = 0; w < kXThreads / 32; ++w) mx[i] = fmaxf(mx[i], red[i][w]);
+        if (tid == 0 && i < 2) rank_max[i] = mx[i];
+    }
+    if (ranks > 1) {
+        __syncthreads();
+        cluster_sync_all();
+        for (int r = 0; r < ranks; ++r) {
+            mx[0] = fmaxf(mx[0], ld_rank(&rank_max[0], r));
+            mx[1] = fmaxf(mx[1], ld_rank(&rank_max[1], r));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int ex = min(max(static_cast<int>(__float_as_uint(mx[i]) >> 23) - 127 - (i == 1 ? 11 : 0), -115), 115);
+        inv[i] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        if (rank == 0 && tid == 0) p.units[4 * bh + i] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+    }
+
+    auto put = [&](void* base, int64_t row, const float* x, float f) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row * p.ld + d0) =
+            make_uint4(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f), pack_f16x2(x[4] * f, x[5] * f),
+                       pack_f16x2(x[6] * f, x[7] * f));
+    };
+    if (lane_on) {
+        for (int t0 = r0 + lr; t0 < r1; t0 += kXRows * RPP) {
+            uint32_t ck[kXRows][2], cv[kXRows][2];
+            uint2 par[kXRows];
+#pragma unroll
+            for (int k = 0; k < kXRows; ++k) {
+                const int t = t0 + k * RPP;
+                if (t >= r1) break;
+                const int64_t row = slot_row(t), at = row * (4 * G * BITS) + d0 * BITS / 8;
+                if constexpr (BITS == 4) {
+                    ck[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
+                    cv[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
+                } else {
+                    const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at));
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.v + at));
+                    ck[k][0] = a.x; ck[k][1] = a.y; cv[k][0] = w.x; cv[k][1] = w.y;
+                }
+                par[k] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * G + (c >> 2)) * 4));
+            }
+#pragma unroll
+            for (int k = 0; k < kXRows; ++k) {
+                const int t = t0 + k * RPP;
+                if (t >= r1) break;
+                float x[8];
+                expand8<BITS>(ck[k], par[k].x, x);
+                put(p.k_mem, bh * p.n + t, x, inv[0]);
+                expand8<BITS>(cv[k], par[k].y, x);
+                put(p.v_mem, bh * p.n + t, x, inv[1]);
+            }
+        }
+#pragma unroll 2
+        for (int t = s0 + lr; t < s1; t += RPP) {
+            float x[8];
+            load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, t), d0, p.D, p.vec_k, 0.f, x);
+            put(p.k_seg, bh * p.L + t, x, inv[0]);
+            load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, t), d0, p.D, p.vec_v, 0.f, x);
+            put(p.v_seg, bh * p.L + t, x, inv[1]);
+            if (p.q_seg) {
+                load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh, t), d0, p.D, p.vec_q, 0.f, x);
+                store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
+            }
+        }
+        // this head's rows of r, shared out over the batch entries and ranks
+        const int64_t part = static_cast<int64_t>(b) * ranks + rank, parts = static_cast<int64_t>(p.B) * ranks;
+        for (int t = share(p.n_r, part, parts) + lr; t < share(p.n_r, part + 1, parts); t += RPP) {
+            float x[8];
+            const int64_t row = static_cast<int64_t>(t) * p.H + h;
+            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.r16) + row * p.ld + d0) =
+                make_uint4(pack_f16x2_sat(x[0] * inv[2], x[1] * inv[2]), pack_f16x2_sat(x[2] * inv[2], x[3] * inv[2]),
+                           pack_f16x2_sat(x[4] * inv[2], x[5] * inv[2]), pack_f16x2_sat(x[6] * inv[2], x[7] * inv[2]));
+        }
+    }
+    __syncthreads();
+    if (ranks > 1) cluster_sync_all();                    // rank_max stays until every rank has read it
+}
+
+template <int BITS, int G>
+cudaError_t launch_expand(const QexpandParams& p, int ranks, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks, p.H, p.B);
+    cfg.blockDim = dim3(kXThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, qmem_expand_kernel<BITS, G>, p, ranks);
+}
+
 template <int BITS, int G>
 cudaError_t launch(const QmemParams& p, bool f32, bool push, cudaStream_t s)
 {
@@ -294,6 +477,26 @@ cudaError_t launch_any(const QmemParams& p, txl_dtype dtype, bool push, cudaStre
 }
 
 }  // namespace
+
+cudaError_t launch_qmem_expand(const QexpandParams& p, int sm_count, cudaStream_t s)
+{
+    // CTAs per (b, h): until eight per SM, while each keeps 128 rows
+    int ranks = 1;
+    while (ranks < 8 && static_cast<int64_t>(p.B) * p.H * ranks < 8 * sm_count &&
+           static_cast<int64_t>(p.n) + p.L > 128 * ranks)
+        ranks *= 2;
+    switch (p.G * 16 + (p.n > 0 ? p.bits : 4)) {
+    case 1 * 16 + 4: return launch_expand<4, 1>(p, ranks, s);
+    case 2 * 16 + 4: return launch_expand<4, 2>(p, ranks, s);
+    case 3 * 16 + 4: return launch_expand<4, 3>(p, ranks, s);
+    case 4 * 16 + 4: return launch_expand<4, 4>(p, ranks, s);
+    case 1 * 16 + 8: return launch_expand<8, 1>(p, ranks, s);
+    case 2 * 16 + 8: return launch_expand<8, 2>(p, ranks, s);
+    case 3 * 16 + 8: return launch_expand<8, 3>(p, ranks, s);
+    case 4 * 16 + 8: return launch_expand<8, 4>(p, ranks, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
 
 cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t s)
 {

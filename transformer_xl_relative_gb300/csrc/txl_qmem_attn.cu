@@ -109,20 +109,6 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src, uint32_t s
 
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void cluster_sync_all()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ float ld_rank(const float* p, uint32_t rank)       // this address in another CTA of the cluster
-{
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-
 // Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
 // large at 4 bits).  `half` selects the upper byte (4 bits).
 template <int BITS>
