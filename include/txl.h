@@ -448,11 +448,14 @@ int txl_rel_attn_table_path(int B, int L, int H, int D, int max_len,
  * and stands for x'_d = lo + step * c_d, so |x'_d - x_d| <= step / 2.  These definitions are met
  * exactly, whatever the input type.  A group with a NaN or an infinity, or one whose lo, step or
  * max - lo is not finite, is held with step = lo = NaN and stands for NaN throughout.
- *   k, v : device, 16-byte aligned, dense [B][H][M][G * 4 * bits] bytes.  The bytes of a row hold
- *          the codes in the order of d (4 bits: byte t holds d = 2t in its low and d = 2t + 1 in
- *          its high half); codes of d >= D in the last group are 0.
- *   par  : device, 16-byte aligned, dense bf16 [B][H][M][G][4]: the k step, k lo, v step and v lo
- *          of each group.
+ *   k, v : device, 16-byte aligned, dense [B][H][M][G * 4 * bits] bytes.  A row holds the codes in
+ *          the order of d (4 bits: byte t holds d = 2t in its low and d = 2t + 1 in its high half;
+ *          codes of d >= D in the last group are 0), its 16-byte chunks permuted by slot: of nc
+ *          chunks, chunk c of slot s lies at position c ^ ((s >> 2) & 1) for nc = 2, c ^ ((s >> 1) & 3)
+ *          for nc = 4, c ^ (s & 7) for nc = 8, else at c.  (Rows copied to shared memory as they are
+ *          can then be read column by column without bank conflicts.)
+ *   par  : device, 16-byte aligned, dense bf16 [B][H][M][2 ceil(G/2)][4]: the k step, k lo, v step
+ *          and v lo of each group (zeros for the group that makes their number even).
  *   bits : 4 or 8.  D <= 128.
  *   wp, valid : as in txl_mem (logical key j in slot (wp + j) mod M, valid iff j >= M - valid).
  * Slots that are not valid are never read, so the arrays need no initial values.  M = 0 means no

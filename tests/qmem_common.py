@@ -81,9 +81,15 @@ def held(x: np.ndarray, bits: int) -> np.ndarray:
     return v.reshape(code.shape)[..., : x.shape[-1]]
 
 
-def unpack(code: torch.Tensor, bits: int) -> np.ndarray:
-    """The code bytes of a QuantMemory as codes in the order of d."""
+def unpack(code: torch.Tensor, bits: int, slots) -> np.ndarray:
+    """The code bytes [B, H, n, row] of the given slots of a QuantMemory as codes in the order of d."""
     c = code.cpu().numpy()
+    nc = c.shape[-1] // 16
+    s = np.asarray(slots)
+    swap = {2: (s >> 2) & 1, 4: (s >> 1) & 3, 8: s & 7}.get(nc, 0 * s)
+    at = np.arange(nc)[None] ^ swap[:, None]                          # position of chunk c in each row
+    c = c.reshape(c.shape[:3] + (nc, 16))
+    c = np.take_along_axis(c, at[None, None, :, :, None], 3).reshape(c.shape[:3] + (-1,))
     if bits == 8:
         return c
     return np.stack((c & 15, c >> 4), -1).reshape(c.shape[:-1] + (-1,))

@@ -54,9 +54,12 @@ def fresh(txl, B, M, H, D, bits, wp=0, valid=0, fill=0xA5):
 def expect_slots(mem, x, which, slots, bits):
     """Codes and parameters of x [B, n, H, D] in the given slots."""
     code, step, lo = quantise64(f64(x).transpose(0, 2, 1, 3), bits)
-    got = unpack(getattr(mem, which)[:, :, slots], bits)
+    got = unpack(getattr(mem, which)[:, :, slots], bits, slots)
     np.testing.assert_array_equal(got, code)
     par = f64(mem.par[:, :, slots])
+    G = step.shape[-1]
+    assert (par[..., G:, :] == 0).all()
+    par = par[..., :G, :]
     o = 0 if which == "k" else 2
     np.testing.assert_array_equal(par[..., o], step)
     np.testing.assert_array_equal(par[..., o + 1], lo)
@@ -149,7 +152,7 @@ def test_push_at_the_edges(txl, dtype, bits):
     txl.qmem_push(mem, k, k)
     torch.cuda.synchronize()
     for which, o in (("k", 0), ("v", 2)):
-        codes = unpack(getattr(mem, which)[0, 0], bits)
+        codes = unpack(getattr(mem, which)[:1, :1], bits, np.arange(n))[0, 0]
         par = f64(mem.par[0, 0, :, 0])
         for i, (code, step, lo) in enumerate(ref):
             assert par[i, o] == step and par[i, o + 1] == lo, (i, par[i], step, lo)

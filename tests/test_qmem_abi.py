@@ -37,6 +37,8 @@ def test_sizes(native):
     assert lib.txl_qmem_code_bytes(1, 1, 1, 41, 4) == 32            # two groups
     assert lib.txl_qmem_code_bytes(1, 70000, 2, 128, 8) == 70000 * 2 * 128
     assert lib.txl_qmem_par_bytes(1, 3, 2, 41) == 3 * 2 * 2 * 8
+    assert lib.txl_qmem_par_bytes(1, 3, 2, 65) == 3 * 2 * 4 * 8     # three groups, kept as four
+    assert lib.txl_qmem_par_bytes(1, 3, 2, 32) == 3 * 2 * 2 * 8
     assert lib.txl_qmem_code_bytes(65535, 2 ** 31 - 1, 1, 128, 8) == 65535 * (2 ** 31 - 1) * 128
     for bad in ((0, 1, 1, 64, 4), (1, 0, 1, 64, 4), (1, 1, 1, 129, 4), (1, 1, 1, 64, 3), (1, -1, 1, 64, 4)):
         assert lib.txl_qmem_code_bytes(*bad) == 0

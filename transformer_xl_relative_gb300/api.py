@@ -408,7 +408,7 @@ def rel_attn_table_path(q, k, v, r_table, max_len: int, out, key_mask=None) -> i
 class QuantMemory:
     """K/V memory of M positions per batch entry held as 4- or 8-bit codes (txl_qmem): groups of 32
     channels of a head share a bf16 step and minimum.  ``k`` and ``v`` are uint8 [B, H, M, row bytes],
-    ``par`` bf16 [B, H, M, groups, 4]; ``wp``/``valid`` as in Memory.  Filled by qmem_push, read by
+    ``par`` bf16 [B, H, M, groups (an even number), 4]; ``wp``/``valid`` as in Memory.  Filled by qmem_push, read by
     rel_attn_qmem and qmem_read."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, par: torch.Tensor, D: int, bits: int, wp: int = 0,
@@ -421,11 +421,12 @@ class QuantMemory:
             raise ValueError("k and v must be uint8 [B, H, M, row bytes]")
         B, H, M, _ = k.shape
         G = (D + 31) // 32
+        GP = (G + 1) // 2 * 2
         for t, shape, dtype in ((k, (B, H, M, 4 * G * bits), torch.uint8), (v, (B, H, M, 4 * G * bits), torch.uint8),
-                                (par, (B, H, M, G, 4), torch.bfloat16)):
+                                (par, (B, H, M, GP, 4), torch.bfloat16)):
             if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != k.device:
                 raise ValueError("a quantised memory holds contiguous uint8 k, v %s and bf16 par %s on one device"
-                                 % ((B, H, M, 4 * G * bits), (B, H, M, G, 4)))
+                                 % ((B, H, M, 4 * G * bits), (B, H, M, GP, 4)))
         if not k.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
         self.k, self.v, self.par = k, v, par
@@ -436,7 +437,7 @@ class QuantMemory:
     def empty(cls, B, M, H, D, bits=4, device="cuda"):
         G = (D + 31) // 32
         code = [torch.zeros(B, H, M, 4 * G * bits, dtype=torch.uint8, device=device) for _ in range(2)]
-        return cls(*code, torch.zeros(B, H, M, G, 4, dtype=torch.bfloat16, device=device), D, bits)
+        return cls(*code, torch.zeros(B, H, M, (G + 1) // 2 * 2, 4, dtype=torch.bfloat16, device=device), D, bits)
 
     @property
     def M(self) -> int:

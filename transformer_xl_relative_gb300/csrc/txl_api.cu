@@ -1111,7 +1111,7 @@ size_t txl_qmem_code_bytes(int B, int M, int H, int D, int bits)
 size_t txl_qmem_par_bytes(int B, int M, int H, int D)
 {
     if (B <= 0 || M <= 0 || H <= 0 || D <= 0 || D > 128) return 0;
-    return static_cast<size_t>(B) * H * M * q_groups(D) * 8;
+    return static_cast<size_t>(B) * H * M * q_par_groups(q_groups(D)) * 8;
 }
 
 txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v_new, int L, txl_dtype dtype,
@@ -1258,6 +1258,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.qscale = scale * 1.4426950408889634f;
     const int elem = dtype == TXL_F32 ? 4 : 2;
     p.vec_r = a16(r) && s16(ld_r, elem);
+    p.err_flag = err_flag;
     p.chk = range_counter();
     const int sms = sm_count();
     if (sms <= 0) return TXL_ERR_CUDA;

@@ -269,6 +269,14 @@ cudaError_t launch_mem_push(const MemPushParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- quantised memory
 constexpr int kQGroup = 32;         // channels that share a step and a minimum
+// Groups of the parameter rows of G groups: even, so that a row is 16 or 32 bytes.
+__host__ __device__ constexpr int q_par_groups(int G) { return (G + 1) & ~1; }
+// A code row of nc 16-byte chunks holds chunk c at position c ^ q_swizzle(nc, slot): eight consecutive
+// rows, copied to shared memory as they are, then hold one chunk in eight different bank groups.
+__host__ __device__ constexpr int q_swizzle(int nc, int slot)
+{
+    return nc == 2 ? (slot >> 2) & 1 : nc == 4 ? (slot >> 1) & 3 : nc == 8 ? slot & 7 : 0;
+}
 
 // Push (positions t0 .. t0+n-1 of the segment into slots (slot0 + t) mod M) and read (n logical
 // positions from slot slot0 on into t = 0 .. n-1) of a quantised memory.  x_*: the k and v tensors
@@ -277,7 +285,7 @@ struct QmemParams {
     void* xk; int64_t xk_sb, xk_st, xk_sh;
     void* xv; int64_t xv_sb, xv_st, xv_sh;
     uint8_t* k; uint8_t* v;             // [B][H][M][G * 4 * bits]
-    uint16_t* par;                      // bf16 [B][H][M][G][4]
+    uint16_t* par;                      // bf16 [B][H][M][q_par_groups(G)][4]
     int B, H, D, M, G, bits;
     int slot0, t0, n;
     int vec_k, vec_v;                   // every row of the tensor starts on a 16-byte boundary
@@ -320,6 +328,7 @@ struct QattnParams {
     int n_rows;
     float qscale;                               // scale * log2(e)
     int vec_r;                                  // rows of r start on 16-byte boundaries
+    int* err_flag;                              // TXL_ERR_TIMEOUT on a wait abandoned, may be null
     int* chk;                                   // range-check counter (checked build)
 };
 cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s);

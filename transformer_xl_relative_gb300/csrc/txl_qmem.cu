@@ -164,8 +164,18 @@ __device__ __forceinline__ uint32_t par_word(float step, float lo)
     return (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
+// Byte offset, in the code arrays, of the eight channels from d0 of a row.
+template <int BITS, int G>
+__device__ __forceinline__ int64_t code_at(int64_t row, int slot, int d0)
+{
+    constexpr int NC = G * BITS / 4;
+    const int byte = d0 * BITS / 8;
+    return row * (16 * NC) + ((((byte >> 4) ^ q_swizzle(NC, slot)) << 4) | (byte & 15));
+}
+
 struct QPos {
     int64_t row;          // row of the code and parameter arrays
+    int slot;
     int t, g, d0;         // position of the segment, group, first channel of the lane
 };
 
@@ -183,6 +193,7 @@ __device__ __forceinline__ bool q_pos(const QmemParams& p, int64_t i, QPos& o)
     if (slot >= p.M) slot -= p.M;
     const bool live = t < p.n;
     if (live && !in_range(slot, 0, p.M, p.chk)) slot = 0;
+    o.slot = static_cast<int>(slot);
     o.row = (static_cast<int64_t>(blockIdx.z) * p.H + blockIdx.y) * p.M + slot;
     return live;
 }
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_push_kernel(const __grid_const
     quantise8<BITS>(xk, live, ck, ks, kl);
     quantise8<BITS>(xv, live, cv, vs, vl);
     if (!on) return;
-    const int64_t at = o.row * (4 * G * BITS) + o.d0 * BITS / 8;
+    const int64_t at = code_at<BITS, G>(o.row, o.slot, o.d0);
     if constexpr (BITS == 4) {
         *reinterpret_cast<uint32_t*>(p.k + at) = ck[0];
         *reinterpret_cast<uint32_t*>(p.v + at) = cv[0];
@@ -221,8 +232,11 @@ __global__ void __launch_bounds__(kQThreads) qmem_push_kernel(const __grid_const
         *reinterpret_cast<uint2*>(p.k + at) = make_uint2(ck[0], ck[1]);
         *reinterpret_cast<uint2*>(p.v + at) = make_uint2(cv[0], cv[1]);
     }
-    if ((o.d0 & (kQGroup - 1)) == 0)
-        *reinterpret_cast<uint2*>(p.par + (o.row * G + o.g) * 4) = make_uint2(par_word(ks, kl), par_word(vs, vl));
+    if ((o.d0 & (kQGroup - 1)) == 0) {
+        uint2* par = reinterpret_cast<uint2*>(p.par + o.row * q_par_groups(G) * 4) + o.g;
+        *par = make_uint2(par_word(ks, kl), par_word(vs, vl));
+        if (G < q_par_groups(G) && o.g == G - 1) par[1] = make_uint2(0, 0);     // the group that fills the row up
+    }
 }
 
 template <int BITS>
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
     if (!q_pos<G>(p, i, o)) return;
     constexpr int E = F32 ? 4 : 2;
-    const int64_t at = o.row * (4 * G * BITS) + o.d0 * BITS / 8;
+    const int64_t at = code_at<BITS, G>(o.row, o.slot, o.d0);
     uint32_t ck[2], cv[2];
     if constexpr (BITS == 4) {
         ck[0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
         const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at)), b = __ldg(reinterpret_cast<const uint2*>(p.v + at));
         ck[0] = a.x; ck[1] = a.y; cv[0] = b.x; cv[1] = b.y;
     }
-    const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (o.row * G + o.g) * 4));
+    const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (o.row * q_par_groups(G) + o.g) * 4));
     float xk[8], xv[8];
     expand8<BITS>(ck, par.x, xk);
     expand8<BITS>(cv, par.y, xv);
@@ -287,11 +301,11 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
     auto share = [](int64_t n, int64_t part, int64_t parts) { return static_cast<int>(n * part / parts); };
     const int r0 = share(p.n, rank, ranks), r1 = share(p.n, rank + 1, ranks);
     const int s0 = share(p.L, rank, ranks), s1 = share(p.L, rank + 1, ranks);
-    auto slot_row = [&](int t) {
+    auto slot_of = [&](int t) {
         int64_t s = static_cast<int64_t>(p.slot0) + t;
         if (s >= p.M) s -= p.M;
         if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        return bh * p.M + s;
+        return static_cast<int>(s);
     };
     auto seg = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int t) {
         return static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh;
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
 #pragma unroll 4
     for (int64_t x = static_cast<int64_t>(r0) * G + tid; x < x1; x += kXThreads) {
         const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + (slot_row(t) * G + g) * 4));
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + ((bh * p.M + slot_of(t)) * q_par_groups(G) + g) * 4));
         const uint32_t kv[2] = {w.x, w.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -380,7 +394,8 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
             for (int k = 0; k < kXRows; ++k) {
                 const int t = t0 + k * RPP;
                 if (t >= r1) break;
-                const int64_t row = slot_row(t), at = row * (4 * G * BITS) + d0 * BITS / 8;
+                const int slot = slot_of(t);
+                const int64_t row = bh * p.M + slot, at = code_at<BITS, G>(row, slot, d0);
                 if constexpr (BITS == 4) {
                     ck[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
                     cv[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
                     const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.v + at));
                     ck[k][0] = a.x; ck[k][1] = a.y; cv[k][0] = w.x; cv[k][1] = w.y;
                 }
-                par[k] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * G + (c >> 2)) * 4));
+                par[k] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(G) + (c >> 2)) * 4));
             }
 #pragma unroll
             for (int k = 0; k < kXRows; ++k) {

@@ -28,7 +28,8 @@
 // entries, which share every r row.  Distances at or past the clamp share one entry.
 //
 // One CTA: NB batch entries x one head x a range of keys; 8 / NB warps per entry, each with its own
-// ring of cp.async stages (no block barriers in the key loop).  The key ranges of a head are the ranks
+// ring of bulk-copy stages (no block barriers between the stages of a band; cp.async, 16 bytes per lane,
+// held the issuing warp for 2400 to 4000 cycles per stage until its requests were accepted).  The key ranges of a head are the ranks
 // of a cluster, merged through distributed shared memory.
 #include <algorithm>
 
@@ -46,6 +47,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+constexpr int kMaxRanks = 16;                  // CTAs of a cluster (beyond 8: not portable, but this GPU's)
 constexpr int kMaxRows = 8;                    // (batch entry, query) rows of a CTA
 constexpr int kBandBytes = 16384;              // of position terms: 16384 / (4 rows) keys per block
 constexpr int kBandPad = 40;                   // floats after a row's keys: up to 22 more entries; rows 8 banks apart
@@ -65,7 +67,6 @@ struct QSplit {               // how the host divides the work
     int range;                // keys of a range (a multiple of the stage)
     int block;                // keys of a position band
     int pitch;                // floats between band rows
-    int nc_mul;               // 65536 / (16-byte chunks of a code row) + 1
 };
 
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
@@ -101,14 +102,6 @@ __device__ __forceinline__ uint32_t split_f16(float x)
     return __half_as_ushort(hi) | half_bits(x - __half2float(hi)) << 16;
 }
 
-__device__ __forceinline__ void cp_async8(void* dst, const void* src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
-                 : "memory");
-}
-
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
 // large at 4 bits).  `half` selects the upper byte (4 bits).
 template <int BITS>
@@ -122,18 +115,23 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
     constexpr int DP = NG * 32;                           // channels, padded
     constexpr int NC = NG * BITS / 4;                     // 16-byte chunks of a code row
     constexpr int KS = stage_keys(BITS, NG);
-    constexpr int kParOff = KS * 2 * NC * 16;             // of a stage: k chunks, v chunks, parameters
+    constexpr int kVOff = KS * NC * 16, kParOff = 2 * kVOff;   // of a stage: k rows, v rows, parameters
     constexpr int kStageBytes = stage_bytes(BITS, NG);
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per chunk and product
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kBandTiles = NG == 2 ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* stages = smem;
     float* band = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
-    float* qu = band + kBandBytes / 4 + kMaxRows * kBandPad;    // [row][DP], scaled into fp16's range
-    float* qv = qu + kMaxRows * DP;                       // [row][DP], log2 units
-    float* norm = qv + kMaxRows * DP;                     // [row]: qu times this is in log2 units
-    float* mine = norm + kMaxRows;                        // [row][DP + 2]: this CTA's O, m, l
-    uint16_t* qvh = reinterpret_cast<uint16_t*>(mine + kMaxRows * (DP + 2));   // [2 row + part][DP] bf16 parts of qv
-
+    float* qu = band + kBandBytes / 4 + kMaxRows * kBandPad;   // [row][DP]: (q+u) and (q+v) in log2 units
+    float* qv = qu + kMaxRows * DP;
+    float* mine = qv + kMaxRows * DP;                     // [row][DP + 2]: this CTA's O, m, l
+    float* norm = mine + kMaxRows * (DP + 2);             // [row]: what the fp16 parts of qu are multiples of
+    float* qsum = norm + kMaxRows;                        // [row][NG]: group sums of qu
+    float* own_s = qsum + kMaxRows * NG;                  // [row][kDecodeMaxL]: scores of the segment's own keys
+    uint16_t* quh = reinterpret_cast<uint16_t*>(own_s + kMaxRows * kDecodeMaxL);   // [2 row + part][DP] fp16 parts of qu
+    uint16_t* qvh = quh + 2 * kMaxRows * DP;              // [2 row + part][DP] bf16 parts of qv
+    uint64_t* bars = reinterpret_cast<uint64_t*>(qvh + 2 * kMaxRows * DP);   // [warp][stage]: copies landed
+    int* abort_flag = reinterpret_cast<int*>(bars + kWarps * kStages);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
     const int rank = blockIdx.x % sp.ranks, i0 = blockIdx.x / sp.ranks * sp.lq;
     const int h = blockIdx.y, b0 = blockIdx.z * sp.nb;
@@ -144,90 +142,91 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
     const int lp_log = Lq >= 3 ? 2 : Lq - 1, Lp = 1 << lp_log;
     const int NS = min(4 >> lp_log, KS / 16);
     pdl_launch_dependents();
+    if (tid == 0) *abort_flag = 0;
+    __syncthreads();
+    const WaitCtl wc{abort_flag, p.err_flag, kWaitTimeoutNs};
     pdl_wait();
 
     const int j_lo = static_cast<int>(min(static_cast<int64_t>(p.M), p.lo + static_cast<int64_t>(rank) * sp.range));
     const int j_hi = static_cast<int>(min(static_cast<int64_t>(p.M), static_cast<int64_t>(j_lo) + sp.range));
 
-    // ---- this warp's copies: stage n covers keys j_lo + (n * wpe + sw) * KS ..
+    // ---- this warp's copies: stage n covers keys j_lo + (n * wpe + sw) * KS ..; rows as they are in memory,
+    // one bulk copy each for the k codes, the v codes and the parameters, two where the ring wraps
     uint8_t* my_stages = stages + warp * kStages * kStageBytes;
+    uint64_t* full = bars + warp * kStages;
     const int n_stage = b < p.B ? max(0, (j_hi - j_lo - sw * KS + wpe * KS - 1) / (wpe * KS)) : 0;
-    const int64_t head_row = (static_cast<int64_t>(b) * p.H + h) * p.M;
-    const int nc = p.G * BITS / 4;
-    auto copy_stage = [&](int n) {
-        if (n < n_stage) {
-            uint8_t* st = my_stages + (n % kStages) * kStageBytes;
-            const int j = j_lo + (n * wpe + sw) * KS;
-            const int live = min(KS, j_hi - j);
-            int64_t slot0 = static_cast<int64_t>(p.wp) + j;
-            if (slot0 >= p.M) slot0 -= p.M;
-            auto row_of = [&](int r) {
-                int64_t s = slot0 + r;
-                if (s >= p.M) s -= p.M;
-                if (!in_range(r < live ? s : 0, 0, p.M, p.chk)) s = 0;
-                return r < live ? head_row + s : head_row;
-            };
-            for (int x = lane; x < KS * nc; x += 32) {
-                const int r = (x * sp.nc_mul) >> 16, c = x - r * nc;
-                const int64_t at = (row_of(r) * nc + c) * 16;
-                const uint32_t bytes = r < live ? 16u : 0u;
-                mma::cp_async16(st + (c * KS + r) * 16, p.k + at, bytes);
-                mma::cp_async16(st + ((NC + c) * KS + r) * 16, p.v + at, bytes);
-            }
-            if (p.G & 1) {
-                for (int x = lane; x < KS * p.G; x += 32) {
-                    const int r = p.G == 1 ? x : x / 3, c = x - r * p.G;
-                    cp_async8(st + kParOff + r * 8 * NG + 8 * c, p.par + (row_of(r) * p.G + c) * 4, r < live ? 8u : 0u);
-                }
-            } else {
-                for (int x = lane; x < KS * (p.G >> 1); x += 32) {
-                    const int r = p.G == 2 ? x : x >> 1, c = p.G == 2 ? 0 : x & 1;
-                    mma::cp_async16(st + kParOff + r * 8 * NG + 16 * c, p.par + (row_of(r) * p.G + 2 * c) * 4,
-                                    r < live ? 16u : 0u);
-                }
-            }
-        }
-        mma::cp_async_commit();
+    const int nc = p.G * BITS / 4, row_bytes = nc * 16;
+    auto slot_of = [&](int j) {                           // of a logical key, j < 2^31 - M
+        const int64_t s = static_cast<int64_t>(p.wp) + j;
+        return static_cast<int>(s >= p.M ? s - p.M : s);
     };
-    if (p.G != NG) {                                      // parameters of groups past G stay zero
-        for (int x = lane; x < kStages * KS * NG; x += 32) {
-            const int st = x / (KS * NG), rem = x % (KS * NG);
-            if (rem % NG >= p.G) *reinterpret_cast<uint2*>(my_stages + st * kStageBytes + kParOff + 8 * rem) = make_uint2(0, 0);
-        }
-        __syncwarp();
-    }
+    auto copy_stage = [&](int n) {                        // one lane
+        uint8_t* st = my_stages + (n % kStages) * kStageBytes;
+        const int j = j_lo + (n * wpe + sw) * KS;
+        const int live = min(KS, j_hi - j);
+        int slot = slot_of(j);
+        if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
+        mbar_expect_tx(&full[n % kStages], live * (2 * row_bytes + 8 * NG));
+        auto rows = [&](int at, int s, int count) {
+            const int64_t row = (static_cast<int64_t>(b) * p.H + h) * p.M + s;
+            bulk_load(st + at * row_bytes, p.k + row * row_bytes, count * row_bytes, &full[n % kStages]);
+            bulk_load(st + kVOff + at * row_bytes, p.v + row * row_bytes, count * row_bytes, &full[n % kStages]);
+            bulk_load(st + kParOff + at * 8 * NG, p.par + row * NG * 4, count * 8 * NG, &full[n % kStages]);
+        };
+        const int first = min(live, p.M - slot);
+        rows(0, slot, first);
+        if (first < live) rows(first, 0, live - first);
+    };
+    if (lane == 0) {
 #pragma unroll
-    for (int n = 0; n < kStages - 1; ++n) copy_stage(n);
+        for (int n = 0; n < kStages; ++n) mbar_init(&full[n], 1);
+        fence_mbar_init();
+#pragma unroll
+        for (int n = 0; n < kStages; ++n)
+            if (n < n_stage) copy_stage(n);
+    }
+    __syncwarp();
 
-    // ---- queries: (q+u), (q+v) times scale log2 e; rows past the last batch entry are zero
-    for (int x = tid; x < kMaxRows * DP; x += kThreads) {
-        const int row = x / DP, d = x % DP;
-        const int be = b0 + row / Lq, i = i0 + row % Lq;
-        float a = 0.f, c = 0.f;
-        if (row < rows && be < p.B && d < p.D) {
-            const float q = ld_elem(p.q, be * p.q_sb + i * p.q_st + h * p.q_sh + d, p.f32);
-            a = (q + __ldg(p.u + h * p.D + d)) * p.qscale;
-            c = (q + __ldg(p.vb + h * p.D + d)) * p.qscale;
-        }
-        qu[x] = a;
-        qv[x] = c;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(c);
-        qvh[2 * row * DP + d] = __bfloat16_as_ushort(hi);
-        qvh[(2 * row + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
-    }
-    __syncthreads();
+    // ---- queries: warp w prepares row w: (q+u), (q+v) times scale log2 e in fp32; (q+u) scaled by a power
+    // of two so that its largest entry lies in [2^11, 2^12) as two fp16 parts, in the order in which the
+    // B operands of a chunk take them (4 bits: d = 0 4 1 5 2 6 3 7 of every eight, odd ones over 16; 8 bits:
+    // 0 2 1 3 of every four); (q+v) as two bf16 parts.  Rows past the last query are zero.
     {
-        // each row of qu scaled by a power of two so that its largest entry lies in [2^11, 2^12)
-        float mx = 0.f;
+        const int row = warp, be = b0 + row / Lq, i = i0 + row % Lq;
+        float a[NG], c[NG], mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < NG; ++e) mx = fmaxf(mx, fabsf(qu[warp * DP + 32 * e + lane]));
+        for (int e = 0; e < NG; ++e) {
+            const int d = 32 * e + lane;
+            a[e] = c[e] = 0.f;
+            if (row < rows && be < p.B && d < p.D) {
+                const float q = ld_elem(p.q, be * p.q_sb + i * p.q_st + h * p.q_sh + d, p.f32);
+                a[e] = (q + __ldg(p.u + h * p.D + d)) * p.qscale;
+                c[e] = (q + __ldg(p.vb + h * p.D + d)) * p.qscale;
+            }
+            mx = fmaxf(mx, fabsf(a[e]));
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
         const float up = __uint_as_float(static_cast<uint32_t>(11 - ex + 127) << 23);
+        if (lane == 0) norm[row] = __uint_as_float(static_cast<uint32_t>(ex - 11 + 127) << 23);
 #pragma unroll
-        for (int e = 0; e < NG; ++e) qu[warp * DP + 32 * e + lane] *= up;
-        if (lane == 0) norm[warp] = __uint_as_float(static_cast<uint32_t>(ex - 11 + 127) << 23);
+        for (int e = 0; e < NG; ++e) {
+            const int d = 32 * e + lane;
+            qu[row * DP + d] = a[e];
+            qv[row * DP + d] = c[e];
+            const int at = BITS == 4 ? (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1) : (d & ~3) + ((d & 1) << 1) + ((d >> 1) & 1);
+            const uint32_t w = split_f16(a[e] * (BITS == 4 && (d & 1) ? up * 0.0625f : up));
+            quh[2 * row * DP + at] = static_cast<uint16_t>(w);
+            quh[(2 * row + 1) * DP + at] = static_cast<uint16_t>(w >> 16);
+            const __nv_bfloat16 hi = __float2bfloat16_rn(c[e]);
+            qvh[2 * row * DP + d] = __bfloat16_as_ushort(hi);
+            qvh[(2 * row + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c[e] - __bfloat162float(hi)));
+            float sum = a[e];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) qsum[row * NG + e] = sum;
+        }
     }
     __syncthreads();
 
@@ -238,30 +237,50 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int il = min(((g >> 1) & (Lp - 1)) + 4 * t, Lq - 1);
-        const float* row = qu + (bs * Lq + il) * DP;
-        auto part = [&](int d, float f) {
-            const uint32_t w = split_f16(row[d] * f);
-            return g & 1 ? w >> 16 : w & 0xffffu;
-        };
+        const uint16_t* row = quh + (2 * (bs * Lq + il) + (g & 1)) * DP;
 #pragma unroll
-        for (int ks = 0; ks < NG * 2; ++ks) {
+        for (int G = 0; G < NG; ++G) {
             if constexpr (BITS == 4) {
-                const int d = 32 * (ks >> 1) + 8 * c4 + 2 * (ks & 1);
-                bq[t][ks][0] = part(d, 1.f) | part(d + 4, 1.f) << 16;
-                bq[t][ks][1] = part(d + 1, 0.0625f) | part(d + 5, 0.0625f) << 16;
+                const uint4 w = *reinterpret_cast<const uint4*>(row + 32 * G + 8 * c4);
+                bq[t][2 * G][0] = w.x; bq[t][2 * G][1] = w.y;
+                bq[t][2 * G + 1][0] = w.z; bq[t][2 * G + 1][1] = w.w;
             } else {
-                const int d = 16 * ks + 4 * c4;
-                bq[t][ks][0] = part(d, 1.f) | part(d + 2, 1.f) << 16;
-                bq[t][ks][1] = part(d + 1, 1.f) | part(d + 3, 1.f) << 16;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(row + 32 * G + 16 * x + 4 * c4);
+                    bq[t][2 * G + x][0] = w.x; bq[t][2 * G + x][1] = w.y;
+                }
             }
         }
         const int is = bs * Lq + min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
         sc[t] = norm[is] * kTwo24;
 #pragma unroll
-        for (int G = 0; G < NG; ++G) {
+        for (int G = 0; G < NG; ++G) qs[t][G] = qsum[is * NG + G];
+    }
+
+    // ---- scores of the segment's own keys (the last rank's work): eight lanes per (row, key)
+    const bool has_own = rank == sp.ranks - 1;
+    const int n_own = i0 + Lq;                            // keys any of these queries sees
+    if (has_own) {
+        for (int x0 = warp * 4; x0 < rows * n_own; x0 += kWarps * 4) {
+            const int x = min(x0 + (lane >> 3), rows * n_own - 1);
+            const int row = x / n_own, j = x % n_own, be = b0 + row / Lq, i = i0 + row % Lq;
+            const bool on = be < p.B && j <= i;
+            int rr = on ? min(i - j, p.C) : 0;
+            if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
             float s = 0.f;
-            for (int d = 0; d < 32; ++d) s += qu[is * DP + 32 * G + d];
-            qs[t][G] = s * norm[is];
+#pragma unroll
+            for (int e = 0; e < DP / 8; ++e) {
+                const int d = (lane & 7) + 8 * e;
+                if (on && d < p.D) {
+                    const float k = ld_elem(p.kcur, be * p.kc_sb + j * p.kc_st + h * p.kc_sh + d, p.f32);
+                    const float r = ld_elem(p.r, rr * p.r_row + h * p.r_head + d, p.f32);
+                    s = fmaf(qu[row * DP + d], k, fmaf(qv[row * DP + d], r, s));
+                }
+            }
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            if ((lane & 7) == 0) own_s[row * kDecodeMaxL + j] = on ? s : -INFINITY;
         }
     }
 
@@ -288,39 +307,46 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
         if (jb != j_lo) __syncthreads();
         if (!p.f32) {
             const int n_ct = (rows + 3) >> 2;
-            for (int t16 = (rho_c >> 4) + warp; t16 * 16 < n_rho; t16 += kWarps) {
-                uint4 a[2][NG];
+            // kBandTiles tiles of 16 entries at a time per warp, the loads of r first
+            for (int t0 = (rho_c >> 4) + kBandTiles * warp; t0 * 16 < n_rho; t0 += kBandTiles * kWarps) {
+                uint4 a[kBandTiles][2][NG];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    int rr = max(0, min(top - (t16 * 16 + g + 8 * half), p.C));
+                for (int x = 0; x < 2 * kBandTiles; ++x) {
+                    int rr = max(0, min(top - (t0 * 16 + g + 8 * x), p.C));
                     if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
                     const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
                         const int d = 32 * G + 8 * c4;
                         if (p.vec_r && d + 8 <= p.D) {
-                            a[half][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
+                            a[x >> 1][x & 1][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
                         } else {
                             uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
-                            a[half][G] = make_uint4(w[0], w[1], w[2], w[3]);
+                            a[x >> 1][x & 1][G] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                 }
                 for (int ct = 0; ct < n_ct; ++ct) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint4 bw[NG];
 #pragma unroll
-                    for (int G = 0; G < NG; ++G) {
-                        const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
-                        mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
-                        mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
-                    }
-                    if (4 * ct + c4 < rows) {
-                        float* e = band + (4 * ct + c4) * sp.pitch + t16 * 16 + g;
-                        e[0] = acc[0] + acc[1];
-                        e[8] = acc[2] + acc[3];
+                    for (int G = 0; G < NG; ++G)
+                        bw[G] = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
+#pragma unroll
+                    for (int x = 0; x < kBandTiles; ++x) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int G = 0; G < NG; ++G) {
+                            mma::mma16816(acc, a[x][0][G].x, a[x][1][G].x, a[x][0][G].y, a[x][1][G].y, bw[G].x, bw[G].y);
+                            mma::mma16816(acc, a[x][0][G].z, a[x][1][G].z, a[x][0][G].w, a[x][1][G].w, bw[G].z, bw[G].w);
+                        }
+                        if (4 * ct + c4 < rows && (t0 + x) * 16 < n_rho) {
+                            float* e = band + (4 * ct + c4) * sp.pitch + (t0 + x) * 16 + g;
+                            e[0] = acc[0] + acc[1];
+                            e[8] = acc[2] + acc[3];
+                        }
                     }
                 }
             }
@@ -342,11 +368,19 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
         for (; n < n_stage; ++n) {
             const int js = j_lo + (n * wpe + sw) * KS;
             if (js >= jb + kb) break;
-            copy_stage(n + kStages - 1);
-            cp_async_wait<kStages - 1>();
-            __syncwarp();
+            if (!warp_wait(&full[n % kStages], (n / kStages) & 1, wc, 50)) break;   // abandoned: no results
             const uint8_t* st = my_stages + (n % kStages) * kStageBytes;
-            const uint32_t st_addr = smem_u32(st) + (((lane >> 4) * KS) + ((lane >> 3) & 1) * 8 + (lane & 7)) * 16;
+            const uint32_t st_addr = smem_u32(st);
+            const int slot0 = slot_of(js);
+            // ldmatrix's four 8 x 8 matrices are chunks c2, c2 + 1 of 16 keys: this lane's row of them
+            auto frag_row = [&](int k, uint32_t& row, uint32_t& swap) {
+                const int r = k + (lane & 15);
+                int s = slot0 + r;
+                if (s >= p.M) s -= p.M;
+                row = st_addr + r * row_bytes;
+                swap = q_swizzle(nc, s);
+            };
+            auto frag = [&](uint32_t row, uint32_t swap, int c2) { return row + (((c2 + (lane >> 4)) ^ swap) << 4); };
             for (int k0 = 0; k0 < KS; k0 += 16 * NS) {
                 if (js + k0 >= j_hi) break;
                 // Q.K: acc[t][G] = for slot c4, keys g and g+8 of its stream's tile, (hi, lo) parts
@@ -357,10 +391,12 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                     for (int G = 0; G < NG; ++G) acc[t][G][0] = acc[t][G][1] = acc[t][G][2] = acc[t][G][3] = 0.f;
                 for (int T = 0; T < NS; ++T) {
                     const bool on = my_stream == T;
+                    uint32_t row, swap;
+                    frag_row(k0 + 16 * T, row, swap);
 #pragma unroll
                     for (int c2 = 0; c2 < NC; c2 += 2) {
                         uint32_t w[4];
-                        mma::ldsm_x4(st_addr + (c2 * KS + k0 + 16 * T) * 16, w[0], w[1], w[2], w[3]);
+                        mma::ldsm_x4(frag(row, swap, c2), w[0], w[1], w[2], w[3]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int c = c2 + half, G = c * 4 / BITS;
@@ -384,8 +420,9 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int G = 0; G < NG; ++G)
-                        par[x][G] = in_use ? *reinterpret_cast<const uint2*>(st + kParOff + (kk + 8 * x) * 8 * NG + 8 * G)
-                                           : make_uint2(0, 0);
+                        par[x][G] = in_use && js + kk + 8 * x < j_hi       // other rows hold what was there before
+                                        ? *reinterpret_cast<const uint2*>(st + kParOff + (kk + 8 * x) * 8 * NG + 8 * G)
+                                        : make_uint2(0, 0);
                 uint32_t bp[QT][NG][2];
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
@@ -405,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                         s[x] = live ? fmaf(d, sc[t], a) : -INFINITY;
                         pr[x] = ex2_approx(s[x] - m[t]);
                     }
-                    const float f = 1.f / rf[t];                      // a power of two
+                    const float f = __uint_as_float(0x7f000000u - __float_as_uint(rf[t]));   // 1 / rf, a power of two
                     float big = fmaxf(pr[0], pr[1]) * 16.f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
@@ -432,7 +469,8 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                         for (int off = 4; off <= 16; off <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
                         ref = fminf(fmaxf(fmaxf(ref, rf[t] * dl), kMinUnit), kMaxUnit);
                         const float unit = __uint_as_float(__float_as_uint(ref) & 0x7f800000u);      // its power of two
-                        const float so = dl * rf[t] / unit;
+                        const float f2 = __uint_as_float(0x7f000000u - __float_as_uint(unit));
+                        const float so = dl * rf[t] * f2;
                         rf[t] = unit;
                         m[t] = mn;
                         l[t] *= dl;
@@ -442,7 +480,6 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                         for (int x = 0; x < NG * 2; ++x) {
                             o[t][x][0] *= so; o[t][x][1] *= so; o[t][x][2] *= so; o[t][x][3] *= so;
                         }
-                        const float f2 = 1.f / unit;
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -461,10 +498,12 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                 // P.V: o[t][mt] = for slot c4, channels of row g and g+8 of the tile, (hi, lo) parts
                 for (int T = 0; T < NS; ++T) {
                     const bool on = my_stream == T;
+                    uint32_t row, swap;
+                    frag_row(k0 + 16 * T, row, swap);
 #pragma unroll
                     for (int c2 = 0; c2 < NC; c2 += 2) {
                         uint32_t w[4];
-                        mma::ldsm_x4_t(st_addr + ((NC + c2) * KS + k0 + 16 * T) * 16, w[0], w[1], w[2], w[3]);
+                        mma::ldsm_x4_t(frag(row + kVOff, swap, c2), w[0], w[1], w[2], w[3]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int c = c2 + half, G = c * 4 / BITS;
@@ -480,14 +519,20 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
                     }
                 }
             }
-            __syncwarp();                                 // the stage may be overwritten
+            __syncwarp();                                 // every lane has read the stage
+            if (lane == 0 && n + kStages < n_stage) copy_stage(n + kStages);
         }
     }
+    if (n < n_stage && lane == 0)                         // abandoned: no copy may land after the CTA has gone
+        for (int x = n; x < min(n + kStages, n_stage); ++x) {
+            int never = 0;
+            const WaitCtl dw{&never, nullptr, 100000000ull};
+            (void)mbar_wait(&full[x % kStages], (x / kStages) & 1, dw, 51);
+        }
     __syncthreads();
 
     // ---- merge: the streams of a warp, its warps, the segment's own keys, the ranks
     float* part = reinterpret_cast<float*>(stages);       // [warp][query][DP + 2]
-    float* own_part = part + kWarps * sp.lq * (DP + 2);   // [row][DP + 2] of the segment's own keys
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         float lt = l[t], zt[NG], ot[NG * 4];
@@ -530,68 +575,32 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
             }
         }
     }
-    const bool has_own = rank == sp.ranks - 1;
-    if (has_own) {
-        for (int row = warp; row < rows; row += kWarps) {
-            const int be = b0 + row / Lq, i = i0 + row % Lq;
-            if (be >= p.B) continue;
-            float mo = kNoMax, lo = 0.f, oo[NG];
-#pragma unroll
-            for (int e = 0; e < NG; ++e) oo[e] = 0.f;
-            const float nm = norm[row];
-            for (int j = 0; j <= i; ++j) {
-                int rr = min(i - j, p.C);
-                if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < NG; ++e) {
-                    const int d = lane + 32 * e;
-                    if (d < p.D) {
-                        const float k = ld_elem(p.kcur, be * p.kc_sb + j * p.kc_st + h * p.kc_sh + d, p.f32);
-                        const float r = ld_elem(p.r, rr * p.r_row + h * p.r_head + d, p.f32);
-                        s = fmaf(qu[row * DP + d] * nm, k, fmaf(qv[row * DP + d], r, s));
-                    }
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-                const float mn = fmaxf(mo, s), a = ex2_approx(mo - mn), w = ex2_approx(s - mn);
-                mo = mn;
-                lo = lo * a + w;
-#pragma unroll
-                for (int e = 0; e < NG; ++e) {
-                    const int d = lane + 32 * e;
-                    const float v = d < p.D ? ld_elem(p.vcur, be * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
-                    oo[e] = oo[e] * a + w * v;
-                }
-            }
-            float* dst = own_part + row * (DP + 2);
-#pragma unroll
-            for (int e = 0; e < NG; ++e) dst[lane + 32 * e] = oo[e];
-            if (lane == 0) {
-                dst[DP] = mo;
-                dst[DP + 1] = lo;
-            }
-        }
-    }
     __syncthreads();
     for (int x = tid; x < rows * DP; x += kThreads) {
-        const int row = x / DP, d = x % DP, wb = row / Lq * wpe, il = row % Lq;
-        const float* own = own_part + row * (DP + 2);
-        const bool use_own = has_own && b0 + row / Lq < p.B;
-        float mx = use_own ? own[DP] : kNoMax;
-        for (int w = 0; w < wpe; ++w) mx = fmaxf(mx, part[((wb + w) * sp.lq + il) * (DP + 2) + DP]);
+        const int row = x / DP, d = x % DP, wb = row / Lq * wpe, il = row % Lq, be = b0 + row / Lq;
+        const int own = has_own && be < p.B ? i0 + il + 1 : 0;
+        float v[kDecodeMaxL];
+#pragma unroll
+        for (int j = 0; j < kDecodeMaxL; ++j)
+            v[j] = j < own && d < p.D ? ld_elem(p.vcur, be * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
+        const float* src = part + (wb * sp.lq + il) * (DP + 2);
+        const int step = sp.lq * (DP + 2);
+        float mx = kNoMax;
+        for (int w = 0; w < wpe; ++w) mx = fmaxf(mx, src[w * step + DP]);
+        for (int j = 0; j < own; ++j) mx = fmaxf(mx, own_s[row * kDecodeMaxL + j]);
         float lt = 0.f, ot = 0.f;
         for (int w = 0; w < wpe; ++w) {
-            const float* src = part + ((wb + w) * sp.lq + il) * (DP + 2);
-            const float a = ex2_approx(src[DP] - mx);
-            lt += src[DP + 1] * a;
-            ot += src[d] * a;
+            const float a = ex2_approx(src[w * step + DP] - mx);
+            lt += src[w * step + DP + 1] * a;
+            ot += src[w * step + d] * a;
         }
-        if (use_own) {
-            const float a = ex2_approx(own[DP] - mx);
-            lt += own[DP + 1] * a;
-            ot += own[d] * a;
-        }
+#pragma unroll
+        for (int j = 0; j < kDecodeMaxL; ++j)
+            if (j < own) {
+                const float a = ex2_approx(own_s[row * kDecodeMaxL + j] - mx);
+                lt += a;
+                ot = fmaf(a, v[j], ot);
+            }
         mine[row * (DP + 2) + d] = ot;
         if (d == 0) {
             mine[row * (DP + 2) + DP] = mx;
@@ -609,15 +618,15 @@ __global__ void __launch_bounds__(kThreads) qattn_kernel(const __grid_constant__
             ot = src[d];
             lt = src[DP + 1];
         } else {
-            float mr[8], mx = kNoMax;
+            float mr[kMaxRanks], mx = kNoMax;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < kMaxRanks; ++r) {
                 mr[r] = r < sp.ranks ? ld_rank(src + DP, r) : kNoMax;
                 mx = fmaxf(mx, mr[r]);
             }
             lt = ot = 0.f;
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
+            for (int r = 0; r < kMaxRanks; ++r)
                 if (r < sp.ranks) {
                     const float a = ex2_approx(mr[r] - mx);
                     lt += ld_rank(src + DP + 1, r) * a;
@@ -637,10 +646,12 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
 {
     constexpr int DP = NG * 32;
     const size_t bytes = kWarps * kStages * stage_bytes(BITS, NG) + kBandBytes + kMaxRows * kBandPad * 4 +
-                         (2 * kMaxRows * DP + kMaxRows + kMaxRows * (DP + 2)) * 4 + 2 * kMaxRows * DP * 2;
-    static_assert(kWarps * kStages * stage_bytes(BITS, NG) >= (kWarps + 1) * kMaxRows * (DP + 2) * 4, "partial results fit");
+                         kMaxRows * (2 * DP + DP + 2 + 1 + NG + kDecodeMaxL) * 4 + 4 * kMaxRows * DP * 2 +
+                         kWarps * kStages * 8 + 16;
+    static_assert(kWarps * kStages * stage_bytes(BITS, NG) >= kWarps * kMaxRows * (DP + 2) * 4, "partial results fit");
     auto* kernel = qattn_kernel<BITS, NG, QT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && sp.ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -681,21 +692,21 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
     while (2 * sp.nb * sp.lq <= kMaxRows && sp.nb < p.B) sp.nb *= 2;
     auto blocks = [&](int nb) { return static_cast<int64_t>(p.H) * ((p.B + nb - 1) / nb) * groups; };
     while (sp.nb > 1 && blocks(sp.nb) * 8 < sm_count) sp.nb /= 2;
-    // Key ranges: until two CTAs per SM, while each warp keeps two stages.
+    // Key ranges: until two CTAs per SM, while each warp keeps two stages; 16 ranks only where eight
+    // leave SMs idle.
     sp.ranks = 1;
-    while (sp.ranks < 8 && blocks(sp.nb) * sp.ranks < 2 * sm_count &&
+    while (sp.ranks < kMaxRanks && blocks(sp.nb) * sp.ranks < (sp.ranks < 8 ? 2 * sm_count : sm_count) &&
            keys > static_cast<int64_t>(sp.ranks) * 2 * ks * (kWarps / sp.nb))
         sp.ranks *= 2;
     const int64_t unit = static_cast<int64_t>(ks) * (kWarps / sp.nb);
-    sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + unit - 1) / unit * unit);
-    if (sp.range == 0) sp.range = static_cast<int>(unit);
+    sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + ks - 1) / ks * ks);
+    if (sp.range == 0) sp.range = ks;
     // Position band: a multiple of the stages of one round of the warps
     const int rows = sp.nb * sp.lq;
     const int fit = kBandBytes / 4 / rows / static_cast<int>(unit) * static_cast<int>(unit);
     sp.block = std::max(fit, static_cast<int>(unit));
-    if (sp.block > sp.range) sp.block = sp.range;
+    sp.block = static_cast<int>(std::min<int64_t>(sp.block, (sp.range + unit - 1) / unit * unit));
     sp.pitch = sp.block + kBandPad;
-    sp.nc_mul = 65536 / (p.G * bits / 4) + 1;
     const dim3 grid(sp.ranks * groups, p.H, (p.B + sp.nb - 1) / sp.nb);
     if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, grid, s) : launch_qt<4, 4>(p, sp, grid, s);
     return ng == 2 ? launch_qt<8, 2>(p, sp, grid, s) : launch_qt<8, 4>(p, sp, grid, s);
