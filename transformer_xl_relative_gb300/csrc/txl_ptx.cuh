@@ -188,9 +188,19 @@ __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, const 
 
 // ------------------------------------------------------------------------------- clusters
 // Barrier of every thread of the cluster (whole warps arrive together), shared memory included.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
+}
+
+// Store to this shared-memory address in a CTA of the cluster.
+__device__ __forceinline__ void st_rank(float* p, uint32_t rank, float v)
+{
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+                 "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(p)), "r"(rank), "f"(v) : "memory");
 }
 
 // The float at this shared-memory address in another CTA of the cluster.
