@@ -501,8 +501,8 @@ txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_o
  *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_qmem_workspace_size(B, L,
  *            H, D, mem, dtype) bytes (TXL_ERR_WORKSPACE otherwise; may be NULL when that is 0).
  *            Calls that share a workspace must not overlap on the GPU.
- * L <= 16 (generation): one launch, the codes expanded on chip in fp32-like precision (q and the
- * weights held to 22 bits); no workspace.  L > 16, bf16: K and V of the memory's valid positions and
+ * L <= 16 (generation): the position terms (q+v).r go into the workspace, then the codes are expanded
+ * on chip in fp32-like precision (q and the weights held to 22 bits); two launches.  L > 16, bf16: K and V of the memory's valid positions and
  * of the segment, and r, are written into the workspace once in fp16, in units of powers of two per
  * (b, h) taken from the data, and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16
  * operands and P, for q, k_cur, v_cur and r of any layout.  (Queries and position terms that would bring
@@ -520,9 +520,10 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len,
                              void* workspace, size_t workspace_bytes,
                              int* err_flag, void* stream);
 
-/* Bytes of device workspace txl_rel_attn_qmem needs: 0 for L <= 16 or without a memory, else, with D
- * rounded up to a multiple of 8 in each row of a head, M rows of K and V in dtype and for bf16 also 3 L
- * such rows, M + L rows of r and 16 bytes per (b, h). */
+/* Bytes of device workspace txl_rel_attn_qmem needs.  L <= 16: B*H*L rows of M + L floats (a multiple of
+ * four, and up to seven more).  L > 16: 0 without a memory, else, with D rounded up to a multiple of 8
+ * in each row of a head, M rows of K and V in dtype and for bf16 also 3 L such rows, M + L rows of r and
+ * 16 bytes per (b, h). */
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype);
 
 /* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the kernel that expands the

@@ -126,17 +126,20 @@ def test_attention_refusals(native):
     assert attn(native, m=big) == E.TXL_ERR_UNSUPPORTED                    # M + L past 32 bits
 
 
-def test_long_segments_need_their_workspace(native):
+def test_calls_need_their_workspace(native):
     lib, E = native.load(), native
     m = qmem(native)
     p = ctypes.byref
     need = ((2 * 128 + 3 * 17) * 2 + 128 + 17) * 4 * 64 * 2 + 2 * 4 * 16
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 1) == need
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 2 * 128 * 2 * 4 * 64 * 4
-    assert lib.txl_rel_attn_qmem_workspace_size(2, 16, 4, 64, p(m), 1) == 0
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 16, 4, 64, p(m), 1) == 2 * 4 * 16 * (148 + 1) * 4
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 1, 4, 64, None, 1) == 2 * 4 * 1 * (4 + 1) * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, None, 1) == 0
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 41, p(qmem(native, D=41)), 1) == (need - 128) // 64 * 48 + 128
     assert attn(native, L=17) == E.TXL_ERR_WORKSPACE
+    assert attn(native, L=1) == E.TXL_ERR_WORKSPACE
+    assert attn(native, L=1, ws=FAKE, ws_bytes=2 * 4 * 1 * (132 + 1) * 4 - 1) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=17, ws=FAKE, ws_bytes=need - 1) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=17, ws=FAKE + 8, ws_bytes=need) == E.TXL_ERR_WORKSPACE
 

@@ -499,7 +499,7 @@ def qmem_read(mem: QuantMemory, j0: int, n: int, k_out: torch.Tensor, v_out: tor
 
 
 def rel_attn_qmem_workspace_size(q: torch.Tensor, mem: QuantMemory | None) -> int:
-    """Bytes of workspace rel_attn_qmem needs (txl_rel_attn_qmem_workspace_size): 0 for up to 16 queries."""
+    """Bytes of workspace rel_attn_qmem needs (txl_rel_attn_qmem_workspace_size)."""
     B, L, H, D = q.shape
     memc = ctypes.byref(mem.c_struct) if mem is not None else None
     return int(_lib().txl_rel_attn_qmem_workspace_size(B, L, H, D, memc, dtype_code(q)))
@@ -528,24 +528,22 @@ def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor,
                   out: torch.Tensor, scale: float = 0.0, workspace: torch.Tensor | None = None,
                   err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Relative attention over [quantised memory ++ current segment] (txl_rel_attn_qmem).  Without
-    `workspace`, a device buffer of the required size (none for up to 16 queries) is taken from
-    torch's allocator for the call."""
+    `workspace`, a device buffer of the required size is taken from torch's allocator for the call."""
     _qattn_check(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out)
     B, L, H, D = q.shape
     memc = ctypes.byref(mem.c_struct) if mem is not None else None
     vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)
-    if workspace is None and L > 16:
+    if workspace is None:
         # from the pool of the stream that will use it, so that it is not reused before it has been
         with torch.cuda.stream(stream) if stream is not None else _on(q.device):
             need = rel_attn_qmem_workspace_size(q, mem)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    wp, nbytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
-        else (None, 0)
+    nbytes = workspace.numel() * workspace.element_size()
     with _on(q.device):
         st = _lib().txl_rel_attn_qmem(
             B, L, H, D, int(clamp_len), ctypes.byref(vq), memc, ctypes.byref(vk), ctypes.byref(vv),
             u.data_ptr(), v_bias.data_ptr(), r.data_ptr(), r.stride(1), int(n_rows), float(scale),
-            ctypes.byref(vo), dtype_code(q), wp, nbytes,
+            ctypes.byref(vo), dtype_code(q), workspace.data_ptr(), nbytes,
             err_flag.data_ptr() if err_flag is not None else None, _stream(stream))
     check(st, "txl_rel_attn_qmem")
     return out

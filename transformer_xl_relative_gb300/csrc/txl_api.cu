@@ -1149,7 +1149,11 @@ txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_o
 
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype)
 {
-    if (B <= 0 || L <= kDecodeMaxL || H <= 0 || D <= 0 || D > 128 || !mem || mem->M <= 0) return 0;
+    if (B <= 0 || L <= 0 || H <= 0 || D <= 0 || D > 128) return 0;
+    const size_t M = mem && mem->M > 0 ? mem->M : 0;
+    // position terms: a row of at most M + L + 3 keys, a multiple of four floats, and one value more
+    if (L <= kDecodeMaxL) return static_cast<size_t>(B) * H * L * ((M + L + 6) / 4 * 4 + 1) * 4;
+    if (M == 0) return 0;
     const size_t row = static_cast<size_t>(B) * H * ((D + 7) / 8 * 8);
     if (dtype == TXL_F32) return 2 * row * mem->M * 4;
     const size_t r_rows = static_cast<size_t>(H) * ((D + 7) / 8 * 8) * (static_cast<size_t>(mem->M) + L);
@@ -1183,8 +1187,8 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     const int valid = M > 0 ? mem->valid : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (B > 65535 || H > 65535) return TXL_ERR_UNSUPPORTED;
+    const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
     if (L > kDecodeMaxL) {
-        const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
         if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
         if (valid == 0)
             return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, nullptr, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale,
@@ -1236,6 +1240,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
         return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, &m, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale, out,
                                 dtype, nullptr, 0, err_flag, stream);
     }
+    if (!workspace || workspace_bytes < need || !a16(workspace)) return TXL_ERR_WORKSPACE;
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
     QattnParams p;
     std::memset(&p, 0, sizeof(p));
@@ -1258,6 +1263,13 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.qscale = scale * 1.4426950408889634f;
     const int elem = dtype == TXL_F32 ? 4 : 2;
     p.vec_r = a16(r) && s16(ld_r, elem);
+    // keys up to M - C are at the clamp for every query
+    const int first_near = std::max<int64_t>(p.lo, std::min<int64_t>(M, static_cast<int64_t>(M) - clamp_len + 1));
+    p.jn = first_near - (first_near - p.lo) % 4;
+    p.e_pitch = (M + L - p.jn + 3) / 4 * 4;
+    p.n_dist = std::max<int64_t>(static_cast<int64_t>(M) + L - p.jn, p.jn > p.lo ? static_cast<int64_t>(clamp_len) + 1 : 0);
+    p.E = static_cast<float*>(workspace);
+    p.far = p.E + static_cast<int64_t>(B) * H * L * p.e_pitch;
     p.err_flag = err_flag;
     p.chk = range_counter();
     const int sms = sm_count();

@@ -328,6 +328,10 @@ struct QattnParams {
     int n_rows;
     float qscale;                               // scale * log2(e)
     int vec_r;                                  // rows of r start on 16-byte boundaries
+    // position terms, workspace: E[b][h][i][j - jn] for keys j >= jn (own keys too), e_pitch floats per row (a
+    // multiple of 4, lo <= jn = lo mod 4), and far[b][h][i] for keys before; n_dist distances are computed
+    float* E; float* far;
+    int jn, e_pitch, n_dist;
     int* err_flag;                              // TXL_ERR_TIMEOUT on a wait abandoned, may be null
     int* chk;                                   // range-check counter (checked build)
 };
