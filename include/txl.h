@@ -520,10 +520,28 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len,
                              void* workspace, size_t workspace_bytes,
                              int* err_flag, void* stream);
 
+/* txl_rel_attn_qmem with its arguments in one struct, for bindings that pay per argument. */
+typedef struct {
+    int B, L, H, D, clamp_len, n_rows;
+    int dtype;                 /* a txl_dtype */
+    float scale;
+    txl_view q, k_cur, v_cur, out;
+    const txl_qmem* mem;
+    const float* u;
+    const float* v_bias;
+    const void* r;
+    int64_t ld_r;
+    void* workspace;
+    size_t workspace_bytes;
+    int* err_flag;
+    void* stream;
+} txl_rel_attn_qmem_args;
+txl_status txl_rel_attn_qmem_call(const txl_rel_attn_qmem_args* args);
+
 /* Bytes of device workspace txl_rel_attn_qmem needs.  L <= 16: B*H*L rows of M + L floats (a multiple of
  * four, and up to seven more).  L > 16: 0 without a memory, else, with D rounded up to a multiple of 8
  * in each row of a head, M rows of K and V in dtype and for bf16 also 3 L such rows, M + L rows of r and
- * 16 bytes per (b, h). */
+ * 144 bytes per (b, h). */
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype);
 
 /* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the kernel that expands the

@@ -130,13 +130,13 @@ def test_calls_need_their_workspace(native):
     lib, E = native.load(), native
     m = qmem(native)
     p = ctypes.byref
-    need = ((2 * 128 + 3 * 17) * 2 + 128 + 17) * 4 * 64 * 2 + 2 * 4 * 16
+    need = ((2 * 128 + 3 * 17) * 2 + 128 + 17) * 4 * 64 * 2 + 2 * 4 * 144
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 1) == need
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 2 * 128 * 2 * 4 * 64 * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 16, 4, 64, p(m), 1) == 2 * 4 * 16 * (148 + 1) * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 1, 4, 64, None, 1) == 2 * 4 * 1 * (4 + 1) * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, None, 1) == 0
-    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 41, p(qmem(native, D=41)), 1) == (need - 128) // 64 * 48 + 128
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 41, p(qmem(native, D=41)), 1) == (need - 1152) // 64 * 48 + 1152
     assert attn(native, L=17) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=1) == E.TXL_ERR_WORKSPACE
     assert attn(native, L=1, ws=FAKE, ws_bytes=2 * 4 * 1 * (132 + 1) * 4 - 1) == E.TXL_ERR_WORKSPACE
@@ -173,3 +173,26 @@ def test_python_checks():
                 lambda: txl.QuantMemory(k, k, par, 64, 4)):            # the last: not on a CUDA device
         with pytest.raises(ValueError):
             bad()
+
+
+def test_the_struct_form_reads_its_arguments(native):
+    """txl_rel_attn_qmem_call with the packed arguments of the binding: the statuses of the long form."""
+    q = (FAKE, 1 * 4 * 64, 4 * 64, 64)
+    m = qmem(native)
+
+    def call(B=2, n_rows=11, dtype=1, ws=FAKE, ws_bytes=1 << 20, r=FAKE, ld_r=64, L=1, mem=None, C=10):
+        a = native.QMEM_ARGS.pack(B, L, 4, 64, C, n_rows, dtype, 0.0, *q, *q, *q, *q,
+                                  ctypes.addressof(m) if mem is None else mem, FAKE, FAKE, r, ld_r, ws, ws_bytes, 0, 0)
+        return native.load().txl_rel_attn_qmem_call(a)
+
+    assert native.load().txl_rel_attn_qmem_call(None) == native.TXL_ERR_INVALID_ARG
+    assert call(L=0) == native.TXL_OK
+    assert call(B=3) == native.TXL_ERR_INVALID_ARG
+    assert call(n_rows=10) == native.TXL_ERR_INVALID_ARG
+    assert call(C=-1) == native.TXL_ERR_INVALID_ARG
+    assert call(dtype=9) == native.TXL_ERR_INVALID_ARG
+    assert call(r=0) == native.TXL_ERR_INVALID_ARG
+    assert call(ld_r=63) == native.TXL_ERR_INVALID_ARG
+    assert call(ws=0) == native.TXL_ERR_WORKSPACE
+    assert call(ws=FAKE + 4) == native.TXL_ERR_WORKSPACE
+    assert call(ws_bytes=100) == native.TXL_ERR_WORKSPACE

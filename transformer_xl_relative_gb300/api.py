@@ -45,20 +45,17 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-class _on:
-    """Makes `device` current for a call when it is not (the library launches on the current device)."""
+def _raw_stream(stream, device: int) -> int:
+    """cudaStream_t of `stream`, or of the current stream of CUDA device `device`."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
-    def __init__(self, device):
-        self._to = device.index
 
-    def __enter__(self):
-        self._from = torch.cuda.current_device()
-        if self._to is not None and self._to != self._from:
-            torch.cuda.set_device(self._to)
-
-    def __exit__(self, *exc):
-        if self._to is not None and self._to != self._from:
-            torch.cuda.set_device(self._from)
+def _on_device(device: int, call):
+    """Runs call() with CUDA device `device` current (the library launches on the current device)."""
+    if device == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(device):
+        return call()
 
 
 class Memory:
@@ -429,9 +426,10 @@ class QuantMemory:
                                  % ((B, H, M, 4 * G * bits), (B, H, M, GP, 4)))
         if not k.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
-        self.k, self.v, self.par = k, v, par
+        self.k, self.v, self.par, self.device = k, v, par, k.get_device()
         self._c = TxlQmem(k.data_ptr() if M else None, v.data_ptr() if M else None, par.data_ptr() if M else None,
                           B, M, H, D, bits, int(wp), int(valid))
+        self.address = ctypes.addressof(self._c)          # of the C struct, for calls that take it as a number
 
     @classmethod
     def empty(cls, B, M, H, D, bits=4, device="cuda"):
@@ -463,38 +461,37 @@ class QuantMemory:
         return self._c
 
 
-def _qmem_kv(mem: QuantMemory, k: torch.Tensor, v: torch.Tensor, T: int) -> None:
+def _qmem_kv(mem: QuantMemory, k: torch.Tensor, v: torch.Tensor, T: int):
+    """Views of k and v [B, T, H, D] of the memory's shape and device, and their dtype's code."""
     c = mem.c_struct
-    for t in (k, v):
-        if t.shape != (c.B, T, c.H, c.D):
-            raise ValueError("expected [B, T, H, D] = %s, got %s" % ((c.B, T, c.H, c.D), tuple(t.shape)))
-        if t.device != mem.k.device:
-            raise ValueError("tensors must live on the memory's device")
+    shape = (c.B, T, c.H, c.D)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("expected [B, T, H, D] = %s, got %s and %s" % (shape, tuple(k.shape), tuple(v.shape)))
+    if k.get_device() != mem.device or v.get_device() != mem.device:
+        raise ValueError("tensors must live on the memory's device")
     if k.dtype != v.dtype:
         raise TypeError("k and v must share a dtype")
+    sk, sv = k.stride(), v.stride()
+    if c.D > 1 and (sk[3] != 1 or sv[3] != 1):
+        raise ValueError("the last (d) dimension must be contiguous")
+    return TxlView(k.data_ptr(), sk[0], sk[1], sk[2]), TxlView(v.data_ptr(), sv[0], sv[1], sv[2]), dtype_code(k)
 
 
 def qmem_push(mem: QuantMemory, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> QuantMemory:
     """Quantise k_new/v_new [B, L, H, D] into the FIFO memory (txl_qmem_push)."""
     L = k_new.shape[1]
-    _qmem_kv(mem, k_new, v_new, L)
-    vk, vv = view(k_new), view(v_new)
-    with _on(k_new.device):
-        st = _lib().txl_qmem_push(ctypes.byref(mem.c_struct), ctypes.byref(vk), ctypes.byref(vv), L,
-                                  dtype_code(k_new), _stream(stream))
-    check(st, "txl_qmem_push")
+    vk, vv, dtype = _qmem_kv(mem, k_new, v_new, L)
+    check(_on_device(mem.device, lambda: _lib().txl_qmem_push(mem.c_struct, vk, vv, L, dtype,
+                                                              _raw_stream(stream, mem.device))), "txl_qmem_push")
     return mem
 
 
 def qmem_read(mem: QuantMemory, j0: int, n: int, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
     """What the memory's logical positions j0 .. j0+n-1 (oldest first, all valid) stand for, into
     k_out/v_out [B, n, H, D] (txl_qmem_read)."""
-    _qmem_kv(mem, k_out, v_out, n)
-    vk, vv = view(k_out), view(v_out)
-    with _on(k_out.device):
-        st = _lib().txl_qmem_read(ctypes.byref(mem.c_struct), int(j0), int(n), ctypes.byref(vk), ctypes.byref(vv),
-                                  dtype_code(k_out), _stream(stream))
-    check(st, "txl_qmem_read")
+    vk, vv, dtype = _qmem_kv(mem, k_out, v_out, n)
+    check(_on_device(mem.device, lambda: _lib().txl_qmem_read(mem.c_struct, j0, n, vk, vv, dtype,
+                                                              _raw_stream(stream, mem.device))), "txl_qmem_read")
     return k_out, v_out
 
 
@@ -505,22 +502,26 @@ def rel_attn_qmem_workspace_size(q: torch.Tensor, mem: QuantMemory | None) -> in
     return int(_lib().txl_rel_attn_qmem_workspace_size(B, L, H, D, memc, dtype_code(q)))
 
 
-def _qattn_check(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out):
-    B, L, H, D = q.shape
-    dtype, device = q.dtype, q.device
+def _qattn_refusal(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out, dev):
+    """Raises what is wrong with the arguments of rel_attn_qmem (called when something is)."""
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    if q.dtype not in _DTYPES:
+        raise TypeError("libtxl computes in float32 or bfloat16, got %s" % q.dtype)
+    H, D = q.shape[2:]
     for t in (k_cur, v_cur, out):
-        if t.shape != q.shape or t.dtype != dtype or t.device != device:
+        if t.shape != q.shape or t.dtype != q.dtype or t.get_device() != dev:
             raise ValueError("q, k_cur, v_cur and out must share shape, dtype and device")
     for t in (u, v_bias):
         if t.dtype != torch.float32:
             raise TypeError("u and v_bias are fp32 [H, D]")
-        if t.shape != (H, D) or not t.is_contiguous() or t.device != device:
+        if t.shape != (H, D) or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError("u and v_bias must be contiguous [H, D] on the queries' device")
-    if (r.dim() != 3 or r.dtype != dtype or r.device != device or r.shape[0] < n_rows or r.shape[1] != H
-            or r.shape[2] < D or r.stride(2) != 1 or (r.shape[0] > 1 and r.stride(0) != H * r.stride(1))):
-        raise ValueError("r must be [n_rows, H, ld_r] of the queries' dtype and device, rows H * ld_r apart")
-    if mem is not None and mem.k.device != device:
+    if mem is not None and mem.device != dev:
         raise ValueError("tensors must live on the memory's device")
+    if any(t.stride(3) != 1 for t in (q, k_cur, v_cur, out)) and D > 1:
+        raise ValueError("the last (d) dimension must be contiguous")
+    raise ValueError("r must be [n_rows, H, ld_r] of the queries' dtype and device, rows H * ld_r apart")
 
 
 def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor, v_cur: torch.Tensor,
@@ -529,23 +530,32 @@ def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor,
                   err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Relative attention over [quantised memory ++ current segment] (txl_rel_attn_qmem).  Without
     `workspace`, a device buffer of the required size is taken from torch's allocator for the call."""
-    _qattn_check(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out)
-    B, L, H, D = q.shape
-    memc = ctypes.byref(mem.c_struct) if mem is not None else None
-    vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    B, L, H, D = shape
+    (q0, q1, q2, q3), (k0, k1, k2, k3), (v0, v1, v2, v3), (o0, o1, o2, o3) = (
+        q.stride(), k_cur.stride(), v_cur.stride(), out.stride())
+    rs, rt = r.shape, r.stride()
+    if not (dev >= 0 and dtype in _DTYPES and k_cur.shape == shape and v_cur.shape == shape and out.shape == shape
+            and k_cur.dtype == dtype and v_cur.dtype == dtype and out.dtype == dtype and r.dtype == dtype
+            and k_cur.get_device() == dev and v_cur.get_device() == dev and out.get_device() == dev
+            and u.get_device() == dev and v_bias.get_device() == dev and r.get_device() == dev
+            and u.dtype == torch.float32 and v_bias.dtype == torch.float32
+            and u.shape == (H, D) and v_bias.shape == (H, D) and u.is_contiguous() and v_bias.is_contiguous()
+            and (D == 1 or q3 == k3 == v3 == o3 == 1) and (mem is None or mem.device == dev)
+            and len(rs) == 3 and rs[0] >= n_rows and rs[1] == H and rs[2] >= D and rt[2] == 1
+            and (rs[0] <= 1 or rt[0] == H * rt[1])):
+        _qattn_refusal(q, mem, k_cur, v_cur, u, v_bias, r, n_rows, out, dev)
     if workspace is None:
         # from the pool of the stream that will use it, so that it is not reused before it has been
-        with torch.cuda.stream(stream) if stream is not None else _on(q.device):
-            need = rel_attn_qmem_workspace_size(q, mem)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    nbytes = workspace.numel() * workspace.element_size()
-    with _on(q.device):
-        st = _lib().txl_rel_attn_qmem(
-            B, L, H, D, int(clamp_len), ctypes.byref(vq), memc, ctypes.byref(vk), ctypes.byref(vv),
-            u.data_ptr(), v_bias.data_ptr(), r.data_ptr(), r.stride(1), int(n_rows), float(scale),
-            ctypes.byref(vo), dtype_code(q), workspace.data_ptr(), nbytes,
-            err_flag.data_ptr() if err_flag is not None else None, _stream(stream))
-    check(st, "txl_rel_attn_qmem")
+        need = max(rel_attn_qmem_workspace_size(q, mem), 16)
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    args = native.QMEM_ARGS.pack(
+        B, L, H, D, clamp_len, n_rows, _DTYPES[dtype], scale, q.data_ptr(), q0, q1, q2, k_cur.data_ptr(), k0, k1, k2,
+        v_cur.data_ptr(), v0, v1, v2, out.data_ptr(), o0, o1, o2, mem.address if mem is not None else 0, u.data_ptr(),
+        v_bias.data_ptr(), r.data_ptr(), rt[1], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev))
+    check(_on_device(dev, lambda: _lib().txl_rel_attn_qmem_call(args)), "txl_rel_attn_qmem")
     return out
 
 

@@ -1157,7 +1157,7 @@ size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qm
     const size_t row = static_cast<size_t>(B) * H * ((D + 7) / 8 * 8);
     if (dtype == TXL_F32) return 2 * row * mem->M * 4;
     const size_t r_rows = static_cast<size_t>(H) * ((D + 7) / 8 * 8) * (static_cast<size_t>(mem->M) + L);
-    return (2 * row * mem->M + 3 * row * L + r_rows) * 2 + static_cast<size_t>(B) * H * 16;
+    return (2 * row * mem->M + 3 * row * L + r_rows) * 2 + static_cast<size_t>(B) * H * 144;
 }
 
 int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem, const txl_view* k_cur,
@@ -1229,8 +1229,8 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
             e.r16 = at + 3 * seg;
             e.units = reinterpret_cast<float*>(at + 3 * seg + static_cast<int64_t>(e.n_r) * H * ld);
             e.chk = range_counter();
-            const int sms = sm_count();
-            if (sms <= 0 || launch_qmem_expand(e, sms, s) != cudaSuccess) return TXL_ERR_CUDA;
+            e.absmax = e.units + static_cast<int64_t>(B) * H * 4;
+            if (launch_qmem_expand(e, s) != cudaSuccess) return TXL_ERR_CUDA;
             return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
                                   err_flag, s, 0, nullptr, 0, e.units);
         }
@@ -1275,6 +1275,14 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     const int sms = sm_count();
     if (sms <= 0) return TXL_ERR_CUDA;
     return launch_qattn(p, sms, s) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
+txl_status txl_rel_attn_qmem_call(const txl_rel_attn_qmem_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    return txl_rel_attn_qmem(a->B, a->L, a->H, a->D, a->clamp_len, &a->q, a->mem, &a->k_cur, &a->v_cur, a->u, a->v_bias,
+                             a->r, a->ld_r, a->n_rows, a->scale, &a->out, static_cast<txl_dtype>(a->dtype), a->workspace,
+                             a->workspace_bytes, a->err_flag, a->stream);
 }
 
 int txl_checked_build(void) { return kCheckedBuild ? 1 : 0; }

@@ -310,9 +310,10 @@ struct QexpandParams {
     void* q_seg;                        // bf16 copy for TMA, or null where q serves as it is
     void* r16;                          // [n_r][H][ld]
     float* units;                       // [B][H][4], 16-byte aligned: powers of two of K, V and r
+    float* absmax;                      // [B][H][8][4], 16-byte aligned: largest |k|, |v|, |r| of shares of the rows
     int* chk;
 };
-cudaError_t launch_qmem_expand(const QexpandParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_qmem_expand(const QexpandParams& p, cudaStream_t s);
 
 // Attention of 1 .. kDecodeMaxL queries over a quantised memory and the segment's own keys.
 struct QattnParams {

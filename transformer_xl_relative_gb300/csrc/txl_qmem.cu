@@ -13,6 +13,8 @@
 // Both kernels are bound by HBM.  Four lanes share a group, eight channels each: 16-byte accesses to
 // bf16 rows, and consecutive threads walk the groups of a row, then the positions of one head, which
 // are contiguous in the code arrays.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "txl_internal.h"
@@ -283,47 +285,42 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
 // of the memory and of the segment, and r.  Each takes its range from a power of two, the unit: the
 // largest |k| of a (b, h) comes into [1, 2) (its unit multiplies c(q+u)), the largest |v| into
 // [2^11, 2^12) (P of the attention goes up to 2^8), and the largest |r| of 64 rows of the head into [1, 2)
-// (rows of up to 2^15 times that size have room).  One cluster per (b, h); each CTA takes a share of the rows, first for
-// the largest values (a group's end points bound its values, so the parameters suffice for the memory),
-// then to write.  Rows are taken four at a time per thread, the loads first.
+// (rows of up to 2^15 times that size have room).
+//
+// Two passes: qmem_absmax_kernel takes the largest values of up to kXSplits shares of the rows of a (b, h)
+// (a group's end points bound its values, so the parameters suffice for the memory), qmem_expand_kernel
+// writes, one lane per eight channels of a row.  (One kernel with a cluster per (b, h), exchanging the
+// maxima through shared memory, took 62 us on the large shape: its CTAs waited for one another.)
 constexpr int kXThreads = 256;
-constexpr int kXRows = 4;
+constexpr int kXSplits = 8;
+
+__device__ __forceinline__ int x_share(int64_t n, int64_t part, int64_t parts) { return static_cast<int>(n * part / parts); }
 
 template <int BITS, int G>
-__global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int ranks)
+__global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p)
 {
     __shared__ float red[3][kXThreads / 32];
-    __shared__ float rank_max[2];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x, h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(b) * p.H + h;
-    auto share = [](int64_t n, int64_t part, int64_t parts) { return static_cast<int>(n * part / parts); };
-    const int r0 = share(p.n, rank, ranks), r1 = share(p.n, rank + 1, ranks);
-    const int s0 = share(p.L, rank, ranks), s1 = share(p.L, rank + 1, ranks);
-    auto slot_of = [&](int t) {
-        int64_t s = static_cast<int64_t>(p.slot0) + t;
-        if (s >= p.M) s -= p.M;
-        if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        return static_cast<int>(s);
-    };
-    auto seg = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int t) {
-        return static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh;
-    };
     constexpr int LPR = 4 * G;                            // lanes of a row, eight channels each
     constexpr int RPP = kXThreads / LPR;                  // rows of a pass
-    const int lr = tid / LPR, c = tid % LPR, d0 = 8 * c;
+    const int lr = tid / LPR, d0 = 8 * (tid % LPR);
     const bool lane_on = lr < RPP && d0 < p.D;
 
     float mx[3] = {0.f, 0.f, 0.f};                        // k, v, r; values that are not finite do not count
     auto see = [&](int which, float a) {
         if (a < INFINITY) mx[which] = fmaxf(mx[which], a);
     };
-    const int64_t x1 = static_cast<int64_t>(r1) * G;
+    const int64_t x1 = static_cast<int64_t>(x_share(p.n, part + 1, parts)) * G;
 #pragma unroll 4
-    for (int64_t x = static_cast<int64_t>(r0) * G + tid; x < x1; x += kXThreads) {
+    for (int64_t x = static_cast<int64_t>(x_share(p.n, part, parts)) * G + tid; x < x1; x += kXThreads) {
         const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + ((bh * p.M + slot_of(t)) * q_par_groups(G) + g) * 4));
+        int64_t s = static_cast<int64_t>(p.slot0) + t;
+        if (s >= p.M) s -= p.M;
+        if (!in_range(s, 0, p.M, p.chk)) s = 0;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + ((bh * p.M + s) * q_par_groups(G) + g) * 4));
         const uint32_t kv[2] = {w.x, w.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -331,28 +328,28 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
             see(i, fmaxf(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo))));
         }
     }
-    if (lane_on)
-#pragma unroll 2
-        for (int t = s0 + lr; t < s1; t += RPP) {
-            float xk[8], xv[8];
-            load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, t), d0, p.D, p.vec_k, 0.f, xk);
-            load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, t), d0, p.D, p.vec_v, 0.f, xv);
+    if (lane_on) {
+        auto rows = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int vec, int which) {
+            const int s1 = x_share(p.L, part + 1, parts);
+#pragma unroll 4
+            for (int t = x_share(p.L, part, parts) + lr; t < s1; t += RPP) {
+                float v[8];
+                load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, 0.f, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                see(0, fabsf(xk[e]));
-                see(1, fabsf(xv[e]));
+                for (int e = 0; e < 8; ++e) see(which, fabsf(v[e]));
             }
-        }
-    const int samples = min(p.n_r, 64);                   // the same rows in every CTA of the head
-    if (lane_on)
-        for (int i = lr; i < samples; i += RPP) {
-            const int64_t row = static_cast<int64_t>(share(p.n_r - 1, i, max(samples - 1, 1))) * p.H + h;
-            float x[8];
-            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
+        };
+        rows(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, p.vec_k, 0);
+        rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
+        const int samples = min(p.n_r, 64);               // the same rows of r for every entry of the head
+        for (int i = x_share(samples, part, parts) + lr; i < x_share(samples, part + 1, parts); i += RPP) {
+            const int64_t row = static_cast<int64_t>(x_share(p.n_r - 1, i, max(samples - 1, 1))) * p.H + h;
+            float v[8];
+            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) see(2, fabsf(x[e]));
+            for (int e = 0; e < 8; ++e) see(2, fabsf(v[e]));
         }
-    float inv[3];
+    }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
 #pragma unroll
@@ -360,107 +357,99 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
         if ((tid & 31) == 0) red[i][tid >> 5] = mx[i];
     }
     __syncthreads();
+    if (tid < 3) {
+        float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-#pragma unroll
-        for (int w = 0; w < kXThreads / 32; ++w) mx[i] = fmaxf(mx[i], red[i][w]);
-        if (tid == 0 && i < 2) rank_max[i] = mx[i];
+        for (int w = 0; w < kXThreads / 32; ++w) m = fmaxf(m, red[tid][w]);
+        p.absmax[(bh * kXSplits + part) * 4 + tid] = m;
     }
-    if (ranks > 1) {
-        __syncthreads();
-        cluster_sync_all();
-        for (int r = 0; r < ranks; ++r) {
-            mx[0] = fmaxf(mx[0], ld_rank(&rank_max[0], r));
-            mx[1] = fmaxf(mx[1], ld_rank(&rank_max[1], r));
-        }
+}
+
+// Grid: x over the lanes of the rows (memory, segment, this entry's share of the head's rows of r), y head, z entry.
+template <int BITS, int G>
+__global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int64_t bh = static_cast<int64_t>(b) * p.H + h;
+    float mx[3] = {0.f, 0.f, 0.f}, inv[3];
+    for (int i = 0; i < parts; ++i) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.absmax) + bh * kXSplits + i);
+        mx[0] = fmaxf(mx[0], a.x); mx[1] = fmaxf(mx[1], a.y); mx[2] = fmaxf(mx[2], a.z);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int ex = min(max(static_cast<int>(__float_as_uint(mx[i]) >> 23) - 127 - (i == 1 ? 11 : 0), -115), 115);
         inv[i] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        if (rank == 0 && tid == 0) p.units[4 * bh + i] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.units[4 * bh + i] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
     }
-
+    constexpr int LPR = 4 * G;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kXThreads + threadIdx.x;
+    int64_t t = i / LPR;
+    const int c = static_cast<int>(i - t * LPR), d0 = 8 * c;
+    if (d0 >= p.D) return;
     auto put = [&](void* base, int64_t row, const float* x, float f) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row * p.ld + d0) =
-            make_uint4(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f), pack_f16x2(x[4] * f, x[5] * f),
-                       pack_f16x2(x[6] * f, x[7] * f));
+            make_uint4(pack_f16x2_sat(x[0] * f, x[1] * f), pack_f16x2_sat(x[2] * f, x[3] * f),
+                       pack_f16x2_sat(x[4] * f, x[5] * f), pack_f16x2_sat(x[6] * f, x[7] * f));
     };
-    if (lane_on) {
-        for (int t0 = r0 + lr; t0 < r1; t0 += kXRows * RPP) {
-            uint32_t ck[kXRows][2], cv[kXRows][2];
-            uint2 par[kXRows];
-#pragma unroll
-            for (int k = 0; k < kXRows; ++k) {
-                const int t = t0 + k * RPP;
-                if (t >= r1) break;
-                const int slot = slot_of(t);
-                const int64_t row = bh * p.M + slot, at = code_at<BITS, G>(row, slot, d0);
-                if constexpr (BITS == 4) {
-                    ck[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
-                    cv[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
-                } else {
-                    const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at));
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.v + at));
-                    ck[k][0] = a.x; ck[k][1] = a.y; cv[k][0] = w.x; cv[k][1] = w.y;
-                }
-                par[k] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(G) + (c >> 2)) * 4));
-            }
-#pragma unroll
-            for (int k = 0; k < kXRows; ++k) {
-                const int t = t0 + k * RPP;
-                if (t >= r1) break;
-                float x[8];
-                expand8<BITS>(ck[k], par[k].x, x);
-                put(p.k_mem, bh * p.n + t, x, inv[0]);
-                expand8<BITS>(cv[k], par[k].y, x);
-                put(p.v_mem, bh * p.n + t, x, inv[1]);
-            }
+    float x[8], y[8];
+    if (t < p.n) {
+        int64_t s = static_cast<int64_t>(p.slot0) + t;
+        if (s >= p.M) s -= p.M;
+        if (!in_range(s, 0, p.M, p.chk)) s = 0;
+        const int64_t row = bh * p.M + s, at = code_at<BITS, G>(row, static_cast<int>(s), d0);
+        uint32_t ck[2], cv[2];
+        if constexpr (BITS == 4) {
+            ck[0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
+            cv[0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
+        } else {
+            const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at)), w = __ldg(reinterpret_cast<const uint2*>(p.v + at));
+            ck[0] = a.x; ck[1] = a.y; cv[0] = w.x; cv[1] = w.y;
         }
-#pragma unroll 2
-        for (int t = s0 + lr; t < s1; t += RPP) {
-            float x[8];
-            load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, t), d0, p.D, p.vec_k, 0.f, x);
-            put(p.k_seg, bh * p.L + t, x, inv[0]);
-            load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, t), d0, p.D, p.vec_v, 0.f, x);
-            put(p.v_seg, bh * p.L + t, x, inv[1]);
-            if (p.q_seg) {
-                load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh, t), d0, p.D, p.vec_q, 0.f, x);
-                store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
-            }
-        }
-        // this head's rows of r, shared out over the batch entries and ranks
-        const int64_t part = static_cast<int64_t>(b) * ranks + rank, parts = static_cast<int64_t>(p.B) * ranks;
-        for (int t = share(p.n_r, part, parts) + lr; t < share(p.n_r, part + 1, parts); t += RPP) {
-            float x[8];
-            const int64_t row = static_cast<int64_t>(t) * p.H + h;
-            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.r16) + row * p.ld + d0) =
-                make_uint4(pack_f16x2_sat(x[0] * inv[2], x[1] * inv[2]), pack_f16x2_sat(x[2] * inv[2], x[3] * inv[2]),
-                           pack_f16x2_sat(x[4] * inv[2], x[5] * inv[2]), pack_f16x2_sat(x[6] * inv[2], x[7] * inv[2]));
-        }
+        const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(G) + (c >> 2)) * 4));
+        expand8<BITS>(ck, par.x, x);
+        expand8<BITS>(cv, par.y, y);
+        put(p.k_mem, bh * p.n + t, x, inv[0]);
+        put(p.v_mem, bh * p.n + t, y, inv[1]);
+        return;
     }
-    __syncthreads();
-    if (ranks > 1) cluster_sync_all();                    // rank_max stays until every rank has read it
+    t -= p.n;
+    auto seg = [&](const void* v, int64_t sb, int64_t st, int64_t sh) {
+        return static_cast<const uint16_t*>(v) + b * sb + t * st + h * sh;
+    };
+    if (t < p.L) {
+        load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, 0.f, x);
+        load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, 0.f, y);
+        put(p.k_seg, bh * p.L + t, x, inv[0]);
+        put(p.v_seg, bh * p.L + t, y, inv[1]);
+        if (p.q_seg) {
+            load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, 0.f, x);
+            store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
+        }
+        return;
+    }
+    t += x_share(p.n_r, b, p.B) - p.L;
+    if (t < x_share(p.n_r, b + 1, p.B)) {
+        const int64_t row = t * p.H + h;
+        load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
+        put(p.r16, row, x, inv[2]);
+    }
 }
 
 template <int BITS, int G>
-cudaError_t launch_expand(const QexpandParams& p, int ranks, cudaStream_t s)
+cudaError_t launch_expand(const QexpandParams& p, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks, p.H, p.B);
-    cfg.blockDim = dim3(kXThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, qmem_expand_kernel<BITS, G>, p, ranks);
+    // shares of about 128 rows
+    const int parts = std::min<int64_t>(kXSplits, std::max<int64_t>(1, (std::max<int64_t>(p.n / G, p.L) + 127) / 128));
+    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts, p.H, p.B), dim3(kXThreads), 0, s, p);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = static_cast<int64_t>(p.n) + p.L + (p.n_r + p.B - 1) / p.B;
+    const int64_t blocks = (rows * 4 * G + kXThreads - 1) / kXThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_dependent(qmem_expand_kernel<BITS, G>, dim3(static_cast<unsigned>(blocks), p.H, p.B), dim3(kXThreads), 0, s,
+                            p, parts);
 }
 
 template <int BITS, int G>
@@ -493,22 +482,17 @@ cudaError_t launch_any(const QmemParams& p, txl_dtype dtype, bool push, cudaStre
 
 }  // namespace
 
-cudaError_t launch_qmem_expand(const QexpandParams& p, int sm_count, cudaStream_t s)
+cudaError_t launch_qmem_expand(const QexpandParams& p, cudaStream_t s)
 {
-    // CTAs per (b, h): until eight per SM, while each keeps 128 rows
-    int ranks = 1;
-    while (ranks < 8 && static_cast<int64_t>(p.B) * p.H * ranks < 8 * sm_count &&
-           static_cast<int64_t>(p.n) + p.L > 128 * ranks)
-        ranks *= 2;
     switch (p.G * 16 + (p.n > 0 ? p.bits : 4)) {
-    case 1 * 16 + 4: return launch_expand<4, 1>(p, ranks, s);
-    case 2 * 16 + 4: return launch_expand<4, 2>(p, ranks, s);
-    case 3 * 16 + 4: return launch_expand<4, 3>(p, ranks, s);
-    case 4 * 16 + 4: return launch_expand<4, 4>(p, ranks, s);
-    case 1 * 16 + 8: return launch_expand<8, 1>(p, ranks, s);
-    case 2 * 16 + 8: return launch_expand<8, 2>(p, ranks, s);
-    case 3 * 16 + 8: return launch_expand<8, 3>(p, ranks, s);
-    case 4 * 16 + 8: return launch_expand<8, 4>(p, ranks, s);
+    case 1 * 16 + 4: return launch_expand<4, 1>(p, s);
+    case 2 * 16 + 4: return launch_expand<4, 2>(p, s);
+    case 3 * 16 + 4: return launch_expand<4, 3>(p, s);
+    case 4 * 16 + 4: return launch_expand<4, 4>(p, s);
+    case 1 * 16 + 8: return launch_expand<8, 1>(p, s);
+    case 2 * 16 + 8: return launch_expand<8, 2>(p, s);
+    case 3 * 16 + 8: return launch_expand<8, 3>(p, s);
+    case 4 * 16 + 8: return launch_expand<8, 4>(p, s);
     default: return cudaErrorInvalidValue;
     }
 }

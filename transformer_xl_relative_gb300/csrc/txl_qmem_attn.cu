@@ -25,7 +25,7 @@
 // B is masked to the tile's own slots.
 //
 // The position term (q_i+v).r comes from a kernel of its own (qpos_kernel): a product of r's rows with the
-// queries of every batch entry, so that each row of r is read once per 32 (entry, query) pairs, written
+// queries of every batch entry, so that each row of r is read once per 64 (entry, query) pairs, written
 // by key, E[b][h][i][j - jn], and copied into the stages with the codes.  Keys j < jn are at the clamp
 // for every query and take one value per query, far[b][h][i].  (Computed inside the attention kernel
 // instead, for the keys of a block between the steps of the one before, the 32 registers of r rows in
@@ -38,6 +38,7 @@
 // of a head are the ranks of a cluster: each writes its partial results into the shared memory of the
 // rank that finishes the row.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,6 +81,8 @@ __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
     return f32 ? __ldg(static_cast<const float*>(p) + i)
                : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // D += A B: m16n8k16, fp16 operands, fp32 accumulators
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -124,72 +127,102 @@ template <int BITS>
 __device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : (w >> 8) & 0x00ff00ffu; }
 
 // E[b][h][i][x] = (q_i+v).r[min(M+i-j, C)] in log2 units for keys j = jn + x, and far[b][h][i] = (q_i+v).r[C].
-// Grid: (128 distances, head, 32 (entry, query) pairs); warp w takes 16 distances: A = rows of r (bf16, read from
-// global memory as fragments), B = q+v of four pairs as two bf16 parts.
-constexpr int kPosPairs = 32;
+// Bound by reading r once: a CTA prepares q+v of up to pos_pairs (entry, query) pairs of a head as two bf16 parts
+// (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
+// from global memory as fragments) are requested one tile ahead.
+__host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
 template <int NG>
 __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ QattnParams p)
 {
-    constexpr int DP = NG * 32;
-    __shared__ __align__(16) uint16_t qvh[2 * kPosPairs * DP];        // [2 pair + part][DP]
+    constexpr int DP = NG * 32, PAIRS = pos_pairs(NG);
+    __shared__ __align__(16) uint16_t qvh[2 * PAIRS * DP];            // [2 pair + part][DP]
+    __shared__ float* e_key[PAIRS];                                   // E of the pair at x = M + i - jn (distance 0)
+    __shared__ float* far_at[PAIRS];
+    __shared__ int x_zero[PAIRS];                                     // that x
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
-    const int h = blockIdx.y, pair0 = blockIdx.z * kPosPairs, pairs = min(kPosPairs, p.B * p.L - pair0);
-    const int d0 = blockIdx.x * 128 + warp * 16;                      // first distance of the warp
+    const int h = blockIdx.y, pair0 = blockIdx.z * PAIRS, pairs = min(PAIRS, p.B * p.L - pair0);
     // Everything before this kernel is complete when it lets the attention kernel start, which reads the
     // memory and the queries before its own wait.
     pdl_wait();
     pdl_launch_dependents();
-    uint4 a[2][NG];
+    auto load = [&](int d0, uint4 (&a)[2][NG]) {
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        int rr = min(d0 + g + 8 * y, p.C);
-        if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;      // past the distances of the call
-        const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
+        for (int y = 0; y < 2; ++y) {
+            int rr = min(d0 + g + 8 * y, p.C);
+            if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;  // past the distances of the call
+            const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
 #pragma unroll
-        for (int G = 0; G < NG; ++G) {
-            const int d = 32 * G + 8 * c4;
-            if (p.vec_r && d + 8 <= p.D) {
-                a[y][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
-            } else {
-                uint32_t w[4] = {0, 0, 0, 0};
+            for (int G = 0; G < NG; ++G) {
+                const int d = 32 * G + 8 * c4;
+                if (p.vec_r && d + 8 <= p.D) {
+                    a[y][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
+                } else {
+                    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
-                a[y][G] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 8; ++e)
+                        if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
+                    a[y][G] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
         }
+    };
+    uint4 a[2][NG];
+    int d0 = blockIdx.x * 128 + warp * 16;                            // first distance of the warp's tile
+    load(d0, a);
+    const int n_ct = (pairs + 3) >> 2;
+    float vb[NG];
+#pragma unroll
+    for (int e = 0; e < NG; ++e) vb[e] = 32 * e + lane < p.D ? __ldg(p.vb + h * p.D + 32 * e + lane) : 0.f;
+#pragma unroll 4
+    for (int pr = warp; pr < 4 * n_ct; pr += kWarps) {                // a warp per pair
+        const int be = (pair0 + pr) / p.L, i = (pair0 + pr) - be * p.L;
+        const int64_t at = be * p.q_sb + i * p.q_st + h * p.q_sh;
+#pragma unroll
+        for (int e = 0; e < NG; ++e) {
+            const int d = 32 * e + lane;
+            const float c = pr < pairs && d < p.D ? (ld_elem(p.q, at + d, 0) + vb[e]) * p.qscale : 0.f;
+            const __nv_bfloat16 hi = __float2bfloat16_rn(c);
+            qvh[2 * pr * DP + d] = __bfloat16_as_ushort(hi);
+            qvh[(2 * pr + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
+        }
     }
-    for (int x = tid; x < kPosPairs * DP; x += kThreads) {
-        const int pr = x / DP, d = x % DP, be = (pair0 + pr) / p.L, i = (pair0 + pr) % p.L;
-        float c = 0.f;
-        if (pr < pairs && d < p.D)
-            c = (ld_elem(p.q, be * p.q_sb + i * p.q_st + h * p.q_sh + d, 0) + __ldg(p.vb + h * p.D + d)) * p.qscale;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(c);
-        qvh[2 * pr * DP + d] = __bfloat16_as_ushort(hi);
-        qvh[(2 * pr + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
+    if (tid < pairs) {
+        const int be = (pair0 + tid) / p.L, i = (pair0 + tid) % p.L;
+        const int64_t row = (static_cast<int64_t>(be) * p.H + h) * p.L + i;
+        x_zero[tid] = p.M + i - p.jn;
+        e_key[tid] = p.E + row * p.e_pitch + x_zero[tid];
+        far_at[tid] = p.far + row;
     }
     __syncthreads();
-    if (d0 >= p.n_dist) return;
-    for (int ct = 0; 4 * ct < pairs; ++ct) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (; d0 < p.n_dist; d0 += gridDim.x * 128) {
+        uint4 next[2][NG];
+        load(d0 + static_cast<int>(gridDim.x) * 128, next);
+        for (int ct = 0; ct < n_ct; ++ct) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int G = 0; G < NG; ++G) {
+                const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
+                mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
+                mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
+            }
+            const int pr = 4 * ct + c4;
+            if (pr < pairs) {
+                float* e = e_key[pr];
+                const int x0 = x_zero[pr];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int delta = d0 + g + 8 * y;
+                    const float v = acc[2 * y] + acc[2 * y + 1];
+                    if (delta <= x0) e[-delta] = v;
+                    if (delta == p.C) *far_at[pr] = v;
+                }
+            }
+        }
 #pragma unroll
         for (int G = 0; G < NG; ++G) {
-            const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
-            mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
-            mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
-        }
-        const int pr = 4 * ct + c4;
-        if (pr < pairs) {
-            const int be = (pair0 + pr) / p.L, i = (pair0 + pr) % p.L;
-            const int64_t row = (static_cast<int64_t>(be) * p.H + h) * p.L + i;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int delta = d0 + g + 8 * y, x = p.M + i - delta - p.jn;
-                const float v = acc[2 * y] + acc[2 * y + 1];
-                if (x >= 0 && delta >= 0 && x < p.e_pitch) p.E[row * p.e_pitch + x] = v;
-                if (delta == p.C) p.far[row] = v;
-            }
+            a[0][G] = next[0][G];
+            a[1][G] = next[1][G];
         }
     }
 }
@@ -264,6 +297,15 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             if (p.f32) q_raw[e] = __ldg(static_cast<const uint32_t*>(p.q) + at);
             else q_raw[e] = __ldg(static_cast<const uint16_t*>(p.q) + at);
         }
+    }
+
+    // ---- and the lines of the segment's own keys and values (the last rank's work), into L2
+    const bool has_own = rank == sp.ranks - 1;
+    const int n_own = i0 + Lq;                            // own keys any of these queries sees
+    if (has_own && tid < n_own) {
+        const int e = p.f32 ? 4 : 2;
+        prefetch_l2(static_cast<const char*>(p.kcur) + (b * p.kc_sb + tid * p.kc_st + h * p.kc_sh) * e);
+        prefetch_l2(static_cast<const char*>(p.vcur) + (b * p.vc_sb + tid * p.vc_st + h * p.vc_sh) * e);
     }
 
     // ---- this warp's copies: stage n covers keys j_lo + (8 n + warp) KS ..; rows as they are in memory, one bulk
@@ -401,9 +443,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             if (n < n_stage) copy_e(n);
     }
 
-    // ---- scores of the segment's own keys (the last rank's work): eight lanes per (query, key)
-    const bool has_own = rank == sp.ranks - 1;
-    const int n_own = i0 + Lq;                            // own keys any of these queries sees
+    // ---- scores of the segment's own keys: eight lanes per (query, key)
     if (has_own) {
         for (int x0 = warp * 4; x0 < Lq * n_own; x0 += kWarps * 4) {
             const int x = min(x0 + (lane >> 3), Lq * n_own - 1);
@@ -776,9 +816,18 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
     auto* kernel = qattn_kernel<BITS, NG, QT, ONE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && sp.ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    // once per device: the shared memory, and clusters of sixteen
+    static std::atomic<uint64_t> prepared{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(prepared.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        prepared.fetch_or(bit, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
@@ -815,7 +864,10 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
         e = launch_dependent(qpos_f32_kernel, dim3((p.n_dist + kThreads - 1) / kThreads, p.H, std::min<int64_t>(pairs, 256)),
                              dim3(kThreads), 0, s, p);
     } else {
-        const dim3 grid((p.n_dist + 127) / 128, p.H, static_cast<unsigned>((pairs + kPosPairs - 1) / kPosPairs));
+        // as many CTAs as three per SM, each walking over its share of the distances
+        const int64_t tiles = (p.n_dist + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
+        const int64_t per_head = std::max<int64_t>(1, 3 * sm_count / (sets * p.H));
+        const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
         e = ng == 2 ? launch_dependent(qpos_kernel<2>, grid, dim3(kThreads), 0, s, p)
                     : launch_dependent(qpos_kernel<4>, grid, dim3(kThreads), 0, s, p);
     }

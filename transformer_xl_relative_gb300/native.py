@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # TXL_CHECKED=1 selects the range-checked build of the same library (built on request by
@@ -29,6 +30,7 @@ EXPORTS = (
     "txl_rel_attn_table_path", "txl_rel_attn_decode_path", "txl_rel_attn_fwd_lse", "txl_rel_attn_bwd_lse",
     "txl_rel_attn_bwd_path", "txl_qmem_code_bytes", "txl_qmem_par_bytes", "txl_qmem_push", "txl_qmem_read",
     "txl_rel_attn_qmem", "txl_rel_attn_qmem_workspace_size", "txl_rel_attn_qmem_path",
+    "txl_rel_attn_qmem_call",
 )
 
 
@@ -49,6 +51,11 @@ class TxlQmem(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("par", ctypes.c_void_p),
                 ("B", ctypes.c_int), ("M", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
                 ("bits", ctypes.c_int), ("wp", ctypes.c_int), ("valid", ctypes.c_int)]
+
+
+# txl_rel_attn_qmem_args: B, L, H, D, clamp_len, n_rows, dtype, scale; the views q, k_cur, v_cur, out; mem, u,
+# v_bias, r, ld_r, workspace, workspace_bytes, err_flag, stream (pointers as unsigned 64-bit numbers)
+QMEM_ARGS = struct.Struct("@7if" + 4 * "Qqqq" + "QQQQqQQQQ")
 
 
 class TxlError(RuntimeError):
@@ -150,6 +157,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.txl_rel_attn_qmem.argtypes = [i, i, i, i, i, V, Qp, V, V, vp, vp, vp, i64, i, fp, V, i,
                                       vp, ctypes.c_size_t, vp, vp]
     lib.txl_rel_attn_qmem.restype = i
+    lib.txl_rel_attn_qmem_call.argtypes = [ctypes.c_char_p]
+    lib.txl_rel_attn_qmem_call.restype = i
     lib.txl_rel_attn_qmem_workspace_size.argtypes = [i, i, i, i, Qp, i]
     lib.txl_rel_attn_qmem_workspace_size.restype = ctypes.c_size_t
     lib.txl_rel_attn_qmem_path.argtypes = [i, i, i, i, V, Qp, V, V, vp, i64, V, i]
