@@ -93,26 +93,47 @@ __device__ __forceinline__ void store8(void* row, int d0, int D, bool vec, const
         }
 }
 
-// One lane's part (eight channels, `live` of them inside D) of quantising a group shared by four
-// consecutive lanes.  Returns the codes and the group's step and lo.
-template <int BITS>
-__device__ __forceinline__ void quantise8(const float* x, int live, uint32_t* code, float& step, float& lo)
+__device__ __forceinline__ float min_nan(float a, float b)      // NaN if either is
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// One lane's part (eight channels; ALL: every group is whole, else `live` of them inside D) of quantising
+// a group shared by four consecutive lanes.  Returns the codes and the group's step and lo.
+//
+// Eight instructions per channel: minimum and maximum; d = x - lo; y = d / step + 1.5 2^23, whose low bits
+// are the rounded quotient c; the remainder e = d - c step, which is exact; and a shift-add into the code
+// word, the constant bits of the y subtracted once.  Where |e| comes to half a step (bf16 inputs: one
+// channel in 300 at 4 bits, exact ties) the channels of the lane are decided again, with what the
+// subtraction x - lo lost.
+template <int BITS, bool ALL>
+__device__ __forceinline__ void quantise8(const float* xin, int live, uint32_t* code, float& step, float& lo)
 {
     constexpr float n = static_cast<float>((1 << BITS) - 1);
-    float mn = INFINITY, mx = -INFINITY;
-    bool bad = false;
+    constexpr float kMagic = 12582912.f;                    // 1.5 2^23
+    constexpr uint32_t kMagicBits = 0x4B400000u;
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < live) {
-            mn = fminf(mn, x[e]);
-            mx = fmaxf(mx, x[e]);
-            bad |= !(fabsf(x[e]) < INFINITY);
+    for (int e = 0; e < 8; ++e) x[e] = xin[e];
+    float mn = ALL || live > 0 ? x[0] : INFINITY, mx = ALL || live > 0 ? x[0] : -INFINITY;
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+        if (ALL || e < live) {
+            mn = min_nan(mn, x[e]);
+            mx = max_nan(mx, x[e]);
         }
 #pragma unroll
     for (int off = 1; off <= 2; off <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        bad |= __shfl_xor_sync(0xffffffffu, bad ? 1 : 0, off) != 0;
+        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     }
     lo = bf16_floor(mn);
     // max - lo = span + err exactly
@@ -127,36 +148,63 @@ __device__ __forceinline__ void quantise8(const float* x, int live, uint32_t* co
     const float down = __uint_as_float(__float_as_uint(step) - (step > 0.f ? 0x10000u : 0u));
     if (below(step)) step = __uint_as_float(__float_as_uint(step) + 0x10000u);
     else if (!below(down)) step = down;
-    bad |= !(span < INFINITY) || !(lo > -INFINITY);    // (then step = span / n is finite too)
-    if (bad) step = lo = __uint_as_float(0x7fc00000u);
-
-    // quotients from the reciprocal (a tiny step scaled up first, so that it has one); within 1e-4 of
-    // the exact quotient, so only those near a half need the exact comparison with (c + 1/2) step
-    const float sc = step < 1e-30f ? kTwo64 : 1.f;
-    const float inv = step > 0.f ? 1.f / (step * sc) : 0.f;
-    uint32_t c[8];
+    // (a NaN or an infinity in the group, or a range that is not finite; otherwise step = span / n is finite too)
+    const bool bad = !(span < INFINITY) || !(lo > -INFINITY);
+    float st = step, l = lo;
+    if (bad || !(step > 0.f)) {                        // every code is 0
+        if (bad) step = lo = __uint_as_float(0x7fc00000u);
+        code[0] = 0;
+        if constexpr (BITS == 8) code[1] = 0;
+        return;
+    }
+    if (step < 1e-30f) {                               // scaled up (exactly), so that its reciprocal is finite
+        st *= kTwo64;
+        l *= kTwo64;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= kTwo64;
+    }
+    const float inv = 1.f / st;
+    const float half = 0.5f * st, nearly = half * (1.f - 1.f / 16384.f);   // what x - lo lost is below 2^-15 half
+    float y[8];
+    bool close = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float d = x[e] - lo;
-        const float t = d * sc * inv;
-        float r = rintf(t);
-        if (fabsf(t - r) > 0.499f && e < live) {
-            const float base = floorf(t);
-            const float diff = d - (base + 0.5f) * step;           // exact: both sides agree to a factor of 2
-            const float b2 = d - x[e];
-            const float lost = (x[e] - (d - b2)) + (-lo - b2);     // x - lo = d + lost exactly
-            const bool up = diff > 0.f || (diff == 0.f && lost > 0.f);
-            const bool tie = diff == 0.f && lost == 0.f;
-            r = up ? base + 1.f : base;
-            if (tie) r = 2.f * rintf(0.5f * base) == base ? base : base + 1.f;
-        }
-        c[e] = e < live && !bad ? static_cast<uint32_t>(r) : 0u;
+        const float d = x[e] - l;
+        y[e] = fmaf(d, inv, kMagic);
+        close |= fabsf(fmaf(kMagic - y[e], st, d)) >= nearly;
     }
+    if (close) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = x[e] - l, b2 = d - x[e];
+            const float lost = (x[e] - (d - b2)) + (-l - b2);              // x - lo = d + lost exactly
+            const float rem = fmaf(kMagic - y[e], st, d);
+            const float over = fabsf(rem) - half;                          // exact: both are near half a step
+            const float more = rem > 0.f ? lost : -lost;
+            const bool past = over > 0.f || (over == 0.f && more > 0.f);   // |over| > |lost| unless over = 0
+            const bool tie = over == 0.f && more == 0.f && (__float_as_uint(y[e]) & 1u);
+            if (past || tie) y[e] += rem > 0.f ? 1.f : -1.f;
+        }
+    }
+    if constexpr (!ALL) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= live) y[e] = kMagic;
+    }
+    auto pack = [&](int e0, int count) {               // sum of y's bits, BITS apart, less their constant parts
+        uint32_t w = 0, c = 0;
+#pragma unroll
+        for (int e = count - 1; e >= 0; --e) {
+            w = (w << BITS) + __float_as_uint(y[e0 + e]);
+            c = (c << BITS) + kMagicBits;
+        }
+        return w - c;
+    };
     if constexpr (BITS == 4) {
-        code[0] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12 | c[4] << 16 | c[5] << 20 | c[6] << 24 | c[7] << 28;
+        code[0] = pack(0, 8);
     } else {
-        code[0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-        code[1] = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+        code[0] = pack(0, 4);
+        code[1] = pack(4, 4);
     }
 }
 
@@ -201,7 +249,7 @@ __device__ __forceinline__ bool q_pos(const QmemParams& p, int64_t i, QPos& o)
 }
 
 template <int BITS, int G, bool F32>
-__global__ void __launch_bounds__(kQThreads) qmem_push_kernel(const __grid_constant__ QmemParams p)
+__global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_constant__ QmemParams p)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -221,22 +269,23 @@ __global__ void __launch_bounds__(kQThreads) qmem_push_kernel(const __grid_const
 #pragma unroll
         for (int e = 0; e < 8; ++e) xk[e] = xv[e] = 0.f;
     }
-    uint32_t ck[2], cv[2];
-    float ks, kl, vs, vl;
-    quantise8<BITS>(xk, live, ck, ks, kl);
-    quantise8<BITS>(xv, live, cv, vs, vl);
-    if (!on) return;
     const int64_t at = code_at<BITS, G>(o.row, o.slot, o.d0);
-    if constexpr (BITS == 4) {
-        *reinterpret_cast<uint32_t*>(p.k + at) = ck[0];
-        *reinterpret_cast<uint32_t*>(p.v + at) = cv[0];
-    } else {
-        *reinterpret_cast<uint2*>(p.k + at) = make_uint2(ck[0], ck[1]);
-        *reinterpret_cast<uint2*>(p.v + at) = make_uint2(cv[0], cv[1]);
+    float step[2], lo[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const float* x = w ? xv : xk;
+        uint32_t c[2];
+        if (p.D == 32 * G) quantise8<BITS, true>(x, 8, c, step[w], lo[w]);
+        else quantise8<BITS, false>(x, live, c, step[w], lo[w]);
+        if (on) {
+            uint8_t* dst = (w ? p.v : p.k) + at;
+            if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = c[0];
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+        }
     }
-    if ((o.d0 & (kQGroup - 1)) == 0) {
+    if (on && (o.d0 & (kQGroup - 1)) == 0) {
         uint2* par = reinterpret_cast<uint2*>(p.par + o.row * q_par_groups(G) * 4) + o.g;
-        *par = make_uint2(par_word(ks, kl), par_word(vs, vl));
+        *par = make_uint2(par_word(step[0], lo[0]), par_word(step[1], lo[1]));
         if (G < q_par_groups(G) && o.g == G - 1) par[1] = make_uint2(0, 0);     // the group that fills the row up
     }
 }
@@ -279,6 +328,57 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     char* rv = static_cast<char*>(p.xv) + (blockIdx.z * p.xv_sb + t * p.xv_st + blockIdx.y * p.xv_sh) * E;
     store8<F32>(rk, o.d0, p.D, p.vec_k, xk);
     store8<F32>(rv, o.d0, p.D, p.vec_v, xv);
+}
+
+// Rows that do not start on 16-byte boundaries: a warp per row, a lane per channel, so that the stores of a
+// warp are contiguous (by eights, each lane's stores lay 16 bytes apart: 16.5 instead of READ_ROWS_US us on the
+// base shape).
+constexpr int kReadRows = 4;                           // rows of a warp, loaded together
+
+template <int BITS, bool F32>
+__global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_constant__ QmemParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
+    const int nc = p.G * BITS / 4;
+    const int64_t head = (static_cast<int64_t>(b) * p.H + h) * p.M;
+    for (int g = 0; g < p.G; ++g) {
+        const int d = 32 * g + lane, byte = d * BITS / 8;
+        const int sh = BITS == 4 ? 4 * (d & 1) : 0, mask = (1 << BITS) - 1;
+        if (d >= p.D) break;
+        uint2 par[kReadRows];
+        int ck[kReadRows], cv[kReadRows];
+#pragma unroll
+        for (int u = 0; u < kReadRows; ++u) {
+            int64_t slot = p.slot0 + min(t0 + u, static_cast<int64_t>(p.n - 1));
+            if (slot >= p.M) slot -= p.M;
+            if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
+            const int64_t row = head + slot;
+            const int64_t at = row * (16 * nc) + ((((byte >> 4) ^ q_swizzle(nc, static_cast<int>(slot))) << 4) | (byte & 15));
+            par[u] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(p.G) + g) * 4));
+            ck[u] = __ldg(p.k + at);
+            cv[u] = __ldg(p.v + at);
+        }
+#pragma unroll
+        for (int u = 0; u < kReadRows; ++u) {
+            const int64_t t = t0 + u;
+            if (t >= p.n) break;
+            const float k = fmaf(__uint_as_float(par[u].x << 16), static_cast<float>((ck[u] >> sh) & mask),
+                                 __uint_as_float(par[u].x & 0xffff0000u));
+            const float v = fmaf(__uint_as_float(par[u].y << 16), static_cast<float>((cv[u] >> sh) & mask),
+                                 __uint_as_float(par[u].y & 0xffff0000u));
+            const int64_t ok = b * p.xk_sb + t * p.xk_st + h * p.xk_sh + d, ov = b * p.xv_sb + t * p.xv_st + h * p.xv_sh + d;
+            if constexpr (F32) {
+                static_cast<float*>(p.xk)[ok] = k;
+                static_cast<float*>(p.xv)[ov] = v;
+            } else {
+                static_cast<__nv_bfloat16*>(p.xk)[ok] = __float2bfloat16_rn(k);
+                static_cast<__nv_bfloat16*>(p.xv)[ov] = __float2bfloat16_rn(v);
+            }
+        }
+    }
 }
 
 // The operands of the fused attention kernels in fp16, which keeps 11 bits where bf16 keeps 8: K and V
@@ -504,6 +604,13 @@ cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t 
 
 cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s)
 {
+    if (!p.vec_k || !p.vec_v) {
+        constexpr int rows = kQThreads / 32 * kReadRows;
+        const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.n) + rows - 1) / rows), p.H, p.B);
+        auto* kernel = p.bits == 4 ? (dtype == TXL_F32 ? qmem_read_rows_kernel<4, true> : qmem_read_rows_kernel<4, false>)
+                                   : (dtype == TXL_F32 ? qmem_read_rows_kernel<8, true> : qmem_read_rows_kernel<8, false>);
+        return launch_dependent(kernel, grid, dim3(kQThreads), 0, s, p);
+    }
     return launch_any(p, dtype, false, s);
 }
 
