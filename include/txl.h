@@ -448,34 +448,28 @@ int txl_rel_attn_table_path(int B, int L, int H, int D, int max_len,
  * and stands for x'_d = lo + step * c_d, so |x'_d - x_d| <= step / 2.  These definitions are met
  * exactly, whatever the input type.  A group with a NaN or an infinity, or one whose lo, step or
  * max - lo is not finite, is held with step = lo = NaN and stands for NaN throughout.
- *   k, v : device, 16-byte aligned, dense [B][H][M][G * 4 * bits] bytes.  A row holds the codes in
- *          the order of d (4 bits: byte t holds d = 2t in its low and d = 2t + 1 in its high half;
- *          codes of d >= D in the last group are 0), its 16-byte chunks permuted by slot: of nc
- *          chunks, chunk c of slot s lies at position c ^ ((s >> 2) & 1) for nc = 2, c ^ ((s >> 1) & 3)
- *          for nc = 4, c ^ (s & 7) for nc = 8, else at c.  (Rows copied to shared memory as they are
- *          can then be read column by column without bank conflicts.)
- *   par  : device, 16-byte aligned, dense bf16 [B][H][M][2 ceil(G/2)][4]: the k step, k lo, v step
- *          and v lo of each group (zeros for the group that makes their number even).
+ *   rows : device, 16-byte aligned, dense [B][H][M][row] bytes, row = txl_qmem_row_bytes(D, bits).  A row
+ *          holds the k codes of G groups in the order of d (4 bits: byte t holds d = 2t in its low and
+ *          d = 2t + 1 in its high half; codes of d >= D are 0), the v codes likewise, then for each
+ *          group four bf16: the k step, k lo, v step and v lo (zeros for one group more where G is
+ *          odd).  That is G * bits / 2 + ceil(G / 2) units of 16 bytes; where their number is a
+ *          multiple of eight, an unused unit follows (eight rows in shared memory must not begin in
+ *          the same banks).  One position of a head is one contiguous piece, and so are its neighbours.
  *   bits : 4 or 8.  D <= 128.
  *   wp, valid : as in txl_mem (logical key j in slot (wp + j) mod M, valid iff j >= M - valid).
- * Slots that are not valid are never read, so the arrays need no initial values.  M = 0 means no
- * memory (the pointers may then be NULL).  Heads and batch entries are contiguous in M so that a
- * head's keys stream from memory.
+ * Slots that are not valid are never read, so the rows need no initial values.  M = 0 means no
+ * memory (rows may then be NULL).
  */
 typedef struct {
-    void* k;
-    void* v;
-    void* par;
+    void* rows;
     int B, M, H, D;
     int bits;
     int wp;
     int valid;
 } txl_qmem;
 
-/* Bytes of each of the k and v arrays, and of the par array, of a quantised memory (0 for an empty
- * or invalid shape). */
-size_t txl_qmem_code_bytes(int B, int M, int H, int D, int bits);
-size_t txl_qmem_par_bytes(int B, int M, int H, int D);
+/* Bytes of a row of a quantised memory (0 for an invalid shape): it takes B * H * M of them. */
+size_t txl_qmem_row_bytes(int D, int bits);
 
 /*
  * txl_qmem_push -- txl_mem_push into a quantised memory: quantises k_new/v_new [B][L][H][D] (device

@@ -81,18 +81,21 @@ def held(x: np.ndarray, bits: int) -> np.ndarray:
     return v.reshape(code.shape)[..., : x.shape[-1]]
 
 
-def unpack(code: torch.Tensor, bits: int, slots) -> np.ndarray:
-    """The code bytes [B, H, n, row] of the given slots of a QuantMemory as codes in the order of d."""
-    c = code.cpu().numpy()
-    nc = c.shape[-1] // 16
-    s = np.asarray(slots)
-    swap = {2: (s >> 2) & 1, 4: (s >> 1) & 3, 8: s & 7}.get(nc, 0 * s)
-    at = np.arange(nc)[None] ^ swap[:, None]                          # position of chunk c in each row
-    c = c.reshape(c.shape[:3] + (nc, 16))
-    c = np.take_along_axis(c, at[None, None, :, :, None], 3).reshape(c.shape[:3] + (-1,))
-    if bits == 8:
-        return c
-    return np.stack((c & 15, c >> 4), -1).reshape(c.shape[:-1] + (-1,))
+def parse(rows: torch.Tensor, D: int, bits: int):
+    """Rows [..., row bytes] of a QuantMemory as (k codes, k step, k lo), (v codes, v step, v lo), and the bf16 left
+    over after the G groups' parameters (one group's zeros where G is odd)."""
+    G = (D + GROUP - 1) // GROUP
+    r = rows.cpu()
+    n = 4 * G * bits
+    par = r[..., 2 * n:2 * n + 8 * (G + G % 2)].contiguous().view(torch.bfloat16).double().numpy()
+    par = par.reshape(par.shape[:-1] + (-1, 4))
+
+    def codes(c):
+        c = c.numpy()
+        return c if bits == 8 else np.stack((c & 15, c >> 4), -1).reshape(c.shape[:-1] + (-1,))
+
+    return ((codes(r[..., :n]), par[..., :G, 0], par[..., :G, 1]),
+            (codes(r[..., n:2 * n]), par[..., :G, 2], par[..., :G, 3]), par[..., G:, :])
 
 
 def f64(t: torch.Tensor) -> np.ndarray:

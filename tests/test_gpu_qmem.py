@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from qmem_common import f64, held, quantise64, quantise_exact, unpack
+from qmem_common import f64, held, parse, quantise64, quantise_exact
 
 pytestmark = pytest.mark.gpu
 
@@ -42,11 +42,9 @@ def tensor(shape, dtype, seed, layout="dense"):
 
 
 def fresh(txl, B, M, H, D, bits, wp=0, valid=0, fill=0xA5):
-    """A memory whose arrays hold a pattern, so that untouched bytes show."""
+    """A memory whose rows hold a pattern, so that untouched bytes show."""
     mem = txl.QuantMemory.empty(B, M, H, D, bits=bits)
-    mem.k.fill_(fill)
-    mem.v.fill_(fill)
-    mem.par.view(torch.uint8).fill_(fill)
+    mem.rows.fill_(fill)
     mem.restore(wp, valid)
     return mem
 
@@ -54,15 +52,12 @@ def fresh(txl, B, M, H, D, bits, wp=0, valid=0, fill=0xA5):
 def expect_slots(mem, x, which, slots, bits):
     """Codes and parameters of x [B, n, H, D] in the given slots."""
     code, step, lo = quantise64(f64(x).transpose(0, 2, 1, 3), bits)
-    got = unpack(getattr(mem, which)[:, :, slots], bits, slots)
-    np.testing.assert_array_equal(got, code)
-    par = f64(mem.par[:, :, slots])
-    G = step.shape[-1]
-    assert (par[..., G:, :] == 0).all()
-    par = par[..., :G, :]
-    o = 0 if which == "k" else 2
-    np.testing.assert_array_equal(par[..., o], step)
-    np.testing.assert_array_equal(par[..., o + 1], lo)
+    k, v, rest = parse(mem.rows[:, :, slots], x.shape[-1], bits)
+    got = k if which == "k" else v
+    np.testing.assert_array_equal(got[0], code)
+    np.testing.assert_array_equal(got[1], step)
+    np.testing.assert_array_equal(got[2], lo)
+    assert (rest == 0).all()
 
 
 PUSH = [
@@ -98,8 +93,7 @@ def test_push_holds_the_definition(txl, c, bits):
     assert mem.state() == ((wp + L) % M, min(min(2, M) + L, M))
     rest = [s for s in range(M) if s not in slots]
     if rest:
-        for t in (mem.k, mem.v, mem.par.view(torch.uint8)):
-            assert (t[:, :, rest] == 0xA5).all()
+        assert (mem.rows[:, :, rest] == 0xA5).all()
 
 
 def special_groups():
@@ -151,11 +145,9 @@ def test_push_at_the_edges(txl, dtype, bits):
     mem = fresh(txl, 1, n, 1, 32, bits)
     txl.qmem_push(mem, k, k)
     torch.cuda.synchronize()
-    for which, o in (("k", 0), ("v", 2)):
-        codes = unpack(getattr(mem, which)[:1, :1], bits, np.arange(n))[0, 0]
-        par = f64(mem.par[0, 0, :, 0])
+    for codes, steps, los in parse(mem.rows[0, 0], 32, bits)[:2]:
         for i, (code, step, lo) in enumerate(ref):
-            assert par[i, o] == step and par[i, o + 1] == lo, (i, par[i], step, lo)
+            assert steps[i, 0] == step and los[i, 0] == lo, (i, steps[i], step, los[i], lo)
             np.testing.assert_array_equal(codes[i], code, err_msg=str((i, x[i])))
 
 
@@ -222,13 +214,12 @@ def test_read_returns_what_is_held(txl, c, bits):
 
 
 def test_a_memory_past_four_gigabytes(txl):
-    """Offsets into the code arrays need 64 bits: 2 heads of 40 million slots of 64 bytes."""
+    """Offsets of rows need 64 bits: 2 heads of 40 million slots of 144 bytes."""
     M, D, bits = 40_000_000, 64, 8
     if torch.cuda.mem_get_info()[0] < 20 << 30:
         pytest.skip("needs 20 GB of device memory")
-    code = [torch.empty(1, 2, M, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    par = torch.empty(1, 2, M, 2, 4, dtype=torch.bfloat16, device="cuda")
-    mem = txl.QuantMemory(code[0], code[1], par, D, bits, wp=M - 40, valid=0)
+    rows = torch.empty(1, 2, M, 144, dtype=torch.uint8, device="cuda")
+    mem = txl.QuantMemory(rows, D, bits, wp=M - 40, valid=0)
     k, v = tensor((1, 100, 2, D), "bf16", 1), tensor((1, 100, 2, D), "bf16", 2)
     txl.qmem_push(mem, k, v)
     assert mem.state() == (60, 100)

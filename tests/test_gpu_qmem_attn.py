@@ -42,9 +42,7 @@ class Call:
         self.mem = None
         if M > 0:
             self.mem = txl.QuantMemory.empty(B, M, H, D, bits=bits)
-            self.mem.k.fill_(0xFF)                     # slots that are not valid hold NaN parameters
-            self.mem.v.fill_(0xFF)
-            self.mem.par.fill_(float("nan"))
+            self.mem.rows.fill_(0xFF)                  # slots that are not valid hold NaN parameters
             self.mem.restore((wp - valid) % M, 0)
             if valid:
                 txl.qmem_push(self.mem, self.kh.cuda(), self.vh.cuda())
@@ -358,9 +356,8 @@ def test_a_memory_past_four_gigabytes(txl):
     if torch.cuda.mem_get_info()[0] < 20 << 30:
         pytest.skip("needs 20 GB of device memory")
     g = torch.Generator().manual_seed(9)
-    code = [torch.empty(1, 2, M, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    par = torch.empty(1, 2, M, 2, 4, dtype=torch.bfloat16, device="cuda")
-    mem = txl.QuantMemory(code[0], code[1], par, D, bits, wp=M - 40, valid=0)
+    rows = torch.empty(1, 2, M, 144, dtype=torch.uint8, device="cuda")
+    mem = txl.QuantMemory(rows, D, bits, wp=M - 40, valid=0)
     kh, vh = (randn(g, 1, 100, 2, D).bfloat16() for _ in range(2))
     txl.qmem_push(mem, kh.cuda(), vh.cuda())
     q, k, v = (randn(g, 1, 1, 2, D).bfloat16() for _ in range(3))

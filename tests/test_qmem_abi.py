@@ -22,37 +22,33 @@ def native():
     return n
 
 
-def qmem(native, B=2, M=128, H=4, D=64, bits=4, wp=0, valid=None, k=FAKE, v=FAKE, par=FAKE):
-    return native.TxlQmem(k, v, par, B, M, H, D, bits, wp, M if valid is None else valid)
+def qmem(native, B=2, M=128, H=4, D=64, bits=4, wp=0, valid=None, rows=FAKE):
+    return native.TxlQmem(rows, B, M, H, D, bits, wp, M if valid is None else valid)
 
 
 def dense(native, B, T, H, D, ptr=FAKE):
     return native.TxlView(ptr, T * H * D, H * D, D)
 
 
-def test_sizes(native):
-    lib = native.load()
-    assert lib.txl_qmem_code_bytes(2, 100, 4, 64, 4) == 2 * 100 * 4 * 32
-    assert lib.txl_qmem_code_bytes(2, 100, 4, 64, 8) == 2 * 100 * 4 * 64
-    assert lib.txl_qmem_code_bytes(1, 1, 1, 41, 4) == 32            # two groups
-    assert lib.txl_qmem_code_bytes(1, 70000, 2, 128, 8) == 70000 * 2 * 128
-    assert lib.txl_qmem_par_bytes(1, 3, 2, 41) == 3 * 2 * 2 * 8
-    assert lib.txl_qmem_par_bytes(1, 3, 2, 65) == 3 * 2 * 4 * 8     # three groups, kept as four
-    assert lib.txl_qmem_par_bytes(1, 3, 2, 32) == 3 * 2 * 2 * 8
-    assert lib.txl_qmem_code_bytes(65535, 2 ** 31 - 1, 1, 128, 8) == 65535 * (2 ** 31 - 1) * 128
-    for bad in ((0, 1, 1, 64, 4), (1, 0, 1, 64, 4), (1, 1, 1, 129, 4), (1, 1, 1, 64, 3), (1, -1, 1, 64, 4)):
-        assert lib.txl_qmem_code_bytes(*bad) == 0
+def test_row_sizes(native):
+    """G groups take G * bits / 2 units of codes and ceil(G / 2) of parameters; never a multiple of eight."""
+    row = native.load().txl_qmem_row_bytes
+    assert row(64, 4) == 80 and row(64, 8) == 144 and row(41, 4) == 80
+    assert row(32, 4) == 48 and row(1, 8) == 80
+    assert row(96, 4) == 144 and row(96, 8) == 224                  # 8 units become 9; 14
+    assert row(128, 4) == 160 and row(128, 8) == 288
+    for bad in ((0, 4), (129, 4), (64, 3), (-1, 8)):
+        assert row(*bad) == 0
 
 
 MEM_ERRORS = [
     (dict(bits=5), "TXL_ERR_UNSUPPORTED"), (dict(D=129), "TXL_ERR_UNSUPPORTED"),
-    (dict(k=None), "TXL_ERR_INVALID_ARG"), (dict(v=None), "TXL_ERR_INVALID_ARG"),
-    (dict(par=None), "TXL_ERR_INVALID_ARG"), (dict(wp=128), "TXL_ERR_INVALID_ARG"),
+    (dict(rows=None), "TXL_ERR_INVALID_ARG"), (dict(wp=128), "TXL_ERR_INVALID_ARG"),
     (dict(wp=-1), "TXL_ERR_INVALID_ARG"), (dict(valid=129), "TXL_ERR_INVALID_ARG"),
     (dict(valid=-1), "TXL_ERR_INVALID_ARG"), (dict(M=-1, valid=0), "TXL_ERR_INVALID_ARG"),
     (dict(M=0, valid=1), "TXL_ERR_INVALID_ARG"), (dict(B=-1), "TXL_ERR_INVALID_ARG"),
     (dict(H=0), "TXL_ERR_INVALID_ARG"), (dict(D=0), "TXL_ERR_INVALID_ARG"),
-    (dict(k=FAKE + 8), "TXL_ERR_ALIGNMENT"), (dict(par=FAKE + 8), "TXL_ERR_ALIGNMENT"),
+    (dict(rows=FAKE + 8), "TXL_ERR_ALIGNMENT"),
     (dict(B=65536), "TXL_ERR_UNSUPPORTED"), (dict(H=65536), "TXL_ERR_UNSUPPORTED"),
 ]
 
@@ -164,13 +160,11 @@ def test_python_checks():
     import torch
 
     import transformer_xl_relative_gb300 as txl
-    u8, bf = torch.uint8, torch.bfloat16
-    k, par = torch.zeros(1, 2, 8, 32, dtype=u8), torch.zeros(1, 2, 8, 2, 4, dtype=bf)
-    for bad in (lambda: txl.QuantMemory(k, k, par, 64, 5), lambda: txl.QuantMemory(k, k, par, 129, 4),
-                lambda: txl.QuantMemory(k, k, par, 64, 8), lambda: txl.QuantMemory(k, k[:, :, :7], par, 64, 4),
-                lambda: txl.QuantMemory(k, k, par.float(), 64, 4), lambda: txl.QuantMemory(k[0], k[0], par, 64, 4),
-                lambda: txl.QuantMemory(k, k.transpose(1, 2), par, 64, 4),
-                lambda: txl.QuantMemory(k, k, par, 64, 4)):            # the last: not on a CUDA device
+    rows = torch.zeros(1, 2, 8, 80, dtype=torch.uint8)
+    for bad in (lambda: txl.QuantMemory(rows, 64, 5), lambda: txl.QuantMemory(rows, 129, 4),
+                lambda: txl.QuantMemory(rows, 64, 8), lambda: txl.QuantMemory(rows[0], 64, 4),
+                lambda: txl.QuantMemory(rows.float(), 64, 4), lambda: txl.QuantMemory(rows.transpose(1, 2), 64, 4),
+                lambda: txl.QuantMemory(rows, 64, 4)):                # the last: not on a CUDA device
         with pytest.raises(ValueError):
             bad()
 

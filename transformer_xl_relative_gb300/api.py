@@ -404,38 +404,32 @@ def rel_attn_table_path(q, k, v, r_table, max_len: int, out, key_mask=None) -> i
 
 class QuantMemory:
     """K/V memory of M positions per batch entry held as 4- or 8-bit codes (txl_qmem): groups of 32
-    channels of a head share a bf16 step and minimum.  ``k`` and ``v`` are uint8 [B, H, M, row bytes],
-    ``par`` bf16 [B, H, M, groups (an even number), 4]; ``wp``/``valid`` as in Memory.  Filled by qmem_push, read by
-    rel_attn_qmem and qmem_read."""
+    channels of a head share a bf16 step and minimum.  ``rows`` is uint8 [B, H, M, row bytes], a position
+    and head's k codes, v codes and parameters; ``wp``/``valid`` as in Memory.  Filled by qmem_push, read
+    by rel_attn_qmem and qmem_read."""
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, par: torch.Tensor, D: int, bits: int, wp: int = 0,
-                 valid: int = 0):
-        if bits not in (4, 8):
-            raise ValueError("bits must be 4 or 8")
-        if not 1 <= D <= 128:
-            raise ValueError("D must be in 1..128")
-        if k.dim() != 4:
-            raise ValueError("k and v must be uint8 [B, H, M, row bytes]")
-        B, H, M, _ = k.shape
-        G = (D + 31) // 32
-        GP = (G + 1) // 2 * 2
-        for t, shape, dtype in ((k, (B, H, M, 4 * G * bits), torch.uint8), (v, (B, H, M, 4 * G * bits), torch.uint8),
-                                (par, (B, H, M, GP, 4), torch.bfloat16)):
-            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != k.device:
-                raise ValueError("a quantised memory holds contiguous uint8 k, v %s and bf16 par %s on one device"
-                                 % ((B, H, M, 4 * G * bits), (B, H, M, GP, 4)))
-        if not k.is_cuda:
+    def __init__(self, rows: torch.Tensor, D: int, bits: int, wp: int = 0, valid: int = 0):
+        row = self.row_bytes(D, bits)
+        if rows.dim() != 4 or rows.shape[3] != row or rows.dtype != torch.uint8 or not rows.is_contiguous():
+            raise ValueError("a quantised memory of d_head %d holds contiguous uint8 [B, H, M, %d]" % (D, row))
+        if not rows.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
-        self.k, self.v, self.par, self.device = k, v, par, k.get_device()
-        self._c = TxlQmem(k.data_ptr() if M else None, v.data_ptr() if M else None, par.data_ptr() if M else None,
-                          B, M, H, D, bits, int(wp), int(valid))
+        B, H, M, _ = rows.shape
+        self.rows, self.device = rows, rows.get_device()
+        self._c = TxlQmem(rows.data_ptr() if M else None, B, M, H, D, bits, int(wp), int(valid))
         self.address = ctypes.addressof(self._c)          # of the C struct, for calls that take it as a number
+
+    @staticmethod
+    def row_bytes(D: int, bits: int) -> int:
+        """Bytes a position and head take (txl_qmem_row_bytes)."""
+        row = int(_lib().txl_qmem_row_bytes(D, bits))
+        if row == 0:
+            raise ValueError("bits must be 4 or 8 and D in 1..128")
+        return row
 
     @classmethod
     def empty(cls, B, M, H, D, bits=4, device="cuda"):
-        G = (D + 31) // 32
-        code = [torch.zeros(B, H, M, 4 * G * bits, dtype=torch.uint8, device=device) for _ in range(2)]
-        return cls(*code, torch.zeros(B, H, M, (G + 1) // 2 * 2, 4, dtype=torch.bfloat16, device=device), D, bits)
+        return cls(torch.zeros(B, H, M, cls.row_bytes(D, bits), dtype=torch.uint8, device=device), D, bits)
 
     @property
     def M(self) -> int:

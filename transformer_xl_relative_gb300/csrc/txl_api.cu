@@ -1034,9 +1034,9 @@ txl_status check_qmem(const txl_qmem* m)
     if (m->B < 0 || m->M < 0 || m->H <= 0 || m->D <= 0) return TXL_ERR_INVALID_ARG;
     if (m->D > 128 || (m->bits != 4 && m->bits != 8)) return TXL_ERR_UNSUPPORTED;
     if (m->M == 0) return m->valid == 0 ? TXL_OK : TXL_ERR_INVALID_ARG;
-    if (!m->k || !m->v || !m->par) return TXL_ERR_INVALID_ARG;
+    if (!m->rows) return TXL_ERR_INVALID_ARG;
     if (m->wp < 0 || m->wp >= m->M || m->valid < 0 || m->valid > m->M) return TXL_ERR_INVALID_ARG;
-    if (!a16(m->k) || !a16(m->v) || !a16(m->par)) return TXL_ERR_ALIGNMENT;
+    if (!a16(m->rows)) return TXL_ERR_ALIGNMENT;
     if (m->B > 65535 || m->H > 65535) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
 }
@@ -1052,9 +1052,7 @@ QmemParams qmem_params(const txl_qmem* m, const txl_view* xk, const txl_view* xv
     QmemParams p{};
     p.xk = xk->ptr; p.xk_sb = xk->stride_b; p.xk_st = xk->stride_t; p.xk_sh = xk->stride_h;
     p.xv = xv->ptr; p.xv_sb = xv->stride_b; p.xv_st = xv->stride_t; p.xv_sh = xv->stride_h;
-    p.k = static_cast<uint8_t*>(m->k);
-    p.v = static_cast<uint8_t*>(m->v);
-    p.par = static_cast<uint16_t*>(m->par);
+    p.rows = static_cast<uint8_t*>(m->rows);
     p.B = m->B; p.H = m->H; p.D = m->D; p.M = m->M; p.G = q_groups(m->D); p.bits = m->bits;
     p.vec_k = rows16(xk);
     p.vec_v = rows16(xv);
@@ -1102,16 +1100,10 @@ txl_mem read_back_mem(int B, int H, int D, const txl_qmem* mem, txl_dtype dtype,
 
 }  // namespace
 
-size_t txl_qmem_code_bytes(int B, int M, int H, int D, int bits)
+size_t txl_qmem_row_bytes(int D, int bits)
 {
-    if (B <= 0 || M <= 0 || H <= 0 || D <= 0 || D > 128 || (bits != 4 && bits != 8)) return 0;
-    return static_cast<size_t>(B) * H * M * q_groups(D) * 4 * bits;
-}
-
-size_t txl_qmem_par_bytes(int B, int M, int H, int D)
-{
-    if (B <= 0 || M <= 0 || H <= 0 || D <= 0 || D > 128) return 0;
-    return static_cast<size_t>(B) * H * M * q_par_groups(q_groups(D)) * 8;
+    if (D <= 0 || D > 128 || (bits != 4 && bits != 8)) return 0;
+    return q_row_bytes(q_groups(D), bits);
 }
 
 txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v_new, int L, txl_dtype dtype,
@@ -1168,7 +1160,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
     if (L <= kDecodeMaxL) return 5;
     if (!mem || mem->valid == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
     if (dtype == TXL_BF16) return 1;
-    const txl_mem m = read_back_mem(B, H, D, mem, dtype, mem->k);   // an aligned address; nothing is read
+    const txl_mem m = read_back_mem(B, H, D, mem, dtype, mem->rows);  // an aligned address; nothing is read
     return txl_rel_attn_path(B, L, H, D, q, &m, k_cur, v_cur, r, ld_r, out, dtype);
 }
 
@@ -1199,9 +1191,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
             const int ld = (D + 7) / 8 * 8;
             const int64_t seg = static_cast<int64_t>(B) * H * L * ld;
             QexpandParams e{};
-            e.k = static_cast<const uint8_t*>(mem->k);
-            e.v = static_cast<const uint8_t*>(mem->v);
-            e.par = static_cast<const uint16_t*>(mem->par);
+            e.rows = static_cast<const uint8_t*>(mem->rows);
             e.B = B; e.H = H; e.D = D; e.M = M; e.G = q_groups(D); e.bits = mem->bits;
             e.slot0 = ring_slot(mem, M - valid);
             e.n = valid; e.L = L; e.ld = ld;
@@ -1249,9 +1239,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.vcur = v_cur->ptr; p.vc_sb = v_cur->stride_b; p.vc_st = v_cur->stride_t; p.vc_sh = v_cur->stride_h;
     p.out = out->ptr; p.o_sb = out->stride_b; p.o_st = out->stride_t; p.o_sh = out->stride_h;
     if (valid > 0) {
-        p.k = static_cast<const uint8_t*>(mem->k);
-        p.v = static_cast<const uint8_t*>(mem->v);
-        p.par = static_cast<const uint16_t*>(mem->par);
+        p.rows = static_cast<const uint8_t*>(mem->rows);
         p.bits = mem->bits;
         p.wp = mem->wp;
     }

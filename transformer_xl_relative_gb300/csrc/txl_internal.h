@@ -269,13 +269,15 @@ cudaError_t launch_mem_push(const MemPushParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- quantised memory
 constexpr int kQGroup = 32;         // channels that share a step and a minimum
-// Groups of the parameter rows of G groups: even, so that a row is 16 or 32 bytes.
-__host__ __device__ constexpr int q_par_groups(int G) { return (G + 1) & ~1; }
-// A code row of nc 16-byte chunks holds chunk c at position c ^ q_swizzle(nc, slot): eight consecutive
-// rows, copied to shared memory as they are, then hold one chunk in eight different bank groups.
-__host__ __device__ constexpr int q_swizzle(int nc, int slot)
+// A row (one position and head): the k codes, the v codes, then for every group the bf16 k step, k lo, v step and v
+// lo, an even number of groups; 16-byte units, one more where their number would be a multiple of eight (eight
+// consecutive rows in shared memory must not begin in one bank group).
+__host__ __device__ constexpr int q_v_offset(int G, int bits) { return 4 * G * bits; }
+__host__ __device__ constexpr int q_par_offset(int G, int bits) { return 8 * G * bits; }
+__host__ __device__ constexpr int q_row_bytes(int G, int bits)
 {
-    return nc == 2 ? (slot >> 2) & 1 : nc == 4 ? (slot >> 1) & 3 : nc == 8 ? slot & 7 : 0;
+    const int units = G * bits / 2 + (G + 1) / 2;
+    return 16 * (units + (units % 8 == 0));
 }
 
 // Push (positions t0 .. t0+n-1 of the segment into slots (slot0 + t) mod M) and read (n logical
@@ -284,8 +286,7 @@ __host__ __device__ constexpr int q_swizzle(int nc, int slot)
 struct QmemParams {
     void* xk; int64_t xk_sb, xk_st, xk_sh;
     void* xv; int64_t xv_sb, xv_st, xv_sh;
-    uint8_t* k; uint8_t* v;             // [B][H][M][G * 4 * bits]
-    uint16_t* par;                      // bf16 [B][H][M][q_par_groups(G)][4]
+    uint8_t* rows;                      // [B][H][M][q_row_bytes(G, bits)]
     int B, H, D, M, G, bits;
     int slot0, t0, n;
     int vec_k, vec_v;                   // every row of the tensor starts on a 16-byte boundary
@@ -297,7 +298,7 @@ cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t 
 // The fp16 operands of the fused attention over a quantised memory (positions slot0 .. of the ring,
 // n of them) and a segment of L: K, V and q head-major [B][H][rows][ld], ld = D rounded up to 8.
 struct QexpandParams {
-    const uint8_t* k; const uint8_t* v; const uint16_t* par;
+    const uint8_t* rows;
     int B, H, D, M, G, bits, slot0, n, L, ld;
     const void* vcur; int64_t vc_sb, vc_st, vc_sh;
     const void* kcur; int64_t kc_sb, kc_st, kc_sh;
@@ -321,7 +322,7 @@ struct QattnParams {
     const void* kcur; int64_t kc_sb, kc_st, kc_sh;
     const void* vcur; int64_t vc_sb, vc_st, vc_sh;
     void* out; int64_t o_sb, o_st, o_sh;
-    const uint8_t* k; const uint8_t* v; const uint16_t* par;
+    const uint8_t* rows;                        // of the memory
     const float* u; const float* vb;
     const void* r; int64_t r_row, r_head;       // element strides of the r table
     int f32;                                    // dtype: 1 = fp32, 0 = bf16

@@ -10,9 +10,8 @@
 // corrected where the exact value could lie on the other side of a border (all comparisons below
 // are between exactly represented numbers).
 //
-// Both kernels are bound by HBM.  Four lanes share a group, eight channels each: 16-byte accesses to
-// bf16 rows, and consecutive threads walk the groups of a row, then the positions of one head, which
-// are contiguous in the code arrays.
+// Four lanes share a group, eight channels each: 16-byte accesses to bf16 rows, and consecutive threads walk the
+// groups of a row, then the positions of one head, whose rows are contiguous.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -214,18 +213,8 @@ __device__ __forceinline__ uint32_t par_word(float step, float lo)
     return (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
-// Byte offset, in the code arrays, of the eight channels from d0 of a row.
-template <int BITS, int G>
-__device__ __forceinline__ int64_t code_at(int64_t row, int slot, int d0)
-{
-    constexpr int NC = G * BITS / 4;
-    const int byte = d0 * BITS / 8;
-    return row * (16 * NC) + ((((byte >> 4) ^ q_swizzle(NC, slot)) << 4) | (byte & 15));
-}
-
 struct QPos {
-    int64_t row;          // row of the code and parameter arrays
-    int slot;
+    int64_t row;          // of the memory
     int t, g, d0;         // position of the segment, group, first channel of the lane
 };
 
@@ -243,7 +232,6 @@ __device__ __forceinline__ bool q_pos(const QmemParams& p, int64_t i, QPos& o)
     if (slot >= p.M) slot -= p.M;
     const bool live = t < p.n;
     if (live && !in_range(slot, 0, p.M, p.chk)) slot = 0;
-    o.slot = static_cast<int>(slot);
     o.row = (static_cast<int64_t>(blockIdx.z) * p.H + blockIdx.y) * p.M + slot;
     return live;
 }
@@ -269,7 +257,7 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < 8; ++e) xk[e] = xv[e] = 0.f;
     }
-    const int64_t at = code_at<BITS, G>(o.row, o.slot, o.d0);
+    uint8_t* row = p.rows + o.row * q_row_bytes(G, BITS);
     float step[2], lo[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -278,15 +266,15 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
         if (p.D == 32 * G) quantise8<BITS, true>(x, 8, c, step[w], lo[w]);
         else quantise8<BITS, false>(x, live, c, step[w], lo[w]);
         if (on) {
-            uint8_t* dst = (w ? p.v : p.k) + at;
+            uint8_t* dst = row + w * q_v_offset(G, BITS) + o.d0 * BITS / 8;
             if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = c[0];
             else *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
         }
     }
     if (on && (o.d0 & (kQGroup - 1)) == 0) {
-        uint2* par = reinterpret_cast<uint2*>(p.par + o.row * q_par_groups(G) * 4) + o.g;
+        uint2* par = reinterpret_cast<uint2*>(row + q_par_offset(G, BITS)) + o.g;
         *par = make_uint2(par_word(step[0], lo[0]), par_word(step[1], lo[1]));
-        if (G < q_par_groups(G) && o.g == G - 1) par[1] = make_uint2(0, 0);     // the group that fills the row up
+        if (G % 2 && o.g == G - 1) par[1] = make_uint2(0, 0);      // the group that makes their number even
     }
 }
 
@@ -301,6 +289,22 @@ __device__ __forceinline__ void expand8(const uint32_t* code, uint32_t par, floa
     }
 }
 
+// The codes of eight channels from d0 of a row, and their group's parameters.
+template <int BITS, int G>
+__device__ __forceinline__ uint2 row_unit(const uint8_t* row, int d0, uint32_t* ck, uint32_t* cv)
+{
+    const uint8_t* k = row + d0 * BITS / 8;
+    const uint8_t* v = k + q_v_offset(G, BITS);
+    if constexpr (BITS == 4) {
+        ck[0] = __ldg(reinterpret_cast<const uint32_t*>(k));
+        cv[0] = __ldg(reinterpret_cast<const uint32_t*>(v));
+    } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(k)), b = __ldg(reinterpret_cast<const uint2*>(v));
+        ck[0] = a.x; ck[1] = a.y; cv[0] = b.x; cv[1] = b.y;
+    }
+    return __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + d0 / kQGroup);
+}
+
 template <int BITS, int G, bool F32>
 __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_constant__ QmemParams p)
 {
@@ -310,16 +314,8 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
     if (!q_pos<G>(p, i, o)) return;
     constexpr int E = F32 ? 4 : 2;
-    const int64_t at = code_at<BITS, G>(o.row, o.slot, o.d0);
     uint32_t ck[2], cv[2];
-    if constexpr (BITS == 4) {
-        ck[0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
-        cv[0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
-    } else {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at)), b = __ldg(reinterpret_cast<const uint2*>(p.v + at));
-        ck[0] = a.x; ck[1] = a.y; cv[0] = b.x; cv[1] = b.y;
-    }
-    const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (o.row * q_par_groups(G) + o.g) * 4));
+    const uint2 par = row_unit<BITS, G>(p.rows + o.row * q_row_bytes(G, BITS), o.d0, ck, cv);
     float xk[8], xv[8];
     expand8<BITS>(ck, par.x, xk);
     expand8<BITS>(cv, par.y, xv);
@@ -342,7 +338,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
     pdl_wait();
     const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
     const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
-    const int nc = p.G * BITS / 4;
+    const int row_bytes = q_row_bytes(p.G, BITS);
     const int64_t head = (static_cast<int64_t>(b) * p.H + h) * p.M;
     for (int g = 0; g < p.G; ++g) {
         const int d = 32 * g + lane, byte = d * BITS / 8;
@@ -355,11 +351,10 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
             int64_t slot = p.slot0 + min(t0 + u, static_cast<int64_t>(p.n - 1));
             if (slot >= p.M) slot -= p.M;
             if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
-            const int64_t row = head + slot;
-            const int64_t at = row * (16 * nc) + ((((byte >> 4) ^ q_swizzle(nc, static_cast<int>(slot))) << 4) | (byte & 15));
-            par[u] = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(p.G) + g) * 4));
-            ck[u] = __ldg(p.k + at);
-            cv[u] = __ldg(p.v + at);
+            const uint8_t* row = p.rows + (head + slot) * row_bytes;
+            par[u] = __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(p.G, BITS)) + g);
+            ck[u] = __ldg(row + byte);
+            cv[u] = __ldg(row + q_v_offset(p.G, BITS) + byte);
         }
 #pragma unroll
         for (int u = 0; u < kReadRows; ++u) {
@@ -420,7 +415,8 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
         int64_t s = static_cast<int64_t>(p.slot0) + t;
         if (s >= p.M) s -= p.M;
         if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.par + ((bh * p.M + s) * q_par_groups(G) + g) * 4));
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
+                                                              q_par_offset(G, BITS)) + g);
         const uint32_t kv[2] = {w.x, w.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -499,16 +495,8 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
         int64_t s = static_cast<int64_t>(p.slot0) + t;
         if (s >= p.M) s -= p.M;
         if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        const int64_t row = bh * p.M + s, at = code_at<BITS, G>(row, static_cast<int>(s), d0);
         uint32_t ck[2], cv[2];
-        if constexpr (BITS == 4) {
-            ck[0] = __ldg(reinterpret_cast<const uint32_t*>(p.k + at));
-            cv[0] = __ldg(reinterpret_cast<const uint32_t*>(p.v + at));
-        } else {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.k + at)), w = __ldg(reinterpret_cast<const uint2*>(p.v + at));
-            ck[0] = a.x; ck[1] = a.y; cv[0] = w.x; cv[1] = w.y;
-        }
-        const uint2 par = __ldg(reinterpret_cast<const uint2*>(p.par + (row * q_par_groups(G) + (c >> 2)) * 4));
+        const uint2 par = row_unit<BITS, G>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS), d0, ck, cv);
         expand8<BITS>(ck, par.x, x);
         expand8<BITS>(cv, par.y, y);
         put(p.k_mem, bh * p.n + t, x, inv[0]);

@@ -67,7 +67,7 @@ __host__ __device__ constexpr int stage_keys(int bits, int ng, int qt) { return 
 __host__ __device__ constexpr int stage_rows(int qt, bool one) { return one ? 1 : 4 * qt; }
 __host__ __device__ constexpr int stage_bytes(int bits, int ng, int qt, bool one)
 {
-    return stage_keys(bits, ng, qt) * (8 * ng * bits + 8 * ng + 4 * stage_rows(qt, one));
+    return stage_keys(bits, ng, qt) * (q_row_bytes(ng, bits) + 4 * stage_rows(qt, one));
 }
 
 struct QSplit {               // how the host divides the work
@@ -257,7 +257,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     constexpr int NC = NG * BITS / 4;                     // 16-byte chunks of a code row
     constexpr int CPG = BITS / 4;                         // chunks of a group
     constexpr int KS = stage_keys(BITS, NG, QT);
-    constexpr int kVOff = KS * NC * 16, kParOff = 2 * kVOff, kEOff = kParOff + KS * 8 * NG;   // parts of a stage
+    constexpr int kEOff = KS * q_row_bytes(NG, BITS);     // of a stage: rows, position terms
     constexpr int kStageBytes = stage_bytes(BITS, NG, QT, ONE);
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per register of codes and product
     constexpr int kOwn = ONE ? 1 : kDecodeMaxL;           // keys of the segment a query can see
@@ -308,13 +308,13 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         prefetch_l2(static_cast<const char*>(p.vcur) + (b * p.vc_sb + tid * p.vc_st + h * p.vc_sh) * e);
     }
 
-    // ---- this warp's copies: stage n covers keys j_lo + (8 n + warp) KS ..; rows as they are in memory, one bulk
-    // copy each for the k codes, the v codes and the parameters, two where the ring wraps.  The position terms
-    // follow once qpos_kernel is done; a stage's barrier counts both.
+    // ---- this warp's copies: stage n covers keys j_lo + (8 n + warp) KS ..; its rows as they are in memory, one bulk
+    // copy, two where the ring wraps.  The position terms follow once qpos_kernel is done; a stage's barrier
+    // counts both.
     const int j_lo = static_cast<int>(min(static_cast<int64_t>(p.M), p.lo + static_cast<int64_t>(rank) * sp.range));
     const int j_hi = static_cast<int>(min(static_cast<int64_t>(p.M), static_cast<int64_t>(j_lo) + sp.range));
     const int n_stage = max(0, (j_hi - j_lo - warp * KS + kWarps * KS - 1) / (kWarps * KS));
-    const int nc = p.G * BITS / 4, row_bytes = nc * 16;
+    const int row_bytes = q_row_bytes(p.G, BITS), v_off = q_v_offset(p.G, BITS), par_off = q_par_offset(p.G, BITS);
     uint8_t* my_stages = stages + warp * kStages * kStageBytes;
     uint64_t* full = bars + warp * kStages;
     auto slot_of = [&](int j) {                           // of a logical key
@@ -322,12 +322,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         return static_cast<int>(s >= p.M ? s - p.M : s);
     };
     const uint32_t stage_addr = smem_u32(my_stages), full_addr = smem_u32(full);
-    auto copy_rows = [&](uint32_t st, uint32_t bar, int at, int slot, uint32_t count) {
-        const int64_t row = bh * p.M + slot;
-        bulk_load_addr(st + at * row_bytes, p.k + row * row_bytes, count * row_bytes, bar);
-        bulk_load_addr(st + kVOff + at * row_bytes, p.v + row * row_bytes, count * row_bytes, bar);
-        bulk_load_addr(st + kParOff + at * 8 * NG, p.par + row * NG * 4, count * 8 * NG, bar);
-    };
+    const uint8_t* head = p.rows + bh * p.M * row_bytes;
     // keys of the stage from j with position terms of their own, a multiple of four (a stage starts a
     // multiple of four keys from jn, and the rows of E have room)
     auto near_of = [&](int j) { return max(0, min(KS, (min(KS, j_hi - j) + 3) & ~3) - max(0, p.jn - j)); };
@@ -337,10 +332,10 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         const int live = min(KS, j_hi - j);
         int slot = slot_of(j);
         if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
-        mbar_expect_tx_addr(bar, live * (2 * row_bytes + 8 * NG) + near_of(j) * 4 * Lq);
+        mbar_expect_tx_addr(bar, live * row_bytes + near_of(j) * 4 * Lq);
         const int first = min(live, p.M - slot);
-        copy_rows(st, bar, 0, slot, first);
-        if (first < live) copy_rows(st, bar, first, 0, live - first);
+        bulk_load_addr(st, head + static_cast<uint64_t>(slot) * row_bytes, first * row_bytes, bar);
+        if (first < live) bulk_load_addr(st + first * row_bytes, head, (live - first) * row_bytes, bar);
     };
     auto copy_e = [&](int n) {
         const int j = j_lo + (n * kWarps + warp) * KS, near = near_of(j), x0 = max(0, p.jn - j);
@@ -401,6 +396,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     uint32_t bq[QT][NG * 2][2];
     float qs[QT][NG], sc[QT], far_of[QT];
     const int my_stream = (g >> 1) >> lp_log;             // of the column this lane holds in B operands
+    const int one_key = (g + 2 * c4) & 7;
     const uint16_t* one_row = quh + ((g >> 1) == c4 ? (g & 1) : 2 * kMaxRows) * DP;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
@@ -481,40 +477,24 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         const int js = j_lo + (n * kWarps + warp) * KS;
         const uint8_t* st = my_stages + (n % kStages) * kStageBytes;
         const uint32_t st_addr = stage_addr + (n % kStages) * kStageBytes;
-        const int slot0 = slot_of(js);
-        // permutation of the chunks of the stage's row r: that of its slot, which repeats every eight rows
-        // unless the ring wraps within the stage
-        const bool wraps = slot0 + KS > p.M;
-        auto swap_of = [&](int r) {
-            int s = slot0 + r;
-            if (wraps && s >= p.M) s -= p.M;
-            return q_swizzle(nc, s);
-        };
-        const int swap_lane = q_swizzle(nc, slot0 + (lane & 15)), swap_key = q_swizzle(nc, slot0 + g);
         const bool whole = js + KS <= j_hi;               // no row past the end
         for (int k0 = 0; k0 < (ONE ? 1 : KS); k0 += 16 * NS) {
             if (js + k0 >= j_hi) break;
-            // Q.K: acc[t][G] = for slot c4, keys g and g+8 of its stream's tile, (hi, lo) parts.  ONE: in the
-            // place of group G that of group G ^ gx, gx chosen so that the lanes' rows meet in no bank
+            // Q.K: acc[t][G] = for slot c4, two keys of its stream's tile, (hi, lo) parts: keys g and g+8; ONE:
+            // keys (g + 2 c4) mod 8 and 8 more, so that eight lanes of a load read rows 0 .. 7 of the eight
             float acc[QT][NG][4];
 #pragma unroll
             for (int t = 0; t < QT; ++t)
 #pragma unroll
                 for (int G = 0; G < NG; ++G) acc[t][G][0] = acc[t][G][1] = acc[t][G][2] = acc[t][G][3] = 0.f;
-            const int cx = NC == 2 ? c4 & 1 : NC == 4 ? c4 : 2 * c4;       // chunk c ^ cx in the place of chunk c
-            const int gx = cx / CPG;
             if constexpr (ONE) {
-                // this lane's rows: keys g and g+8 of tile c4 (of the tiles there are)
-                const int r0 = 16 * min(c4, KS / 16 - 1) + g;
-                const uint32_t row0 = st_addr + r0 * row_bytes, row1 = row0 + 8 * row_bytes;
-                const uint32_t sw0 = wraps ? swap_of(r0) : swap_key, sw1 = wraps ? swap_of(r0 + 8) : swap_key;
+                const uint32_t row0 = st_addr + (16 * min(c4, KS / 16 - 1) + one_key) * row_bytes, row1 = row0 + 8 * row_bytes;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const uint32_t cc = c ^ cx;
                     uint32_t wa[4], wb[4];
-                    lds128(row0 + ((cc ^ sw0) << 4), wa);
-                    lds128(row1 + ((cc ^ sw1) << 4), wb);
-                    const uint16_t* bsrc = one_row + cc * (128 / BITS);
+                    lds128(row0 + 16 * c, wa);
+                    lds128(row1 + 16 * c, wb);
+                    const uint16_t* bsrc = one_row + c * (128 / BITS);
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         uint32_t bb[2 * SUB];
@@ -536,12 +516,11 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             } else {
                 for (int T = 0; T < NS; ++T) {
                     const bool on = QT > 1 || my_stream == T;
-                    const int r = k0 + 16 * T + (lane & 15);
-                    const uint32_t row = st_addr + r * row_bytes, swap = wraps ? swap_of(r) : swap_lane;
+                    const uint32_t row = st_addr + (k0 + 16 * T + (lane & 15)) * row_bytes + (lane & 16);
 #pragma unroll
                     for (int c2 = 0; c2 < NC; c2 += 2) {
                         uint32_t w[4];
-                        mma::ldsm_x4(row + (((c2 + (lane >> 4)) ^ swap) << 4), w[0], w[1], w[2], w[3]);
+                        mma::ldsm_x4(row + 16 * c2, w[0], w[1], w[2], w[3]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int c = c2 + half;
@@ -559,19 +538,18 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                 }
             }
             // scores, weights, and the P operands: two keys per lane
-            const int kk = k0 + 16 * (c4 >> lp_log) + g;          // key of the stage (and kk + 8)
+            const int kk = k0 + 16 * (c4 >> lp_log) + (ONE ? one_key : g);     // key of the stage (and kk + 8)
             const bool in_use = (c4 >> lp_log) < NS;              // slots past the streams hold no keys
             uint2 par[2][NG];
-            float kstep[2][NG];
             bool live[2] = {true, true};
-            const uint8_t* par_row = st + kParOff + (in_use ? kk : g) * 8 * NG;
+            const uint8_t* par_row = st + (in_use ? kk : g) * row_bytes + par_off;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int G = 0; G < NG; ++G) {
-                    par[x][G] = *reinterpret_cast<const uint2*>(par_row + 64 * NG * x + 8 * G);
-                    kstep[x][G] = __uint_as_float(
-                        (ONE ? *reinterpret_cast<const uint32_t*>(par_row + 64 * NG * x + 8 * (G ^ gx)) : par[x][G].x) << 16);
+                for (int G = 0; G < NG; G += 2) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(par_row + 8 * x * row_bytes + 8 * G);
+                    par[x][G] = make_uint2(w.x, w.y);
+                    par[x][G + 1] = make_uint2(w.z, w.w);
                 }
             if (!whole || NS << lp_log < 4) {                     // rows past the end hold what was there before
 #pragma unroll
@@ -579,10 +557,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                     live[x] = in_use && js + kk + 8 * x < j_hi;
 #pragma unroll
                     for (int G = 0; G < NG; ++G)
-                        if (!live[x]) {
-                            par[x][G] = make_uint2(0, 0);
-                            kstep[x][G] = 0.f;
-                        }
+                        if (!live[x]) par[x][G] = make_uint2(0, 0);
                 }
             }
             const float* e_st = reinterpret_cast<const float*>(st + kEOff) + (in_use ? kk : g);
@@ -597,7 +572,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                     float a = (x ? near1 : near0) ? e_st[il * KS + 8 * x] : far_of[t], d = 0.f;
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
-                        d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], kstep[x][G], d);
+                        d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], __uint_as_float(par[x][G].x << 16), d);
                         a = fmaf(__uint_as_float(par[x][G].x & 0xffff0000u), qs[t][G], a);
                     }
                     s[x] = live[x] ? fmaf(d, sc[t], a) : -INFINITY;
@@ -661,12 +636,12 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             // P.V: o[t][mt] = for slot c4, channels of row g and g+8 of the tile, (hi, lo) parts
             auto pv_tile = [&](int T) {
                 const bool on = QT > 1 || my_stream == T;
-                const int r = k0 + 16 * T + (lane & 15);
-                const uint32_t row = st_addr + kVOff + r * row_bytes, swap = wraps ? swap_of(r) : swap_lane;
+                const int key = ONE ? ((lane + 2 * T) & 7) | (lane & 8) : lane & 15;
+                const uint32_t row = st_addr + (k0 + 16 * T + key) * row_bytes + v_off + (lane & 16);
 #pragma unroll
                 for (int c2 = 0; c2 < NC; c2 += 2) {
                     uint32_t w[4];
-                    mma::ldsm_x4_t(row + (((c2 + (lane >> 4)) ^ swap) << 4), w[0], w[1], w[2], w[3]);
+                    mma::ldsm_x4_t(row + 16 * c2, w[0], w[1], w[2], w[3]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int c = c2 + half, G = c / CPG;

@@ -28,7 +28,7 @@ EXPORTS = (
     "txl_checked_build", "txl_range_errors", "txl_range_errors_clear", "txl_selftest_range_check",
     "txl_rel_attn_bwd", "txl_rel_attn_bwd_workspace_size", "txl_rel_pos_bwd", "txl_rel_attn_table_fwd",
     "txl_rel_attn_table_path", "txl_rel_attn_decode_path", "txl_rel_attn_fwd_lse", "txl_rel_attn_bwd_lse",
-    "txl_rel_attn_bwd_path", "txl_qmem_code_bytes", "txl_qmem_par_bytes", "txl_qmem_push", "txl_qmem_read",
+    "txl_rel_attn_bwd_path", "txl_qmem_row_bytes", "txl_qmem_push", "txl_qmem_read",
     "txl_rel_attn_qmem", "txl_rel_attn_qmem_workspace_size", "txl_rel_attn_qmem_path",
     "txl_rel_attn_qmem_call",
 )
@@ -48,7 +48,7 @@ class TxlMem(ctypes.Structure):
 
 
 class TxlQmem(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("par", ctypes.c_void_p),
+    _fields_ = [("rows", ctypes.c_void_p),
                 ("B", ctypes.c_int), ("M", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
                 ("bits", ctypes.c_int), ("wp", ctypes.c_int), ("valid", ctypes.c_int)]
 
@@ -146,10 +146,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.txl_rel_attn_decode_path.argtypes = [i, i, i, i, V, Mp, V, V, vp, i64, V, i]
     lib.txl_rel_attn_decode_path.restype = i
     Qp = ctypes.POINTER(TxlQmem)
-    lib.txl_qmem_code_bytes.argtypes = [i, i, i, i, i]
-    lib.txl_qmem_code_bytes.restype = ctypes.c_size_t
-    lib.txl_qmem_par_bytes.argtypes = [i, i, i, i]
-    lib.txl_qmem_par_bytes.restype = ctypes.c_size_t
+    lib.txl_qmem_row_bytes.argtypes = [i, i]
+    lib.txl_qmem_row_bytes.restype = ctypes.c_size_t
     lib.txl_qmem_push.argtypes = [Qp, V, V, i, i, vp]
     lib.txl_qmem_push.restype = i
     lib.txl_qmem_read.argtypes = [Qp, i, i, V, V, i, vp]
