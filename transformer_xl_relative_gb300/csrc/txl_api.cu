@@ -1251,6 +1251,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.qscale = scale * 1.4426950408889634f;
     const int elem = dtype == TXL_F32 ? 4 : 2;
     p.vec_r = a16(r) && s16(ld_r, elem);
+    p.vec_k = a16(k_cur->ptr) && s16(k_cur->stride_b, elem) && s16(k_cur->stride_t, elem) && s16(k_cur->stride_h, elem);
     // keys up to M - C are at the clamp for every query
     const int first_near = std::max<int64_t>(p.lo, std::min<int64_t>(M, static_cast<int64_t>(M) - clamp_len + 1));
     p.jn = first_near - (first_near - p.lo) % 4;

@@ -329,7 +329,7 @@ struct QattnParams {
     int B, L, H, D, M, G, bits, lo, wp, C;      // lo: first valid logical key
     int n_rows;
     float qscale;                               // scale * log2(e)
-    int vec_r;                                  // rows of r start on 16-byte boundaries
+    int vec_r, vec_k;                           // rows of r, of kcur start on 16-byte boundaries
     // position terms, workspace: E[b][h][i][j - jn] for keys j >= jn (own keys too), e_pitch floats per row (a
     // multiple of 4, lo <= jn = lo mod 4), and far[b][h][i] for keys before; n_dist distances are computed
     float* E; float* far;

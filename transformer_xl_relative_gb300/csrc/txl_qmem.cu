@@ -18,6 +18,7 @@
 
 #include "txl_internal.h"
 #include "txl_ptx.cuh"
+#include "txl_rows.cuh"
 
 namespace txl {
 
@@ -36,37 +37,6 @@ __device__ __forceinline__ float bf16_floor(float x)
 __device__ __forceinline__ float bf16_ceil_pos(float x)
 {
     return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
-}
-
-// Eight channels d0 .. d0+7 of a row; channels at or past D read as `fill`.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, float fill, float* x)
-{
-    if (vec && d0 + 8 <= D) {
-        if constexpr (F32) {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + d0);
-            const float4 a = __ldg(q), b = __ldg(q + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + d0));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = __uint_as_float(w[e] << 16);
-                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = fill;
-        if (d0 + e < D) {
-            if constexpr (F32) x[e] = __ldg(static_cast<const float*>(row) + d0 + e);
-            else x[e] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
-        }
-    }
 }
 
 template <bool F32>
@@ -251,8 +221,8 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
     if (on) {
         const char* rk = static_cast<const char*>(p.xk) + (blockIdx.z * p.xk_sb + t * p.xk_st + blockIdx.y * p.xk_sh) * E;
         const char* rv = static_cast<const char*>(p.xv) + (blockIdx.z * p.xv_sb + t * p.xv_st + blockIdx.y * p.xv_sh) * E;
-        load8<F32>(rk, o.d0, p.D, p.vec_k, 0.f, xk);
-        load8<F32>(rv, o.d0, p.D, p.vec_v, 0.f, xv);
+        load8<F32>(rk, o.d0, p.D, p.vec_k, xk);
+        load8<F32>(rv, o.d0, p.D, p.vec_v, xv);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) xk[e] = xv[e] = 0.f;
@@ -430,7 +400,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
 #pragma unroll 4
             for (int t = x_share(p.L, part, parts) + lr; t < s1; t += RPP) {
                 float v[8];
-                load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, 0.f, v);
+                load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) see(which, fabsf(v[e]));
             }
@@ -441,7 +411,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
         for (int i = x_share(samples, part, parts) + lr; i < x_share(samples, part + 1, parts); i += RPP) {
             const int64_t row = static_cast<int64_t>(x_share(p.n_r - 1, i, max(samples - 1, 1))) * p.H + h;
             float v[8];
-            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, v);
+            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) see(2, fabsf(v[e]));
         }
@@ -508,12 +478,12 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
         return static_cast<const uint16_t*>(v) + b * sb + t * st + h * sh;
     };
     if (t < p.L) {
-        load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, 0.f, x);
-        load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, 0.f, y);
+        load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, x);
+        load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, y);
         put(p.k_seg, bh * p.L + t, x, inv[0]);
         put(p.v_seg, bh * p.L + t, y, inv[1]);
         if (p.q_seg) {
-            load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, 0.f, x);
+            load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, x);
             store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
         }
         return;
@@ -521,7 +491,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
     t += x_share(p.n_r, b, p.B) - p.L;
     if (t < x_share(p.n_r, b + 1, p.B)) {
         const int64_t row = t * p.H + h;
-        load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, 0.f, x);
+        load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, x);
         put(p.r16, row, x, inv[2]);
     }
 }

@@ -46,6 +46,7 @@
 #include "txl_internal.h"
 #include "txl_mma.cuh"
 #include "txl_ptx.cuh"
+#include "txl_rows.cuh"
 
 namespace txl {
 
@@ -56,6 +57,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 constexpr int kMaxRanks = 16;                  // CTAs of a cluster (beyond 8: not portable, but this GPU's)
 constexpr int kMaxRows = 8;                    // queries of a CTA
+static_assert(kWarps + kDecodeMaxL <= 32 && kMaxRows <= kWarps, "a lane per part of a row, a warp per row");
 constexpr float kNoMax = -3e38f;               // running maximum before any key
 constexpr float kTwo24 = 16777216.f;
 constexpr float kMinUnit = 3.00926553e-36f;    // 2^-118 and 2^126: bounds of the weights' unit, so that a weight
@@ -268,7 +270,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     float* norm = inbox + kMaxRanks * (DP + 4);           // [row]: what the fp16 parts of qu are multiples of
     float* qsum = norm + kMaxRows;                        // [row][NG]: group sums of qu
     float* own_s = qsum + kMaxRows * NG;                  // [row][kOwn]: scores of the segment's own keys
-    uint16_t* quh = reinterpret_cast<uint16_t*>(own_s + kMaxRows * kDecodeMaxL);   // [2 row + part][DP], a row of zeros
+    float* weights = own_s + kMaxRows * kDecodeMaxL;      // [row][32]: of the parts that make the result
+    uint16_t* quh = reinterpret_cast<uint16_t*>(weights + kMaxRows * 32);   // [2 row + part][DP], a row of zeros
     uint64_t* bars = reinterpret_cast<uint64_t*>(quh + (2 * kMaxRows + 1) * DP);   // [warp][stage]: copies landed
     int* abort_flag = reinterpret_cast<int*>(bars + kWarps * kStages);
 
@@ -437,25 +440,6 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
         for (int n = 0; n < kStages; ++n)
             if (n < n_stage) copy_e(n);
-    }
-
-    // ---- scores of the segment's own keys: eight lanes per (query, key)
-    if (has_own) {
-        for (int x0 = warp * 4; x0 < Lq * n_own; x0 += kWarps * 4) {
-            const int x = min(x0 + (lane >> 3), Lq * n_own - 1);
-            const int row = x / n_own, j = x % n_own, i = i0 + row;
-            float s = 0.f;
-#pragma unroll 4
-            for (int e = 0; e < DP / 8; ++e) {
-                const int d = (lane & 7) + 8 * e;
-                if (j <= i && d < p.D)
-                    s = fmaf(qu[row * DP + d], ld_elem(p.kcur, b * p.kc_sb + j * p.kc_st + h * p.kc_sh + d, p.f32), s);
-            }
-#pragma unroll
-            for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            if ((lane & 7) == 0)
-                own_s[row * kOwn + j] = j <= i ? s + __ldg(e_row0 + row * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
-        }
     }
 
     // ---- running state of slot c4: maximum, weight unit rf (O is in units of rf), sums
@@ -671,6 +655,29 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             copy_e(n + kStages);
         }
     }
+    // ---- scores of the segment's own keys: eight lanes per (query, key), eight channels at a time.  (After the
+    // key loop: before it the loads waited behind the copies, 10000 cycles, with the queries of all warps.)
+    if (has_own) {
+        for (int x0 = warp * 4; x0 < Lq * n_own; x0 += kWarps * 4) {
+            const int x = min(x0 + (lane >> 3), Lq * n_own - 1);
+            const int row = x / n_own, j = x % n_own, i = i0 + row;
+            const int64_t at = b * p.kc_sb + j * p.kc_st + h * p.kc_sh;
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < DP / 64; ++e) {
+                const int d = 64 * e + 8 * (lane & 7);
+                float k[8];
+                if (p.f32) load8<true>(static_cast<const float*>(p.kcur) + at, d, p.D, p.vec_k, k);
+                else load8<false>(static_cast<const uint16_t*>(p.kcur) + at, d, p.D, p.vec_k, k);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) s = fmaf(qu[row * DP + d + y], k[y], s);
+            }
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            if ((lane & 7) == 0)
+                own_s[row * kOwn + j] = j <= i ? s + __ldg(e_row0 + row * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
+        }
+    }
     if (n < n_stage && lane == 0)                         // abandoned: no copy may land after the CTA has gone
         for (int x = n; x < min(n + kStages, n_stage); ++x) {
             int never = 0;
@@ -725,41 +732,43 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     }
     if (sp.ranks > 1) cluster_wait();                     // every rank has started
     __syncthreads();
-    // Row r is finished by rank r mod ranks, whose inbox takes the ranks' partial results of it.
+    // Row r is finished by rank r mod ranks, whose inbox takes the ranks' partial results of it.  First a warp per
+    // row takes the weights of its parts: lanes 0 .. 7 the warps' partial results, the others own keys.
+    if (warp < Lq) {
+        const int own = has_own ? min(i0 + warp + 1, kOwn) : 0;
+        const float* src = part + (min(lane, kWarps - 1) * sp.lq + warp) * (DP + 2);
+        const bool of_warp = lane < kWarps, of_key = lane >= kWarps && lane - kWarps < own;
+        const float val = of_warp ? src[DP] : of_key ? own_s[warp * kOwn + lane - kWarps] : kNoMax;
+        float mx = val;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float w = of_warp || of_key ? ex2_approx(val - mx) : 0.f;
+        float lt = w * (of_warp ? src[DP + 1] : 1.f);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
+        weights[warp * 32 + lane] = w;
+        if (lane == 0) {
+            float* dst = inbox + (warp / sp.ranks * sp.ranks + rank) * (DP + 2) + DP;
+            st_rank(dst, warp % sp.ranks, mx);
+            st_rank(dst + 1, warp % sp.ranks, lt);
+        }
+    }
+    __syncthreads();
     for (int x = tid; x < Lq * DP; x += kThreads) {
         const int row = x / DP, d = x % DP;
-        const int own = has_own ? i0 + row + 1 : 0;
+        const int own = has_own && d < p.D ? min(i0 + row + 1, kOwn) : 0;
         float v[kOwn];
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            v[j] = j < own && d < p.D ? ld_elem(p.vcur, b * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
-        const float* src = part + row * (DP + 2);
-        const int step = sp.lq * (DP + 2);
-        float mx = kNoMax;
+            v[j] = j < own ? ld_elem(p.vcur, b * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
+        const float* w = weights + row * 32;
+        float ot = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, src[w * step + DP]);
-        for (int j = 0; j < own; ++j) mx = fmaxf(mx, own_s[row * kOwn + j]);
-        float lt = 0.f, ot = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float a = ex2_approx(src[w * step + DP] - mx);
-            lt += src[w * step + DP + 1] * a;
-            ot += src[w * step + d] * a;
-        }
+        for (int k = 0; k < kWarps; ++k) ot = fmaf(part[(k * sp.lq + row) * (DP + 2) + d], w[k], ot);
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            if (j < own) {
-                const float a = ex2_approx(own_s[row * kOwn + j] - mx);
-                lt += a;
-                ot = fmaf(a, v[j], ot);
-            }
-        float* dst = inbox + (row / sp.ranks * sp.ranks + rank) * (DP + 2);
-        const uint32_t to = row % sp.ranks;
-        st_rank(dst + d, to, ot);
-        if (d == 0) {
-            st_rank(dst + DP, to, mx);
-            st_rank(dst + DP + 1, to, lt);
-        }
+            if (j < own) ot = fmaf(w[kWarps + j], v[j], ot);
+        st_rank(inbox + (row / sp.ranks * sp.ranks + rank) * (DP + 2) + d, row % sp.ranks, ot);
     }
     __syncthreads();
     if (sp.ranks > 1) cluster_sync_all();
@@ -786,7 +795,7 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
 {
     constexpr int DP = NG * 32;
     constexpr int staged = kWarps * kStages * stage_bytes(BITS, NG, QT, ONE);
-    constexpr int bytes = staged + (kMaxRows * (DP + 1 + NG + kDecodeMaxL) + kMaxRanks * (DP + 4)) * 4 +
+    constexpr int bytes = staged + (kMaxRows * (DP + 1 + NG + kDecodeMaxL + 32) + kMaxRanks * (DP + 4)) * 4 +
                           (2 * kMaxRows + 1) * DP * 2 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");

@@ -1,0 +1,39 @@
+// txl_rows.cuh -- loads of fp32 or bf16 rows, shared by the kernels of the quantised memory.
+#pragma once
+
+#include <cstdint>
+
+namespace txl {
+
+// Eight channels d0 .. d0+7 of a row; channels at or past D read as 0.  vec: the row starts on a 16-byte boundary.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, float* x)
+{
+    if (vec && d0 + 8 <= D) {
+        if constexpr (F32) {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + d0);
+            const float4 a = __ldg(q), b = __ldg(q + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + d0));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = 0.f;
+        if (d0 + e < D) {
+            if constexpr (F32) x[e] = __ldg(static_cast<const float*>(row) + d0 + e);
+            else x[e] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
+        }
+    }
+}
+
+}  // namespace txl
