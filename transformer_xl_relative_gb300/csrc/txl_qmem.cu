@@ -183,26 +183,29 @@ __device__ __forceinline__ uint32_t par_word(float step, float lo)
     return (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
+// Grid: (ceil(n / rows of a block), H, B); the lanes of a row's groups are consecutive, then the next position of
+// the same head.  32-bit positions, 64-bit offsets from the head's first row.
+template <int G> constexpr int kRowLanes = 4 * G;                      // eight channels each
+template <int G> constexpr int kBlockRows = kQThreads / kRowLanes<G>;
+
 struct QPos {
-    int64_t row;          // of the memory
+    uint8_t* row;         // of the memory
     int t, g, d0;         // position of the segment, group, first channel of the lane
 };
 
-// Grid: (ceil(n * G * 4 / kQThreads), H, B); consecutive threads take the lanes of a row's groups,
-// then the next position of the same head.
-template <int G>
-__device__ __forceinline__ bool q_pos(const QmemParams& p, int64_t i, QPos& o)
+template <int BITS, int G>
+__device__ __forceinline__ bool q_pos(const QmemParams& p, QPos& o)
 {
-    const int64_t t = i / (4 * G);
-    const int rem = static_cast<int>(i - t * (4 * G));
-    o.t = static_cast<int>(t);
-    o.g = rem >> 2;
-    o.d0 = o.g * kQGroup + (rem & 3) * 8;
-    int64_t slot = p.slot0 + t;
-    if (slot >= p.M) slot -= p.M;
-    const bool live = t < p.n;
+    const int lr = threadIdx.x / kRowLanes<G>, c = threadIdx.x % kRowLanes<G>;
+    o.t = static_cast<int>(blockIdx.x) * kBlockRows<G> + lr;
+    o.g = c >> 2;
+    o.d0 = 8 * c;
+    const bool live = lr < kBlockRows<G> && o.t < p.n;
+    unsigned slot = static_cast<unsigned>(p.slot0) + o.t;              // below 2 M
+    if (slot >= static_cast<unsigned>(p.M)) slot -= p.M;
     if (live && !in_range(slot, 0, p.M, p.chk)) slot = 0;
-    o.row = (static_cast<int64_t>(blockIdx.z) * p.H + blockIdx.y) * p.M + slot;
+    uint8_t* head = p.rows + (static_cast<int64_t>(blockIdx.z) * p.H + blockIdx.y) * p.M * q_row_bytes(G, BITS);
+    o.row = head + static_cast<uint64_t>(slot) * static_cast<unsigned>(q_row_bytes(G, BITS));
     return live;
 }
 
@@ -212,8 +215,7 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
     pdl_launch_dependents();
     pdl_wait();
     QPos o;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
-    const bool on = q_pos<G>(p, i, o);                 // the four lanes of a group are on or off together
+    const bool on = q_pos<BITS, G>(p, o);              // the four lanes of a group are on or off together
     constexpr int E = F32 ? 4 : 2;
     float xk[8], xv[8];
     const int live = on ? min(max(p.D - o.d0, 0), 8) : 0;
@@ -227,7 +229,6 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < 8; ++e) xk[e] = xv[e] = 0.f;
     }
-    uint8_t* row = p.rows + o.row * q_row_bytes(G, BITS);
     float step[2], lo[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -236,22 +237,21 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
         if (p.D == 32 * G) quantise8<BITS, true>(x, 8, c, step[w], lo[w]);
         else quantise8<BITS, false>(x, live, c, step[w], lo[w]);
         if (on) {
-            uint8_t* dst = row + w * q_v_offset(G, BITS) + o.d0 * BITS / 8;
+            uint8_t* dst = o.row + w * q_v_offset(G, BITS) + o.d0 * BITS / 8;
             if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = c[0];
             else *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
         }
     }
     if (on && (o.d0 & (kQGroup - 1)) == 0) {
-        uint2* par = reinterpret_cast<uint2*>(row + q_par_offset(G, BITS)) + o.g;
+        uint2* par = reinterpret_cast<uint2*>(o.row + q_par_offset(G, BITS)) + o.g;
         *par = make_uint2(par_word(step[0], lo[0]), par_word(step[1], lo[1]));
         if (G % 2 && o.g == G - 1) par[1] = make_uint2(0, 0);      // the group that makes their number even
     }
 }
 
 template <int BITS>
-__device__ __forceinline__ void expand8(const uint32_t* code, uint32_t par, float* x)
+__device__ __forceinline__ void expand8(const uint32_t* code, float step, float lo, float* x)
 {
-    const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xffff0000u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t c = BITS == 4 ? (code[0] >> (4 * e)) & 15u : (code[e >> 2] >> (8 * (e & 3))) & 255u;
@@ -281,14 +281,13 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     pdl_launch_dependents();
     pdl_wait();
     QPos o;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
-    if (!q_pos<G>(p, i, o)) return;
+    if (!q_pos<BITS, G>(p, o)) return;
     constexpr int E = F32 ? 4 : 2;
     uint32_t ck[2], cv[2];
-    const uint2 par = row_unit<BITS, G>(p.rows + o.row * q_row_bytes(G, BITS), o.d0, ck, cv);
+    const uint2 par = row_unit<BITS, G>(o.row, o.d0, ck, cv);
     float xk[8], xv[8];
-    expand8<BITS>(ck, par.x, xk);
-    expand8<BITS>(cv, par.y, xv);
+    expand8<BITS>(ck, __uint_as_float(par.x << 16), __uint_as_float(par.x & 0xffff0000u), xk);
+    expand8<BITS>(cv, __uint_as_float(par.y << 16), __uint_as_float(par.y & 0xffff0000u), xv);
     const int64_t t = o.t;
     char* rk = static_cast<char*>(p.xk) + (blockIdx.z * p.xk_sb + t * p.xk_st + blockIdx.y * p.xk_sh) * E;
     char* rv = static_cast<char*>(p.xv) + (blockIdx.z * p.xv_sb + t * p.xv_st + blockIdx.y * p.xv_sh) * E;
@@ -356,21 +355,25 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
 // (a group's end points bound its values, so the parameters suffice for the memory), qmem_expand_kernel
 // writes, one lane per eight channels of a row.  (One kernel with a cluster per (b, h), exchanging the
 // maxima through shared memory, took 62 us on the large shape: its CTAs waited for one another.)
-constexpr int kXThreads = 256;
 constexpr int kXSplits = 8;
 
-__device__ __forceinline__ int x_share(int64_t n, int64_t part, int64_t parts) { return static_cast<int>(n * part / parts); }
+// First of the n items that fall to share `part` of `parts`.
+__device__ __forceinline__ int x_share(int n, int part, int parts)
+{
+    const unsigned each = static_cast<unsigned>(n) / parts, more = static_cast<unsigned>(n) - each * parts;
+    return static_cast<int>(each * part + min(static_cast<unsigned>(part), more));
+}
 
 template <int BITS, int G>
-__global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p)
+__global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p)
 {
-    __shared__ float red[3][kXThreads / 32];
+    __shared__ float red[3][kQThreads / 32];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x, h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(b) * p.H + h;
     constexpr int LPR = 4 * G;                            // lanes of a row, eight channels each
-    constexpr int RPP = kXThreads / LPR;                  // rows of a pass
+    constexpr int RPP = kQThreads / LPR;                  // rows of a pass
     const int lr = tid / LPR, d0 = 8 * (tid % LPR);
     const bool lane_on = lr < RPP && d0 < p.D;
 
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
     };
     const int64_t x1 = static_cast<int64_t>(x_share(p.n, part + 1, parts)) * G;
 #pragma unroll 4
-    for (int64_t x = static_cast<int64_t>(x_share(p.n, part, parts)) * G + tid; x < x1; x += kXThreads) {
+    for (int64_t x = static_cast<int64_t>(x_share(p.n, part, parts)) * G + tid; x < x1; x += kQThreads) {
         const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
         int64_t s = static_cast<int64_t>(p.slot0) + t;
         if (s >= p.M) s -= p.M;
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
         rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
         const int samples = min(p.n_r, 64);               // the same rows of r for every entry of the head
         for (int i = x_share(samples, part, parts) + lr; i < x_share(samples, part + 1, parts); i += RPP) {
-            const int64_t row = static_cast<int64_t>(x_share(p.n_r - 1, i, max(samples - 1, 1))) * p.H + h;
+            const int64_t row = (static_cast<int64_t>(p.n_r - 1) * i / 63) * p.H + h;
             float v[8];
             load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, v);
 #pragma unroll
@@ -426,53 +429,59 @@ __global__ void __launch_bounds__(kXThreads) qmem_absmax_kernel(const __grid_con
     if (tid < 3) {
         float m = 0.f;
 #pragma unroll
-        for (int w = 0; w < kXThreads / 32; ++w) m = fmaxf(m, red[tid][w]);
+        for (int w = 0; w < kQThreads / 32; ++w) m = fmaxf(m, red[tid][w]);
         p.absmax[(bh * kXSplits + part) * 4 + tid] = m;
     }
 }
 
 // Grid: x over the lanes of the rows (memory, segment, this entry's share of the head's rows of r), y head, z entry.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
+__global__ void __launch_bounds__(kQThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(b) * p.H + h;
+    const int lr = threadIdx.x / kRowLanes<G>, d0 = 8 * (threadIdx.x % kRowLanes<G>);
+    int t = static_cast<int>(blockIdx.x) * kBlockRows<G> + lr;
+    if (lr >= kBlockRows<G>) t = INT32_MAX;
+    uint32_t ck[2], cv[2];
+    uint2 par;
+    if (t < p.n && d0 < p.D) {                             // requested before the maxima
+        unsigned s = static_cast<unsigned>(p.slot0) + t;
+        if (s >= static_cast<unsigned>(p.M)) s -= p.M;
+        if (!in_range(s, 0, p.M, p.chk)) s = 0;
+        const uint8_t* head = p.rows + bh * p.M * q_row_bytes(G, BITS);
+        par = row_unit<BITS, G>(head + static_cast<uint64_t>(s) * static_cast<unsigned>(q_row_bytes(G, BITS)), d0, ck, cv);
+    }
     float mx[3] = {0.f, 0.f, 0.f}, inv[3];
-    for (int i = 0; i < parts; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p.absmax) + bh * kXSplits + i);
+    for (int y = 0; y < parts; ++y) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.absmax) + bh * kXSplits + y);
         mx[0] = fmaxf(mx[0], a.x); mx[1] = fmaxf(mx[1], a.y); mx[2] = fmaxf(mx[2], a.z);
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const int ex = min(max(static_cast<int>(__float_as_uint(mx[i]) >> 23) - 127 - (i == 1 ? 11 : 0), -115), 115);
-        inv[i] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.units[4 * bh + i] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+    for (int y = 0; y < 3; ++y) {
+        const int ex = min(max(static_cast<int>(__float_as_uint(mx[y]) >> 23) - 127 - (y == 1 ? 11 : 0), -115), 115);
+        inv[y] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.units[4 * bh + y] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
     }
-    constexpr int LPR = 4 * G;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kXThreads + threadIdx.x;
-    int64_t t = i / LPR;
-    const int c = static_cast<int>(i - t * LPR), d0 = 8 * c;
     if (d0 >= p.D) return;
-    auto put = [&](void* base, int64_t row, const float* x, float f) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row * p.ld + d0) =
-            make_uint4(pack_f16x2_sat(x[0] * f, x[1] * f), pack_f16x2_sat(x[2] * f, x[3] * f),
-                       pack_f16x2_sat(x[4] * f, x[5] * f), pack_f16x2_sat(x[6] * f, x[7] * f));
+    const unsigned ld_bytes = 2 * p.ld;
+    auto put = [&](void* base, int64_t first_row, int r, const float* x, float f) {
+        char* dst = static_cast<char*>(base) + first_row * ld_bytes + static_cast<uint64_t>(r) * ld_bytes + 2 * d0;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_f16x2_sat(x[0] * f, x[1] * f), pack_f16x2_sat(x[2] * f, x[3] * f),
+                                                    pack_f16x2_sat(x[4] * f, x[5] * f), pack_f16x2_sat(x[6] * f, x[7] * f));
     };
     float x[8], y[8];
     if (t < p.n) {
-        int64_t s = static_cast<int64_t>(p.slot0) + t;
-        if (s >= p.M) s -= p.M;
-        if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        uint32_t ck[2], cv[2];
-        const uint2 par = row_unit<BITS, G>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS), d0, ck, cv);
-        expand8<BITS>(ck, par.x, x);
-        expand8<BITS>(cv, par.y, y);
-        put(p.k_mem, bh * p.n + t, x, inv[0]);
-        put(p.v_mem, bh * p.n + t, y, inv[1]);
+        // lo + step c in units (a power of two, so scaling the parameters rounds nothing)
+        expand8<BITS>(ck, __uint_as_float(par.x << 16) * inv[0], __uint_as_float(par.x & 0xffff0000u) * inv[0], x);
+        expand8<BITS>(cv, __uint_as_float(par.y << 16) * inv[1], __uint_as_float(par.y & 0xffff0000u) * inv[1], y);
+        put(p.k_mem, bh * p.n, t, x, 1.f);
+        put(p.v_mem, bh * p.n, t, y, 1.f);
         return;
     }
+    if (t == INT32_MAX) return;
     t -= p.n;
     auto seg = [&](const void* v, int64_t sb, int64_t st, int64_t sh) {
         return static_cast<const uint16_t*>(v) + b * sb + t * st + h * sh;
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
     if (t < p.L) {
         load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, x);
         load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, y);
-        put(p.k_seg, bh * p.L + t, x, inv[0]);
-        put(p.v_seg, bh * p.L + t, y, inv[1]);
+        put(p.k_seg, bh * p.L, t, x, inv[0]);
+        put(p.v_seg, bh * p.L, t, y, inv[1]);
         if (p.q_seg) {
             load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, x);
             store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
@@ -490,9 +499,9 @@ __global__ void __launch_bounds__(kXThreads) qmem_expand_kernel(const __grid_con
     }
     t += x_share(p.n_r, b, p.B) - p.L;
     if (t < x_share(p.n_r, b + 1, p.B)) {
-        const int64_t row = t * p.H + h;
+        const int64_t row = static_cast<int64_t>(t) * p.H + h;
         load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, x);
-        put(p.r16, row, x, inv[2]);
+        put(p.r16, row, 0, x, inv[2]);
     }
 }
 
@@ -501,22 +510,18 @@ cudaError_t launch_expand(const QexpandParams& p, cudaStream_t s)
 {
     // shares of about 128 rows
     const int parts = std::min<int64_t>(kXSplits, std::max<int64_t>(1, (std::max<int64_t>(p.n / G, p.L) + 127) / 128));
-    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts, p.H, p.B), dim3(kXThreads), 0, s, p);
+    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts, p.H, p.B), dim3(kQThreads), 0, s, p);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.n) + p.L + (p.n_r + p.B - 1) / p.B;
-    const int64_t blocks = (rows * 4 * G + kXThreads - 1) / kXThreads;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_dependent(qmem_expand_kernel<BITS, G>, dim3(static_cast<unsigned>(blocks), p.H, p.B), dim3(kXThreads), 0, s,
-                            p, parts);
+    if (rows > INT32_MAX - kQThreads) return cudaErrorInvalidValue;
+    return launch_dependent(qmem_expand_kernel<BITS, G>, dim3((rows - 1) / kBlockRows<G> + 1, p.H, p.B), dim3(kQThreads), 0,
+                            s, p, parts);
 }
 
 template <int BITS, int G>
 cudaError_t launch(const QmemParams& p, bool f32, bool push, cudaStream_t s)
 {
-    const int64_t units = static_cast<int64_t>(p.n) * G * 4;
-    const int64_t blocks = (units + kQThreads - 1) / kQThreads;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks), p.H, p.B);
+    const dim3 grid((p.n - 1) / kBlockRows<G> + 1, p.H, p.B);
     auto* kernel = push ? (f32 ? qmem_push_kernel<BITS, G, true> : qmem_push_kernel<BITS, G, false>)
                         : (f32 ? qmem_read_kernel<BITS, G, true> : qmem_read_kernel<BITS, G, false>);
     return launch_dependent(kernel, grid, dim3(kQThreads), 0, s, p);

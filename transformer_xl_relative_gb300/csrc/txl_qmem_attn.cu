@@ -305,10 +305,11 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     // ---- and the lines of the segment's own keys and values (the last rank's work), into L2
     const bool has_own = rank == sp.ranks - 1;
     const int n_own = i0 + Lq;                            // own keys any of these queries sees
-    if (has_own && tid < n_own) {
-        const int e = p.f32 ? 4 : 2;
-        prefetch_l2(static_cast<const char*>(p.kcur) + (b * p.kc_sb + tid * p.kc_st + h * p.kc_sh) * e);
-        prefetch_l2(static_cast<const char*>(p.vcur) + (b * p.vc_sb + tid * p.vc_st + h * p.vc_sh) * e);
+    if (has_own && (tid >> 3) < n_own) {
+        const int e = p.f32 ? 4 : 2, j = tid >> 3, part = (tid & 3) * 128;     // a row has at most four lines
+        const char* src = tid & 4 ? static_cast<const char*>(p.vcur) + (b * p.vc_sb + j * p.vc_st + h * p.vc_sh) * e
+                                  : static_cast<const char*>(p.kcur) + (b * p.kc_sb + j * p.kc_st + h * p.kc_sh) * e;
+        if (part < p.D * e) prefetch_l2(src + part);
     }
 
     // ---- this warp's copies: stage n covers keys j_lo + (8 n + warp) KS ..; its rows as they are in memory, one bulk
