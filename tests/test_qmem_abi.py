@@ -120,6 +120,8 @@ def test_attention_refusals(native):
     assert attn(native, L=0) == E.TXL_OK
     big = qmem(native, M=2 ** 31 - 1, valid=5)
     assert attn(native, m=big) == E.TXL_ERR_UNSUPPORTED                    # M + L past 32 bits
+    assert attn(native, m=qmem(native, M=2 ** 31 - 4097, valid=5)) == E.TXL_ERR_UNSUPPORTED
+    assert attn(native, m=qmem(native, M=2 ** 31 - 4098, valid=5)) == E.TXL_ERR_WORKSPACE   # the first that is taken
 
 
 def test_calls_need_their_workspace(native):

@@ -1075,7 +1075,7 @@ txl_status check_qattn(int B, int L, int H, int D, const txl_view* q, const txl_
     st = check_qmem(mem);
     if (st != TXL_OK) return st;
     if (mem->M > 0 && (mem->B != B || mem->H != H || mem->D != D)) return TXL_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(mem->M) + L > INT32_MAX) return TXL_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(mem->M) + L > INT32_MAX - 4096) return TXL_ERR_UNSUPPORTED;   // 32-bit positions
     return TXL_OK;
 }
 

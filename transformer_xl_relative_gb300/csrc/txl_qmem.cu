@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
 }
 
 // Rows that do not start on 16-byte boundaries: a warp per row, a lane per channel, so that the stores of a
-// warp are contiguous (by eights, each lane's stores lay 16 bytes apart: 16.5 instead of READ_ROWS_US us on the
+// warp are contiguous (by eights, each lane's stores lay 16 bytes apart: 16.5 instead of 12 us on the
 // base shape).
 constexpr int kReadRows = 4;                           // rows of a warp, loaded together
 

@@ -96,6 +96,16 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit elements across a warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
@@ -126,7 +136,7 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w)
 template <int BITS>
 __device__ __forceinline__ uint32_t pair_even(uint32_t w) { return w & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu); }
 template <int BITS>
-__device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : (w >> 8) & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : __byte_perm(w, 0, 0x4341); }
 
 // E[b][h][i][x] = (q_i+v).r[min(M+i-j, C)] in log2 units for keys j = jn + x, and far[b][h][i] = (q_i+v).r[C].
 // Bound by reading r once: a CTA prepares q+v of up to pos_pairs (entry, query) pairs of a head as two bf16 parts
@@ -148,10 +158,10 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
     // memory and the queries before its own wait.
     pdl_wait();
     pdl_launch_dependents();
-    auto load = [&](int d0, uint4 (&a)[2][NG]) {
+    auto load = [&](unsigned d0, uint4 (&a)[2][NG]) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            int rr = min(d0 + g + 8 * y, p.C);
+            int rr = static_cast<int>(min(d0 + g + 8 * y, static_cast<unsigned>(p.C)));
             if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;  // past the distances of the call
             const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
 #pragma unroll
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
         }
     };
     uint4 a[2][NG];
-    int d0 = blockIdx.x * 128 + warp * 16;                            // first distance of the warp's tile
+    unsigned d0 = blockIdx.x * 128 + warp * 16;                       // first distance of the warp's tile
     load(d0, a);
     const int n_ct = (pairs + 3) >> 2;
     float vb[NG];
@@ -197,9 +207,9 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
         far_at[tid] = p.far + row;
     }
     __syncthreads();
-    for (; d0 < p.n_dist; d0 += gridDim.x * 128) {
+    for (; d0 < static_cast<unsigned>(p.n_dist); d0 += gridDim.x * 128) {
         uint4 next[2][NG];
-        load(d0 + static_cast<int>(gridDim.x) * 128, next);
+        load(d0 + gridDim.x * 128, next);
         for (int ct = 0; ct < n_ct; ++ct) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -214,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
                 const int x0 = x_zero[pr];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int delta = d0 + g + 8 * y;
+                    const int delta = static_cast<int>(d0 + g + 8 * y);
                     const float v = acc[2 * y] + acc[2 * y + 1];
                     if (delta <= x0) e[-delta] = v;
                     if (delta == p.C) *far_at[pr] = v;
@@ -468,10 +478,10 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             // Q.K: acc[t][G] = for slot c4, two keys of its stream's tile, (hi, lo) parts: keys g and g+8; ONE:
             // keys (g + 2 c4) mod 8 and 8 more, so that eight lanes of a load read rows 0 .. 7 of the eight
             float acc[QT][NG][4];
+            if constexpr (QT == 1 && !ONE) {                          // several tiles may add up
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
-#pragma unroll
-                for (int G = 0; G < NG; ++G) acc[t][G][0] = acc[t][G][1] = acc[t][G][2] = acc[t][G][3] = 0.f;
+                for (int G = 0; G < NG; ++G) acc[0][G][0] = acc[0][G][1] = acc[0][G][2] = acc[0][G][3] = 0.f;
+            }
             if constexpr (ONE) {
                 const uint32_t row0 = st_addr + (16 * min(c4, KS / 16 - 1) + one_key) * row_bytes, row1 = row0 + 8 * row_bytes;
 #pragma unroll
@@ -493,8 +503,12 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
                         for (int s = 0; s < SUB; ++s) {
                             const uint32_t x = wa[w] >> (8 * s), y = wb[w] >> (8 * s);
-                            mma_f16(acc[0][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
-                                    pair_odd<BITS>(y), bb[2 * s], bb[2 * s + 1]);
+                            if (c % CPG == 0 && w == 0 && s == 0)
+                                mma_f16_first(acc[0][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
+                                              pair_odd<BITS>(y), bb[2 * s], bb[2 * s + 1]);
+                            else
+                                mma_f16(acc[0][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
+                                        pair_odd<BITS>(y), bb[2 * s], bb[2 * s + 1]);
                         }
                     }
                 }
@@ -514,9 +528,14 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                                 const uint32_t x = w[2 * half] >> (8 * s), y = w[2 * half + 1] >> (8 * s);
                                 const int ks = c * SUB + s;
 #pragma unroll
-                                for (int t = 0; t < QT; ++t)
-                                    mma_f16(acc[t][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
-                                            pair_odd<BITS>(y), on ? bq[t][ks][0] : 0u, on ? bq[t][ks][1] : 0u);
+                                for (int t = 0; t < QT; ++t) {
+                                    if (QT > 1 && c % CPG == 0 && s == 0)
+                                        mma_f16_first(acc[t][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y),
+                                                      pair_odd<BITS>(x), pair_odd<BITS>(y), bq[t][ks][0], bq[t][ks][1]);
+                                    else
+                                        mma_f16(acc[t][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
+                                                pair_odd<BITS>(y), on ? bq[t][ks][0] : 0u, on ? bq[t][ks][1] : 0u);
+                                }
                             }
                         }
                     }
@@ -758,17 +777,23 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     for (int x = tid; x < Lq * DP; x += kThreads) {
         const int row = x / DP, d = x % DP;
         const int own = has_own && d < p.D ? min(i0 + row + 1, kOwn) : 0;
-        float v[kOwn];
+        // the values of all own keys at once: the type is told apart outside the loop, so that the loads overlap
+        uint32_t v[kOwn];
+        const int64_t v_at = b * p.vc_sb + h * p.vc_sh + d;
+        if (p.f32) {
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j)
-            v[j] = j < own ? ld_elem(p.vcur, b * p.vc_sb + j * p.vc_st + h * p.vc_sh + d, p.f32) : 0.f;
+            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? __ldg(static_cast<const uint32_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? __ldg(static_cast<const uint16_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
+        }
         const float* w = weights + row * 32;
         float ot = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) ot = fmaf(part[(k * sp.lq + row) * (DP + 2) + d], w[k], ot);
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            if (j < own) ot = fmaf(w[kWarps + j], v[j], ot);
+            if (j < own) ot = fmaf(w[kWarps + j], __uint_as_float(p.f32 ? v[j] : v[j] << 16), ot);
         st_rank(inbox + (row / sp.ranks * sp.ranks + rank) * (DP + 2) + d, row % sp.ranks, ot);
     }
     __syncthreads();
@@ -850,7 +875,7 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
                              dim3(kThreads), 0, s, p);
     } else {
         // as many CTAs as three per SM, each walking over its share of the distances
-        const int64_t tiles = (p.n_dist + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
+        const int64_t tiles = (static_cast<int64_t>(p.n_dist) + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
         const int64_t per_head = std::max<int64_t>(1, 3 * sm_count / (sets * p.H));
         const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
         e = ng == 2 ? launch_dependent(qpos_kernel<2>, grid, dim3(kThreads), 0, s, p)
