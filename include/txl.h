@@ -495,15 +495,15 @@ txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_o
  *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_qmem_workspace_size(B, L,
  *            H, D, mem, dtype) bytes (TXL_ERR_WORKSPACE otherwise; may be NULL when that is 0).
  *            Calls that share a workspace must not overlap on the GPU.
- * L <= 16 (generation): the position terms (q+v).r go into the workspace, then the codes are expanded
- * on chip in fp32-like precision (q and the weights held to 22 bits); two launches.  L > 16, bf16: K and V of the memory's valid positions and
- * of the segment, and r, are written into the workspace once in fp16, in units of powers of two per
- * (b, h) taken from the data, and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16
- * operands and P, for q, k_cur, v_cur and r of any layout.  (Queries and position terms that would bring
- * scores past fp16's range, 65504, are held at it, and so are rows of r more than 2^15 times as large
- * as the largest of 64 rows spread over the table.)  L > 16, fp32: the memory is
- * read back and txl_rel_attn_fwd's fp32 kernel runs.  err_flag is used for L > 16.  Enqueues one
- * launch, or two.
+ * L <= 16 (generation), two launches: the position terms (q+v).r go into the workspace, then the codes
+ * are expanded on chip in fp32-like precision (q and the weights held to 22 bits).
+ * L > 16, bf16, three launches: K and V of the memory's valid positions and of the segment, and r, are
+ * written into the workspace once in fp16, in units of powers of two per (b, h) taken from the data,
+ * and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16 operands and P, for q,
+ * k_cur, v_cur and r of any layout.  (Queries that would bring scores past fp16's range, 65504, are held
+ * at it.)
+ * L > 16, fp32, two launches: the memory is read back and txl_rel_attn_fwd's fp32 kernel runs.
+ * err_flag as for txl_rel_attn_fwd: every kernel that waits for copies sets it if a wait runs out.
  */
 txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len,
                              const txl_view* q, const txl_qmem* mem,

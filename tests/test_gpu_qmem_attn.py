@@ -118,6 +118,17 @@ DECODE = [
     (2, 1, 41, 5, 300, 300, 5, 1000, "f32", None, 1),
     (1, 2, 128, 16, 200, 200, 5, 1000, "f32", None, 0),
     (4, 1, 64, 1, 40, 40, 5, 1000, "f32", None, 0),
+    (1, 2, 64, 1, 40003, 40000, 12345, 1000, "bf16", None, 0),     # the largest clusters
+    (1, 1, 64, 6, 9000, 9000, 8999, 8000, "bf16", None, 0),
+    (1, 1, 128, 1, 3329, 3329, 17, 1000, "bf16", None, 0),         # the last ranks of a cluster without keys
+    (1, 1, 64, 16, 3400, 3393, 17, 3000, "bf16", None, 0),
+    (9, 2, 64, 16, 70, 70, 11, 1000, "bf16", None, 0),             # more (entry, query) pairs than a block takes
+    (9, 1, 128, 9, 70, 66, 11, 50, "bf16", None, 0),
+    (1, 2, 96, 6, 333, 331, 100, 97, "bf16", None, 0),
+    (2, 2, 64, 1, 301, 301, 100, 98, "bf16", None, 1),             # distances beyond the table, off alignment
+    (2, 2, 64, 2, 302, 299, 100, 99, "bf16", None, 1),
+    (2, 1, 41, 3, 303, 303, 302, 101, "bf16", 47, 1),
+    (1, 2, 72, 4, 5000, 5000, 4321, 100, "f32", 76, 0),
 ]
 IDS = ["B%dH%dD%d_L%dM%dv%dwp%dC%d_%s_hs%s_s%d" % c for c in DECODE]
 
@@ -265,6 +276,17 @@ def test_segment_keys_of_any_magnitude(txl, factor):
     call.r.mul_(factor)
     call.mem.restore((9 - 300) % 300, 0)
     txl.qmem_push(call.mem, call.kh.cuda(), call.vh.cuda())
+    call.run(txl)
+    torch.cuda.synchronize()
+    check_segment(call)
+
+
+@pytest.mark.parametrize("row", [0, 37, 138])
+def test_segment_one_large_position_row(txl, row):
+    """A table whose rows are all small but one."""
+    call = Call(txl, 3, 2, 64, 40, 100, 100, 9, 1000, 4, "bf16")
+    call.r.mul_(2.0 ** -20)
+    call.r[row] *= 2.0 ** 20
     call.run(txl)
     torch.cuda.synchronize()
     check_segment(call)

@@ -348,8 +348,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
 // The operands of the fused attention kernels in fp16, which keeps 11 bits where bf16 keeps 8: K and V
 // of the memory and of the segment, and r.  Each takes its range from a power of two, the unit: the
 // largest |k| of a (b, h) comes into [1, 2) (its unit multiplies c(q+u)), the largest |v| into
-// [2^11, 2^12) (P of the attention goes up to 2^8), and the largest |r| of 64 rows of the head into [1, 2)
-// (rows of up to 2^15 times that size have room).
+// [2^11, 2^12) (P of the attention goes up to 2^8), and the largest |r| of the head into [1, 2).
 //
 // Two passes: qmem_absmax_kernel takes the largest values of up to kXSplits shares of the rows of a (b, h)
 // (a group's end points bound its values, so the parameters suffice for the memory), qmem_expand_kernel
@@ -410,11 +409,12 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
         };
         rows(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, p.vec_k, 0);
         rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
-        const int samples = min(p.n_r, 64);               // the same rows of r for every entry of the head
-        for (int i = x_share(samples, part, parts) + lr; i < x_share(samples, part + 1, parts); i += RPP) {
-            const int64_t row = (static_cast<int64_t>(p.n_r - 1) * i / 63) * p.H + h;
+        // this entry's share of the head's rows of r
+        const int r0 = x_share(p.n_r, b, p.B), n_r = x_share(p.n_r, b + 1, p.B) - r0, s1 = x_share(n_r, part + 1, parts);
+#pragma unroll 2
+        for (int i = x_share(n_r, part, parts) + lr; i < s1; i += RPP) {
             float v[8];
-            load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, v);
+            load8<false>(p.r + (static_cast<int64_t>(r0 + i) * p.H + h) * p.ld_r, d0, p.D, p.vec_r, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) see(2, fabsf(v[e]));
         }
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
 
 // Grid: x over the lanes of the rows (memory, segment, this entry's share of the head's rows of r), y head, z entry.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kQThreads) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
+__global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -457,7 +457,21 @@ __global__ void __launch_bounds__(kQThreads) qmem_expand_kernel(const __grid_con
     float mx[3] = {0.f, 0.f, 0.f}, inv[3];
     for (int y = 0; y < parts; ++y) {
         const float4 a = __ldg(reinterpret_cast<const float4*>(p.absmax) + bh * kXSplits + y);
-        mx[0] = fmaxf(mx[0], a.x); mx[1] = fmaxf(mx[1], a.y); mx[2] = fmaxf(mx[2], a.z);
+        mx[0] = fmaxf(mx[0], a.x); mx[1] = fmaxf(mx[1], a.y);
+    }
+    // the head's rows of r: over the shares of every entry, where it is used
+    __shared__ float red[kQThreads / 32];
+    if (blockIdx.x == 0 || (static_cast<int64_t>(blockIdx.x) + 1) * kBlockRows<G> > static_cast<int64_t>(p.n) + p.L) {
+        for (int e = threadIdx.x; e < p.B * parts; e += kQThreads) {
+            const int64_t at = (static_cast<int64_t>(e / parts) * p.H + h) * kXSplits + e % parts;
+            mx[2] = fmaxf(mx[2], __ldg(p.absmax + at * 4 + 2));
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx[2] = fmaxf(mx[2], __shfl_xor_sync(0xffffffffu, mx[2], off));
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx[2];
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kQThreads / 32; ++w) mx[2] = fmaxf(mx[2], red[w]);
     }
 #pragma unroll
     for (int y = 0; y < 3; ++y) {
