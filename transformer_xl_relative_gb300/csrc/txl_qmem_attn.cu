@@ -817,7 +817,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 }
 
 template <int BITS, int NG, int QT, bool ONE>
-cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream_t s)
+cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
 {
     constexpr int DP = NG * 32;
     constexpr int staged = kWarps * kStages * stage_bytes(BITS, NG, QT, ONE);
@@ -826,8 +826,10 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
     auto* kernel = qattn_kernel<BITS, NG, QT, ONE>;
-    // once per device: the shared memory, and clusters of sixteen
+    // once per device: the shared memory, clusters of more than eight, and how many clusters of each size the device
+    // holds at a time
     static std::atomic<uint64_t> prepared{0};
+    static std::atomic<int> held[64][kMaxRanks + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -835,9 +837,42 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
     if (!(prepared.load(std::memory_order_acquire) & bit)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (int ranks = 1; ranks <= kMaxRanks && e == cudaSuccess; ++ranks) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(ranks * 64);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = bytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = ranks;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            held[dev & 63][ranks].store(n, std::memory_order_relaxed);
+        }
         if (e != cudaSuccess) return e;
         prepared.fetch_or(bit, std::memory_order_release);
     }
+    // Key ranges: the cluster size whose waves of clusters, each over 1/ranks of the keys, take the least time, while
+    // each warp keeps a stage.  A GPC holds a whole number of clusters, so that large ones leave SMs idle: 16 heads of
+    // one sequence fit in one wave as clusters of up to 13 (65536 4-bit keys: 48.4 us), not of 16 (55.6; 8 take 57.7).
+    constexpr int ks = stage_keys(BITS, NG, QT);
+    const int64_t keys = p.M - p.lo, heads = static_cast<int64_t>(p.H) * p.B * groups;
+    int64_t waves = 0;
+    for (int ranks = 1; ranks <= kMaxRanks; ++ranks) {
+        const int n = held[dev & 63][ranks].load(std::memory_order_relaxed);
+        if (ranks > 1 && (n == 0 || keys <= static_cast<int64_t>(ranks) * ks * kWarps)) continue;
+        const int64_t w = n ? (heads + n - 1) / n : heads;
+        if (ranks > 1 && w * sp.ranks >= waves * ranks) continue;
+        sp.ranks = ranks;
+        waves = w;
+    }
+    sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + ks - 1) / ks * ks);
+    if (sp.range == 0) sp.range = ks;
+    const dim3 grid(sp.ranks * groups, p.H, p.B);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
@@ -856,10 +891,10 @@ cudaError_t launch(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream
 }
 
 template <int BITS, int NG>
-cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, dim3 grid, cudaStream_t s)
+cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, int groups, cudaStream_t s)
 {
-    if (sp.lq == 1) return launch<BITS, NG, 1, true>(p, sp, grid, s);
-    return sp.lq <= 4 ? launch<BITS, NG, 1, false>(p, sp, grid, s) : launch<BITS, NG, 2, false>(p, sp, grid, s);
+    if (sp.lq == 1) return launch<BITS, NG, 1, true>(p, sp, groups, s);
+    return sp.lq <= 4 ? launch<BITS, NG, 1, false>(p, sp, groups, s) : launch<BITS, NG, 2, false>(p, sp, groups, s);
 }
 
 }  // namespace
@@ -874,9 +909,10 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
         e = launch_dependent(qpos_f32_kernel, dim3((p.n_dist + kThreads - 1) / kThreads, p.H, std::min<int64_t>(pairs, 256)),
                              dim3(kThreads), 0, s, p);
     } else {
-        // as many CTAs as three per SM, each walking over its share of the distances
+        // four CTAs per SM, each walking over its share of the distances (65536 keys of 16 heads, the whole call:
+        // 62.4 us with two, 58.3 with three, 56.0 with four, 58.7 with six)
         const int64_t tiles = (static_cast<int64_t>(p.n_dist) + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
-        const int64_t per_head = std::max<int64_t>(1, 3 * sm_count / (sets * p.H));
+        const int64_t per_head = std::max<int64_t>(1, 4 * sm_count / (sets * p.H));
         const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
         e = ng == 2 ? launch_dependent(qpos_kernel<2>, grid, dim3(kThreads), 0, s, p)
                     : launch_dependent(qpos_kernel<4>, grid, dim3(kThreads), 0, s, p);
@@ -885,19 +921,8 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
     QSplit sp{};
     const int groups = p.L > 8 ? 2 : 1;                   // queries: eight at most per CTA
     sp.lq = (p.L + groups - 1) / groups;
-    const int ks = stage_keys(bits, ng, sp.lq > 4 ? 2 : 1);
-    // Key ranges: as long as one wave of two CTAs per SM holds them all and each warp keeps two stages; 16
-    // ranks only where eight leave SMs idle.
-    const int64_t keys = p.M - p.lo, blocks = static_cast<int64_t>(p.H) * p.B * groups;
-    sp.ranks = 1;
-    while (sp.ranks < kMaxRanks && blocks * sp.ranks <= (sp.ranks < 8 ? sm_count : sm_count - 1) &&
-           keys > static_cast<int64_t>(sp.ranks) * 2 * ks * kWarps)
-        sp.ranks *= 2;
-    sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + ks - 1) / ks * ks);
-    if (sp.range == 0) sp.range = ks;
-    const dim3 grid(sp.ranks * groups, p.H, p.B);
-    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, grid, s) : launch_qt<4, 4>(p, sp, grid, s);
-    return ng == 2 ? launch_qt<8, 2>(p, sp, grid, s) : launch_qt<8, 4>(p, sp, grid, s);
+    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, groups, s) : launch_qt<4, 4>(p, sp, groups, s);
+    return ng == 2 ? launch_qt<8, 2>(p, sp, groups, s) : launch_qt<8, 4>(p, sp, groups, s);
 }
 
 }  // namespace txl
