@@ -340,34 +340,40 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     // keys of the stage from j with position terms of their own, a multiple of four (a stage starts a
     // multiple of four keys from jn, and the rows of E have room)
     auto near_of = [&](int j) { return max(0, min(KS, (min(KS, j_hi - j) + 3) & ~3) - max(0, p.jn - j)); };
-    auto copy_codes = [&](int n) {                        // one lane
-        const int j = j_lo + (n * kWarps + warp) * KS;
-        const uint32_t st = stage_addr + (n % kStages) * kStageBytes, bar = full_addr + 8 * (n % kStages);
-        const int live = min(KS, j_hi - j);
-        int slot = slot_of(j);
-        if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
-        mbar_expect_tx_addr(bar, live * row_bytes + near_of(j) * 4 * Lq);
-        const int first = min(live, p.M - slot);
-        bulk_load_addr(st, head + static_cast<uint64_t>(slot) * row_bytes, first * row_bytes, bar);
-        if (first < live) bulk_load_addr(st + first * row_bytes, head, (live - first) * row_bytes, bar);
-    };
-    auto copy_e = [&](int n) {
+    // The whole warp: lane 0 copies rows, lane 1 those past the ring's wrap, lanes 2 .. the queries' position terms.
+    // (One lane for all of them took 800 cycles per stage for one query, 1700 for eight.)
+    const bool e_lane = lane >= 2 && lane < 2 + Lq;
+    const float* e_src = p.E + (bh * p.L + i0 + (e_lane ? lane - 2 : 0)) * p.e_pitch;
+    const uint32_t e_dst = kEOff + 4 * KS * (e_lane ? lane - 2 : 0);
+    auto copy = [&](int n, bool codes, bool terms) {
         const int j = j_lo + (n * kWarps + warp) * KS, near = near_of(j), x0 = max(0, p.jn - j);
-        if (near > 0) {
-            const uint32_t at = stage_addr + (n % kStages) * kStageBytes + kEOff, bar = full_addr + 8 * (n % kStages);
-            const float* src = p.E + (bh * p.L + i0) * p.e_pitch + (j + x0 - p.jn);
-            for (int i = 0; i < Lq; ++i)
-                bulk_load_addr(at + 4 * (i * KS + x0), src + i * p.e_pitch, near * 4, bar);
+        const uint32_t st = stage_addr + (n % kStages) * kStageBytes, bar = full_addr + 8 * (n % kStages);
+        const void* src = e_src + (j + x0 - p.jn);
+        uint32_t dst = st + e_dst + 4 * x0, bytes = terms && e_lane ? near * 4 : 0;
+        if (codes) {
+            const int live = min(KS, j_hi - j);
+            int slot = slot_of(j);
+            if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
+            if (lane == 0) mbar_expect_tx_addr(bar, live * row_bytes + near * 4 * Lq);
+            const int first = min(live, p.M - slot);
+            if (lane < 2) {
+                src = head + (lane ? 0 : static_cast<uint64_t>(slot) * row_bytes);
+                dst = st + (lane ? first * row_bytes : 0);
+                bytes = (lane ? live - first : first) * row_bytes;
+            }
+            __syncwarp();                                 // the barrier expects what follows
         }
+        if (bytes > 0) bulk_load_addr(dst, src, bytes, bar);
     };
     if (lane == 0) {
 #pragma unroll
         for (int n = 0; n < kStages; ++n) mbar_init(&full[n], 1);
         fence_mbar_init();
-#pragma unroll
-        for (int n = 0; n < kStages; ++n)
-            if (n < n_stage) copy_codes(n);
     }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < kStages; ++n)
+        if (n < n_stage) copy(n, true, false);
 
     // ---- queries: warp w prepares row w: (q+u) times scale log2 e in fp32, and scaled by a power of two so that
     // its largest entry lies in [2^11, 2^12) as two fp16 parts, in the order in which the B operands take them
@@ -447,11 +453,9 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
         far_of[t] = p.jn > j_lo ? __ldg(p.far + bh * p.L + i0 + is) : 0.f;
     }
-    if (lane == 0) {
 #pragma unroll
-        for (int n = 0; n < kStages; ++n)
-            if (n < n_stage) copy_e(n);
-    }
+    for (int n = 0; n < kStages; ++n)
+        if (n < n_stage) copy(n, false, true);
 
     // ---- running state of slot c4: maximum, weight unit rf (O is in units of rf), sums
     float o[QT][NG * 2][4], z[QT][NG], m[QT], l[QT], rf[QT];
@@ -670,32 +674,40 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             }
         }
         __syncwarp();                                     // every lane has read the stage
-        if (lane == 0 && n + kStages < n_stage) {
-            copy_codes(n + kStages);
-            copy_e(n + kStages);
-        }
+        if (n + kStages < n_stage) copy(n + kStages, true, true);
     }
-    // ---- scores of the segment's own keys: eight lanes per (query, key), eight channels at a time.  (After the
-    // key loop: before it the loads waited behind the copies, 10000 cycles, with the queries of all warps.)
+    // ---- scores of the segment's own keys: eight lanes per key hold its row, and the groups of lanes share the
+    // queries.  (After the key loop: before it the loads waited behind the copies, 10000 cycles, with the
+    // queries of all warps.)
     if (has_own) {
-        for (int x0 = warp * 4; x0 < Lq * n_own; x0 += kWarps * 4) {
-            const int x = min(x0 + (lane >> 3), Lq * n_own - 1);
-            const int row = x / n_own, j = x % n_own, i = i0 + row;
-            const int64_t at = b * p.kc_sb + j * p.kc_st + h * p.kc_sh;
+        const int kp_log = ONE ? 0 : 32 - __clz(n_own - 1);          // groups 2^kp_log apart have the same key
+        const int group = tid >> 3, j = group & ((1 << kp_log) - 1), row0 = group >> kp_log, row_step = 32 >> kp_log;
+        float k[DP / 64][8], e[ONE ? 1 : 4];                         // eight queries at most, and 16 keys
+        const int64_t at = b * p.kc_sb + min(j, n_own - 1) * p.kc_st + h * p.kc_sh;
+#pragma unroll
+        for (int x = 0; x < DP / 64; ++x) {
+            const int d = 64 * x + 8 * (lane & 7);
+            if (p.f32) load8<true>(static_cast<const float*>(p.kcur) + at, d, p.D, p.vec_k, k[x]);
+            else load8<false>(static_cast<const uint16_t*>(p.kcur) + at, d, p.D, p.vec_k, k[x]);
+        }
+#pragma unroll
+        for (int y = 0; y < (ONE ? 1 : 4); ++y) {
+            const int row = row0 + y * row_step;
+            e[y] = row < Lq && j <= i0 + row ? __ldg(e_row0 + row * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
+        }
+#pragma unroll
+        for (int y = 0; y < (ONE ? 1 : 4); ++y) {
+            if (y * row_step >= Lq) break;
+            const int row = row0 + y * row_step;
+            const float* qr = qu + min(row, Lq - 1) * DP + 8 * (lane & 7);
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < DP / 64; ++e) {
-                const int d = 64 * e + 8 * (lane & 7);
-                float k[8];
-                if (p.f32) load8<true>(static_cast<const float*>(p.kcur) + at, d, p.D, p.vec_k, k);
-                else load8<false>(static_cast<const uint16_t*>(p.kcur) + at, d, p.D, p.vec_k, k);
+            for (int x = 0; x < DP / 64; ++x)
 #pragma unroll
-                for (int y = 0; y < 8; ++y) s = fmaf(qu[row * DP + d + y], k[y], s);
-            }
+                for (int z8 = 0; z8 < 8; ++z8) s = fmaf(qr[64 * x + z8], k[x][z8], s);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            if ((lane & 7) == 0)
-                own_s[row * kOwn + j] = j <= i ? s + __ldg(e_row0 + row * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
+            if ((lane & 7) == 0 && row < Lq && j < n_own) own_s[row * kOwn + j] = s + e[y];
         }
     }
     if (n < n_stage && lane == 0)                         // abandoned: no copy may land after the CTA has gone
