@@ -364,12 +364,12 @@ __device__ __forceinline__ int x_share(int n, int part, int parts)
 }
 
 template <int BITS, int G>
-__global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p)
+__global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p, int parts)
 {
     __shared__ float red[3][kQThreads / 32];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(b) * p.H + h;
     constexpr int LPR = 4 * G;                            // lanes of a row, eight channels each
     constexpr int RPP = kQThreads / LPR;                  // rows of a pass
@@ -380,39 +380,43 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
     auto see = [&](int which, float a) {
         if (a < INFINITY) mx[which] = fmaxf(mx[which], a);
     };
-    const int64_t x1 = static_cast<int64_t>(x_share(p.n, part + 1, parts)) * G;
+    if (part < parts) {
+        const int64_t x1 = static_cast<int64_t>(x_share(p.n, part + 1, parts)) * G;
 #pragma unroll 4
-    for (int64_t x = static_cast<int64_t>(x_share(p.n, part, parts)) * G + tid; x < x1; x += kQThreads) {
-        const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
-        int64_t s = static_cast<int64_t>(p.slot0) + t;
-        if (s >= p.M) s -= p.M;
-        if (!in_range(s, 0, p.M, p.chk)) s = 0;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
-                                                              q_par_offset(G, BITS)) + g);
-        const uint32_t kv[2] = {w.x, w.y};
+        for (int64_t x = static_cast<int64_t>(x_share(p.n, part, parts)) * G + tid; x < x1; x += kQThreads) {
+            const int t = static_cast<int>(x / G), g = static_cast<int>(x - static_cast<int64_t>(t) * G);
+            int64_t s = static_cast<int64_t>(p.slot0) + t;
+            if (s >= p.M) s -= p.M;
+            if (!in_range(s, 0, p.M, p.chk)) s = 0;
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
+                                                                  q_par_offset(G, BITS)) + g);
+            const uint32_t kv[2] = {w.x, w.y};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float step = __uint_as_float(kv[i] << 16), lo = __uint_as_float(kv[i] & 0xffff0000u);
-            see(i, fmaxf(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo))));
-        }
-    }
-    if (lane_on) {
-        auto rows = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int vec, int which) {
-            const int s1 = x_share(p.L, part + 1, parts);
-#pragma unroll 4
-            for (int t = x_share(p.L, part, parts) + lr; t < s1; t += RPP) {
-                float v[8];
-                load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) see(which, fabsf(v[e]));
+            for (int i = 0; i < 2; ++i) {
+                const float step = __uint_as_float(kv[i] << 16), lo = __uint_as_float(kv[i] & 0xffff0000u);
+                see(i, fmaxf(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo))));
             }
-        };
-        rows(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, p.vec_k, 0);
-        rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
+        }
+        if (lane_on) {
+            auto rows = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int vec, int which) {
+                const int s1 = x_share(p.L, part + 1, parts);
+#pragma unroll 4
+                for (int t = x_share(p.L, part, parts) + lr; t < s1; t += RPP) {
+                    float v[8];
+                    load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) see(which, fabsf(v[e]));
+                }
+            };
+            rows(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, p.vec_k, 0);
+            rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
+        }
+    } else if (lane_on) {
         // this entry's share of the head's rows of r
-        const int r0 = x_share(p.n_r, b, p.B), n_r = x_share(p.n_r, b + 1, p.B) - r0, s1 = x_share(n_r, part + 1, parts);
-#pragma unroll 2
-        for (int i = x_share(n_r, part, parts) + lr; i < s1; i += RPP) {
+        const int rp = part - parts, r_parts = gridDim.x - parts;
+        const int r0 = x_share(p.n_r, b, p.B), n_r = x_share(p.n_r, b + 1, p.B) - r0, s1 = x_share(n_r, rp + 1, r_parts);
+#pragma unroll 4
+        for (int i = x_share(n_r, rp, r_parts) + lr; i < s1; i += RPP) {
             float v[8];
             load8<false>(p.r + (static_cast<int64_t>(r0 + i) * p.H + h) * p.ld_r, d0, p.D, p.vec_r, v);
 #pragma unroll
@@ -426,17 +430,17 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
         if ((tid & 31) == 0) red[i][tid >> 5] = mx[i];
     }
     __syncthreads();
-    if (tid < 3) {
+    if (part < parts ? tid < 2 : tid == 2) {
         float m = 0.f;
 #pragma unroll
         for (int w = 0; w < kQThreads / 32; ++w) m = fmaxf(m, red[tid][w]);
-        p.absmax[(bh * kXSplits + part) * 4 + tid] = m;
+        p.absmax[(bh * kXSplits + (part < parts ? part : part - parts)) * 4 + tid] = m;
     }
 }
 
 // Grid: x over the lanes of the rows (memory, segment, this entry's share of the head's rows of r), y head, z entry.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts)
+__global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_constant__ QexpandParams p, int parts, int r_parts)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -462,8 +466,8 @@ __global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_
     // the head's rows of r: over the shares of every entry, where it is used
     __shared__ float red[kQThreads / 32];
     if (blockIdx.x == 0 || (static_cast<int64_t>(blockIdx.x) + 1) * kBlockRows<G> > static_cast<int64_t>(p.n) + p.L) {
-        for (int e = threadIdx.x; e < p.B * parts; e += kQThreads) {
-            const int64_t at = (static_cast<int64_t>(e / parts) * p.H + h) * kXSplits + e % parts;
+        for (int e = threadIdx.x; e < p.B * r_parts; e += kQThreads) {
+            const int64_t at = (static_cast<int64_t>(e / r_parts) * p.H + h) * kXSplits + e % r_parts;
             mx[2] = fmaxf(mx[2], __ldg(p.absmax + at * 4 + 2));
         }
 #pragma unroll
@@ -523,13 +527,14 @@ template <int BITS, int G>
 cudaError_t launch_expand(const QexpandParams& p, cudaStream_t s)
 {
     // shares of about 128 rows
-    const int parts = std::min<int64_t>(kXSplits, std::max<int64_t>(1, (std::max<int64_t>(p.n / G, p.L) + 127) / 128));
-    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts, p.H, p.B), dim3(kQThreads), 0, s, p);
+    auto shares = [](int64_t rows) { return static_cast<int>(std::min<int64_t>(kXSplits, std::max<int64_t>(1, (rows + 127) / 128))); };
+    const int parts = shares(std::max<int64_t>(p.n / G, p.L)), r_parts = shares(p.n_r / p.B);
+    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts + r_parts, p.H, p.B), dim3(kQThreads), 0, s, p, parts);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.n) + p.L + (p.n_r + p.B - 1) / p.B;
     if (rows > INT32_MAX - kQThreads) return cudaErrorInvalidValue;
     return launch_dependent(qmem_expand_kernel<BITS, G>, dim3((rows - 1) / kBlockRows<G> + 1, p.H, p.B), dim3(kQThreads), 0,
-                            s, p, parts);
+                            s, p, parts, r_parts);
 }
 
 template <int BITS, int G>
