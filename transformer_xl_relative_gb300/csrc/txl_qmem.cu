@@ -75,15 +75,29 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// Of both halves, NaN if either is
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // One lane's part (eight channels; ALL: every group is whole, else `live` of them inside D) of quantising
 // a group shared by four consecutive lanes.  Returns the codes and the group's step and lo.
 //
-// Eight instructions per channel: minimum and maximum; d = x - lo; y = d / step + 1.5 2^23, whose low bits
-// are the rounded quotient c; the remainder e = d - c step, which is exact; and a shift-add into the code
-// word, the constant bits of the y subtracted once.  Where |e| comes to half a step (bf16 inputs: one
-// channel in 300 at 4 bits, exact ties) the channels of the lane are decided again, with what the
-// subtraction x - lo lost.
-template <int BITS, bool ALL>
+// Eight instructions per channel: minimum and maximum (of bf16 inputs in pairs); d = x - lo; y = d / step
+// + 1.5 2^23, whose low bits are the rounded quotient c; the remainder e = d - c step, which is exact; and
+// a shift-add into the code word, the constant bits of the y subtracted once.  Where |e| comes to half a step (bf16 inputs: one
+// channel in 300 at 4 bits, exact ties) the channel is decided again, with what the subtraction x - lo lost.
+template <int BITS, bool ALL, bool F32>
 __device__ __forceinline__ void quantise8(const float* xin, int live, uint32_t* code, float& step, float& lo)
 {
     constexpr float n = static_cast<float>((1 << BITS) - 1);
@@ -92,19 +106,34 @@ __device__ __forceinline__ void quantise8(const float* xin, int live, uint32_t* 
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = xin[e];
-    float mn = ALL || live > 0 ? x[0] : INFINITY, mx = ALL || live > 0 ? x[0] : -INFINITY;
+    float mx;
+    if constexpr (ALL && !F32) {
+        uint32_t w[4];
 #pragma unroll
-    for (int e = 1; e < 8; ++e)
-        if (ALL || e < live) {
-            mn = min_nan(mn, x[e]);
-            mx = max_nan(mx, x[e]);
+        for (int e = 0; e < 4; ++e) w[e] = __byte_perm(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]), 0x7632);
+        const uint32_t a = max2_nan(max2_nan(w[0], w[1]), max2_nan(w[2], w[3]));
+        const uint32_t c = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3])) ^ 0x80008000u;
+        uint32_t both = max2_nan(__byte_perm(a, c, 0x5410), __byte_perm(a, c, 0x7632));     // (max, -min)
+#pragma unroll
+        for (int off = 1; off <= 2; off <<= 1) both = max2_nan(both, __shfl_xor_sync(0xffffffffu, both, off));
+        mx = __uint_as_float(both << 16);
+        lo = -__uint_as_float(both & 0xffff0000u);
+    } else {
+        float mn = ALL || live > 0 ? x[0] : INFINITY;
+        mx = ALL || live > 0 ? x[0] : -INFINITY;
+#pragma unroll
+        for (int e = 1; e < 8; ++e)
+            if (ALL || e < live) {
+                mn = min_nan(mn, x[e]);
+                mx = max_nan(mx, x[e]);
+            }
+#pragma unroll
+        for (int off = 1; off <= 2; off <<= 1) {
+            mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         }
-#pragma unroll
-    for (int off = 1; off <= 2; off <<= 1) {
-        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        lo = bf16_floor(mn);
     }
-    lo = bf16_floor(mn);
     // max - lo = span + err exactly
     const float span = mx - lo;
     const float bb = span - mx;
@@ -132,28 +161,38 @@ __device__ __forceinline__ void quantise8(const float* xin, int live, uint32_t* 
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= kTwo64;
     }
-    const float inv = 1.f / st;
-    const float half = 0.5f * st, nearly = half * (1.f - 1.f / 16384.f);   // what x - lo lost is below 2^-15 half
+    // inv is off by 2^-23 and d by 2^-24 of themselves, so that d inv (at most 256) is off by less than 2^-14:
+    // a code that this rounds to the wrong side lies within that of half a step
+    const float inv = rcp_approx(st);
+    const float half = 0.5f * st, nearly = half * (1.f - 1.f / 4096.f);
     float y[8];
-    bool close = false;
+    uint32_t close = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float d = x[e] - l;
         y[e] = fmaf(d, inv, kMagic);
-        close |= fabsf(fmaf(kMagic - y[e], st, d)) >= nearly;
+        if (fabsf(fmaf(kMagic - y[e], st, d)) >= nearly) close |= 1u << e;
     }
-    if (close) {
+    while (close) {                                        // one channel at a time: few lanes have any
+        const uint32_t bit = close & (0u - close);
+        close ^= bit;
+        float xe = x[0], ye = y[0];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = x[e] - l, b2 = d - x[e];
-            const float lost = (x[e] - (d - b2)) + (-l - b2);              // x - lo = d + lost exactly
-            const float rem = fmaf(kMagic - y[e], st, d);
-            const float over = fabsf(rem) - half;                          // exact: both are near half a step
-            const float more = rem > 0.f ? lost : -lost;
-            const bool past = over > 0.f || (over == 0.f && more > 0.f);   // |over| > |lost| unless over = 0
-            const bool tie = over == 0.f && more == 0.f && (__float_as_uint(y[e]) & 1u);
-            if (past || tie) y[e] += rem > 0.f ? 1.f : -1.f;
+        for (int e = 1; e < 8; ++e) {
+            xe = bit >> e & 1u ? x[e] : xe;
+            ye = bit >> e & 1u ? y[e] : ye;
         }
+        const float d = xe - l, b2 = d - xe;
+        const float lost = (xe - (d - b2)) + (-l - b2);                    // x - lo = d + lost exactly
+        const float rem = fmaf(kMagic - ye, st, d);
+        const float over = fabsf(rem) - half;                              // exact: both are near half a step
+        const float more = rem > 0.f ? lost : -lost;
+        const bool past = over > 0.f || (over == 0.f && more > 0.f);       // |over| > |lost| unless over = 0
+        const bool tie = over == 0.f && more == 0.f && (__float_as_uint(ye) & 1u);
+        const float move = past || tie ? copysignf(1.f, rem) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (bit >> e & 1u) y[e] += move;
     }
     if constexpr (!ALL) {
 #pragma unroll
@@ -234,8 +273,8 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
     for (int w = 0; w < 2; ++w) {
         const float* x = w ? xv : xk;
         uint32_t c[2];
-        if (p.D == 32 * G) quantise8<BITS, true>(x, 8, c, step[w], lo[w]);
-        else quantise8<BITS, false>(x, live, c, step[w], lo[w]);
+        if (p.D == 32 * G) quantise8<BITS, true, F32>(x, 8, c, step[w], lo[w]);
+        else quantise8<BITS, false, F32>(x, live, c, step[w], lo[w]);
         if (on) {
             uint8_t* dst = o.row + w * q_v_offset(G, BITS) + o.d0 * BITS / 8;
             if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = c[0];
