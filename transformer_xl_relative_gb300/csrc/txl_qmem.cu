@@ -12,6 +12,11 @@
 //
 // Four lanes share a group, eight channels each: 16-byte accesses to bf16 rows, and consecutive threads walk the
 // groups of a row, then the positions of one head, whose rows are contiguous.
+//
+// What bounds them: push, instructions (98304 rows of 64 bf16 channels to 4 bits: 18.0 us for 33 MB, 500
+// instructions per warp at 73% of the issue slots; 4.9 us of HBM); read, HBM and the ramp (131072 rows of 128
+// channels from 4 bits: 13.9 us for 88 MB, 6.3 TB/s).  Two units of work per thread in either cost more
+// than the addresses they share (push 24 instead of 19.6 us).
 #include <algorithm>
 
 #include <cuda_bf16.h>
