@@ -483,7 +483,7 @@ txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v
 /*
  * txl_qmem_read -- what the memory stands for: logical positions j0 .. j0+n-1 (oldest first; all of
  * them valid: M - valid <= j0, j0 + n <= M, TXL_ERR_INVALID_ARG otherwise) into views k_out, v_out
- * of [B][n][H][D], dtype, each value rounded once to it.  Only d < D is written.
+ * of [B][n][H][D], dtype: one fp32 multiply-add, rounded to dtype.  Only d < D is written.
  */
 txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_out,
                          const txl_view* v_out, txl_dtype dtype, void* stream);

@@ -2,6 +2,10 @@
 arithmetic over what the memory stands for, and the run of push and attention that generates."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -154,7 +158,7 @@ def test_a_given_scale(txl):
     check(call, scale=0.31)
 
 
-@pytest.mark.parametrize("factor", [1e-30, 1e-6, 1e4, 1e25])
+@pytest.mark.parametrize("factor", [1e-30, 1e-6, 1e4, 1e25, 1e33])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_values_of_any_magnitude(txl, bits, factor):
     """The output scales with the values, whatever their size (the softmax does not see them)."""
@@ -370,6 +374,68 @@ def test_replayed_from_a_graph(txl, L):
         if not turned:
             assert torch.equal(call.out, first)
         check(call) if L <= 16 else check_segment(call)
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, %r)
+import transformer_xl_relative_gb300 as txl
+B, H, D, M, L, C = 1, 2, 64, 200, int(sys.argv[1]), 1000
+k, q = (torch.randn(B, max(M, L), H, D, device="cuda").bfloat16() for _ in range(2))
+u = torch.zeros(H, D, device="cuda")
+r = torch.randn(M + L, H, D, device="cuda").bfloat16()
+mem = txl.QuantMemory.empty(B, M, H, D)
+outs = [torch.empty(B, L, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+ws = torch.empty(txl.rel_attn_qmem_workspace_size(q[:, :L], mem) + 1048576, dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+def step(out):
+    mem.restore(0, 0)
+    txl.qmem_push(mem, k[:, :M], q[:, :M])
+    txl.rel_attn_qmem(q[:, :L], mem, k[:, :L], k[:, :L], u, u, r, M + L, C, out, workspace=ws)
+with torch.cuda.graph(g):
+    step(outs[0])
+mem.rows.zero_()
+g.replay()
+torch.cuda.synchronize()
+step(outs[1])
+torch.cuda.synchronize()
+assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
+print("same")
+"""
+
+
+@pytest.mark.parametrize("L", [1, 40])
+def test_the_first_call_of_a_process_may_be_captured(txl, L):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL % root, str(L)], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "same" in p.stdout, p.stderr[-2000:]
+
+
+def test_workspaces_and_flags_elsewhere_are_refused(txl):
+    call = Call(txl, 1, 2, 64, 1, 100, 100, 0, 1000, 4, "bf16")
+    need = txl.rel_attn_qmem_workspace_size(call.q, call.mem)
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(need)):
+        with pytest.raises(ValueError):
+            call.run(txl, workspace=bad)
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64, device="cuda"),
+                torch.zeros(0, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            call.run(txl, err_flag=bad)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call.run(txl, err_flag=flag)
+    torch.cuda.synchronize()
+    assert flag.item() == 0
+    check(call)
+
+
+def test_the_output_may_replace_the_queries(txl):
+    for L in (1, 3, 16):
+        call = Call(txl, 2, 2, 64, L, 3000, 3000, 50, 1000, 4, "bf16")
+        ref, size, vmax = call.reference()
+        call.out = call.q
+        call.run(txl)
+        torch.cuda.synchronize()
+        assert (np.abs(f64(call.out) - ref) <= decode_tolerance(ref, size, vmax, call.dtype)).all()
 
 
 def test_a_memory_past_four_gigabytes(txl):

@@ -544,6 +544,10 @@ def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor,
         need = max(rel_attn_qmem_workspace_size(q, mem), 16)
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and live on the queries' device")
+    if err_flag is not None and (err_flag.get_device() != dev or err_flag.dtype != torch.int32 or err_flag.numel() < 1):
+        raise ValueError("err_flag must be an int32 on the queries' device")
     args = native.QMEM_ARGS.pack(
         B, L, H, D, clamp_len, n_rows, _DTYPES[dtype], scale, q.data_ptr(), q0, q1, q2, k_cur.data_ptr(), k0, k1, k2,
         v_cur.data_ptr(), v0, v1, v2, out.data_ptr(), o0, o1, o2, mem.address if mem is not None else 0, u.data_ptr(),

@@ -699,7 +699,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
         for (int y = 0; y < (ONE ? 1 : 4); ++y) {
             const int row = row0 + y * row_step;
-            e[y] = row < Lq && j <= i0 + row ? __ldg(e_row0 + row * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
+            e[y] = row < Lq && j <= i0 + row ? __ldg(e_row0 + static_cast<int64_t>(row) * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
         }
 #pragma unroll
         for (int y = 0; y < (ONE ? 1 : 4); ++y) {
@@ -737,11 +737,11 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) zt[G] += __shfl_xor_sync(0xffffffffu, zt[G], off);
         }
-        const float un = rf[t] * kTwo24;
 #pragma unroll
         for (int x = 0; x < NG * 2; ++x) {
-            ot[2 * x] = fmaf(o[t][x][0] + o[t][x][1], un, zt[x >> 1]);
-            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (BITS == 4 ? 0.0625f : 1.f), un, zt[x >> 1]);
+            // (the unit last: times 2^24 it could leave fp32)
+            ot[2 * x] = fmaf((o[t][x][0] + o[t][x][1]) * kTwo24, rf[t], zt[x >> 1]);
+            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (BITS == 4 ? kTwo24 / 16 : kTwo24), rf[t], zt[x >> 1]);
         }
         float mt = m[t];
         for (int off = Lp; off <= 2; off <<= 1) {
