@@ -278,6 +278,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     constexpr int kEOff = KS * q_row_bytes(NG, BITS);     // of a stage: rows, position terms
     constexpr int kStageBytes = stage_bytes(BITS, NG, QT, ONE);
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per register of codes and product
+    constexpr int QP = DP + 8;                            // rows of q's parts: the three that a load of ONE reads
+                                                          // (both parts, zeros) lie in different banks
     constexpr int kOwn = ONE ? 1 : kDecodeMaxL;           // keys of the segment a query can see
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* stages = smem;
@@ -287,8 +289,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     float* qsum = norm + kMaxRows;                        // [row][NG]: group sums of qu
     float* own_s = qsum + kMaxRows * NG;                  // [row][kOwn]: scores of the segment's own keys
     float* weights = own_s + kMaxRows * kDecodeMaxL;      // [row][32]: of the parts that make the result
-    uint16_t* quh = reinterpret_cast<uint16_t*>(weights + kMaxRows * 32);   // [2 row + part][DP], a row of zeros
-    uint64_t* bars = reinterpret_cast<uint64_t*>(quh + (2 * kMaxRows + 1) * DP);   // [warp][stage]: copies landed
+    uint16_t* quh = reinterpret_cast<uint16_t*>(weights + kMaxRows * 32);   // [2 row + part][QP]; rows past Lq are zeros
+    uint64_t* bars = reinterpret_cast<uint64_t*>(quh + 2 * kMaxRows * QP);   // [warp][stage]: copies landed
     int* abort_flag = reinterpret_cast<int*>(bars + kWarps * kStages);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
@@ -406,9 +408,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             const int at = BITS == 4 ? (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1) : (d & ~3) + ((d & 1) << 1) + ((d >> 1) & 1);
             uint32_t w, unused;
             split_f16(a[e] * (BITS == 4 && (d & 1) ? up * 0.0625f : up), 0.f, w, unused);
-            quh[2 * row * DP + at] = static_cast<uint16_t>(w);
-            quh[(2 * row + 1) * DP + at] = static_cast<uint16_t>(w >> 16);
-            if (row == 0) quh[2 * kMaxRows * DP + d] = 0;
+            quh[2 * row * QP + at] = static_cast<uint16_t>(w);
+            quh[(2 * row + 1) * QP + at] = static_cast<uint16_t>(w >> 16);
             float sum = a[e];
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -423,12 +424,12 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     float qs[QT][NG], sc[QT], far_of[QT];
     const int my_stream = (g >> 1) >> lp_log;             // of the column this lane holds in B operands
     const int one_key = (g + 2 * c4) & 7;
-    const uint16_t* one_row = quh + ((g >> 1) == c4 ? (g & 1) : 2 * kMaxRows) * DP;
+    const uint16_t* one_row = quh + ((g >> 1) == c4 ? (g & 1) : 2) * QP;       // or zeros
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         if constexpr (!ONE) {
             const int il = min(((g >> 1) & (Lp - 1)) + 4 * t, Lq - 1);
-            const uint16_t* row = quh + (2 * il + (g & 1)) * DP;
+            const uint16_t* row = quh + (2 * il + (g & 1)) * QP;
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
                 if constexpr (BITS == 4) {
@@ -840,7 +841,7 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
     constexpr int DP = NG * 32;
     constexpr int staged = kWarps * kStages * stage_bytes(BITS, NG, QT, ONE);
     constexpr int bytes = staged + (kMaxRows * (DP + 1 + NG + kDecodeMaxL + 32) + kMaxRanks * (DP + 4)) * 4 +
-                          (2 * kMaxRows + 1) * DP * 2 + kWarps * kStages * 8 + 16;
+                          2 * kMaxRows * (DP + 8) * 2 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
     auto* kernel = qattn_kernel<BITS, NG, QT, ONE>;
