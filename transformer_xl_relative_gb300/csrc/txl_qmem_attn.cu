@@ -73,9 +73,11 @@ constexpr float kMaxUnit = 8.50705917e37f;     // (at most 2^8) over the unit st
 __host__ __device__ constexpr int stage_keys(int bits, int ng, int qt) { return bits * ng <= 8 && qt == 1 ? 64 : 32; }
 // Queries whose position terms a stage has room for.
 __host__ __device__ constexpr int stage_rows(int qt, bool one) { return one ? 1 : 4 * qt; }
+// Floats from one query's position terms to the next: four queries' eight keys lie in different banks.
+__host__ __device__ constexpr int e_stride(int bits, int ng, int qt, bool one) { return stage_keys(bits, ng, qt) + (one ? 0 : 8); }
 __host__ __device__ constexpr int stage_bytes(int bits, int ng, int qt, bool one)
 {
-    return stage_keys(bits, ng, qt) * (q_row_bytes(ng, bits) + 4 * stage_rows(qt, one));
+    return stage_keys(bits, ng, qt) * q_row_bytes(ng, bits) + 4 * stage_rows(qt, one) * e_stride(bits, ng, qt, one);
 }
 
 struct QSplit {               // how the host divides the work
@@ -147,14 +149,17 @@ __device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w 
 // E[b][h][i][x] = (q_i+v).r[min(M+i-j, C)] in log2 units for keys j = jn + x, and far[b][h][i] = (q_i+v).r[C].
 // Bound by reading r once: a CTA prepares q+v of up to pos_pairs (entry, query) pairs of a head as two bf16 parts
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
-// from global memory as fragments) are requested one tile ahead.
+// from global memory as fragments) are requested one tile ahead.  WALK: more tiles than three CTAs per SM; four CTAs per SM
+// (64 registers) then keep more rows in flight (65537 distances of 16 heads: the whole call 44.8 us, 62.4 with three);
+// with fewer the free choice of registers (66) is quicker (token over 4096 keys 15.4 us, 16.0 with 64).
 __host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
-template <int NG>
-__global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ QattnParams p)
+template <int NG, bool WALK>
+__global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kernel(const __grid_constant__ QattnParams p)
 {
     constexpr int DP = NG * 32, PAIRS = pos_pairs(NG);
-    __shared__ __align__(16) uint16_t qvh[2 * PAIRS * DP];            // [2 pair + part][DP]
+    // [2 pair + part][DP], the groups of part 1 swapped in pairs: a load takes both parts, from different banks
+    __shared__ __align__(16) uint16_t qvh[2 * PAIRS * DP];
     __shared__ float* e_key[PAIRS];                                   // E of the pair at x = M + i - jn (distance 0)
     __shared__ float* far_at[PAIRS];
     __shared__ int x_zero[PAIRS];                                     // that x
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
             const float c = pr < pairs && d < p.D ? (ld_elem(p.q, at + d, 0) + vb[e]) * p.qscale : 0.f;
             const __nv_bfloat16 hi = __float2bfloat16_rn(c);
             qvh[2 * pr * DP + d] = __bfloat16_as_ushort(hi);
-            qvh[(2 * pr + 1) * DP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
+            qvh[(2 * pr + 1) * DP + (d ^ 32)] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
         }
     }
     if (tid < pairs) {
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) qpos_kernel(const __grid_constant__ 
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
-                const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * G + 8 * c4);
+                const uint4 bw = *reinterpret_cast<const uint4*>(qvh + (8 * ct + g) * DP + 32 * (G ^ (g & 1)) + 8 * c4);
                 mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
                 mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
             }
@@ -276,6 +281,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     constexpr int CPG = BITS / 4;                         // chunks of a group
     constexpr int KS = stage_keys(BITS, NG, QT);
     constexpr int kEOff = KS * q_row_bytes(NG, BITS);     // of a stage: rows, position terms
+    constexpr int kEStride = e_stride(BITS, NG, QT, ONE);
     constexpr int kStageBytes = stage_bytes(BITS, NG, QT, ONE);
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per register of codes and product
     constexpr int QP = DP + 8;                            // rows of q's parts: the three that a load of ONE reads
@@ -352,7 +358,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     // (One lane for all of them took 800 cycles per stage for one query, 1700 for eight.)
     const bool e_lane = lane >= 2 && lane < 2 + Lq;
     const float* e_src = p.E + (bh * p.L + i0 + (e_lane ? lane - 2 : 0)) * p.e_pitch;
-    const uint32_t e_dst = kEOff + 4 * KS * (e_lane ? lane - 2 : 0);
+    const uint32_t e_dst = kEOff + 4 * kEStride * (e_lane ? lane - 2 : 0);
     auto copy = [&](int n, bool codes, bool terms) {
         const int j = j_lo + (n * kWarps + warp) * KS, near = near_of(j), x0 = max(0, p.jn - j);
         const uint32_t st = stage_addr + (n % kStages) * kStageBytes, bar = full_addr + 8 * (n % kStages);
@@ -584,7 +590,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                 float s[2], pr[2], w[2][NG];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float a = (x ? near1 : near0) ? e_st[il * KS + 8 * x] : far_of[t], d = 0.f;
+                    float a = (x ? near1 : near0) ? e_st[il * kEStride + 8 * x] : far_of[t], d = 0.f;
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
                         d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], __uint_as_float(par[x][G].x << 16), d);
@@ -933,8 +939,8 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
         const int64_t tiles = (static_cast<int64_t>(p.n_dist) + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
         const int64_t per_head = std::max<int64_t>(1, 4 * sm_count / (sets * p.H));
         const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
-        e = ng == 2 ? launch_dependent(qpos_kernel<2>, grid, dim3(kThreads), 0, s, p)
-                    : launch_dependent(qpos_kernel<4>, grid, dim3(kThreads), 0, s, p);
+        auto* kernel = ng > 2 ? qpos_kernel<4, true> : tiles * sets * p.H > 3 * sm_count ? qpos_kernel<2, true> : qpos_kernel<2, false>;
+        e = launch_dependent(kernel, grid, dim3(kThreads), 0, s, p);
     }
     if (e != cudaSuccess) return e;
     QSplit sp{};
