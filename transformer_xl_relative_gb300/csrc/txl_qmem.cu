@@ -343,51 +343,55 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_kernel(const __grid_const
     store8<F32>(rv, o.d0, p.D, p.vec_v, xv);
 }
 
-// Rows that do not start on 16-byte boundaries: a warp per row, a lane per channel, so that the stores of a
+// Rows that do not start on 16-byte boundaries: a warp per row, a lane per channel of a group, so that the stores of a
 // warp are contiguous (by eights, each lane's stores lay 16 bytes apart: 16.5 instead of 12 us on the
-// base shape).
-constexpr int kReadRows = 4;                           // rows of a warp, loaded together
+// base shape); the loads of kReadRows rows, all groups, come before their stores.
+template <int G> constexpr int kReadRows = G <= 2 ? 4 : 2;
 
-template <int BITS, bool F32>
+template <int BITS, int G, bool F32>
 __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_constant__ QmemParams p)
 {
+    constexpr int ROWS = kReadRows<G>;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
-    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
-    const int row_bytes = q_row_bytes(p.G, BITS);
-    const int64_t head = (static_cast<int64_t>(b) * p.H + h) * p.M;
-    for (int g = 0; g < p.G; ++g) {
-        const int d = 32 * g + lane, byte = d * BITS / 8;
-        const int sh = BITS == 4 ? 4 * (d & 1) : 0, mask = (1 << BITS) - 1;
-        if (d >= p.D) break;
-        uint2 par[kReadRows];
-        int ck[kReadRows], cv[kReadRows];
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * ROWS;
+    const uint8_t* head = p.rows + (static_cast<int64_t>(b) * p.H + h) * p.M * q_row_bytes(G, BITS);
+    const int byte = lane * BITS / 8, sh = BITS == 4 ? 4 * (lane & 1) : 0, mask = (1 << BITS) - 1;
+    uint2 par[ROWS][G];
+    int ck[ROWS][G], cv[ROWS][G];
 #pragma unroll
-        for (int u = 0; u < kReadRows; ++u) {
-            int64_t slot = p.slot0 + min(t0 + u, static_cast<int64_t>(p.n - 1));
-            if (slot >= p.M) slot -= p.M;
-            if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
-            const uint8_t* row = p.rows + (head + slot) * row_bytes;
-            par[u] = __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(p.G, BITS)) + g);
-            ck[u] = __ldg(row + byte);
-            cv[u] = __ldg(row + q_v_offset(p.G, BITS) + byte);
+    for (int u = 0; u < ROWS; ++u) {
+        int64_t slot = p.slot0 + min(t0 + u, static_cast<int64_t>(p.n - 1));
+        if (slot >= p.M) slot -= p.M;
+        if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
+        const uint8_t* row = head + slot * q_row_bytes(G, BITS);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            par[u][g] = __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + g);
+            ck[u][g] = __ldg(row + 4 * BITS * g + byte);
+            cv[u][g] = __ldg(row + q_v_offset(G, BITS) + 4 * BITS * g + byte);
         }
+    }
 #pragma unroll
-        for (int u = 0; u < kReadRows; ++u) {
-            const int64_t t = t0 + u;
-            if (t >= p.n) break;
-            const float k = fmaf(__uint_as_float(par[u].x << 16), static_cast<float>((ck[u] >> sh) & mask),
-                                 __uint_as_float(par[u].x & 0xffff0000u));
-            const float v = fmaf(__uint_as_float(par[u].y << 16), static_cast<float>((cv[u] >> sh) & mask),
-                                 __uint_as_float(par[u].y & 0xffff0000u));
-            const int64_t ok = b * p.xk_sb + t * p.xk_st + h * p.xk_sh + d, ov = b * p.xv_sb + t * p.xv_st + h * p.xv_sh + d;
+    for (int u = 0; u < ROWS; ++u) {
+        const int64_t t = t0 + u;
+        if (t >= p.n) break;
+        const int64_t ok = b * p.xk_sb + t * p.xk_st + h * p.xk_sh, ov = b * p.xv_sb + t * p.xv_st + h * p.xv_sh;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int d = 32 * g + lane;
+            if (d >= p.D) break;
+            const float k = fmaf(__uint_as_float(par[u][g].x << 16), static_cast<float>((ck[u][g] >> sh) & mask),
+                                 __uint_as_float(par[u][g].x & 0xffff0000u));
+            const float v = fmaf(__uint_as_float(par[u][g].y << 16), static_cast<float>((cv[u][g] >> sh) & mask),
+                                 __uint_as_float(par[u][g].y & 0xffff0000u));
             if constexpr (F32) {
-                static_cast<float*>(p.xk)[ok] = k;
-                static_cast<float*>(p.xv)[ov] = v;
+                static_cast<float*>(p.xk)[ok + d] = k;
+                static_cast<float*>(p.xv)[ov + d] = v;
             } else {
-                static_cast<__nv_bfloat16*>(p.xk)[ok] = __float2bfloat16_rn(k);
-                static_cast<__nv_bfloat16*>(p.xv)[ov] = __float2bfloat16_rn(v);
+                static_cast<__nv_bfloat16*>(p.xk)[ok + d] = __float2bfloat16_rn(k);
+                static_cast<__nv_bfloat16*>(p.xv)[ov + d] = __float2bfloat16_rn(v);
             }
         }
     }
@@ -588,6 +592,11 @@ cudaError_t launch_expand(const QexpandParams& p, cudaStream_t s)
 template <int BITS, int G>
 cudaError_t launch(const QmemParams& p, bool f32, bool push, cudaStream_t s)
 {
+    if (!push && !(p.vec_k && p.vec_v)) {
+        constexpr int rows = kQThreads / 32 * kReadRows<G>;
+        return launch_dependent(f32 ? qmem_read_rows_kernel<BITS, G, true> : qmem_read_rows_kernel<BITS, G, false>,
+                                dim3((p.n - 1) / rows + 1, p.H, p.B), dim3(kQThreads), 0, s, p);
+    }
     const dim3 grid((p.n - 1) / kBlockRows<G> + 1, p.H, p.B);
     auto* kernel = push ? (f32 ? qmem_push_kernel<BITS, G, true> : qmem_push_kernel<BITS, G, false>)
                         : (f32 ? qmem_read_kernel<BITS, G, true> : qmem_read_kernel<BITS, G, false>);
@@ -634,13 +643,6 @@ cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t 
 
 cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s)
 {
-    if (!p.vec_k || !p.vec_v) {
-        constexpr int rows = kQThreads / 32 * kReadRows;
-        const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.n) + rows - 1) / rows), p.H, p.B);
-        auto* kernel = p.bits == 4 ? (dtype == TXL_F32 ? qmem_read_rows_kernel<4, true> : qmem_read_rows_kernel<4, false>)
-                                   : (dtype == TXL_F32 ? qmem_read_rows_kernel<8, true> : qmem_read_rows_kernel<8, false>);
-        return launch_dependent(kernel, grid, dim3(kQThreads), 0, s, p);
-    }
     return launch_any(p, dtype, false, s);
 }
 
