@@ -488,6 +488,18 @@ txl_status txl_qmem_push(txl_qmem* mem, const txl_view* k_new, const txl_view* v
 txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_out,
                          const txl_view* v_out, txl_dtype dtype, void* stream);
 
+/* txl_qmem_push and txl_qmem_read with their arguments in one struct, for bindings that pay per argument: k, v are
+ * k_new, v_new or k_out, v_out; n is L or n; j0 is read by txl_qmem_read_call alone. */
+typedef struct {
+    txl_qmem* mem;
+    txl_view k, v;
+    int j0, n;
+    int dtype;                 /* a txl_dtype */
+    void* stream;
+} txl_qmem_kv_args;
+txl_status txl_qmem_push_call(const txl_qmem_kv_args* args);
+txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
+
 /*
  * txl_rel_attn_qmem -- txl_rel_attn_fwd with the memory's keys and values held in a txl_qmem: the
  * same scores, mask, clamp and softmax over k'_j, v'_j = what the memory stands for, and the current

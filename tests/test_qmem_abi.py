@@ -192,3 +192,25 @@ def test_the_struct_form_reads_its_arguments(native):
     assert call(ws=0) == native.TXL_ERR_WORKSPACE
     assert call(ws=FAKE + 4) == native.TXL_ERR_WORKSPACE
     assert call(ws_bytes=100) == native.TXL_ERR_WORKSPACE
+
+
+def test_the_struct_forms_of_push_and_read(native):
+    """txl_qmem_push_call and txl_qmem_read_call with the packed arguments of the binding: the statuses of
+    the long forms."""
+    x = (FAKE, 1 * 4 * 64, 4 * 64, 64)
+    m = qmem(native, valid=100)
+    lib = native.load()
+
+    def args(mem=None, k=x, v=x, j0=0, n=0, dtype=1):
+        return native.QMEM_KV_ARGS.pack(ctypes.addressof(m) if mem is None else mem, *k, *v, j0, n, dtype, 0)
+
+    for f in (lib.txl_qmem_push_call, lib.txl_qmem_read_call):
+        assert f(None) == native.TXL_ERR_INVALID_ARG
+        assert f(args(mem=0)) == native.TXL_ERR_INVALID_ARG
+        assert f(args(k=(0, *x[1:]))) == native.TXL_ERR_INVALID_ARG
+        assert f(args(v=(0, *x[1:]))) == native.TXL_ERR_INVALID_ARG
+        assert f(args(n=-1, j0=28)) == native.TXL_ERR_INVALID_ARG
+        assert f(args(dtype=9, j0=28)) == native.TXL_ERR_INVALID_ARG
+        assert f(args(j0=28)) == native.TXL_OK                              # nothing to do
+    assert lib.txl_qmem_read_call(args(j0=27)) == native.TXL_ERR_INVALID_ARG     # not valid yet
+    assert lib.txl_qmem_read_call(args(j0=128, n=1)) == native.TXL_ERR_INVALID_ARG

@@ -50,12 +50,12 @@ def _raw_stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _on_device(device: int, call):
-    """Runs call() with CUDA device `device` current (the library launches on the current device)."""
+def _on_device(device: int, call, args):
+    """call(args) with CUDA device `device` current (the library launches on the current device)."""
     if device == torch.cuda.current_device():
-        return call()
+        return call(args)
     with torch.cuda.device(device):
-        return call()
+        return call(args)
 
 
 class Memory:
@@ -415,7 +415,7 @@ class QuantMemory:
         if not rows.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
         B, H, M, _ = rows.shape
-        self.rows, self.device = rows, rows.get_device()
+        self.rows, self.device, self._bhd = rows, rows.get_device(), (B, H, D)
         self._c = TxlQmem(rows.data_ptr() if M else None, B, M, H, D, bits, int(wp), int(valid))
         self.address = ctypes.addressof(self._c)          # of the C struct, for calls that take it as a number
 
@@ -455,37 +455,37 @@ class QuantMemory:
         return self._c
 
 
-def _qmem_kv(mem: QuantMemory, k: torch.Tensor, v: torch.Tensor, T: int):
-    """Views of k and v [B, T, H, D] of the memory's shape and device, and their dtype's code."""
-    c = mem.c_struct
-    shape = (c.B, T, c.H, c.D)
+def _qmem_kv(mem: QuantMemory, k: torch.Tensor, v: torch.Tensor, j0: int, T: int, stream) -> bytes:
+    """The packed txl_qmem_kv_args of k and v [B, T, H, D] of the memory's shape and device."""
+    shape, dev, dtype = (*mem._bhd[:1], T, *mem._bhd[1:]), mem.device, k.dtype
     if k.shape != shape or v.shape != shape:
         raise ValueError("expected [B, T, H, D] = %s, got %s and %s" % (shape, tuple(k.shape), tuple(v.shape)))
-    if k.get_device() != mem.device or v.get_device() != mem.device:
+    if k.get_device() != dev or v.get_device() != dev:
         raise ValueError("tensors must live on the memory's device")
-    if k.dtype != v.dtype:
+    if dtype != v.dtype:
         raise TypeError("k and v must share a dtype")
-    sk, sv = k.stride(), v.stride()
-    if c.D > 1 and (sk[3] != 1 or sv[3] != 1):
+    (k0, k1, k2, k3), (v0, v1, v2, v3) = k.stride(), v.stride()
+    if (k3 != 1 or v3 != 1) and shape[3] > 1:
         raise ValueError("the last (d) dimension must be contiguous")
-    return TxlView(k.data_ptr(), sk[0], sk[1], sk[2]), TxlView(v.data_ptr(), sv[0], sv[1], sv[2]), dtype_code(k)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError("libtxl computes in float32 or bfloat16, got %s" % dtype)
+    return native.QMEM_KV_ARGS.pack(mem.address, k.data_ptr(), k0, k1, k2, v.data_ptr(), v0, v1, v2, j0, T, code,
+                                    _raw_stream(stream, dev))
 
 
 def qmem_push(mem: QuantMemory, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> QuantMemory:
     """Quantise k_new/v_new [B, L, H, D] into the FIFO memory (txl_qmem_push)."""
-    L = k_new.shape[1]
-    vk, vv, dtype = _qmem_kv(mem, k_new, v_new, L)
-    check(_on_device(mem.device, lambda: _lib().txl_qmem_push(mem.c_struct, vk, vv, L, dtype,
-                                                              _raw_stream(stream, mem.device))), "txl_qmem_push")
+    args = _qmem_kv(mem, k_new, v_new, 0, k_new.shape[1], stream)
+    check(_on_device(mem.device, _lib().txl_qmem_push_call, args), "txl_qmem_push")
     return mem
 
 
 def qmem_read(mem: QuantMemory, j0: int, n: int, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
     """What the memory's logical positions j0 .. j0+n-1 (oldest first, all valid) stand for, into
     k_out/v_out [B, n, H, D] (txl_qmem_read)."""
-    vk, vv, dtype = _qmem_kv(mem, k_out, v_out, n)
-    check(_on_device(mem.device, lambda: _lib().txl_qmem_read(mem.c_struct, j0, n, vk, vv, dtype,
-                                                              _raw_stream(stream, mem.device))), "txl_qmem_read")
+    args = _qmem_kv(mem, k_out, v_out, j0, n, stream)
+    check(_on_device(mem.device, _lib().txl_qmem_read_call, args), "txl_qmem_read")
     return k_out, v_out
 
 
@@ -553,7 +553,7 @@ def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor,
         v_cur.data_ptr(), v0, v1, v2, out.data_ptr(), o0, o1, o2, mem.address if mem is not None else 0, u.data_ptr(),
         v_bias.data_ptr(), r.data_ptr(), rt[1], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev))
-    check(_on_device(dev, lambda: _lib().txl_rel_attn_qmem_call(args)), "txl_rel_attn_qmem")
+    check(_on_device(dev, _lib().txl_rel_attn_qmem_call, args), "txl_rel_attn_qmem")
     return out
 
 

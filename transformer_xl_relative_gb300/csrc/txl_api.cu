@@ -1139,6 +1139,18 @@ txl_status txl_qmem_read(const txl_qmem* mem, int j0, int n, const txl_view* k_o
     return launch_qmem_read(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
 }
 
+txl_status txl_qmem_push_call(const txl_qmem_kv_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    return txl_qmem_push(a->mem, &a->k, &a->v, a->n, static_cast<txl_dtype>(a->dtype), a->stream);
+}
+
+txl_status txl_qmem_read_call(const txl_qmem_kv_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    return txl_qmem_read(a->mem, a->j0, a->n, &a->k, &a->v, static_cast<txl_dtype>(a->dtype), a->stream);
+}
+
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype)
 {
     if (B <= 0 || L <= 0 || H <= 0 || D <= 0 || D > 128) return 0;

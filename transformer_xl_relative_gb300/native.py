@@ -30,7 +30,7 @@ EXPORTS = (
     "txl_rel_attn_table_path", "txl_rel_attn_decode_path", "txl_rel_attn_fwd_lse", "txl_rel_attn_bwd_lse",
     "txl_rel_attn_bwd_path", "txl_qmem_row_bytes", "txl_qmem_push", "txl_qmem_read",
     "txl_rel_attn_qmem", "txl_rel_attn_qmem_workspace_size", "txl_rel_attn_qmem_path",
-    "txl_rel_attn_qmem_call",
+    "txl_rel_attn_qmem_call", "txl_qmem_push_call", "txl_qmem_read_call",
 )
 
 
@@ -53,6 +53,8 @@ class TxlQmem(ctypes.Structure):
                 ("bits", ctypes.c_int), ("wp", ctypes.c_int), ("valid", ctypes.c_int)]
 
 
+# txl_qmem_kv_args: mem; the views k, v; j0, n, dtype; stream (pointers as unsigned 64-bit numbers)
+QMEM_KV_ARGS = struct.Struct("@Q" + 2 * "Qqqq" + "3iQ")
 # txl_rel_attn_qmem_args: B, L, H, D, clamp_len, n_rows, dtype, scale; the views q, k_cur, v_cur, out; mem, u,
 # v_bias, r, ld_r, workspace, workspace_bytes, err_flag, stream (pointers as unsigned 64-bit numbers)
 QMEM_ARGS = struct.Struct("@7if" + 4 * "Qqqq" + "QQQQqQQQQ")
@@ -157,6 +159,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.txl_rel_attn_qmem.restype = i
     lib.txl_rel_attn_qmem_call.argtypes = [ctypes.c_char_p]
     lib.txl_rel_attn_qmem_call.restype = i
+    lib.txl_qmem_push_call.argtypes = [ctypes.c_char_p]
+    lib.txl_qmem_push_call.restype = i
+    lib.txl_qmem_read_call.argtypes = [ctypes.c_char_p]
+    lib.txl_qmem_read_call.restype = i
     lib.txl_rel_attn_qmem_workspace_size.argtypes = [i, i, i, i, Qp, i]
     lib.txl_rel_attn_qmem_workspace_size.restype = ctypes.c_size_t
     lib.txl_rel_attn_qmem_path.argtypes = [i, i, i, i, V, Qp, V, V, vp, i64, V, i]
