@@ -514,7 +514,7 @@ txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
  * and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16 operands and P, for q,
  * k_cur, v_cur and r of any layout.  (Queries that would bring scores past fp16's range, 65504, are held
  * at it.)
- * L > 16, fp32, two launches: the memory is read back and txl_rel_attn_fwd's fp32 kernel runs.
+ * L > 16, fp32, one launch: codes are expanded tile by tile in shared memory, all arithmetic in fp32.
  * err_flag as for txl_rel_attn_fwd: every kernel that waits for copies sets it if a wait runs out.
  */
 txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len,
@@ -545,15 +545,15 @@ typedef struct {
 txl_status txl_rel_attn_qmem_call(const txl_rel_attn_qmem_args* args);
 
 /* Bytes of device workspace txl_rel_attn_qmem needs.  L <= 16: B*H*L rows of M + L floats (a multiple of
- * four, and up to seven more).  L > 16: 0 without a memory, else, with D rounded up to a multiple of 8
- * in each row of a head, M rows of K and V in dtype and for bf16 also 3 L such rows, M + L rows of r and
- * 144 bytes per (b, h). */
+ * four, and up to seven more).  L > 16: 0 without a memory or in fp32, else, with D rounded up to a
+ * multiple of 8 in each row of a head, M rows of K and V in 16 bits, 3 L such rows, M + L rows of r and 144
+ * bytes per (b, h). */
 size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qmem* mem, txl_dtype dtype);
 
-/* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the kernel that expands the
- * codes on chip (L <= 16), 1 or 2 = the memory read back, then that kernel of txl_rel_attn_path, or a
- * negative txl_status if the arguments are rejected.  Nothing is launched; the workspace is not
- * checked. */
+/* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the one that multiplies the codes
+ * (L <= 16), 6 = the fp32 one of longer segments, 1 = the expanded memory, then the tcgen05 kernels, 1 or
+ * 2 = the kernel of txl_rel_attn_path for a bf16 call without valid positions, or a negative txl_status if
+ * the arguments are rejected.  Nothing is launched; the workspace is not checked. */
 int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem,
                            const txl_view* k_cur, const txl_view* v_cur, const void* r,
                            int64_t ld_r, const txl_view* out, txl_dtype dtype);

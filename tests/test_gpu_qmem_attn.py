@@ -235,15 +235,22 @@ SEGMENT = [
     (2, 2, 128, 100, 130, 130, 7, 1000, "bf16", 1),
     (1, 2, 64, 40, 64, 0, 5, 1000, "bf16", 1),              # nothing valid yet
     (1, 2, 64, 40, 0, 0, 0, 1000, "bf16", 1),
-    (1, 2, 41, 30, 50, 50, 13, 1000, "f32", 2),
+    (1, 2, 41, 30, 50, 50, 13, 1000, "f32", 6),
+    (2, 2, 64, 32, 64, 64, 1, 1000, "f32", 6),              # whole tiles
+    (1, 3, 64, 33, 1000, 990, 77, 300, "f32", 6),           # eight ranks, one query in the last tile
+    (3, 2, 128, 17, 129, 129, 128, 50, "f32", 6),
+    (1, 1, 8, 100, 300, 300, 299, 0, "f32", 6),
+    (2, 1, 96, 65, 200, 1, 150, 1000, "f32", 6),
+    (1, 2, 24, 70, 64, 0, 5, 1000, "f32", 6),               # nothing valid yet
+    (1, 2, 64, 95, 0, 0, 0, 40, "f32", 6),
+    (20, 8, 33, 20, 30, 30, 29, 1000, "f32", 6),            # more heads than multiprocessors
 ]
 
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("c", SEGMENT, ids=["B%dH%dD%d_L%dM%dv%dwp%dC%d_%s_p%d" % c for c in SEGMENT])
 def test_segments_match_64_bits(txl, c, bits):
-    """Longer segments run the framework's attention kernels over the memory read back: bf16 operands
-    on the tensor cores, fp32 arithmetic for fp32."""
+    """Longer segments: the fused kernels over the expanded memory in bf16, a kernel of its own for fp32."""
     B, H, D, L, M, valid, wp, C, dtype, path = c
     call = Call(txl, B, H, D, L, M, valid, wp, C, bits, dtype)
     assert txl.rel_attn_qmem_path(call.q, call.mem, call.k, call.v, call.r, call.out) == path
@@ -253,6 +260,20 @@ def test_segments_match_64_bits(txl, c, bits):
         check(call)
     else:
         check_segment(call)
+
+
+def test_fp32_segment_sees_no_later_key(txl):
+    """Keys and values of the segment that are NaN or infinite reach the queries from their position on."""
+    call = Call(txl, 1, 2, 64, 50, 200, 200, 9, 1000, 4, "f32", hs=65, shift=1)
+    ref, size, vmax = call.reference()
+    call.k[:, 40:] = float("nan")
+    call.v[:, 35:] = float("inf")
+    call.run(txl)
+    torch.cuda.synchronize()
+    out = f64(call.out)
+    tol = decode_tolerance(ref, size, vmax, call.dtype)
+    assert (np.abs(out - ref) <= tol)[:, :35].all()
+    assert np.isinf(out[:, 35:40]).all() and np.isnan(out[:, 40:]).all()
 
 
 @pytest.mark.parametrize("factor", [1e-30, 1e-5, 1e5, 1e30])

@@ -130,7 +130,7 @@ def test_calls_need_their_workspace(native):
     p = ctypes.byref
     need = ((2 * 128 + 3 * 17) * 2 + 128 + 17) * 4 * 64 * 2 + 2 * 4 * 144
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 1) == need
-    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 2 * 128 * 2 * 4 * 64 * 4
+    assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, p(m), 0) == 0
     assert lib.txl_rel_attn_qmem_workspace_size(2, 16, 4, 64, p(m), 1) == 2 * 4 * 16 * (148 + 1) * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 1, 4, 64, None, 1) == 2 * 4 * 1 * (4 + 1) * 4
     assert lib.txl_rel_attn_qmem_workspace_size(2, 17, 4, 64, None, 1) == 0
@@ -152,7 +152,7 @@ def test_path_selection(native):
     assert path() == 5 and path(L=16) == 5 and path(L=16, dtype=0) == 5 and path(D=41) == 5
     assert path(L=17) == 1                                             # read back, fused tcgen05 kernel
     assert path(L=200, m=qmem(native, M=300, wp=77, valid=250)) == 1   # whatever the ring's write pointer
-    assert path(L=200, dtype=0) == 2                                   # fp32: CUDA cores
+    assert path(L=200, dtype=0) == 6                                   # fp32: CUDA cores
     assert path(L=200, D=41, ld_r=48) == 1                             # dense 82-byte rows are copied
     assert path(L=200, ptr=FAKE + 2) == 1                              # and so are misaligned ones
     assert path(L=200, m=qmem(native, valid=0)) == 1

@@ -558,8 +558,8 @@ def rel_attn_qmem(q: torch.Tensor, mem: QuantMemory | None, k_cur: torch.Tensor,
 
 
 def rel_attn_qmem_path(q, mem, k_cur, v_cur, r, out) -> int:
-    """5 = the kernel that expands the codes on chip (up to 16 queries), 1 or 2 = the memory read back,
-    then the kernel of rel_attn_path (txl_rel_attn_qmem_path)."""
+    """5 = the kernel that multiplies the codes (up to 16 queries), 6 = the fp32 one of longer segments, 1 = the
+    expanded memory, then the tcgen05 kernels (txl_rel_attn_qmem_path)."""
     B, L, H, D = q.shape
     memc = ctypes.byref(mem.c_struct) if mem is not None else None
     vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)

@@ -1081,18 +1081,17 @@ txl_status check_qattn(int B, int L, int H, int D, const txl_view* q, const txl_
 
 // The memory's valid positions as read back into the workspace: head-major [B][H][valid][ld], oldest
 // first, ld = D rounded up to 8 so that rows start on 16-byte boundaries.
-txl_mem read_back_mem(int B, int H, int D, const txl_qmem* mem, txl_dtype dtype, void* workspace)
+txl_mem read_back_mem(int B, int H, int D, const txl_qmem* mem, void* workspace)
 {
     const int64_t ld = (D + 7) / 8 * 8, n = mem->valid;
-    const int64_t elem = dtype == TXL_F32 ? 4 : 2;
     txl_mem m{};
     m.k = workspace;
-    m.v = static_cast<char*>(workspace) + B * H * n * ld * elem;
+    m.v = static_cast<uint16_t*>(workspace) + B * H * n * ld;
     m.stride_b = H * n * ld;
     m.stride_t = ld;
     m.stride_h = n * ld;
     m.B = B; m.M = mem->valid; m.H = H; m.D = D;
-    m.dtype = dtype;
+    m.dtype = TXL_BF16;
     m.wp = 0;
     m.valid = mem->valid;
     return m;
@@ -1157,9 +1156,8 @@ size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qm
     const size_t M = mem && mem->M > 0 ? mem->M : 0;
     // position terms: a row of at most M + L + 3 keys, a multiple of four floats, and one value more
     if (L <= kDecodeMaxL) return static_cast<size_t>(B) * H * L * ((M + L + 6) / 4 * 4 + 1) * 4;
-    if (M == 0) return 0;
+    if (M == 0 || dtype == TXL_F32) return 0;
     const size_t row = static_cast<size_t>(B) * H * ((D + 7) / 8 * 8);
-    if (dtype == TXL_F32) return 2 * row * mem->M * 4;
     const size_t r_rows = static_cast<size_t>(H) * ((D + 7) / 8 * 8) * (static_cast<size_t>(mem->M) + L);
     return (2 * row * mem->M + 3 * row * L + r_rows) * 2 + static_cast<size_t>(B) * H * 144;
 }
@@ -1170,10 +1168,9 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
     const txl_status st = check_qattn(B, L, H, D, q, mem, k_cur, v_cur, r, ld_r, out, dtype);
     if (st != TXL_OK) return -static_cast<int>(st);
     if (L <= kDecodeMaxL) return 5;
+    if (dtype == TXL_F32) return 6;
     if (!mem || mem->valid == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
-    if (dtype == TXL_BF16) return 1;
-    const txl_mem m = read_back_mem(B, H, D, mem, dtype, mem->rows);  // an aligned address; nothing is read
-    return txl_rel_attn_path(B, L, H, D, q, &m, k_cur, v_cur, r, ld_r, out, dtype);
+    return 1;
 }
 
 txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const txl_view* q, const txl_qmem* mem,
@@ -1192,57 +1189,49 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (B > 65535 || H > 65535) return TXL_ERR_UNSUPPORTED;
     const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
-    if (L > kDecodeMaxL) {
-        if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
+    if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
+    if (L > kDecodeMaxL && dtype == TXL_BF16) {
         if (valid == 0)
             return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, nullptr, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale,
                                     out, dtype, nullptr, 0, err_flag, stream);
         if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
-        const txl_mem m = read_back_mem(B, H, D, mem, dtype, workspace);
-        if (dtype == TXL_BF16) {
-            const int ld = (D + 7) / 8 * 8;
-            const int64_t seg = static_cast<int64_t>(B) * H * L * ld;
-            QexpandParams e{};
-            e.rows = static_cast<const uint8_t*>(mem->rows);
-            e.B = B; e.H = H; e.D = D; e.M = M; e.G = q_groups(D); e.bits = mem->bits;
-            e.slot0 = ring_slot(mem, M - valid);
-            e.n = valid; e.L = L; e.ld = ld;
-            auto rows16 = [&](const txl_view* v) {
-                return a16(v->ptr) && s16(v->stride_b, 2) && s16(v->stride_t, 2) && s16(v->stride_h, 2);
-            };
-            e.vcur = v_cur->ptr; e.vc_sb = v_cur->stride_b; e.vc_st = v_cur->stride_t; e.vc_sh = v_cur->stride_h;
-            e.kcur = k_cur->ptr; e.kc_sb = k_cur->stride_b; e.kc_st = k_cur->stride_t; e.kc_sh = k_cur->stride_h;
-            e.q = q->ptr; e.q_sb = q->stride_b; e.q_st = q->stride_t; e.q_sh = q->stride_h;
-            e.r = static_cast<const uint16_t*>(r);
-            e.ld_r = ld_r;
-            e.n_r = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(valid) + L, static_cast<int64_t>(clamp_len) + 1));
-            e.vec_v = rows16(v_cur); e.vec_k = rows16(k_cur); e.vec_q = rows16(q); e.vec_r = a16(r) && s16(ld_r, 2);
-            e.k_mem = m.k;
-            e.v_mem = m.v;
-            uint16_t* at = static_cast<uint16_t*>(m.v) + static_cast<int64_t>(B) * H * valid * ld;
-            e.k_seg = at;
-            e.v_seg = at + seg;
-            const txl_view ks{e.k_seg, static_cast<int64_t>(H) * L * ld, ld, static_cast<int64_t>(L) * ld};
-            txl_view vs = ks, qs = ks;
-            vs.ptr = e.v_seg;
-            // q that TMA cannot address is copied to rows that it can
-            if (!view_tma_ok(q, L, H, B)) qs.ptr = e.q_seg = at + 2 * seg;
-            else qs = *q;
-            e.r16 = at + 3 * seg;
-            e.units = reinterpret_cast<float*>(at + 3 * seg + static_cast<int64_t>(e.n_r) * H * ld);
-            e.chk = range_counter();
-            e.absmax = e.units + static_cast<int64_t>(B) * H * 4;
-            if (launch_qmem_expand(e, s) != cudaSuccess) return TXL_ERR_CUDA;
-            return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
-                                  err_flag, s, 0, nullptr, 0, e.units);
-        }
-        const txl_view kw{m.k, m.stride_b, m.stride_t, m.stride_h}, vw{m.v, m.stride_b, m.stride_t, m.stride_h};
-        st = txl_qmem_read(mem, M - valid, valid, &kw, &vw, dtype, stream);
-        if (st != TXL_OK) return st;
-        return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, &m, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale, out,
-                                dtype, nullptr, 0, err_flag, stream);
+        const txl_mem m = read_back_mem(B, H, D, mem, workspace);
+        const int ld = (D + 7) / 8 * 8;
+        const int64_t seg = static_cast<int64_t>(B) * H * L * ld;
+        QexpandParams e{};
+        e.rows = static_cast<const uint8_t*>(mem->rows);
+        e.B = B; e.H = H; e.D = D; e.M = M; e.G = q_groups(D); e.bits = mem->bits;
+        e.slot0 = ring_slot(mem, M - valid);
+        e.n = valid; e.L = L; e.ld = ld;
+        auto rows16 = [&](const txl_view* v) {
+            return a16(v->ptr) && s16(v->stride_b, 2) && s16(v->stride_t, 2) && s16(v->stride_h, 2);
+        };
+        e.vcur = v_cur->ptr; e.vc_sb = v_cur->stride_b; e.vc_st = v_cur->stride_t; e.vc_sh = v_cur->stride_h;
+        e.kcur = k_cur->ptr; e.kc_sb = k_cur->stride_b; e.kc_st = k_cur->stride_t; e.kc_sh = k_cur->stride_h;
+        e.q = q->ptr; e.q_sb = q->stride_b; e.q_st = q->stride_t; e.q_sh = q->stride_h;
+        e.r = static_cast<const uint16_t*>(r);
+        e.ld_r = ld_r;
+        e.n_r = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(valid) + L, static_cast<int64_t>(clamp_len) + 1));
+        e.vec_v = rows16(v_cur); e.vec_k = rows16(k_cur); e.vec_q = rows16(q); e.vec_r = a16(r) && s16(ld_r, 2);
+        e.k_mem = m.k;
+        e.v_mem = m.v;
+        uint16_t* at = static_cast<uint16_t*>(m.v) + static_cast<int64_t>(B) * H * valid * ld;
+        e.k_seg = at;
+        e.v_seg = at + seg;
+        const txl_view ks{e.k_seg, static_cast<int64_t>(H) * L * ld, ld, static_cast<int64_t>(L) * ld};
+        txl_view vs = ks, qs = ks;
+        vs.ptr = e.v_seg;
+        // q that TMA cannot address is copied to rows that it can
+        if (!view_tma_ok(q, L, H, B)) qs.ptr = e.q_seg = at + 2 * seg;
+        else qs = *q;
+        e.r16 = at + 3 * seg;
+        e.units = reinterpret_cast<float*>(at + 3 * seg + static_cast<int64_t>(e.n_r) * H * ld);
+        e.chk = range_counter();
+        e.absmax = e.units + static_cast<int64_t>(B) * H * 4;
+        if (launch_qmem_expand(e, s) != cudaSuccess) return TXL_ERR_CUDA;
+        return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
+                              err_flag, s, 0, nullptr, 0, e.units);
     }
-    if (!workspace || workspace_bytes < need || !a16(workspace)) return TXL_ERR_WORKSPACE;
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
     QattnParams p;
     std::memset(&p, 0, sizeof(p));
@@ -1263,7 +1252,15 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.qscale = scale * 1.4426950408889634f;
     const int elem = dtype == TXL_F32 ? 4 : 2;
     p.vec_r = a16(r) && s16(ld_r, elem);
-    p.vec_k = a16(k_cur->ptr) && s16(k_cur->stride_b, elem) && s16(k_cur->stride_t, elem) && s16(k_cur->stride_h, elem);
+    auto rows16 = [&](const txl_view* v) {
+        return a16(v->ptr) && s16(v->stride_b, elem) && s16(v->stride_t, elem) && s16(v->stride_h, elem);
+    };
+    p.vec_k = rows16(k_cur);
+    p.vec_v = rows16(v_cur);
+    p.chk = range_counter();
+    const int sms = sm_count();
+    if (sms <= 0) return TXL_ERR_CUDA;
+    if (L > kDecodeMaxL) return launch_qseg_f32(p, sms, s) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
     // keys up to M - C are at the clamp for every query
     const int first_near = std::max<int64_t>(p.lo, std::min<int64_t>(M, static_cast<int64_t>(M) - clamp_len + 1));
     p.jn = first_near - (first_near - p.lo) % 4;
@@ -1272,9 +1269,6 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     p.E = static_cast<float*>(workspace);
     p.far = p.E + static_cast<int64_t>(B) * H * L * p.e_pitch;
     p.err_flag = err_flag;
-    p.chk = range_counter();
-    const int sms = sm_count();
-    if (sms <= 0) return TXL_ERR_CUDA;
     return launch_qattn(p, sms, s) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
 }
 

@@ -316,7 +316,7 @@ struct QexpandParams {
 };
 cudaError_t launch_qmem_expand(const QexpandParams& p, cudaStream_t s);
 
-// Attention of 1 .. kDecodeMaxL queries over a quantised memory and the segment's own keys.
+// Attention over a quantised memory and the segment's own keys: of 1 .. kDecodeMaxL queries, or of an fp32 segment.
 struct QattnParams {
     const void* q; int64_t q_sb, q_st, q_sh;
     const void* kcur; int64_t kc_sb, kc_st, kc_sh;
@@ -329,7 +329,7 @@ struct QattnParams {
     int B, L, H, D, M, G, bits, lo, wp, C;      // lo: first valid logical key
     int n_rows;
     float qscale;                               // scale * log2(e)
-    int vec_r, vec_k;                           // rows of r, of kcur start on 16-byte boundaries
+    int vec_r, vec_k, vec_v;                    // rows of r, kcur, vcur start on 16-byte boundaries
     // position terms, workspace: E[b][h][i][j - jn] for keys j >= jn (own keys too), e_pitch floats per row (a
     // multiple of 4, lo <= jn = lo mod 4), and far[b][h][i] for keys before; n_dist distances are computed
     float* E; float* far;
@@ -338,6 +338,7 @@ struct QattnParams {
     int* chk;                                   // range-check counter (checked build)
 };
 cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_qseg_f32(const QattnParams& p, int sm_count, cudaStream_t s);   // E, far, jn .. unused
 
 cudaError_t launch_selftest_wait(int* err_flag, unsigned timeout_us, cudaStream_t s);
 // One failing and one passing range check on the device (the checked build's counter gains one).

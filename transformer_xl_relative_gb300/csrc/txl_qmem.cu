@@ -293,20 +293,6 @@ __global__ void __launch_bounds__(kQThreads, 6) qmem_push_kernel(const __grid_co
     }
 }
 
-// lo + step c of eight codes.  A code becomes a float as the low bits of 2^23 + c.
-template <int BITS>
-__device__ __forceinline__ void expand8(const uint32_t* code, float step, float lo, float* x)
-{
-    constexpr float kTwo23 = 8388608.f;
-    const uint32_t even = BITS == 4 ? code[0] & 0x0f0f0f0fu : 0, odd = BITS == 4 ? (code[0] >> 4) & 0x0f0f0f0fu : 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t w = BITS == 4 ? (e & 1 ? odd : even) : code[e >> 2];
-        const float c = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + (BITS == 4 ? e >> 1 : e & 3))) - kTwo23;
-        x[e] = fmaf(step, c, lo);
-    }
-}
-
 // The codes of eight channels from d0 of a row, and their group's parameters.
 template <int BITS, int G>
 __device__ __forceinline__ uint2 row_unit(const uint8_t* row, int d0, uint32_t* ck, uint32_t* cv)

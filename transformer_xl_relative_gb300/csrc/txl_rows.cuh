@@ -1,4 +1,4 @@
-// txl_rows.cuh -- loads of fp32 or bf16 rows, shared by the kernels of the quantised memory.
+// txl_rows.cuh -- loads of fp32 or bf16 rows and expansion of codes, shared by the kernels of the quantised memory.
 #pragma once
 
 #include <cstdint>
@@ -33,6 +33,20 @@ __device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, 
             if constexpr (F32) x[e] = __ldg(static_cast<const float*>(row) + d0 + e);
             else x[e] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
         }
+    }
+}
+
+// lo + step c of eight codes.  A code becomes a float as the low bits of 2^23 + c.
+template <int BITS>
+__device__ __forceinline__ void expand8(const uint32_t* code, float step, float lo, float* x)
+{
+    constexpr float kTwo23 = 8388608.f;
+    const uint32_t even = BITS == 4 ? code[0] & 0x0f0f0f0fu : 0, odd = BITS == 4 ? (code[0] >> 4) & 0x0f0f0f0fu : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t w = BITS == 4 ? (e & 1 ? odd : even) : code[e >> 2];
+        const float c = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + (BITS == 4 ? e >> 1 : e & 3))) - kTwo23;
+        x[e] = fmaf(step, c, lo);
     }
 }
 
