@@ -38,11 +38,12 @@
 // of a head are the ranks of a cluster: each writes its partial results into the shared memory of the
 // rank that finishes the row.
 //
-// Measured (both kernels, B8 H16 D64, one query): 4096 keys of 4 bits 17.0 us (44 MB; 6.5 us of HBM), of 8 bits
-// 22.5 us (78 MB), 16384 keys of 4 bits 37.5 us (170 MB, 4.5 TB/s; 5.9 TB/s of what each further key adds).
+// Measured (both kernels, B8 H16 D64, one query): 4096 keys of 4 bits 15.4 us (44 MB; 6.5 us of HBM), of 8 bits
+// 19.9 us (78 MB), 16384 keys of 4 bits 34.4 us (170 MB, 4.9 TB/s; 6.6 TB/s of what each further key adds).
 // The bf16 memory's decode takes 40 us at 4096 keys.  Two CTAs of eight warps fill the registers of an SM; of
-// a token's 13 us in the kernel 3 are the prologue (the copies of half the memory are in flight), 2.5 the
-// merge, and the loop issues on 35 to 50% of the cycles: products and shared memory wait for each other.
+// a token's 12 us in the kernel 3 are the prologue (the copies of half the memory are in flight), 2.5 the
+// merge.  The loop is latency: every shared-memory access is free of bank conflicts (with the parts of q in the
+// same banks it took 1000 instead of 640 cycles per stage for Q.K, and the call 17.0 us).
 #include <algorithm>
 #include <atomic>
 
@@ -140,7 +141,7 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w)
 }
 
 // Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
-// large at 4 bits).  `half` selects the upper byte (4 bits).
+// large at 4 bits).
 template <int BITS>
 __device__ __forceinline__ uint32_t pair_even(uint32_t w) { return w & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu); }
 template <int BITS>
@@ -149,9 +150,10 @@ __device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w 
 // E[b][h][i][x] = (q_i+v).r[min(M+i-j, C)] in log2 units for keys j = jn + x, and far[b][h][i] = (q_i+v).r[C].
 // Bound by reading r once: a CTA prepares q+v of up to pos_pairs (entry, query) pairs of a head as two bf16 parts
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
-// from global memory as fragments) are requested one tile ahead.  WALK: more tiles than three CTAs per SM; four CTAs per SM
-// (64 registers) then keep more rows in flight (65537 distances of 16 heads: the whole call 44.8 us, 62.4 with three);
-// with fewer the free choice of registers (66) is quicker (token over 4096 keys 15.4 us, 16.0 with 64).
+// from global memory as fragments) are requested one tile ahead.  65537 distances of 16 heads: 26 us, 5.1 TB/s.
+// WALK: more tiles than three CTAs per SM; four CTAs per SM (64 registers) then keep more rows in flight (those
+// 65537 distances: the whole call 44.8 us, 62.4 with three); with fewer the free choice of registers (66) is
+// quicker (token over 4096 keys 15.4 us, 16.0 with 64).
 __host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
 template <int NG, bool WALK>
@@ -883,7 +885,7 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
     }
     // Key ranges: the cluster size whose waves of clusters, each over 1/ranks of the keys, take the least time, while
     // each warp keeps a stage.  A GPC holds a whole number of clusters, so that large ones leave SMs idle: 16 heads of
-    // one sequence fit in one wave as clusters of up to 13 (65536 4-bit keys: 48.4 us), not of 16 (55.6; 8 take 57.7).
+    // one sequence fit in one wave as clusters of up to 13 (65536 4-bit keys: 48.4 us when chosen), not of 16 (55.6; 8: 57.7).
     constexpr int ks = stage_keys(BITS, NG, QT);
     const int64_t keys = p.M - p.lo, heads = static_cast<int64_t>(p.H) * p.B * groups;
     int64_t waves = 0;
