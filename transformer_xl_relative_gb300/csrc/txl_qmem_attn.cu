@@ -1,5 +1,5 @@
 // txl_qmem_attn.cu -- relative attention of 1 .. 16 queries over a quantised memory and the segment's
-// own keys: the generation step over a memory of 4- or 8-bit codes, in two launches.
+// own keys: the generation step over a memory of 4- or 8-bit codes, in two launches or one.
 //
 //     s_ij = scale [ (q_i+u).k'_j + (q_i+v).r[min(M+i-j, C)] ],  out_i = softmax_j(s_ij) v'_j
 // with k'_jd = lo_jG + step_jG c_jd in group G of 32 channels.  The codes never become k' or v':
@@ -30,7 +30,7 @@
 // for every query and take one value per query, far[b][h][i].  (Computed inside the attention kernel
 // instead, for the keys of a block between the steps of the one before, the 32 registers of r rows in
 // flight and a block barrier per stage cost more than the launch: 66 instead of then 49 us at B8
-// H16 D64 M16384.)  The attention kernel's prologue and first copies run while qpos_kernel does.
+// H16 D64 M16384.  A CTA that has few such keys computes them itself, before the key loop.)  The attention kernel's prologue and first copies run while qpos_kernel does.
 //
 // One CTA: one batch entry, one head, up to eight queries and a range of keys; eight warps, each with
 // its own ring of bulk-copy stages and no block barrier in the key loop (cp.async, 16 bytes per lane, held
@@ -85,6 +85,7 @@ struct QSplit {               // how the host divides the work
     int lq;                   // queries of a CTA; blockIdx.x / ranks selects the group of queries
     int ranks;                // CTAs of a cluster: key ranges
     int range;                // keys of a range (a multiple of the stage)
+    int fused;                // the CTA computes its position terms itself
 };
 
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
@@ -147,6 +148,32 @@ __device__ __forceinline__ uint32_t pair_even(uint32_t w) { return w & (BITS == 
 template <int BITS>
 __device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : __byte_perm(w, 0, 0x4341); }
 
+// Rows of r of 16 distances from d0 as the A operand's fragments: this lane's of distances g and g + 8.
+template <int NG>
+__device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0, uint4 (&a)[2][NG])
+{
+    const int g = (threadIdx.x & 31) >> 2, c4 = threadIdx.x & 3;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        int rr = static_cast<int>(min(d0 + g + 8 * y, static_cast<unsigned>(p.C)));
+        if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;  // past the distances of the call
+        const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+            const int d = 32 * G + 8 * c4;
+            if (p.vec_r && d + 8 <= p.D) {
+                a[y][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
+            } else {
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
+                a[y][G] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
 // E[b][h][i][x] = (q_i+v).r[min(M+i-j, C)] in log2 units for keys j = jn + x, and far[b][h][i] = (q_i+v).r[C].
 // Bound by reading r once: a CTA prepares q+v of up to pos_pairs (entry, query) pairs of a head as two bf16 parts
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
@@ -171,30 +198,9 @@ __global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kern
     // memory and the queries before its own wait.
     pdl_wait();
     pdl_launch_dependents();
-    auto load = [&](unsigned d0, uint4 (&a)[2][NG]) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            int rr = static_cast<int>(min(d0 + g + 8 * y, static_cast<unsigned>(p.C)));
-            if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;  // past the distances of the call
-            const uint16_t* src = static_cast<const uint16_t*>(p.r) + rr * p.r_row + h * p.r_head;
-#pragma unroll
-            for (int G = 0; G < NG; ++G) {
-                const int d = 32 * G + 8 * c4;
-                if (p.vec_r && d + 8 <= p.D) {
-                    a[y][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
-                } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
-                    a[y][G] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-        }
-    };
     uint4 a[2][NG];
     unsigned d0 = blockIdx.x * 128 + warp * 16;                       // first distance of the warp's tile
-    load(d0, a);
+    load_r<NG>(p, h, d0, a);
     const int n_ct = (pairs + 3) >> 2;
     float vb[NG];
 #pragma unroll
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kern
     __syncthreads();
     for (; d0 < static_cast<unsigned>(p.n_dist); d0 += gridDim.x * 128) {
         uint4 next[2][NG];
-        load(d0 + gridDim.x * 128, next);
+        load_r<NG>(p, h, d0 + gridDim.x * 128, next);
         for (int ct = 0; ct < n_ct; ++ct) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -298,7 +304,9 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     float* own_s = qsum + kMaxRows * NG;                  // [row][kOwn]: scores of the segment's own keys
     float* weights = own_s + kMaxRows * kDecodeMaxL;      // [row][32]: of the parts that make the result
     uint16_t* quh = reinterpret_cast<uint16_t*>(weights + kMaxRows * 32);   // [2 row + part][QP]; rows past Lq are zeros
-    uint64_t* bars = reinterpret_cast<uint64_t*>(quh + 2 * kMaxRows * QP);   // [warp][stage]: copies landed
+    uint16_t* qvs = quh + 2 * kMaxRows * QP;              // fused: [2 row + part][QP] of q+v in bf16, or [row][QP] floats
+    float* far_s = reinterpret_cast<float*>(qvs + 2 * kMaxRows * QP);       // fused: [row]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(far_s + kMaxRows);         // [warp][stage]: copies landed
     int* abort_flag = reinterpret_cast<int*>(bars + kWarps * kStages);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
@@ -313,6 +321,10 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     if (tid == 0) *abort_flag = 0;
     const WaitCtl wc{abort_flag, p.err_flag, kWaitTimeoutNs};
 
+    if (sp.fused) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     // ---- the queries' elements, requested before the copies fill the memory system (raw: the conversion would
     // wait for them).  qpos_kernel started this grid after everything before it had completed.
     uint32_t q_raw[NG];
@@ -422,6 +434,17 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             if (lane == 0) qsum[row * NG + e] = sum;
+            if (sp.fused) {
+                const float q = __uint_as_float(p.f32 ? q_raw[e] : q_raw[e] << 16);
+                const float c = my_row && d < p.D ? (q + __ldg(p.vb + h * p.D + d)) * p.qscale : 0.f;
+                if (p.f32) {
+                    reinterpret_cast<float*>(qvs)[row * QP + d] = c;
+                } else {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(c);
+                    qvs[2 * row * QP + d] = __bfloat16_as_ushort(hi);
+                    qvs[(2 * row + 1) * QP + d] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
+                }
+            }
         }
     }
     __syncthreads();
@@ -459,14 +482,69 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         for (int G = 0; G < NG; ++G) qs[t][G] = qsum[is * NG + G];
     }
 
-    // ---- from here on the position terms are there
-    pdl_wait();
-    pdl_launch_dependents();
-    const float* e_row0 = p.E + (bh * p.L + i0) * p.e_pitch;
+    float* e_row0 = p.E + (bh * p.L + i0) * p.e_pitch;
+    if (sp.fused) {
+        // ---- position terms of the keys ja <= j < jb of this CTA, as qpos_kernel computes them
+        const int ja = max(j_lo, p.jn), jb = has_own ? p.M + n_own : j_hi, i_end = p.M + i0 + Lq;
+        if (!p.f32) {
+            auto tile = [&](int d0, bool clamp) {
+                uint4 a[2][NG];
+                load_r<NG>(p, h, d0, a);
+                for (int ct = 0; 4 * ct < Lq; ++ct) {
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int G = 0; G < NG; ++G) {
+                        const uint4 bw = *reinterpret_cast<const uint4*>(qvs + (8 * ct + g) * QP + 32 * G + 8 * c4);
+                        mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
+                        mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
+                    }
+                    const int row = 4 * ct + c4;
+                    if (row >= Lq) continue;
+                    if (clamp) {
+                        if (g == 0) far_s[row] = acc[0] + acc[1];
+                        continue;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j = p.M + i0 + row - (d0 + g + 8 * y);
+                        if (j >= ja && j < jb) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = acc[2 * y] + acc[2 * y + 1];
+                    }
+                }
+            };
+            for (int d0 = max(0, p.M + i0 + 1 - jb) + 16 * warp; d0 < i_end - ja; d0 += 16 * kWarps) tile(d0, false);
+            if (p.jn > j_lo && warp == kWarps - 1) tile(p.C, true);
+        } else {
+            auto dot = [&](int row, int delta) {
+                int rr = min(delta, p.C);
+                if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
+                const float* r = static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head;
+                float sum = 0.f;
+                for (int d = 0; d < p.D; d += 8) {
+                    float x[8];
+                    load8<true>(r, d, p.D, p.vec_r, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum = fmaf(reinterpret_cast<const float*>(qvs)[row * QP + d + e], x[e], sum);
+                }
+                return sum;
+            };
+            const int n = max(0, jb - ja);
+            for (int x = tid; x < Lq * n; x += kThreads) {
+                const int row = x / n, j = ja + x % n, delta = p.M + i0 + row - j;
+                if (delta >= 0) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = dot(row, delta);
+            }
+            if (p.jn > j_lo && tid < Lq) far_s[tid] = dot(tid, p.C);
+        }
+        fence_proxy_async_global();                       // the copies read what was stored
+        __syncthreads();
+    } else {
+        // ---- from here on the position terms are there
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
-        far_of[t] = p.jn > j_lo ? __ldg(p.far + bh * p.L + i0 + is) : 0.f;
+        far_of[t] = p.jn <= j_lo ? 0.f : sp.fused ? far_s[is] : __ldg(p.far + bh * p.L + i0 + is);
     }
 #pragma unroll
     for (int n = 0; n < kStages; ++n)
@@ -708,7 +786,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
         for (int y = 0; y < (ONE ? 1 : 4); ++y) {
             const int row = row0 + y * row_step;
-            e[y] = row < Lq && j <= i0 + row ? __ldg(e_row0 + static_cast<int64_t>(row) * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
+            e[y] = row < Lq && j <= i0 + row ? __ldcg(e_row0 + static_cast<int64_t>(row) * p.e_pitch + (p.M + j - p.jn)) : -INFINITY;
         }
 #pragma unroll
         for (int y = 0; y < (ONE ? 1 : 4); ++y) {
@@ -843,13 +921,29 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     }
 }
 
+cudaError_t launch_qpos(const QattnParams& p, int ng, int sm_count, cudaStream_t s)
+{
+    const int64_t pairs = static_cast<int64_t>(p.B) * p.L;
+    if (p.f32) {
+        return launch_dependent(qpos_f32_kernel, dim3((p.n_dist + kThreads - 1) / kThreads, p.H, std::min<int64_t>(pairs, 256)),
+                                dim3(kThreads), 0, s, p);
+    }
+    // four CTAs per SM, each walking over its share of the distances (65536 keys of 16 heads, the whole call:
+    // 62.4 us with two, 58.3 with three, 56.0 with four, 58.7 with six)
+    const int64_t tiles = (static_cast<int64_t>(p.n_dist) + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
+    const int64_t per_head = std::max<int64_t>(1, 4 * sm_count / (sets * p.H));
+    const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
+    auto* kernel = ng > 2 ? qpos_kernel<4, true> : tiles * sets * p.H > 3 * sm_count ? qpos_kernel<2, true> : qpos_kernel<2, false>;
+    return launch_dependent(kernel, grid, dim3(kThreads), 0, s, p);
+}
+
 template <int BITS, int NG, int QT, bool ONE>
-cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
+cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cudaStream_t s)
 {
     constexpr int DP = NG * 32;
     constexpr int staged = kWarps * kStages * stage_bytes(BITS, NG, QT, ONE);
     constexpr int bytes = staged + (kMaxRows * (DP + 1 + NG + kDecodeMaxL + 32) + kMaxRanks * (DP + 4)) * 4 +
-                          2 * kMaxRows * (DP + 8) * 2 + kWarps * kStages * 8 + 16;
+                          4 * kMaxRows * (DP + 8) * 2 + kMaxRows * 4 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
     auto* kernel = qattn_kernel<BITS, NG, QT, ONE>;
@@ -899,6 +993,16 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
     }
     sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + ks - 1) / ks * ks);
     if (sp.range == 0) sp.range = ks;
+    // Position terms in the kernel itself where a CTA has few: one launch less.  One query of 16 heads, B 1: over 250 keys
+    // 8.1 instead of 10.2 us eagerly (the host), 6.3 instead of 6.0 replayed; over 500 keys 8.4 and 7.8, over 1000
+    // 11.0 instead of 7.3.  fp32, a dot product per thread: one query over 500 keys 10.5 instead of 14.5, four
+    // over 200 keys 15.7 instead of 14.2.
+    const int64_t near = std::min<int64_t>(sp.range, p.M - p.jn) + p.L;
+    sp.fused = p.f32 ? near * sp.lq <= 512 : near <= 256;
+    if (!sp.fused) {
+        e = launch_qpos(p, NG, sm_count, s);
+        if (e != cudaSuccess) return e;
+    }
     const dim3 grid(sp.ranks * groups, p.H, p.B);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -918,10 +1022,10 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, cudaStream_t s)
 }
 
 template <int BITS, int NG>
-cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, int groups, cudaStream_t s)
+cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, int groups, int sm_count, cudaStream_t s)
 {
-    if (sp.lq == 1) return launch<BITS, NG, 1, true>(p, sp, groups, s);
-    return sp.lq <= 4 ? launch<BITS, NG, 1, false>(p, sp, groups, s) : launch<BITS, NG, 2, false>(p, sp, groups, s);
+    if (sp.lq == 1) return launch<BITS, NG, 1, true>(p, sp, groups, sm_count, s);
+    return sp.lq <= 4 ? launch<BITS, NG, 1, false>(p, sp, groups, sm_count, s) : launch<BITS, NG, 2, false>(p, sp, groups, sm_count, s);
 }
 
 }  // namespace
@@ -929,27 +1033,11 @@ cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, int groups, cudaSt
 cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
 {
     const int ng = p.G <= 2 ? 2 : 4, bits = p.bits == 8 ? 8 : 4;
-    // position terms
-    const int64_t pairs = static_cast<int64_t>(p.B) * p.L;
-    cudaError_t e;
-    if (p.f32) {
-        e = launch_dependent(qpos_f32_kernel, dim3((p.n_dist + kThreads - 1) / kThreads, p.H, std::min<int64_t>(pairs, 256)),
-                             dim3(kThreads), 0, s, p);
-    } else {
-        // four CTAs per SM, each walking over its share of the distances (65536 keys of 16 heads, the whole call:
-        // 62.4 us with two, 58.3 with three, 56.0 with four, 58.7 with six)
-        const int64_t tiles = (static_cast<int64_t>(p.n_dist) + 127) / 128, sets = (pairs + pos_pairs(ng) - 1) / pos_pairs(ng);
-        const int64_t per_head = std::max<int64_t>(1, 4 * sm_count / (sets * p.H));
-        const dim3 grid(static_cast<unsigned>(std::min(tiles, per_head)), p.H, static_cast<unsigned>(sets));
-        auto* kernel = ng > 2 ? qpos_kernel<4, true> : tiles * sets * p.H > 3 * sm_count ? qpos_kernel<2, true> : qpos_kernel<2, false>;
-        e = launch_dependent(kernel, grid, dim3(kThreads), 0, s, p);
-    }
-    if (e != cudaSuccess) return e;
     QSplit sp{};
     const int groups = p.L > 8 ? 2 : 1;                   // queries: eight at most per CTA
     sp.lq = (p.L + groups - 1) / groups;
-    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, groups, s) : launch_qt<4, 4>(p, sp, groups, s);
-    return ng == 2 ? launch_qt<8, 2>(p, sp, groups, s) : launch_qt<8, 4>(p, sp, groups, s);
+    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, groups, sm_count, s) : launch_qt<4, 4>(p, sp, groups, sm_count, s);
+    return ng == 2 ? launch_qt<8, 2>(p, sp, groups, sm_count, s) : launch_qt<8, 4>(p, sp, groups, sm_count, s);
 }
 
 }  // namespace txl
