@@ -30,7 +30,8 @@
 // for every query and take one value per query, far[b][h][i].  (Computed inside the attention kernel
 // instead, for the keys of a block between the steps of the one before, the 32 registers of r rows in
 // flight and a block barrier per stage cost more than the launch: 66 instead of then 49 us at B8
-// H16 D64 M16384.  A CTA that has few such keys computes them itself, before the key loop.)  The attention kernel's prologue and first copies run while qpos_kernel does.
+// H16 D64 M16384.  A CTA that has few such keys computes them itself, before the key loop.)  The attention
+// kernel's prologue and first copies run while qpos_kernel does.
 //
 // One CTA: one batch entry, one head, up to eight queries and a range of keys; eight warps, each with
 // its own ring of bulk-copy stages and no block barrier in the key loop (cp.async, 16 bytes per lane, held
@@ -85,7 +86,6 @@ struct QSplit {               // how the host divides the work
     int lq;                   // queries of a CTA; blockIdx.x / ranks selects the group of queries
     int ranks;                // CTAs of a cluster: key ranges
     int range;                // keys of a range (a multiple of the stage)
-    int fused;                // the CTA computes its position terms itself
 };
 
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
@@ -280,7 +280,67 @@ __global__ void __launch_bounds__(kThreads) qpos_f32_kernel(const __grid_constan
     }
 }
 
-template <int BITS, int NG, int QT, bool ONE>
+// Position terms of the keys ja <= j < jb for queries i0 .. i0 + Lq - 1 of a CTA that computes them itself, as qpos_kernel
+// does, and those at the clamp.
+template <int NG>
+__device__ __forceinline__ void own_terms(const QattnParams& p, const uint16_t* qvs, float* e_row0, float* far_s, int i0,
+                                          int Lq, int ja, int jb, bool clamped)
+{
+    constexpr int QP = NG * 32 + 8;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3, h = blockIdx.y;
+    const int i_end = p.M + i0 + Lq;
+    if (!p.f32) {
+        auto tile = [&](int d0, bool clamp) {
+            uint4 a[2][NG];
+            load_r<NG>(p, h, d0, a);
+            for (int ct = 0; 4 * ct < Lq; ++ct) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int G = 0; G < NG; ++G) {
+                    const uint4 bw = *reinterpret_cast<const uint4*>(qvs + (8 * ct + g) * QP + 32 * G + 8 * c4);
+                    mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
+                    mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
+                }
+                const int row = 4 * ct + c4;
+                if (row >= Lq) continue;
+                if (clamp) {
+                    if (g == 0) far_s[row] = acc[0] + acc[1];
+                    continue;
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = p.M + i0 + row - (d0 + g + 8 * y);
+                    if (j >= ja && j < jb) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = acc[2 * y] + acc[2 * y + 1];
+                }
+            }
+        };
+        for (int d0 = max(0, p.M + i0 + 1 - jb) + 16 * warp; d0 < i_end - ja; d0 += 16 * kWarps) tile(d0, false);
+        if (clamped && warp == kWarps - 1) tile(p.C, true);
+    } else {
+        auto dot = [&](int row, int delta) {
+            int rr = min(delta, p.C);
+            if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
+            const float* r = static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head;
+            float sum = 0.f;
+            for (int d = 0; d < p.D; d += 8) {
+                float x[8];
+                load8<true>(r, d, p.D, p.vec_r, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(reinterpret_cast<const float*>(qvs)[row * QP + d + e], x[e], sum);
+            }
+            return sum;
+        };
+        const int n = max(0, jb - ja);
+        for (int x = tid; x < Lq * n; x += kThreads) {
+            const int row = x / n, j = ja + x % n, delta = p.M + i0 + row - j;
+            if (delta >= 0) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = dot(row, delta);
+        }
+        if (clamped && tid < Lq) far_s[tid] = dot(tid, p.C);
+    }
+}
+
+// FUSED: the CTA computes its position terms itself (a variant, because its code costs the others 0.3 us).
+template <int BITS, int NG, int QT, bool ONE, bool FUSED>
 __global__ void __launch_bounds__(kThreads, NG == 2 || (BITS == 4 && QT == 1) ? 2 : 1)
 qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSplit sp)
 {
@@ -321,7 +381,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     if (tid == 0) *abort_flag = 0;
     const WaitCtl wc{abort_flag, p.err_flag, kWaitTimeoutNs};
 
-    if (sp.fused) {
+    if constexpr (FUSED) {
         pdl_wait();
         pdl_launch_dependents();
     }
@@ -434,7 +494,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             if (lane == 0) qsum[row * NG + e] = sum;
-            if (sp.fused) {
+            if constexpr (FUSED) {
                 const float q = __uint_as_float(p.f32 ? q_raw[e] : q_raw[e] << 16);
                 const float c = my_row && d < p.D ? (q + __ldg(p.vb + h * p.D + d)) * p.qscale : 0.f;
                 if (p.f32) {
@@ -483,57 +543,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     }
 
     float* e_row0 = p.E + (bh * p.L + i0) * p.e_pitch;
-    if (sp.fused) {
-        // ---- position terms of the keys ja <= j < jb of this CTA, as qpos_kernel computes them
-        const int ja = max(j_lo, p.jn), jb = has_own ? p.M + n_own : j_hi, i_end = p.M + i0 + Lq;
-        if (!p.f32) {
-            auto tile = [&](int d0, bool clamp) {
-                uint4 a[2][NG];
-                load_r<NG>(p, h, d0, a);
-                for (int ct = 0; 4 * ct < Lq; ++ct) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int G = 0; G < NG; ++G) {
-                        const uint4 bw = *reinterpret_cast<const uint4*>(qvs + (8 * ct + g) * QP + 32 * G + 8 * c4);
-                        mma::mma16816(acc, a[0][G].x, a[1][G].x, a[0][G].y, a[1][G].y, bw.x, bw.y);
-                        mma::mma16816(acc, a[0][G].z, a[1][G].z, a[0][G].w, a[1][G].w, bw.z, bw.w);
-                    }
-                    const int row = 4 * ct + c4;
-                    if (row >= Lq) continue;
-                    if (clamp) {
-                        if (g == 0) far_s[row] = acc[0] + acc[1];
-                        continue;
-                    }
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int j = p.M + i0 + row - (d0 + g + 8 * y);
-                        if (j >= ja && j < jb) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = acc[2 * y] + acc[2 * y + 1];
-                    }
-                }
-            };
-            for (int d0 = max(0, p.M + i0 + 1 - jb) + 16 * warp; d0 < i_end - ja; d0 += 16 * kWarps) tile(d0, false);
-            if (p.jn > j_lo && warp == kWarps - 1) tile(p.C, true);
-        } else {
-            auto dot = [&](int row, int delta) {
-                int rr = min(delta, p.C);
-                if (!in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
-                const float* r = static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head;
-                float sum = 0.f;
-                for (int d = 0; d < p.D; d += 8) {
-                    float x[8];
-                    load8<true>(r, d, p.D, p.vec_r, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum = fmaf(reinterpret_cast<const float*>(qvs)[row * QP + d + e], x[e], sum);
-                }
-                return sum;
-            };
-            const int n = max(0, jb - ja);
-            for (int x = tid; x < Lq * n; x += kThreads) {
-                const int row = x / n, j = ja + x % n, delta = p.M + i0 + row - j;
-                if (delta >= 0) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = dot(row, delta);
-            }
-            if (p.jn > j_lo && tid < Lq) far_s[tid] = dot(tid, p.C);
-        }
+    if constexpr (FUSED) {
+        own_terms<NG>(p, qvs, e_row0, far_s, i0, Lq, max(j_lo, p.jn), has_own ? p.M + n_own : j_hi, p.jn > j_lo);
         fence_proxy_async_global();                       // the copies read what was stored
         __syncthreads();
     } else {
@@ -544,7 +555,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
-        far_of[t] = p.jn <= j_lo ? 0.f : sp.fused ? far_s[is] : __ldg(p.far + bh * p.L + i0 + is);
+        far_of[t] = p.jn <= j_lo ? 0.f : FUSED ? far_s[is] : __ldg(p.far + bh * p.L + i0 + is);
     }
 #pragma unroll
     for (int n = 0; n < kStages; ++n)
@@ -946,7 +957,8 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
                           4 * kMaxRows * (DP + 8) * 2 + kMaxRows * 4 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
-    auto* kernel = qattn_kernel<BITS, NG, QT, ONE>;
+    auto* kernel = qattn_kernel<BITS, NG, QT, ONE, false>;
+    auto* fused_kernel = qattn_kernel<BITS, NG, QT, ONE, true>;
     // once per device: the shared memory, clusters of more than eight, and how many clusters of each size the device
     // holds at a time
     static std::atomic<uint64_t> prepared{0};
@@ -956,8 +968,11 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (!(prepared.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (auto* k : {kernel, fused_kernel}) {
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
         for (int ranks = 1; ranks <= kMaxRanks && e == cudaSuccess; ++ranks) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(ranks * 64);
@@ -998,8 +1013,8 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     // 11.0 instead of 7.3.  fp32, a dot product per thread: one query over 500 keys 10.5 instead of 14.5, four
     // over 200 keys 15.7 instead of 14.2.
     const int64_t near = std::min<int64_t>(sp.range, p.M - p.jn) + p.L;
-    sp.fused = p.f32 ? near * sp.lq <= 512 : near <= 256;
-    if (!sp.fused) {
+    const bool fused = p.f32 ? near * sp.lq <= 512 : near <= 256;
+    if (!fused) {
         e = launch_qpos(p, NG, sm_count, s);
         if (e != cudaSuccess) return e;
     }
@@ -1018,7 +1033,7 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p, sp);
+    return cudaLaunchKernelEx(&cfg, fused ? fused_kernel : kernel, p, sp);
 }
 
 template <int BITS, int NG>
