@@ -138,8 +138,10 @@ DECODE = [
     (2, 2, 128, 8, 248, 240, 100, 230, "bf16", None, 0),
     (1, 2, 41, 16, 4000, 4000, 77, 210, "bf16", None, 1),          # clamped except the last range
     (1, 2, 64, 2, 20000, 19999, 77, 60, "bf16", None, 0),
-    (1, 2, 64, 1, 511, 511, 100, 1000, "f32", None, 0),
-    (1, 2, 64, 1, 512, 512, 100, 1000, "f32", None, 0),
+    (1, 2, 64, 1, 255, 255, 100, 1000, "f32", None, 0),
+    (1, 2, 64, 1, 256, 256, 100, 1000, "f32", None, 0),
+    (2, 2, 64, 16, 600, 600, 100, 500, "f32", None, 0),            # 32 pairs of (entry, query)
+    (3, 1, 96, 11, 400, 400, 100, 380, "f32", None, 1),            # 33
     (2, 1, 33, 16, 3000, 3000, 77, 30, "f32", None, 1),
 ]
 IDS = ["B%dH%dD%d_L%dM%dv%dwp%dC%d_%s_hs%s_s%d" % c for c in DECODE]

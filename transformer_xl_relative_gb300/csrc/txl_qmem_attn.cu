@@ -88,10 +88,9 @@ struct QSplit {               // how the host divides the work
     int range;                // keys of a range (a multiple of the stage)
 };
 
-__device__ __forceinline__ float ld_elem(const void* p, int64_t i, int f32)
+__device__ __forceinline__ float ld_bf16(const void* p, int64_t i)
 {
-    return f32 ? __ldg(static_cast<const float*>(p) + i)
-               : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kern
 #pragma unroll
         for (int e = 0; e < NG; ++e) {
             const int d = 32 * e + lane;
-            const float c = pr < pairs && d < p.D ? (ld_elem(p.q, at + d, 0) + vb[e]) * p.qscale : 0.f;
+            const float c = pr < pairs && d < p.D ? (ld_bf16(p.q, at + d) + vb[e]) * p.qscale : 0.f;
             const __nv_bfloat16 hi = __float2bfloat16_rn(c);
             qvh[2 * pr * DP + d] = __bfloat16_as_ushort(hi);
             qvh[(2 * pr + 1) * DP + (d ^ 32)] = __bfloat16_as_ushort(__float2bfloat16_rn(c - __bfloat162float(hi)));
@@ -258,25 +257,61 @@ __global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kern
     }
 }
 
-// The same in fp32 arithmetic: a thread per (pair, distance).
+// The same in fp32 arithmetic: 64 distances (32 of heads above 64) by up to 32 pairs per CTA, rows of both in shared
+// memory; a thread takes two pairs, 16 apart, by distances 16 apart.  Bound by the loads from shared memory: 16 pairs
+// by 2000 distances of B4 H16 D64 take 11.6 us, half of it the launch (a thread per pair and distance, reading its row of r itself: 125).
+template <int NG>
 __global__ void __launch_bounds__(kThreads) qpos_f32_kernel(const __grid_constant__ QattnParams p)
 {
-    pdl_wait();
+    constexpr int DP = NG * 32, P = DP + 4, TD = NG == 2 ? 64 : 32, PAIRS = 32, UPR = DP / 8;
+    __shared__ __align__(16) float r[TD * P], q[PAIRS * P];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+    const int pair0 = blockIdx.z * PAIRS, pairs = min(PAIRS, p.B * p.L - pair0);
+    const unsigned d0 = blockIdx.x * static_cast<unsigned>(TD);
+    pdl_wait();                                           // as in qpos_kernel
     pdl_launch_dependents();
-    const int delta = blockIdx.x * kThreads + threadIdx.x, h = blockIdx.y;
-    if (delta >= p.n_dist) return;
-    int rr = min(delta, p.C);
-    if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;
-    const float* r = static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head;
-    for (int pr = blockIdx.z; pr < p.B * p.L; pr += gridDim.z) {
-        const int be = pr / p.L, i = pr % p.L;
-        const float* q = static_cast<const float*>(p.q) + be * p.q_sb + i * p.q_st + h * p.q_sh;
-        float s = 0.f;
-        for (int d = 0; d < p.D; ++d) s = fmaf((__ldg(q + d) + __ldg(p.vb + h * p.D + d)) * p.qscale, __ldg(r + d), s);
+#pragma unroll
+    for (int x = tid; x < TD * UPR; x += kThreads) {
+        const int row = x / UPR, d = 8 * (x % UPR);
+        int rr = static_cast<int>(min(d0 + row, static_cast<unsigned>(p.C)));
+        if (rr >= p.n_rows || !in_range(rr, 0, p.n_rows, p.chk)) rr = 0;      // past the distances of the call
+        float v[8];
+        load8<true>(static_cast<const float*>(p.r) + rr * p.r_row + h * p.r_head, d, p.D, p.vec_r, v);
+        put8(r + row * P + d, v);
+    }
+    for (int x = tid; x < pairs * DP; x += kThreads) {
+        const int pr = x / DP, d = x % DP, be = (pair0 + pr) / p.L, i = (pair0 + pr) - be * p.L;
+        const int64_t at = be * p.q_sb + i * p.q_st + h * p.q_sh + d;
+        q[pr * P + d] = d < p.D ? (__ldg(static_cast<const float*>(p.q) + at) + __ldg(p.vb + h * p.D + d)) * p.qscale : 0.f;
+    }
+    __syncthreads();
+    const int qp = (warp & 3) * 4 + (lane >> 3), kq = (warp >> 2) * 8 + (lane & 7);
+    if ((warp & 3) * 4 >= pairs) return;                  // none of this warp's pairs
+    float s[2][TD / 16] = {};
+    const bool both = pairs > 16;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        const float4 q0 = f4(q + qp * P + d);
+#pragma unroll
+        for (int x = 0; x < TD / 16; ++x) s[0][x] = dot4(q0, f4(r + (kq + 16 * x) * P + d), s[0][x]);
+        if (both) {
+            const float4 q1 = f4(q + (qp + 16) * P + d);
+#pragma unroll
+            for (int x = 0; x < TD / 16; ++x) s[1][x] = dot4(q1, f4(r + (kq + 16 * x) * P + d), s[1][x]);
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int pr = qp + 16 * a;
+        if (pr >= pairs) break;
+        const int be = (pair0 + pr) / p.L, i = (pair0 + pr) - be * p.L;
         const int64_t row = (static_cast<int64_t>(be) * p.H + h) * p.L + i;
-        const int x = p.M + i - delta - p.jn;
-        if (x >= 0 && x < p.e_pitch) p.E[row * p.e_pitch + x] = s;
-        if (delta == p.C) p.far[row] = s;
+#pragma unroll
+        for (int x = 0; x < TD / 16; ++x) {
+            const int delta = static_cast<int>(d0 + kq + 16 * x), at = p.M + i - delta - p.jn;
+            if (at >= 0 && delta < p.n_dist) p.E[row * p.e_pitch + at] = s[a][x];
+            if (delta == p.C) p.far[row] = s[a][x];
+        }
     }
 }
 
@@ -936,8 +971,9 @@ cudaError_t launch_qpos(const QattnParams& p, int ng, int sm_count, cudaStream_t
 {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.L;
     if (p.f32) {
-        return launch_dependent(qpos_f32_kernel, dim3((p.n_dist + kThreads - 1) / kThreads, p.H, std::min<int64_t>(pairs, 256)),
-                                dim3(kThreads), 0, s, p);
+        const int td = ng == 2 ? 64 : 32;
+        const dim3 grid((p.n_dist + td - 1) / td, p.H, static_cast<unsigned>((pairs + 31) / 32));
+        return launch_dependent(ng == 2 ? qpos_f32_kernel<2> : qpos_f32_kernel<4>, grid, dim3(kThreads), 0, s, p);
     }
     // four CTAs per SM, each walking over its share of the distances (65536 keys of 16 heads, the whole call:
     // 62.4 us with two, 58.3 with three, 56.0 with four, 58.7 with six)
@@ -1009,11 +1045,11 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     sp.range = static_cast<int>(((keys + sp.ranks - 1) / sp.ranks + ks - 1) / ks * ks);
     if (sp.range == 0) sp.range = ks;
     // Position terms in the kernel itself where a CTA has few: one launch less.  One query of 16 heads, B 1: over 250 keys
-    // 8.1 instead of 10.2 us eagerly (the host), 6.3 instead of 6.0 replayed; over 500 keys 8.4 and 7.8, over 1000
-    // 11.0 instead of 7.3.  fp32, a dot product per thread: one query over 500 keys 10.5 instead of 14.5, four
-    // over 200 keys 15.7 instead of 14.2.
+    // 8.0 instead of 10.2 us eagerly (the host), 6.2 instead of 6.0 replayed; over 500 keys 8.4 and 7.8, over 1000
+    // 11.0 instead of 7.3.  fp32, a dot product per thread: over 250 keys 8.0 instead of 9.6 eagerly, 7.6 instead of
+    // 6.4 replayed; over 500 keys 10.4 instead of 9.8.
     const int64_t near = std::min<int64_t>(sp.range, p.M - p.jn) + p.L;
-    const bool fused = p.f32 ? near * sp.lq <= 512 : near <= 256;
+    const bool fused = (p.f32 ? near * sp.lq : near) <= 256;
     if (!fused) {
         e = launch_qpos(p, NG, sm_count, s);
         if (e != cudaSuccess) return e;

@@ -37,17 +37,6 @@ struct SegSmem {
     float m[kTQ], l[kTQ], alpha[kTQ];
 };
 
-__device__ __forceinline__ float4 f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c)
-{
-    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
-}
-__device__ __forceinline__ void put8(float* dst, const float* x)
-{
-    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-
 template <int NG>
 __global__ void __launch_bounds__(kThreads, NG == 2 ? 2 : 1)
 qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_rank)

@@ -1,4 +1,4 @@
-// txl_rows.cuh -- loads of fp32 or bf16 rows and expansion of codes, shared by the kernels of the quantised memory.
+// txl_rows.cuh -- loads of fp32 or bf16 rows, expansion of codes and products of rows in shared memory, shared by the kernels of the quantised memory.
 #pragma once
 
 #include <cstdint>
@@ -48,6 +48,17 @@ __device__ __forceinline__ void expand8(const uint32_t* code, float step, float 
         const float c = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + (BITS == 4 ? e >> 1 : e & 3))) - kTwo23;
         x[e] = fmaf(step, c, lo);
     }
+}
+
+__device__ __forceinline__ float4 f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c)
+{
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+__device__ __forceinline__ void put8(float* dst, const float* x)
+{
+    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
 }  // namespace txl
