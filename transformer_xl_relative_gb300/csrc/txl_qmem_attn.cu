@@ -141,11 +141,22 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w)
 }
 
 // Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
-// large at 4 bits).
-template <int BITS>
-__device__ __forceinline__ uint32_t pair_even(uint32_t w) { return w & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu); }
-template <int BITS>
-__device__ __forceinline__ uint32_t pair_odd(uint32_t w) { return BITS == 4 ? w & 0x00f000f0u : __byte_perm(w, 0, 0x4341); }
+// large at 4 bits).  The tensor cores align products by the exponents of their operands, in which a subnormal's
+// leading zeros count, and drop what lies some 24 bits below: a code in the lowest bits leaves 15 good bits of a sum (4-bit
+// codes; 19 of 8-bit ones), enough for bf16.  WIDE (fp32 calls): the codes moved up to the highest bits below the
+// exponent, at one shift per pair; 64 c and 4 c.
+template <int BITS, bool WIDE>
+__device__ __forceinline__ uint32_t pair_even(uint32_t w)
+{
+    if constexpr (BITS == 4) return WIDE ? (w << 6) & 0x03c003c0u : w & 0x000f000fu;
+    else return WIDE ? (w << 2) & 0x03fc03fcu : w & 0x00ff00ffu;
+}
+template <int BITS, bool WIDE>
+__device__ __forceinline__ uint32_t pair_odd(uint32_t w)
+{
+    if constexpr (BITS == 4) return WIDE ? (w << 2) & 0x03c003c0u : w & 0x00f000f0u;
+    else return WIDE ? (w >> 6) & 0x03fc03fcu : __byte_perm(w, 0, 0x4341);
+}
 
 // Rows of r of 16 distances from d0 as the A operand's fragments: this lane's of distances g and g + 8.
 template <int NG>
@@ -375,7 +386,7 @@ __device__ __forceinline__ void own_terms(const QattnParams& p, const uint16_t* 
 }
 
 // FUSED: the CTA computes its position terms itself (a variant, because its code costs the others 0.3 us).
-template <int BITS, int NG, int QT, bool ONE, bool FUSED>
+template <int BITS, int NG, int QT, bool ONE, bool FUSED, bool WIDE>
 __global__ void __launch_bounds__(kThreads, NG == 2 || (BITS == 4 && QT == 1) ? 2 : 1)
 qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSplit sp)
 {
@@ -389,6 +400,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per register of codes and product
     constexpr int QP = DP + 8;                            // rows of q's parts: the three that a load of ONE reads
                                                           // (both parts, zeros) lie in different banks
+    constexpr float kCode = WIDE ? (BITS == 4 ? kTwo24 / 64 : kTwo24 / 4) : kTwo24;      // 1 / what a code of one is
+    constexpr float kOdd = BITS == 4 && !WIDE ? 0.0625f : 1.f;                           // of odd channels, besides
     constexpr int kOwn = ONE ? 1 : kDecodeMaxL;           // keys of the segment a query can see
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* stages = smem;
@@ -522,7 +535,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             qu[row * DP + d] = a[e];
             const int at = BITS == 4 ? (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1) : (d & ~3) + ((d & 1) << 1) + ((d >> 1) & 1);
             uint32_t w, unused;
-            split_f16(a[e] * (BITS == 4 && (d & 1) ? up * 0.0625f : up), 0.f, w, unused);
+            split_f16(a[e] * (BITS == 4 && (d & 1) ? up * kOdd : up), 0.f, w, unused);
             quh[2 * row * QP + at] = static_cast<uint16_t>(w);
             quh[(2 * row + 1) * QP + at] = static_cast<uint16_t>(w >> 16);
             float sum = a[e];
@@ -572,7 +585,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             }
         }
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
-        sc[t] = norm[is] * kTwo24;
+        sc[t] = norm[is] * kCode;
 #pragma unroll
         for (int G = 0; G < NG; ++G) qs[t][G] = qsum[is * NG + G];
     }
@@ -647,11 +660,11 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                         for (int s = 0; s < SUB; ++s) {
                             const uint32_t x = wa[w] >> (8 * s), y = wb[w] >> (8 * s);
                             if (c % CPG == 0 && w == 0 && s == 0)
-                                mma_f16_first(acc[0][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
-                                              pair_odd<BITS>(y), bb[2 * s], bb[2 * s + 1]);
+                                mma_f16_first(acc[0][c / CPG], pair_even<BITS, WIDE>(x), pair_even<BITS, WIDE>(y), pair_odd<BITS, WIDE>(x),
+                                              pair_odd<BITS, WIDE>(y), bb[2 * s], bb[2 * s + 1]);
                             else
-                                mma_f16(acc[0][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
-                                        pair_odd<BITS>(y), bb[2 * s], bb[2 * s + 1]);
+                                mma_f16(acc[0][c / CPG], pair_even<BITS, WIDE>(x), pair_even<BITS, WIDE>(y), pair_odd<BITS, WIDE>(x),
+                                        pair_odd<BITS, WIDE>(y), bb[2 * s], bb[2 * s + 1]);
                         }
                     }
                 }
@@ -673,11 +686,11 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
                                 for (int t = 0; t < QT; ++t) {
                                     if (QT > 1 && c % CPG == 0 && s == 0)
-                                        mma_f16_first(acc[t][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y),
-                                                      pair_odd<BITS>(x), pair_odd<BITS>(y), bq[t][ks][0], bq[t][ks][1]);
+                                        mma_f16_first(acc[t][c / CPG], pair_even<BITS, WIDE>(x), pair_even<BITS, WIDE>(y),
+                                                      pair_odd<BITS, WIDE>(x), pair_odd<BITS, WIDE>(y), bq[t][ks][0], bq[t][ks][1]);
                                     else
-                                        mma_f16(acc[t][c / CPG], pair_even<BITS>(x), pair_even<BITS>(y), pair_odd<BITS>(x),
-                                                pair_odd<BITS>(y), on ? bq[t][ks][0] : 0u, on ? bq[t][ks][1] : 0u);
+                                        mma_f16(acc[t][c / CPG], pair_even<BITS, WIDE>(x), pair_even<BITS, WIDE>(y), pair_odd<BITS, WIDE>(x),
+                                                pair_odd<BITS, WIDE>(y), on ? bq[t][ks][0] : 0u, on ? bq[t][ks][1] : 0u);
                                 }
                             }
                         }
@@ -797,8 +810,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                             const uint32_t x = w[2 * half] >> (8 * s), y = w[2 * half + 1] >> (8 * s);
 #pragma unroll
                             for (int t = 0; t < QT; ++t)
-                                mma_f16(o[t][c * SUB + s], pair_even<BITS>(x), pair_odd<BITS>(x), pair_even<BITS>(y),
-                                        pair_odd<BITS>(y), on ? bp[t][G][0] : 0u, on ? bp[t][G][1] : 0u);
+                                mma_f16(o[t][c * SUB + s], pair_even<BITS, WIDE>(x), pair_odd<BITS, WIDE>(x), pair_even<BITS, WIDE>(y),
+                                        pair_odd<BITS, WIDE>(y), on ? bp[t][G][0] : 0u, on ? bp[t][G][1] : 0u);
                         }
                     }
                 }
@@ -873,8 +886,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
         for (int x = 0; x < NG * 2; ++x) {
             // (the unit last: times 2^24 it could leave fp32)
-            ot[2 * x] = fmaf((o[t][x][0] + o[t][x][1]) * kTwo24, rf[t], zt[x >> 1]);
-            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (BITS == 4 ? kTwo24 / 16 : kTwo24), rf[t], zt[x >> 1]);
+            ot[2 * x] = fmaf((o[t][x][0] + o[t][x][1]) * kCode, rf[t], zt[x >> 1]);
+            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (kCode * kOdd), rf[t], zt[x >> 1]);
         }
         float mt = m[t];
         for (int off = Lp; off <= 2; off <<= 1) {
@@ -984,7 +997,7 @@ cudaError_t launch_qpos(const QattnParams& p, int ng, int sm_count, cudaStream_t
     return launch_dependent(kernel, grid, dim3(kThreads), 0, s, p);
 }
 
-template <int BITS, int NG, int QT, bool ONE>
+template <int BITS, int NG, int QT, bool ONE, bool WIDE>
 cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cudaStream_t s)
 {
     constexpr int DP = NG * 32;
@@ -993,8 +1006,8 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
                           4 * kMaxRows * (DP + 8) * 2 + kMaxRows * 4 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
-    auto* kernel = qattn_kernel<BITS, NG, QT, ONE, false>;
-    auto* fused_kernel = qattn_kernel<BITS, NG, QT, ONE, true>;
+    auto* kernel = qattn_kernel<BITS, NG, QT, ONE, false, WIDE>;
+    auto* fused_kernel = qattn_kernel<BITS, NG, QT, ONE, true, WIDE>;
     // once per device: the shared memory, clusters of more than eight, and how many clusters of each size the device
     // holds at a time
     static std::atomic<uint64_t> prepared{0};
@@ -1072,11 +1085,19 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     return cudaLaunchKernelEx(&cfg, fused ? fused_kernel : kernel, p, sp);
 }
 
-template <int BITS, int NG>
+template <int BITS, int NG, bool WIDE>
 cudaError_t launch_qt(const QattnParams& p, const QSplit& sp, int groups, int sm_count, cudaStream_t s)
 {
-    if (sp.lq == 1) return launch<BITS, NG, 1, true>(p, sp, groups, sm_count, s);
-    return sp.lq <= 4 ? launch<BITS, NG, 1, false>(p, sp, groups, sm_count, s) : launch<BITS, NG, 2, false>(p, sp, groups, sm_count, s);
+    if (sp.lq == 1) return launch<BITS, NG, 1, true, WIDE>(p, sp, groups, sm_count, s);
+    return sp.lq <= 4 ? launch<BITS, NG, 1, false, WIDE>(p, sp, groups, sm_count, s)
+                      : launch<BITS, NG, 2, false, WIDE>(p, sp, groups, sm_count, s);
+}
+
+template <int BITS, int NG>
+cudaError_t launch_type(const QattnParams& p, const QSplit& sp, int groups, int sm_count, cudaStream_t s)
+{
+    return p.f32 ? launch_qt<BITS, NG, true>(p, sp, groups, sm_count, s)
+                 : launch_qt<BITS, NG, false>(p, sp, groups, sm_count, s);
 }
 
 }  // namespace
@@ -1087,8 +1108,8 @@ cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s)
     QSplit sp{};
     const int groups = p.L > 8 ? 2 : 1;                   // queries: eight at most per CTA
     sp.lq = (p.L + groups - 1) / groups;
-    if (bits == 4) return ng == 2 ? launch_qt<4, 2>(p, sp, groups, sm_count, s) : launch_qt<4, 4>(p, sp, groups, sm_count, s);
-    return ng == 2 ? launch_qt<8, 2>(p, sp, groups, sm_count, s) : launch_qt<8, 4>(p, sp, groups, sm_count, s);
+    if (bits == 4) return ng == 2 ? launch_type<4, 2>(p, sp, groups, sm_count, s) : launch_type<4, 4>(p, sp, groups, sm_count, s);
+    return ng == 2 ? launch_type<8, 2>(p, sp, groups, sm_count, s) : launch_type<8, 4>(p, sp, groups, sm_count, s);
 }
 
 }  // namespace txl
