@@ -508,8 +508,8 @@ txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
  *            H, D, mem, dtype) bytes (TXL_ERR_WORKSPACE otherwise; may be NULL when that is 0).
  *            Calls that share a workspace must not overlap on the GPU.
  * L <= 16 (generation), two launches, or one where few positions are not clamped: the position terms
- * (q+v).r go into the workspace, then the codes are multiplied as they are, in fp32-like precision (q and
- * the weights held to 22 bits).
+ * (q+v).r go into the workspace, then the codes are multiplied as they are (q and the weights
+ * held to 22 bits; fp32 calls keep fp32's precision, bf16 ones 15 bits).
  * L > 16, bf16, three launches: K and V of the memory's valid positions and of the segment, and r, are
  * written into the workspace once in fp16, in units of powers of two per (b, h) taken from the data,
  * and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16 operands and P, for q,

@@ -161,6 +161,20 @@ def test_few_queries_match_64_bits(txl, c, bits):
         assert torch.isnan(gap).all()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("c", [(10, 2, 64, 3, 358), (2, 2, 8, 8, 1377), (1, 2, 128, 1, 4653), (1, 3, 41, 7, 8938)])
+def test_fp32_keeps_its_bits(txl, c, bits):
+    """The parts of q and of the weights are off by 2^-23 of themselves, the exponential by 2^-22: a term of the
+    sums by less than 2^-20.  The sums average such errors, and the codes are centred, so that terms do not cancel
+    more than the values themselves do; another factor of two is for the roundings of the sums."""
+    B, H, D, L, M = c
+    call = Call(txl, B, H, D, L, M, M, 5, 1000, bits, "f32")
+    call.run(txl)
+    torch.cuda.synchronize()
+    ref, _, _ = call.reference()
+    assert np.linalg.norm(f64(call.out) - ref) <= 2.0 ** -19 * np.linalg.norm(ref)
+
+
 def test_a_given_scale(txl):
     call = Call(txl, 2, 2, 64, 1, 200, 200, 9, 1000, 4, "bf16")
     call.run(txl, scale=0.31)

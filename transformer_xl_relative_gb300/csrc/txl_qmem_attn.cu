@@ -140,22 +140,30 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 }
 
-// Pairs of codes of a register as fp16 subnormals; odd = the second pair of a 16-bit half (16 times as
-// large at 4 bits).  The tensor cores align products by the exponents of their operands, in which a subnormal's
-// leading zeros count, and drop what lies some 24 bits below: a code in the lowest bits leaves 15 good bits of a sum (4-bit
-// codes; 19 of 8-bit ones), enough for bf16.  WIDE (fp32 calls): the codes moved up to the highest bits below the
-// exponent, at one shift per pair; 64 c and 4 c.
+// Pairs of codes of a register as fp16 numbers; odd = the second pair of a 16-bit half (16 times as large at 4 bits).
+// As subnormals, c 2^-24, for bf16 calls: one AND.  The tensor cores align products by the exponents of their operands,
+// in which a subnormal's leading zeros count, and drop what lies some 24 bits below, so that sums keep 15 good bits (of
+// 4-bit codes; 19 of 8-bit ones).  WIDE, for fp32 calls: c - c0 (8, 128) exactly, by way of 1024 + c, and lo + c0 step in
+// place of lo; besides the bits this keeps the sums of codes and of lo from cancelling (those alone left errors of 1e-6 to 1e-5; now 1e-7 to 4e-7).
+template <int BITS> constexpr float kCentre = BITS == 4 ? 8.f : 128.f;
+
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("add.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 template <int BITS, bool WIDE>
 __device__ __forceinline__ uint32_t pair_even(uint32_t w)
 {
-    if constexpr (BITS == 4) return WIDE ? (w << 6) & 0x03c003c0u : w & 0x000f000fu;
-    else return WIDE ? (w << 2) & 0x03fc03fcu : w & 0x00ff00ffu;
+    const uint32_t c = w & (BITS == 4 ? 0x000f000fu : 0x00ff00ffu);
+    return WIDE ? add_f16x2(c | 0x64006400u, BITS == 4 ? 0xe408e408u : 0xe480e480u) : c;      // less 1032, 1152
 }
 template <int BITS, bool WIDE>
 __device__ __forceinline__ uint32_t pair_odd(uint32_t w)
 {
-    if constexpr (BITS == 4) return WIDE ? (w << 2) & 0x03c003c0u : w & 0x00f000f0u;
-    else return WIDE ? (w >> 6) & 0x03fc03fcu : __byte_perm(w, 0, 0x4341);
+    const uint32_t c = BITS == 4 ? w & 0x00f000f0u : __byte_perm(w, 0, 0x4341);
+    return WIDE ? add_f16x2(c | 0x64006400u, 0xe480e480u) : c;                                // less 1152
 }
 
 // Rows of r of 16 distances from d0 as the A operand's fragments: this lane's of distances g and g + 8.
@@ -400,8 +408,13 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     constexpr int SUB = BITS == 4 ? 2 : 1;                // MMAs per register of codes and product
     constexpr int QP = DP + 8;                            // rows of q's parts: the three that a load of ONE reads
                                                           // (both parts, zeros) lie in different banks
-    constexpr float kCode = WIDE ? (BITS == 4 ? kTwo24 / 64 : kTwo24 / 4) : kTwo24;      // 1 / what a code of one is
-    constexpr float kOdd = BITS == 4 && !WIDE ? 0.0625f : 1.f;                           // of odd channels, besides
+    constexpr float kCode = WIDE ? 1.f : kTwo24;           // 1 / what a code of one is
+    constexpr float kOdd = BITS == 4 ? 0.0625f : 1.f;     // and of odd channels, besides
+    // of a parameter word (step, lo)
+    auto lo_of = [](uint32_t w) {
+        const float lo = __uint_as_float(w & 0xffff0000u);
+        return WIDE ? fmaf(__uint_as_float(w << 16), kCentre<BITS>, lo) : lo;
+    };
     constexpr int kOwn = ONE ? 1 : kDecodeMaxL;           // keys of the segment a query can see
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* stages = smem;
@@ -733,7 +746,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
                         d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], __uint_as_float(par[x][G].x << 16), d);
-                        a = fmaf(__uint_as_float(par[x][G].x & 0xffff0000u), qs[t][G], a);
+                        a = fmaf(lo_of(par[x][G].x), qs[t][G], a);
                     }
                     s[x] = live[x] ? fmaf(d, sc[t], a) : -INFINITY;
                     pr[x] = ex2_approx(s[x] - m[t]);
@@ -784,8 +797,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                 l[t] += pr[0] + pr[1];
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
-                    z[t][G] = fmaf(pr[0], __uint_as_float(par[0][G].y & 0xffff0000u),
-                                   fmaf(pr[1], __uint_as_float(par[1][G].y & 0xffff0000u), z[t][G]));
+                    z[t][G] = fmaf(pr[0], lo_of(par[0][G].y), fmaf(pr[1], lo_of(par[1][G].y), z[t][G]));
                     // row = key, columns (2 slot, 2 slot + 1) -> rows = columns of B, pairs of keys
                     uint32_t w0, w1;
                     split_f16(w[0][G], w[1][G], w0, w1);
