@@ -553,8 +553,8 @@ size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qm
 
 /* Which kernels txl_rel_attn_qmem would run for these arguments: 5 = the one that multiplies the codes
  * (L <= 16), 6 = the fp32 one of longer segments, 1 = the expanded memory, then the tcgen05 kernels, 1 or
- * 2 = the kernel of txl_rel_attn_path for a bf16 call without valid positions, or a negative txl_status if
- * the arguments are rejected.  Nothing is launched; the workspace is not checked. */
+ * 2 = the kernel of txl_rel_attn_path for a bf16 call without a memory, or a negative txl_status if the
+ * arguments are rejected.  Nothing is launched; the workspace is not checked. */
 int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem,
                            const txl_view* k_cur, const txl_view* v_cur, const void* r,
                            int64_t ld_r, const txl_view* out, txl_dtype dtype);

@@ -1169,7 +1169,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
     if (st != TXL_OK) return -static_cast<int>(st);
     if (L <= kDecodeMaxL) return 5;
     if (dtype == TXL_F32) return 6;
-    if (!mem || mem->valid == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
+    if (!mem || mem->M == 0) return txl_rel_attn_path(B, L, H, D, q, nullptr, k_cur, v_cur, r, ld_r, out, dtype);
     return 1;
 }
 
@@ -1191,7 +1191,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
     const size_t need = txl_rel_attn_qmem_workspace_size(B, L, H, D, mem, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need || !a16(workspace))) return TXL_ERR_WORKSPACE;
     if (L > kDecodeMaxL && dtype == TXL_BF16) {
-        if (valid == 0)
+        if (M == 0)
             return txl_rel_attn_fwd(B, L, H, D, clamp_len, q, nullptr, k_cur, v_cur, u, v_bias, r, ld_r, n_rows, scale,
                                     out, dtype, nullptr, 0, err_flag, stream);
         if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));

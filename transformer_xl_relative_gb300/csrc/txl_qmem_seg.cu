@@ -128,7 +128,7 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
         }
         __syncthreads();
 
-        float s[2][4] = {};
+        float s[2][4] = {}, e[2][4] = {};                   // summed apart: half the roundings
 #pragma unroll 2
         for (int d = 0; d < S::DP; d += 4) {
             float4 qu[2], qv[2], r[5];
@@ -143,7 +143,10 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
             for (int x = 0; x < 4; ++x) {
                 const float4 k = f4(sm.k + (kq + 16 * x) * P + d);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) s[a][x] = dot4(qv[a], r[a - x + 3], dot4(qu[a], k, s[a][x]));
+                for (int a = 0; a < 2; ++a) {
+                    s[a][x] = dot4(qu[a], k, s[a][x]);
+                    e[a][x] = dot4(qv[a], r[a - x + 3], e[a][x]);
+                }
             }
         }
 #pragma unroll
@@ -151,7 +154,7 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int ii = qp + 16 * a, kk = kq + 16 * x;
-                sm.s[ii * kSPitch + kk] = j0 + kk <= p.M + i0 + ii && j0 + kk < end ? s[a][x] : -INFINITY;
+                sm.s[ii * kSPitch + kk] = j0 + kk <= p.M + i0 + ii && j0 + kk < end ? s[a][x] + e[a][x] : -INFINITY;
             }
         __syncthreads();
 #pragma unroll
@@ -183,8 +186,9 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
 #pragma unroll
             for (int x = 0; x < NG / 2; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[a][x][e] *= scale;
+                for (int y = 0; y < 4; ++y) o[a][x][y] *= scale;
         }
+        float ot[2][NG / 2][4] = {};                        // of this tile: sums of 64 terms, then of tiles
         const bool whole = j0 + kTK - 1 <= p.M + i0;        // no key is masked for any query
 #pragma unroll 4
         for (int kk = 0; kk < kTK; kk += 4) {
@@ -205,10 +209,16 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
                         // a value that the query does not see may be infinite or NaN
                         const bool seen = whole || j0 + kk + y <= p.M + i0 + qp + 16 * a;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[a][x][e] = seen ? fmaf(pr[a][y], vv[e], o[a][x][e]) : o[a][x][e];
+                        for (int d = 0; d < 4; ++d) ot[a][x][d] = seen ? fmaf(pr[a][y], vv[d], ot[a][x][d]) : ot[a][x][d];
                     }
                 }
         }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int x = 0; x < NG / 2; ++x)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) o[a][x][d] += ot[a][x][d];
     }
 
     // ---- join the ranks: each leaves its output in its shared memory, row ii is finished by rank ii mod ranks
