@@ -510,11 +510,14 @@ txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
  * L <= 16 (generation), two launches, or one where few positions are not clamped: the position terms
  * (q+v).r go into the workspace, then the codes are multiplied as they are (q and the weights
  * held to 22 bits; fp32 calls keep fp32's precision, bf16 ones 15 bits).
- * L > 16, bf16, three launches: K and V of the memory's valid positions and of the segment, and r, are
- * written into the workspace once in fp16, in units of powers of two per (b, h) taken from the data,
- * and the fused tcgen05 kernels of txl_rel_attn_fwd run over them with fp16 operands and P, for q,
- * k_cur, v_cur and r of any layout.  (Queries that would bring scores past fp16's range, 65504, are held
- * at it.)
+ * L > 16, bf16, four launches (three for D > 64): K and V of the memory's valid positions and of the segment,
+ * and r, are written into the workspace once in 16 bits, and the fused tcgen05 kernels of txl_rel_attn_fwd run
+ * over them, for q, k_cur, v_cur and r of any layout.  A (b, h) has fp16 operands and P, in units of powers of
+ * two taken from the data, where fp16 has the range: all its values are finite, D times a bound of
+ * |scale log2(e) (q+u)| times the largest |k'| is at most 2^15, the same for (q+v) and the head's r, and the
+ * largest |v'| is at most 2^12 times the smallest that a group of 32 channels which is not zero has as its
+ * largest.  Otherwise it has bf16 ones, as in txl_rel_attn_fwd.  (Where r's rows do not start on 16-byte
+ * boundaries, all entries of a head have one type.)
  * L > 16, fp32, one launch: codes are expanded tile by tile in shared memory, all arithmetic in fp32.
  * err_flag as for txl_rel_attn_fwd: every kernel that waits for copies sets it if a wait runs out.
  */

@@ -1,0 +1,210 @@
+"""GPU tests of txl_rel_attn_qmem on values of unlike size: infinities and NaN, elements far above or
+below the rest of their head.  References in 64 bits over what the memory stands for."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from qmem_common import f64
+from test_gpu_qmem_attn import Call
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def txl():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import transformer_xl_relative_gb300 as m
+    return m
+
+
+def attend(q, k, v, u, vb, r, C):
+    """out [B, L, H, D] by the formula, and s2 as segment_tolerance counts it: out_i is a sum over the keys
+    that query i sees, so that what it does not see may be anything.  Also the variance var of an output
+    whose operands, position terms and weights each deviate by 1 of their value, independently (values that
+    are not finite apart)."""
+    B, L, H, D = q.shape
+    K = k.shape[1]
+    delta = K - L + np.arange(L)[:, None] - np.arange(K)[None]
+    seen, row = delta >= 0, np.clip(delta, 0, C)
+    out, var = np.empty((B, L, H, D)), np.empty((B, L, H, D))
+
+    def finite(x):
+        return np.where(np.isfinite(x), x, 0.0)
+
+    with np.errstate(all="ignore"):
+        for b in range(B):
+            for h in range(H):
+                qu, qv, kk, vv, rr = q[b, :, h] + u[h], q[b, :, h] + vb[h], k[b, :, h], v[b, :, h], r[:, h, :D]
+                s = (qu @ kk.T + np.take_along_axis(qv @ rr.T, row, 1)) * D ** -0.5
+                s = np.where(seen, s, -np.inf)
+                p = np.exp(s - s.max(-1, keepdims=True))
+                p /= p.sum(-1, keepdims=True)
+                o = p @ finite(vv)
+                for j, d in np.argwhere(~np.isfinite(vv)):
+                    o[:, d] = np.where(seen[:, j], o[:, d] + p[:, j] * vv[j, d], o[:, d])
+                out[b, :, h] = o
+                p, o, vv = finite(p), finite(o), finite(vv)
+                qu, qv, kk, rr = finite(qu), finite(qv), finite(kk), finite(rr)
+                bd = np.take_along_axis(qv @ rr.T, row, 1)
+                s2 = (2 * (qu ** 2) @ (kk ** 2).T + np.take_along_axis((qv ** 2) @ (rr ** 2).T, row, 1) + bd ** 2) / D
+                w = p ** 2 * s2
+                var[b, :, h] = w @ vv ** 2 - 2 * (w @ vv) * o + w.sum(-1, keepdims=True) * o ** 2 + 2 * (p ** 2) @ vv ** 2
+    return out, np.maximum(var, 0)
+
+
+def check(call, rows=slice(None)):
+    """NaN and infinities where the formula has them; elsewhere at most six deviations of operands, position
+    terms and weights rounded to bf16 (2^-8 of the value, uniform: 2^-8 / sqrt(3)) and the output's own
+    rounding, half a step, 2^-8 of its value: what any of the segment kernels keeps."""
+    ref, var = attend(*call.operands_as_given(), call.C)
+    ref, var, out = ref[:, rows], var[:, rows], f64(call.out)[:, rows]
+    assert np.array_equal(np.isnan(out), np.isnan(ref)), np.argwhere(np.isnan(out) != np.isnan(ref))[:5]
+    inf = np.isinf(ref)
+    assert np.array_equal(np.isinf(out), inf) and np.array_equal(out[inf], ref[inf])
+    ok = np.isfinite(ref)
+    err = np.abs(np.where(ok, out, 0) - np.where(ok, ref, 0))
+    tol = 2.0 ** -8 * np.abs(np.where(ok, ref, 0)) + 6 * 2.0 ** -8 / np.sqrt(3) * np.sqrt(var)
+    assert (err <= tol)[ok].all(), float((err / np.maximum(tol, 1e-300))[ok].max())
+
+
+class Ranged(Call):
+    def operands_as_given(self):
+        """As operands(), with r's channels as they are (its padding is not read)."""
+        q, k, v, u, vb, _ = self.operands()
+        return q, k, v, u, vb, f64(self.r[..., :self.dims[3]])
+
+    def push_again(self, txl, wp):
+        M = self.mem.M
+        self.mem.restore((wp - self.kh.shape[1]) % M, 0)
+        txl.qmem_push(self.mem, self.kh.cuda(), self.vh.cuda())
+
+    def go(self, txl):
+        self.run(txl)
+        torch.cuda.synchronize()
+
+
+def segment(txl, D, L=40, M=200, bits=8, dtype="bf16", C=1000, **kw):
+    return Ranged(txl, 2, 2, D, L, M, M, 9, C, bits, dtype, **kw)
+
+
+WHERE = ["q", "first own key", "first own value", "position row", "clamped position row", "memory key", "memory value"]
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN], ids=str)
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("where", WHERE)
+def test_segment_values_that_are_not_finite(txl, where, D, value):
+    """One element that is not finite and that every query sees (of q: its own row) does to a bf16 segment
+    what the formula says, and nothing to the other heads and entries."""
+    call = segment(txl, D, C=100 if where.startswith("clamped") else 1000)
+    if where == "q":
+        call.q[1, 20, 0, 3] = value
+    elif where == "first own key":
+        call.k[1, 0, 0, 3] = value
+    elif where == "first own value":
+        call.v[1, 0, 0, 3] = value
+    elif where == "position row":
+        call.r[3, 1, 5] = value
+    elif where == "clamped position row":
+        call.r[100, 1, 5] = value
+    else:
+        (call.kh if where == "memory key" else call.vh)[1, 77, 0, 3] = value
+        call.push_again(txl, 9)
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("where", ["memory", "own"])
+def test_segment_large_key_in_a_channel_without_query(txl, where, D):
+    """A key of 2^17 in a channel where the queries are 0: scores of ordinary size."""
+    call = segment(txl, D)
+    call.q[..., 40], call.u[:, 40], call.vb[:, 40] = 0, 0, 0
+    if where == "own":
+        call.k[0, 0, 0, 40] = 2.0 ** 17
+    else:
+        call.kh[0, 33, 0, 40] = 2.0 ** 17
+        call.push_again(txl, 9)
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("D", [64, 96])
+def test_segment_large_position_in_a_channel_without_query(txl, D):
+    call = segment(txl, D)
+    call.q[..., 40], call.u[:, 40], call.vb[:, 40] = 0, 0, 0
+    call.r[7, 0, 40] = 2.0 ** 17
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_segment_large_values_that_no_query_sees_yet(txl, what, D):
+    """Own keys or values of 2^40 behind position 30: the queries before them do not see them."""
+    call = segment(txl, D)
+    getattr(call, what)[:, 30:] *= 2.0 ** 40
+    call.go(txl)
+    check(call, slice(0, 30))
+
+
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("octaves,score", [(34, -40.0), (23, -16.0)])
+def test_segment_large_value_with_little_weight(txl, D, octaves, score):
+    """A position whose value is 2^octaves times the others' and whose weight is about e^score of theirs."""
+    call = segment(txl, D)
+    q = call.q[:, :1, :].float() + call.u
+    call.q.copy_(call.q[:, :1].clone().expand_as(call.q))
+    t = score * D ** 0.5 / (q ** 2).sum(-1, keepdim=True)
+    call.kh[:, 50] = (q * t)[:, 0].cpu().to(call.dtype)
+    call.vh[:, 50] *= 2.0 ** octaves
+    call.push_again(txl, 9)
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("D", [64, 96])
+def test_segment_value_channels_of_unlike_size(txl, D):
+    """Channels 32 .. 63 of the values 2^40 times smaller than the others."""
+    call = segment(txl, D)
+    call.vh[..., 32:64] *= 2.0 ** -40
+    call.v[..., 32:64] *= 2.0 ** -40
+    call.push_again(txl, 9)
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("B,H,L,D", [(40, 8, 20, 64), (30, 4, 300, 41), (3, 2, 200, 96)])
+def test_segment_heads_of_either_kind(txl, B, H, L, D):
+    """Heads with a large key, large values or an infinity between ordinary ones, more of them than multiprocessors."""
+    call = Ranged(txl, B, H, D, L, 60, 60, 9, 1000, 8, "bf16")
+    call.q[..., 20], call.u[:, 20], call.vb[:, 20] = 0, 0, 0
+    g = torch.Generator().manual_seed(B)
+    kind = torch.randint(0, 6, (B, H), generator=g)
+    for b, h in torch.argwhere(kind < 3).tolist():
+        if kind[b, h] == 0:
+            call.kh[b, 33, h, 20] = 2.0 ** 17
+        elif kind[b, h] == 1:
+            call.v[b, L // 2, h] *= 2.0 ** 20
+        else:
+            call.v[b, 0, h, 3] = INF
+    call.push_again(txl, 9)
+    call.go(txl)
+    check(call)
+
+
+@pytest.mark.parametrize("D", [41, 64, 96])
+def test_segment_heads_of_either_kind_without_a_loadable_table(txl, D):
+    """The same where r's rows do not start on 16-byte boundaries."""
+    call = segment(txl, D)
+    flat = torch.empty(call.r.numel() + 1, dtype=torch.bfloat16, device="cuda")
+    flat[1:].copy_(call.r.reshape(-1))
+    call.r = flat[1:].view(call.r.shape)
+    call.v[0, 5, 1] *= 2.0 ** 20
+    call.go(txl)
+    check(call)

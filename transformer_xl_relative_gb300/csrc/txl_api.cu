@@ -244,7 +244,7 @@ txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_v
                           const txl_view* k_cur, const txl_view* v_cur, const float* u, const float* v_bias,
                           const void* r, int64_t ld_r, int n_rows, float scale, const txl_view* out, int* err_flag,
                           cudaStream_t s, int ring_slots, float* lse = nullptr, int lse_out = 0,
-                          const float* units = nullptr)
+                          const float* units = nullptr, const void* r_bf16 = nullptr, int64_t ld_rb = 0)
 {
     const int M = (mem && mem->M > 0) ? mem->M : 0;
     const int valid = M > 0 ? mem->valid : 0;
@@ -271,6 +271,7 @@ txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_v
             p.tm_vmem = p.tm_vcur;
         }
     }
+    if (ok && units) ok = encode_rtab(&p.tm_rb, r_bf16, D, H, n_rows, ld_rb);
     if (!ok) return TXL_ERR_CUDA;
     p.u = u;
     p.vb = v_bias;
@@ -1213,6 +1214,10 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
         e.ld_r = ld_r;
         e.n_r = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(valid) + L, static_cast<int64_t>(clamp_len) + 1));
         e.vec_v = rows16(v_cur); e.vec_k = rows16(k_cur); e.vec_q = rows16(q); e.vec_r = a16(r) && s16(ld_r, 2);
+        e.u = u;
+        e.vb = v_bias;
+        e.qscale = scale * 1.4426950408889634f;
+        e.r_alone = !e.vec_r;
         e.k_mem = m.k;
         e.v_mem = m.v;
         uint16_t* at = static_cast<uint16_t*>(m.v) + static_cast<int64_t>(B) * H * valid * ld;
@@ -1227,10 +1232,10 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
         e.r16 = at + 3 * seg;
         e.units = reinterpret_cast<float*>(at + 3 * seg + static_cast<int64_t>(e.n_r) * H * ld);
         e.chk = range_counter();
-        e.absmax = e.units + static_cast<int64_t>(B) * H * 4;
+        e.ranges = reinterpret_cast<uint32_t*>(e.units + static_cast<int64_t>(B) * H * 4);
         if (launch_qmem_expand(e, s) != cudaSuccess) return TXL_ERR_CUDA;
         return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
-                              err_flag, s, 0, nullptr, 0, e.units);
+                              err_flag, s, 0, nullptr, 0, e.units, e.r_alone ? e.r16 : r, e.r_alone ? ld : ld_r);
     }
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
     QattnParams p;

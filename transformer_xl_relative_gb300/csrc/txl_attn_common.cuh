@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 
+#include "txl_internal.h"
 #include "txl_ptx.cuh"
 
 namespace txl {
@@ -15,6 +16,20 @@ constexpr int kBdPitchWords = 132;           // per-row ring of 256 bf16 + 4 exc
 constexpr int kBdBytes = 128 * kBdPitchWords * 4;
 constexpr uint32_t kColS0 = 0, kColS1 = 128, kColBD = 256, kColO = 384;
 constexpr uint32_t kColP = 448;             // P of the current tile when D <= 64 (see kSeparateP)
+// Where the operands come from, and their type: the caller's tensors, bf16; or an expanded memory (p.units), of a
+// (b, h) with fp16 operands or of one with bf16 ones.
+enum Operands { kOpsGiven, kOpsF16, kOpsBf16 };
+
+// Whether the operands of (b, h) of an expanded memory are fp16.  (Not through the read-only path: the kernel
+// before may write the units while this one starts.)
+__device__ __forceinline__ bool operands_f16(const AttnTcParams& p, int b, int h)
+{
+    return __ldcg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h)) > 0.f;
+}
+
+// Whether any (b, h) has bf16 ones.
+__device__ __forceinline__ bool any_bf16(const AttnTcParams& p) { return __ldcg(p.units + 3) != 0.f; }
+
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P values stay below 2^8
 
 __device__ __forceinline__ int query_of_row(int li) { return 2 * (li & 63) + (li >> 6); }
@@ -24,8 +39,9 @@ __device__ __forceinline__ void pair_bar(int li) { named_bar_sync(2 + (li >> 5),
 
 // ---------------------------------------------------------------------------------------------
 // Logits of one thread's 64 columns of a tile (log2 domain): s = AC + BD(remapped), in place,
-// returning their maximum.  kF16: the ring holds fp16 instead of bf16.  The ring already carries the mask (-inf) and the clamp (the value of
-// r[clamp_len]) in the positions concerned, so every tile runs this one branch-free loop.
+// returning their maximum.  kF16: the ring holds fp16 instead of bf16.  The ring already carries the mask
+// (-inf) and the clamp (the value of r[clamp_len]) in the positions concerned, so every tile runs this one
+// branch-free loop.
 template <bool kF16 = false>
 __device__ __forceinline__ float logits_interior(float* s, const uint32_t* bdrow, int wbase)
 {
@@ -49,7 +65,7 @@ __device__ __forceinline__ float logits_interior(float* s, const uint32_t* bdrow
 
 // A pair of position terms as the ring holds them, and -inf in both halves of a word.
 template <bool kF16>
-__device__ __forceinline__ uint32_t ring_pair(float lo, float hi) { return kF16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi); }
+__device__ __forceinline__ uint32_t ring_pair(float lo, float hi) { return kF16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); }
 template <bool kF16> constexpr uint32_t kRingNegInf = kF16 ? 0xFC00FC00u : 0xFF80FF80u;
 
 // Copy this thread's half of a new BD chunk (64 fp32 columns, in registers) into the row's ring

@@ -137,6 +137,19 @@ __device__ __forceinline__ bool item_at(const AttnTcParams& p, const int* first,
     return true;
 }
 
+// The first of this CTA's items from the x-th on that a kernel of kOps computes.
+template <bool kTab, int kOps>
+__device__ __forceinline__ bool next_item(const AttnTcParams& p, const int* first, const int* count, int& x, Item& it)
+{
+    if constexpr (kOps == kOpsBf16) {
+        for (; item_at<kTab>(p, first, count, x, it); ++x)
+            if (!operands_f16(p, it.b, it.h)) return true;
+        return false;
+    } else {
+        return item_at<kTab>(p, first, count, x, it);
+    }
+}
+
 __device__ __forceinline__ bool need_chunk(int t, int C) { return 128 * t < C; }
 
 // Key tile t of an item covers keys j0 = M + i0 - 128 t; memory keys come from the ring slot
@@ -178,17 +191,25 @@ constexpr uint16_t kMaskedKeyBf16 = 0xF14A;
 
 // kLse = 1: the row statistics alone (log-sum-exp for the gradient kernels): no output is written.
 // kLse = 2: the forward output and, besides it, every row's log-sum-exp.
-// kF16 (operands read back from a quantised memory): K, V, r, c(q + u), c(q + v), the position ring and
-// P are fp16, K, V and r in units of powers of two per (b, h) (p.units).  Operands, the argument of the
-// exponential and P keep 11 bits instead of 8, at the same time (B16 H16 D64 L384 M384: 67 us cold).
-template <bool kTab, bool kMask = false, int kLse = 0, bool kF16 = false>
+// kOps: with operands of an expanded memory, K, V, r, c(q + u), c(q + v), the position ring and P of a (b, h) are
+// fp16, K, V and r in units of powers of two, or bf16 where its values do not have the range for that.  In fp16,
+// operands, the argument of the exponential and P keep 11 bits instead of 8, at the same time (B16 H16 D64 L384
+// M384: 67 us cold).  A launch for either type: with both forms of the softmax in one kernel it took 79 to 83 us.  The
+// one for fp16 walks over all items and leaves out the results of those with bf16 operands (leaving out the items
+// cost 4 us, in the loops of every role); the one for bf16 walks over those, or ends at once.
+template <bool kTab, bool kMask = false, int kLse = 0, int kOps = kOpsGiven>
 __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid_constant__ AttnTcParams p)
 {
     constexpr int NPV = 64;
+    constexpr bool kF16 = kOps == kOpsF16;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
+    if constexpr (kOps == kOpsBf16) {
+        pdl_wait();
+        if (!any_bf16(p)) return;
+    }
     if ((smem_u32(smem) & 1023u) != 0) {
         pdl_wait();
         if (tid == 0 && p.err_flag) atomicCAS(p.err_flag, 0, TXL_ERR_ALIGNMENT);
@@ -265,12 +286,13 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 const int s = rc % kNR;
                 if (!mbar_wait(&bar.r_empty[s], ((rc / kNR) & 1) ^ 1, wc, 10)) return false;
                 mbar_expect_tx(&bar.r_full[s], kTile);
-                tma_load_3d(smem + PSmem::R + s * kTile, &p.tm_r, 0, h, row0, &bar.r_full[s]);
+                tma_load_3d(smem + PSmem::R + s * kTile, kOps == kOpsBf16 ? &p.tm_rb : &p.tm_r, 0, h, row0,
+                            &bar.r_full[s]);
                 ++rc;
                 return true;
             };
             Item it;
-            for (int n = 0; ok && item_at<kTab>(p, sched_first, sched_count, n, it); ++n) {
+            for (int n = 0, x = 0; ok && next_item<kTab, kOps>(p, sched_first, sched_count, x, it); ++n, ++x) {
                 // raw q rows in TMEM-lane order: even queries of the tile to rows 0-63, odd
                 // queries to rows 64-127 (the even and odd row maps both step two tokens per row)
                 const int qb = n & 1;
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
         const int c = lane & 7;
         bool ok = true;
         Item it;
-        for (int n = 0; ok && item_at<kTab>(p, sched_first, sched_count, n, it); ++n) {
+        for (int n = 0, x = 0; ok && next_item<kTab, kOps>(p, sched_first, sched_count, x, it); ++n, ++x) {
             const int qb = n & 1;
             float us[8], vs[8];
 #pragma unroll
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
             uint64_t sc2 = f2_pack(p.qscale, p.qscale), sc2u = sc2;      // of Qv and Qu
             if constexpr (kF16) {                           // times the units of r and K
                 const float* un = p.units + 4 * (static_cast<int64_t>(it.b) * p.H + it.h);
-                const float ku = __ldg(un), ru = __ldg(un + 2);
+                const float ku = __ldcg(un), ru = __ldcg(un + 2);
                 sc2u = f2_pack(p.qscale * ku, p.qscale * ku);
                 sc2 = f2_pack(p.qscale * ru, p.qscale * ru);
 #pragma unroll
@@ -352,8 +374,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                     float a0, a1, b0, b1;
                     f2_unpack(f2_fma(q2, sc2u, f2_pack(us[2 * e], us[2 * e + 1])), a0, a1);
                     f2_unpack(f2_fma(q2, sc2, f2_pack(vs[2 * e], vs[2 * e + 1])), b0, b1);
-                    wu[e] = kF16 ? pack_f16x2_sat(a0, a1) : pack_bf16x2(a0, a1);
-                    wv[e] = kF16 ? pack_f16x2_sat(b0, b1) : pack_bf16x2(b0, b1);
+                    wu[e] = kF16 ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
+                    wv[e] = kF16 ? pack_f16x2(b0, b1) : pack_bf16x2(b0, b1);
                 }
                 *reinterpret_cast<uint4*>(qu + off) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
                 *reinterpret_cast<uint4*>(qv + off) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
@@ -412,7 +434,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 return true;
             };
             Item it;
-            for (int n = 0; ok && item_at<kTab>(p, sched_first, sched_count, n, it); ++n) {
+            for (int n = 0, x = 0; ok && next_item<kTab, kOps>(p, sched_first, sched_count, x, it); ++n, ++x) {
                 const int qb = n & 1;
                 if (!(ok = mbar_wait(&bar.q_ready[qb], (n >> 1) & 1, wc, 20))) break;
                 tc_fence_after();
@@ -446,19 +468,21 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
             const uint32_t b_vempty = smem_u32(bar.v_empty), b_pvdone = smem_u32(bar.pv_done);
             // two cursors over the flattened (item, tile) sequence: V loads run one tile ahead
             struct Cursor {
-                int n, t;
+                int n, x, t;                 // n-th item, the CTA's x-th; tile
                 Item it;
                 bool valid;
             };
             auto advance = [&](Cursor& cu) {
                 if (++cu.t >= cu.it.n_t) {
                     ++cu.n;
+                    ++cu.x;
                     cu.t = 0;
-                    cu.valid = item_at<kTab>(p, sched_first, sched_count, cu.n, cu.it);
+                    cu.valid = next_item<kTab, kOps>(p, sched_first, sched_count, cu.x, cu.it);
                 }
             };
             Cursor ld, cs;
-            ld.n = 0; ld.t = 0; ld.valid = item_at<kTab>(p, sched_first, sched_count, 0, ld.it);
+            ld.n = 0; ld.x = 0; ld.t = 0;
+            ld.valid = next_item<kTab, kOps>(p, sched_first, sched_count, ld.x, ld.it);
             cs = ld;
             int vc = 0, T = 0;
             bool ok = true;
@@ -522,7 +546,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
         bool ok = true;
         int T = 0, bd = 0;                           // tiles and BD products consumed so far
         Item it;
-        for (int n = 0; item_at<kTab>(p, sched_first, sched_count, n, it); ++n) {
+        for (int n = 0, x = 0; next_item<kTab, kOps>(p, sched_first, sched_count, x, it); ++n, ++x) {
             const int M = p.M;
             float m_run = -INFINITY, l_half = 0.f;
             uint32_t bdc_bits = 0;                  // fp32 bits of (q+v).r[clamp_len] for this row
@@ -662,7 +686,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                     float alpha = 1.f;
                     bool rescale_o = false;
                     if (t == 0) {
-                        m_run = mt;
+                        // (kOpsBf16: a query may see only keys of -inf in this tile)
+                        m_run = kOps == kOpsBf16 ? fmaxf(mt, -3e38f) : mt;
                     } else if (mt > m_run + kRescaleThreshold) {
                         alpha = ex2_approx(m_run - mt);
                         m_run = mt;
@@ -753,6 +778,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
             xchg[2 * (it.n_t & 1) + hf] = l_half;
             pair_bar(li);
             const bool staged = p.out_a16 != 0;
+            bool stored = true;                             // kOpsF16: not if the operands are bf16
             if (ok && kLse == 1) {
                 // log2-domain log-sum-exp of the row, in the scaled score units of the logits
                 __syncwarp();
@@ -770,7 +796,12 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 __syncwarp();
                 mbar_arrive_if(bar.o_free, lane == 0);
                 float inv_l = rcp_approx(l_half + xchg[2 * (it.n_t & 1) + (hf ^ 1)]);
-                if constexpr (kF16) inv_l *= __ldg(p.units + 4 * (static_cast<int64_t>(it.b) * p.H + it.h) + 1);
+                if constexpr (kOps != kOpsGiven) {
+                    const float2 un = __ldcg(reinterpret_cast<const float2*>(p.units) +
+                                             2 * (static_cast<int64_t>(it.b) * p.H + it.h));
+                    inv_l *= un.y;
+                    stored = !kF16 || un.x > 0.f;
+                }
                 if constexpr (kLse == 2) {
                     // the row sum of the bf16 P that P.V multiplied, the normaliser of out
                     const int i = it.i0 + pi;
@@ -791,7 +822,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                     }
                 } else {
                     const int i = it.i0 + pi, d0 = (NPV / 2) * hf;
-                    if (i < p.L) {
+                    if (i < p.L && stored) {
                         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + it.b * p.o_sb +
                                               static_cast<int64_t>(i) * p.o_st + it.h * p.o_sh;
 #pragma unroll
@@ -801,7 +832,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 }
             }
             pair_bar(li);                                   // both halves of every row are staged
-            if (kLse != 1 && ok && staged) {
+            if (kLse != 1 && ok && staged && stored) {
                 // this warp stores rows (li & ~31) + 16 hf + 0..15: lane -> row + lane / 8, chunk
                 // of 8 columns lane mod 8
                 const uint32_t* bd0 = reinterpret_cast<const uint32_t*>(smem + PSmem::BD);
@@ -859,16 +890,23 @@ cudaError_t launch_attn_persist(const AttnTcParams& p, int sm_count, cudaStream_
         e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 2>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, true>,
+        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, kOpsF16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, kOpsBf16>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
         if (e != cudaSuccess) return e;
         attr_done = true;
     }
     const int64_t items = static_cast<int64_t>(p.n_qt) * p.H * p.B;
     const int grid = static_cast<int>(items < sm_count ? items : sm_count);
-    if (p.units)
-        return launch_dependent(attn_persist_kernel<false, false, 0, true>, dim3(grid), dim3(kPThreads), PSmem::Size,
+    if (p.units) {
+        const cudaError_t e = launch_dependent(attn_persist_kernel<false, false, 0, kOpsF16>, dim3(grid), dim3(kPThreads),
+                                               PSmem::Size, s, p);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(attn_persist_kernel<false, false, 0, kOpsBf16>, dim3(grid), dim3(kPThreads), PSmem::Size,
                                 s, p);
+    }
     if (p.lse && !p.table && p.lse_out)
         return launch_dependent(attn_persist_kernel<false, false, 2>, dim3(grid), dim3(kPThreads), PSmem::Size,
                                 s, p);

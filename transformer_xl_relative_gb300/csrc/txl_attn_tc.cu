@@ -102,10 +102,11 @@ struct Plan {
     __device__ bool need_chunk(int t, int C) const { return 128 * t < C; }
 };
 
-// kF16: fp16 operands read back from a quantised memory, K, V and r in units of p.units per (b, h).
-template <int NA, bool kF16>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnTcParams p)
+// kOps: with operands of an expanded memory, fp16 with K, V and r in units of p.units per (b, h), or bf16.
+template <int NA, int kOps>
+__device__ __forceinline__ void attn_tc_tile(const AttnTcParams& p)
 {
+    constexpr bool kF16 = kOps == kOpsF16;
     using S = AttnSmem<NA>;
     constexpr int NS = S::NS;
     constexpr int NV = S::NV;
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (!mbar_wait(&bar.r_empty[s], ((rs / NS) & 1) ^ 1, wc, 10)) return false;
                 mbar_expect_tx(&bar.r_full[s], NA * kTile);
                 for (int a = 0; a < NA; ++a)
-                    tma_load_3d(smem + S::R + (s * NA + a) * kTile, &p.tm_r, 64 * a, h, row0,
-                                &bar.r_full[s]);
+                    tma_load_3d(smem + S::R + (s * NA + a) * kTile, kOps == kOpsBf16 ? &p.tm_rb : &p.tm_r, 64 * a, h,
+                                row0, &bar.r_full[s]);
                 ++rs;
                 return true;
             };
@@ -411,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             float scu = p.qscale, scv = p.qscale;
             if constexpr (kF16) {                           // times the units of K and r
                 const float* un = p.units + 4 * (static_cast<int64_t>(b) * p.H + h);
-                scu *= __ldg(un);
-                scv *= __ldg(un + 2);
+                scu *= __ldcg(un);
+                scv *= __ldcg(un + 2);
             }
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
@@ -433,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         const float v0 = vh[d0], v1 = vh[d0 + 1];
                         const float x0 = z0 ? 0.f : (q0 + u0) * scu, x1 = z1 ? 0.f : (q1 + u1) * scu;
                         const float y0 = z0 ? 0.f : (q0 + v0) * scv, y1 = z1 ? 0.f : (q1 + v1) * scv;
-                        wu[e] = kF16 ? pack_f16x2_sat(x0, x1) : pack_bf16x2(x0, x1);
-                        wv[e] = kF16 ? pack_f16x2_sat(y0, y1) : pack_bf16x2(y0, y1);
+                        wu[e] = kF16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+                        wv[e] = kF16 ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
                     }
                     const int off = a * kTile + li * 128 + ((c ^ (li & 7)) << 4);
                     *reinterpret_cast<uint4*>(smem + S::Qu + off) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
@@ -548,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 float alpha = 1.f;
                 bool rescale_o = false;
                 if (t == 0) {
-                    m_run = mt;
+                    // (kOpsBf16: a query may see only keys of -inf in this tile)
+                    m_run = kOps == kOpsBf16 ? fmaxf(mt, -3e38f) : mt;
                 } else if (mt > m_run + kRescaleThreshold) {
                     alpha = ex2_approx(m_run - mt);
                     m_run = mt;
@@ -618,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const float l_row = l_half + xchg[2 * (n_t & 1) + (hf ^ 1)];
             const int i = plan.i0 + pi;
             float inv_l = 1.f / l_row;
-            if constexpr (kF16) inv_l *= __ldg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h) + 1);
+            if constexpr (kOps != kOpsGiven)
+                inv_l *= __ldcg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h) + 1);
             __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_sb +
                                   static_cast<int64_t>(i) * p.o_st + h * p.o_sh;
             const bool vec = p.out_vec != 0;
@@ -655,18 +658,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
 }
 
-template <int NA, bool kF16>
+// kUnits: operands from an expanded memory.
+template <int NA, bool kUnits>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnTcParams p)
+{
+    if constexpr (!kUnits) attn_tc_tile<NA, kOpsGiven>(p);
+    else if (operands_f16(p, blockIdx.z, blockIdx.y)) attn_tc_tile<NA, kOpsF16>(p);
+    else attn_tc_tile<NA, kOpsBf16>(p);
+}
+
+template <int NA, bool kUnits>
 cudaError_t launch_na(const AttnTcParams& p, cudaStream_t s)
 {
     static bool attr_done = false;
     if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NA, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NA, kUnits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              AttnSmem<NA>::Size);
         if (e != cudaSuccess) return e;
         attr_done = true;
     }
     dim3 grid(p.n_qt, p.H, p.B);
-    attn_tc_kernel<NA, kF16><<<grid, kThreads, AttnSmem<NA>::Size, s>>>(p);
+    attn_tc_kernel<NA, kUnits><<<grid, kThreads, AttnSmem<NA>::Size, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -141,10 +141,12 @@ struct AttnTcParams {
     // lse_out is set, not otherwise
     float* lse;
     int lse_out;
-    // fp16 operands (units != null): k, v, r are fp16 in units of units[4 (b H + h) + 0, 1, 2]; c(q+u)
-    // times the K unit, c(q+v) times the r unit, the position term and P are taken in fp16, and the
-    // output is multiplied by the V unit
+    // operands from an expanded memory (units != null): units[4 (b H + h) + 0, 1, 2] are the units of k, v and r.
+    // k, v, r are fp16 in their units, c(q+u) times the K unit, c(q+v) times the r unit, the position term and P are
+    // taken in fp16; where the K unit is negative, all of them are bf16 instead, r through tm_rb, and units[3] is
+    // not 0.  The output is multiplied by the V unit.
     const float* units;
+    CUtensorMap tm_rb;
 };
 
 cudaError_t launch_attn_tc(const AttnTcParams& p, cudaStream_t s);
@@ -295,7 +297,7 @@ struct QmemParams {
 cudaError_t launch_qmem_push(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
 cudaError_t launch_qmem_read(const QmemParams& p, txl_dtype dtype, cudaStream_t s);
 
-// The fp16 operands of the fused attention over a quantised memory (positions slot0 .. of the ring,
+// The 16-bit operands of the fused attention over a quantised memory (positions slot0 .. of the ring,
 // n of them) and a segment of L: K, V and q head-major [B][H][rows][ld], ld = D rounded up to 8.
 struct QexpandParams {
     const uint8_t* rows;
@@ -305,13 +307,16 @@ struct QexpandParams {
     const void* q; int64_t q_sb, q_st, q_sh;
     const uint16_t* r; int64_t ld_r;    // bf16 [n_r][H][ld_r]
     int vec_v, vec_k, vec_q, vec_r;     // rows of these start on 16-byte boundaries
+    const float* u; const float* vb;
+    float qscale;                       // scale * log2(e)
     int n_r;
+    int r_alone;                        // r16 holds the only rows of r that the attention can load
     void* k_mem; void* v_mem;           // n rows per head, in the units below
     void* k_seg; void* v_seg;           // L rows per head, the same units
     void* q_seg;                        // bf16 copy for TMA, or null where q serves as it is
     void* r16;                          // [n_r][H][ld]
-    float* units;                       // [B][H][4], 16-byte aligned: powers of two of K, V and r
-    float* absmax;                      // [B][H][8][4], 16-byte aligned: largest |k|, |v|, |r| of shares of the rows
+    float* units;                       // [B][H][4], 16-byte aligned: powers of two of K, V and r (see AttnTcParams)
+    uint32_t* ranges;                   // [B][H][8][4], 16-byte aligned: ranges of shares of the rows
     int* chk;
 };
 cudaError_t launch_qmem_expand(const QexpandParams& p, cudaStream_t s);

@@ -542,18 +542,11 @@ __device__ __forceinline__ float add_bf16lo_f32(uint32_t w, float c)
     return r;
 }
 
-// The same two of an fp16 pair, and the packing, plain and with values past fp16's range held at its ends.
+// The same two of an fp16 pair, and the packing.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 

@@ -383,16 +383,45 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
     }
 }
 
-// The operands of the fused attention kernels in fp16, which keeps 11 bits where bf16 keeps 8: K and V
-// of the memory and of the segment, and r.  Each takes its range from a power of two, the unit: the
-// largest |k| of a (b, h) comes into [1, 2) (its unit multiplies c(q+u)), the largest |v| into
-// [2^11, 2^12) (P of the attention goes up to 2^8), and the largest |r| of the head into [1, 2).
+// The operands of the fused attention kernels: K and V of the memory and of the segment, and r, in fp16, which
+// keeps 11 bits where bf16 keeps 8, for every (b, h) whose values fp16 has the range for, else in bf16.  In fp16
+// each takes its range from a power of two, the unit: the largest |k| of a (b, h) comes into [1, 2) (its unit
+// multiplies c(q+u)), the largest |v| into [2^14, 2^15) (P of the attention goes up to 2^8, the sums are fp32), and
+// the largest |r| of the head into [1, 2).  What that can lose:
+//   * An element of k below 2^-14 of its unit is off by up to 2^-25 of the unit, a score by D max|c(q+u)| max|k|
+//     2^-25: 2^-10 where that product is at most 2^15.  No c(q+u) leaves fp16's range then, nor does a
+//     score.  The same for r and c(q+v), whose sums, the position terms, are held in fp16.
+//   * P is off by up to 2^-25 (of its largest, 1 to 2^8) where it is below 2^-14: of a key whose value is R times
+//     another's, by 2^-25 R of that one's.  R is at most 2^12, over all groups of 32 channels that are not zero.
+//     (v's own elements are off by 2^-39 of the largest.)
+// Ordinary values are far inside (D max|c(q+u)| max|k| around 2^9, R of 2^4); a head with an infinity, a NaN, an element
+// far above the rest or nearly empty positions is not, and is computed as txl_rel_attn_fwd would, in bf16.
 //
-// Two passes: qmem_absmax_kernel takes the largest values of up to kXSplits shares of the rows of a (b, h)
-// (a group's end points bound its values, so the parameters suffice for the memory), qmem_expand_kernel
-// writes, one lane per eight channels of a row.  (One kernel with a cluster per (b, h), exchanging the
-// maxima through shared memory, took 62 us on the large shape: its CTAs waited for one another.)
+// Two passes: qmem_ranges_kernel takes the ranges of up to kXSplits shares of the rows of a (b, h) (a group's end
+// points bound its values, so the parameters suffice for the memory), qmem_expand_kernel writes, one lane per eight
+// channels of a row.  (One kernel with a cluster per (b, h), exchanging the maxima through shared memory, took
+// 62 us on the large shape: its CTAs waited for one another.)
 constexpr int kXSplits = 8;
+
+// A share's ranges, four words: largest |k| and |v| as bf16 halves, rounded up; bounds of |c(q+u)| and |c(q+v)|
+// likewise; largest |r| (shares of their own); the smallest over groups that are not zero of a group's largest |v|.
+// What is not finite counts as infinite.
+struct XRange {
+    float k = 0.f, v = 0.f, qu = 0.f, qv = 0.f, v_least = INFINITY;
+    __device__ __forceinline__ void join(const uint4& w)
+    {
+        k = fmaxf(k, __uint_as_float(w.x << 16));
+        v = fmaxf(v, __uint_as_float(w.x & 0xffff0000u));
+        qu = fmaxf(qu, __uint_as_float(w.y << 16));
+        qv = fmaxf(qv, __uint_as_float(w.y & 0xffff0000u));
+        v_least = fminf(v_least, __uint_as_float(w.w));
+    }
+    // whether this (b, h) has the range for fp16 (false for any infinity)
+    __device__ __forceinline__ bool fits(int D, float r) const
+    {
+        return D * qu * k <= 32768.f && D * qv * r <= 32768.f && v < INFINITY && v <= 4096.f * v_least;
+    }
+};
 
 // First of the n items that fall to share `part` of `parts`.
 __device__ __forceinline__ int x_share(int n, int part, int parts)
@@ -402,21 +431,23 @@ __device__ __forceinline__ int x_share(int n, int part, int parts)
 }
 
 template <int BITS, int G>
-__global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_constant__ QexpandParams p, int parts)
+__global__ void __launch_bounds__(kQThreads, G == 3 ? 6 : 8) qmem_ranges_kernel(const __grid_constant__ QexpandParams p, int parts)
 {
-    __shared__ float red[3][kQThreads / 32];
+    __shared__ float red[6][kQThreads / 32];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(b) * p.H + h;
+    if (tid == 0 && part == 0 && bh == 0) p.units[3] = 0.f;      // (set by the expansion where a head is bf16)
     constexpr int LPR = 4 * G;                            // lanes of a row, eight channels each
     constexpr int RPP = kQThreads / LPR;                  // rows of a pass
     const int lr = tid / LPR, d0 = 8 * (tid % LPR);
-    const bool lane_on = lr < RPP && d0 < p.D;
+    const bool lane_on = lr < RPP;                        // the four lanes of a group are on or off together
 
-    float mx[3] = {0.f, 0.f, 0.f};                        // k, v, r; values that are not finite do not count
-    auto see = [&](int which, float a) {
-        if (a < INFINITY) mx[which] = fmaxf(mx[which], a);
+    float k = 0.f, v = 0.f, q = 0.f, u = 0.f, vb = 0.f, v_least = INFINITY;      // (k: r in blocks of r); NaN stays
+    auto group_v = [&](float a) {                         // the largest |v| of a group
+        v = max_nan(v, a);
+        if (a > 0.f) v_least = fminf(v_least, a);
     };
     if (part < parts) {
         const int64_t x1 = static_cast<int64_t>(x_share(p.n, part + 1, parts)) * G;
@@ -428,26 +459,46 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
             if (!in_range(s, 0, p.M, p.chk)) s = 0;
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
                                                                   q_par_offset(G, BITS)) + g);
-            const uint32_t kv[2] = {w.x, w.y};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float step = __uint_as_float(kv[i] << 16), lo = __uint_as_float(kv[i] & 0xffff0000u);
-                see(i, fmaxf(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo))));
-            }
+            auto most = [&](uint32_t kv) {
+                const float step = __uint_as_float(kv << 16), lo = __uint_as_float(kv & 0xffff0000u);
+                return max_nan(fabsf(lo), fabsf(fmaf(step, static_cast<float>((1 << BITS) - 1), lo)));
+            };
+            k = max_nan(k, most(w.x));
+            group_v(most(w.y));
         }
         if (lane_on) {
-            auto rows = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int vec, int which) {
-                const int s1 = x_share(p.L, part + 1, parts);
-#pragma unroll 4
-                for (int t = x_share(p.L, part, parts) + lr; t < s1; t += RPP) {
-                    float v[8];
-                    load8<false>(static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh, d0, p.D, vec, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) see(which, fabsf(v[e]));
-                }
+            const int s0 = x_share(p.L, part, parts) + lr, s1 = x_share(p.L, part + 1, parts);
+            auto row = [&](const void* x, int64_t sb, int64_t st, int64_t sh, int64_t t) {
+                return static_cast<const uint16_t*>(x) + b * sb + t * st + h * sh;
             };
-            rows(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, p.vec_k, 0);
-            rows(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, p.vec_v, 1);
+#pragma unroll 4
+            for (int t = s0; t < s1; t += RPP) {
+                float x[8];
+                load8<false>(row(p.kcur, p.kc_sb, p.kc_st, p.kc_sh, t), d0, p.D, p.vec_k, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) k = max_nan(k, fabsf(x[e]));
+            }
+#pragma unroll 4
+            for (int t = s0; t < s1; t += RPP) {
+                float x[8], a = 0.f;
+                load8<false>(row(p.vcur, p.vc_sb, p.vc_st, p.vc_sh, t), d0, p.D, p.vec_v, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a = max_nan(a, fabsf(x[e]));
+#pragma unroll
+                for (int off = 1; off <= 2; off <<= 1) a = max_nan(a, __shfl_xor_sync(0xfu << (lane & 28), a, off));
+                group_v(a);
+            }
+#pragma unroll 4
+            for (int t = s0; t < s1; t += RPP) {
+                float x[8];
+                load8<false>(row(p.q, p.q_sb, p.q_st, p.q_sh, t), d0, p.D, p.vec_q, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q = max_nan(q, fabsf(x[e]));
+            }
+        }
+        if (tid < p.D) {
+            u = fabsf(__ldg(p.u + h * p.D + tid));
+            vb = fabsf(__ldg(p.vb + h * p.D + tid));
         }
     } else if (lane_on) {
         // this entry's share of the head's rows of r
@@ -455,24 +506,40 @@ __global__ void __launch_bounds__(kQThreads) qmem_absmax_kernel(const __grid_con
         const int r0 = x_share(p.n_r, b, p.B), n_r = x_share(p.n_r, b + 1, p.B) - r0, s1 = x_share(n_r, rp + 1, r_parts);
 #pragma unroll 4
         for (int i = x_share(n_r, rp, r_parts) + lr; i < s1; i += RPP) {
-            float v[8];
-            load8<false>(p.r + (static_cast<int64_t>(r0 + i) * p.H + h) * p.ld_r, d0, p.D, p.vec_r, v);
+            float x[8];
+            load8<false>(p.r + (static_cast<int64_t>(r0 + i) * p.H + h) * p.ld_r, d0, p.D, p.vec_r, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) see(2, fabsf(v[e]));
+            for (int e = 0; e < 8; ++e) k = max_nan(k, fabsf(x[e]));
         }
     }
+    // over the block (v_least as the maximum of its negative)
+    float m[6] = {k, v, q, u, vb, -v_least};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 6; ++i) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
-        if ((tid & 31) == 0) red[i][tid >> 5] = mx[i];
+        for (int off = 16; off > 0; off >>= 1) m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+        if (lane == 0) red[i][tid >> 5] = m[i];
     }
     __syncthreads();
-    if (part < parts ? tid < 2 : tid == 2) {
-        float m = 0.f;
+    if (tid >= 32) return;
 #pragma unroll
-        for (int w = 0; w < kQThreads / 32; ++w) m = fmaxf(m, red[tid][w]);
-        p.absmax[(bh * kXSplits + (part < parts ? part : part - parts)) * 4 + tid] = m;
+    for (int i = 0; i < 6; ++i) {
+        m[i] = red[i][lane & 7];
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+    }
+    if (lane != 0) return;
+    uint32_t* out = p.ranges + (bh * kXSplits + (part < parts ? part : part - parts)) * 4;
+    auto or_inf = [](float a) { return a < INFINITY ? a : INFINITY; };
+    auto pair = [&](float a, float c) {
+        return (__float_as_uint(bf16_ceil_pos(or_inf(a))) >> 16) | __float_as_uint(bf16_ceil_pos(or_inf(c)));
+    };
+    if (part < parts) {
+        out[0] = pair(m[0], m[1]);
+        out[1] = pair((m[2] + m[3]) * p.qscale, (m[2] + m[4]) * p.qscale);
+        out[3] = __float_as_uint(-m[5]);
+    } else {
+        out[2] = __float_as_uint(or_inf(m[0]));
     }
 }
 
@@ -489,52 +556,89 @@ __global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_
     if (lr >= kBlockRows<G>) t = INT32_MAX;
     uint32_t ck[2], cv[2];
     uint2 par;
-    if (t < p.n && d0 < p.D) {                             // requested before the maxima
+    if (t < p.n && d0 < p.D) {                             // requested before the ranges
         unsigned s = static_cast<unsigned>(p.slot0) + t;
         if (s >= static_cast<unsigned>(p.M)) s -= p.M;
         if (!in_range(s, 0, p.M, p.chk)) s = 0;
         const uint8_t* head = p.rows + bh * p.M * q_row_bytes(G, BITS);
         par = row_unit<BITS, G>(head + static_cast<uint64_t>(s) * static_cast<unsigned>(q_row_bytes(G, BITS)), d0, ck, cv);
     }
-    float mx[3] = {0.f, 0.f, 0.f}, inv[3];
-    for (int y = 0; y < parts; ++y) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p.absmax) + bh * kXSplits + y);
-        mx[0] = fmaxf(mx[0], a.x); mx[1] = fmaxf(mx[1], a.y);
-    }
-    // the head's rows of r: over the shares of every entry, where it is used
-    __shared__ float red[kQThreads / 32];
-    if (blockIdx.x == 0 || (static_cast<int64_t>(blockIdx.x) + 1) * kBlockRows<G> > static_cast<int64_t>(p.n) + p.L) {
-        for (int e = threadIdx.x; e < p.B * r_parts; e += kQThreads) {
-            const int64_t at = (static_cast<int64_t>(e / r_parts) * p.H + h) * kXSplits + e % r_parts;
-            mx[2] = fmaxf(mx[2], __ldg(p.absmax + at * 4 + 2));
+    // the ranges, by the first warp: this (b, h)'s shares, and the head's rows of r over the shares of every entry
+    __shared__ float red[kQThreads / 32], scale_by[4];     // of k, v, r, and of the rows of r16
+    __shared__ int in_f16;
+    const uint4* ranges = reinterpret_cast<const uint4*>(p.ranges);
+    const int lane = threadIdx.x & 31;
+    XRange x;
+    if (threadIdx.x < parts) x.join(__ldcg(ranges + bh * kXSplits + threadIdx.x));
+    float r = 0.f;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < p.B * r_parts; e += kQThreads)
+        r = fmaxf(r, __uint_as_float(__ldcg(p.ranges + ((static_cast<int64_t>(e / r_parts) * p.H + h) * kXSplits + e % r_parts) * 4 + 2)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, off));
+    if (lane == 0) red[threadIdx.x >> 5] = r;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        r = red[lane & 7];
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) {
+            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, off));
+            x.k = fmaxf(x.k, __shfl_xor_sync(0xffffffffu, x.k, off));
+            x.v = fmaxf(x.v, __shfl_xor_sync(0xffffffffu, x.v, off));
+            x.qu = fmaxf(x.qu, __shfl_xor_sync(0xffffffffu, x.qu, off));
+            x.qv = fmaxf(x.qv, __shfl_xor_sync(0xffffffffu, x.qv, off));
+            x.v_least = fminf(x.v_least, __shfl_xor_sync(0xffffffffu, x.v_least, off));
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx[2] = fmaxf(mx[2], __shfl_xor_sync(0xffffffffu, mx[2], off));
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx[2];
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kQThreads / 32; ++w) mx[2] = fmaxf(mx[2], red[w]);
+        bool f16 = __shfl_sync(0xffffffffu, x.fits(p.D, r) ? 1 : 0, 0);
+        if (p.r_alone) {                                   // one copy of r: one type for every entry's share of the head
+            bool all = true;
+#pragma unroll 1
+            for (int e = lane; e < p.B; e += 32) {
+                XRange o;
+#pragma unroll 1
+                for (int y = 0; y < parts; ++y) o.join(__ldcg(ranges + (static_cast<int64_t>(e) * p.H + h) * kXSplits + y));
+                all = all && o.fits(p.D, r);
+            }
+            f16 = __all_sync(0xffffffffu, all);
+        }
+        if (lane < 3) {
+            // bf16 operands stay as they are, but values whose sums could overflow fp32
+            const float top = lane == 0 ? x.k : lane == 1 ? x.v : r;
+            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // 128: not finite
+            const int fit = min(max(e - (lane == 1 ? 14 : 0), -115), 115);
+            const int ex = f16 ? fit : lane == 1 && e > 64 && e < 128 ? e - 64 : 0;
+            scale_by[lane] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            // (entries in bf16 read r itself where they can)
+            if (lane == 2) scale_by[3] = p.r_alone && !f16 ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - fit) << 23);
+            if (blockIdx.x == 0)
+                p.units[4 * bh + lane] = lane == 0 && !f16 ? -1.f : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        } else if (lane == 3) {
+            in_f16 = f16;
+            if (blockIdx.x == 0 && !f16) p.units[3] = 1.f;
+        }
     }
-#pragma unroll
-    for (int y = 0; y < 3; ++y) {
-        const int ex = min(max(static_cast<int>(__float_as_uint(mx[y]) >> 23) - 127 - (y == 1 ? 11 : 0), -115), 115);
-        inv[y] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.units[4 * bh + y] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-    }
+    __syncthreads();
+    const bool f16 = in_f16 != 0;
     if (d0 >= p.D) return;
     const unsigned ld_bytes = 2 * p.ld;
-    auto put = [&](void* base, int64_t first_row, int r, const float* x, float f) {
-        char* dst = static_cast<char*>(base) + first_row * ld_bytes + static_cast<uint64_t>(r) * ld_bytes + 2 * d0;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_f16x2_sat(x[0] * f, x[1] * f), pack_f16x2_sat(x[2] * f, x[3] * f),
-                                                    pack_f16x2_sat(x[4] * f, x[5] * f), pack_f16x2_sat(x[6] * f, x[7] * f));
+    auto put = [&](void* base, int64_t first_row, int at, const float* a, float f, bool half) {
+        char* dst = static_cast<char*>(base) + first_row * ld_bytes + static_cast<uint64_t>(at) * ld_bytes + 2 * d0;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a0 = a[2 * e] * f, a1 = a[2 * e + 1] * f;
+            w[e] = half ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     };
-    float x[8], y[8];
+    float a[8];
     if (t < p.n) {
         // lo + step c in units (a power of two, so scaling the parameters rounds nothing)
-        expand8<BITS>(ck, __uint_as_float(par.x << 16) * inv[0], __uint_as_float(par.x & 0xffff0000u) * inv[0], x);
-        expand8<BITS>(cv, __uint_as_float(par.y << 16) * inv[1], __uint_as_float(par.y & 0xffff0000u) * inv[1], y);
-        put(p.k_mem, bh * p.n, t, x, 1.f);
-        put(p.v_mem, bh * p.n, t, y, 1.f);
+        const float ki = scale_by[0], vi = scale_by[1];
+        expand8<BITS>(ck, __uint_as_float(par.x << 16) * ki, __uint_as_float(par.x & 0xffff0000u) * ki, a);
+        put(p.k_mem, bh * p.n, t, a, 1.f, f16);
+        expand8<BITS>(cv, __uint_as_float(par.y << 16) * vi, __uint_as_float(par.y & 0xffff0000u) * vi, a);
+        put(p.v_mem, bh * p.n, t, a, 1.f, f16);
         return;
     }
     if (t == INT32_MAX) return;
@@ -543,21 +647,22 @@ __global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_
         return static_cast<const uint16_t*>(v) + b * sb + t * st + h * sh;
     };
     if (t < p.L) {
-        load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, x);
-        load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, y);
-        put(p.k_seg, bh * p.L, t, x, inv[0]);
-        put(p.v_seg, bh * p.L, t, y, inv[1]);
+        load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, a);
+        float c[8];
+        load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, c);
+        put(p.k_seg, bh * p.L, t, a, scale_by[0], f16);
+        put(p.v_seg, bh * p.L, t, c, scale_by[1], f16);
         if (p.q_seg) {
-            load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, x);
-            store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, x);
+            load8<false>(seg(p.q, p.q_sb, p.q_st, p.q_sh), d0, p.D, p.vec_q, a);
+            store8<false>(static_cast<uint16_t*>(p.q_seg) + (bh * p.L + t) * p.ld, d0, p.ld, true, a);
         }
         return;
     }
     t += x_share(p.n_r, b, p.B) - p.L;
     if (t < x_share(p.n_r, b + 1, p.B)) {
         const int64_t row = static_cast<int64_t>(t) * p.H + h;
-        load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, x);
-        put(p.r16, row, 0, x, inv[2]);
+        load8<false>(p.r + row * p.ld_r, d0, p.D, p.vec_r, a);
+        put(p.r16, row, 0, a, scale_by[3], !p.r_alone || f16);
     }
 }
 
@@ -567,7 +672,7 @@ cudaError_t launch_expand(const QexpandParams& p, cudaStream_t s)
     // shares of about 128 rows
     auto shares = [](int64_t rows) { return static_cast<int>(std::min<int64_t>(kXSplits, std::max<int64_t>(1, (rows + 127) / 128))); };
     const int parts = shares(std::max<int64_t>(p.n / G, p.L)), r_parts = shares(p.n_r / p.B);
-    cudaError_t e = launch_dependent(qmem_absmax_kernel<BITS, G>, dim3(parts + r_parts, p.H, p.B), dim3(kQThreads), 0, s, p, parts);
+    cudaError_t e = launch_dependent(qmem_ranges_kernel<BITS, G>, dim3(parts + r_parts, p.H, p.B), dim3(kQThreads), 0, s, p, parts);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.n) + p.L + (p.n_r + p.B - 1) / p.B;
     if (rows > INT32_MAX - kQThreads) return cudaErrorInvalidValue;
