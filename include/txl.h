@@ -517,7 +517,8 @@ txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
  * |scale log2(e) (q+u)| times the largest |k'| is at most 2^15, the same for (q+v) and the head's r, and the
  * largest |v'| is at most 2^12 times the smallest that a group of 32 channels which is not zero has as its
  * largest.  Otherwise it has bf16 ones, as in txl_rel_attn_fwd.  (Where r's rows do not start on 16-byte
- * boundaries, all entries of a head have one type.)
+ * boundaries, all entries of a head have one type.)  Keys and values of the segment reach the queries from
+ * their position on alone, whatever they are.  (A call without a memory, M = 0, is txl_rel_attn_fwd's.)
  * L > 16, fp32, one launch: codes are expanded tile by tile in shared memory, all arithmetic in fp32.
  * err_flag as for txl_rel_attn_fwd: every kernel that waits for copies sets it if a wait runs out.
  */

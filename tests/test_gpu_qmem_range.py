@@ -208,3 +208,30 @@ def test_segment_heads_of_either_kind_without_a_loadable_table(txl, D):
     call.v[0, 5, 1] *= 2.0 ** 20
     call.go(txl)
     check(call)
+
+
+@pytest.mark.parametrize("L", [50, 300])
+@pytest.mark.parametrize("D", [24, 64, 96])
+@pytest.mark.parametrize("key,value", [(NAN, INF), (INF, NAN), (-INF, -INF), (3e38, -3e38)], ids=str)
+def test_segment_sees_no_later_key(txl, key, value, D, L):
+    """Keys and values of the segment that are NaN, infinite or at the end of bf16's range reach the queries from
+    their position on, and no query before it (positions from 3/5 and 4/5 of the segment on)."""
+    call = segment(txl, D, L=L, hs=D + 1, shift=1)
+    call.v[:, 3 * L // 5:] = value
+    call.v[0, 7 * L // 10, 0] = -value
+    call.k[:, 4 * L // 5:] = key
+    call.go(txl)
+    # (scores past fp32's range are not compared)
+    check(call, slice(0, 4 * L // 5) if key == 3e38 else slice(None))
+
+
+@pytest.mark.parametrize("D", [64, 96])
+def test_segment_values_that_are_not_finite_apart_in_the_segment(txl, D):
+    """One element each, in different tiles, channels and heads."""
+    call = segment(txl, D, L=400)
+    call.v[0, 100, 0, 3], call.v[0, 300, 0, 3], call.v[0, 130, 0, D - 1] = INF, -INF, NAN
+    call.v[1, 399, 1, 0] = INF
+    call.v[0, 50, 1], call.v[0, 390, 1, 7] = 3e38, INF
+    call.k[1, 200, 0, 5] = NAN
+    call.go(txl)
+    check(call)

@@ -244,7 +244,8 @@ txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_v
                           const txl_view* k_cur, const txl_view* v_cur, const float* u, const float* v_bias,
                           const void* r, int64_t ld_r, int n_rows, float scale, const txl_view* out, int* err_flag,
                           cudaStream_t s, int ring_slots, float* lse = nullptr, int lse_out = 0,
-                          const float* units = nullptr, const void* r_bf16 = nullptr, int64_t ld_rb = 0)
+                          const float* units = nullptr, const void* r_bf16 = nullptr, int64_t ld_rb = 0,
+                          const txl_view* v_given = nullptr)
 {
     const int M = (mem && mem->M > 0) ? mem->M : 0;
     const int valid = M > 0 ? mem->valid : 0;
@@ -297,6 +298,10 @@ txl_status attn_tc_launch(int B, int L, int H, int D, int clamp_len, const txl_v
     p.lse = lse;
     p.lse_out = lse_out;
     p.units = units;
+    if (units) {
+        p.vcur = static_cast<const uint16_t*>(v_given->ptr);
+        p.vc_sb = v_given->stride_b; p.vc_st = v_given->stride_t; p.vc_sh = v_given->stride_h;
+    }
     if (lse && p.n_atoms != 1) return TXL_ERR_UNSUPPORTED;
     if (p.n_atoms == 1) {
         if (static_cast<int64_t>(p.n_qt) * H * B > INT32_MAX) return TXL_ERR_UNSUPPORTED;
@@ -1235,7 +1240,7 @@ txl_status txl_rel_attn_qmem(int B, int L, int H, int D, int clamp_len, const tx
         e.ranges = reinterpret_cast<uint32_t*>(e.units + static_cast<int64_t>(B) * H * 4);
         if (launch_qmem_expand(e, s) != cudaSuccess) return TXL_ERR_CUDA;
         return attn_tc_launch(B, L, H, D, clamp_len, &qs, &m, &ks, &vs, u, v_bias, e.r16, ld, e.n_r, scale, out,
-                              err_flag, s, 0, nullptr, 0, e.units, e.r_alone ? e.r16 : r, e.r_alone ? ld : ld_r);
+                              err_flag, s, 0, nullptr, 0, e.units, e.r_alone ? e.r16 : r, e.r_alone ? ld : ld_r, v_cur);
     }
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
     QattnParams p;

@@ -30,6 +30,27 @@ __device__ __forceinline__ bool operands_f16(const AttnTcParams& p, int b, int h
 // Whether any (b, h) has bf16 ones.
 __device__ __forceinline__ bool any_bf16(const AttnTcParams& p) { return __ldcg(p.units + 3) != 0.f; }
 
+// kOpsBf16: keys after the query, in the diagonal tile (this thread's 64 columns from `first`, the query at pi): their
+// products may be anything, the ring's -inf masks what is finite.
+__device__ __forceinline__ void clear_later_keys(float* s, int first, int pi)
+{
+#pragma unroll
+    for (int k = 0; k < 64; ++k) s[k] = first + k > pi ? 0.f : s[k];
+}
+
+// kOpsBf16: the segment's values that are not finite of the positions up to i, added to channels d0 .. d0+31 of query i.
+__device__ __forceinline__ void add_values_not_finite(const AttnTcParams& p, int b, int h, int i, int d0, uint32_t* o)
+{
+    const uint16_t* v = p.vcur + b * p.vc_sb + h * p.vc_sh;
+    for (int j = 0; j <= min(i, p.L - 1); ++j, v += p.vc_st)
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (d0 + k < p.D) {
+                const float x = __uint_as_float(static_cast<uint32_t>(__ldg(v + d0 + k)) << 16);
+                if (!(fabsf(x) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + x);
+            }
+}
+
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P values stay below 2^8
 
 __device__ __forceinline__ int query_of_row(int li) { return 2 * (li & 63) + (li >> 6); }

@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 }
                 float mloc = -INFINITY;
                 if (ok) {
+                    if (kOps == kOpsBf16 && t == 0) clear_later_keys(s, 64 * hf, pi);
                     mloc = logits_interior<kF16>(s, bdrow, wbase);
                     xchg[2 * (t & 1) + hf] = mloc;
                 }
@@ -799,8 +800,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
                 if constexpr (kOps != kOpsGiven) {
                     const float2 un = __ldcg(reinterpret_cast<const float2*>(p.units) +
                                              2 * (static_cast<int64_t>(it.b) * p.H + it.h));
-                    inv_l *= un.y;
+                    inv_l *= fabsf(un.y);
                     stored = !kF16 || un.x > 0.f;
+                    if (kOps == kOpsBf16 && un.y < 0.f)
+                        add_values_not_finite(p, it.b, it.h, it.i0 + pi, (NPV / 2) * hf, o);
                 }
                 if constexpr (kLse == 2) {
                     // the row sum of the bf16 P that P.V multiplied, the normaliser of out

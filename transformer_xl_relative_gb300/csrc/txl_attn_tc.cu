@@ -540,6 +540,7 @@ __device__ __forceinline__ void attn_tc_tile(const AttnTcParams& p)
             }
             float mloc = -INFINITY;
             if (ok) {
+                if (kOps == kOpsBf16 && t == 0) clear_later_keys(s, 64 * hf, pi);
                 mloc = logits_interior<kF16>(s, bdrow, wbase);
                 xchg[2 * (t & 1) + hf] = mloc;
             }
@@ -620,8 +621,9 @@ __device__ __forceinline__ void attn_tc_tile(const AttnTcParams& p)
             const float l_row = l_half + xchg[2 * (n_t & 1) + (hf ^ 1)];
             const int i = plan.i0 + pi;
             float inv_l = 1.f / l_row;
-            if constexpr (kOps != kOpsGiven)
-                inv_l *= __ldcg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h) + 1);
+            float v_unit = 1.f;
+            if constexpr (kOps != kOpsGiven) v_unit = __ldcg(p.units + 4 * (static_cast<int64_t>(b) * p.H + h) + 1);
+            inv_l *= fabsf(v_unit);
             __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_sb +
                                   static_cast<int64_t>(i) * p.o_st + h * p.o_sh;
             const bool vec = p.out_vec != 0;
@@ -632,6 +634,7 @@ __device__ __forceinline__ void attn_tc_tile(const AttnTcParams& p)
                 tmem_ld32(tmem + lane_base + kColO + d0, o);
                 tmem_ld_wait();
                 if (i >= p.L) continue;
+                if (kOps == kOpsBf16 && v_unit < 0.f) add_values_not_finite(p, b, h, i, d0, o);
                 if (vec && d0 + 32 <= p.D) {
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {

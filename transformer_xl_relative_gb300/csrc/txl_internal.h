@@ -144,9 +144,11 @@ struct AttnTcParams {
     // operands from an expanded memory (units != null): units[4 (b H + h) + 0, 1, 2] are the units of k, v and r.
     // k, v, r are fp16 in their units, c(q+u) times the K unit, c(q+v) times the r unit, the position term and P are
     // taken in fp16; where the K unit is negative, all of them are bf16 instead, r through tm_rb, and units[3] is
-    // not 0.  The output is multiplied by the V unit.
+    // not 0.  The output is multiplied by the V unit.  That one is negative where v may have values that are not
+    // finite: those of the segment are 0 in the expanded rows, and the queries that see them add them from vcur.
     const float* units;
     CUtensorMap tm_rb;
+    const uint16_t* vcur; int64_t vc_sb, vc_st, vc_sh;
 };
 
 cudaError_t launch_attn_tc(const AttnTcParams& p, cudaStream_t s);

@@ -606,12 +606,14 @@ __global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_
             const float top = lane == 0 ? x.k : lane == 1 ? x.v : r;
             const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // 128: not finite
             const int fit = min(max(e - (lane == 1 ? 14 : 0), -115), 115);
-            const int ex = f16 ? fit : lane == 1 && e > 64 && e < 128 ? e - 64 : 0;
+            const int ex = f16 ? fit : lane == 1 && e > 64 ? 32 : 0;
             scale_by[lane] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
             // (entries in bf16 read r itself where they can)
             if (lane == 2) scale_by[3] = p.r_alone && !f16 ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - fit) << 23);
-            if (blockIdx.x == 0)
-                p.units[4 * bh + lane] = lane == 0 && !f16 ? -1.f : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+            if (blockIdx.x == 0) {
+                const float unit = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+                p.units[4 * bh + lane] = (lane == 0 && !f16) || (lane == 1 && !(x.v < INFINITY)) ? -unit : unit;
+            }
         } else if (lane == 3) {
             in_f16 = f16;
             if (blockIdx.x == 0 && !f16) p.units[3] = 1.f;
@@ -650,6 +652,9 @@ __global__ void __launch_bounds__(kQThreads, 8) qmem_expand_kernel(const __grid_
         load8<false>(seg(p.kcur, p.kc_sb, p.kc_st, p.kc_sh), d0, p.D, p.vec_k, a);
         float c[8];
         load8<false>(seg(p.vcur, p.vc_sb, p.vc_st, p.vc_sh), d0, p.D, p.vec_v, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)                        // (a weight of 0 would not hide them: see AttnTcParams)
+            if (!(fabsf(c[e]) < INFINITY)) c[e] = 0.f;
         put(p.k_seg, bh * p.L, t, a, scale_by[0], f16);
         put(p.v_seg, bh * p.L, t, c, scale_by[1], f16);
         if (p.q_seg) {
