@@ -1,5 +1,5 @@
 """GPU tests of txl_rel_attn_qmem on values of unlike size: infinities and NaN, elements far above or
-below the rest of their head.  References in 64 bits over what the memory stands for."""
+below the rest of their head or group of channels.  References in 64 bits over what the memory stands for."""
 from __future__ import annotations
 
 import numpy as np
@@ -235,3 +235,62 @@ def test_segment_values_that_are_not_finite_apart_in_the_segment(txl, D):
     call.k[1, 200, 0, 5] = NAN
     call.go(txl)
     check(call)
+
+
+def groups_within(call, bound):
+    """The error's norm over each group of 32 channels against the result's."""
+    ref, _ = attend(*call.operands_as_given(), call.C)
+    out = f64(call.out)
+    for d in range(0, ref.shape[-1], 32):
+        e, n = np.linalg.norm((out - ref)[..., d:d + 32]), np.linalg.norm(ref[..., d:d + 32])
+        assert e <= bound * n, (d, e / n)
+
+
+# fp32: the bound of test_fp32_keeps_its_bits.  bf16: the output's rounding, at most 2^-8 / sqrt(3) of its value,
+# and sums of 15 bits, whose 2^-15 is far below the rest of 2^-8.
+GROUP_BOUND = {"f32": 2.0 ** -19, "bf16": 2.0 ** -8}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("octaves", [10, 16, 30])
+@pytest.mark.parametrize("L", [1, 4, 16])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_value_groups_of_unlike_size(txl, bits, L, octaves, dtype):
+    """A group of 32 channels whose values are 2^octaves times smaller than the other's keeps its own bits."""
+    for D in (64, 128):
+        call = Ranged(txl, 2, 2, D, L, 900, 900, 9, 500, bits, dtype)
+        for x in (call.vh, call.v):
+            x[..., 32:64] *= 2.0 ** -octaves
+        call.push_again(txl, 9)
+        call.go(txl)
+        groups_within(call, GROUP_BOUND[dtype])
+
+
+@pytest.mark.parametrize("L", [1, 4, 16])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_one_position_of_large_values_and_little_weight(txl, bits, L):
+    """Its value is 2^16 times the others' and its weight some 2^-16: the others keep their bits."""
+    call = Ranged(txl, 1, 2, 64, L, 4000, 4000, 9, 500, bits, "f32")
+    q = call.q[:, :1].float() + call.u
+    call.q.copy_(call.q[:, :1].clone().expand_as(call.q))
+    t = -11.0 * 8 / (q ** 2).sum(-1, keepdim=True)
+    call.kh[:, 50] = (q * t)[:, 0].cpu()
+    call.vh[:, 50] *= 2.0 ** 16
+    call.push_again(txl, 9)
+    call.go(txl)
+    groups_within(call, GROUP_BOUND["f32"])
+
+
+@pytest.mark.parametrize("L", [1, 4, 16])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("octaves", [10, 20])
+def test_query_groups_of_unlike_size(txl, octaves, bits, L):
+    """Queries of a group of 32 channels 2^octaves times smaller than the other's, keys as much larger."""
+    call = Ranged(txl, 2, 2, 64, L, 900, 900, 9, 500, bits, "f32")
+    for x in (call.q, call.u, call.vb):
+        x[..., 32:] *= 2.0 ** -octaves
+    for x in (call.kh, call.k):
+        x[..., 32:] *= 2.0 ** octaves
+    call.push_again(txl, 9)
+    call.go(txl)
+    groups_within(call, GROUP_BOUND["f32"])

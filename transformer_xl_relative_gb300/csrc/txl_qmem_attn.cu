@@ -16,8 +16,11 @@
 // costs 0.6 instructions for K and for V, where converting to floats took about three.  (tcgen05 would
 // want the codes expanded into shared memory first, and 128 rows of queries where there are 1 to 16.)
 //
-// Precision: q+u is held as two fp16 parts (scaled by a power of two per row; 22 bits) in two columns
-// of the B operand, p step likewise; the accumulators are fp32.  The eight columns of an MMA are four
+// Precision: q+u is held as two fp16 parts (22 bits) in two columns of the B operand, p step likewise; the
+// accumulators are fp32.  Both are scaled by powers of two per row and group of 32 channels, so that a group keeps
+// its bits whatever the others hold (one unit for all: a group of values 2^10 times smaller than another was off
+// by 5e-5): the largest of q+u into [2^14, 2^15), which leaves 22 bits down to 2^-13 of it (odd channels at 4
+// bits; 2^-17 else), the largest p step into [2^8, 2^9) when its unit is set, 22 bits down to 2^-11.  The eight columns of an MMA are four
 // slots x (hi, lo).  A slot is a query; with fewer than three queries the other slots take other tiles
 // of 16 keys ("streams"), so that the work per key after the first product (scale, softmax, splitting
 // p) falls on all 32 lanes whatever L is.  With one query the four k-quarters of a Q.K MMA belong to the
@@ -68,8 +71,13 @@ constexpr int kMaxRows = 8;                    // queries of a CTA
 static_assert(kWarps + kDecodeMaxL <= 32 && kMaxRows <= kWarps, "a lane per part of a row, a warp per row");
 constexpr float kNoMax = -3e38f;               // running maximum before any key
 constexpr float kTwo24 = 16777216.f;
-constexpr float kMinUnit = 3.00926553e-36f;    // 2^-118 and 2^126: bounds of the weights' unit, so that a weight
+constexpr float kMinUnit = 3.00926553e-36f;    // 2^-118 and 2^126: bounds of the weights' units, so that a weight
 constexpr float kMaxUnit = 8.50705917e37f;     // (at most 2^8) over the unit stays finite
+constexpr uint32_t kMinUnits = 0x04800480u;    // 2^-118 twice, as below
+
+// Powers of two of two groups in a register, as bf16 halves: the units, and one over them (2^-126 .. 2^126).
+__device__ __forceinline__ float unit_of(uint32_t w, int G) { return __uint_as_float(G & 1 ? w & 0xffff0000u : w << 16); }
+__device__ __forceinline__ uint32_t one_over(uint32_t w) { return 0x7f007f00u - w; }
 
 // Keys of a stage: 64 where a key's codes are small and the queries few, else 32.
 __host__ __device__ constexpr int stage_keys(int bits, int ng, int qt) { return bits * ng <= 8 && qt == 1 ? 64 : 32; }
@@ -420,8 +428,9 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     uint8_t* stages = smem;
     float* qu = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);   // [row][DP]: q+u in log2 units
     float* inbox = qu + kMaxRows * DP;                    // [row of this rank][rank][DP + 2]: O, m, l
-    float* norm = inbox + kMaxRanks * (DP + 4);           // [row]: what the fp16 parts of qu are multiples of
-    float* qsum = norm + kMaxRows;                        // [row][NG]: group sums of qu
+    // [row][NG] bf16: what the fp16 parts of qu are multiples of, over what a code of one is
+    uint16_t* norm = reinterpret_cast<uint16_t*>(inbox + kMaxRanks * (DP + 4));
+    float* qsum = reinterpret_cast<float*>(norm + kMaxRows * NG);   // [row][NG]: group sums of qu
     float* own_s = qsum + kMaxRows * NG;                  // [row][kOwn]: scores of the segment's own keys
     float* weights = own_s + kMaxRows * kDecodeMaxL;      // [row][32]: of the parts that make the result
     uint16_t* quh = reinterpret_cast<uint16_t*>(weights + kMaxRows * 32);   // [2 row + part][QP]; rows past Lq are zeros
@@ -524,28 +533,30 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     for (int n = 0; n < kStages; ++n)
         if (n < n_stage) copy(n, true, false);
 
-    // ---- queries: warp w prepares row w: (q+u) times scale log2 e in fp32, and scaled by a power of two so that
-    // its largest entry lies in [2^11, 2^12) as two fp16 parts, in the order in which the B operands take them
-    // (4 bits: d = 0 4 1 5 2 6 3 7 of every eight, odd ones over 16; 8 bits: 0 2 1 3 of every four)
+    // ---- queries: warp w prepares row w: (q+u) times scale log2 e in fp32, and with every group scaled by a power of
+    // two so that its largest entry lies in [2^14, 2^15) as two fp16 parts, in the order in which the B operands
+    // take them (4 bits: d = 0 4 1 5 2 6 3 7 of every eight, odd ones over 16; 8 bits: 0 2 1 3 of every four)
     {
         const int row = warp;
-        float a[NG], mx = 0.f;
+        float a[NG];
 #pragma unroll
         for (int e = 0; e < NG; ++e) {
             const int d = 32 * e + lane;
             const float q = __uint_as_float(p.f32 ? q_raw[e] : q_raw[e] << 16);
             a[e] = my_row && d < p.D ? (q + __ldg(p.u + h * p.D + d)) * p.qscale : 0.f;
-            mx = fmaxf(mx, fabsf(a[e]));
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
-        const float up = __uint_as_float(static_cast<uint32_t>(11 - ex + 127) << 23);
-        if (lane == 0) norm[row] = __uint_as_float(static_cast<uint32_t>(ex - 11 + 127) << 23);
 #pragma unroll
         for (int e = 0; e < NG; ++e) {
             const int d = 32 * e + lane;
             qu[row * DP + d] = a[e];
+            float mx = fabsf(a[e]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+            if (lane == 0)
+                norm[row * NG + e] = static_cast<uint16_t>(
+                    __float_as_uint(__uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23) * kCode) >> 16);
             const int at = BITS == 4 ? (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1) : (d & ~3) + ((d & 1) << 1) + ((d >> 1) & 1);
             uint32_t w, unused;
             split_f16(a[e] * (BITS == 4 && (d & 1) ? up * kOdd : up), 0.f, w, unused);
@@ -573,7 +584,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     // ---- B operands of Q.K, column g = (slot g/2, part g%2), and per slot c4 the group sums of q.  ONE: the
     // k-quarter of this lane belongs to stream c4, so only columns of slot c4 are not zero there.
     uint32_t bq[QT][NG * 2][2];
-    float qs[QT][NG], sc[QT], far_of[QT];
+    float qs[QT][NG], far_of[QT];
+    uint32_t sc[QT][NG / 2];
     const int my_stream = (g >> 1) >> lp_log;             // of the column this lane holds in B operands
     const int one_key = (g + 2 * c4) & 7;
     const uint16_t* one_row = quh + ((g >> 1) == c4 ? (g & 1) : 2) * QP;       // or zeros
@@ -598,9 +610,10 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
             }
         }
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
-        sc[t] = norm[is] * kCode;
 #pragma unroll
         for (int G = 0; G < NG; ++G) qs[t][G] = qsum[is * NG + G];
+#pragma unroll
+        for (int G = 0; G < NG; G += 2) sc[t][G / 2] = *reinterpret_cast<const uint32_t*>(norm + is * NG + G);
     }
 
     float* e_row0 = p.E + (bh * p.L + i0) * p.e_pitch;
@@ -622,13 +635,15 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
     for (int n = 0; n < kStages; ++n)
         if (n < n_stage) copy(n, false, true);
 
-    // ---- running state of slot c4: maximum, weight unit rf (O is in units of rf), sums
-    float o[QT][NG * 2][4], z[QT][NG], m[QT], l[QT], rf[QT];
+    // ---- running state of slot c4: maximum, units rf of the weights by group (O is in units of rf), sums
+    float o[QT][NG * 2][4], z[QT][NG], m[QT], l[QT];
+    uint32_t rf[QT][NG / 2];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         m[t] = kNoMax;
         l[t] = 0.f;
-        rf[t] = kMinUnit;
+#pragma unroll
+        for (int G = 0; G < NG / 2; ++G) rf[t][G] = kMinUnits;
 #pragma unroll
         for (int G = 0; G < NG; ++G) z[t][G] = 0.f;
 #pragma unroll
@@ -745,54 +760,52 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
                     float a = (x ? near1 : near0) ? e_st[il * kEStride + 8 * x] : far_of[t], d = 0.f;
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
-                        d = fmaf(acc[t][G][2 * x] + acc[t][G][2 * x + 1], __uint_as_float(par[x][G].x << 16), d);
+                        d = fmaf((acc[t][G][2 * x] + acc[t][G][2 * x + 1]) * unit_of(sc[t][G / 2], G),
+                                 __uint_as_float(par[x][G].x << 16), d);
                         a = fmaf(lo_of(par[x][G].x), qs[t][G], a);
                     }
-                    s[x] = live[x] ? fmaf(d, sc[t], a) : -INFINITY;
+                    s[x] = live[x] ? d + a : -INFINITY;
                     pr[x] = ex2_approx(s[x] - m[t]);
                 }
-                const float f = __uint_as_float(0x7f000000u - __float_as_uint(rf[t]));   // 1 / rf, a power of two
-                float big = fmaxf(pr[0], pr[1]) * 16.f;
+                float big = fmaxf(pr[0], pr[1]) * 128.f;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int G = 0; G < NG; ++G) {
+                    const float f = unit_of(one_over(rf[t][G / 2]), G);
 #pragma unroll
-                    for (int G = 0; G < NG; ++G) {
+                    for (int x = 0; x < 2; ++x) {
                         w[x][G] = pr[x] * f * __uint_as_float(par[x][G].y << 16);
                         big = fmaxf(big, w[x][G]);
                     }
-                if (__any_sync(0xffffffffu, big > 4096.f)) {
-                    // a weight grew past 2^8, or its product with a step past 2^12: new maximum and unit
+                }
+                if (__any_sync(0xffffffffu, big > 32768.f)) {
+                    // a weight grew past 2^8, or its product with a step past 2^15 units: new maximum and units
                     float mx = fmaxf(s[0], s[1]);
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                     const float mn = fmaxf(m[t], mx);
                     const float dl = ex2_approx(m[t] - mn);
-                    float ref = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        pr[x] = ex2_approx(s[x] - mn);
-#pragma unroll
-                        for (int G = 0; G < NG; ++G) ref = fmaxf(ref, pr[x] * __uint_as_float(par[x][G].y << 16));
-                    }
-#pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
-                    ref = fminf(fmaxf(fmaxf(ref, rf[t] * dl), kMinUnit), kMaxUnit);
-                    const float unit = __uint_as_float(__float_as_uint(ref) & 0x7f800000u);      // its power of two
-                    const float f2 = __uint_as_float(0x7f000000u - __float_as_uint(unit));
-                    const float so = dl * rf[t] * f2;
-                    rf[t] = unit;
+                    for (int x = 0; x < 2; ++x) pr[x] = ex2_approx(s[x] - mn);
                     m[t] = mn;
                     l[t] *= dl;
 #pragma unroll
-                    for (int G = 0; G < NG; ++G) z[t][G] *= dl;
+                    for (int G = 0; G < NG; ++G) {
+                        float ref = fmaxf(pr[0] * __uint_as_float(par[0][G].y << 16), pr[1] * __uint_as_float(par[1][G].y << 16));
 #pragma unroll
-                    for (int x = 0; x < NG * 2; ++x) {
-                        o[t][x][0] *= so; o[t][x][1] *= so; o[t][x][2] *= so; o[t][x][3] *= so;
+                        for (int off = 4; off <= 16; off <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+                        const float was = unit_of(rf[t][G / 2], G);
+                        ref = fminf(fmaxf(fmaxf(ref * 0.00390625f, was * dl), kMinUnit), kMaxUnit);
+                        const uint32_t unit = __float_as_uint(ref) & 0x7f800000u;        // its power of two
+                        const float f = __uint_as_float(0x7f000000u - unit), so = dl * was * f;
+                        rf[t][G / 2] = __byte_perm(rf[t][G / 2], unit, G & 1 ? 0x7610 : 0x3276);
+                        z[t][G] *= dl;
+#pragma unroll
+                        for (int x = 2 * G; x < 2 * G + 2; ++x) {
+                            o[t][x][0] *= so; o[t][x][1] *= so; o[t][x][2] *= so; o[t][x][3] *= so;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) w[x][G] = pr[x] * f * __uint_as_float(par[x][G].y << 16);
                     }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int G = 0; G < NG; ++G) w[x][G] = pr[x] * f2 * __uint_as_float(par[x][G].y << 16);
                 }
                 l[t] += pr[0] + pr[1];
 #pragma unroll
@@ -898,8 +911,9 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
         for (int x = 0; x < NG * 2; ++x) {
             // (the unit last: times 2^24 it could leave fp32)
-            ot[2 * x] = fmaf((o[t][x][0] + o[t][x][1]) * kCode, rf[t], zt[x >> 1]);
-            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (kCode * kOdd), rf[t], zt[x >> 1]);
+            const float unit = unit_of(rf[t][x >> 2], x >> 1);
+            ot[2 * x] = fmaf((o[t][x][0] + o[t][x][1]) * kCode, unit, zt[x >> 1]);
+            ot[2 * x + 1] = fmaf((o[t][x][2] + o[t][x][3]) * (kCode * kOdd), unit, zt[x >> 1]);
         }
         float mt = m[t];
         for (int off = Lp; off <= 2; off <<= 1) {
@@ -1014,7 +1028,7 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
 {
     constexpr int DP = NG * 32;
     constexpr int staged = kWarps * kStages * stage_bytes(BITS, NG, QT, ONE);
-    constexpr int bytes = staged + (kMaxRows * (DP + 1 + NG + kDecodeMaxL + 32) + kMaxRanks * (DP + 4)) * 4 +
+    constexpr int bytes = staged + (kMaxRows * (DP + NG / 2 + NG + kDecodeMaxL + 32) + kMaxRanks * (DP + 4)) * 4 +
                           4 * kMaxRows * (DP + 8) * 2 + kMaxRows * 4 + kWarps * kStages * 8 + 16;
     static_assert(staged >= kWarps * stage_rows(QT, ONE) * (DP + 2) * 4, "the warps' partial results fit");
     static_assert(bytes <= 232448, "a CTA's shared memory");
