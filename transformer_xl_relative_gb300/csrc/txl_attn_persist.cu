@@ -877,30 +877,12 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_persist_kernel(const __grid
 cudaError_t launch_attn_persist(const AttnTcParams& p, int sm_count, cudaStream_t s)
 {
     if (p.B == 0 || p.L == 0 || p.H == 0) return cudaSuccess;
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(attn_persist_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 1>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 2>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, kOpsF16>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_persist_kernel<false, false, 0, kOpsBf16>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(
+        once, PSmem::Size, attn_persist_kernel<false>, attn_persist_kernel<true>, attn_persist_kernel<true, true>,
+        attn_persist_kernel<false, false, 1>, attn_persist_kernel<false, false, 2>,
+        attn_persist_kernel<false, false, 0, kOpsF16>, attn_persist_kernel<false, false, 0, kOpsBf16>);
+    if (prepared != cudaSuccess) return prepared;
     const int64_t items = static_cast<int64_t>(p.n_qt) * p.H * p.B;
     const int grid = static_cast<int>(items < sm_count ? items : sm_count);
     if (p.units) {

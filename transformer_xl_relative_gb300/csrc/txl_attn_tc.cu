@@ -673,13 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 template <int NA, bool kUnits>
 cudaError_t launch_na(const AttnTcParams& p, cudaStream_t s)
 {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NA, kUnits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             AttnSmem<NA>::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, AttnSmem<NA>::Size, attn_tc_kernel<NA, kUnits>);
+    if (prepared != cudaSuccess) return prepared;
     dim3 grid(p.n_qt, p.H, p.B);
     attn_tc_kernel<NA, kUnits><<<grid, kThreads, AttnSmem<NA>::Size, s>>>(p);
     return cudaGetLastError();

@@ -572,12 +572,9 @@ bool bwd_tc_eligible(const BwdParams& p, txl_dtype dtype)
 // dq, pac, pbd are written; dk, dv and dr must be zero on entry (atomic accumulation).
 cudaError_t launch_bwd_tc(const BwdParams& p, cudaStream_t s)
 {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, BSmem::Size, bwd_tc_kernel);
+    if (prepared != cudaSuccess) return prepared;
     const dim3 grid(p.a.H, p.a.B, (p.a.L + kQT - 1) / kQT);
     bwd_tc_kernel<<<grid, kBT, BSmem::Size, s>>>(p);
     return cudaGetLastError();

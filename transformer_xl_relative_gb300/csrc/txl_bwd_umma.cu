@@ -772,13 +772,9 @@ bool bwd_umma_eligible(const BwdParams& p, txl_dtype dtype)
 // du and dv_bias must be zero on entry (atomic accumulation).
 cudaError_t launch_bwd_umma(const BwdParams& p, cudaStream_t s)
 {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(bwd_umma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, USmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, USmem::Size, bwd_umma_kernel);
+    if (prepared != cudaSuccess) return prepared;
     const int64_t rows = static_cast<int64_t>(p.a.B) * p.a.L * p.a.H;
     bwd_rowdot_kernel<<<static_cast<unsigned>((rows + 31) / 32), 256, 0, s>>>(p);
     const int n_qt = (p.a.L + 127) / 128;

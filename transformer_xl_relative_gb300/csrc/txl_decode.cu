@@ -689,23 +689,14 @@ cudaError_t launch_lq(const DecodeParams& p, cudaStream_t s)
     dim3 grid(p.n_chunks, p.H, p.B);
     const bool staged = sizeof(T) == 2 && p.vec_kv && p.vec_r && (p.D % 8) == 0 && p.D <= 64;
     if (staged) {
-        static bool attr_st = false;
-        if (!attr_st) {
-            cudaError_t e = cudaFuncSetAttribute(decode_staged_kernel<LQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(decode_staged_smem_bytes(LQ)));
-            if (e != cudaSuccess) return e;
-            attr_st = true;
-        }
+        static OncePerDevice once;
+        const cudaError_t prepared = allow_smem(once, static_cast<int>(decode_staged_smem_bytes(LQ)), decode_staged_kernel<LQ>);
+        if (prepared != cudaSuccess) return prepared;
         decode_staged_kernel<LQ><<<grid, kDecThreads, decode_staged_smem_bytes(LQ), s>>>(p);
     } else {
-        static bool attr_done = false;
-        if (!attr_done) {
-            cudaError_t e = cudaFuncSetAttribute(decode_partial_kernel<T, LQ>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(decode_smem_bytes(LQ, 128)));
-            if (e != cudaSuccess) return e;
-            attr_done = true;
-        }
+        static OncePerDevice once;
+        const cudaError_t prepared = allow_smem(once, static_cast<int>(decode_smem_bytes(LQ, 128)), decode_partial_kernel<T, LQ>);
+        if (prepared != cudaSuccess) return prepared;
         decode_partial_kernel<T, LQ><<<grid, kDecThreads, decode_smem_bytes(LQ, p.Dp), s>>>(p);
     }
     cudaError_t e = cudaGetLastError();

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/txl.h"
+#include "txl_once.h"
 
 namespace txl {
 

@@ -246,13 +246,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
 cudaError_t launch_linear(const LinearParams& p, int sm_count, cudaStream_t s)
 {
     if (p.n_tiles == 0) return cudaSuccess;
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   LinSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, LinSmem::Size, linear_kernel);
+    if (prepared != cudaSuccess) return prepared;
     const int grid = p.n_tiles < sm_count ? p.n_tiles : sm_count;
     return launch_dependent(linear_kernel, dim3(grid), dim3(kLinThreads), LinSmem::Size, s, p);
 }

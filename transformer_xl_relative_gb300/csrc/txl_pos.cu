@@ -396,13 +396,9 @@ cudaError_t launch_pos_gen_f32(const PosGenF32Params& p, cudaStream_t s)
 cudaError_t launch_pos_gen_tc(const PosGenTcParams& p, cudaStream_t s)
 {
     if (p.n_rows == 0) return cudaSuccess;
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(pos_gen_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             PosSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, PosSmem::Size, pos_gen_tc_kernel);
+    if (prepared != cudaSuccess) return prepared;
     dim3 grid((p.n_rows + 127) / 128, (p.H * p.D + 127) / 128);
     return launch_dependent(pos_gen_tc_kernel, grid, dim3(kPosThreads), PosSmem::Size, s, p);
 }

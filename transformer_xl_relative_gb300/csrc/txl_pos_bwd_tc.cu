@@ -236,13 +236,9 @@ __global__ void __launch_bounds__(kPBThreads, 1) pos_bwd_tc_kernel(const __grid_
 // dW must be zero on entry (the distance shares add into it).
 cudaError_t launch_pos_bwd_tc(const PosBwdParams& p, int sm_count, cudaStream_t s)
 {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(pos_bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PBSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, PBSmem::Size, pos_bwd_tc_kernel);
+    if (prepared != cudaSuccess) return prepared;
     const int tn = (p.H * p.D + kPBN - 1) / kPBN, tm = (p.d_model + kPBM - 1) / kPBM;
     const int chunks = (p.n_rows + kPBChunk - 1) / kPBChunk;
     // one CTA per SM (its shared memory): as many distance shares as fit one wave

@@ -1036,13 +1036,12 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
     auto* fused_kernel = qattn_kernel<BITS, NG, QT, ONE, true, WIDE>;
     // once per device: the shared memory, clusters of more than eight, and how many clusters of each size the device
     // holds at a time
-    static std::atomic<uint64_t> prepared{0};
+    static OncePerDevice once;
     static std::atomic<int> held[64][kMaxRanks + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t{1} << (dev & 63);
-    if (!(prepared.load(std::memory_order_acquire) & bit)) {
+    e = once([&] {
         for (auto* k : {kernel, fused_kernel}) {
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1064,9 +1063,9 @@ cudaError_t launch(const QattnParams& p, QSplit sp, int groups, int sm_count, cu
             e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
             held[dev & 63][ranks].store(n, std::memory_order_relaxed);
         }
-        if (e != cudaSuccess) return e;
-        prepared.fetch_or(bit, std::memory_order_release);
-    }
+        return e;
+    });
+    if (e != cudaSuccess) return e;
     // Key ranges: the cluster size whose waves of clusters, each over 1/ranks of the keys, take the least time, while
     // each warp keeps a stage.  A GPC holds a whole number of clusters, so that large ones leave SMs idle: 16 heads of
     // one sequence fit in one wave as clusters of up to 13 (65536 4-bit keys: 48.4 us when chosen), not of 16 (55.6; 8: 57.7).

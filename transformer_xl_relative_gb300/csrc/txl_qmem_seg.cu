@@ -12,7 +12,6 @@
 // have no place on the tensor cores without splitting every operand.)  B2 H16 D64, 128 queries over 1500 4-bit
 // keys: 150 us, 16 TFLOP/s; the general fp32 kernel over the memory read back took three times as long.
 #include <algorithm>
-#include <atomic>
 
 #include "txl_internal.h"
 #include "txl_ptx.cuh"
@@ -256,16 +255,9 @@ cudaError_t launch(const QattnParams& p, int sm_count, cudaStream_t s)
     auto* kernel = qseg_f32_kernel<NG>;
     constexpr int bytes = sizeof(SegSmem<NG>);
     static_assert(bytes <= 232448, "a CTA's shared memory");
-    static std::atomic<uint64_t> prepared{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t{1} << (dev & 63);
-    if (!(prepared.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        prepared.fetch_or(bit, std::memory_order_release);
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, bytes, kernel);
+    if (prepared != cudaSuccess) return prepared;
     // key ranges: until every SM has a CTA (with two CTAs each 165 us instead of 150 on the shape above), of a tile at
     // least (two at least: 46 instead of 32 us for 100 queries over 700 keys of 8 heads)
     const int64_t groups = (p.L + kTQ - 1) / kTQ, tiles = (static_cast<int64_t>(p.M) - p.lo + p.L + kTK - 1) / kTK;

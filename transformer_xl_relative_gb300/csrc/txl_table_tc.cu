@@ -275,12 +275,9 @@ bool table_tc_eligible(const TableParams& p, txl_dtype dtype)
 
 cudaError_t launch_table_tc(const TableParams& p, cudaStream_t s)
 {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(table_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TSmem::Size);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t prepared = allow_smem(once, TSmem::Size, table_tc_kernel);
+    if (prepared != cudaSuccess) return prepared;
     const dim3 grid((p.L + kTQ - 1) / kTQ, p.H, p.B);
     table_tc_kernel<<<grid, kTT, TSmem::Size, s>>>(p);
     return cudaGetLastError();
