@@ -46,7 +46,7 @@ __device__ __forceinline__ void add_values_not_finite(const AttnTcParams& p, int
 #pragma unroll
         for (int k = 0; k < 32; ++k)
             if (d0 + k < p.D) {
-                const float x = __uint_as_float(static_cast<uint32_t>(__ldg(v + d0 + k)) << 16);
+                const float x = __uint_as_float(static_cast<uint32_t>(v[d0 + k]) << 16);
                 if (!(fabsf(x) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + x);
             }
 }

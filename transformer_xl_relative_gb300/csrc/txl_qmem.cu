@@ -300,13 +300,13 @@ __device__ __forceinline__ uint2 row_unit(const uint8_t* row, int d0, uint32_t* 
     const uint8_t* k = row + d0 * BITS / 8;
     const uint8_t* v = k + q_v_offset(G, BITS);
     if constexpr (BITS == 4) {
-        ck[0] = __ldg(reinterpret_cast<const uint32_t*>(k));
-        cv[0] = __ldg(reinterpret_cast<const uint32_t*>(v));
+        ck[0] = ld(reinterpret_cast<const uint32_t*>(k));
+        cv[0] = ld(reinterpret_cast<const uint32_t*>(v));
     } else {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(k)), b = __ldg(reinterpret_cast<const uint2*>(v));
+        const uint2 a = ld(reinterpret_cast<const uint2*>(k)), b = ld(reinterpret_cast<const uint2*>(v));
         ck[0] = a.x; ck[1] = a.y; cv[0] = b.x; cv[1] = b.y;
     }
-    return __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + d0 / kQGroup);
+    return ld(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + d0 / kQGroup);
 }
 
 template <int BITS, int G, bool F32>
@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kQThreads) qmem_read_rows_kernel(const __grid_
         const uint8_t* row = head + slot * q_row_bytes(G, BITS);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            par[u][g] = __ldg(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + g);
-            ck[u][g] = __ldg(row + 4 * BITS * g + byte);
-            cv[u][g] = __ldg(row + q_v_offset(G, BITS) + 4 * BITS * g + byte);
+            par[u][g] = ld(reinterpret_cast<const uint2*>(row + q_par_offset(G, BITS)) + g);
+            ck[u][g] = ld(row + 4 * BITS * g + byte);
+            cv[u][g] = ld(row + q_v_offset(G, BITS) + 4 * BITS * g + byte);
         }
     }
 #pragma unroll
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kQThreads, G == 3 ? 6 : 8) qmem_ranges_kernel(
             int64_t s = static_cast<int64_t>(p.slot0) + t;
             if (s >= p.M) s -= p.M;
             if (!in_range(s, 0, p.M, p.chk)) s = 0;
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
+            const uint2 w = ld(reinterpret_cast<const uint2*>(p.rows + (bh * p.M + s) * q_row_bytes(G, BITS) +
                                                                   q_par_offset(G, BITS)) + g);
             auto most = [&](uint32_t kv) {
                 const float step = __uint_as_float(kv << 16), lo = __uint_as_float(kv & 0xffff0000u);

@@ -98,7 +98,16 @@ struct QSplit {               // how the host divides the work
 
 __device__ __forceinline__ float ld_bf16(const void* p, int64_t i)
 {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(ld(static_cast<const uint16_t*>(p) + i)) << 16);
+}
+
+// The rows of r are requested a tile ahead of their use.  The compiler puts plain loads off until then (0.7 us per
+// call); a volatile one stays where it is, after the wait for the kernel that may write r.
+__device__ __forceinline__ uint4 ld_early(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -188,12 +197,12 @@ __device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0,
         for (int G = 0; G < NG; ++G) {
             const int d = 32 * G + 8 * c4;
             if (p.vec_r && d + 8 <= p.D) {
-                a[y][G] = __ldg(reinterpret_cast<const uint4*>(src + d));
+                a[y][G] = ld_early(reinterpret_cast<const uint4*>(src + d));
             } else {
                 uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + d + e)) << (16 * (e & 1));
+                    if (d + e < p.D) w[e >> 1] |= static_cast<uint32_t>(ld(src + d + e)) << (16 * (e & 1));
                 a[y][G] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
@@ -205,8 +214,8 @@ __device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0,
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
 // from global memory as fragments) are requested one tile ahead.  65537 distances of 16 heads: 26 us, 5.1 TB/s.
 // WALK: more tiles than three CTAs per SM; four CTAs per SM (64 registers) then keep more rows in flight (those
-// 65537 distances: the whole call 44.8 us, 62.4 with three); with fewer the free choice of registers (66) is
-// quicker (token over 4096 keys 15.4 us, 16.0 with 64).
+// 65537 distances: the whole call 44.8 us, 62.4 with three); with fewer the free choice of registers (71) is
+// quicker (token over 4096 keys 15.9 us, 16.6 with 64).
 __host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
 template <int NG, bool WALK>
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) qpos_f32_kernel(const __grid_constan
     for (int x = tid; x < pairs * DP; x += kThreads) {
         const int pr = x / DP, d = x % DP, be = (pair0 + pr) / p.L, i = (pair0 + pr) - be * p.L;
         const int64_t at = be * p.q_sb + i * p.q_st + h * p.q_sh + d;
-        q[pr * P + d] = d < p.D ? (__ldg(static_cast<const float*>(p.q) + at) + __ldg(p.vb + h * p.D + d)) * p.qscale : 0.f;
+        q[pr * P + d] = d < p.D ? (ld(static_cast<const float*>(p.q) + at) + __ldg(p.vb + h * p.D + d)) * p.qscale : 0.f;
     }
     __syncthreads();
     const int qp = (warp & 3) * 4 + (lane >> 3), kq = (warp >> 2) * 8 + (lane & 7);
@@ -456,7 +465,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         pdl_launch_dependents();
     }
     // ---- the queries' elements, requested before the copies fill the memory system (raw: the conversion would
-    // wait for them).  qpos_kernel started this grid after everything before it had completed.
+    // wait for them).  qpos_kernel started this grid after everything before it had completed; from L2, because
+    // this grid has not waited itself.
     uint32_t q_raw[NG];
     const bool my_row = warp < Lq;
 #pragma unroll
@@ -465,8 +475,8 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         q_raw[e] = 0;
         if (my_row && d < p.D) {
             const int64_t at = b * p.q_sb + (i0 + warp) * p.q_st + h * p.q_sh + d;
-            if (p.f32) q_raw[e] = __ldg(static_cast<const uint32_t*>(p.q) + at);
-            else q_raw[e] = __ldg(static_cast<const uint16_t*>(p.q) + at);
+            if (p.f32) q_raw[e] = __ldcg(static_cast<const uint32_t*>(p.q) + at);
+            else q_raw[e] = __ldcg(static_cast<const uint16_t*>(p.q) + at);
         }
     }
 
@@ -629,7 +639,7 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int is = min((c4 & (Lp - 1)) + 4 * t, Lq - 1);
-        far_of[t] = p.jn <= j_lo ? 0.f : FUSED ? far_s[is] : __ldg(p.far + bh * p.L + i0 + is);
+        far_of[t] = p.jn <= j_lo ? 0.f : FUSED ? far_s[is] : __ldcg(p.far + bh * p.L + i0 + is);
     }
 #pragma unroll
     for (int n = 0; n < kStages; ++n)
@@ -972,10 +982,10 @@ qattn_kernel(const __grid_constant__ QattnParams p, const __grid_constant__ QSpl
         const int64_t v_at = b * p.vc_sb + h * p.vc_sh + d;
         if (p.f32) {
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? __ldg(static_cast<const uint32_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
+            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? ld(static_cast<const uint32_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
         } else {
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? __ldg(static_cast<const uint16_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
+            for (int j = 0; j < kOwn; ++j) v[j] = j < own ? ld(static_cast<const uint16_t*>(p.vcur) + v_at + j * p.vc_st) : 0u;
         }
         const float* w = weights + row * 32;
         float ot = 0.f;

@@ -55,7 +55,7 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
         const int ii = x / S::DP, d = x % S::DP;
         float a = 0.f, c = 0.f;
         if (ii < Lq && d < p.D) {
-            const float q = __ldg(static_cast<const float*>(p.q) + b * p.q_sb + (i0 + ii) * p.q_st + h * p.q_sh + d);
+            const float q = ld(static_cast<const float*>(p.q) + b * p.q_sb + (i0 + ii) * p.q_st + h * p.q_sh + d);
             a = (q + __ldg(p.u + h * p.D + d)) * p.qscale;
             c = (q + __ldg(p.vb + h * p.D + d)) * p.qscale;
         }
@@ -88,19 +88,19 @@ qseg_f32_kernel(const __grid_constant__ QattnParams p, int ranks, int tiles_per_
                     if (slot >= p.M) slot -= p.M;
                     if (!in_range(slot, 0, p.M, p.chk)) slot = 0;
                     const uint8_t* row = head + slot * row_bytes;
-                    const uint2 par = __ldg(reinterpret_cast<const uint2*>(row + par_off) + d0 / 32);
+                    const uint2 par = ld(reinterpret_cast<const uint2*>(row + par_off) + d0 / 32);
                     uint32_t ck[2], cv[2];
                     const uint8_t* at = row + d0 * p.bits / 8;
-                    ck[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-                    cv[0] = __ldg(reinterpret_cast<const uint32_t*>(at + v_off));
+                    ck[0] = ld(reinterpret_cast<const uint32_t*>(at));
+                    cv[0] = ld(reinterpret_cast<const uint32_t*>(at + v_off));
                     const float ks = __uint_as_float(par.x << 16), kl = __uint_as_float(par.x & 0xffff0000u);
                     const float vs = __uint_as_float(par.y << 16), vl = __uint_as_float(par.y & 0xffff0000u);
                     if (p.bits == 4) {
                         expand8<4>(ck, ks, kl, a);
                         expand8<4>(cv, vs, vl, c);
                     } else {
-                        ck[1] = __ldg(reinterpret_cast<const uint32_t*>(at) + 1);
-                        cv[1] = __ldg(reinterpret_cast<const uint32_t*>(at + v_off) + 1);
+                        ck[1] = ld(reinterpret_cast<const uint32_t*>(at) + 1);
+                        cv[1] = ld(reinterpret_cast<const uint32_t*>(at + v_off) + 1);
                         expand8<8>(ck, ks, kl, a);
                         expand8<8>(cv, vs, vl, c);
                     }

@@ -5,6 +5,11 @@
 
 namespace txl {
 
+// A load of what an earlier kernel may have written: this grid may start before that one has ended, so that the data
+// is not read-only while it runs, as __ldg wants it (that is for u and v alone).  After pdl_wait.
+template <typename T>
+__device__ __forceinline__ T ld(const T* p) { return *p; }
+
 // Eight channels d0 .. d0+7 of a row; channels at or past D read as 0.  vec: the row starts on a 16-byte boundary.
 template <bool F32>
 __device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, float* x)
@@ -12,11 +17,11 @@ __device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, 
     if (vec && d0 + 8 <= D) {
         if constexpr (F32) {
             const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + d0);
-            const float4 a = __ldg(q), b = __ldg(q + 1);
+            const float4 a = ld(q), b = ld(q + 1);
             x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
             x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
         } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + d0));
+            const uint4 a = ld(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + d0));
             const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -30,8 +35,8 @@ __device__ __forceinline__ void load8(const void* row, int d0, int D, bool vec, 
     for (int e = 0; e < 8; ++e) {
         x[e] = 0.f;
         if (d0 + e < D) {
-            if constexpr (F32) x[e] = __ldg(static_cast<const float*>(row) + d0 + e);
-            else x[e] = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
+            if constexpr (F32) x[e] = ld(static_cast<const float*>(row) + d0 + e);
+            else x[e] = __uint_as_float(static_cast<uint32_t>(ld(static_cast<const uint16_t*>(row) + d0 + e)) << 16);
         }
     }
 }
