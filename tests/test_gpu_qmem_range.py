@@ -294,3 +294,29 @@ def test_query_groups_of_unlike_size(txl, octaves, bits, L):
     call.push_again(txl, 9)
     call.go(txl)
     groups_within(call, GROUP_BOUND["f32"])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [41, 64, 96, 128])
+def test_segments_keep_fp16s_bits(txl, D, bits):
+    """Ordinary values: operands, position terms and weights deviate by fp16's 2^-11 / sqrt(3) of their value at
+    most, twice that with the argument of the exponential, and the output by its own rounding, 2^-8 / sqrt(3) at
+    most.  In the norm over all outputs the two add in squares.  (Rounding the operands to bf16 comes to
+    four times what fp16 is allowed here.)"""
+    call = Ranged(txl, 2, 3, D, 100, 700, 700, 9, 500, bits, "bf16")
+    call.go(txl)
+    ref, var = attend(*call.operands_as_given(), call.C)
+    most = np.sqrt(((2.0 ** -8 / np.sqrt(3) * ref) ** 2 + (2 * 2.0 ** -11 / np.sqrt(3)) ** 2 * var).sum())
+    assert np.linalg.norm(f64(call.out) - ref) <= most
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("c", [(2, 3, 64, 100, 1500), (1, 2, 128, 33, 700), (2, 1, 41, 17, 3000)])
+def test_fp32_segments_keep_their_bits(txl, c, bits):
+    """Products and sums in fp32, sums of at most 64 terms joined: each off by less than 2^-24 times sqrt(64) of
+    its size; the exponential by 2^-22: a term of the output by less than 2^-20, and a factor of two for the sums."""
+    B, H, D, L, M = c
+    call = Ranged(txl, B, H, D, L, M, M, 5, 1000, bits, "f32")
+    call.go(txl)
+    ref, _ = attend(*call.operands_as_given(), call.C)
+    assert np.linalg.norm(f64(call.out) - ref) <= 2.0 ** -19 * np.linalg.norm(ref)
