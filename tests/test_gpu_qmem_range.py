@@ -320,3 +320,17 @@ def test_fp32_segments_keep_their_bits(txl, c, bits):
     call.go(txl)
     ref, _ = attend(*call.operands_as_given(), call.C)
     assert np.linalg.norm(f64(call.out) - ref) <= 2.0 ** -19 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [2, 4, 9, 16])
+@pytest.mark.parametrize("key,value", [(NAN, INF), (INF, NAN), (3e38, -3e38)], ids=str)
+def test_few_queries_see_no_later_key(txl, key, value, L, dtype):
+    """Up to 16 queries: what an own key or value holds reaches the queries from its position on."""
+    for M in (0, 100, 1500):
+        call = Ranged(txl, 2, 2, 64, L, M, M, 7 if M else 0, 1000, 4, dtype)
+        n = (L + 1) // 2
+        call.v[:, n:] = value
+        call.k[:, n:] = key
+        call.go(txl)
+        check(call, slice(0, n) if key == 3e38 else slice(None))
