@@ -42,8 +42,8 @@
 // of a head are the ranks of a cluster: each writes its partial results into the shared memory of the
 // rank that finishes the row.
 //
-// Measured (both kernels, B8 H16 D64, one query): 4096 keys of 4 bits 15.4 us (44 MB; 6.5 us of HBM), of 8 bits
-// 19.9 us (78 MB), 16384 keys of 4 bits 34.4 us (170 MB, 4.9 TB/s; 6.6 TB/s of what each further key adds).
+// Measured (both kernels, B8 H16 D64, one query): 4096 keys of 4 bits 15.8 us (44 MB; 6.5 us of HBM), of 8 bits
+// 20.0 us (78 MB), 16384 keys of 4 bits 35.6 us (170 MB, 4.8 TB/s; 6.4 TB/s of what each further key adds).
 // The bf16 memory's decode takes 40 us at 4096 keys.  Two CTAs of eight warps fill the registers of an SM; of
 // a token's 12 us in the kernel 3 are the prologue (the copies of half the memory are in flight), 2.5 the
 // merge.  The loop is latency: every shared-memory access is free of bank conflicts (with the parts of q in the
@@ -214,8 +214,8 @@ __device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0,
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
 // from global memory as fragments) are requested one tile ahead.  65537 distances of 16 heads: 26 us, 5.1 TB/s.
 // WALK: more tiles than three CTAs per SM; four CTAs per SM (64 registers) then keep more rows in flight (those
-// 65537 distances: the whole call 44.8 us, 62.4 with three); with fewer the free choice of registers (71) is
-// quicker (token over 4096 keys 15.9 us, 16.6 with 64).
+// 65537 distances: the whole call 45.2 us, 62.4 with three); with fewer the free choice of registers (69) is
+// quicker (token over 4096 keys 15.8 us, 16.6 with 64).
 __host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
 template <int NG, bool WALK>

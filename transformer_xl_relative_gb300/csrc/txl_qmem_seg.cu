@@ -8,9 +8,10 @@
 // four keys (16 apart), so that five rows of r serve its eight pairs.  Key ranges are the ranks of a cluster, joined
 // through shared memory, because 32 queries of few heads fill few SMs.
 //
-// Bound by shared memory: 13 loads of 16 bytes for 64 multiply-adds of the scores, 6 for 32 of P.V.  (fp32 products
-// have no place on the tensor cores without splitting every operand.)  B2 H16 D64, 128 queries over 1500 4-bit
-// keys: 150 us, 16 TFLOP/s; the general fp32 kernel over the memory read back took three times as long.
+// Bound by shared memory: 13 loads of 16 bytes for 64 multiply-adds of the scores, 6 for 32 of P.V.  (CUDA cores: on the
+// tensor cores the codes could be multiplied as they are, as the kernel of few queries does, but q, the weights,
+// r and the segment's own keys and values would have to be split.)  B2 H16 D64, 128 queries over 1500 4-bit keys: 150 us,
+// 16 TFLOP/s; the general fp32 kernel over the memory read back took three times as long.
 #include <algorithm>
 
 #include "txl_internal.h"
@@ -259,7 +260,7 @@ cudaError_t launch(const QattnParams& p, int sm_count, cudaStream_t s)
     const cudaError_t prepared = allow_smem(once, bytes, kernel);
     if (prepared != cudaSuccess) return prepared;
     // key ranges: until every SM has a CTA (with two CTAs each 165 us instead of 150 on the shape above), of a tile at
-    // least (two at least: 46 instead of 32 us for 100 queries over 700 keys of 8 heads)
+    // least (two at least: 46 instead of 28 us for 100 queries over 700 keys of 8 heads)
     const int64_t groups = (p.L + kTQ - 1) / kTQ, tiles = (static_cast<int64_t>(p.M) - p.lo + p.L + kTK - 1) / kTK;
     int ranks = 1;
     while (ranks < kMaxRanks && groups * p.H * p.B * ranks < sm_count && tiles >= 2 * ranks) ranks *= 2;
