@@ -334,3 +334,28 @@ def test_few_queries_see_no_later_key(txl, key, value, L, dtype):
         call.k[:, n:] = key
         call.go(txl)
         check(call, slice(0, n) if key == 3e38 else slice(None))
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN], ids=str)
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L,M", [(1, 1200), (3, 200), (16, 600), (1, 150)])
+def test_few_queries_values_that_are_not_finite(txl, L, M, dtype, where, value):
+    """As test_segment_values_that_are_not_finite for up to 16 queries, with the position terms in a kernel of their own
+    and in the attention kernel."""
+    call = Ranged(txl, 2, 2, 64, L, M, M, 9, 100 if where.startswith("clamped") else 2000, 4, dtype)
+    if where == "q":
+        call.q[1, L // 2, 0, 3] = value
+    elif where == "first own key":
+        call.k[1, 0, 0, 3] = value
+    elif where == "first own value":
+        call.v[1, 0, 0, 3] = value
+    elif where == "position row":
+        call.r[3, 1, 5] = value
+    elif where == "clamped position row":
+        call.r[100, 1, 5] = value
+    else:
+        (call.kh if where == "memory key" else call.vh)[1, 77, 0, 3] = value
+        call.push_again(txl, 9)
+    call.go(txl)
+    check(call)

@@ -183,6 +183,10 @@ __device__ __forceinline__ uint32_t pair_odd(uint32_t w)
     return WIDE ? add_f16x2(c | 0x64006400u, 0xe480e480u) : c;                                // less 1152
 }
 
+// A position term from the products with the high and the low part of q+v.  An infinity of r meets a low part of 0 or
+// of the other sign: the high part has the answer.
+__device__ __forceinline__ float both_parts(float hi, float lo) { return fabsf(hi) < INFINITY ? hi + lo : hi; }
+
 // Rows of r of 16 distances from d0 as the A operand's fragments: this lane's of distances g and g + 8.
 template <int NG>
 __device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0, uint4 (&a)[2][NG])
@@ -214,7 +218,7 @@ __device__ __forceinline__ void load_r(const QattnParams& p, int h, unsigned d0,
 // (the B operands) and walks over tiles of 128 distances, 16 per warp, whose rows of r (the A operands, read
 // from global memory as fragments) are requested one tile ahead.  65537 distances of 16 heads: 26 us, 5.1 TB/s.
 // WALK: more tiles than three CTAs per SM; four CTAs per SM (64 registers) then keep more rows in flight (those
-// 65537 distances: the whole call 45.2 us, 62.4 with three); with fewer the free choice of registers (69) is
+// 65537 distances: the whole call 45.2 us, 62.4 with three); with fewer the free choice of registers (75) is
 // quicker (token over 4096 keys 15.8 us, 16.6 with 64).
 __host__ __device__ constexpr int pos_pairs(int ng) { return ng == 2 ? 64 : 32; }
 
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, NG > 2 ? 2 : WALK ? 4 : 0) qpos_kern
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int delta = static_cast<int>(d0 + g + 8 * y);
-                    const float v = acc[2 * y] + acc[2 * y + 1];
+                    const float v = both_parts(acc[2 * y], acc[2 * y + 1]);
                     if (delta <= x0) e[-delta] = v;
                     if (delta == p.C) *far_at[pr] = v;
                 }
@@ -375,13 +379,13 @@ __device__ __forceinline__ void own_terms(const QattnParams& p, const uint16_t* 
                 const int row = 4 * ct + c4;
                 if (row >= Lq) continue;
                 if (clamp) {
-                    if (g == 0) far_s[row] = acc[0] + acc[1];
+                    if (g == 0) far_s[row] = both_parts(acc[0], acc[1]);
                     continue;
                 }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int j = p.M + i0 + row - (d0 + g + 8 * y);
-                    if (j >= ja && j < jb) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = acc[2 * y] + acc[2 * y + 1];
+                    if (j >= ja && j < jb) e_row0[static_cast<int64_t>(row) * p.e_pitch + (j - p.jn)] = both_parts(acc[2 * y], acc[2 * y + 1]);
                 }
             }
         };
