@@ -510,7 +510,9 @@ txl_status txl_qmem_read_call(const txl_qmem_kv_args* args);
  * L <= 16 (generation), two launches, or one where few positions are not clamped: the position terms
  * (q+v).r go into the workspace, then the codes are multiplied as they are (q and the weights, each group of 32
  * channels in units of its own, held to 22 bits, or to 2^-34 of the group's largest where that is more; fp32
- * calls keep sums to fp32's precision, bf16 ones to 15 bits).
+ * calls keep sums to fp32's precision, bf16 ones to 15 bits).  A position whose step in a group of values is far
+ * above the others' costs the group bits: its sums are then off by up to 2^-12 of that position's weighted step,
+ * in fp32 2^-14 (what it stands for is off by up to half a step from what was pushed).
  * L > 16, bf16, four launches (three for D > 64): K and V of the memory's valid positions and of the segment,
  * and r, are written into the workspace once in 16 bits, and the fused tcgen05 kernels of txl_rel_attn_fwd run
  * over them, for q, k_cur, v_cur and r of any layout.  A (b, h) has fp16 operands and P, in units of powers of

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from qmem_common import f64
+from qmem_common import attend64, decode_tolerance, f64, quantise64
 from test_gpu_qmem_attn import Call
 
 pytestmark = pytest.mark.gpu
@@ -359,3 +359,32 @@ def test_few_queries_values_that_are_not_finite(txl, L, M, dtype, where, value):
         call.push_again(txl, 9)
     call.go(txl)
     check(call)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("octaves", [12, 40])
+@pytest.mark.parametrize("L", [1, 4, 16])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_one_position_with_a_step_far_above_the_others(txl, bits, L, octaves, dtype):
+    """One element of 2^octaves makes its group's step there that large: the group's sums are off by no more than
+    2^-12 (fp32: 2^-14) of the weighted steps.  (bf16: one product is aligned to the position's, whose code counts as
+    1024 at most, and drops what lies 24 bits below: 2^-14 of its weighted step.  fp32: the centred codes of at most 128
+    cancel against lo + 128 step, 2^-17, in a sum of some ten terms per lane.  Weights 2^-33 below the largest are
+    lost: 900 of them times 255 come to 2^-15.)"""
+    call = Ranged(txl, 2, 2, 64, L, 900, 900, 9, 500, bits, dtype)
+    call.vh[:, 50, :, 5] = 2.0 ** octaves
+    call.push_again(txl, 9)
+    call.go(txl)
+    q, k, v, u, vb, r = call.operands_as_given()
+    step = quantise64(f64(call.vh), bits)[1].repeat(32, -1)
+    weighted, _ = attend(q, k, np.concatenate((step, np.zeros_like(v[:, -L:])), 1), u, vb, r, call.C)
+    ref, size = attend64(q, k, v, u, vb, r, call.C)
+    rest = np.delete(v, 50, 1)
+    tol = decode_tolerance(ref, size, np.abs(rest).max(), call.dtype)
+    # (what an error of the scores makes of that position's value is its weight times that error times the value)
+    ds = (2.0 ** -16 if dtype == "f32" else 2.0 ** -15) * size
+    at = np.abs(v[:, 50:51])
+    p = weighted / np.maximum(step[:, 50:51], 1e-300)
+    tol = tol + 4 * ds * np.minimum(p, 1.0) * at + 2.0 ** (-14 if dtype == "f32" else -12) * weighted
+    err = np.abs(f64(call.out) - ref)
+    assert (err <= tol).all(), float((err / tol).max())
