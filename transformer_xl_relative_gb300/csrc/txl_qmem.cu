@@ -101,8 +101,9 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
 // Per channel: minimum and maximum (of bf16 inputs in pairs); d = x - lo; y = d / step + 1.5 2^23, whose low bits are
 // the rounded quotient c; the remainder e = d - c step, which is exact, and its comparison; and a shift-add into the
 // code word, the constant bits of the y subtracted once.  (In all 31 instructions per channel of a lane: the group's
-// parameters, which each of its four lanes computes, addresses, conversions and near ties among them.)  Where |e| comes to half a step (bf16 inputs: one
-// channel in 300 at 4 bits, exact ties) the channel is decided again, with what the subtraction x - lo lost.
+// parameters, which each of its four lanes computes, addresses, conversions and near ties among them.)  Where |e|
+// comes to half a step (bf16 inputs: one channel in 300 at 4 bits, exact ties) the channel is decided again, with what
+// the subtraction x - lo lost.
 template <int BITS, bool ALL, bool F32>
 __device__ __forceinline__ void quantise8(const float* xin, int live, uint32_t* code, float& step, float& lo)
 {
