@@ -40,7 +40,8 @@ typedef enum {
     TXL_ERR_ALIGNMENT = 3,     /* a base address or stride is not 16-byte aligned where needed */
     TXL_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed                            */
     TXL_ERR_TIMEOUT = 5,       /* written to err_flag by a kernel whose bounded wait expired   */
-    TXL_ERR_WORKSPACE = 6      /* workspace missing or smaller than txl_rel_attn_workspace_size */
+    TXL_ERR_WORKSPACE = 6,     /* workspace missing or smaller than txl_rel_attn_workspace_size */
+    TXL_ERR_PAGE = 7           /* written to a paged memory's err_flag: a position without a page */
 } txl_status;
 
 typedef enum { TXL_F32 = 0, TXL_BF16 = 1 } txl_dtype;
@@ -565,6 +566,147 @@ size_t txl_rel_attn_qmem_workspace_size(int B, int L, int H, int D, const txl_qm
 int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const txl_qmem* mem,
                            const txl_view* k_cur, const txl_view* v_cur, const void* r,
                            int64_t ld_r, const txl_view* out, txl_dtype dtype);
+
+/*
+ * Paged K/V memory: the cached keys and values of B sequences of different lengths in pages of one pool (a service of
+ * this library; the pages of the reference hold one length for the batch).  Slot s of sequence b is row s mod page_len
+ * of page table[b][s / page_len]; a sequence uses its slots 0 .. length[b]-1.  Each slot holds a position (the
+ * attention takes distances from it, so slots may be in any order, and positions may be missing), and the attention
+ * weight that it has received so far.  The positions of a sequence are distinct and below next_pos[b], that of its next
+ * one.  Lengths, positions and table are device memory: a captured graph of calls may be replayed, and each replay works
+ * on what the memory then holds.
+ *   k, v     : device, 16-byte aligned, [n_pages][H][page_len][ld] of dtype; ld >= D, rows of a multiple of 16 bytes.
+ *              What a row holds at and past D is never used (pushes write zeros there).
+ *   pos, weight : device [n_pages][page_len], 16-byte aligned.
+ *   table    : device [B][max_pages]; entries outside 0 .. n_pages-1 are no page.  A page that a push, an eviction or the
+ *              sum of weights writes belongs to one sequence; pages that are only read may be shared.
+ *   length, next_pos : device [B];  arrivals : device [B], zero (pushes leave it so).
+ *   err_flag : optional device int: a call that meets a slot without a page writes TXL_ERR_PAGE there if it is 0 (never
+ *              cleared by the library).  Such a slot counts as not there; a push that does not find pages for all new
+ *              positions of a sequence leaves that sequence as it was, and its queries' outputs too.
+ * Limits (TXL_ERR_UNSUPPORTED): D <= 128; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
+ * max_pages * page_len below 2^31.  Positions are ints.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int* pos;
+    float* weight;
+    const int* table;
+    int* length;
+    int* next_pos;
+    int* arrivals;
+    int* err_flag;
+    int B, H, D, ld, n_pages, page_len, max_pages;
+    int dtype;                 /* a txl_dtype */
+} txl_paged;
+
+/*
+ * txl_paged_push -- new positions of every sequence: rows t < counts[b] of k_new, v_new [B][T][H][D] (device views of
+ * the memory's dtype) into slots length[b] + t, with positions next_pos[b] + t and weight 0; then length[b] and next_pos[b]
+ * advance by counts[b].  counts: device [B] (values outside 0 .. T count as 0 or T), or NULL for T each.  Rows past
+ * counts[b] are not read.  Bit-exact copy; any strides.  T = 0: nothing to do.
+ */
+txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl_view* v_new, int T, const int* counts,
+                          void* stream);
+
+/*
+ * txl_rel_attn_paged -- relative attention of T = 1 .. 16 new tokens a sequence over a paged memory (incremental
+ * generation, "Transformer-XL架构解析" §3.2: each new token attends to the cached memory and itself).  With k_new, v_new
+ * the call first pushes them as txl_paged_push does; with both NULL the last counts[b] positions of each sequence are in
+ * the memory already.  Query i < counts[b] of sequence b has position p_i = next_pos[b] - counts[b] + i (next_pos after
+ * the push), slot j position p_j:
+ *   visible(i, j) <=> p_j <= p_i,   delta = min(p_i - p_j, clamp_len, n_rows - 1)
+ *   s_ij  = scale * ( q_i.k_j + q_i.r[delta] + u_h.k_j + v_h.r[delta] )
+ *   out_i = sum_j softmax_j(s_ij over visible j) * v_j       (0 where nothing is visible)
+ * Rows i >= counts[b] of out are left as they were (and those of q not read).
+ *   u, v_bias, r, ld_r, scale : as txl_rel_attn_fwd;  n_rows >= 1 rows of r.
+ *   accumulate : not 0: weight[j] += sum over heads and queries of softmax_j(s_ij), for txl_paged_evict (a slot's weight
+ *              is the sum over the calls since it entered).
+ *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_paged_workspace_size bytes (TXL_ERR_WORKSPACE).
+ *              Calls that share a workspace, or a memory, must not overlap on the GPU.
+ * The slots of all (sequence, head) pairs are cut into equal shares for the blocks, whatever the lengths.  bf16: mma.sync
+ * products; scale log2(e) (q + u), scale log2(e) (q + v) and the weights of the softmax are held to 16 bits (two bf16
+ * each).  f32: fp32 arithmetic on the CUDA cores.  The result does not depend on the order in which blocks run.  A key or value
+ * that a query does not see does not reach it, whatever it is.  Two launches, three with accumulate.
+ */
+typedef struct {
+    int T, clamp_len, n_rows, accumulate;
+    float scale;
+    const txl_paged* mem;
+    txl_view q, k_new, v_new, out;
+    const int* counts;
+    const float* u;
+    const float* v_bias;
+    const void* r;
+    int64_t ld_r;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+} txl_rel_attn_paged_args;
+txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* args);
+
+/* Bytes of device workspace txl_rel_attn_paged needs for n_rows distances (min(n_rows, clamp_len + 1) are enough): mostly
+ * B*H*T floats a distance, with accumulate as many a slot of max_pages pages, and parts of the sums (1280 T rows of D
+ * floats).  0 for an invalid shape. */
+size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate);
+
+/*
+ * txl_paged_evict -- cut every sequence to `keep` positions: of a sequence with more, the length[b] - keep slots of
+ * the least weight leave (of equal weights the older positions; NaN counts as the largest weight), but none of the last
+ * `recent` positions (those >= next_pos[b] - recent).  The survivors in slots >= keep move, in order, into the
+ * slots that became free in front (keys, values, position, weight), and length[b] = keep.  Other slots are left as
+ * they were; next_pos does not change, so later tokens keep their distances.  keep >= 1, 0 <= recent <= keep.
+ *   workspace : device scratch, 16-byte aligned, of txl_paged_evict_workspace_size(mem) bytes.
+ * A sequence that has a slot without a page is left as it was.  Two launches.
+ */
+txl_status txl_paged_evict(const txl_paged* mem, int keep, int recent, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Bytes of device workspace txl_paged_evict needs: two ints a sequence and slot of half the sequence's capacity. */
+size_t txl_paged_evict_workspace_size(const txl_paged* mem);
+
+/*
+ * 4-bit weights: a matrix W [k][n] held as codes of 4 bits; each column's entries k in groups of 32, 64 or 128 (the last
+ * group shorter) share
+ *     lo   = the largest bf16 that is not above the group's least entry
+ *     step = the smallest bf16 that is not below (most - lo) / 15
+ *     c    = the integer nearest to (w - lo) / step, ties to even (0 where step = 0)
+ * and stand for w' = lo + step c (differences and quotients in double precision).  A group with a NaN or an infinity, or
+ * whose step is not finite, stands for NaN throughout.
+ *   data : device, 16-byte aligned, txl_q4_bytes(k, n, group) bytes: the codes as the kernels' lanes read them (16 columns
+ *          by 64 k in 512 bytes), then the groups' parameters.
+ */
+typedef struct {
+    void* data;
+    int k, n;
+    int group;
+} txl_q4;
+
+/* Bytes of a matrix of 4-bit weights (0 for an invalid shape): k, n >= 1 and at most 2^21, group 32, 64 or 128. */
+size_t txl_q4_bytes(int k, int n, int group);
+
+/* Quantise device bf16 W [k][ld_w] (columns 0 .. n-1 are read; any alignment) into w->data. */
+txl_status txl_q4_quantise(const txl_q4* w, const void* W, int64_t ld_w, void* stream);
+
+/* What the codes stand for, rounded to bf16 once, into device bf16 W [k][ld_w] (columns 0 .. n-1 are written). */
+txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
+
+/*
+ * txl_linear_q4 -- Y = X W' for bf16 X [m][ld_x] (columns 0 .. k-1 are read) and 4-bit weights: txl_linear with a quarter
+ * of the weights' bytes, for the projections of a generated token.  Y bf16 [m][ld_y], columns 0 .. n-1 are written.
+ * Up to 64 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
+ * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry of x that is not finite makes its row of
+ * Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
+ *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
+ *            may be NULL when that is 0).  Calls that share a workspace must not overlap on the GPU.
+ * Limits: m >= 0 (0: nothing to do), m <= 2^20; ld_x >= k, ld_y >= n.  err_flag as txl_linear.
+ */
+txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, void* Y, int64_t ld_y, void* workspace,
+                         size_t workspace_bytes, int* err_flag, void* stream);
+
+/* Bytes of device workspace txl_linear_q4 needs: 0 for m <= 64, else 2 k (n rounded up to a multiple of 8). */
+size_t txl_linear_q4_workspace_size(int m, const txl_q4* w);
 
 /*
  * Checked build.  libtxl_checked.so is this library compiled with -DTXL_CHECKED (the package builds

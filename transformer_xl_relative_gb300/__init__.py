@@ -7,9 +7,16 @@ Importing the package loads the library and fails loudly if it has not been buil
 from . import native
 from .api import (  # noqa: F401
     Memory,
+    PagedMemory,
     QuantMemory,
+    QuantWeight,
     linear,
+    linear_q4,
+    linear_q4_workspace_size,
     mem_push,
+    paged_evict,
+    paged_evict_workspace_size,
+    paged_push,
     qmem_push,
     qmem_read,
     rel_attn_bwd,
@@ -22,6 +29,8 @@ from .api import (  # noqa: F401
     rel_attn_layer_workspace_size,
     rel_attn_layer_fused,
     rel_attn_layer_fused_workspace_size,
+    rel_attn_paged,
+    rel_attn_paged_workspace_size,
     rel_attn_path,
     rel_attn_qmem,
     rel_attn_qmem_path,

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import native
-from .native import TxlMem, TxlQmem, TxlView, check
+from .native import TxlMem, TxlPaged, TxlQ4, TxlQmem, TxlView, check
 
 _DTYPES = {torch.float32: native.TXL_F32, torch.bfloat16: native.TXL_BF16}
 
@@ -565,6 +565,328 @@ def rel_attn_qmem_path(q, mem, k_cur, v_cur, r, out) -> int:
     vq, vk, vv, vo = view(q), view(k_cur), view(v_cur), view(out)
     return _lib().txl_rel_attn_qmem_path(B, L, H, D, ctypes.byref(vq), memc, ctypes.byref(vk), ctypes.byref(vv),
                                          r.data_ptr(), r.stride(1), ctypes.byref(vo), dtype_code(q))
+
+
+class PagedMemory:
+    """K/V memory of B sequences of different lengths in pages of one pool (txl_paged).
+
+    ``k``/``v`` are [n_pages, H, page_len, D] (rows padded to 16 bytes), ``pos`` int32 and ``weight`` fp32 [n_pages,
+    page_len], ``table`` int32 [B, max_pages], ``length`` and ``next_pos`` int32 [B], all on one device: slot s of
+    sequence b is row s % page_len of page table[b, s // page_len].  Filled by paged_push and rel_attn_paged, cut by
+    paged_evict.  The host gives pages to sequences: reserve before positions are pushed, release for a sequence that has
+    ended, trim for pages that an eviction left empty."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, table: torch.Tensor,
+                 length: torch.Tensor, next_pos: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be [n_pages, H, page_len, D] of one shape, layout and dtype")
+        if not k.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        n, H, page_len, D = k.shape
+        ld = k.stride(2)
+        if k.stride(3) != 1 or k.stride(1) != page_len * ld or (n > 1 and k.stride(0) != H * page_len * ld):
+            raise ValueError("pages must be dense [n_pages, H, page_len, ld], the first D of each row")
+        dev = k.get_device()
+        for t, shape, dtype, what in ((pos, (n, page_len), torch.int32, "pos"), (weight, (n, page_len), torch.float32, "weight"),
+                                      (table, None, torch.int32, "table"), (length, table.shape[:1], torch.int32, "length"),
+                                      (next_pos, table.shape[:1], torch.int32, "next_pos")):
+            if t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev or (
+                    t.dim() != 2 if shape is None else t.shape != torch.Size(shape)):
+                raise ValueError("%s must be a contiguous %s%s on the pages' device"
+                                 % (what, dtype, "" if shape is None else " " + str(list(shape))))
+        self.k, self.v, self.pos, self.weight = k, v, pos, weight
+        self.table, self.length, self.next_pos, self.device = table, length, next_pos, dev
+        B, most = table.shape
+        self._scratch = torch.zeros(B + 1, dtype=torch.int32, device=k.device)     # arrivals, err_flag
+        at = self._scratch.data_ptr()
+        self._c = TxlPaged(k.data_ptr(), v.data_ptr(), pos.data_ptr(), weight.data_ptr(), table.data_ptr(),
+                           length.data_ptr(), next_pos.data_ptr(), at, at + 4 * B, B, H, D, ld, n, page_len, most, dtype_code(k))
+        self.address = ctypes.addressof(self._c)
+        self._shape, self._dtype = (B, H, D), k.dtype
+        rows = table.tolist()
+        used = {p for row in rows for p in row if 0 <= p < n}
+        self._rows = [[p for p in row if 0 <= p < n] for row in rows]              # pages of every sequence
+        self._free = [p for p in range(n - 1, -1, -1) if p not in used]
+        self._room = length.tolist()                                               # positions that room was asked for
+
+    @classmethod
+    def empty(cls, B, n_pages, page_len, H, D, max_pages=None, dtype=torch.bfloat16, device="cuda"):
+        """An empty memory; a sequence may hold up to max_pages pages (all of them by default)."""
+        unit = 16 // torch.empty(0, dtype=dtype).element_size()
+        ld = (D + unit - 1) // unit * unit
+        k, v = (torch.zeros(n_pages, H, page_len, ld, dtype=dtype, device=device)[..., :D] for _ in range(2))
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(k, v, torch.zeros(n_pages, page_len, **i32), torch.zeros(n_pages, page_len, device=device),
+                   torch.full((B, n_pages if max_pages is None else max_pages), -1, **i32),
+                   torch.zeros(B, **i32), torch.zeros(B, **i32))
+
+    @property
+    def c_struct(self) -> TxlPaged:
+        return self._c
+
+    @property
+    def page_len(self) -> int:
+        return self._c.page_len
+
+    @property
+    def free_pages(self) -> int:
+        """Pages that no sequence has."""
+        return len(self._free)
+
+    def reserve(self, positions) -> None:
+        """Pages for `positions` more positions of every sequence (an int, or one of each).  A pushed position must
+        have been reserved; one that was reserved and then not pushed keeps its room until trim.  Raises, and changes
+        nothing, when the pool or a sequence's row of the table is too small."""
+        B = self._shape[0]
+        more = [positions] * B if isinstance(positions, int) else [int(x) for x in positions]
+        if len(more) != B or min(more, default=0) < 0:
+            raise ValueError("reserve takes a number of positions, or one for each sequence")
+        L = self.page_len
+        want = [(r + m + L - 1) // L - len(p) if m else 0 for r, m, p in zip(self._room, more, self._rows)]
+        if any(w > 0 and len(p) + w > self._c.max_pages for w, p in zip(want, self._rows)):
+            raise ValueError("a sequence takes at most %d pages" % self._c.max_pages)
+        if sum(w for w in want if w > 0) > len(self._free):
+            raise ValueError("the pool has %d free pages" % len(self._free))
+        for p, w in zip(self._rows, want):
+            p.extend(self._free.pop() for _ in range(w))
+        self._room = [r + m for r, m in zip(self._room, more)]
+        if any(w > 0 for w in want):
+            self._write_table()
+
+    def release(self, b: int) -> None:
+        """Sequence b has ended: it is empty, and its pages are free."""
+        self._free.extend(reversed(self._rows[b]))
+        self._rows[b], self._room[b] = [], 0
+        self._write_table()
+        with torch.cuda.device(self.device):
+            self.length[b] = 0
+            self.next_pos[b] = 0
+
+    def trim(self) -> None:
+        """Frees the pages that hold no position (reads the lengths: waits for the device)."""
+        self._room = self.length.tolist()
+        L = self.page_len
+        for p, n in zip(self._rows, self._room):
+            keep = (n + L - 1) // L
+            self._free.extend(reversed(p[keep:]))
+            del p[keep:]
+        self._write_table()
+
+    def check(self) -> None:
+        """Raises if a call met a slot without a page since the last check (waits for the device)."""
+        with torch.cuda.device(self.device):
+            flag = int(self._scratch[-1])
+            self._scratch[-1] = 0
+        check(flag, "paged memory")
+
+    def _write_table(self) -> None:
+        most = self._c.max_pages
+        host = torch.tensor([p + [-1] * (most - len(p)) for p in self._rows], dtype=torch.int32).view(self.table.shape)
+        with torch.cuda.device(self.device):
+            self.table.copy_(host)
+
+
+def _paged_counts(mem: PagedMemory, counts) -> int:
+    if counts is None:
+        return 0
+    if counts.dtype != torch.int32 or counts.shape != mem._shape[:1] or not counts.is_contiguous() or counts.get_device() != mem.device:
+        raise ValueError("counts must be a contiguous int32 [B] on the memory's device")
+    return counts.data_ptr()
+
+
+def paged_push(mem: PagedMemory, k_new: torch.Tensor, v_new: torch.Tensor, counts: torch.Tensor | None = None,
+               stream=None) -> PagedMemory:
+    """New positions of every sequence into its reserved pages (txl_paged_push): rows t < counts[b] (int32 [B], all
+    T without it) of k_new, v_new [B, T, H, D]."""
+    B, H, D = mem._shape
+    T = k_new.shape[1] if k_new.dim() == 4 else 0
+    if k_new.shape != (B, T, H, D) or v_new.shape != k_new.shape:
+        raise ValueError("expected k_new and v_new [%d, T, %d, %d]" % (B, H, D))
+    if k_new.dtype != mem._dtype or v_new.dtype != mem._dtype:
+        raise TypeError("k_new and v_new must have the memory's dtype")
+    if k_new.get_device() != mem.device or v_new.get_device() != mem.device:
+        raise ValueError("tensors must live on the memory's device")
+    vk, vv, n = view(k_new), view(v_new), _paged_counts(mem, counts)
+    raw = _raw_stream(stream, mem.device)
+    st = _on_device(mem.device, lambda _: _lib().txl_paged_push(ctypes.byref(mem._c), ctypes.byref(vk), ctypes.byref(vv), T,
+                                                                n, raw), None)
+    check(st, "txl_paged_push")
+    return mem
+
+
+def rel_attn_paged_workspace_size(q: torch.Tensor, mem: PagedMemory, n_rows: int, accumulate: bool = False) -> int:
+    """Bytes of workspace rel_attn_paged needs (txl_rel_attn_paged_workspace_size)."""
+    return int(_lib().txl_rel_attn_paged_workspace_size(ctypes.byref(mem._c), q.shape[1], int(n_rows), int(accumulate)))
+
+
+def _paged_refusal(q, mem, k_new, v_new, u, v_bias, r, n_rows, out):
+    """Raises what is wrong with the arguments of rel_attn_paged (called when something is)."""
+    B, H, D = mem._shape
+    given = [t for t in (q, k_new, v_new, out) if t is not None]
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new come together")
+    if any(t.dtype != mem._dtype for t in (*given, r)):
+        raise TypeError("q, k_new, v_new, r and out must have the memory's dtype")
+    if u.dtype != torch.float32 or v_bias.dtype != torch.float32:
+        raise TypeError("u and v_bias are fp32 [H, D]")
+    if any(t.get_device() != mem.device for t in (*given, u, v_bias, r)):
+        raise ValueError("tensors must live on the memory's device")
+    if any(t.dim() != 4 or t.shape != q.shape for t in given) or (q.shape[0], *q.shape[2:]) != (B, H, D):
+        raise ValueError("q, k_new, v_new and out must be [%d, T, %d, %d]" % (B, H, D))
+    if any(t.shape != (H, D) or not t.is_contiguous() for t in (u, v_bias)):
+        raise ValueError("u and v_bias must be contiguous [H, D]")
+    if any(t.stride(3) != 1 for t in given) and D > 1:
+        raise ValueError("the last (d) dimension must be contiguous")
+    raise ValueError("r must be [n_rows, H, ld_r], rows H * ld_r apart")
+
+
+def rel_attn_paged(q: torch.Tensor, mem: PagedMemory, k_new: torch.Tensor | None, v_new: torch.Tensor | None,
+                   u: torch.Tensor, v_bias: torch.Tensor, r: torch.Tensor, n_rows: int, clamp_len: int,
+                   out: torch.Tensor, scale: float = 0.0, counts: torch.Tensor | None = None, accumulate: bool = False,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Relative attention of 1..16 new tokens a sequence over a paged memory (txl_rel_attn_paged): pushes k_new, v_new
+    [B, T, H, D] into their reserved pages (or takes the last positions as pushed already, both None), then attends;
+    rows past counts[b] (int32 [B]) are left alone.  With `accumulate`, every slot's weight grows by the attention it
+    receives.  Without `workspace`, a device buffer of the required size is taken from torch's allocator for the call."""
+    shape, dtype, dev = q.shape, q.dtype, mem.device
+    B, H, D = mem._shape
+    own = k_new is not None
+    rs, rt = r.shape, r.stride()
+    if not (len(shape) == 4 and shape[0] == B and shape[2] == H and shape[3] == D and out.shape == shape
+            and own == (v_new is not None) and (not own or (k_new.shape == shape and v_new.shape == shape
+                                                            and k_new.dtype == dtype and v_new.dtype == dtype
+                                                            and k_new.get_device() == dev and v_new.get_device() == dev
+                                                            and (D == 1 or k_new.stride(3) == v_new.stride(3) == 1)))
+            and dtype == mem._dtype and out.dtype == dtype and r.dtype == dtype
+            and q.get_device() == dev and out.get_device() == dev and r.get_device() == dev
+            and u.get_device() == dev and v_bias.get_device() == dev
+            and u.dtype == torch.float32 and v_bias.dtype == torch.float32
+            and u.shape == (H, D) and v_bias.shape == (H, D) and u.is_contiguous() and v_bias.is_contiguous()
+            and (D == 1 or q.stride(3) == out.stride(3) == 1)
+            and len(rs) == 3 and rs[0] >= n_rows and rs[1] == H and rs[2] >= D and rt[2] == 1
+            and (rs[0] <= 1 or rt[0] == H * rt[1])):
+        _paged_refusal(q, mem, k_new, v_new, u, v_bias, r, n_rows, out)
+    n = _paged_counts(mem, counts)
+    if workspace is None:
+        # from the pool of the stream that will use it, so that it is not reused before it has been
+        need = max(rel_attn_paged_workspace_size(q, mem, min(n_rows, clamp_len + 1), accumulate), 16)
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and live on the memory's device")
+    none = (0, 0, 0, 0)
+    args = native.PAGED_ARGS.pack(
+        shape[1], clamp_len, n_rows, bool(accumulate), scale, mem.address, q.data_ptr(), *q.stride()[:3],
+        *((k_new.data_ptr(), *k_new.stride()[:3], v_new.data_ptr(), *v_new.stride()[:3]) if own else none + none),
+        out.data_ptr(), *out.stride()[:3], n, u.data_ptr(), v_bias.data_ptr(), r.data_ptr(), rt[1], workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+    check(_on_device(dev, _lib().txl_rel_attn_paged, args), "txl_rel_attn_paged")
+    return out
+
+
+def paged_evict_workspace_size(mem: PagedMemory) -> int:
+    """Bytes of workspace paged_evict needs (txl_paged_evict_workspace_size)."""
+    return int(_lib().txl_paged_evict_workspace_size(ctypes.byref(mem._c)))
+
+
+def paged_evict(mem: PagedMemory, keep: int, recent: int = 0, workspace: torch.Tensor | None = None,
+                stream=None) -> PagedMemory:
+    """Cut every sequence to `keep` positions (txl_paged_evict): the last `recent` ones and those of the largest
+    weight stay.  The pages stay with their sequences (PagedMemory.trim frees them)."""
+    dev = mem.device
+    if workspace is None:
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            workspace = torch.empty(max(paged_evict_workspace_size(mem), 16), dtype=torch.uint8, device=mem.k.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and live on the memory's device")
+    raw, size = _raw_stream(stream, dev), workspace.numel() * workspace.element_size()
+    st = _on_device(dev, lambda _: _lib().txl_paged_evict(ctypes.byref(mem._c), int(keep), int(recent), workspace.data_ptr(),
+                                                          size, raw), None)
+    check(st, "txl_paged_evict")
+    mem._room = [min(x, int(keep)) for x in mem._room]
+    return mem
+
+
+class QuantWeight:
+    """A matrix W [k, n] as 4-bit codes (txl_q4): groups of 32, 64 or 128 entries of a column share a bf16 step and
+    minimum.  Multiplied by linear_q4."""
+
+    def __init__(self, data: torch.Tensor, k: int, n: int, group: int):
+        need = int(_lib().txl_q4_bytes(k, n, group))
+        if need == 0:
+            raise ValueError("4-bit weights are [k, n] with k, n >= 1 in groups of 32, 64 or 128")
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != need or not data.is_cuda:
+            raise ValueError("4-bit weights of [%d, %d] in groups of %d take %d bytes of a CUDA device" % (k, n, group, need))
+        self.data, self.shape, self.group, self.device = data, (k, n), group, data.get_device()
+        self._c = TxlQ4(data.data_ptr(), k, n, group)
+
+    @classmethod
+    def quantise(cls, W: torch.Tensor, group: int = 64, stream=None):
+        """The codes of bf16 W [k, n] (txl_q4_quantise)."""
+        p, ld = _rows2d(W, "W")
+        if W.dtype != torch.bfloat16:
+            raise TypeError("linear_q4 computes in bfloat16, got %s" % W.dtype)
+        if not W.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        size = int(_lib().txl_q4_bytes(W.shape[0], W.shape[1], group))
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(W.get_device()):
+            w = cls(torch.empty(size, dtype=torch.uint8, device=W.device), W.shape[0], W.shape[1], group)
+        raw = _raw_stream(stream, w.device)
+        check(_on_device(w.device, lambda _: _lib().txl_q4_quantise(ctypes.byref(w._c), p, ld, raw), None), "txl_q4_quantise")
+        return w
+
+    def expand(self, W: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """What the codes stand for, as bf16 [k, n] (txl_q4_expand)."""
+        if W is None:
+            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(self.device):
+                W = torch.empty(self.shape, dtype=torch.bfloat16, device=self.data.device)
+        p, ld = _rows2d(W, "W")
+        if W.dtype != torch.bfloat16 or tuple(W.shape) != self.shape or W.get_device() != self.device:
+            raise ValueError("W must be bfloat16 [%d, %d] on the weights' device" % self.shape)
+        raw = _raw_stream(stream, self.device)
+        check(_on_device(self.device, lambda _: _lib().txl_q4_expand(ctypes.byref(self._c), p, ld, raw), None), "txl_q4_expand")
+        return W
+
+
+def linear_q4_workspace_size(m: int, w: QuantWeight) -> int:
+    """Bytes of workspace linear_q4 needs for m rows (txl_linear_q4_workspace_size)."""
+    return int(_lib().txl_linear_q4_workspace_size(int(m), ctypes.byref(w._c)))
+
+
+def linear_q4(X: torch.Tensor, w: QuantWeight, Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W for bf16 X [m, k] and 4-bit W [k, n] (txl_linear_q4); Y [m, n] is allocated if not given, and so is the
+    workspace where more than 64 rows need one."""
+    dev = w.device
+    px, ldx = _rows2d(X, "X")
+    m, k = X.shape
+    if k != w.shape[0]:
+        raise ValueError("inner dimensions differ")
+    if X.dtype != torch.bfloat16:
+        raise TypeError("linear_q4 computes in bfloat16, got %s" % X.dtype)
+    if Y is None or (workspace is None and m > 64):
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            if Y is None:
+                Y = torch.empty(m, w.shape[1], dtype=X.dtype, device=X.device)
+            if workspace is None and m > 64:
+                workspace = torch.empty(max(linear_q4_workspace_size(m, w), 16), dtype=torch.uint8, device=X.device)
+    py, ldy = _rows2d(Y, "Y")
+    if Y.shape[0] != m or Y.shape[1] != w.shape[1] or Y.dtype != X.dtype:
+        raise ValueError("Y must be bfloat16 [%d, %d]" % (m, w.shape[1]))
+    if X.get_device() != dev or Y.get_device() != dev:
+        raise ValueError("tensors must live on the weights' device")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and live on the weights' device")
+    pw, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
+    ef = err_flag.data_ptr() if err_flag is not None else None
+    raw = _raw_stream(stream, dev)
+    if dev == torch.cuda.current_device():
+        st = _lib().txl_linear_q4(m, ctypes.byref(w._c), px, max(ldx, k), py, max(ldy, w.shape[1]), pw, size, ef, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = _lib().txl_linear_q4(m, ctypes.byref(w._c), px, max(ldx, k), py, max(ldy, w.shape[1]), pw, size, ef, raw)
+    check(st, "txl_linear_q4")
+    return Y
 
 
 def selftest_wait_timeout(err_flag: torch.Tensor, timeout_us: int, stream=None) -> None:

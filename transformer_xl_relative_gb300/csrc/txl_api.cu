@@ -172,6 +172,7 @@ const char* txl_status_str(txl_status status)
     case TXL_ERR_CUDA: return "CUDA error";
     case TXL_ERR_TIMEOUT: return "device wait timed out";
     case TXL_ERR_WORKSPACE: return "workspace missing or too small";
+    case TXL_ERR_PAGE: return "a position without a page";
     }
     return "unknown status";
 }
@@ -1288,6 +1289,264 @@ txl_status txl_rel_attn_qmem_call(const txl_rel_attn_qmem_args* a)
     return txl_rel_attn_qmem(a->B, a->L, a->H, a->D, a->clamp_len, &a->q, a->mem, &a->k_cur, &a->v_cur, a->u, a->v_bias,
                              a->r, a->ld_r, a->n_rows, a->scale, &a->out, static_cast<txl_dtype>(a->dtype), a->workspace,
                              a->workspace_bytes, a->err_flag, a->stream);
+}
+
+// ---------------------------------------------------------------- paged memory
+namespace {
+
+inline bool a4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+txl_status check_paged(const txl_paged* m)
+{
+    if (!m || m->B < 0 || m->H <= 0 || m->D <= 0 || m->n_pages < 0 || m->page_len <= 0 || m->max_pages < 0 || m->ld < m->D)
+        return TXL_ERR_INVALID_ARG;
+    if (m->dtype != TXL_F32 && m->dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
+    if (m->D > 128 || m->page_len % kPageUnit || m->B > kPagedMaxB || m->H > 65535) return TXL_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(m->n_pages) * m->page_len > INT32_MAX || static_cast<int64_t>(m->max_pages) * m->page_len > INT32_MAX)
+        return TXL_ERR_UNSUPPORTED;
+    if (m->B == 0) return TXL_OK;
+    if (!m->length || !m->next_pos || !m->arrivals || (m->max_pages && !m->table)) return TXL_ERR_INVALID_ARG;
+    if (m->n_pages && (!m->k || !m->v || !m->pos || !m->weight)) return TXL_ERR_INVALID_ARG;
+    if (!a16(m->k) || !a16(m->v) || !a16(m->pos) || !a16(m->weight) || !s16(m->ld, m->dtype == TXL_F32 ? 4 : 2))
+        return TXL_ERR_ALIGNMENT;
+    if (!a4(m->length) || !a4(m->next_pos) || !a4(m->arrivals) || !a4(m->table) || !a4(m->err_flag)) return TXL_ERR_ALIGNMENT;
+    return TXL_OK;
+}
+
+PagedParams paged_params(const txl_paged* m)
+{
+    PagedParams p{};
+    p.k = m->k; p.v = m->v; p.pos = m->pos; p.weight = m->weight; p.table = m->table;
+    p.length = m->length; p.next_pos = m->next_pos; p.arrivals = m->arrivals; p.err_flag = m->err_flag;
+    p.B = m->B; p.H = m->H; p.D = m->D; p.ld = m->ld;
+    p.n_pages = m->n_pages; p.page_len = m->page_len; p.max_pages = m->max_pages;
+    return p;
+}
+
+PagedPushParams paged_push_params(const txl_paged* m, const txl_view* k, const txl_view* v, int T, const int* counts)
+{
+    const int elem = m->dtype == TXL_F32 ? 4 : 2;
+    auto rows16 = [&](const txl_view* x) {
+        return a16(x->ptr) && s16(x->stride_b, elem) && s16(x->stride_t, elem) && s16(x->stride_h, elem);
+    };
+    PagedPushParams p{};
+    p.m = paged_params(m);
+    p.xk = k->ptr; p.xk_sb = k->stride_b; p.xk_st = k->stride_t; p.xk_sh = k->stride_h;
+    p.xv = v->ptr; p.xv_sb = v->stride_b; p.xv_st = v->stride_t; p.xv_sh = v->stride_h;
+    p.counts = counts;
+    p.T = T;
+    p.vec_k = rows16(k);
+    p.vec_v = rows16(v);
+    return p;
+}
+
+// The workspace of txl_rel_attn_paged in order; bytes in all, or with `p` its pointers from `base` on.
+size_t paged_workspace(const txl_paged* m, int T, int n_e, int accumulate, char* base, PagedAttnParams* p)
+{
+    const size_t pairs = static_cast<size_t>(m->B) * m->H, rows = pairs * T;
+    const size_t cap = static_cast<size_t>(m->max_pages) * m->page_len;
+    const int Dp = (m->D + 31) / 32 * 32, e_pitch = (n_e + 7) / 8 * 8;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* q = base + at;
+        at += (bytes + 15) / 16 * 16;
+        return q;
+    };
+    char* now = take(static_cast<size_t>(m->B) * sizeof(int4));
+    char* tickets = take(pairs * 4);
+    char* part = take(2 * static_cast<size_t>(kPagedMaxCtas) * T * Dp * 4);
+    char* ml = take(2 * static_cast<size_t>(kPagedMaxCtas) * T * 8);
+    char* E = take(rows * e_pitch * 4);
+    char* lse = accumulate ? take(rows * 4) : nullptr;
+    char* S = accumulate ? take(rows * cap * 4) : nullptr;
+    if (p) {
+        p->now = reinterpret_cast<int4*>(now);
+        p->tickets = reinterpret_cast<int*>(tickets);
+        p->part = reinterpret_cast<float*>(part);
+        p->ml = reinterpret_cast<float*>(ml);
+        p->E = reinterpret_cast<float*>(E);
+        p->lse = reinterpret_cast<float*>(lse);
+        p->S = reinterpret_cast<float*>(S);
+        p->Dp = Dp;
+        p->n_e = n_e;
+        p->e_pitch = e_pitch;
+    }
+    return at;
+}
+
+txl_status check_q4(const txl_q4* w)
+{
+    if (!w || txl_q4_bytes(w->k, w->n, w->group) == 0 || !w->data) return TXL_ERR_INVALID_ARG;
+    return a16(w->data) ? TXL_OK : TXL_ERR_ALIGNMENT;
+}
+
+// The codes and the groups' parameters in a txl_q4's data.
+uint4* q4_codes(const txl_q4* w) { return static_cast<uint4*>(w->data); }
+uint32_t* q4_par(const txl_q4* w)
+{
+    return reinterpret_cast<uint32_t*>(static_cast<char*>(w->data) + static_cast<size_t>((w->n + 15) / 16) * ((w->k + 63) / 64) * 512);
+}
+
+Q4WeightParams q4_params(const txl_q4* w, void* W, int64_t ld_w)
+{
+    Q4WeightParams p{};
+    p.w = W; p.ld_w = ld_w; p.codes = q4_codes(w); p.par = q4_par(w);
+    p.n = w->n; p.k = w->k; p.group = w->group;
+    return p;
+}
+
+}  // namespace
+
+txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl_view* v_new, int T, const int* counts,
+                          void* stream)
+{
+    const txl_status st = check_paged(mem);
+    if (st != TXL_OK) return st;
+    if (T < 0 || (T > 0 && (!view_ok(k_new) || !view_ok(v_new)))) return TXL_ERR_INVALID_ARG;
+    if (!a4(counts)) return TXL_ERR_ALIGNMENT;
+    if (T == 0 || mem->B == 0) return TXL_OK;
+    const PagedPushParams p = paged_push_params(mem, k_new, v_new, T, counts);
+    return launch_paged_push(p, static_cast<txl_dtype>(mem->dtype), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TXL_OK : TXL_ERR_CUDA;
+}
+
+size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate)
+{
+    if (!mem || mem->B <= 0 || mem->H <= 0 || mem->D <= 0 || mem->D > 128 || T <= 0 || T > kDecodeMaxL || n_rows <= 0 ||
+        mem->max_pages < 0 || mem->page_len <= 0)
+        return 0;
+    return paged_workspace(mem, T, n_rows, accumulate, nullptr, nullptr);
+}
+
+txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    txl_status st = check_paged(a->mem);
+    if (st != TXL_OK) return st;
+    const txl_paged* m = a->mem;
+    const bool pushes = a->k_new.ptr || a->v_new.ptr;
+    if (a->T < 0 || a->clamp_len < 0 || a->n_rows < 1 || !a->u || !a->v_bias || !a->r || a->ld_r < m->D) return TXL_ERR_INVALID_ARG;
+    if (pushes && (!a->k_new.ptr || !a->v_new.ptr)) return TXL_ERR_INVALID_ARG;
+    if (a->T > kDecodeMaxL) return TXL_ERR_UNSUPPORTED;
+    if (m->B == 0 || a->T == 0) return TXL_OK;
+    if (!a->q.ptr || !a->out.ptr) return TXL_ERR_INVALID_ARG;
+    const int elem = m->dtype == TXL_F32 ? 4 : 2;
+    const uintptr_t odd = reinterpret_cast<uintptr_t>(a->q.ptr) | reinterpret_cast<uintptr_t>(a->out.ptr) |
+                          reinterpret_cast<uintptr_t>(a->k_new.ptr) | reinterpret_cast<uintptr_t>(a->v_new.ptr) |
+                          reinterpret_cast<uintptr_t>(a->r);
+    if (!a4(a->u) || !a4(a->v_bias) || !a4(a->counts) || (odd & (elem - 1))) return TXL_ERR_ALIGNMENT;
+    const int n_e = static_cast<int>(std::min<int64_t>(a->n_rows, static_cast<int64_t>(a->clamp_len) + 1));
+    PagedAttnParams p{};
+    const size_t need = paged_workspace(m, a->T, n_e, a->accumulate, nullptr, nullptr);
+    if (!a->workspace || a->workspace_bytes < need) return TXL_ERR_WORKSPACE;
+    if (!a16(a->workspace)) return TXL_ERR_ALIGNMENT;
+    const int sms = sm_count();
+    if (sms <= 0) return TXL_ERR_CUDA;
+    paged_workspace(m, a->T, n_e, a->accumulate, static_cast<char*>(a->workspace), &p);
+    p.n = paged_push_params(m, &a->k_new, &a->v_new, a->T, a->counts);
+    p.q = a->q.ptr; p.q_sb = a->q.stride_b; p.q_st = a->q.stride_t; p.q_sh = a->q.stride_h;
+    p.out = a->out.ptr; p.o_sb = a->out.stride_b; p.o_st = a->out.stride_t; p.o_sh = a->out.stride_h;
+    p.u = a->u;
+    p.vb = a->v_bias;
+    p.r = a->r;
+    p.r_row = static_cast<int64_t>(m->H) * a->ld_r;
+    p.r_head = a->ld_r;
+    p.vec_r = a16(a->r) && s16(a->ld_r, elem);
+    p.qscale = (a->scale > 0.f ? a->scale : 1.0f / std::sqrt(static_cast<float>(m->D))) * 1.4426950408889634f;
+    p.accumulate = a->accumulate != 0;
+    p.cap = m->max_pages * m->page_len;
+    return launch_paged_attn(p, static_cast<txl_dtype>(m->dtype), sms, static_cast<cudaStream_t>(a->stream)) == cudaSuccess
+               ? TXL_OK : TXL_ERR_CUDA;
+}
+
+size_t txl_paged_evict_workspace_size(const txl_paged* mem)
+{
+    if (!mem || mem->B <= 0 || mem->max_pages <= 0 || mem->page_len <= 0) return 0;
+    const size_t half = static_cast<size_t>(mem->max_pages) * mem->page_len / 2;      // moves of a sequence, at most
+    return (static_cast<size_t>(mem->B) * (1 + 2 * half) * 4 + 15) / 16 * 16;
+}
+
+txl_status txl_paged_evict(const txl_paged* mem, int keep, int recent, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const txl_status st = check_paged(mem);
+    if (st != TXL_OK) return st;
+    if (keep < 1 || recent < 0 || recent > keep) return TXL_ERR_INVALID_ARG;
+    const int64_t cap = static_cast<int64_t>(mem->max_pages) * mem->page_len;
+    if (mem->B == 0 || cap <= keep) return TXL_OK;
+    if (!workspace || workspace_bytes < txl_paged_evict_workspace_size(mem)) return TXL_ERR_WORKSPACE;
+    if (!a16(workspace)) return TXL_ERR_ALIGNMENT;
+    const int sms = sm_count();
+    if (sms <= 0) return TXL_ERR_CUDA;
+    PagedEvictParams p{};
+    p.m = paged_params(mem);
+    p.keep = keep;
+    p.recent = recent;
+    p.elem = mem->dtype == TXL_F32 ? 4 : 2;
+    p.most = static_cast<int>(std::min<int64_t>(keep, cap - keep));
+    p.moves = static_cast<int*>(workspace);
+    p.to = p.moves + mem->B;
+    p.from = p.to + static_cast<int64_t>(mem->B) * p.most;
+    return launch_paged_evict(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+size_t txl_q4_bytes(int k, int n, int group)
+{
+    if (k < 1 || n < 1 || k > (1 << 21) || n > (1 << 21) || (group != 32 && group != 64 && group != 128)) return 0;
+    const size_t tiles = static_cast<size_t>((n + 15) / 16);
+    return tiles * ((k + 63) / 64) * 512 + tiles * ((k + group - 1) / group) * 64;
+}
+
+txl_status txl_q4_quantise(const txl_q4* w, const void* W, int64_t ld_w, void* stream)
+{
+    const txl_status st = check_q4(w);
+    if (st != TXL_OK) return st;
+    if (!W || ld_w < w->n) return TXL_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(W) & 1u) return TXL_ERR_ALIGNMENT;
+    return launch_q4_quantise(q4_params(w, const_cast<void*>(W), ld_w), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TXL_OK : TXL_ERR_CUDA;
+}
+
+txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream)
+{
+    const txl_status st = check_q4(w);
+    if (st != TXL_OK) return st;
+    if (!W || ld_w < w->n) return TXL_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(W) & 1u) return TXL_ERR_ALIGNMENT;
+    return launch_q4_expand(q4_params(w, W, ld_w), static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
+size_t txl_linear_q4_workspace_size(int m, const txl_q4* w)
+{
+    if (m <= kQ4MaxRows || !w || txl_q4_bytes(w->k, w->n, w->group) == 0) return 0;
+    return static_cast<size_t>(w->k) * ((w->n + 7) / 8 * 8) * 2;
+}
+
+txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, void* Y, int64_t ld_y, void* workspace,
+                         size_t workspace_bytes, int* err_flag, void* stream)
+{
+    txl_status st = check_q4(w);
+    if (st != TXL_OK) return st;
+    if (m < 0 || !X || !Y || ld_x < w->k || ld_y < w->n) return TXL_ERR_INVALID_ARG;
+    if (m > (1 << 20)) return TXL_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y)) & 1u) return TXL_ERR_ALIGNMENT;
+    if (m == 0) return TXL_OK;
+    const bool rows16 = a16(X) && s16(ld_x, 2);
+    const size_t need = txl_linear_q4_workspace_size(m, w);
+    if (need && (!workspace || workspace_bytes < need)) return TXL_ERR_WORKSPACE;
+    if (need && !a16(workspace)) return TXL_ERR_ALIGNMENT;
+    if (need && rows16) {
+        const int64_t ld_w = (w->n + 7) / 8 * 8;
+        st = txl_q4_expand(w, workspace, ld_w, stream);
+        return st != TXL_OK ? st : txl_linear(m, w->n, w->k, X, ld_x, workspace, ld_w, Y, ld_y, TXL_BF16, err_flag, stream);
+    }
+    const int sms = sm_count();
+    if (sms <= 0) return TXL_ERR_CUDA;
+    LinearQ4Params p{};
+    p.x = X; p.ld_x = ld_x; p.codes = q4_codes(w); p.par = q4_par(w); p.y = Y; p.ld_y = ld_y;
+    p.m = m; p.n = w->n; p.k = w->k; p.group = w->group;
+    p.vec_x = rows16;
+    return launch_linear_q4(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
 }
 
 int txl_checked_build(void) { return kCheckedBuild ? 1 : 0; }

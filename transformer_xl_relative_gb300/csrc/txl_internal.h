@@ -348,6 +348,84 @@ struct QattnParams {
 cudaError_t launch_qattn(const QattnParams& p, int sm_count, cudaStream_t s);
 cudaError_t launch_qseg_f32(const QattnParams& p, int sm_count, cudaStream_t s);   // E, far, jn .. unused
 
+// ---------------------------------------------------------------- paged memory
+constexpr int kPageUnit = 16;       // a page holds a multiple of this many positions: the tile of the attention
+constexpr int kPagedMaxB = 4096;    // sequences of a paged memory
+constexpr int kPagedMaxCtas = 640;  // blocks of the attention over a paged memory, at most (4 on each of 160 SMs)
+
+struct PagedParams {
+    void* k; void* v;                           // [n_pages][H][page_len][ld]
+    int* pos; float* weight;                    // [n_pages][page_len]
+    const int* table;                           // [B][max_pages]
+    int* length; int* next_pos; int* arrivals;  // [B]
+    int* err_flag;                              // TXL_ERR_PAGE, may be null
+    int B, H, D, ld, n_pages, page_len, max_pages;
+};
+
+// New positions: rows t < counts[b] (all T where counts is null) of every sequence.
+struct PagedPushParams {
+    PagedParams m;
+    const void* xk; int64_t xk_sb, xk_st, xk_sh;
+    const void* xv; int64_t xv_sb, xv_st, xv_sh;
+    const int* counts;
+    int T;
+    int vec_k, vec_v;                           // every row of the tensor starts on a 16-byte boundary
+};
+cudaError_t launch_paged_push(const PagedPushParams& p, txl_dtype dtype, cudaStream_t s);
+
+struct PagedAttnParams {
+    PagedPushParams n;                          // xk null: the queries' own positions are in the memory already
+    const void* q; int64_t q_sb, q_st, q_sh;
+    void* out; int64_t o_sb, o_st, o_sh;
+    const float* u; const float* vb;
+    const void* r; int64_t r_row, r_head;       // element strides of the r table
+    int vec_r;                                  // rows of r start on 16-byte boundaries
+    int n_e, e_pitch;                           // distances with a position term (the last one counts for those beyond)
+    float qscale;                               // scale * log2(e)
+    int accumulate;                             // add the attention weights to m.weight
+    int cap;                                    // max_pages * page_len
+    // workspace
+    int* tickets;                               // [B][H] parts of a (b, h) that are done
+    int4* now;                                  // [B] length, first query's position, queries
+    float* E;                                   // [B][H][T][e_pitch] position terms, log2 domain
+    float* S;                                   // [B][H][T][cap] scores, log2 domain (accumulate)
+    float* lse;                                 // [B][H][T] their log-sum-exp (accumulate)
+    float* part; float* ml;                     // [2 kPagedMaxCtas][T][Dp], [..][T][2]: sums, maximum and weight
+    int Dp;                                     // D rounded up to 32
+};
+cudaError_t launch_paged_attn(const PagedAttnParams& p, txl_dtype dtype, int sm_count, cudaStream_t s);
+
+struct PagedEvictParams {
+    PagedParams m;
+    int keep, recent, elem;
+    int most;                                   // moves of a sequence, at most
+    int* moves;                                 // [B]
+    int* to; int* from;                         // [B][most] rows of the pool: page * page_len + row
+};
+cudaError_t launch_paged_evict(const PagedEvictParams& p, int sm_count, cudaStream_t s);
+
+// ---------------------------------------------------------------- 4-bit weights
+constexpr int kQ4MaxRows = 64;      // rows of X up to which they are multiplied with the codes as they are
+
+struct LinearQ4Params {
+    const void* x; int64_t ld_x;                // bf16 [m][ld_x]
+    const uint4* codes;                         // [ceil(n/16)][ceil(k/64)][32 lanes]
+    const uint32_t* par;                        // [ceil(n/16)][groups][16]: step | lo << 16, bf16
+    void* y; int64_t ld_y;
+    int m, n, k, group;
+    int vec_x;                                  // rows of x start on 16-byte boundaries
+};
+cudaError_t launch_linear_q4(const LinearQ4Params& p, int sm_count, cudaStream_t s);
+
+struct Q4WeightParams {
+    void* w; int64_t ld_w;                      // bf16 [k][ld_w]: read by the quantisation, written by the expansion
+    uint4* codes;
+    uint32_t* par;
+    int n, k, group;
+};
+cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s);
+cudaError_t launch_q4_expand(const Q4WeightParams& p, cudaStream_t s);
+
 cudaError_t launch_selftest_wait(int* err_flag, unsigned timeout_us, cudaStream_t s);
 // One failing and one passing range check on the device (the checked build's counter gains one).
 cudaError_t launch_selftest_range(int* chk, cudaStream_t s);

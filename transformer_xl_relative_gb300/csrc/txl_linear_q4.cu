@@ -1,0 +1,249 @@
+// txl_linear_q4.cu -- Y = X W for few rows of X, with W held as 4-bit codes: groups of 32, 64 or 128 entries of a
+// column share a bf16 step and minimum lo, w = lo + step c (the projections of "TransformerXL 相对位置编码" §3.1).
+//
+//     y = sum over groups ( step sum_k x_k c_k + lo sum_k x_k ),     c exact in bf16, sums in fp32
+#include <cuda_bf16.h>
+
+#include "txl_mma.cuh"
+#include "txl_internal.h"
+#include "txl_ptx.cuh"
+
+namespace txl {
+
+namespace {
+
+// A block of codes: 16 columns of W (rows of an mma's A) by 64 k.  Lane (g, t) holds 32 codes: word s (0..3) those of a k16
+// step, k = 32 (s / 2) + 8 t + 4 (s % 2) + 0..3, so that a lane's x are two pieces of 16 bytes and a step stays within 32 k.
+// Nibble j of a word and nibble j + 4 are a pair of A's register j: column g + 8 (j % 2), k + 2 (j / 2) and the next.
+constexpr int kQ4K = 64, kQ4N = 16;
+constexpr int kQ4Threads = 256, kQ4Warps = kQ4Threads / 32;
+
+__device__ __forceinline__ uint4 load_codes(const uint4* p)
+{
+    uint4 w;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+    return w;
+}
+
+// Eight bf16 of a row of x from channel k on; 0 at and past k_end.
+__device__ __forceinline__ uint4 load_x8(const uint16_t* row, int k, int k_end, bool vec)
+{
+    if (vec && k + 8 <= k_end) return *reinterpret_cast<const uint4*>(row + k);
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = k + i < k_end ? row[k + i] : 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
+// 128 + c as bf16 pairs: a code is the low bits of the mantissa.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u; }
+
+// A block of threads computes 16 NT columns of Y for 8 MT rows, its warps each eighth block of k.
+// The products see 128 + c; what that adds, 128 step sum x, leaves with the minimum: lo - 128 step times sum x, which an mma
+// with a matrix of ones gives in the same lanes.  Both cost 2^-24 of 128 step sum |x| (2^-16 of a step for each x).
+template <int NT, int MT, int SUB>
+__global__ void __launch_bounds__(kQ4Threads, MT == 1 && NT == 1 ? 4 : 2) linear_q4_kernel(const __grid_constant__ LinearQ4Params p)
+{
+    __shared__ float red[kQ4Warps][16 * NT][8 * MT + 1];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+    const int nt_all = (p.n + kQ4N - 1) / kQ4N, nt0 = blockIdx.x * NT;
+    const int row0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.m - row0);
+    const uint16_t* x[MT];
+    bool live[MT];
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        live[a] = 8 * a + g < rows;
+        x[a] = static_cast<const uint16_t*>(p.x) + (row0 + (live[a] ? 8 * a + g : 0)) * p.ld_x;
+    }
+    float tot[NT][MT][4] = {};
+    constexpr uint32_t kOnes = 0x3f803f80u;
+#pragma unroll 2
+    for (int kb = warp; kb < kb_all; kb += kQ4Warps) {
+        uint4 w[NT], xv[MT][2];
+        uint32_t par[NT][SUB][2];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+            const int nt = min(nt0 + b, nt_all - 1);
+            w[b] = load_codes(p.codes + (static_cast<int64_t>(nt) * kb_all + kb) * 32 + lane);
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                const int gr = min((kb * kQ4K + s * (kQ4K / SUB)) / p.group, groups - 1);
+                const uint32_t* q = p.par + (static_cast<int64_t>(nt) * groups + gr) * 16 + g;
+                par[b][s][0] = q[0];
+                par[b][s][1] = q[8];
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                xv[a][h] = live[a] ? load_x8(x[a], kb * kQ4K + 32 * h + 8 * t, p.k, p.vec_x) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            float xs[MT][4] = {};
+            float c[NT][MT][4] = {};
+#pragma unroll
+            for (int i = 0; i < 4 / SUB; ++i) {
+                const int step = s * (4 / SUB) + i;
+                uint32_t b0[MT], b1[MT];
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const uint4 v = xv[a][step >> 1];
+                    b0[a] = step & 1 ? v.z : v.x;
+                    b1[a] = step & 1 ? v.w : v.y;
+                    mma::mma16816(xs[a], kOnes, kOnes, kOnes, kOnes, b0[a], b1[a]);
+                }
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    const uint32_t q = step == 0 ? w[b].x : step == 1 ? w[b].y : step == 2 ? w[b].z : w[b].w;
+                    const uint32_t a0 = code_pair(q, 0), a1 = code_pair(q, 1), a2 = code_pair(q, 2), a3 = code_pair(q, 3);
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) mma::mma16816(c[b][a], a0, a1, a2, a3, b0[a], b1[a]);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float step = mma::bf16_lo(par[b][s][r]), lo = fmaf(-128.f, step, mma::bf16_hi(par[b][s][r]));
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            tot[b][a][2 * r + e] = fmaf(step, c[b][a][2 * r + e], fmaf(lo, xs[a][e], tot[b][a][2 * r + e]));
+                }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[warp][16 * b + g + 8 * (e >> 1)][8 * a + 2 * t + (e & 1)] = tot[b][a][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * NT * rows; i += kQ4Threads) {
+        const int row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
+        if (n >= p.n) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kQ4Warps; ++w) s += red[w][col][row];
+        static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
+    }
+}
+
+// ---------------------------------------------------------------- weights
+constexpr int kWThreads = 128, kWK = 128;
+
+// 16 columns by 128 k of W.  lo: the largest bf16 not above the group's minimum; step: the smallest bf16 not below
+// (max - lo) / 15; codes: the nearest integers to (w - lo) / step, ties to even; quotients in double precision.
+__global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_constant__ Q4WeightParams p)
+{
+    __shared__ float x[kWK][kQ4N + 1];
+    __shared__ float step[4][kQ4N], lo[4][kQ4N];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, nt = blockIdx.x, k0 = blockIdx.y * kWK;
+    const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+    for (int i = tid; i < kWK * kQ4N; i += kWThreads) {
+        const int k = k0 + i / kQ4N, n = nt * kQ4N + i % kQ4N;
+        x[i / kQ4N][i % kQ4N] = k < p.k && n < p.n ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.w)[k * p.ld_w + n]) << 16) : 0.f;
+    }
+    __syncthreads();
+    const int here = kWK / p.group;
+    for (int i = tid; i < here * kQ4N; i += kWThreads) {
+        const int gr = i / kQ4N, c = i % kQ4N, first = gr * p.group, n = min(p.group, p.k - k0 - first);
+        if (n <= 0) continue;
+        float a = x[first][c], z = a;
+        bool bad = false;
+        for (int k = 0; k < n; ++k) {
+            const float v = x[first + k][c];
+            bad |= !isfinite(v);
+            a = fminf(a, v);
+            z = fmaxf(z, v);
+        }
+        // (bf16 entries: the minimum is a bf16 already)
+        const double span = static_cast<double>(z) - a;
+        auto up = [](float v) { return __uint_as_float((__float_as_uint(v) + 0xffffu) & 0xffff0000u); };
+        float s = up(static_cast<float>(span / 15.0));
+        if (static_cast<double>(s) * 15.0 < span) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
+        const float less = s > 0.f ? __uint_as_float(__float_as_uint(s) - 0x10000u) : 0.f;
+        if (static_cast<double>(less) * 15.0 >= span) s = less;
+        if (bad || !isfinite(s)) s = a = __uint_as_float(0x7fc00000u);
+        step[gr][c] = s;
+        lo[gr][c] = a;
+        p.par[(static_cast<int64_t>(nt) * groups + k0 / p.group + gr) * 16 + c] = __float_as_uint(s) >> 16 | (__float_as_uint(a) & 0xffff0000u);
+    }
+    __syncthreads();
+    for (int i = tid; i < kWK / kQ4K * 128; i += kWThreads) {
+        const int kb = i / 128, lane = i % 128 / 4, s = i % 4, g = lane >> 2, t = lane & 3;
+        if (k0 / kQ4K + kb >= kb_all) continue;
+        uint32_t w = 0;
+        for (int j = 0; j < 8; ++j) {
+            const int c = g + 8 * (j & 1), k = kb * kQ4K + 32 * (s >> 1) + 8 * t + 4 * (s & 1) + (j & 2) + (j >> 2);
+            if (k0 + k >= p.k) continue;
+            const float a = lo[k / p.group][c], d = step[k / p.group][c];
+            if (d > 0.f) w |= static_cast<uint32_t>(rint((static_cast<double>(x[k][c]) - a) / d)) << (4 * j);
+        }
+        reinterpret_cast<uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + k0 / kQ4K + kb) * 32 + lane)[s] = w;
+    }
+}
+
+// 64 columns by 64 k of W from the codes: one fp32 multiply-add, rounded to bf16.
+__global__ void __launch_bounds__(kQ4Threads) q4_expand_kernel(const __grid_constant__ Q4WeightParams p)
+{
+    __shared__ uint16_t x[kQ4K][72];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, kb = blockIdx.y, n0 = blockIdx.x * 64;
+    const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+    for (int i = tid; i < 4 * 128; i += kQ4Threads) {
+        const int nt = n0 / kQ4N + i / 128, lane = i % 128 / 4, s = i % 4, g = lane >> 2, t = lane & 3;
+        if (nt * kQ4N >= p.n) continue;
+        const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + kb) * 32 + lane)[s];
+        const int k = 32 * (s >> 1) + 8 * t + 4 * (s & 1), gr = min((kb * kQ4K + k) / p.group, groups - 1);
+        const uint32_t* q = p.par + (static_cast<int64_t>(nt) * groups + gr) * 16 + g;
+        const uint32_t par[2] = {q[0], q[8]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = fmaf(mma::bf16_lo(par[j & 1]), static_cast<float>((w >> (4 * j)) & 15u), mma::bf16_hi(par[j & 1]));
+            x[k + (j & 2) + (j >> 2)][i / 128 * kQ4N + g + 8 * (j & 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < kQ4K * 64; i += kQ4Threads) {
+        const int k = kb * kQ4K + i / 64, n = n0 + i % 64;
+        if (k < p.k && n < p.n) static_cast<uint16_t*>(p.w)[static_cast<int64_t>(k) * p.ld_w + n] = x[i / 64][i % 64];
+    }
+}
+
+template <int NT, int MT>
+cudaError_t launch_rows(const LinearQ4Params& p, cudaStream_t s)
+{
+    const dim3 grid((p.n + kQ4N * NT - 1) / (kQ4N * NT), (p.m + 8 * MT - 1) / (8 * MT));
+    if (p.group == 32) return launch_dependent(linear_q4_kernel<NT, MT, 2>, grid, dim3(kQ4Threads), 0, s, p);
+    return launch_dependent(linear_q4_kernel<NT, MT, 1>, grid, dim3(kQ4Threads), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_q4(const LinearQ4Params& p, int sm_count, cudaStream_t s)
+{
+    (void)sm_count;
+    return p.m <= 8 ? launch_rows<1, 1>(p, s) : launch_rows<1, 2>(p, s);
+}
+
+cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s)
+{
+    return launch_dependent(q4_quantise_kernel, dim3((p.n + kQ4N - 1) / kQ4N, (p.k + kWK - 1) / kWK), dim3(kWThreads), 0, s, p);
+}
+
+cudaError_t launch_q4_expand(const Q4WeightParams& p, cudaStream_t s)
+{
+    return launch_dependent(q4_expand_kernel, dim3((p.n + 63) / 64, (p.k + kQ4K - 1) / kQ4K), dim3(kQ4Threads), 0, s, p);
+}
+
+}  // namespace txl

@@ -15,7 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtxl_checked.so" if os.environ.get("TXL_CHECKED") == "1" else "libtxl.so")
 
 TXL_OK, TXL_ERR_INVALID_ARG, TXL_ERR_UNSUPPORTED, TXL_ERR_ALIGNMENT = 0, 1, 2, 3
-TXL_ERR_CUDA, TXL_ERR_TIMEOUT, TXL_ERR_WORKSPACE = 4, 5, 6
+TXL_ERR_CUDA, TXL_ERR_TIMEOUT, TXL_ERR_WORKSPACE, TXL_ERR_PAGE = 4, 5, 6, 7
 TXL_F32, TXL_BF16 = 0, 1
 
 # every function include/txl.h declares
@@ -31,6 +31,9 @@ EXPORTS = (
     "txl_rel_attn_bwd_path", "txl_qmem_row_bytes", "txl_qmem_push", "txl_qmem_read",
     "txl_rel_attn_qmem", "txl_rel_attn_qmem_workspace_size", "txl_rel_attn_qmem_path",
     "txl_rel_attn_qmem_call", "txl_qmem_push_call", "txl_qmem_read_call",
+    "txl_paged_push", "txl_rel_attn_paged", "txl_rel_attn_paged_workspace_size", "txl_paged_evict",
+    "txl_paged_evict_workspace_size", "txl_q4_bytes", "txl_q4_quantise", "txl_q4_expand", "txl_linear_q4",
+    "txl_linear_q4_workspace_size",
 )
 
 
@@ -53,6 +56,19 @@ class TxlQmem(ctypes.Structure):
                 ("bits", ctypes.c_int), ("wp", ctypes.c_int), ("valid", ctypes.c_int)]
 
 
+class TxlPaged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "pos", "weight", "table", "length", "next_pos", "arrivals",
+                                               "err_flag")] + \
+               [(n, ctypes.c_int) for n in ("B", "H", "D", "ld", "n_pages", "page_len", "max_pages", "dtype")]
+
+
+class TxlQ4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("k", ctypes.c_int), ("n", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+# txl_rel_attn_paged_args: T, clamp_len, n_rows, accumulate, scale; mem; the views q, k_new, v_new, out; counts, u,
+# v_bias, r, ld_r, workspace, workspace_bytes, stream (pointers as unsigned 64-bit numbers)
+PAGED_ARGS = struct.Struct("@4if" + "Q" + 4 * "Qqqq" + "QQQQqQQQ")
 # txl_qmem_kv_args: mem; the views k, v; j0, n, dtype; stream (pointers as unsigned 64-bit numbers)
 QMEM_KV_ARGS = struct.Struct("@Q" + 2 * "Qqqq" + "3iQ")
 # txl_rel_attn_qmem_args: B, L, H, D, clamp_len, n_rows, dtype, scale; the views q, k_cur, v_cur, out; mem, u,
@@ -167,6 +183,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.txl_rel_attn_qmem_workspace_size.restype = ctypes.c_size_t
     lib.txl_rel_attn_qmem_path.argtypes = [i, i, i, i, V, Qp, V, V, vp, i64, V, i]
     lib.txl_rel_attn_qmem_path.restype = i
+    Pp, Wp, sz = ctypes.POINTER(TxlPaged), ctypes.POINTER(TxlQ4), ctypes.c_size_t
+    lib.txl_paged_push.argtypes = [Pp, V, V, i, vp, vp]
+    lib.txl_paged_push.restype = i
+    lib.txl_rel_attn_paged.argtypes = [ctypes.c_char_p]
+    lib.txl_rel_attn_paged.restype = i
+    lib.txl_rel_attn_paged_workspace_size.argtypes = [Pp, i, i, i]
+    lib.txl_rel_attn_paged_workspace_size.restype = sz
+    lib.txl_paged_evict.argtypes = [Pp, i, i, vp, sz, vp]
+    lib.txl_paged_evict.restype = i
+    lib.txl_paged_evict_workspace_size.argtypes = [Pp]
+    lib.txl_paged_evict_workspace_size.restype = sz
+    lib.txl_q4_bytes.argtypes = [i, i, i]
+    lib.txl_q4_bytes.restype = sz
+    lib.txl_q4_quantise.argtypes = [Wp, vp, i64, vp]
+    lib.txl_q4_quantise.restype = i
+    lib.txl_q4_expand.argtypes = [Wp, vp, i64, vp]
+    lib.txl_q4_expand.restype = i
+    lib.txl_linear_q4.argtypes = [i, Wp, vp, i64, vp, i64, vp, sz, vp, vp]
+    lib.txl_linear_q4.restype = i
+    lib.txl_linear_q4_workspace_size.argtypes = [i, Wp]
+    lib.txl_linear_q4_workspace_size.restype = sz
     _lib = lib
     return lib
 
