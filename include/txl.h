@@ -577,10 +577,10 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
  * on what the memory then holds.
  *   k, v     : device, 16-byte aligned, [n_pages][H][page_len][ld] of dtype; ld >= D, rows of a multiple of 16 bytes.
  *              What a row holds at and past D is never used (pushes write zeros there).
- *   pos, weight : device [n_pages][page_len], 16-byte aligned.
+ *   pos, weight : device [n_pages][page_len]; pos 8-byte aligned.
  *   table    : device [B][max_pages]; entries outside 0 .. n_pages-1 are no page.  A page that a push, an eviction or the
  *              sum of weights writes belongs to one sequence; pages that are only read may be shared.
- *   length, next_pos : device [B];  arrivals : device [B], zero (pushes leave it so).
+ *   length, next_pos : device [B];  scratch : device, B * (H + 1) + 1 ints, zero (every call leaves it so).
  *   err_flag : optional device int: a call that meets a slot without a page writes TXL_ERR_PAGE there if it is 0 (never
  *              cleared by the library).  Such a slot counts as not there; a push that does not find pages for all new
  *              positions of a sequence leaves that sequence as it was, and its queries' outputs too.
@@ -595,7 +595,7 @@ typedef struct {
     const int* table;
     int* length;
     int* next_pos;
-    int* arrivals;
+    int* scratch;
     int* err_flag;
     int B, H, D, ld, n_pages, page_len, max_pages;
     int dtype;                 /* a txl_dtype */
@@ -628,7 +628,7 @@ txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl
  * The slots of all (sequence, head) pairs are cut into equal shares for the blocks, whatever the lengths.  bf16: mma.sync
  * products; scale log2(e) (q + u), scale log2(e) (q + v) and the weights of the softmax are held to 16 bits (two bf16
  * each).  f32: fp32 arithmetic on the CUDA cores.  The result does not depend on the order in which blocks run.  A key or value
- * that a query does not see does not reach it, whatever it is.  Two launches, three with accumulate.
+ * that a query does not see does not reach it, whatever it is.  One launch for one bf16 token, else two; one more with accumulate.
  */
 typedef struct {
     int T, clamp_len, n_rows, accumulate;
@@ -647,8 +647,8 @@ typedef struct {
 txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* args);
 
 /* Bytes of device workspace txl_rel_attn_paged needs for n_rows distances (min(n_rows, clamp_len + 1) are enough): mostly
- * B*H*T floats a distance, with accumulate as many a slot of max_pages pages, and parts of the sums (1280 T rows of D
- * floats).  0 for an invalid shape. */
+ * B*H*T floats a distance (not for one bf16 token), with accumulate as many a slot of max_pages pages, and parts of the
+ * sums (1280 T rows of D floats).  0 for an invalid shape. */
 size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate);
 
 /*

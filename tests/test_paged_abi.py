@@ -23,7 +23,7 @@ def native():
 
 
 def paged(native, **kw):
-    f = dict(k=FAKE, v=FAKE, pos=FAKE, weight=FAKE, table=FAKE, length=FAKE, next_pos=FAKE, arrivals=FAKE, err_flag=None,
+    f = dict(k=FAKE, v=FAKE, pos=FAKE, weight=FAKE, table=FAKE, length=FAKE, next_pos=FAKE, scratch=FAKE, err_flag=None,
              B=2, H=4, D=41, ld=48, n_pages=10, page_len=16, max_pages=5, dtype=1)
     f.update(kw)
     return native.TxlPaged(*[f[n] for n, _ in native.TxlPaged._fields_])
@@ -33,7 +33,7 @@ BAD_MEMORIES = [
     (dict(B=-1), "INVALID_ARG"), (dict(H=0), "INVALID_ARG"), (dict(D=0), "INVALID_ARG"), (dict(ld=40), "INVALID_ARG"),
     (dict(n_pages=-1), "INVALID_ARG"), (dict(page_len=0), "INVALID_ARG"), (dict(max_pages=-1), "INVALID_ARG"),
     (dict(dtype=2), "INVALID_ARG"), (dict(k=None), "INVALID_ARG"), (dict(weight=None), "INVALID_ARG"),
-    (dict(table=None), "INVALID_ARG"), (dict(length=None), "INVALID_ARG"), (dict(arrivals=None), "INVALID_ARG"),
+    (dict(table=None), "INVALID_ARG"), (dict(length=None), "INVALID_ARG"), (dict(scratch=None), "INVALID_ARG"),
     (dict(D=129, ld=136), "UNSUPPORTED"), (dict(page_len=24), "UNSUPPORTED"), (dict(B=4097), "UNSUPPORTED"),
     (dict(H=65536), "UNSUPPORTED"), (dict(n_pages=1 << 28), "UNSUPPORTED"), (dict(max_pages=1 << 28), "UNSUPPORTED"),
     (dict(ld=44), "ALIGNMENT"), (dict(k=FAKE + 8), "ALIGNMENT"), (dict(pos=FAKE + 4), "ALIGNMENT"),

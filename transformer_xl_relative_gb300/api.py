@@ -597,10 +597,10 @@ class PagedMemory:
         self.k, self.v, self.pos, self.weight = k, v, pos, weight
         self.table, self.length, self.next_pos, self.device = table, length, next_pos, dev
         B, most = table.shape
-        self._scratch = torch.zeros(B + 1, dtype=torch.int32, device=k.device)     # arrivals, err_flag
+        self._scratch = torch.zeros(B * (H + 1) + 2, dtype=torch.int32, device=k.device)     # the last is err_flag
         at = self._scratch.data_ptr()
         self._c = TxlPaged(k.data_ptr(), v.data_ptr(), pos.data_ptr(), weight.data_ptr(), table.data_ptr(),
-                           length.data_ptr(), next_pos.data_ptr(), at, at + 4 * B, B, H, D, ld, n, page_len, most, dtype_code(k))
+                           length.data_ptr(), next_pos.data_ptr(), at, at + 4 * (B * (H + 1) + 1), B, H, D, ld, n, page_len, most, dtype_code(k))
         self.address = ctypes.addressof(self._c)
         self._shape, self._dtype = (B, H, D), k.dtype
         rows = table.tolist()

@@ -1305,11 +1305,11 @@ txl_status check_paged(const txl_paged* m)
     if (static_cast<int64_t>(m->n_pages) * m->page_len > INT32_MAX || static_cast<int64_t>(m->max_pages) * m->page_len > INT32_MAX)
         return TXL_ERR_UNSUPPORTED;
     if (m->B == 0) return TXL_OK;
-    if (!m->length || !m->next_pos || !m->arrivals || (m->max_pages && !m->table)) return TXL_ERR_INVALID_ARG;
+    if (!m->length || !m->next_pos || !m->scratch || (m->max_pages && !m->table)) return TXL_ERR_INVALID_ARG;
     if (m->n_pages && (!m->k || !m->v || !m->pos || !m->weight)) return TXL_ERR_INVALID_ARG;
-    if (!a16(m->k) || !a16(m->v) || !a16(m->pos) || !a16(m->weight) || !s16(m->ld, m->dtype == TXL_F32 ? 4 : 2))
-        return TXL_ERR_ALIGNMENT;
-    if (!a4(m->length) || !a4(m->next_pos) || !a4(m->arrivals) || !a4(m->table) || !a4(m->err_flag)) return TXL_ERR_ALIGNMENT;
+    if (!a16(m->k) || !a16(m->v) || !s16(m->ld, m->dtype == TXL_F32 ? 4 : 2)) return TXL_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(m->pos) & 7u) || !a4(m->weight)) return TXL_ERR_ALIGNMENT;
+    if (!a4(m->length) || !a4(m->next_pos) || !a4(m->scratch) || !a4(m->table) || !a4(m->err_flag)) return TXL_ERR_ALIGNMENT;
     return TXL_OK;
 }
 
@@ -1317,7 +1317,7 @@ PagedParams paged_params(const txl_paged* m)
 {
     PagedParams p{};
     p.k = m->k; p.v = m->v; p.pos = m->pos; p.weight = m->weight; p.table = m->table;
-    p.length = m->length; p.next_pos = m->next_pos; p.arrivals = m->arrivals; p.err_flag = m->err_flag;
+    p.length = m->length; p.next_pos = m->next_pos; p.scratch = m->scratch; p.err_flag = m->err_flag;
     p.B = m->B; p.H = m->H; p.D = m->D; p.ld = m->ld;
     p.n_pages = m->n_pages; p.page_len = m->page_len; p.max_pages = m->max_pages;
     return p;
@@ -1353,15 +1353,14 @@ size_t paged_workspace(const txl_paged* m, int T, int n_e, int accumulate, char*
         return q;
     };
     char* now = take(static_cast<size_t>(m->B) * sizeof(int4));
-    char* tickets = take(pairs * 4);
     char* part = take(2 * static_cast<size_t>(kPagedMaxCtas) * T * Dp * 4);
     char* ml = take(2 * static_cast<size_t>(kPagedMaxCtas) * T * 8);
-    char* E = take(rows * e_pitch * 4);
+    // one bf16 token a sequence multiplies r beside the keys
+    char* E = take(m->dtype == TXL_BF16 && T == 1 ? 0 : rows * e_pitch * 4);
     char* lse = accumulate ? take(rows * 4) : nullptr;
     char* S = accumulate ? take(rows * cap * 4) : nullptr;
     if (p) {
         p->now = reinterpret_cast<int4*>(now);
-        p->tickets = reinterpret_cast<int*>(tickets);
         p->part = reinterpret_cast<float*>(part);
         p->ml = reinterpret_cast<float*>(ml);
         p->E = reinterpret_cast<float*>(E);

@@ -357,7 +357,8 @@ struct PagedParams {
     void* k; void* v;                           // [n_pages][H][page_len][ld]
     int* pos; float* weight;                    // [n_pages][page_len]
     const int* table;                           // [B][max_pages]
-    int* length; int* next_pos; int* arrivals;  // [B]
+    int* length; int* next_pos;                 // [B]
+    int* scratch;                               // [B] blocks that have pushed, one: that have read the lengths, [B][H] parts done
     int* err_flag;                              // TXL_ERR_PAGE, may be null
     int B, H, D, ld, n_pages, page_len, max_pages;
 };
@@ -385,7 +386,6 @@ struct PagedAttnParams {
     int accumulate;                             // add the attention weights to m.weight
     int cap;                                    // max_pages * page_len
     // workspace
-    int* tickets;                               // [B][H] parts of a (b, h) that are done
     int4* now;                                  // [B] length, first query's position, queries
     float* E;                                   // [B][H][T][e_pitch] position terms, log2 domain
     float* S;                                   // [B][H][T][cap] scores, log2 domain (accumulate)

@@ -32,10 +32,10 @@ __global__ void __launch_bounds__(kPushThreads) paged_push_kernel(const __grid_c
         bool last = true;
         if (gridDim.x > 1) {
             __threadfence();
-            last = atomicAdd(p.m.arrivals + b, 1) == static_cast<int>(gridDim.x) - 1;
+            last = atomicAdd(p.m.scratch + b, 1) == static_cast<int>(gridDim.x) - 1;
         }
         if (last) {
-            p.m.arrivals[b] = 0;
+            p.m.scratch[b] = 0;
             if (room) {
                 p.m.length[b] = len + n;
                 p.m.next_pos[b] = next + n;

@@ -5,11 +5,12 @@
 //     s_ij = scale [ (q_i+u).k_j + (q_i+v).r_min(p_i - p_j, C) ],  visible iff p_j <= p_i,  out_i = softmax_j(s_ij) V
 // and, where asked, weight_j += sum over heads and queries of the softmax.
 //
-//   paged_prep_kernel    new keys and values enter their pages; position terms E[b][h][i][distance]; what the call works
-//                        on (lengths, queries' positions) is fixed in the workspace
+//   paged_prep_kernel    (more than one token, or fp32) new keys and values enter their pages; position terms
+//                        E[b][h][i][distance]; what the call works on (lengths, queries' positions) goes to the workspace
 //   paged_attn_kernel    the tiles of 16 keys of all (sequence, head) pairs in one line, cut into equal shares: a block
-//                        takes a share, and the last block of a pair joins its parts
-//   paged_weight_kernel  (accumulate) 2^(score - log-sum-exp) summed over heads and queries, a thread per slot
+//                        takes a share, and the last block of a pair joins its parts.  One bf16 token a sequence needs no
+//                        preparation: each key's row of r is multiplied beside the key, the new key is a part of its own
+//   paged_weight_kernel  (accumulate) 2^(score - log-sum-exp) summed over heads and queries
 #include <cuda_bf16.h>
 
 #include "txl_mma.cuh"
@@ -21,7 +22,10 @@ namespace txl {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kMinTiles = 8;               // tiles of a share, at least: two a warp
+// A block's work is measured in tiles.  Beginning a pair costs it about as long as kHead tiles take (the chain from the
+// table over the first copies to the join), so a pair counts kHead tiles more; shares are at least kMinTiles, and a pair of
+// up to kWholeTiles goes to one block whole.
+constexpr int kHead = 20, kMinTiles = 8, kWholeTiles = 16;
 constexpr float kNone = -INFINITY;
 
 template <typename T> __device__ __forceinline__ float to_f(T x);
@@ -31,39 +35,23 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ uint4 load16(const void* p)
-{
-    uint4 w;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
-    return w;
-}
-
-// Keeps the first `live` bf16 of eight.
-__device__ __forceinline__ uint4 first_of8(uint4 w, int live)
-{
-    auto keep = [&](uint32_t x, int e) { return live >= e + 2 ? x : live == e + 1 ? x & 0xffffu : 0u; };
-    return make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
-}
-
 // ---------------------------------------------------------------- fragments of the queries
 // A 16 x 16 fragment of mma.m16n8k16 holds eight queries twice: row g the upper 8 bits of (q + bias) * scale, row
-// g + 8 the next 8, so that the sum of the two rows' products has 16 bits of the query.  The channels are permuted:
-// lane (g, t) holds channels 8 c .. 8 c + 7 of query g for its chunks c = t + 4 j, as the keys' rows are loaded.
-template <int NC> struct QFrag { uint32_t hi[NC][4], lo[NC][4]; };
+// g + 8 the next 8, so that the sum of the two rows' products has 16 bits of the query.  Step j: channels 16 j .. 16 j + 15.
+template <int NC> struct QFrag { uint32_t hi[2 * NC][2], lo[2 * NC][2]; };
 
 template <int NC>
 __device__ __forceinline__ void load_q(QFrag<NC>& f, const __nv_bfloat16* q, const float* bias, bool live, int D, float scale,
                                        int t)
 {
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < 2 * NC; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
             float x[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int d = 8 * (t + 4 * j) + 2 * e + k;
+                const int d = 16 * j + 8 * e + 2 * t + k;
                 x[k] = live && d < D ? (__bfloat162float(q[d]) + bias[d]) * scale : 0.f;
             }
             f.hi[j][e] = mma::pack2(x[0], x[1]);
@@ -71,27 +59,13 @@ __device__ __forceinline__ void load_q(QFrag<NC>& f, const __nv_bfloat16* q, con
         }
 }
 
-// Scores of eight queries and the eight rows whose chunks are w: c[0], c[1] rows 2t, 2t+1 for query g.
-template <int NC>
-__device__ __forceinline__ void score8(const QFrag<NC>& f, const uint4* w, float* s)
-{
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        mma::mma16816(c, f.hi[j][0], f.lo[j][0], f.hi[j][1], f.lo[j][1], w[j].x, w[j].y);
-        mma::mma16816(c, f.hi[j][2], f.lo[j][2], f.hi[j][3], f.lo[j][3], w[j].z, w[j].w);
-    }
-    s[0] = c[0] + c[2];
-    s[1] = c[1] + c[3];
-}
-
 // ---------------------------------------------------------------- preparation
-// Blocks 0 .. B-1 take a sequence's new positions, the others position terms: of 8 queries (of all sequences) and a head
-// with kPrepRows distances.
+// The first B * copies blocks take the sequences' new positions, `share` positions a block, the others position terms: of 8
+// queries (of all sequences) and a head with kPrepRows distances.
 constexpr int kPrepRows = 128;
 
 template <typename T>
-__device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b)
+__device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b, int part, int share)
 {
     const PagedParams& m = p.n.m;
     const int n = paged_count(p.n.counts, b, p.n.T);
@@ -99,7 +73,8 @@ __device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b)
     int4 now = make_int4(len, next, n, 0);
     if (p.n.xk && n > 0) {
         if (paged_room(m, b, len, n)) {
-            paged_copy<T>(p.n, b, len, next, 0, n);
+            const int t0 = part * share, t1 = min(n, t0 + share);
+            if (t0 < t1) paged_copy<T>(p.n, b, len, next, t0, t1);
             now.x = len + n;
         } else {
             if (threadIdx.x == 0) page_error(m);
@@ -112,8 +87,7 @@ __device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b)
             now.x = now.z = 0;
         }
     }
-    if (threadIdx.x == 0) p.now[b] = now;
-    for (int h = threadIdx.x; h < m.H; h += kThreads) p.tickets[b * m.H + h] = 0;
+    if (threadIdx.x == 0 && part == 0) p.now[b] = now;
 }
 
 template <int NC>
@@ -129,24 +103,27 @@ __device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h,
     load_q<NC>(q, qr, p.vb + h * m.D, live, m.D, p.qscale, t);
     float* E = p.E + ((static_cast<int64_t>(b) * m.H + h) * T + i) * p.e_pitch;
     const uint16_t* r = static_cast<const uint16_t*>(p.r) + h * p.r_head;
-    for (int x0 = d0 + warp * 8; x0 < min(p.n_e, d0 + kPrepRows); x0 += kWarps * 8) {
-        const uint16_t* row = r + static_cast<int64_t>(min(x0 + g, p.n_e - 1)) * p.r_row;
-        uint4 w[NC];
+    constexpr int kEach = kPrepRows / (8 * kWarps);
+    uint32_t w[kEach][2 * NC][2];
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int c = t + 4 * j;
-            if (p.vec_r && 8 * c + 8 <= m.D) {
-                w[j] = *reinterpret_cast<const uint4*>(row + 8 * c);
-            } else {
-                uint32_t x[8];
+    for (int y = 0; y < kEach; ++y) {
+        const uint16_t* row = r + static_cast<int64_t>(min(d0 + (y * kWarps + warp) * 8 + g, p.n_e - 1)) * p.r_row;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 8 * c + e < m.D ? row[8 * c + e] : 0u;
-                w[j] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        for (int j = 0; j < 2 * NC; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = 16 * j + 8 * e + 2 * t;
+                if (p.vec_r && d + 2 <= m.D) w[y][j][e] = *reinterpret_cast<const uint32_t*>(row + d);
+                else w[y][j][e] = (d < m.D ? row[d] : 0u) | (d + 1 < m.D ? row[d + 1] : 0u) << 16;
             }
-        }
-        float s[2];
-        score8<NC>(q, w, s);
-        if (live) *reinterpret_cast<float2*>(E + x0 + 2 * t) = make_float2(s[0], s[1]);
+    }
+#pragma unroll
+    for (int y = 0; y < kEach; ++y) {
+        const int x0 = d0 + (y * kWarps + warp) * 8;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 2 * NC; ++j) mma::mma16816(c, q.hi[j][0], q.lo[j][0], q.hi[j][1], q.lo[j][1], w[y][j][0], w[y][j][1]);
+        if (live && x0 < p.n_e) *reinterpret_cast<float2*>(E + x0 + 2 * t) = make_float2(c[0] + c[2], c[1] + c[3]);
     }
 }
 
@@ -180,18 +157,18 @@ __device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, 
 }
 
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_constant__ PagedAttnParams p)
+__global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_constant__ PagedAttnParams p, int copies, int share)
 {
     __shared__ float qs[sizeof(T) == 4 ? 8 * 128 : 1];
     __shared__ int far;
     pdl_wait();
     pdl_launch_dependents();
     const PagedParams& m = p.n.m;
-    if (blockIdx.x < static_cast<unsigned>(m.B)) {
-        prep_sequence<T>(p, blockIdx.x);
+    if (blockIdx.x < static_cast<unsigned>(m.B * copies)) {
+        prep_sequence<T>(p, blockIdx.x / copies, blockIdx.x % copies, share);
         return;
     }
-    const int x = blockIdx.x - m.B, parts = (p.n_e + kPrepRows - 1) / kPrepRows;
+    const int x = blockIdx.x - m.B * copies, parts = (p.n_e + kPrepRows - 1) / kPrepRows;
     const int d0 = x % parts * kPrepRows, h = x / parts % m.H, f0 = x / parts / m.H * 8;
     // distances beyond the start of all of these sequences are not met (next_pos changes in the attention's kernel)
     if (threadIdx.x == 0) far = 0;
@@ -207,10 +184,20 @@ __global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------- attention
+// a / b where that is an int (64-bit divisions are slow, and most numbers are small).
+__device__ __forceinline__ int quotient(int64_t a, int b)
+{
+    if (static_cast<uint64_t>(a) >> 32 == 0) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+    return static_cast<int>(a / b);
+}
+
 // What a block knows of the part of a (sequence, head) pair that it works on.
 struct Part {
     int b, h, len, first, n;       // slots, position of the first query, queries
     int t0, t1, tiles;             // its tiles, of the pair's
+    int parts, first_block;        // the pair's parts, and the block of the first
+    bool room;                     // the new key has a page (else the sequence is left as it was)
+    bool own;                      // the pair has a new key that is not among the slots (k_new, position `first`)
 };
 
 // Page of the tiles that a warp will come to: lane x knows that of the warp's x-th tile from `base` on.
@@ -220,8 +207,9 @@ struct Pages {
     {
         base = tile;
         const int at = tile + kWarps * lane;
-        mine = at < a.t1 ? page_of(m, a.b, at * kPageUnit) : -1;
-        if (at < a.t1 && mine < 0) page_error(m);
+        const bool used = at < a.t1 && at * kPageUnit < a.len;
+        mine = used ? page_of(m, a.b, at * kPageUnit) : -1;
+        if (used && mine < 0) page_error(m);
     }
     // page of `tile` (a warp's own, at or after base)
     __device__ __forceinline__ int get(const PagedParams& m, const Part& a, int tile, int lane)
@@ -231,224 +219,378 @@ struct Pages {
     }
 };
 
-// Running softmax of one query: maximum, sum, weighted values are kept by the callers.
+// Index of the position term of a query at `at` and a key at pos <= at.
+__device__ __forceinline__ int term(const PagedAttnParams& p, int at, int pos)
+{
+    return static_cast<int>(min(static_cast<unsigned>(at) - static_cast<unsigned>(pos), static_cast<unsigned>(p.n_e - 1)));
+}
+
 __device__ __forceinline__ float finite_or_0(float m) { return m == kNone ? 0.f : m; }
 
-// bf16.  A warp's tile is 16 keys: lane (g, t) loads chunks t + 4 j of keys g and g + 8, and chunks g + 8 x of the
-// values of keys 2t, 2t+1, 2t+8, 2t+9, all of 16 bytes from global memory: the first are B fragments of the scores' mma as
-// they are, the others become those of P.V by pairing the halves of two keys' words.  NV = ceil(D / 64).
-template <int NC, int NQ, bool W>
-__device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& a, float* buf, float* bml)
+// bf16.  A warp takes every fourth tile of 16 keys through its own ring of stages in shared memory: asynchronous copies
+// of 16 bytes, one or two tiles ahead.  What lies past a sequence's last slot, or past D, arrives as zeros.  Rows are an odd
+// number of 16-byte units apart, so that the eight rows of an ldmatrix lie in different banks.
+template <int NC> constexpr int kStages = NC == 2 ? 2 : 3;              // (four blocks of two stages on an SM, not three of three)
+template <int NC> constexpr int kPitch = (4 * NC + 1) * 16;               // bytes
+template <int NC> constexpr int kStage = 2 * kPageUnit * kPitch<NC>;      // K and V of a tile
+template <int NC> constexpr int kWarpBytes = kStages<NC> * kStage<NC>;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 {
-    constexpr int NV = (NC + 1) / 2;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements, two of row lane / 4 in each lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Products: keys are the 16 rows of the mma's A, as ldmatrix brings them, and columns 2 i, 2 i + 1 of its B hold query i
+// twice: the upper 8 bits of (q + u) scale, and the next 8.  Lane (g, t) then has both for query 4 x + t and keys g and g + 8,
+// and, with the values transposed as A and the weights split likewise as B, the same query's sums of channels g and g + 8 of
+// each 16: everything that belongs to a query stays in its lanes.
+// ONE (one token): (q + v).r of each key's own distance joins the sums, with r's rows as A (each lane loads units t, t + 4,
+// .. of two rows: their channels' order is that of qv).  Otherwise the terms come from E.
+template <int NC> struct BFrag { uint32_t w[2 * NC][2]; };
+
+// The part's queries in shared memory as the columns of B want them, by the whole block: row 2 i the upper 8 bits of (q_i + u)
+// scale, row 2 i + 1 the next 8; with ONE two more rows for v.  Rows of kQPitch bf16 (in different banks), zeros past D
+// and from query n on.
+template <int NC> constexpr int kQPitch = 32 * NC + 8;
+template <int NC, int NQ, bool ONE> constexpr int kQRows = ONE ? 16 : 8 * NQ;
+
+template <int NC, int NQ, bool ONE>
+__device__ __forceinline__ void put_queries(const PagedAttnParams& p, const Part& a, uint16_t* qs)
+{
+    const PagedParams& m = p.n.m;
+    constexpr int kWidth = 32 * NC;
+    for (int x = threadIdx.x; x < kQRows<NC, NQ, ONE> / 2 * kWidth; x += kThreads) {
+        const int row = x / kWidth, d = x % kWidth, i = ONE ? row & 3 : row;
+        float y = 0.f;
+        if (i < a.n && d < m.D) {
+            const float* bias = (ONE && row >= 4 ? p.vb : p.u) + a.h * m.D;
+            y = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d]) + bias[d]) * p.qscale;
+        }
+        const __nv_bfloat16 hi = __float2bfloat16_rn(y);
+        qs[2 * row * kQPitch<NC> + d] = __bfloat16_as_ushort(hi);
+        qs[(2 * row + 1) * kQPitch<NC> + d] = __bfloat16_as_ushort(__float2bfloat16_rn(y - __bfloat162float(hi)));
+    }
+}
+
+// ROWS: in the order of the units of r's rows.
+template <int NC, bool ROWS>
+__device__ __forceinline__ void load_b(BFrag<NC>& f, const uint16_t* row, int t)
+{
+#pragma unroll
+    for (int j = 0; j < 2 * NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = ROWS ? 8 * (t + 4 * (j >> 1)) + 4 * (j & 1) + 2 * e : 16 * j + 8 * e + 2 * t;
+            f.w[j][e] = *reinterpret_cast<const uint32_t*>(row + d);
+        }
+}
+
+// ONE: a pair's new key, by one warp: its score, its values as a part of one key, and its row into the page (which the
+// sequence may lack: then nothing is written).
+template <bool W>
+__device__ __forceinline__ void own_key(const PagedAttnParams& p, const Part& a, float* buf, float* bml)
+{
+    const PagedParams& m = p.n.m;
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + a.b * p.q_sb + a.h * p.q_sh;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
+    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.r) + a.h * p.r_head;
+    const int page = page_of(m, a.b, a.len), row = a.len % m.page_len;
+    __nv_bfloat16 *kd = nullptr, *vd = nullptr;
+    if (page >= 0) {
+        const int64_t at = page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld;
+        kd = static_cast<__nv_bfloat16*>(m.k) + at;
+        vd = static_cast<__nv_bfloat16*>(m.v) + at;
+    }
+    const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
+    float s = 0.f;
+    for (int d = lane; d < m.ld; d += 32) {
+        const bool in = d < m.D;
+        const __nv_bfloat16 kk = in ? k[d] : zero, vv = in ? v[d] : zero;
+        if (in) {
+            const float x = __bfloat162float(q[d]);
+            s = fmaf((x + p.u[a.h * m.D + d]) * p.qscale, __bfloat162float(kk), s);
+            s = fmaf((x + p.vb[a.h * m.D + d]) * p.qscale, __bfloat162float(r[d]), s);
+            buf[d] = __bfloat162float(vv);
+        }
+        if (page >= 0) {
+            kd[d] = kk;
+            vd[d] = vv;
+        }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0) {
+        bml[0] = s;
+        bml[1] = s != s ? s : s == kNone ? 0.f : 1.f;
+        if (page >= 0) {
+            if (W) p.S[(static_cast<int64_t>(a.b) * m.H + a.h) * p.cap + a.len] = s;
+            if (a.h == 0) {
+                m.pos[static_cast<int64_t>(page) * m.page_len + row] = a.first;
+                m.weight[static_cast<int64_t>(page) * m.page_len + row] = 0.f;
+            }
+        } else {
+            page_error(m);
+        }
+    }
+}
+
+// once(): called when the first copies are under way.
+template <int NC, int NQ, bool ONE, bool W, typename F>
+__device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& a, char* ring, float* bml, float* own, uint16_t* qs,
+                                          F&& once)
+{
     const PagedParams& m = p.n.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int T = p.n.T;
-    QFrag<NC> q[NQ];
+    const uint32_t stage0 = smem_u32(ring);
+
+    // a lane's pieces of a tile: of the rows of K and V, units of 16 bytes (a unit wholly past D is never copied, and zero
+    // from the start)
+    constexpr int kUnits = 4 * NC, kPieces = kPageUnit * kUnits / 32;
+    const int units = (m.D + 7) / 8;
+    auto copy = [&](int page, int tile, int stage) {
+        const int row0 = tile * kPageUnit % m.page_len;
+        const int64_t at = page < 0 ? 0 : page_row0(m, page, a.h) + static_cast<int64_t>(row0) * m.ld;
+        const uint16_t* k = static_cast<const uint16_t*>(m.k) + at;
+        const uint16_t* v = static_cast<const uint16_t*>(m.v) + at;
+        const int rows = page < 0 ? 0 : a.len - tile * kPageUnit;          // that hold something
+        const uint32_t dst = stage0 + stage * kStage<NC>;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int x = lane + 32 * j, row = x / kUnits, c = x % kUnits;
+            if (c >= units) continue;
+            const int bytes = row < rows ? min(16, 2 * (m.D - 8 * c)) : 0, off = row < rows ? row * m.ld + 8 * c : 0;
+            copy16(dst + row * kPitch<NC> + 16 * c, k + off, bytes);
+            copy16(dst + (kPageUnit + row) * kPitch<NC> + 16 * c, v + off, bytes);
+        }
+    };
+    Pages pages;
+    pages.look(m, a, a.t0 + warp, lane);
+    if (units < kUnits) {
+        for (int x = lane; x < kStages<NC> * 2 * kPageUnit * (kUnits - units); x += 32) {
+            const int row = x / (kUnits - units), c = units + x % (kUnits - units);
+            *reinterpret_cast<uint4*>(ring + row * kPitch<NC> + 16 * c) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const int first = a.t0 + warp;
+#pragma unroll
+    for (int x = 0; x < kStages<NC> - 1; ++x) {
+        const int tile = first + x * kWarps;
+        if (tile < a.t1) copy(pages.get(m, a, tile, lane), tile, x);
+        mma::cp_async_commit();
+    }
+    // positions of keys g and g + 8, two tiles ahead (a slot that holds nothing is ahead of every query)
+    constexpr int kAhead = 0x7fffffff;
+    int pos[2];
+    auto load_pos = [&](int page, int tile) {
+        const int* at = m.pos + static_cast<int64_t>(max(page, 0)) * m.page_len + tile * kPageUnit % m.page_len + g;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) pos[y] = page >= 0 && tile * kPageUnit + 8 * y + g < a.len ? at[8 * y] : kAhead;
+    };
+    if (first < a.t1) load_pos(pages.get(m, a, first, lane), first);
+    put_queries<NC, NQ, ONE>(p, a, qs);
+    if (ONE && a.own && a.t1 == a.tiles && warp == kWarps - 1) own_key<W>(p, a, own, bml + 2 * kWarps);
+    once();
+    __syncthreads();
+
+    BFrag<NC> q[NQ], qv;
     const float* E[NQ];
     float* S[NQ];
     bool live[NQ];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
-        const int i = 8 * x + g;
-        live[x] = i < a.n;
-        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q);
-        if (live[x]) qr += a.b * p.q_sb + i * p.q_st + a.h * p.q_sh;
-        load_q<NC>(q[x], qr, p.u + a.h * m.D, live[x], m.D, p.qscale, t);
-        const int64_t row = (static_cast<int64_t>(a.b) * m.H + a.h) * T + min(i, T - 1);
-        E[x] = p.E + row * p.e_pitch;
+        load_b<NC, false>(q[x], qs + (8 * x + g) * kQPitch<NC>, t);
+        live[x] = 4 * x + t < a.n;
+        const int64_t row = (static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1);
+        E[x] = ONE ? nullptr : p.E + row * p.e_pitch;
         S[x] = W ? p.S + row * p.cap : nullptr;
     }
-    float o[NQ][NV][8][4];
+    if (ONE) load_b<NC, true>(qv, qs + (8 + g) * kQPitch<NC>, t);
+    float o[NQ][2 * NC][4];
     float mx[NQ], sum[NQ];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
         mx[x] = kNone;
         sum[x] = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[x][v][e][0] = o[x][v][e][1] = o[x][v][e][2] = o[x][v][e][3] = 0.f;
+        for (int z = 0; z < 2 * NC; ++z) o[x][z][0] = o[x][z][1] = o[x][z][2] = o[x][z][3] = 0.f;
     }
-    const int chunks = (m.D + 7) / 8, last_live = m.D - 8 * (chunks - 1);       // channels of a row's last chunk
-
-    Pages pages;
-    pages.look(m, a, a.t0 + warp, lane);
-    uint4 kw[2][NC], vw[4][NV];
-    int2 pw[2], pn[2];
-    auto row_of = [&](int page, int tile) { return tile * kPageUnit % m.page_len; };
-    auto load_k = [&](int page, int tile) {
-        const uint16_t* k = static_cast<const uint16_t*>(m.k) + page_row0(m, page, a.h) + static_cast<int64_t>(row_of(page, tile) + g) * m.ld;
+    // what a tile's position terms come from, one tile ahead: which keys a lane's query sees, E's terms (e) or r's rows (rw)
+    float e[NQ][2];
+    uint4 rw[2][NC];
+    bool near = false;
+    const uint16_t* r = static_cast<const uint16_t*>(p.r) + a.h * p.r_head;
+    auto load_row = [&](int distance, uint4* w) {
+        const uint16_t* row = r + static_cast<int64_t>(distance) * p.r_row;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int j = 0; j < NC; ++j) {
+            const int c = t + 4 * j;
+            if (p.vec_r && 8 * c + 8 <= m.D) {
+                w[j] = *reinterpret_cast<const uint4*>(row + 8 * c);
+            } else {
+                uint32_t x[8];
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int c = t + 4 * j;
-                kw[y][j] = c < chunks ? load16(k + y * 8 * m.ld + 8 * c) : make_uint4(0, 0, 0, 0);
+                for (int z = 0; z < 8; ++z) x[z] = 8 * c + z < m.D ? row[8 * c + z] : 0u;
+                w[j] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
             }
+        }
     };
-    auto load_v = [&](int page, int tile) {
-        const uint16_t* v = static_cast<const uint16_t*>(m.v) + page_row0(m, page, a.h) + static_cast<int64_t>(row_of(page, tile) + 2 * t) * m.ld;
+    auto rows_mma = [&](float* c) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int x = 0; x < NV; ++x) {
-                const int c = g + 8 * x;
-                vw[y][x] = c < chunks ? load16(v + ((y & 1) + (y & 2) * 4) * m.ld + 8 * c) : make_uint4(0, 0, 0, 0);
-            }
+        for (int j = 0; j < NC; ++j) {
+            mma::mma16816(c, rw[0][j].x, rw[1][j].x, rw[0][j].y, rw[1][j].y, qv.w[2 * j][0], qv.w[2 * j][1]);
+            mma::mma16816(c, rw[0][j].z, rw[1][j].z, rw[0][j].w, rw[1][j].w, qv.w[2 * j + 1][0], qv.w[2 * j + 1][1]);
+        }
     };
-    auto load_pos = [&](int page, int tile, int2* w) {
-        const int* at = m.pos + static_cast<int64_t>(page) * m.page_len + row_of(page, tile) + 2 * t;
-        w[0] = *reinterpret_cast<const int2*>(at);
-        w[1] = *reinterpret_cast<const int2*>(at + 8);
-    };
-    // position terms of a tile; what its masks leave out is -inf
-    float e[NQ][4];
-    auto load_e = [&](int tile, const int2* w) {
-        const int pos[4] = {w[0].x, w[0].y, w[1].x, w[1].y};
+    auto load_terms = [&]() {
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int slot = tile * kPageUnit + 2 * t + (y & 1) + (y & 2) * 4;
-                const int delta = a.first + 8 * x + g - pos[y];
-                e[x][y] = kNone;
-                if (live[x] && delta >= 0 && slot < a.len) e[x][y] = E[x][min(delta, p.n_e - 1)];
+            for (int y = 0; y < 2; ++y) {
+                const int at = a.first + 4 * x + t;
+                const bool seen = live[x] && pos[y] <= at;
+                if constexpr (ONE) e[x][y] = seen ? 0.f : kNone;
+                else e[x][y] = seen ? E[x][term(p, at, pos[y])] : kNone;
             }
+        if constexpr (ONE) {
+            const int d0 = pos[0] <= a.first ? term(p, a.first, pos[0]) : p.n_e - 1;
+            const int d1 = pos[1] <= a.first ? term(p, a.first, pos[1]) : p.n_e - 1;
+            near = __any_sync(0xffffffffu, d0 < p.n_e - 1 || d1 < p.n_e - 1);
+            if (near) {
+                load_row(d0, rw[0]);
+                load_row(d1, rw[1]);
+            }
+        }
     };
-    int page = -1, next = -1;
-    int tile = a.t0 + warp;
-    if (tile < a.t1) {
-        page = pages.get(m, a, tile, lane);
-        if (page >= 0) {
-            load_pos(page, tile, pw);
-            load_k(page, tile);
-            load_v(page, tile);
-            load_e(tile, pw);
+    float far = 0.f;                                           // ONE: the term of all distances from n_e - 1 on
+    if constexpr (ONE) {
+        load_row(p.n_e - 1, rw[0]);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) rw[1][j] = rw[0][j];
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        rows_mma(c);
+        far = c[0] + c[1];
+    }
+    if (first < a.t1) {
+        load_terms();
+        if (first + kWarps < a.t1) load_pos(pages.get(m, a, first + kWarps, lane), first + kWarps);
+    }
+    // ldmatrix addresses in a stage: K as [key][channel], V as [key][channel] transposed
+    const uint32_t k_at = stage0 + (lane & 15) * kPitch<NC> + (lane >> 4) * 16;
+    const uint32_t v_at = stage0 + (kPageUnit + (lane & 7) + (lane >> 4) * 8) * kPitch<NC> + ((lane >> 3) & 1) * 16;
+    int stage = 0, ahead = kStages<NC> - 1;
+    for (int tile = first; tile < a.t1; tile += kWarps) {
+        copies_wait<kStages<NC> - 2>();
+        __syncwarp();                                          // everyone's pieces are here, and the last stage is read
+        if (tile + (kStages<NC> - 1) * kWarps < a.t1) {
+            const int to = tile + (kStages<NC> - 1) * kWarps;
+            copy(pages.get(m, a, to, lane), to, ahead);
         }
+        mma::cp_async_commit();
+        ahead = stage;
+        const uint32_t off = stage * kStage<NC>;
+        stage = stage + 1 == kStages<NC> ? 0 : stage + 1;
+
+        float c[NQ][4] = {};
+#pragma unroll
+        for (int j = 0; j < 2 * NC; ++j) {
+            uint32_t w[4];
+            mma::ldsm_x4(k_at + off + 32 * j, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) mma::mma16816(c[x], w[0], w[1], w[2], w[3], q[x].w[j][0], q[x].w[j][1]);
+        }
+        if (ONE) {
+            if (near) rows_mma(c[0]);
+            else c[0][0] += far, c[0][2] += far;
+        }
+        float s[NQ][2];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s[x][y] = e[x][y] == kNone ? kNone : c[x][2 * y] + c[x][2 * y + 1] + e[x][y];
         if (tile + kWarps < a.t1) {
-            next = pages.get(m, a, tile + kWarps, lane);
-            if (next >= 0) load_pos(next, tile + kWarps, pn);
+            load_terms();
+            if (tile + 2 * kWarps < a.t1) load_pos(pages.get(m, a, tile + 2 * kWarps, lane), tile + 2 * kWarps);
         }
-    }
-    for (; tile < a.t1; tile += kWarps) {
-        // page, pw's terms e, kw, vw: this tile's; next, pn: the following one's
-        const bool more = tile + kWarps < a.t1;
-        float s[NQ][4];
-        if (page >= 0) {
-            if (last_live < 8) {
+        // the maximum follows only where a score is far above it: a weight may be up to 2^kSlack
+        constexpr float kSlack = 8.f;
+        bool grows = false;
 #pragma unroll
-                for (int j = 0; j < NC; ++j)
-                    if (t + 4 * j == chunks - 1) {
-                        kw[0][j] = first_of8(kw[0][j], last_live);
-                        kw[1][j] = first_of8(kw[1][j], last_live);
-                    }
-            }
+        for (int x = 0; x < NQ; ++x) grows |= fmaxf(s[x][0], s[x][1]) > mx[x] + kSlack;
+        if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                score8<NC>(q[x], kw[0], s[x]);
-                score8<NC>(q[x], kw[1], s[x] + 2);
+                float top = fmaxf(s[x][0], s[x][1]);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) s[x][y] = e[x][y] == kNone ? kNone : s[x][y] + e[x][y];
+                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float now = fmaxf(mx[x], top), f = mma::ex2(mx[x] - finite_or_0(now));
+                mx[x] = now;
+                sum[x] *= f;
+#pragma unroll
+                for (int z = 0; z < 2 * NC; ++z)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) o[x][z][y] *= f;
             }
         }
-        int after = -1;
-        if (more) {
-            if (next >= 0) {
-                load_k(next, tile + kWarps);
-                load_e(tile + kWarps, pn);
+        uint32_t b0[NQ], b1[NQ];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            if (W && live[x]) {
+                // (not behind the last slot: that is the new key's)
+                if (tile * kPageUnit + g < a.len) S[x][tile * kPageUnit + g] = s[x][0];
+                if (tile * kPageUnit + 8 + g < a.len) S[x][tile * kPageUnit + 8 + g] = s[x][1];
             }
-            if (tile + 2 * kWarps < a.t1) {
-                after = pages.get(m, a, tile + 2 * kWarps, lane);
-                if (after >= 0) load_pos(after, tile + 2 * kWarps, pn);
-            }
+            const float base = finite_or_0(mx[x]);
+            const float p0 = mma::ex2(s[x][0] - base), p1 = mma::ex2(s[x][1] - base);
+            sum[x] += p0 + p1;
+            // rows of keys with a query's weight in two columns (its upper 8 bits, the next 8), transposed into the fragment
+            const uint32_t hi = mma::pack2(p0, p1);
+            const float h0 = mma::bf16_lo(hi), h1 = mma::bf16_hi(hi);
+            b0[x] = transpose8(mma::pack2(h0, p0 - h0));
+            b1[x] = transpose8(mma::pack2(h1, p1 - h1));
         }
-        if (page >= 0) {
-            // values of slots past the end are anything: they count as 0
-            if (tile * kPageUnit + kPageUnit > a.len) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (tile * kPageUnit + 2 * t + (y & 1) + (y & 2) * 4 >= a.len)
+        for (int z = 0; z < 2 * NC; ++z) {
+            uint32_t w[4];
+            mma::ldsm_x4_t(v_at + off + 32 * z, w[0], w[1], w[2], w[3]);
 #pragma unroll
-                        for (int x = 0; x < NV; ++x) vw[y][x] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-                if (W && live[x]) {
-                    *reinterpret_cast<float2*>(S[x] + tile * kPageUnit + 2 * t) = make_float2(s[x][0], s[x][1]);
-                    *reinterpret_cast<float2*>(S[x] + tile * kPageUnit + 8 + 2 * t) = make_float2(s[x][2], s[x][3]);
-                }
-                float top = fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (__any_sync(0xffffffffu, top > mx[x])) {
-                    const float now = fmaxf(mx[x], top), f = mma::ex2(mx[x] - finite_or_0(now));
-                    mx[x] = now;
-                    sum[x] *= f;
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-#pragma unroll
-                        for (int z = 0; z < 8; ++z)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) o[x][v][z][y] *= f;
-                }
-                const float base = finite_or_0(mx[x]);
-                float pr[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    pr[y] = mma::ex2(s[x][y] - base);
-                    sum[x] += pr[y];
-                }
-                // a weight is held to 16 bits as well: its upper 8 in row g, the next 8 in row g + 8
-                const uint32_t h0 = mma::pack2(pr[0], pr[1]), h1 = mma::pack2(pr[2], pr[3]);
-                const uint32_t l0 = mma::pack2(pr[0] - mma::bf16_lo(h0), pr[1] - mma::bf16_hi(h0));
-                const uint32_t l1 = mma::pack2(pr[2] - mma::bf16_lo(h1), pr[3] - mma::bf16_hi(h1));
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&vw[0][v]);
-                        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&vw[1][v]);
-                        const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&vw[2][v]);
-                        const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&vw[3][v]);
-                        const uint32_t pick = z & 1 ? 0x7632 : 0x5410;
-                        mma::mma16816(o[x][v][z], h0, l0, h1, l1, __byte_perm(w0[z >> 1], w1[z >> 1], pick),
-                                      __byte_perm(w2[z >> 1], w3[z >> 1], pick));
-                    }
-            }
+            for (int x = 0; x < NQ; ++x) mma::mma16816(o[x][z], w[0], w[1], w[2], w[3], b0[x], b1[x]);
         }
-        if (more && next >= 0) load_v(next, tile + kWarps);
-        page = next;
-        next = after;
     }
-    // the warp's share into shared memory: channels 64 v + 16 t + z and + 8 + z of query g
+    __syncwarp();                                              // the ring is read: it takes the warp's sums
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], d);
         if (!live[x]) continue;
-        const int i = 8 * x + g;
-        if (t == 0) {
+        const int i = 4 * x + t;
+        if (g == 0) {
             bml[(warp * T + i) * 2] = mx[x];
             bml[(warp * T + i) * 2 + 1] = sum[x];
         }
-        float* row = buf + (warp * T + i) * p.Dp;
+        float* row = reinterpret_cast<float*>(ring) + i * (32 * NC) + g;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int d = 64 * v + 16 * t + 8 * y + z;
-                    if (d < p.Dp) row[d] = o[x][v][z][y] + o[x][v][z][y + 2];
-                }
+        for (int z = 0; z < 2 * NC; ++z) {
+            row[16 * z] = o[x][z][0] + o[x][z][1];
+            row[16 * z + 8] = o[x][z][2] + o[x][z][3];
+        }
     }
 }
 
 // fp32, CUDA cores.  Lane (g, t) takes keys g and g + 8 of a tile and channels 4 (t + 4 j) .. + 3; each of the eight g keeps
 // maximum and sums of its own, which meet at the end.  NQ queries at a time: their sums stay in registers.
 template <int NC, int NQ, bool W>
-__device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a, float* buf, float* bml, float* qs)
+__device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a, float* buf, int share, float* bml, float* qs)
 {
     constexpr int NJ = 2 * NC;             // chunks of four channels of a lane
     const PagedParams& m = p.n.m;
@@ -504,11 +646,10 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
                     }
                     s += __shfl_xor_sync(0xffffffffu, s, 1);
                     s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    const int delta = a.first + i - pos;
-                    const bool seen = i < a.n && slot < a.len && delta >= 0;
+                    const bool seen = i < a.n && slot < a.len && pos <= a.first + i;
                     const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i;
-                    s = seen ? s + p.E[er * p.e_pitch + min(delta, p.n_e - 1)] : kNone;
-                    if (W && t == 0 && i < a.n) p.S[er * p.cap + slot] = s;
+                    s = seen ? s + p.E[er * p.e_pitch + term(p, a.first + i, pos)] : kNone;
+                    if (W && t == 0 && i < a.n && slot < a.len) p.S[er * p.cap + slot] = s;
                     if (seen) {
                         if (!(s <= mx[x])) {
                             const float now = fmaxf(mx[x], s), f = exp2f(mx[x] - finite_or_0(now));
@@ -548,7 +689,7 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
                     if (g == 0 && i0 + x < a.n && 4 * (t + 4 * j) + c < p.Dp)
-                        buf[(warp * T + i0 + x) * p.Dp + 4 * (t + 4 * j) + c] = y;
+                        buf[warp * share + (i0 + x) * p.Dp + 4 * (t + 4 * j) + c] = y;
                 }
             if (lane == 0 && i0 + x < a.n) {
                 bml[(warp * T + i0 + x) * 2] = top;
@@ -558,33 +699,53 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
     }
 }
 
+// Adds one to a ticket: what the block wrote before (and a barrier) is seen by the block that finds it the last.
+__device__ __forceinline__ int arrive(int* ticket)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+    return old;
+}
+
 template <typename T> __device__ __forceinline__ T* out_row(const PagedAttnParams& p, const Part& a, int i)
 {
     return static_cast<T*>(p.out) + a.b * p.o_sb + i * p.o_st + a.h * p.o_sh;
 }
 
 // One query's row again, key by key on the CUDA cores: its sums are not finite, and a value that is not finite at a key
-// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: 2 + kThreads floats.
+// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: kThreads floats.
 template <typename T>
-__device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, float* tot)
+__device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, bool terms, float* tot)
 {
     const PagedParams& m = p.n.m;
     const T* q = static_cast<const T*>(p.q) + a.b * p.q_sb + i * p.q_st + a.h * p.q_sh;
     const float* E = p.E + ((static_cast<int64_t>(a.b) * m.H + a.h) * p.n.T + i) * p.e_pitch;
-    const int at = a.first + i;
-    auto score = [&](int s, int page) {                       // NaN counts as seen
-        const int delta = at - m.pos[static_cast<int64_t>(page) * m.page_len + s % m.page_len];
-        if (delta < 0) return kNone;
-        const T* k = static_cast<const T*>(m.k) + page_row0(m, page, a.h) + static_cast<int64_t>(s % m.page_len) * m.ld;
+    const int at = a.first + i, keys = a.len + (a.own ? 1 : 0);
+    // slot s, or the new key behind the last; null where there is none
+    auto row = [&](int s, bool value) -> const T* {
+        if (s == a.len)
+            return value ? static_cast<const T*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh
+                         : static_cast<const T*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
+        const int page = page_of(m, a.b, s);
+        if (page < 0) return nullptr;
+        return static_cast<const T*>(value ? m.v : m.k) + page_row0(m, page, a.h) + static_cast<int64_t>(s % m.page_len) * m.ld;
+    };
+    auto score = [&](int s) {
+        const T* k = s < keys ? row(s, false) : nullptr;
+        if (!k) return kNone;
+        const int pos = s == a.len ? at : m.pos[static_cast<int64_t>(page_of(m, a.b, s)) * m.page_len + s % m.page_len];
+        if (pos > at) return kNone;
+        const int distance = term(p, at, pos);
+        const T* r = static_cast<const T*>(p.r) + a.h * p.r_head + distance * p.r_row;
         float x = 0.f;
-        for (int d = 0; d < m.D; ++d) x = fmaf((to_f(q[d]) + p.u[a.h * m.D + d]) * p.qscale, to_f(k[d]), x);
-        return x + E[min(delta, p.n_e - 1)];
+        for (int d = 0; d < m.D; ++d) {
+            x = fmaf((to_f(q[d]) + p.u[a.h * m.D + d]) * p.qscale, to_f(k[d]), x);
+            if (!terms) x = fmaf((to_f(q[d]) + p.vb[a.h * m.D + d]) * p.qscale, to_f(r[d]), x);
+        }
+        return terms ? x + E[distance] : x;
     };
     float top = kNone;
-    for (int s = threadIdx.x; s < a.len; s += kThreads) {
-        const int page = page_of(m, a.b, s);
-        if (page >= 0) top = fmaxf(top, score(s, page));
-    }
+    for (int s = threadIdx.x; s < keys; s += kThreads) top = fmaxf(top, score(s));
     __syncthreads();
     tot[threadIdx.x] = top;
     __syncthreads();
@@ -592,35 +753,32 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     top = finite_or_0(top);
     float sum = 0.f, o = 0.f;
     const int d = threadIdx.x;                                // D <= 128: a channel a thread
-    for (int s0 = 0; s0 < a.len; s0 += kThreads) {
-        const int s = s0 + threadIdx.x;
-        const int page = s < a.len ? page_of(m, a.b, s) : -1;
-        float x = kNone;
-        if (page >= 0) x = score(s, page);
+    for (int s0 = 0; s0 < keys; s0 += kThreads) {
+        const float x = score(s0 + threadIdx.x);
         __syncthreads();
         tot[threadIdx.x] = x;
         __syncthreads();
-        for (int y = 0; y < min(kThreads, a.len - s0); ++y) {
-            const int from = page_of(m, a.b, s0 + y);
+        for (int y = 0; y < min(kThreads, keys - s0); ++y) {
             // (a key that is seen and scores -inf weighs 0 as well; its values count as unseen)
-            if (from < 0 || tot[y] == kNone) continue;
+            if (tot[y] == kNone) continue;
             const float w = exp2f(tot[y] - top);
             sum += w;
-            if (d < m.D)
-                o = fmaf(w, to_f(static_cast<const T*>(m.v)[page_row0(m, from, a.h) + static_cast<int64_t>((s0 + y) % m.page_len) * m.ld + d]), o);
+            if (d < m.D) o = fmaf(w, to_f(row(s0 + y, true)[d]), o);
         }
     }
     if (d < m.D) out_row<T>(p, a, i)[d] = from_f<T>(sum == 0.f ? 0.f : o / sum);
 }
 
 // The four warps' shares of a part joined: into the output where the part is the whole pair, else into the workspace;
-// the last block of a pair joins the parts.  buf: the warps' sums [kWarps][T][Dp]; bml: [kWarps][T][2].
-template <typename T, bool W>
-__device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, float* buf, float* bml, int share, int64_t tile0)
+// the last block of a pair joins the parts.  buf: the warps' sums [T][Dp], `pitch` apart, and (a new key's) own[D]; bml:
+// their maxima and weights [kWarps + 1][T][2].  The tickets are zero before and after the call.
+template <typename T, bool ONE, bool W>
+__device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, float* buf, int pitch, const float* own, float* bml)
 {
     __shared__ int last, again;
     const PagedParams& m = p.n.m;
     const int Tq = p.n.T, D = m.D, tid = threadIdx.x;
+    const bool room = a.room, with_own = ONE && a.own && a.t1 == a.tiles;
     if (tid == 0) again = 0;
     __syncthreads();
     const bool whole = a.t0 == 0 && a.t1 == a.tiles;
@@ -631,20 +789,26 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
         float top = kNone;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, bml[(w * Tq + i) * 2]);
+        if (with_own) top = fmaxf(top, bml[2 * kWarps]);
         const float base = finite_or_0(top);
         float y = 0.f, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = exp2f(bml[(w * Tq + i) * 2] - base);
-            y = fmaf(f, buf[(w * Tq + i) * p.Dp + d], y);
+            y = fmaf(f, buf[w * pitch + i * p.Dp + d], y);
             l = fmaf(f, bml[(w * Tq + i) * 2 + 1], l);
         }
-        if (whole) {
+        if (with_own && bml[2 * kWarps] != kNone) {
+            const float f = exp2f(bml[2 * kWarps] - base);
+            y = fmaf(f, own[d], y);
+            l = fmaf(f, bml[2 * kWarps + 1], l);
+        }
+        if (whole && room) {
             const float v = l == 0.f ? 0.f : y / l;
             out_row<T>(p, a, i)[d] = from_f<T>(v);
             if (!isfinite(y) || !isfinite(l)) atomicOr(&again, 1 << i);
             if (W && d == 0) p.lse[(static_cast<int64_t>(a.b) * m.H + a.h) * Tq + i] = base + log2f(l);
-        } else {
+        } else if (!whole) {
             p.part[(static_cast<int64_t>(slot) * Tq + i) * p.Dp + d] = y;
             if (d == 0) {
                 p.ml[(slot * Tq + i) * 2] = top;
@@ -653,38 +817,41 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
         }
     }
     if (!whole) {
-        // blocks first .. first + n - 1 hold the pair's parts
-        const int64_t begin = tile0, end = tile0 + a.tiles;
-        const int first = static_cast<int>(begin / share), n = static_cast<int>((end - 1) / share) - first + 1;
-        __threadfence();
+        // blocks first_block .. first_block + parts - 1 hold the pair's parts, the first one in its odd slot
+        const int n = a.parts;
         __syncthreads();
-        if (tid == 0) last = atomicAdd(p.tickets + a.b * m.H + a.h, 1) == n - 1;
+        if (tid == 0) {
+            int* ticket = m.scratch + m.B + 1 + a.b * m.H + a.h;
+            last = arrive(ticket) == n - 1;
+            if (last) *ticket = 0;
+        }
         __syncthreads();
-        if (last) {
-            __threadfence();
+        if (last && room) {
             const int warp = tid >> 5, lane = tid & 31;
-            auto slot_of = [&](int c) { return 2 * (first + c) + (begin >= static_cast<int64_t>(first + c) * share ? 1 : 0); };
-            for (int i = 0; i < a.n; ++i) {
-                // every warp takes each fourth part; the maximum of all first
+            auto slot_of = [&](int c) { return 2 * (a.first_block + c) + (c == 0 ? 1 : 0); };
+            // one query: every warp takes each fourth part; more: a warp takes a query
+            const int step = a.n == 1 ? kWarps : 1;
+            for (int i = a.n == 1 ? 0 : warp; i < a.n; i += kWarps) {
+                // the maximum of all parts first
                 float top = kNone;
                 for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(p.ml + (slot_of(c) * Tq + i) * 2));
 #pragma unroll
                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const float base = finite_or_0(top);
                 float y[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-                for (int c0 = warp; c0 < n; c0 += 32 * kWarps) {
-                    const int mine = c0 + kWarps * lane;
+                for (int c0 = a.n == 1 ? warp : 0; c0 < n; c0 += 32 * step) {
+                    const int mine = c0 + step * lane;
                     float f = 0.f;
                     if (mine < n) {
                         const float2 s = __ldcg(reinterpret_cast<const float2*>(p.ml + (slot_of(mine) * Tq + i) * 2));
                         f = exp2f(s.x - base);
                         l = fmaf(f, s.y, l);
                     }
-                    const int here = min(32, (n - c0 + kWarps - 1) / kWarps);
+                    const int here = min(32, (n - c0 + step - 1) / step);
 #pragma unroll 4
                     for (int z = 0; z < here; ++z) {
                         const float w = __shfl_sync(0xffffffffu, f, z);
-                        const float* src = p.part + (static_cast<int64_t>(slot_of(c0 + kWarps * z)) * Tq + i) * p.Dp;
+                        const float* src = p.part + (static_cast<int64_t>(slot_of(c0 + step * z)) * Tq + i) * p.Dp;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (32 * k + lane < D) y[k] = fmaf(w, __ldcg(src + 32 * k + lane), y[k]);
@@ -692,55 +859,88 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
                 }
 #pragma unroll
                 for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-                __syncthreads();
+                if (a.n == 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (32 * k + lane < D) buf[warp * p.Dp + 32 * k + lane] = y[k];
+                    if (lane == 0) bml[warp] = l;
+                    __syncthreads();
+                    l = bml[0] + bml[1] + bml[2] + bml[3];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (32 * k + lane < D)
+                            y[k] = buf[32 * k + lane] + buf[p.Dp + 32 * k + lane] + buf[2 * p.Dp + 32 * k + lane] + buf[3 * p.Dp + 32 * k + lane];
+                    if (warp) break;
+                }
+                bool finite = isfinite(l);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (32 * k + lane < D) buf[warp * p.Dp + 32 * k + lane] = y[k];
-                if (lane == 0) bml[warp] = l;
-                __syncthreads();
-                const float total = bml[0] + bml[1] + bml[2] + bml[3];
-                for (int d = tid; d < D; d += kThreads) {
-                    const float v = buf[d] + buf[p.Dp + d] + buf[2 * p.Dp + d] + buf[3 * p.Dp + d];
-                    out_row<T>(p, a, i)[d] = from_f<T>(total == 0.f ? 0.f : v / total);
-                    if (!isfinite(v) || !isfinite(total)) atomicOr(&again, 1 << i);
-                }
-                if (W && tid == 0) p.lse[(static_cast<int64_t>(a.b) * m.H + a.h) * Tq + i] = base + log2f(total);
+                    if (32 * k + lane < D) {
+                        out_row<T>(p, a, i)[32 * k + lane] = from_f<T>(l == 0.f ? 0.f : y[k] / l);
+                        finite = finite && isfinite(y[k]);
+                    }
+                if (!finite) atomicOr(&again, 1 << i);
+                if (W && lane == 0) p.lse[(static_cast<int64_t>(a.b) * m.H + a.h) * Tq + i] = base + log2f(l);
             }
         }
     }
     __syncthreads();
-    for (int bits = again; bits; bits &= bits - 1) row_again<T>(p, a, __ffs(bits) - 1, buf);
+    for (int bits = again; bits; bits &= bits - 1) row_again<T>(p, a, __ffs(bits) - 1, !ONE, buf);
     __syncthreads();
 }
 
-// Blocks of the attention that an SM holds: what the registers of the variants leave room for.
-template <typename T, int NC, int NQ> constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 ? (NC <= 2 ? 4 : 3) : 2) : NC <= 2 && NQ == 1 ? 4 : NC == 1 ? 3 : 2;
+// Blocks of the attention that an SM holds: what registers (bf16: the rings) of the variants leave room for.
+template <typename T, int NC, int NQ> constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 ? (NC <= 2 ? 4 : 3) : 2) : NC <= 2 && NQ <= 2 ? 4 : NC <= 2 ? 3 : 2;
 
-// Shared memory: the pairs' first tiles [B + 1] (64 bits), then the warps' sums.
-template <typename T, int NC, int NQ, bool W>
+// Floats between the warps' sums in shared memory (bf16: in their rings).
+template <typename T, int NC>
+__host__ __device__ __forceinline__ int warp_floats(int queries, int Dp) { return sizeof(T) == 4 ? queries * Dp : kWarpBytes<NC> / 4; }
+
+// Floats of a new key's values (ONE) and the queries.
+template <typename T, int NC, int NQ, bool ONE>
+__host__ __device__ __forceinline__ int beside_floats(int Dp)
+{
+    return sizeof(T) == 4 ? NQ * Dp : (ONE ? Dp : 0) + kQRows<NC, NQ, ONE> * kQPitch<NC> / 2;
+}
+
+// Length and position of the first query of sequence b, for a call that needed no preparation (ONE).
+__device__ __forceinline__ int4 now_of(const PagedAttnParams& p, int b)
+{
+    const PagedParams& m = p.n.m;
+    const int len = m.length[b], next = m.next_pos[b], n = paged_count(p.n.counts, b, 1);
+    const bool ok = len >= 0 && len <= p.cap;
+    if (!ok && n > 0) page_error(m);
+    return make_int4(len, p.n.xk ? next : next - n, ok ? n : 0, 0);
+}
+
+// Shared memory: the warps' rings or sums; a new key's values; queries; maxima and weights; where the
+// sequences' pairs begin [B + 1] (64 bits, padded to an even number); what the sequences' entries of p.now are [B].
+template <typename T, int NC, int NQ, bool ONE, bool W>
 __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
 {
-    extern __shared__ __align__(16) int64_t start[];
+    extern __shared__ __align__(16) float buf[];
     __shared__ int64_t scan[kWarps];
     const PagedParams& m = p.n.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_start = (m.B + 2) & ~1;                        // keeps what follows 16-byte aligned
-    float* buf = reinterpret_cast<float*>(start + n_start);
-    float* bml = buf + kWarps * p.n.T * p.Dp;
-    float* qs = bml + kWarps * p.n.T * 2;
+    const int pitch = warp_floats<T, NC>(p.n.T, p.Dp);
+    float* beside = buf + kWarps * pitch;
+    float* bml = beside + beside_floats<T, NC, NQ, ONE>(p.Dp);
+    int64_t* start = reinterpret_cast<int64_t*>(bml + ((kWarps + 1) * p.n.T * 2 + 3) / 4 * 4);
+    int4* info = reinterpret_cast<int4*>(start + m.B + 2 - m.B % 2);
+    // (no early launch of the next grid: blocks of the weights' kernel that wait would take the place of later blocks)
     pdl_wait();
-    pdl_launch_dependents();
 
-    // start[b]: tiles of all pairs of the sequences before b
+    // start[b]: the work of all pairs of the sequences before b (an empty memory counts as a tile)
     int64_t done = 0;
     for (int b0 = 0; b0 < m.B; b0 += kThreads) {
         const int b = b0 + tid;
         int64_t x = 0;
         if (b < m.B) {
-            const int4 now = p.now[b];
-            x = now.z > 0 ? static_cast<int64_t>((now.x + kPageUnit - 1) / kPageUnit) * m.H : 0;
-            // this call's positions count from now on (nothing below reads the memory's own numbers)
-            if (blockIdx.x == 0 && p.n.xk && now.z > 0) {
+            const int4 now = ONE ? now_of(p, b) : p.now[b];
+            x = now.z > 0 ? static_cast<int64_t>(kHead + max(1, (now.x + kPageUnit - 1) / kPageUnit)) * m.H : 0;
+            info[b] = now;
+            // prepared: the new positions count from now on (nothing here reads the memory's own numbers)
+            if (!ONE && blockIdx.x == 0 && p.n.xk && now.z > 0) {
                 m.length[b] = now.x;
                 m.next_pos[b] = now.y + now.z;
             }
@@ -761,98 +961,153 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
     }
     if (tid == 0) start[m.B] = done;
     __syncthreads();
-    const int share = static_cast<int>(max(static_cast<int64_t>(kMinTiles), (done + gridDim.x - 1) / gridDim.x));
-    // queries of an empty memory: nothing to see
-    for (int b = blockIdx.x; b < m.B; b += gridDim.x) {
-        const int4 now = p.now[b];
-        if (now.z > 0 && now.x == 0)
-            for (int x = tid; x < now.z * m.H * m.D; x += kThreads) {
-                const int i = x / (m.H * m.D), h = x / m.D % m.H, d = x % m.D;
-                static_cast<T*>(p.out)[b * p.o_sb + i * p.o_st + h * p.o_sh + d] = from_f<T>(0.f);
+    // ONE: the last block that has read the lengths advances them (warp 1, while its first copies are under way)
+    bool arrived = !ONE || !(p.n.xk || W);
+    auto advance = [&] {
+        if (arrived || warp != 1) return;
+        arrived = true;
+        int last = 0;
+        if (lane == 0) {
+            last = arrive(m.scratch + m.B) == static_cast<int>(gridDim.x) - 1;
+            if (last) m.scratch[m.B] = 0;
+        }
+        if (!__shfl_sync(0xffffffffu, last, 0)) return;
+        for (int b = lane; b < m.B; b += 32) {
+            int4 now = info[b];
+            if (p.n.xk && now.z > 0) {
+                if (page_of(m, b, now.x) < 0) {
+                    now.z = 0;
+                } else {
+                    m.length[b] = ++now.x;
+                    m.next_pos[b] = now.y + 1;
+                }
             }
-    }
+            if (W) p.now[b] = now;
+        }
+    };
+    const int share = max(kMinTiles, quotient(done + gridDim.x - 1, gridDim.x));
     int64_t at = static_cast<int64_t>(blockIdx.x) * share;
     const int64_t end = min(done, at + share);
-    if (at >= end) return;
-    int lo = 0, hi = m.B;                                      // start[lo] <= at < start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (start[mid] <= at) lo = mid; else hi = mid;
+    if (at >= end) {
+        advance();
+        return;
     }
-    int b = lo;
+    int b = 0, hi = m.B;                                       // start[b] <= at < start[hi]
+    while (hi - b > 1) {
+        const int mid = (b + hi) / 2;
+        if (start[mid] <= at) b = mid; else hi = mid;
+    }
     while (at < end) {
         while (start[b + 1] <= at) ++b;
-        const int4 now = p.now[b];
         Part a;
         a.b = b;
-        a.len = now.x;
-        a.first = now.y;
-        a.n = now.z;
-        a.tiles = (now.x + kPageUnit - 1) / kPageUnit;
-        const int64_t x = at - start[b];
-        a.h = static_cast<int>(x / a.tiles);
-        a.t0 = static_cast<int>(x - static_cast<int64_t>(a.h) * a.tiles);
-        a.t1 = static_cast<int>(min(static_cast<int64_t>(a.tiles), a.t0 + (end - at)));
-        if constexpr (sizeof(T) == 4) part_f32<NC, NQ, W>(p, a, buf, bml, qs);
-        else part_bf16<NC, NQ, W>(p, a, buf, bml);
-        join<T, W>(p, a, buf, bml, share, start[b] + static_cast<int64_t>(a.h) * a.tiles);
-        at += a.t1 - a.t0;
+        a.len = info[b].x;
+        a.first = info[b].y;
+        a.n = info[b].z;
+        a.own = ONE && p.n.xk;
+        a.room = !a.own || page_of(m, b, a.len) >= 0;
+        a.tiles = max(1, (a.len + kPageUnit - 1) / kPageUnit);
+        const int size = kHead + a.tiles;
+        a.h = quotient(at - start[b], size);
+        const int64_t begin = start[b] + static_cast<int64_t>(a.h) * size;
+        // the pair's tiles lie at begin + kHead on; a whole pair belongs to the block in whose share it begins
+        if (a.tiles <= kWholeTiles) {
+            a.t0 = begin >= at ? 0 : a.tiles;
+            a.t1 = a.tiles;
+            a.parts = 1;
+        } else {
+            a.t0 = static_cast<int>(max(at - begin - kHead, static_cast<int64_t>(0)));
+            a.t1 = static_cast<int>(min(end - begin - kHead, static_cast<int64_t>(a.tiles)));
+            a.first_block = quotient(begin + kHead, share);
+            a.parts = quotient(begin + size - 1, share) - a.first_block + 1;
+        }
+        at = min(end, begin + size);
+        if (a.t0 >= a.t1) continue;
+        if constexpr (sizeof(T) == 4) part_f32<NC, NQ, W>(p, a, buf, pitch, bml, beside);
+        else part_bf16<NC, NQ, ONE, W>(p, a, reinterpret_cast<char*>(buf + warp * pitch), bml, beside,
+                                       reinterpret_cast<uint16_t*>(beside + (ONE ? p.Dp : 0)), advance);
+        join<T, ONE, W>(p, a, buf, pitch, beside, bml);
     }
+    advance();
 }
 
 // ---------------------------------------------------------------- attention weights
-__global__ void __launch_bounds__(kThreads) paged_weight_kernel(const __grid_constant__ PagedAttnParams p)
+// A block takes 32 slots of a sequence, its warps every eighth (head, query) row of scores; the sums meet in a fixed order.
+constexpr int kWeightThreads = 256, kWeightWarps = kWeightThreads / 32;
+
+__global__ void __launch_bounds__(kWeightThreads) paged_weight_kernel(const __grid_constant__ PagedAttnParams p)
 {
+    __shared__ float sums[kWeightWarps][32];
     pdl_wait();
     pdl_launch_dependents();
     const PagedParams& m = p.n.m;
-    const int b = blockIdx.y, s = blockIdx.x * kThreads + threadIdx.x;
+    const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 now = p.now[b];
-    if (s >= now.x || now.z == 0) return;
-    const int page = page_of(m, b, s);
-    if (page < 0) return;
-    float sum = 0.f;
-    for (int h = 0; h < m.H; ++h) {
-        const int64_t row = (static_cast<int64_t>(b) * m.H + h) * p.n.T;
-        for (int i = 0; i < now.z; ++i) {
-            const float x = p.S[(row + i) * p.cap + s];
-            if (x != kNone) sum += exp2f(x - p.lse[row + i]);
+    if (now.z == 0) return;
+    const int rows = m.H * now.z;
+    for (int s0 = blockIdx.x * 32; s0 < now.x; s0 += gridDim.x * 32) {
+        const int s = s0 + lane;
+        float sum = 0.f;
+        if (s < now.x) {
+#pragma unroll 8
+            for (int x = warp; x < rows; x += kWeightWarps) {
+                const int64_t row = (static_cast<int64_t>(b) * m.H + x / now.z) * p.n.T + x % now.z;
+                const float y = p.S[row * p.cap + s], l = p.lse[row];
+                sum += y == kNone ? 0.f : exp2f(y - l);
+            }
         }
+        sums[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && s < now.x) {
+            const int page = page_of(m, b, s);
+#pragma unroll
+            for (int w = 1; w < kWeightWarps; ++w) sum += sums[w][lane];
+            if (page >= 0) m.weight[static_cast<int64_t>(page) * m.page_len + s % m.page_len] += sum;
+        }
+        __syncthreads();
     }
-    m.weight[static_cast<int64_t>(page) * m.page_len + s % m.page_len] += sum;
 }
 
-size_t attn_smem(const PagedAttnParams& p, int f32_queries)
-{
-    return static_cast<size_t>((p.n.m.B + 2) & ~1) * 8 +
-           static_cast<size_t>(kWarps) * p.n.T * (p.Dp + 2) * 4 + static_cast<size_t>(f32_queries) * p.Dp * 4;
-}
-
-template <typename T, int NC, int NQ>
+template <typename T, int NC, int NQ, bool ONE>
 cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
     static OncePerDevice once;
     const PagedParams& m = p.n.m;
-    const size_t smem = attn_smem(p, sizeof(T) == 4 ? NQ : 0);
-    cudaError_t e = allow_smem(once, 120 * 1024, paged_attn_kernel<T, NC, NQ, false>, paged_attn_kernel<T, NC, NQ, true>);
+    const size_t smem = 4 * (static_cast<size_t>(kWarps) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
+                             static_cast<size_t>(kWarps + 1) * 2 * p.n.T + 2) + 8 * (3 * static_cast<size_t>(m.B) + 2);
+    cudaError_t e = allow_smem(once, 200 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
     if (e != cudaSuccess) return e;
-    const int64_t terms = static_cast<int64_t>((p.n_e + kPrepRows - 1) / kPrepRows) * m.H * ((static_cast<int64_t>(m.B) * p.n.T + 7) / 8);
-    if (terms + m.B > INT32_MAX) return cudaErrorInvalidConfiguration;
-    e = launch_dependent(paged_prep_kernel<T, NC>, dim3(static_cast<unsigned>(m.B + terms)), dim3(kThreads), 0, s, p);
+    if (!ONE) {
+        // a block copies a few hundred units of 16 bytes
+        const int units = 2 * m.H * (m.ld * static_cast<int>(sizeof(T)) / 16), share = max(1, 512 / units);
+        const int copies = p.n.xk ? (p.n.T + share - 1) / share : 1;
+        const int64_t terms = static_cast<int64_t>((p.n_e + kPrepRows - 1) / kPrepRows) * m.H * ((static_cast<int64_t>(m.B) * p.n.T + 7) / 8);
+        if (terms + m.B * copies > INT32_MAX) return cudaErrorInvalidConfiguration;
+        e = launch_dependent(paged_prep_kernel<T, NC>, dim3(static_cast<unsigned>(m.B * copies + terms)), dim3(kThreads), 0, s, p,
+                             copies, share);
+        if (e != cudaSuccess) return e;
+    }
+    // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its static part besides
+    const int per_sm = max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (smem + 1024 + 64))));
+    const int blocks = min(per_sm * sm_count, kPagedMaxCtas);
+    if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, false>, dim3(blocks), dim3(kThreads), smem, s, p);
+    e = launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, true>, dim3(blocks), dim3(kThreads), smem, s, p);
     if (e != cudaSuccess) return e;
-    const int blocks = min(kBlocks<T, NC, NQ> * sm_count, kPagedMaxCtas);
-    if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, false>, dim3(blocks), dim3(kThreads), smem, s, p);
-    e = launch_dependent(paged_attn_kernel<T, NC, NQ, true>, dim3(blocks), dim3(kThreads), smem, s, p);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(paged_weight_kernel, dim3((p.cap + kThreads - 1) / kThreads, m.B), dim3(kThreads), 0, s, p);
+    const int slots = max(1, min((p.cap + 31) / 32, 16 * sm_count / m.B));
+    return launch_dependent(paged_weight_kernel, dim3(slots, m.B), dim3(kWeightThreads), 0, s, p);
 }
 
 template <typename T, int NC>
 cudaError_t by_queries(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
-    // bf16: groups of eight queries; fp32: queries whose sums fit the registers
-    if constexpr (sizeof(T) == 4) return p.n.T == 1 ? launch<T, NC, 1>(p, sm_count, s) : launch<T, NC, NC <= 2 ? 4 : 2>(p, sm_count, s);
-    else return p.n.T <= 8 ? launch<T, NC, 1>(p, sm_count, s) : launch<T, NC, 2>(p, sm_count, s);
+    // fp32: queries whose sums fit the registers; bf16: groups of four queries
+    if constexpr (sizeof(T) == 4) {
+        return p.n.T == 1 ? launch<T, NC, 1, false>(p, sm_count, s) : launch<T, NC, NC <= 2 ? 4 : 2, false>(p, sm_count, s);
+    } else {
+        if (p.n.T == 1) return launch<T, NC, 1, true>(p, sm_count, s);
+        if (p.n.T <= 4) return launch<T, NC, 1, false>(p, sm_count, s);
+        return p.n.T <= 8 ? launch<T, NC, 2, false>(p, sm_count, s) : launch<T, NC, 4, false>(p, sm_count, s);
+    }
 }
 
 template <typename T>

@@ -57,7 +57,7 @@ class TxlQmem(ctypes.Structure):
 
 
 class TxlPaged(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "pos", "weight", "table", "length", "next_pos", "arrivals",
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "pos", "weight", "table", "length", "next_pos", "scratch",
                                                "err_flag")] + \
                [(n, ctypes.c_int) for n in ("B", "H", "D", "ld", "n_pages", "page_len", "max_pages", "dtype")]
 
