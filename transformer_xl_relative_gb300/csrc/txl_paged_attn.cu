@@ -257,28 +257,40 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 template <int NC> struct BFrag { uint32_t w[2 * NC][2]; };
 
 // The part's queries in shared memory as the columns of B want them, by the whole block: row 2 i the upper 8 bits of (q_i + u)
-// scale, row 2 i + 1 the next 8; with ONE two more rows for v.  Rows of kQPitch bf16 (in different banks), zeros past D
-// and from query n on.
+// scale, row 2 i + 1 the next 8; with ONE rows 8 and 9 are for v, and the other rows stay zero.  Rows of kQPitch
+// bf16 (in different banks), zeros past D and from query n on.
 template <int NC> constexpr int kQPitch = 32 * NC + 8;
 template <int NC, int NQ, bool ONE> constexpr int kQRows = ONE ? 16 : 8 * NQ;
 
-template <int NC, int NQ, bool ONE>
-__device__ __forceinline__ void put_queries(const PagedAttnParams& p, const Part& a, uint16_t* qs)
-{
-    const PagedParams& m = p.n.m;
-    constexpr int kWidth = 32 * NC;
-    for (int x = threadIdx.x; x < kQRows<NC, NQ, ONE> / 2 * kWidth; x += kThreads) {
-        const int row = x / kWidth, d = x % kWidth, i = ONE ? row & 3 : row;
-        float y = 0.f;
-        if (i < a.n && d < m.D) {
-            const float* bias = (ONE && row >= 4 ? p.vb : p.u) + a.h * m.D;
-            y = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d]) + bias[d]) * p.qscale;
+// The elements that a thread puts there: loaded before anything that waits, stored later.
+template <int NC, int NQ, bool ONE> struct Queries {
+    static constexpr int kWidth = 32 * NC, kRows = ONE ? 2 : 4 * NQ, kEach = (kRows * kWidth + kThreads - 1) / kThreads;
+    float y[kEach];
+
+    __device__ __forceinline__ void load(const PagedAttnParams& p, const Part& a)
+    {
+        const PagedParams& m = p.n.m;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int x = threadIdx.x + e * kThreads, row = x / kWidth, d = x % kWidth, i = ONE ? 0 : row;
+            y[e] = 0.f;
+            if (row < kRows && i < a.n && d < m.D)
+                y[e] = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d]) +
+                        (ONE && row ? p.vb : p.u)[a.h * m.D + d]) * p.qscale;
         }
-        const __nv_bfloat16 hi = __float2bfloat16_rn(y);
-        qs[2 * row * kQPitch<NC> + d] = __bfloat16_as_ushort(hi);
-        qs[(2 * row + 1) * kQPitch<NC> + d] = __bfloat16_as_ushort(__float2bfloat16_rn(y - __bfloat162float(hi)));
     }
-}
+    __device__ __forceinline__ void store(uint16_t* qs) const
+    {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int x = threadIdx.x + e * kThreads, row = ONE ? x / kWidth * 8 : x / kWidth * 2, d = x % kWidth;
+            if (x >= kRows * kWidth) continue;
+            const __nv_bfloat16 hi = __float2bfloat16_rn(y[e]);
+            qs[row * kQPitch<NC> + d] = __bfloat16_as_ushort(hi);
+            qs[(row + 1) * kQPitch<NC> + d] = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] - __bfloat162float(hi)));
+        }
+    }
+};
 
 // ROWS: in the order of the units of r's rows.
 template <int NC, bool ROWS>
@@ -294,60 +306,68 @@ __device__ __forceinline__ void load_b(BFrag<NC>& f, const uint16_t* row, int t)
 }
 
 // ONE: a pair's new key, by one warp: its score, its values as a part of one key, and its row into the page (which the
-// sequence may lack: then nothing is written).
-template <bool W>
-__device__ __forceinline__ void own_key(const PagedAttnParams& p, const Part& a, float* buf, float* bml)
-{
-    const PagedParams& m = p.n.m;
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + a.b * p.q_sb + a.h * p.q_sh;
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
-    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.r) + a.h * p.r_head;
-    const int page = page_of(m, a.b, a.len), row = a.len % m.page_len;
-    __nv_bfloat16 *kd = nullptr, *vd = nullptr;
-    if (page >= 0) {
-        const int64_t at = page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld;
-        kd = static_cast<__nv_bfloat16*>(m.k) + at;
-        vd = static_cast<__nv_bfloat16*>(m.v) + at;
-    }
-    const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
-    float s = 0.f;
-    for (int d = lane; d < m.ld; d += 32) {
-        const bool in = d < m.D;
-        const __nv_bfloat16 kk = in ? k[d] : zero, vv = in ? v[d] : zero;
-        if (in) {
-            const float x = __bfloat162float(q[d]);
-            s = fmaf((x + p.u[a.h * m.D + d]) * p.qscale, __bfloat162float(kk), s);
-            s = fmaf((x + p.vb[a.h * m.D + d]) * p.qscale, __bfloat162float(r[d]), s);
-            buf[d] = __bfloat162float(vv);
-        }
-        if (page >= 0) {
-            kd[d] = kk;
-            vd[d] = vv;
-        }
-    }
+// sequence may lack: then nothing is written).  Loaded before anything that waits, worked on later.
+template <int NC, bool W> struct OwnKey {
+    float s, k[NC], v[NC];
+    int page;
+
+    __device__ __forceinline__ void load(const PagedAttnParams& p, const Part& a, int lane)
+    {
+        const PagedParams& m = p.n.m;
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + a.b * p.q_sb + a.h * p.q_sh;
+        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
+        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
+        const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.r) + a.h * p.r_head;
+        page = page_of(m, a.b, a.len);
+        s = 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) {
+        for (int j = 0; j < NC; ++j) {
+            const int d = lane + 32 * j;
+            k[j] = v[j] = 0.f;
+            if (d < m.D) {
+                const float x = __bfloat162float(qr[d]);
+                k[j] = __bfloat162float(kr[d]);
+                v[j] = __bfloat162float(vr[d]);
+                s = fmaf((x + p.u[a.h * m.D + d]) * p.qscale, k[j], s);
+                s = fmaf((x + p.vb[a.h * m.D + d]) * p.qscale, __bfloat162float(r[d]), s);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const PagedAttnParams& p, const Part& a, int lane, float* values, float* bml)
+    {
+        const PagedParams& m = p.n.m;
+        const int row = a.len % m.page_len;
+        const int64_t at = page >= 0 ? page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld : 0;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int d = lane + 32 * j;
+            if (d < m.D) values[d] = v[j];
+            if (page >= 0 && d < m.ld) {
+                static_cast<__nv_bfloat16*>(m.k)[at + d] = __float2bfloat16_rn(k[j]);
+                static_cast<__nv_bfloat16*>(m.v)[at + d] = __float2bfloat16_rn(v[j]);
+            }
+        }
+        for (int d = lane + 32 * NC; page >= 0 && d < m.ld; d += 32)
+            static_cast<uint16_t*>(m.k)[at + d] = static_cast<uint16_t*>(m.v)[at + d] = 0;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (lane) return;
         bml[0] = s;
         bml[1] = s != s ? s : s == kNone ? 0.f : 1.f;
-        if (page >= 0) {
-            if (W) p.S[(static_cast<int64_t>(a.b) * m.H + a.h) * p.cap + a.len] = s;
-            if (a.h == 0) {
-                m.pos[static_cast<int64_t>(page) * m.page_len + row] = a.first;
-                m.weight[static_cast<int64_t>(page) * m.page_len + row] = 0.f;
-            }
-        } else {
+        if (page < 0) {
             page_error(m);
+            return;
+        }
+        if (W) p.S[(static_cast<int64_t>(a.b) * m.H + a.h) * p.cap + a.len] = s;
+        if (a.h == 0) {
+            m.pos[static_cast<int64_t>(page) * m.page_len + row] = a.first;
+            m.weight[static_cast<int64_t>(page) * m.page_len + row] = 0.f;
         }
     }
-}
+};
 
-// once(): called when the first copies are under way.
-template <int NC, int NQ, bool ONE, bool W, typename F>
-__device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& a, char* ring, float* bml, float* own, uint16_t* qs,
-                                          F&& once)
+template <int NC, int NQ, bool ONE, bool W>
+__device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& a, char* ring, float* bml, float* own, uint16_t* qs)
 {
     const PagedParams& m = p.n.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -374,6 +394,13 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
             copy16(dst + (kPageUnit + row) * kPitch<NC> + 16 * c, v + off, bytes);
         }
     };
+    // what hangs on nothing is loaded first, then the pages, then what they lead to
+    Queries<NC, NQ, ONE> queries;
+    queries.load(p, a);
+    OwnKey<NC, W> own_key;
+    const bool owner = ONE && a.own && a.t1 == a.tiles && warp == kWarps - 1;
+    if constexpr (ONE)
+        if (owner) own_key.load(p, a, lane);
     Pages pages;
     pages.look(m, a, a.t0 + warp, lane);
     if (units < kUnits) {
@@ -398,37 +425,20 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         for (int y = 0; y < 2; ++y) pos[y] = page >= 0 && tile * kPageUnit + 8 * y + g < a.len ? at[8 * y] : kAhead;
     };
     if (first < a.t1) load_pos(pages.get(m, a, first, lane), first);
-    put_queries<NC, NQ, ONE>(p, a, qs);
-    if (ONE && a.own && a.t1 == a.tiles && warp == kWarps - 1) own_key<W>(p, a, own, bml + 2 * kWarps);
-    once();
-    __syncthreads();
+    queries.store(qs);
+    if constexpr (ONE)
+        if (owner) own_key.store(p, a, lane, own, bml + 2 * kWarps);
 
-    BFrag<NC> q[NQ], qv;
-    const float* E[NQ];
-    float* S[NQ];
-    bool live[NQ];
-#pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        load_b<NC, false>(q[x], qs + (8 * x + g) * kQPitch<NC>, t);
-        live[x] = 4 * x + t < a.n;
-        const int64_t row = (static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1);
-        E[x] = ONE ? nullptr : p.E + row * p.e_pitch;
-        S[x] = W ? p.S + row * p.cap : nullptr;
-    }
-    if (ONE) load_b<NC, true>(qv, qs + (8 + g) * kQPitch<NC>, t);
-    float o[NQ][2 * NC][4];
-    float mx[NQ], sum[NQ];
-#pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        mx[x] = kNone;
-        sum[x] = 0.f;
-#pragma unroll
-        for (int z = 0; z < 2 * NC; ++z) o[x][z][0] = o[x][z][1] = o[x][z][2] = o[x][z][3] = 0.f;
-    }
     // what a tile's position terms come from, one tile ahead: which keys a lane's query sees, E's terms (e) or r's rows (rw)
     float e[NQ][2];
     uint4 rw[2][NC];
-    bool near = false;
+    const float* E[NQ];
+    bool live[NQ];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        live[x] = 4 * x + t < a.n;
+        E[x] = ONE ? nullptr : p.E + ((static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1)) * p.e_pitch;
+    }
     const uint16_t* r = static_cast<const uint16_t*>(p.r) + a.h * p.r_head;
     auto load_row = [&](int distance, uint4* w) {
         const uint16_t* row = r + static_cast<int64_t>(distance) * p.r_row;
@@ -445,13 +455,6 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
             }
         }
     };
-    auto rows_mma = [&](float* c) {
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            mma::mma16816(c, rw[0][j].x, rw[1][j].x, rw[0][j].y, rw[1][j].y, qv.w[2 * j][0], qv.w[2 * j][1]);
-            mma::mma16816(c, rw[0][j].z, rw[1][j].z, rw[0][j].w, rw[1][j].w, qv.w[2 * j + 1][0], qv.w[2 * j + 1][1]);
-        }
-    };
     auto load_terms = [&]() {
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
@@ -463,27 +466,32 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
                 else e[x][y] = seen ? E[x][term(p, at, pos[y])] : kNone;
             }
         if constexpr (ONE) {
-            const int d0 = pos[0] <= a.first ? term(p, a.first, pos[0]) : p.n_e - 1;
-            const int d1 = pos[1] <= a.first ? term(p, a.first, pos[1]) : p.n_e - 1;
-            near = __any_sync(0xffffffffu, d0 < p.n_e - 1 || d1 < p.n_e - 1);
-            if (near) {
-                load_row(d0, rw[0]);
-                load_row(d1, rw[1]);
-            }
+            load_row(term(p, a.first, min(pos[0], a.first)), rw[0]);
+            load_row(term(p, a.first, min(pos[1], a.first)), rw[1]);
         }
     };
-    float far = 0.f;                                           // ONE: the term of all distances from n_e - 1 on
-    if constexpr (ONE) {
-        load_row(p.n_e - 1, rw[0]);
-#pragma unroll
-        for (int j = 0; j < NC; ++j) rw[1][j] = rw[0][j];
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        rows_mma(c);
-        far = c[0] + c[1];
-    }
     if (first < a.t1) {
         load_terms();
         if (first + kWarps < a.t1) load_pos(pages.get(m, a, first + kWarps, lane), first + kWarps);
+    }
+    __syncthreads();
+
+    BFrag<NC> q[NQ], qv;
+    float* S[NQ];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        load_b<NC, false>(q[x], qs + (8 * x + g) * kQPitch<NC>, t);
+        S[x] = W ? p.S + ((static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1)) * p.cap : nullptr;
+    }
+    if (ONE) load_b<NC, true>(qv, qs + (8 + g) * kQPitch<NC>, t);
+    float o[NQ][2 * NC][4];
+    float mx[NQ], sum[NQ];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        mx[x] = kNone;
+        sum[x] = 0.f;
+#pragma unroll
+        for (int z = 0; z < 2 * NC; ++z) o[x][z][0] = o[x][z][1] = o[x][z][2] = o[x][z][3] = 0.f;
     }
     // ldmatrix addresses in a stage: K as [key][channel], V as [key][channel] transposed
     const uint32_t k_at = stage0 + (lane & 15) * kPitch<NC> + (lane >> 4) * 16;
@@ -510,8 +518,11 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
             for (int x = 0; x < NQ; ++x) mma::mma16816(c[x], w[0], w[1], w[2], w[3], q[x].w[j][0], q[x].w[j][1]);
         }
         if (ONE) {
-            if (near) rows_mma(c[0]);
-            else c[0][0] += far, c[0][2] += far;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                mma::mma16816(c[0], rw[0][j].x, rw[1][j].x, rw[0][j].y, rw[1][j].y, qv.w[2 * j][0], qv.w[2 * j][1]);
+                mma::mma16816(c[0], rw[0][j].z, rw[1][j].z, rw[0][j].w, rw[1][j].w, qv.w[2 * j + 1][0], qv.w[2 * j + 1][1]);
+            }
         }
         float s[NQ][2];
 #pragma unroll
@@ -961,17 +972,16 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
     }
     if (tid == 0) start[m.B] = done;
     __syncthreads();
-    // ONE: the last block that has read the lengths advances them (warp 1, while its first copies are under way)
-    bool arrived = !ONE || !(p.n.xk || W);
+    // ONE: the last block that has read the lengths advances them at its end (the ticket's answer is not waited for before)
+    const bool counts = ONE && (p.n.xk || W);
+    int ticket = -1;
+    if (counts && tid == kThreads - 1)
+        asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;" : "=r"(ticket) : "l"(m.scratch + m.B) : "memory");
     auto advance = [&] {
-        if (arrived || warp != 1) return;
-        arrived = true;
-        int last = 0;
-        if (lane == 0) {
-            last = arrive(m.scratch + m.B) == static_cast<int>(gridDim.x) - 1;
-            if (last) m.scratch[m.B] = 0;
-        }
-        if (!__shfl_sync(0xffffffffu, last, 0)) return;
+        if (!counts || warp != kWarps - 1) return;
+        const bool last = ticket == static_cast<int>(gridDim.x) - 1;
+        if (!__any_sync(0xffffffffu, last)) return;
+        if (last) m.scratch[m.B] = 0;
         for (int b = lane; b < m.B; b += 32) {
             int4 now = info[b];
             if (p.n.xk && now.z > 0) {
@@ -985,6 +995,12 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
             if (W) p.now[b] = now;
         }
     };
+    if constexpr (ONE) {
+        // (the rows of queries that one token does not have)
+        uint32_t* rows = reinterpret_cast<uint32_t*>(beside + p.Dp);
+        for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += kThreads) rows[x] = 0;
+    }
+    __syncthreads();
     const int share = max(kMinTiles, quotient(done + gridDim.x - 1, gridDim.x));
     int64_t at = static_cast<int64_t>(blockIdx.x) * share;
     const int64_t end = min(done, at + share);
@@ -1025,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
         if (a.t0 >= a.t1) continue;
         if constexpr (sizeof(T) == 4) part_f32<NC, NQ, W>(p, a, buf, pitch, bml, beside);
         else part_bf16<NC, NQ, ONE, W>(p, a, reinterpret_cast<char*>(buf + warp * pitch), bml, beside,
-                                       reinterpret_cast<uint16_t*>(beside + (ONE ? p.Dp : 0)), advance);
+                                       reinterpret_cast<uint16_t*>(beside + (ONE ? p.Dp : 0)));
         join<T, ONE, W>(p, a, buf, pitch, beside, bml);
     }
     advance();
