@@ -700,7 +700,7 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
  * Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
  *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
  *            may be NULL when that is 0).  Calls that share a workspace must not overlap on the GPU.
- * Limits: m >= 0 (0: nothing to do), m <= 2^20; ld_x >= k, ld_y >= n.  err_flag as txl_linear.
+ * Limits: m >= 0 (0: nothing to do), m <= 2^19; ld_x >= k, ld_y >= n.  err_flag as txl_linear.
  */
 txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, void* Y, int64_t ld_y, void* workspace,
                          size_t workspace_bytes, int* err_flag, void* stream);

@@ -127,7 +127,7 @@ def test_four_bit_weights(native):
     assert call(ldx=63) == native.TXL_ERR_INVALID_ARG and call(ldy=31) == native.TXL_ERR_INVALID_ARG
     assert call(w=native.TxlQ4(None, 64, 32, 64)) == native.TXL_ERR_INVALID_ARG
     assert call(w=native.TxlQ4(FAKE + 8, 64, 32, 64)) == native.TXL_ERR_ALIGNMENT
-    assert call(X=FAKE + 1) == native.TXL_ERR_ALIGNMENT and call(m=(1 << 20) + 1) == native.TXL_ERR_UNSUPPORTED
+    assert call(X=FAKE + 1) == native.TXL_ERR_ALIGNMENT and call(m=(1 << 19) + 1) == native.TXL_ERR_UNSUPPORTED
     assert lib.txl_linear_q4_workspace_size(64, ctypes.byref(w)) == 0
     need = lib.txl_linear_q4_workspace_size(65, ctypes.byref(w))
     assert need == 64 * 32 * 2

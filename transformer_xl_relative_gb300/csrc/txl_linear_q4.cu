@@ -16,20 +16,17 @@ namespace {
 // step, k = 32 (s / 2) + 8 t + 4 (s % 2) + 0..3, so that a lane's x are two pieces of 16 bytes and a step stays within 32 k.
 // Nibble j of a word and nibble j + 4 are a pair of A's register j: column g + 8 (j % 2), k + 2 (j / 2) and the next.
 constexpr int kQ4K = 64, kQ4N = 16;
-constexpr int kQ4Threads = 256, kQ4Warps = kQ4Threads / 32;
+constexpr int kExpandThreads = 256;
 
-__device__ __forceinline__ uint4 load_codes(const uint4* p)
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 {
-    uint4 w;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
-    return w;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Eight bf16 of a row of x from channel k on; 0 at and past k_end.
-__device__ __forceinline__ uint4 load_x8(const uint16_t* row, int k, int k_end, bool vec)
+// Eight bf16 of a row of x from channel k on, from any address; 0 at and past k_end.
+__device__ __forceinline__ uint4 load_x8(const uint16_t* row, int k, int k_end)
 {
-    if (vec && k + 8 <= k_end) return *reinterpret_cast<const uint4*>(row + k);
     uint32_t e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = k + i < k_end ? row[k + i] : 0u;
@@ -39,53 +36,91 @@ __device__ __forceinline__ uint4 load_x8(const uint16_t* row, int k, int k_end, 
 // 128 + c as bf16 pairs: a code is the low bits of the mantissa.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u; }
 
-// A block of threads computes 16 NT columns of Y for 8 MT rows, its warps each eighth block of k.
+// D = A B without an accumulator to add to.
+__device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// A stage of a warp's ring in shared memory: codes of NT tiles of columns for one block of k, x of 8 MT rows (each lane copies
+// and reads its own 16 bytes of both), and the tiles' parameters.
+constexpr int kQ4Stages = 4, kQ4MaxWarps = 16;
+template <int NT, int MT, int SUB> struct Q4Stage {
+    uint4 w[NT][32], x[MT][2][32];
+    uint32_t par[NT][SUB][16];
+};
+template <int NT, int MT, int SUB> constexpr int kQ4Ring = kQ4Stages * static_cast<int>(sizeof(Q4Stage<NT, MT, SUB>));
+
+// A block of threads computes 16 NT columns of Y for 8 MT rows: its warps take turns over the blocks of k, three ahead, and
+// their sums meet in shared memory.
 // The products see 128 + c; what that adds, 128 step sum x, leaves with the minimum: lo - 128 step times sum x, which an mma
 // with a matrix of ones gives in the same lanes.  Both cost 2^-24 of 128 step sum |x| (2^-16 of a step for each x).
-template <int NT, int MT, int SUB>
-__global__ void __launch_bounds__(kQ4Threads, MT == 1 && NT == 1 ? 4 : 2) linear_q4_kernel(const __grid_constant__ LinearQ4Params p)
+// VEC: rows of x start on 16-byte boundaries.
+template <int NT, int MT, int SUB, bool VEC>
+__global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __grid_constant__ LinearQ4Params p)
 {
-    __shared__ float red[kQ4Warps][16 * NT][8 * MT + 1];
+    using Stage = Q4Stage<NT, MT, SUB>;
+    extern __shared__ __align__(16) char smem[];
+    constexpr int kOut = 16 * NT * 8 * MT;
+    static_assert((kOut + 16 * NT) * 4 <= kQ4Ring<NT, MT, SUB>, "the sums take the rings' place");
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, g = lane >> 2, t = lane & 3;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
     const int nt_all = (p.n + kQ4N - 1) / kQ4N, nt0 = blockIdx.x * NT;
+    const int shift = p.group == 128 ? 1 : 0;
     const int row0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.m - row0);
+    Stage* ring = reinterpret_cast<Stage*>(smem) + warp * kQ4Stages;
     const uint16_t* x[MT];
-    bool live[MT];
+    int live[MT];                                              // bytes of a copy: none for a row that is not there
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
-        live[a] = 8 * a + g < rows;
-        x[a] = static_cast<const uint16_t*>(p.x) + (row0 + (live[a] ? 8 * a + g : 0)) * p.ld_x;
+        x[a] = static_cast<const uint16_t*>(p.x) + (row0 + min(8 * a + g, rows - 1)) * p.ld_x + 8 * t;
+        live[a] = 8 * a + g < rows ? 16 : 0;
     }
-    float tot[NT][MT][4] = {};
-    constexpr uint32_t kOnes = 0x3f803f80u;
-#pragma unroll 2
-    for (int kb = warp; kb < kb_all; kb += kQ4Warps) {
-        uint4 w[NT], xv[MT][2];
-        uint32_t par[NT][SUB][2];
+    // what a lane copies: its codes of every tile, its x, and (the first 4 NT SUB lanes) 16 bytes of one tile's parameters
+    const uint4* codes[NT];
 #pragma unroll
-        for (int b = 0; b < NT; ++b) {
-            const int nt = min(nt0 + b, nt_all - 1);
-            w[b] = load_codes(p.codes + (static_cast<int64_t>(nt) * kb_all + kb) * 32 + lane);
+    for (int b = 0; b < NT; ++b) codes[b] = p.codes + static_cast<int64_t>(min(nt0 + b, nt_all - 1)) * kb_all * 32 + lane;
+    const int par_tile = lane / (4 * SUB), par_sub = lane / 4 % SUB;
+    const uint32_t* par = p.par + static_cast<int64_t>(min(nt0 + par_tile, nt_all - 1)) * groups * 16 + 4 * t;
+    const uint32_t at = smem_u32(ring) + 16 * lane, par_at = smem_u32(&ring[0].par[0][0][0]) + 16 * lane;
+    auto load = [&](int kb, int stage) {
+        const uint32_t dst = at + stage * static_cast<int>(sizeof(Stage));
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-                const int gr = min((kb * kQ4K + s * (kQ4K / SUB)) / p.group, groups - 1);
-                const uint32_t* q = p.par + (static_cast<int64_t>(nt) * groups + gr) * 16 + g;
-                par[b][s][0] = q[0];
-                par[b][s][1] = q[8];
-            }
-        }
+        for (int b = 0; b < NT; ++b) copy16(dst + 512 * b, codes[b] + kb * 32, 16);
+        const int k = kb * kQ4K;
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                xv[a][h] = live[a] ? load_x8(x[a], kb * kQ4K + 32 * h + 8 * t, p.k, p.vec_x) : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t to = dst + 512 * (NT + 2 * a + h);
+                if (VEC && k + kQ4K <= p.k) {
+                    copy16(to, x[a] + k + 32 * h, live[a]);
+                } else if (VEC) {
+                    const int bytes = max(0, min(live[a], 2 * (p.k - (k + 32 * h + 8 * t))));
+                    copy16(to, bytes ? x[a] + k + 32 * h : x[a] - 8 * t, bytes);
+                } else {
+                    ring[stage].x[a][h][lane] = load_x8(x[a], k + 32 * h, p.k - 8 * t);
+                }
+            }
+        if (par_tile < NT)
+            copy16(par_at + stage * static_cast<int>(sizeof(Stage)), par + (SUB == 2 ? min(2 * kb + par_sub, groups - 1) : kb >> shift) * 16, 16);
+    };
+    float tot[NT][MT][4] = {};
+    constexpr uint32_t kOnes = 0x3f803f80u;
+    auto multiply = [&](const Stage& q) {
+        uint4 wv[NT], xv[MT][2];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) wv[b] = q.w[b][lane];
+#pragma unroll
+        for (int a = 0; a < MT; ++a) xv[a][0] = q.x[a][0][lane], xv[a][1] = q.x[a][1][lane];
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
-            float xs[MT][4] = {};
-            float c[NT][MT][4] = {};
+            float xs[MT][4], c[NT][MT][4];
 #pragma unroll
             for (int i = 0; i < 4 / SUB; ++i) {
                 const int step = s * (4 / SUB) + i;
@@ -95,21 +130,26 @@ __global__ void __launch_bounds__(kQ4Threads, MT == 1 && NT == 1 ? 4 : 2) linear
                     const uint4 v = xv[a][step >> 1];
                     b0[a] = step & 1 ? v.z : v.x;
                     b1[a] = step & 1 ? v.w : v.y;
-                    mma::mma16816(xs[a], kOnes, kOnes, kOnes, kOnes, b0[a], b1[a]);
+                    if (i == 0) mma_first(xs[a], kOnes, kOnes, kOnes, kOnes, b0[a], b1[a]);
+                    else mma::mma16816(xs[a], kOnes, kOnes, kOnes, kOnes, b0[a], b1[a]);
                 }
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
-                    const uint32_t q = step == 0 ? w[b].x : step == 1 ? w[b].y : step == 2 ? w[b].z : w[b].w;
-                    const uint32_t a0 = code_pair(q, 0), a1 = code_pair(q, 1), a2 = code_pair(q, 2), a3 = code_pair(q, 3);
+                    const uint32_t w = step == 0 ? wv[b].x : step == 1 ? wv[b].y : step == 2 ? wv[b].z : wv[b].w;
+                    const uint32_t a0 = code_pair(w, 0), a1 = code_pair(w, 1), a2 = code_pair(w, 2), a3 = code_pair(w, 3);
 #pragma unroll
-                    for (int a = 0; a < MT; ++a) mma::mma16816(c[b][a], a0, a1, a2, a3, b0[a], b1[a]);
+                    for (int a = 0; a < MT; ++a) {
+                        if (i == 0) mma_first(c[b][a], a0, a1, a2, a3, b0[a], b1[a]);
+                        else mma::mma16816(c[b][a], a0, a1, a2, a3, b0[a], b1[a]);
+                    }
                 }
             }
 #pragma unroll
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float step = mma::bf16_lo(par[b][s][r]), lo = fmaf(-128.f, step, mma::bf16_hi(par[b][s][r]));
+                    const uint32_t both = q.par[b][s][g + 8 * r];
+                    const float step = mma::bf16_lo(both), lo = fmaf(-128.f, step, mma::bf16_hi(both));
 #pragma unroll
                     for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -117,7 +157,24 @@ __global__ void __launch_bounds__(kQ4Threads, MT == 1 && NT == 1 ? 4 : 2) linear
                             tot[b][a][2 * r + e] = fmaf(step, c[b][a][2 * r + e], fmaf(lo, xs[a][e], tot[b][a][2 * r + e]));
                 }
         }
+    };
+#pragma unroll
+    for (int i = 0; i < kQ4Stages - 1; ++i) {
+        if (warp + i * warps < kb_all) load(warp + i * warps, i);
+        mma::cp_async_commit();
     }
+    int stage = 0;
+    for (int kb = warp; kb < kb_all; kb += warps) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kQ4Stages - 2) : "memory");
+        __syncwarp();                                          // the parameters are other lanes' copies
+        const int ahead = kb + (kQ4Stages - 1) * warps;
+        if (ahead < kb_all) load(ahead, stage == 0 ? kQ4Stages - 1 : stage - 1);
+        mma::cp_async_commit();
+        multiply(ring[stage]);
+        stage = stage + 1 == kQ4Stages ? 0 : stage + 1;
+    }
+    __syncthreads();                                           // the rings are read: the sums take their place
+    float (*red)[16 * NT][8 * MT + 1] = reinterpret_cast<float (*)[16 * NT][8 * MT + 1]>(smem);
 #pragma unroll
     for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -125,12 +182,12 @@ __global__ void __launch_bounds__(kQ4Threads, MT == 1 && NT == 1 ? 4 : 2) linear
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[warp][16 * b + g + 8 * (e >> 1)][8 * a + 2 * t + (e & 1)] = tot[b][a][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * NT * rows; i += kQ4Threads) {
+    for (int i = threadIdx.x; i < 16 * NT * rows; i += blockDim.x) {
         const int row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
         if (n >= p.n) continue;
         float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kQ4Warps; ++w) s += red[w][col][row];
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) s += red[w][col][row];
         static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
     }
 }
@@ -193,14 +250,14 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
 }
 
 // 64 columns by 64 k of W from the codes: one fp32 multiply-add, rounded to bf16.
-__global__ void __launch_bounds__(kQ4Threads) q4_expand_kernel(const __grid_constant__ Q4WeightParams p)
+__global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_constant__ Q4WeightParams p)
 {
     __shared__ uint16_t x[kQ4K][72];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, kb = blockIdx.y, n0 = blockIdx.x * 64;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
-    for (int i = tid; i < 4 * 128; i += kQ4Threads) {
+    for (int i = tid; i < 4 * 128; i += kExpandThreads) {
         const int nt = n0 / kQ4N + i / 128, lane = i % 128 / 4, s = i % 4, g = lane >> 2, t = lane & 3;
         if (nt * kQ4N >= p.n) continue;
         const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + kb) * 32 + lane)[s];
@@ -214,26 +271,39 @@ __global__ void __launch_bounds__(kQ4Threads) q4_expand_kernel(const __grid_cons
         }
     }
     __syncthreads();
-    for (int i = tid; i < kQ4K * 64; i += kQ4Threads) {
+    for (int i = tid; i < kQ4K * 64; i += kExpandThreads) {
         const int k = kb * kQ4K + i / 64, n = n0 + i % 64;
         if (k < p.k && n < p.n) static_cast<uint16_t*>(p.w)[static_cast<int64_t>(k) * p.ld_w + n] = x[i / 64][i % 64];
     }
 }
 
-template <int NT, int MT>
-cudaError_t launch_rows(const LinearQ4Params& p, cudaStream_t s)
+template <int NT, int MT, int SUB, bool VEC>
+cudaError_t launch_variant(const LinearQ4Params& p, int warps, cudaStream_t s)
 {
+    static OncePerDevice once;
+    const cudaError_t e = allow_smem(once, kQ4MaxWarps * kQ4Ring<NT, MT, SUB>, linear_q4_kernel<NT, MT, SUB, VEC>);
+    if (e != cudaSuccess) return e;
     const dim3 grid((p.n + kQ4N * NT - 1) / (kQ4N * NT), (p.m + 8 * MT - 1) / (8 * MT));
-    if (p.group == 32) return launch_dependent(linear_q4_kernel<NT, MT, 2>, grid, dim3(kQ4Threads), 0, s, p);
-    return launch_dependent(linear_q4_kernel<NT, MT, 1>, grid, dim3(kQ4Threads), 0, s, p);
+    return launch_dependent(linear_q4_kernel<NT, MT, SUB, VEC>, grid, dim3(32 * warps), warps * kQ4Ring<NT, MT, SUB>, s, p);
+}
+
+template <int NT, int MT>
+cudaError_t launch_rows(const LinearQ4Params& p, int warps, cudaStream_t s)
+{
+    if (p.group == 32)
+        return p.vec_x ? launch_variant<NT, MT, 2, true>(p, warps, s) : launch_variant<NT, MT, 2, false>(p, warps, s);
+    return p.vec_x ? launch_variant<NT, MT, 1, true>(p, warps, s) : launch_variant<NT, MT, 1, false>(p, warps, s);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_q4(const LinearQ4Params& p, int sm_count, cudaStream_t s)
 {
-    (void)sm_count;
-    return p.m <= 8 ? launch_rows<1, 1>(p, s) : launch_rows<1, 2>(p, s);
+    // Tiles of columns a block: more share x and its sums, as long as most SMs get a block.  Warps: a few blocks of k each.
+    const int tiles = (p.n + kQ4N - 1) / kQ4N, kb = (p.k + kQ4K - 1) / kQ4K;
+    const int nt = tiles >= 3 * sm_count && p.m <= 8 ? 4 : tiles >= 3 * sm_count / 2 ? 2 : 1, warps = kb >= 48 && p.m <= 8 ? 16 : 8;
+    if (p.m <= 8) return nt == 4 ? launch_rows<4, 1>(p, warps, s) : nt == 2 ? launch_rows<2, 1>(p, warps, s) : launch_rows<1, 1>(p, warps, s);
+    return nt == 2 ? launch_rows<2, 2>(p, warps, s) : launch_rows<1, 2>(p, warps, s);
 }
 
 cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s)
@@ -243,7 +313,7 @@ cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s)
 
 cudaError_t launch_q4_expand(const Q4WeightParams& p, cudaStream_t s)
 {
-    return launch_dependent(q4_expand_kernel, dim3((p.n + 63) / 64, (p.k + kQ4K - 1) / kQ4K), dim3(kQ4Threads), 0, s, p);
+    return launch_dependent(q4_expand_kernel, dim3((p.n + 63) / 64, (p.k + kQ4K - 1) / kQ4K), dim3(kExpandThreads), 0, s, p);
 }
 
 }  // namespace txl
