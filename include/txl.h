@@ -610,6 +610,16 @@ typedef struct {
 txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl_view* v_new, int T, const int* counts,
                           void* stream);
 
+/* txl_paged_push with its arguments in one struct, for bindings that pay per argument. */
+typedef struct {
+    const txl_paged* mem;
+    txl_view k_new, v_new;
+    const int* counts;
+    void* stream;
+    int T;
+} txl_paged_push_args;
+txl_status txl_paged_push_call(const txl_paged_push_args* args);
+
 /*
  * txl_rel_attn_paged -- relative attention of T = 1 .. 16 new tokens a sequence over a paged memory (incremental
  * generation, "Transformer-XL架构解析" §3.2: each new token attends to the cached memory and itself).  With k_new, v_new
@@ -704,6 +714,21 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
  */
 txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, void* Y, int64_t ld_y, void* workspace,
                          size_t workspace_bytes, int* err_flag, void* stream);
+
+/* txl_linear_q4 with its arguments in one struct, for bindings that pay per argument. */
+typedef struct {
+    const txl_q4* w;
+    const void* X;
+    int64_t ld_x;
+    void* Y;
+    int64_t ld_y;
+    void* workspace;
+    size_t workspace_bytes;
+    int* err_flag;
+    void* stream;
+    int m;
+} txl_linear_q4_args;
+txl_status txl_linear_q4_call(const txl_linear_q4_args* args);
 
 /* Bytes of device workspace txl_linear_q4 needs: 0 for m <= 64, else 2 k (n rounded up to a multiple of 8). */
 size_t txl_linear_q4_workspace_size(int m, const txl_q4* w);

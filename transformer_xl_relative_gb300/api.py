@@ -698,19 +698,19 @@ def paged_push(mem: PagedMemory, k_new: torch.Tensor, v_new: torch.Tensor, count
                stream=None) -> PagedMemory:
     """New positions of every sequence into its reserved pages (txl_paged_push): rows t < counts[b] (int32 [B], all
     T without it) of k_new, v_new [B, T, H, D]."""
-    B, H, D = mem._shape
-    T = k_new.shape[1] if k_new.dim() == 4 else 0
-    if k_new.shape != (B, T, H, D) or v_new.shape != k_new.shape:
+    (B, H, D), dev, dtype, shape = mem._shape, mem.device, mem._dtype, k_new.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != H or shape[3] != D or v_new.shape != shape:
         raise ValueError("expected k_new and v_new [%d, T, %d, %d]" % (B, H, D))
-    if k_new.dtype != mem._dtype or v_new.dtype != mem._dtype:
+    if k_new.dtype != dtype or v_new.dtype != dtype:
         raise TypeError("k_new and v_new must have the memory's dtype")
-    if k_new.get_device() != mem.device or v_new.get_device() != mem.device:
+    if k_new.get_device() != dev or v_new.get_device() != dev:
         raise ValueError("tensors must live on the memory's device")
-    vk, vv, n = view(k_new), view(v_new), _paged_counts(mem, counts)
-    raw = _raw_stream(stream, mem.device)
-    st = _on_device(mem.device, lambda _: _lib().txl_paged_push(ctypes.byref(mem._c), ctypes.byref(vk), ctypes.byref(vv), T,
-                                                                n, raw), None)
-    check(st, "txl_paged_push")
+    (k0, k1, k2, k3), (v0, v1, v2, v3) = k_new.stride(), v_new.stride()
+    if (k3 != 1 or v3 != 1) and D > 1:
+        raise ValueError("the last (d) dimension must be contiguous")
+    args = native.PAGED_PUSH_ARGS.pack(mem.address, k_new.data_ptr(), k0, k1, k2, v_new.data_ptr(), v0, v1, v2,
+                                       _paged_counts(mem, counts), _raw_stream(stream, dev), shape[1])
+    check(_on_device(dev, _lib().txl_paged_push_call, args), "txl_paged_push")
     return mem
 
 
@@ -819,6 +819,7 @@ class QuantWeight:
             raise ValueError("4-bit weights of [%d, %d] in groups of %d take %d bytes of a CUDA device" % (k, n, group, need))
         self.data, self.shape, self.group, self.device = data, (k, n), group, data.get_device()
         self._c = TxlQ4(data.data_ptr(), k, n, group)
+        self.address = ctypes.addressof(self._c)
 
     @classmethod
     def quantise(cls, W: torch.Tensor, group: int = 64, stream=None):
@@ -856,36 +857,34 @@ def linear_q4_workspace_size(m: int, w: QuantWeight) -> int:
 def linear_q4(X: torch.Tensor, w: QuantWeight, Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
               err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X W for bf16 X [m, k] and 4-bit W [k, n] (txl_linear_q4); Y [m, n] is allocated if not given, and so is the
-    workspace where more than 64 rows need one."""
-    dev = w.device
+    workspace where many rows need one."""
+    dev, (k, n) = w.device, w.shape
     px, ldx = _rows2d(X, "X")
-    m, k = X.shape
-    if k != w.shape[0]:
+    m = X.shape[0]
+    if X.shape[1] != k:
         raise ValueError("inner dimensions differ")
     if X.dtype != torch.bfloat16:
         raise TypeError("linear_q4 computes in bfloat16, got %s" % X.dtype)
-    if Y is None or (workspace is None and m > 64):
+    need = linear_q4_workspace_size(m, w) if workspace is None else 0
+    if Y is None or need:
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
             if Y is None:
-                Y = torch.empty(m, w.shape[1], dtype=X.dtype, device=X.device)
-            if workspace is None and m > 64:
-                workspace = torch.empty(max(linear_q4_workspace_size(m, w), 16), dtype=torch.uint8, device=X.device)
+                Y = torch.empty(m, n, dtype=X.dtype, device=X.device)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
     py, ldy = _rows2d(Y, "Y")
-    if Y.shape[0] != m or Y.shape[1] != w.shape[1] or Y.dtype != X.dtype:
-        raise ValueError("Y must be bfloat16 [%d, %d]" % (m, w.shape[1]))
+    if Y.shape != (m, n) or Y.dtype != torch.bfloat16:
+        raise ValueError("Y must be bfloat16 [%d, %d]" % (m, n))
     if X.get_device() != dev or Y.get_device() != dev:
         raise ValueError("tensors must live on the weights' device")
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and live on the weights' device")
-    pw, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
-    ef = err_flag.data_ptr() if err_flag is not None else None
-    raw = _raw_stream(stream, dev)
-    if dev == torch.cuda.current_device():
-        st = _lib().txl_linear_q4(m, ctypes.byref(w._c), px, max(ldx, k), py, max(ldy, w.shape[1]), pw, size, ef, raw)
-    else:
-        with torch.cuda.device(dev):
-            st = _lib().txl_linear_q4(m, ctypes.byref(w._c), px, max(ldx, k), py, max(ldy, w.shape[1]), pw, size, ef, raw)
-    check(st, "txl_linear_q4")
+    if err_flag is not None and (err_flag.get_device() != dev or err_flag.dtype != torch.int32 or err_flag.numel() < 1):
+        raise ValueError("err_flag must be an int32 on the weights' device")
+    pw, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
+    args = native.Q4_ARGS.pack(w.address, px, ldx if m > 1 else k, py, ldy if m > 1 else n, pw, size,
+                               err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev), m)
+    check(_on_device(dev, _lib().txl_linear_q4_call, args), "txl_linear_q4")
     return Y
 
 

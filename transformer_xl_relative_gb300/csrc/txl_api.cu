@@ -1409,6 +1409,12 @@ txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl
                ? TXL_OK : TXL_ERR_CUDA;
 }
 
+txl_status txl_paged_push_call(const txl_paged_push_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    return txl_paged_push(a->mem, &a->k_new, &a->v_new, a->T, a->counts, a->stream);
+}
+
 size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate)
 {
     if (!mem || mem->B <= 0 || mem->H <= 0 || mem->D <= 0 || mem->D > 128 || T <= 0 || T > kDecodeMaxL || n_rows <= 0 ||
@@ -1546,6 +1552,12 @@ txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, vo
     p.m = m; p.n = w->n; p.k = w->k; p.group = w->group;
     p.vec_x = rows16;
     return launch_linear_q4(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TXL_OK : TXL_ERR_CUDA;
+}
+
+txl_status txl_linear_q4_call(const txl_linear_q4_args* a)
+{
+    if (!a) return TXL_ERR_INVALID_ARG;
+    return txl_linear_q4(a->m, a->w, a->X, a->ld_x, a->Y, a->ld_y, a->workspace, a->workspace_bytes, a->err_flag, a->stream);
 }
 
 int txl_checked_build(void) { return kCheckedBuild ? 1 : 0; }

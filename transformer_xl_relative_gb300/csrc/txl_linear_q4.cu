@@ -243,7 +243,10 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
             const int c = g + 8 * (j & 1), k = kb * kQ4K + 32 * (s >> 1) + 8 * t + 4 * (s & 1) + (j & 2) + (j >> 2);
             if (k0 + k >= p.k) continue;
             const float a = lo[k / p.group][c], d = step[k / p.group][c];
-            if (d > 0.f) w |= static_cast<uint32_t>(rint((static_cast<double>(x[k][c]) - a) / d)) << (4 * j);
+            if (!(d > 0.f)) continue;
+            // the fp32 quotient is within 2^-19 of the exact one: only near a half does it take more bits to round it
+            const float q = (x[k][c] - a) / d, half = fabsf(q - floorf(q) - 0.5f);
+            w |= static_cast<uint32_t>(half > 0x1p-17f ? rintf(q) : static_cast<float>(rint((static_cast<double>(x[k][c]) - a) / d))) << (4 * j);
         }
         reinterpret_cast<uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + k0 / kQ4K + kb) * 32 + lane)[s] = w;
     }
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
 // 64 columns by 64 k of W from the codes: one fp32 multiply-add, rounded to bf16.
 __global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_constant__ Q4WeightParams p)
 {
-    __shared__ uint16_t x[kQ4K][72];
+    __shared__ __align__(16) uint16_t x[kQ4K][72];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, kb = blockIdx.y, n0 = blockIdx.x * 64;
@@ -271,9 +274,16 @@ __global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_
         }
     }
     __syncthreads();
-    for (int i = tid; i < kQ4K * 64; i += kExpandThreads) {
-        const int k = kb * kQ4K + i / 64, n = n0 + i % 64;
-        if (k < p.k && n < p.n) static_cast<uint16_t*>(p.w)[static_cast<int64_t>(k) * p.ld_w + n] = x[i / 64][i % 64];
+    // eight columns a store where rows start on 16-byte boundaries
+    const bool vec = (reinterpret_cast<uintptr_t>(p.w) | static_cast<uintptr_t>(2 * p.ld_w)) % 16 == 0;
+    for (int i = tid; i < kQ4K * 8; i += kExpandThreads) {
+        const int k = kb * kQ4K + i / 8, n = n0 + i % 8 * 8;
+        if (k >= p.k || n >= p.n) continue;
+        uint16_t* row = static_cast<uint16_t*>(p.w) + static_cast<int64_t>(k) * p.ld_w + n;
+        const uint16_t* from = &x[i / 8][i % 8 * 8];
+        if (vec && n + 8 <= p.n) *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(from);
+        else
+            for (int e = 0; e < min(8, p.n - n); ++e) row[e] = from[e];
     }
 }
 

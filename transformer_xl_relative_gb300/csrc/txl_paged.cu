@@ -58,6 +58,9 @@ __device__ __forceinline__ uint64_t leave_key(float w, int pos)
 
 constexpr int kEvictThreads = 1024;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
+constexpr int kEvictHeld = 8192;           // keys of a block that shared memory holds (more are made again each time)
+constexpr int kEvictRanks = 8;             // blocks of a sequence, at most
+constexpr int kEvictEach = 2048;           // slots that are worth a block
 
 // Exclusive sum over the block, and the total (every thread calls; 1024 threads).
 __device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total)
@@ -83,105 +86,143 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total)
     return s - x + (warp ? before : 0);
 }
 
-// One block per sequence: which slots leave (a selection by digits of the key, from the top), then which survivors
-// behind slot `keep` fill which holes in front of it.
-__global__ void __launch_bounds__(kEvictThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p)
+// A cluster of blocks per sequence, each with a range of its slots: which slots leave (a selection by digits of the key,
+// from the top, over the sum of the blocks' histograms), then which survivors behind slot `keep` fill which holes in front.
+// Shared memory: the histograms of this digit and the next, the keys.
+__global__ void __launch_bounds__(kEvictThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p, int held)
 {
-    __shared__ int bins[kBins];
+    extern __shared__ __align__(16) uint64_t keys[];
+    int* bins = reinterpret_cast<int*>(keys + held);                          // [2][kBins]
     __shared__ int sums[32];
-    __shared__ int found[2];
+    __shared__ int found[3];
+    __shared__ int counts[2];                                                 // holes, movers of this block
     pdl_wait();
     pdl_launch_dependents();
     const PagedParams& m = p.m;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.y, tid = threadIdx.x, ranks = gridDim.x, rank = blockIdx.x;
     const int n = m.length[b], keep = p.keep;
-    const bool whole = n > keep ? paged_room(m, b, 0, n) : true;
+    const bool whole = n > keep ? paged_room(m, b, 0, n) : true;              // (the blocks of a sequence agree)
     if (n <= keep || !whole) {
-        if (tid == 0) {
+        if (tid == 0 && rank == 0) {
             p.moves[b] = 0;
             if (!whole) page_error(m);
         }
         return;
     }
     const int64_t guard = static_cast<int64_t>(m.next_pos[b]) - p.recent;      // positions from here on stay
-    auto row = [&](int s) { return static_cast<int64_t>(page_of(m, b, s)) * m.page_len + s % m.page_len; };
+    // this block's slots, an equal number for each thread, in order
+    const int per = (n + ranks * kEvictThreads - 1) / (ranks * kEvictThreads);
+    const int s0 = rank * kEvictThreads * per, mine = max(0, min(n - s0, kEvictThreads * per));
+    constexpr uint64_t kStays = ~uint64_t{0};                                 // (no position is -1)
+    auto row = [&](int s) { return page_of(m, b, s) * m.page_len + s % m.page_len; };
+    auto make = [&](int i) {
+        const int at = row(s0 + i);
+        const int pos = m.pos[at];
+        return pos < guard ? leave_key(m.weight[at], pos) : kStays;
+    };
+    for (int i = tid; i < min(mine, held); i += kEvictThreads) keys[i] = make(i);
+    for (int i = tid; i < 2 * kBins; i += kEvictThreads) bins[i] = 0;
+    auto key_of = [&](int i) { return i < held ? keys[i] : make(i); };
 
     // the least (n - keep) keys: those whose bits above `shift` are at most `limit`
-    int want = n - keep, shift = 64;
+    int want = n - keep, shift = 64, turn = 0;
     uint64_t limit = 0;
-    bool none = false;
     while (shift > 0) {
         const int width = min(kDigit, shift);
-        for (int i = tid; i < kBins; i += kEvictThreads) bins[i] = 0;
+        int* own = bins + turn * kBins;
         __syncthreads();
-        for (int s0 = 0; s0 < n; s0 += kEvictThreads) {
-            const int s = s0 + tid;
+        for (int i0 = 0; i0 < mine; i0 += kEvictThreads) {
+            const int i = i0 + tid;
             int bin = -1;
-            if (s < n) {
-                const int64_t at = row(s);
-                const int pos = m.pos[at];
-                const uint64_t key = leave_key(m.weight[at], pos);
-                if (pos < guard && (shift == 64 || key >> shift == limit))
+            if (i < mine) {
+                const uint64_t key = key_of(i);
+                if (key != kStays && (shift == 64 || key >> shift == limit))
                     bin = static_cast<int>(key >> (shift - width)) & ((1 << width) - 1);
             }
             // many slots of one weight would queue at one bin: a warp that agrees adds once
             const int first = __shfl_sync(0xffffffffu, bin, 0);
             if (__all_sync(0xffffffffu, bin == first)) {
-                if (first >= 0 && (tid & 31) == 0) atomicAdd(bins + first, 32);
+                if (first >= 0 && (tid & 31) == 0) atomicAdd(own + first, 32);
             } else if (bin >= 0) {
-                atomicAdd(bins + bin, 1);
+                atomicAdd(own + bin, 1);
             }
         }
-        __syncthreads();
+        if (ranks > 1) cluster_sync_all();
+        else __syncthreads();
+        turn ^= 1;
         constexpr int kPer = kBins / kEvictThreads;
-        int mine = 0, total;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) mine += bins[tid * kPer + i];
-        int below = block_scan(mine, sums, total);
-        if (total < want) { want = total; none = total == 0; }      // fewer may leave (positions that are out of order)
-        if (none) break;
+        int c[kPer], sum = 0, total;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int c = bins[tid * kPer + i];
-            if (below < want && want <= below + c) { found[0] = tid * kPer + i; found[1] = below; }
-            below += c;
+            c[i] = 0;
+            for (int r = 0; r < ranks; ++r)
+                c[i] += ranks > 1 ? __float_as_int(ld_rank(reinterpret_cast<const float*>(own + tid * kPer + i), r)) : own[tid * kPer + i];
+            sum += c[i];
+            if (shift != 64) bins[turn * kBins + tid * kPer + i] = 0;          // (all blocks have read that one)
+        }
+        int below = block_scan(sum, sums, total);
+        if (total < want) want = total;                                       // (positions that are not distinct)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (below < want && want <= below + c[i]) { found[0] = tid * kPer + i; found[1] = below; found[2] = c[i]; }
+            below += c[i];
         }
         __syncthreads();
+        if (want == 0) break;
         const int digit = found[0];
-        const bool all = found[1] + bins[digit] == want;            // the whole bin leaves: no need to look closer
+        const bool all = found[1] + found[2] == want;                         // the whole bin leaves: no need to look closer
         want -= found[1];
         shift -= width;
         limit = (limit << width) | static_cast<uint64_t>(digit);
-        __syncthreads();
         if (all) break;
     }
-    auto leaves = [&](int s) {
-        const int64_t at = row(s);
-        const int pos = m.pos[at];
-        return !none && pos < guard && leave_key(m.weight[at], pos) >> shift <= limit;
+    // a thread's slots are neighbours: one sum over the threads each orders its holes and its movers
+    auto leaves = [&](int i) {
+        const uint64_t key = key_of(i);
+        return key != kStays && shift < 64 && key >> shift <= limit;
     };
     int holes = 0, movers = 0;
+    for (int i = tid * per; i < min(mine, (tid + 1) * per); ++i) {
+        const bool gone = leaves(i);
+        holes += gone && s0 + i < keep;
+        movers += !gone && s0 + i >= keep;
+    }
+    int all_holes, all_movers;
+    holes = block_scan(holes, sums, all_holes);
+    movers = block_scan(movers, sums, all_movers);
+    if (tid == 0) {
+        counts[0] = all_holes;
+        counts[1] = all_movers;
+    }
+    int total_holes = all_holes, total_movers = all_movers;
+    if (ranks > 1) {
+        cluster_sync_all();
+        total_holes = total_movers = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const int h = __float_as_int(ld_rank(reinterpret_cast<const float*>(counts), r));
+            const int v = __float_as_int(ld_rank(reinterpret_cast<const float*>(counts + 1), r));
+            if (r < rank) { holes += h; movers += v; }
+            total_holes += h;
+            total_movers += v;
+        }
+    }
     int* to = p.to + static_cast<int64_t>(b) * p.most;
     int* from = p.from + static_cast<int64_t>(b) * p.most;
-    for (int s0 = 0; s0 < n; s0 += kEvictThreads) {
-        const int s = s0 + tid;
-        bool hole = false, mover = false;
-        if (s < n) {
-            const bool gone = leaves(s);
-            hole = gone && s < keep;
-            mover = !gone && s >= keep;
+    for (int i = tid * per; i < min(mine, (tid + 1) * per); ++i) {
+        const bool gone = leaves(i);
+        if (gone && s0 + i < keep) {
+            if (holes < p.most) to[holes] = row(s0 + i);
+            ++holes;
+        } else if (!gone && s0 + i >= keep) {
+            if (movers < p.most) from[movers] = row(s0 + i);
+            ++movers;
         }
-        int total;
-        const int rank = block_scan(hole ? 1 : mover ? 0x10000 : 0, sums, total);
-        if (hole && holes + (rank & 0xffff) < p.most) to[holes + (rank & 0xffff)] = static_cast<int>(row(s));
-        if (mover && movers + (rank >> 16) < p.most) from[movers + (rank >> 16)] = static_cast<int>(row(s));
-        holes += total & 0xffff;
-        movers += total >> 16;
     }
-    if (tid == 0) {
-        p.moves[b] = min(holes, movers);
+    if (tid == 0 && rank == 0) {
+        p.moves[b] = min(p.most, min(total_holes, total_movers));
         m.length[b] = keep;
     }
+    if (ranks > 1) cluster_sync_all();                                        // no block leaves while others read its counts
 }
 
 constexpr int kMoveThreads = 256;
@@ -236,7 +277,28 @@ cudaError_t launch_paged_push(const PagedPushParams& p, txl_dtype dtype, cudaStr
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sm_count, cudaStream_t s)
 {
-    cudaError_t e = launch_dependent(paged_select_kernel, dim3(p.m.B), dim3(kEvictThreads), 0, s, p);
+    static OncePerDevice once;
+    const int cap = p.m.max_pages * p.m.page_len;
+    int ranks = 1;
+    while (ranks < kEvictRanks && cap > ranks * kEvictEach) ranks *= 2;
+    const int held = min(kEvictHeld, (cap + ranks * kEvictThreads - 1) / (ranks * kEvictThreads) * kEvictThreads);
+    const int most_smem = kEvictHeld * 8 + 2 * kBins * 4, smem = held * 8 + 2 * kBins * 4;
+    cudaError_t e = allow_smem(once, most_smem, paged_select_kernel);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks, p.m.B);
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, paged_select_kernel, p, held);
     if (e != cudaSuccess) return e;
     const int blocks = min(max(1, sm_count * 8 / p.m.B), (p.most + kMoveThreads / 32 - 1) / (kMoveThreads / 32));
     return launch_dependent(paged_move_kernel, dim3(max(1, blocks), p.m.B), dim3(kMoveThreads), 0, s, p);

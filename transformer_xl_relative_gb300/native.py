@@ -33,7 +33,7 @@ EXPORTS = (
     "txl_rel_attn_qmem_call", "txl_qmem_push_call", "txl_qmem_read_call",
     "txl_paged_push", "txl_rel_attn_paged", "txl_rel_attn_paged_workspace_size", "txl_paged_evict",
     "txl_paged_evict_workspace_size", "txl_q4_bytes", "txl_q4_quantise", "txl_q4_expand", "txl_linear_q4",
-    "txl_linear_q4_workspace_size",
+    "txl_linear_q4_workspace_size", "txl_paged_push_call", "txl_linear_q4_call",
 )
 
 
@@ -69,6 +69,10 @@ class TxlQ4(ctypes.Structure):
 # txl_rel_attn_paged_args: T, clamp_len, n_rows, accumulate, scale; mem; the views q, k_new, v_new, out; counts, u,
 # v_bias, r, ld_r, workspace, workspace_bytes, stream (pointers as unsigned 64-bit numbers)
 PAGED_ARGS = struct.Struct("@4if" + "Q" + 4 * "Qqqq" + "QQQQqQQQ")
+# txl_paged_push_args: mem; the views k_new, v_new; counts, stream; T
+PAGED_PUSH_ARGS = struct.Struct("@Q" + 2 * "Qqqq" + "QQi")
+# txl_linear_q4_args: w, X, ld_x, Y, ld_y, workspace, workspace_bytes, err_flag, stream, m
+Q4_ARGS = struct.Struct("@QQqQqQQQQi")
 # txl_qmem_kv_args: mem; the views k, v; j0, n, dtype; stream (pointers as unsigned 64-bit numbers)
 QMEM_KV_ARGS = struct.Struct("@Q" + 2 * "Qqqq" + "3iQ")
 # txl_rel_attn_qmem_args: B, L, H, D, clamp_len, n_rows, dtype, scale; the views q, k_cur, v_cur, out; mem, u,
@@ -186,6 +190,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     Pp, Wp, sz = ctypes.POINTER(TxlPaged), ctypes.POINTER(TxlQ4), ctypes.c_size_t
     lib.txl_paged_push.argtypes = [Pp, V, V, i, vp, vp]
     lib.txl_paged_push.restype = i
+    lib.txl_paged_push_call.argtypes = [ctypes.c_char_p]
+    lib.txl_paged_push_call.restype = i
+    lib.txl_linear_q4_call.argtypes = [ctypes.c_char_p]
+    lib.txl_linear_q4_call.restype = i
     lib.txl_rel_attn_paged.argtypes = [ctypes.c_char_p]
     lib.txl_rel_attn_paged.restype = i
     lib.txl_rel_attn_paged_workspace_size.argtypes = [Pp, i, i, i]
