@@ -45,23 +45,18 @@ __device__ __forceinline__ bool paged_room(const PagedParams& m, int b, int len,
 }
 
 // Rows t0 .. t1-1 of sequence b into its slots len + t: keys, values, positions; the weights start at 0.  Every
-// slot has its page.  Rows are copied in units of 16 bytes; the channels D .. ld-1 are written as zeros.
+// slot has its page.  Rows are copied in units of 16 bytes; the channels D .. ld-1 are written as zeros.  A thread keeps its
+// unit of a position and goes over the positions, four loaded before the first is stored.
 template <typename T>
 __device__ __forceinline__ void paged_copy(const PagedPushParams& p, int b, int len, int next, int t0, int t1)
 {
-    constexpr int kUnit = 16 / sizeof(T);
+    constexpr int kUnit = 16 / sizeof(T), kAtOnce = 4;
     const PagedParams& m = p.m;
-    const int units = m.ld / kUnit, per = m.H * units, n = (t1 - t0) * per;
-    for (int x = threadIdx.x; x < 2 * n; x += blockDim.x) {
-        const bool value = x >= n;
-        const int y = value ? x - n : x, t = t0 + y / per, z = y % per, h = z / units, c = z % units;
-        const T* src = value ? static_cast<const T*>(p.xv) + b * p.xv_sb + t * p.xv_st + h * p.xv_sh
-                             : static_cast<const T*>(p.xk) + b * p.xk_sb + t * p.xk_st + h * p.xk_sh;
-        const int slot = len + t;
-        T* dst = static_cast<T*>(value ? m.v : m.k) + page_row0(m, page_of(m, b, slot), h) +
-                 static_cast<int64_t>(slot % m.page_len) * m.ld + c * kUnit;
+    const int units = m.ld / kUnit, per = m.H * units, side = max(1, static_cast<int>(blockDim.x) / per);
+    const int first = threadIdx.x / per;                      // of the positions that the block takes side by side
+    auto load = [&](const T* src, int c, bool vec) {
         union { uint4 all; T one[kUnit]; } u;
-        if ((value ? p.vec_v : p.vec_k) && (c + 1) * kUnit <= m.D) {
+        if (vec && (c + 1) * kUnit <= m.D) {
             u.all = *reinterpret_cast<const uint4*>(src + c * kUnit);
         } else {
             u.all = make_uint4(0, 0, 0, 0);
@@ -69,7 +64,29 @@ __device__ __forceinline__ void paged_copy(const PagedPushParams& p, int b, int 
             for (int e = 0; e < kUnit; ++e)
                 if (c * kUnit + e < m.D) u.one[e] = src[c * kUnit + e];
         }
-        *reinterpret_cast<uint4*>(dst) = u.all;
+        return u.all;
+    };
+    for (int z = threadIdx.x - first * per; first < side && z < per; z += blockDim.x) {
+        const int h = z / units, c = z - h * units;
+        const T* k = static_cast<const T*>(p.xk) + b * p.xk_sb + h * p.xk_sh;
+        const T* v = static_cast<const T*>(p.xv) + b * p.xv_sb + h * p.xv_sh;
+        for (int t = t0 + first; t < t1; t += kAtOnce * side) {
+            uint4 w[kAtOnce][2];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (t + i * side < t1) {
+                    w[i][0] = load(k + (t + i * side) * p.xk_st, c, p.vec_k);
+                    w[i][1] = load(v + (t + i * side) * p.xv_st, c, p.vec_v);
+                }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (t + i * side < t1) {
+                    const int slot = len + t + i * side;
+                    const int64_t at = page_row0(m, page_of(m, b, slot), h) + static_cast<int64_t>(slot % m.page_len) * m.ld + c * kUnit;
+                    *reinterpret_cast<uint4*>(static_cast<T*>(m.k) + at) = w[i][0];
+                    *reinterpret_cast<uint4*>(static_cast<T*>(m.v) + at) = w[i][1];
+                }
+        }
     }
     for (int t = t0 + static_cast<int>(threadIdx.x); t < t1; t += blockDim.x) {
         const int slot = len + t;

@@ -35,28 +35,14 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// ---------------------------------------------------------------- fragments of the queries
-// A 16 x 16 fragment of mma.m16n8k16 holds eight queries twice: row g the upper 8 bits of (q + bias) * scale, row
-// g + 8 the next 8, so that the sum of the two rows' products has 16 bits of the query.  Step j: channels 16 j .. 16 j + 15.
-template <int NC> struct QFrag { uint32_t hi[2 * NC][2], lo[2 * NC][2]; };
-
-template <int NC>
-__device__ __forceinline__ void load_q(QFrag<NC>& f, const __nv_bfloat16* q, const float* bias, bool live, int D, float scale,
-                                       int t)
+// Eight bf16 of a row of r from channel d on; channels at and past D are 0.
+__device__ __forceinline__ uint4 row_unit(const uint16_t* row, int d, int D, bool vec)
 {
+    if (vec && d + 8 <= D) return *reinterpret_cast<const uint4*>(row + d);
+    uint32_t x[8];
 #pragma unroll
-    for (int j = 0; j < 2 * NC; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int d = 16 * j + 8 * e + 2 * t + k;
-                x[k] = live && d < D ? (__bfloat162float(q[d]) + bias[d]) * scale : 0.f;
-            }
-            f.hi[j][e] = mma::pack2(x[0], x[1]);
-            f.lo[j][e] = mma::pack2(x[0] - mma::bf16_lo(f.hi[j][e]), x[1] - mma::bf16_hi(f.hi[j][e]));
-        }
+    for (int z = 0; z < 8; ++z) x[z] = d + z < D ? row[d + z] : 0u;
+    return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
 }
 
 // ---------------------------------------------------------------- preparation
@@ -90,66 +76,98 @@ __device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b, i
     if (threadIdx.x == 0 && part == 0) p.now[b] = now;
 }
 
+// bf16: the queries are the 16 rows of the mma's A, row g the upper 8 bits of (q + v) scale and row g + 8 the next 8, so that
+// the sum of the two rows' products has 16 bits of the query.  Lane (g, t) loads units t + 4 j of 16 bytes of r's row g as they
+// are; the channels' order in A follows.
 template <int NC>
-__device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h, int f0, int d0)
+__device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h, int f0, int d0, uint16_t* qs)
 {
+    constexpr int kWidth = 32 * NC, kRow = kWidth + 8, kEach = kPrepRows / (8 * kWarps);
     const PagedParams& m = p.n.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int T = p.n.T, f = f0 + g, b = f / T, i = f - b * T;
-    const bool live = f < m.B * T;
-    QFrag<NC> q;
-    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q);
-    if (live) qr += b * p.q_sb + i * p.q_st + h * p.q_sh;
-    load_q<NC>(q, qr, p.vb + h * m.D, live, m.D, p.qscale, t);
-    float* E = p.E + ((static_cast<int64_t>(b) * m.H + h) * T + i) * p.e_pitch;
+    const int T = p.n.T;
     const uint16_t* r = static_cast<const uint16_t*>(p.r) + h * p.r_head;
-    constexpr int kEach = kPrepRows / (8 * kWarps);
-    uint32_t w[kEach][2 * NC][2];
+    uint4 w[kEach][NC];
 #pragma unroll
     for (int y = 0; y < kEach; ++y) {
         const uint16_t* row = r + static_cast<int64_t>(min(d0 + (y * kWarps + warp) * 8 + g, p.n_e - 1)) * p.r_row;
 #pragma unroll
-        for (int j = 0; j < 2 * NC; ++j)
+        for (int j = 0; j < NC; ++j) w[y][j] = row_unit(row, 8 * (t + 4 * j), m.D, p.vec_r);
+    }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int d = 16 * j + 8 * e + 2 * t;
-                if (p.vec_r && d + 2 <= m.D) w[y][j][e] = *reinterpret_cast<const uint32_t*>(row + d);
-                else w[y][j][e] = (d < m.D ? row[d] : 0u) | (d + 1 < m.D ? row[d + 1] : 0u) << 16;
-            }
+    for (int e = 0; e < 8 * kWidth / kThreads; ++e) {
+        const int x = threadIdx.x + e * kThreads, i = x / kWidth, d = x % kWidth, f = f0 + i, b = f / T;
+        float y = 0.f;
+        if (f < m.B * T && d < m.D)
+            y = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[b * p.q_sb + (f - b * T) * p.q_st + h * p.q_sh + d]) + p.vb[h * m.D + d]) * p.qscale;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(y);
+        qs[i * kRow + d] = __bfloat16_as_ushort(hi);
+        qs[(8 + i) * kRow + d] = __bfloat16_as_ushort(__float2bfloat16_rn(y - __bfloat162float(hi)));
+    }
+    __syncthreads();
+    const int f = f0 + g, b = f / T;
+    float* E = p.E + ((static_cast<int64_t>(b) * m.H + h) * T + f - b * T) * p.e_pitch;
+    float c[kEach][4] = {};
+#pragma unroll
+    for (int j = 0; j < 2 * NC; ++j) {
+        const uint16_t* q = qs + g * kRow + 8 * (t + 4 * (j >> 1)) + 4 * (j & 1);
+        const uint2 hi = *reinterpret_cast<const uint2*>(q), lo = *reinterpret_cast<const uint2*>(q + 8 * kRow);
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+            const uint4 u = w[y][j >> 1];
+            mma::mma16816(c[y], hi.x, lo.x, hi.y, lo.y, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
+        }
     }
 #pragma unroll
     for (int y = 0; y < kEach; ++y) {
         const int x0 = d0 + (y * kWarps + warp) * 8;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 2 * NC; ++j) mma::mma16816(c, q.hi[j][0], q.lo[j][0], q.hi[j][1], q.lo[j][1], w[y][j][0], w[y][j][1]);
-        if (live && x0 < p.n_e) *reinterpret_cast<float2*>(E + x0 + 2 * t) = make_float2(c[0] + c[2], c[1] + c[3]);
+        if (f < m.B * T && x0 < p.n_e) *reinterpret_cast<float2*>(E + x0 + 2 * t) = make_float2(c[y][0] + c[y][2], c[y][1] + c[y][3]);
     }
 }
 
-// fp32: a thread per distance, the queries' rows from shared memory.
+// fp32: a warp takes eight distances at a time; lane (g, t) channels 4 (t + 4 j) .. + 3 of distance g, for eight queries
+// whose rows lie in shared memory.
+template <int NC>
 __device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, int f0, int d0, float* q)
 {
+    constexpr int NJ = 2 * NC, kWidth = 32 * NC;
     const PagedParams& m = p.n.m;
-    const int T = p.n.T, D = m.D;
-    const int n = min(8, m.B * T - f0);
-    for (int x = threadIdx.x; x < 8 * D; x += kThreads) {
-        const int f = f0 + x / D, d = x % D, b = f / T, i = f - b * T;
-        q[x] = x / D < n ? (static_cast<const float*>(p.q)[b * p.q_sb + i * p.q_st + h * p.q_sh + d] + p.vb[h * D + d]) * p.qscale : 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int T = p.n.T, D = m.D, n = min(8, m.B * T - f0);
+    for (int x = threadIdx.x; x < 8 * kWidth; x += kThreads) {
+        const int e = x / kWidth, d = x % kWidth, f = f0 + e, b = f / T, i = f - b * T;
+        q[x] = e < n && d < D ? (static_cast<const float*>(p.q)[b * p.q_sb + i * p.q_st + h * p.q_sh + d] + p.vb[h * D + d]) * p.qscale : 0.f;
     }
     __syncthreads();
-    const int x = d0 + threadIdx.x;
-    if (x < p.n_e) {
-        const float* row = static_cast<const float*>(p.r) + h * p.r_head + static_cast<int64_t>(x) * p.r_row;
-        float s[8] = {};
-        for (int d = 0; d < D; ++d) {
-            const float y = row[d];
+    const float* r = static_cast<const float*>(p.r) + h * p.r_head;
+#pragma unroll 1
+    for (int x0 = d0 + warp * 8; x0 < min(p.n_e, d0 + kPrepRows); x0 += kWarps * 8) {
+        asm volatile("" ::: "memory");                         // (the queries' rows do not fit the registers)
+        const int x = x0 + g;
+        const float* row = r + static_cast<int64_t>(min(x, p.n_e - 1)) * p.r_row;
+        float4 w[NJ];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = fmaf(q[e * D + d], y, s[e]);
+        for (int j = 0; j < NJ; ++j) {
+            const int d = 4 * (t + 4 * j);
+            if (p.vec_r && d + 4 <= D) w[j] = *reinterpret_cast<const float4*>(row + d);
+            else w[j] = make_float4(d < D ? row[d] : 0.f, d + 1 < D ? row[d + 1] : 0.f, d + 2 < D ? row[d + 2] : 0.f, d + 3 < D ? row[d + 3] : 0.f);
         }
+        float s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float4 y = *reinterpret_cast<const float4*>(q + e * kWidth + 4 * (t + 4 * j));
+                s[e] = fmaf(y.w, w[j].w, fmaf(y.z, w[j].z, fmaf(y.y, w[j].y, fmaf(y.x, w[j].x, s[e]))));
+            }
+            s[e] += __shfl_xor_sync(0xffffffffu, s[e], 1);
+            s[e] += __shfl_xor_sync(0xffffffffu, s[e], 2);
+        }
+        // lane t writes queries t and t + 4
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < n) {
+            if ((e & 3) == t && e < n && x < p.n_e) {
                 const int f = f0 + e, b = f / T, i = f - b * T;
                 p.E[((static_cast<int64_t>(b) * m.H + h) * T + i) * p.e_pitch + x] = s[e];
             }
@@ -159,7 +177,7 @@ __device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, 
 template <typename T, int NC>
 __global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_constant__ PagedAttnParams p, int copies, int share)
 {
-    __shared__ float qs[sizeof(T) == 4 ? 8 * 128 : 1];
+    __shared__ __align__(16) float qs[sizeof(T) == 4 ? 8 * 32 * NC : 8 * (32 * NC + 8)];
     __shared__ int far;
     pdl_wait();
     pdl_launch_dependents();
@@ -179,8 +197,8 @@ __global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_const
         atomicMax(&far, m.next_pos[b] + (p.n.xk ? p.n.T : 0));
     __syncthreads();
     if (d0 >= far) return;
-    if constexpr (sizeof(T) == 4) prep_terms_f32(p, h, f0, d0, qs);
-    else prep_terms_bf16<NC>(p, h, f0, d0);
+    if constexpr (sizeof(T) == 4) prep_terms_f32<NC>(p, h, f0, d0, qs);
+    else prep_terms_bf16<NC>(p, h, f0, d0, reinterpret_cast<uint16_t*>(qs));
 }
 
 // ---------------------------------------------------------------- attention
@@ -443,17 +461,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     auto load_row = [&](int distance, uint4* w) {
         const uint16_t* row = r + static_cast<int64_t>(distance) * p.r_row;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int c = t + 4 * j;
-            if (p.vec_r && 8 * c + 8 <= m.D) {
-                w[j] = *reinterpret_cast<const uint4*>(row + 8 * c);
-            } else {
-                uint32_t x[8];
-#pragma unroll
-                for (int z = 0; z < 8; ++z) x[z] = 8 * c + z < m.D ? row[8 * c + z] : 0u;
-                w[j] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-            }
-        }
+        for (int j = 0; j < NC; ++j) w[j] = row_unit(row, 8 * (t + 4 * j), m.D, p.vec_r);
     };
     auto load_terms = [&]() {
 #pragma unroll
@@ -1048,8 +1056,8 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
 }
 
 // ---------------------------------------------------------------- attention weights
-// A block takes 32 slots of a sequence, its warps every eighth (head, query) row of scores; the sums meet in a fixed order.
-constexpr int kWeightThreads = 256, kWeightWarps = kWeightThreads / 32;
+// A block takes 32 slots of a sequence, a warp every 16th head; the sums meet in a fixed order.
+constexpr int kWeightThreads = 512, kWeightWarps = kWeightThreads / 32;
 
 __global__ void __launch_bounds__(kWeightThreads) paged_weight_kernel(const __grid_constant__ PagedAttnParams p)
 {
@@ -1060,18 +1068,19 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weight_kernel(const __gr
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 now = p.now[b];
     if (now.z == 0) return;
-    const int rows = m.H * now.z;
     for (int s0 = blockIdx.x * 32; s0 < now.x; s0 += gridDim.x * 32) {
         const int s = s0 + lane;
         float sum = 0.f;
-        if (s < now.x) {
-#pragma unroll 8
-            for (int x = warp; x < rows; x += kWeightWarps) {
-                const int64_t row = (static_cast<int64_t>(b) * m.H + x / now.z) * p.n.T + x % now.z;
-                const float y = p.S[row * p.cap + s], l = p.lse[row];
-                sum += y == kNone ? 0.f : exp2f(y - l);
+        if (s < now.x)
+            for (int h = warp; h < m.H; h += kWeightWarps) {
+                const int64_t row = (static_cast<int64_t>(b) * m.H + h) * p.n.T;
+                const float* S = p.S + row * p.cap + s;
+#pragma unroll 4
+                for (int i = 0; i < now.z; ++i) {
+                    const float y = S[static_cast<int64_t>(i) * p.cap], l = p.lse[row + i];
+                    sum += y == kNone ? 0.f : exp2f(y - l);
+                }
             }
-        }
         sums[warp][lane] = sum;
         __syncthreads();
         if (warp == 0 && s < now.x) {
