@@ -584,6 +584,8 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
  *   err_flag : optional device int: a call that meets a slot without a page writes TXL_ERR_PAGE there if it is 0 (never
  *              cleared by the library).  Such a slot counts as not there; a push that does not find pages for all new
  *              positions of a sequence leaves that sequence as it was, and its queries' outputs too.
+ * Calls on one memory must not overlap on the GPU (one stream, or ordered streams), and no tensor that a call writes may
+ * overlap one that it reads.
  * Limits (TXL_ERR_UNSUPPORTED): D <= 128; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
  * max_pages * page_len below 2^31.  Positions are ints.
  */
@@ -634,7 +636,7 @@ txl_status txl_paged_push_call(const txl_paged_push_args* args);
  *   accumulate : not 0: weight[j] += sum over heads and queries of softmax_j(s_ij), for txl_paged_evict (a slot's weight
  *              is the sum over the calls since it entered).
  *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_paged_workspace_size bytes (TXL_ERR_WORKSPACE).
- *              Calls that share a workspace, or a memory, must not overlap on the GPU.
+ *              Calls that share a workspace must not overlap on the GPU.
  * The slots of all (sequence, head) pairs are cut into equal shares for the blocks, whatever the lengths.  bf16: mma.sync
  * products; scale log2(e) (q + u), scale log2(e) (q + v) and the weights of the softmax are held to 16 bits (two bf16
  * each).  f32: fp32 arithmetic on the CUDA cores.  The result does not depend on the order in which blocks run.  A key or value

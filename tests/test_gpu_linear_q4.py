@@ -132,6 +132,26 @@ def test_a_weight_larger_than_32_bit_offsets_of_its_entries(txl):
     assert (y[:, :-32] == 0).all() and torch.equal(y[:, -32:], alone)
 
 
+def test_refusals_of_the_binding(txl):
+    W = weights(64, 32).cuda()
+    w = txl.QuantWeight.quantise(W)
+    x = torch.zeros(70, 64, dtype=BF, device="cuda")
+    for args, kw, error in (((x[:, :32], w), {}, ValueError), ((x.float(), w), {}, TypeError), ((x.t(), w), {}, ValueError),
+                            ((x.cpu(), w), {}, ValueError), ((x, w, torch.zeros(70, 31, dtype=BF, device="cuda")), {}, ValueError),
+                            ((x, w), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), txl.TxlError if txl.linear_q4_workspace_size(70, w) else None),
+                            ((x, w), dict(err_flag=torch.zeros(1, device="cuda")), ValueError)):
+        if error:
+            with pytest.raises(error):
+                txl.linear_q4(*args, **kw)
+    for bad in (dict(group=16), dict(W=W.float()), dict(W=W.cpu()), dict(W=W.t())):
+        with pytest.raises((ValueError, TypeError)):
+            txl.QuantWeight.quantise(**{**dict(W=W, group=64), **bad})
+    with pytest.raises(ValueError):
+        txl.QuantWeight(w.data[:-1], 64, 32, 64)
+    with pytest.raises(ValueError):
+        w.expand(torch.zeros(64, 33, dtype=BF, device="cuda"))
+
+
 def test_not_finite_x(txl):
     x = torch.ones(3, 128, dtype=BF, device="cuda")
     x[1, 5] = math.inf

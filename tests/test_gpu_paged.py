@@ -266,6 +266,79 @@ def test_a_page_that_is_missing(txl):
     assert ((out.cpu().double() - want).abs() <= tol).all()
 
 
+def test_a_token_without_room_leaves_the_sequence(txl):
+    """One token a sequence, whose pages the kernel itself finds missing: outputs, lengths and weights as they were."""
+    from transformer_xl_relative_gb300 import native
+    for T in (1, 2):
+        ref = Pages(3, 2, 64, [31, 32, 5], 16, BF, room=0)        # (32 slots each)
+        q, k, v, u, vb, r = new(3, T, 2, 64, BF, 4, 60)
+        mem = ref.to_gpu(txl)
+        mem.table[2, 0] = -1
+        out = torch.full_like(q, 5.0)
+        before = mem.weight.clone()
+        txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 60, 59, out, accumulate=True)
+        with pytest.raises(txl.TxlError) as e:
+            mem.check()
+        assert e.value.status == native.TXL_ERR_PAGE
+        counts = torch.tensor([1 if T == 1 else 0, 0, 0])
+        ref.push(k.cpu(), v.cpu(), counts)
+        assert (out[1:] == 5).all()
+        assert torch.equal(mem.length.cpu(), ref.length) and torch.equal(mem.next_pos.cpu(), ref.next_pos)
+        if T == 1:
+            want, tol, got, got_tol = attend(ref, q.cpu(), u, vb, r, 59, counts)
+            assert ((out.cpu().double() - want).abs() <= tol)[0].all()
+            mine = ref.table[0].long()
+            w = mem.weight.cpu()[mine] - torch.where(ref.weight[mine] == 0, ref.weight[mine], before.cpu()[mine])
+            assert ((w - got[mine]).abs() <= got_tol[mine] + 2.0 ** -22 * (1 + got[mine])).all()
+        others = ref.table[1:].flatten().long()
+        assert torch.equal(mem.weight[others.cuda()], before[others.cuda()])
+
+
+def test_as_many_sequences_as_a_memory_holds(txl):
+    """B = 4096 at the widest head and most tokens: the blocks' shared memory at its largest."""
+    B, T = 4096, 16
+    ref = Pages(4, 1, 128, [20, 0, 33, 7], 16, BF, room=T)
+    q, k, v, u, vb, r = new(4, T, 1, 128, BF, 4, 60)
+    mem4 = ref.to_gpu(txl)
+    pick = torch.tensor([0, 1, 2, 3])
+    at = torch.tensor([0, 1000, 2222, 4095])
+    wide = lambda x: torch.zeros(B, *x.shape[1:], dtype=x.dtype, device="cuda").index_copy_(0, at.cuda(), x.cuda()[pick.cuda()])
+    mem = txl.PagedMemory(mem4.k, mem4.v, mem4.pos, mem4.weight, wide(ref.table), wide(ref.length), wide(ref.next_pos))
+    counts = torch.zeros(B, dtype=torch.int32)
+    counts[at] = T
+    out = torch.full((B, T, 1, 128), 5.0, dtype=BF, device="cuda")
+    txl.rel_attn_paged(wide(q), mem, wide(k), wide(v), u.cuda(), vb.cuda(), r.cuda(), 60, 59, out, counts=counts.cuda(), accumulate=True)
+    ref.push(k.cpu(), v.cpu())
+    want, tol, *_ = attend(ref, q.cpu(), u, vb, r, 59)
+    o = out.cpu()
+    assert ((o[at].double() - want).abs() <= tol).all()
+    idle = torch.ones(B, dtype=torch.bool)
+    idle[at] = False
+    assert (o[idle] == 5).all()
+    assert torch.equal(mem.length.cpu()[at], ref.length) and int(mem.length.sum()) == int(ref.length.sum())
+    mem.check()
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_infinite_keys_and_values_in_a_long_memory(txl, T):
+    """A seen infinite value in a pair of many parts, and a query that is not a number beside one that is."""
+    ref = Pages(2, 2, 64, [9000, 40], 64, BF, room=T)
+    p, row = ref.at(0, 4321)
+    ref.v[p, 1, row, 9] = -math.inf
+    q, k, v, u, vb, r = new(2, T, 2, 64, BF, 4, 60)
+    q[1, 0, 0, 5] = math.nan
+    mem = ref.to_gpu(txl)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 60, 59, out)
+    o = out.cpu().double()
+    assert (o[0, :, 1, 9] == -math.inf).all() and torch.isnan(o[1, 0, 0]).all()
+    ref.v[p, 1, row, 9] = 0.0
+    ref.push(k.cpu(), v.cpu())
+    want, tol, *_ = attend(ref, q.cpu(), u, vb, r, 59)
+    ok = torch.isfinite(o) & ~torch.isnan(want)
+    assert int((~ok).sum()) == T + 64 and ((o - want).abs() <= tol)[ok].all()
+
+
 def test_the_same_bits_every_time(txl):
     ref = Pages(5, 3, 64, [1000, 3, 2222, 0, 517], 16, BF, room=4)
     q, k, v, u, vb, r = new(5, 4, 3, 64, BF, 4, 600)
@@ -406,8 +479,70 @@ def test_generation_with_a_bounded_memory(txl):
             assert mem.free_pages == 40 - sum((int(n) + L - 1) // L for n in ref.length)
         assert torch.equal(mem.length.cpu(), ref.length) and torch.equal(mem.next_pos.cpu(), ref.next_pos)
     mem.check()
+    free = mem.free_pages
     mem.release(0)
-    assert mem.length.tolist()[0] == 0
+    assert mem.length.tolist()[0] == 0 and mem.free_pages > free and (mem.table[0] == -1).all()
+    with pytest.raises(ValueError):
+        mem.reserve(10 ** 6)
+    with pytest.raises(ValueError):
+        mem.reserve([1, 2])
+    with pytest.raises(ValueError):
+        mem.release(3)
+
+
+def test_shared_pages(txl):
+    """Two sequences read one prefix; the page that both have is free when both have gone."""
+    mem = txl.PagedMemory.empty(1, 6, 16, 2, 64)
+    _, k, v, *_ = new(1, 32, 2, 64, BF, 1, 1)
+    mem.reserve(32)
+    txl.paged_push(mem, k, v)
+    pages = mem.table[0, :2].tolist()
+    table = torch.tensor([pages + [5], pages + [-1]], dtype=torch.int32, device="cuda")
+    both = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table, mem.length.repeat(2), mem.next_pos.repeat(2))
+    assert both.free_pages == 3
+    q, kn, vn, u, vb, r = new(2, 1, 2, 64, BF, 2, 40)
+    q[1], kn[1], vn[1] = q[0], kn[0], vn[0]
+    both.reserve(1)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, both, kn, vn, u.cuda(), vb.cuda(), r.cuda(), 40, 39, out)
+    both.check()
+    assert torch.equal(out[0], out[1])
+    both.release(0)
+    assert both.free_pages == 3                              # (its own page; the other sequence took one)
+    both.release(1)
+    assert both.free_pages == 6
+
+
+def test_refusals_of_the_binding(txl):
+    mem = txl.PagedMemory.empty(2, 4, 16, 2, 64)
+    q, k, v, u, vb, r = new(2, 1, 2, 64, BF, 2, 40)
+    u, vb, r = u.cuda(), vb.cuda(), r.cuda()
+    out = torch.empty_like(q)
+    good = dict(q=q, mem=mem, k_new=k, v_new=v, u=u, v_bias=vb, r=r, n_rows=40, clamp_len=39, out=out)
+    for bad, error in ((dict(v_new=None), ValueError), (dict(k_new=k.float()), TypeError), (dict(q=q.float()), TypeError),
+                       (dict(u=u.double()), TypeError), (dict(u=u[:1]), ValueError), (dict(n_rows=41), ValueError),
+                       (dict(r=r[:, :1]), ValueError), (dict(out=out[:1]), ValueError), (dict(q=q.cpu()), ValueError),
+                       (dict(counts=torch.zeros(2, device="cuda")), ValueError),
+                       (dict(counts=torch.zeros(3, dtype=torch.int32, device="cuda")), ValueError),
+                       (dict(workspace=torch.empty(8, dtype=torch.uint8)), ValueError),
+                       (dict(q=q.transpose(1, 3), out=out.transpose(1, 3)), ValueError), (dict(clamp_len=-1), txl.TxlError),
+                       (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), txl.TxlError)):
+        with pytest.raises(error):
+            txl.rel_attn_paged(**{**good, **bad})
+    for bad, error in ((dict(k_new=k[:1], v_new=v[:1]), ValueError), (dict(v_new=v.float()), TypeError),
+                       (dict(k_new=k.cpu(), v_new=v.cpu()), ValueError),
+                       (dict(k_new=k.transpose(2, 3), v_new=v.transpose(2, 3)), ValueError)):
+        with pytest.raises(error):
+            txl.paged_push(**{**dict(mem=mem, k_new=k, v_new=v), **bad})
+    for keep, recent in ((0, 0), (3, 4), (3, -1)):
+        with pytest.raises(txl.TxlError):
+            txl.paged_evict(mem, keep, recent)
+    for kw in (dict(table=mem.table.long()), dict(length=mem.length[:1]), dict(pos=mem.pos[:, :8]), dict(weight=mem.pos)):
+        with pytest.raises(ValueError):
+            txl.PagedMemory(**{**dict(k=mem.k, v=mem.v, pos=mem.pos, weight=mem.weight, table=mem.table, length=mem.length,
+                                      next_pos=mem.next_pos), **kw})
+    mem.check()
+    assert mem.length.tolist() == [0, 0]
 
 
 def test_captured_and_replayed(txl):

@@ -653,10 +653,18 @@ class PagedMemory:
         if any(w > 0 for w in want):
             self._write_table()
 
+    def _give_back(self, b: int, kept: int) -> None:
+        """Sequence b keeps its first `kept` pages; the others are free (but for those it shares)."""
+        gone, self._rows[b] = self._rows[b][kept:], self._rows[b][:kept]
+        used = {p for row in self._rows for p in row} if gone else ()
+        self._free.extend(p for p in reversed(gone) if p not in used)
+
     def release(self, b: int) -> None:
         """Sequence b has ended: it is empty, and its pages are free."""
-        self._free.extend(reversed(self._rows[b]))
-        self._rows[b], self._room[b] = [], 0
+        if not 0 <= b < len(self._rows):
+            raise ValueError("the memory has %d sequences" % len(self._rows))
+        self._give_back(b, 0)
+        self._room[b] = 0
         self._write_table()
         with torch.cuda.device(self.device):
             self.length[b] = 0
@@ -666,10 +674,8 @@ class PagedMemory:
         """Frees the pages that hold no position (reads the lengths: waits for the device)."""
         self._room = self.length.tolist()
         L = self.page_len
-        for p, n in zip(self._rows, self._room):
-            keep = (n + L - 1) // L
-            self._free.extend(reversed(p[keep:]))
-            del p[keep:]
+        for b, n in enumerate(self._room):
+            self._give_back(b, (n + L - 1) // L)
         self._write_table()
 
     def check(self) -> None:
@@ -882,7 +888,7 @@ def linear_q4(X: torch.Tensor, w: QuantWeight, Y: torch.Tensor | None = None, wo
     if err_flag is not None and (err_flag.get_device() != dev or err_flag.dtype != torch.int32 or err_flag.numel() < 1):
         raise ValueError("err_flag must be an int32 on the weights' device")
     pw, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
-    args = native.Q4_ARGS.pack(w.address, px, ldx if m > 1 else k, py, ldy if m > 1 else n, pw, size,
+    args = native.Q4_ARGS.pack(w.address, px, ldx if m > 1 else (k + 7) // 8 * 8, py, ldy if m > 1 else n, pw, size,
                                err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev), m)
     check(_on_device(dev, _lib().txl_linear_q4_call, args), "txl_linear_q4")
     return Y

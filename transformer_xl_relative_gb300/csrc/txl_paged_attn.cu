@@ -630,65 +630,99 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
 #pragma unroll
             for (int j = 0; j < NJ; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
         }
+        // half a tile at a time: u / 2 is the warp's tile, u % 2 its half.  Keys, values and position terms are loaded one half
+        // ahead, positions two.
         Pages pages;
         pages.look(m, a, a.t0 + warp, lane);
-        for (int tile = a.t0 + warp; tile < a.t1; tile += kWarps) {
-            const int page = pages.get(m, a, tile, lane);
-            if (page < 0) continue;
-            const int row = tile * kPageUnit % m.page_len;
+        const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + kWarps - 1) / kWarps) : 0;
+        constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
+        auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * kWarps; };
+        auto load_kv = [&](int u, float4* k, float4* v) {
+            const int page = pages.get(m, a, tile_of(u), lane), slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
+            const bool held = page >= 0 && slot < a.len;
+            const int64_t at = held ? page_row0(m, page, a.h) + static_cast<int64_t>(slot % m.page_len) * m.ld : 0;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int slot = tile * kPageUnit + 8 * y + g;
-                const int64_t at = page_row0(m, page, a.h) + static_cast<int64_t>(row + 8 * y + g) * m.ld;
-                const int pos = m.pos[static_cast<int64_t>(page) * m.page_len + row + 8 * y + g];
-                float4 k[NJ], v[NJ];
+            for (int j = 0; j < NJ; ++j) {
+                const int d = 4 * (t + 4 * j);
+                k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (held && d < D) {
+                    k[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.k) + at + d);
+                    v[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.v) + at + d);
+                }
+            }
+        };
+        auto load_pos = [&](int u) {
+            const int page = pages.get(m, a, tile_of(u), lane), slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
+            return page >= 0 && slot < a.len ? m.pos[static_cast<int64_t>(page) * m.page_len + slot % m.page_len] : kAhead;
+        };
+        const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i0;
+        auto load_e = [&](int pos, float* e) {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                e[x] = i0 + x < a.n && pos <= a.first + i0 + x ? p.E[(er + x) * p.e_pitch + term(p, a.first + i0 + x, pos)] : kNone;
+        };
+        float4 k[NJ], v[NJ];
+        float e[NQ];
+        int pos = kAhead;
+        if (halves) {
+            load_kv(0, k, v);
+            load_e(load_pos(0), e);
+            pos = load_pos(1);
+        }
+        for (int u = 0; u < halves; ++u) {
+            float4 kn[NJ], vn[NJ];
+            float en[NQ];
+            if (u + 1 < halves) {
+                load_kv(u + 1, kn, vn);
+                load_e(pos, en);
+                if (u + 2 < halves) pos = load_pos(u + 2);
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int d = 4 * (t + 4 * j);
+                if (d + 1 >= D) k[j].y = 0.f;                  // a row's padding is anything
+                if (d + 2 >= D) k[j].z = 0.f;
+                if (d + 3 >= D) k[j].w = 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    const int d = 4 * (t + 4 * j);
-                    k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (slot < a.len && d < D) {
-                        k[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.k) + at + d);
-                        v[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.v) + at + d);
-                        if (d + 1 >= D) k[j].y = 0.f;          // a row's padding is anything
-                        if (d + 2 >= D) k[j].z = 0.f;
-                        if (d + 3 >= D) k[j].w = 0.f;
-                    }
+                    const float4 w = *reinterpret_cast<const float4*>(qs + x * p.Dp + 4 * (t + 4 * j));
+                    s = fmaf(w.w, k[j].w, fmaf(w.z, k[j].z, fmaf(w.y, k[j].y, fmaf(w.x, k[j].x, s))));
                 }
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                const bool seen = e[x] != kNone;
+                s = seen ? s + e[x] : kNone;
+                if (W && t == 0 && i0 + x < a.n) {
+                    const int slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
+                    if (slot < a.len) p.S[(er + x) * p.cap + slot] = s;
+                }
+                if (seen) {
+                    if (!(s <= mx[x])) {
+                        const float now = fmaxf(mx[x], s), f = exp2f(mx[x] - finite_or_0(now));
+                        mx[x] = now;
+                        sum[x] *= f;
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    const int i = i0 + x;
-                    float s = 0.f;
+                        for (int j = 0; j < NJ; ++j) { o[x][j][0] *= f; o[x][j][1] *= f; o[x][j][2] *= f; o[x][j][3] *= f; }
+                    }
+                    const float pr = exp2f(s - finite_or_0(mx[x]));
+                    sum[x] += pr;
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) {
-                        const float4 w = *reinterpret_cast<const float4*>(qs + x * p.Dp + 4 * (t + 4 * j));
-                        s = fmaf(w.w, k[j].w, fmaf(w.z, k[j].z, fmaf(w.y, k[j].y, fmaf(w.x, k[j].x, s))));
-                    }
-                    s += __shfl_xor_sync(0xffffffffu, s, 1);
-                    s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    const bool seen = i < a.n && slot < a.len && pos <= a.first + i;
-                    const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i;
-                    s = seen ? s + p.E[er * p.e_pitch + term(p, a.first + i, pos)] : kNone;
-                    if (W && t == 0 && i < a.n && slot < a.len) p.S[er * p.cap + slot] = s;
-                    if (seen) {
-                        if (!(s <= mx[x])) {
-                            const float now = fmaxf(mx[x], s), f = exp2f(mx[x] - finite_or_0(now));
-                            mx[x] = now;
-                            sum[x] *= f;
-#pragma unroll
-                            for (int j = 0; j < NJ; ++j) { o[x][j][0] *= f; o[x][j][1] *= f; o[x][j][2] *= f; o[x][j][3] *= f; }
-                        }
-                        const float pr = exp2f(s - finite_or_0(mx[x]));
-                        sum[x] += pr;
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            o[x][j][0] = fmaf(pr, v[j].x, o[x][j][0]);
-                            o[x][j][1] = fmaf(pr, v[j].y, o[x][j][1]);
-                            o[x][j][2] = fmaf(pr, v[j].z, o[x][j][2]);
-                            o[x][j][3] = fmaf(pr, v[j].w, o[x][j][3]);
-                        }
+                        o[x][j][0] = fmaf(pr, v[j].x, o[x][j][0]);
+                        o[x][j][1] = fmaf(pr, v[j].y, o[x][j][1]);
+                        o[x][j][2] = fmaf(pr, v[j].z, o[x][j][2]);
+                        o[x][j][3] = fmaf(pr, v[j].w, o[x][j][3]);
                     }
                 }
             }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) { k[j] = kn[j]; v[j] = vn[j]; }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) e[x] = en[x];
         }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
@@ -764,28 +798,39 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
         return terms ? x + E[distance] : x;
     };
     float top = kNone;
-    for (int s = threadIdx.x; s < keys; s += kThreads) top = fmaxf(top, score(s));
-    __syncthreads();
+    bool nan = false;
+    for (int s = threadIdx.x; s < keys; s += kThreads) {
+        const float x = score(s);
+        nan |= x != x;
+        top = fmaxf(top, x);
+    }
+    nan = __syncthreads_or(nan);
     tot[threadIdx.x] = top;
     __syncthreads();
     for (int x = 0; x < kThreads; ++x) top = fmaxf(top, tot[x]);
+    nan |= top == INFINITY;                                   // (infinity less itself)
     top = finite_or_0(top);
-    float sum = 0.f, o = 0.f;
+    float sum = nan ? __int_as_float(0x7fc00000) : 0.f, o = sum;
     const int d = threadIdx.x;                                // D <= 128: a channel a thread
-    for (int s0 = 0; s0 < keys; s0 += kThreads) {
-        const float x = score(s0 + threadIdx.x);
+    __shared__ const T* values[kThreads];
+    for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += kThreads) {
+        const int s = s0 + threadIdx.x;
+        const float x = score(s);
         __syncthreads();
-        tot[threadIdx.x] = x;
+        // (a key that is seen and scores -inf weighs 0 as well; its values count as unseen)
+        tot[threadIdx.x] = x == kNone ? 0.f : exp2f(x - top);
+        values[threadIdx.x] = x == kNone ? nullptr : row(s, true);
         __syncthreads();
-        for (int y = 0; y < min(kThreads, keys - s0); ++y) {
-            // (a key that is seen and scores -inf weighs 0 as well; its values count as unseen)
-            if (tot[y] == kNone) continue;
-            const float w = exp2f(tot[y] - top);
+#pragma unroll 8
+        for (int y = 0; y < kThreads; ++y) {
+            const T* v = values[y];
+            const float w = tot[y];
             sum += w;
-            if (d < m.D) o = fmaf(w, to_f(row(s0 + y, true)[d]), o);
+            if (v && d < m.D) o = fmaf(w, to_f(v[d]), o);
         }
     }
     if (d < m.D) out_row<T>(p, a, i)[d] = from_f<T>(sum == 0.f ? 0.f : o / sum);
+    __syncthreads();
 }
 
 // The four warps' shares of a part joined: into the output where the part is the whole pair, else into the workspace;
@@ -909,7 +954,7 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
 }
 
 // Blocks of the attention that an SM holds: what registers (bf16: the rings) of the variants leave room for.
-template <typename T, int NC, int NQ> constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 ? (NC <= 2 ? 4 : 3) : 2) : NC <= 2 && NQ <= 2 ? 4 : NC <= 2 ? 3 : 2;
+template <typename T, int NC, int NQ> constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2) : NC <= 2 && NQ <= 2 ? 4 : NC <= 2 ? 3 : 2;
 
 // Floats between the warps' sums in shared memory (bf16: in their rings).
 template <typename T, int NC>
@@ -1100,7 +1145,7 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
     const PagedParams& m = p.n.m;
     const size_t smem = 4 * (static_cast<size_t>(kWarps) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
                              static_cast<size_t>(kWarps + 1) * 2 * p.n.T + 2) + 8 * (3 * static_cast<size_t>(m.B) + 2);
-    cudaError_t e = allow_smem(once, 200 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
+    cudaError_t e = allow_smem(once, 224 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
     if (e != cudaSuccess) return e;
     if (!ONE) {
         // a block copies a few hundred units of 16 bytes
