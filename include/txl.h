@@ -686,8 +686,8 @@ size_t txl_paged_evict_workspace_size(const txl_paged* mem);
  *     c    = the integer nearest to (w - lo) / step, ties to even (0 where step = 0)
  * and stand for w' = lo + step c (differences and quotients in double precision).  A group with a NaN or an infinity, or
  * whose step is not finite, stands for NaN throughout.
- *   data : device, 16-byte aligned, txl_q4_bytes(k, n, group) bytes: the codes as the kernels' lanes read them (16 columns
- *          by 64 k in 512 bytes), then the groups' parameters.
+ *   data : device, 16-byte aligned, txl_q4_bytes(k, n, group) bytes: the codes as the kernels' lanes read them (64 columns
+ *          by 64 k in 2 KB), then the groups' parameters.
  */
 typedef struct {
     void* data;
@@ -707,7 +707,7 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
 /*
  * txl_linear_q4 -- Y = X W' for bf16 X [m][ld_x] (columns 0 .. k-1 are read) and 4-bit weights: txl_linear with a quarter
  * of the weights' bytes, for the projections of a generated token.  Y bf16 [m][ld_y], columns 0 .. n-1 are written.
- * Up to 64 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
+ * Up to 128 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
  * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry of x that is not finite makes its row of
  * Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
  *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
@@ -732,7 +732,7 @@ typedef struct {
 } txl_linear_q4_args;
 txl_status txl_linear_q4_call(const txl_linear_q4_args* args);
 
-/* Bytes of device workspace txl_linear_q4 needs: 0 for m <= 64, else 2 k (n rounded up to a multiple of 8). */
+/* Bytes of device workspace txl_linear_q4 needs: 0 for m <= 128, else 2 k (n rounded up to a multiple of 8). */
 size_t txl_linear_q4_workspace_size(int m, const txl_q4* w);
 
 /*

@@ -113,9 +113,9 @@ def test_workspaces_of_shapes_that_are_refused(native):
 
 def test_four_bit_weights(native):
     lib = native.load()
-    assert lib.txl_q4_bytes(64, 16, 64) == 512 + 64
-    assert lib.txl_q4_bytes(410, 1230, 64) == 77 * 7 * 512 + 77 * 7 * 64
-    assert lib.txl_q4_bytes(65, 17, 32) == 2 * 2 * 512 + 2 * 3 * 64
+    assert lib.txl_q4_bytes(64, 64, 64) == 2048 + 256
+    assert lib.txl_q4_bytes(410, 1230, 64) == 20 * 7 * 2048 + 20 * 7 * 256
+    assert lib.txl_q4_bytes(65, 65, 32) == 2 * 2 * 2048 + 2 * 3 * 256
     for k, n, g in ((0, 1, 64), (1, 0, 64), (1, 1, 16), (1, 1, 0), ((1 << 21) + 1, 1, 64), (1, (1 << 21) + 1, 64)):
         assert lib.txl_q4_bytes(k, n, g) == 0
         w = native.TxlQ4(FAKE, k, n, g)
@@ -128,11 +128,11 @@ def test_four_bit_weights(native):
     assert call(w=native.TxlQ4(None, 64, 32, 64)) == native.TXL_ERR_INVALID_ARG
     assert call(w=native.TxlQ4(FAKE + 8, 64, 32, 64)) == native.TXL_ERR_ALIGNMENT
     assert call(X=FAKE + 1) == native.TXL_ERR_ALIGNMENT and call(m=(1 << 19) + 1) == native.TXL_ERR_UNSUPPORTED
-    assert lib.txl_linear_q4_workspace_size(64, ctypes.byref(w)) == 0
-    need = lib.txl_linear_q4_workspace_size(65, ctypes.byref(w))
+    assert lib.txl_linear_q4_workspace_size(128, ctypes.byref(w)) == 0
+    need = lib.txl_linear_q4_workspace_size(129, ctypes.byref(w))
     assert need == 64 * 32 * 2
-    assert call(m=65) == native.TXL_ERR_WORKSPACE and call(m=65, ws=FAKE, size=need - 1) == native.TXL_ERR_WORKSPACE
-    assert call(m=65, ws=FAKE + 2, size=need) == native.TXL_ERR_ALIGNMENT
+    assert call(m=129) == native.TXL_ERR_WORKSPACE and call(m=129, ws=FAKE, size=need - 1) == native.TXL_ERR_WORKSPACE
+    assert call(m=129, ws=FAKE + 2, size=need) == native.TXL_ERR_ALIGNMENT
     assert lib.txl_q4_quantise(ctypes.byref(w), FAKE, 31, None) == native.TXL_ERR_INVALID_ARG
     assert lib.txl_q4_quantise(ctypes.byref(w), FAKE + 1, 32, None) == native.TXL_ERR_ALIGNMENT
     assert lib.txl_q4_expand(ctypes.byref(w), None, 32, None) == native.TXL_ERR_INVALID_ARG

@@ -1383,7 +1383,7 @@ txl_status check_q4(const txl_q4* w)
 uint4* q4_codes(const txl_q4* w) { return static_cast<uint4*>(w->data); }
 uint32_t* q4_par(const txl_q4* w)
 {
-    return reinterpret_cast<uint32_t*>(static_cast<char*>(w->data) + static_cast<size_t>((w->n + 15) / 16) * ((w->k + 63) / 64) * 512);
+    return reinterpret_cast<uint32_t*>(static_cast<char*>(w->data) + static_cast<size_t>((w->n + 63) / 64) * ((w->k + 63) / 64) * 2048);
 }
 
 Q4WeightParams q4_params(const txl_q4* w, void* W, int64_t ld_w)
@@ -1498,8 +1498,8 @@ txl_status txl_paged_evict(const txl_paged* mem, int keep, int recent, void* wor
 size_t txl_q4_bytes(int k, int n, int group)
 {
     if (k < 1 || n < 1 || k > (1 << 21) || n > (1 << 21) || (group != 32 && group != 64 && group != 128)) return 0;
-    const size_t tiles = static_cast<size_t>((n + 15) / 16);
-    return tiles * ((k + 63) / 64) * 512 + tiles * ((k + group - 1) / group) * 64;
+    const size_t blocks = static_cast<size_t>((n + 63) / 64);         // of four tiles of 16 columns
+    return blocks * ((k + 63) / 64) * 2048 + blocks * ((k + group - 1) / group) * 256;
 }
 
 txl_status txl_q4_quantise(const txl_q4* w, const void* W, int64_t ld_w, void* stream)

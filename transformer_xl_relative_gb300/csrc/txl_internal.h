@@ -405,12 +405,12 @@ struct PagedEvictParams {
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sm_count, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights
-constexpr int kQ4MaxRows = 64;      // rows of X up to which they are multiplied with the codes as they are
+constexpr int kQ4MaxRows = 128;     // rows of X up to which they are multiplied with the codes as they are
 
 struct LinearQ4Params {
     const void* x; int64_t ld_x;                // bf16 [m][ld_x]
-    const uint4* codes;                         // [ceil(n/16)][ceil(k/64)][32 lanes]
-    const uint32_t* par;                        // [ceil(n/16)][groups][16]: step | lo << 16, bf16
+    const uint4* codes;                         // [ceil(n/64)][ceil(k/64)][4 tiles of 16 columns][32 lanes]
+    const uint32_t* par;                        // [ceil(n/64)][groups][4][16]: step | lo << 16, bf16
     void* y; int64_t ld_y;
     int m, n, k, group;
     int vec_x;                                  // rows of x start on 16-byte boundaries

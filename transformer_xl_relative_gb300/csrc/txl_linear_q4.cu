@@ -15,7 +15,18 @@ namespace {
 // A block of codes: 16 columns of W (rows of an mma's A) by 64 k.  Lane (g, t) holds 32 codes: word s (0..3) those of a k16
 // step, k = 32 (s / 2) + 8 t + 4 (s % 2) + 0..3, so that a lane's x are two pieces of 16 bytes and a step stays within 32 k.
 // Nibble j of a word and nibble j + 4 are a pair of A's register j: column g + 8 (j % 2), k + 2 (j / 2) and the next.
+// Blocks of four neighbouring tiles of columns and one block of k follow one another, and so do the parameters of four tiles and a
+// group, so that a block of threads reads pieces of up to 2 KB.
 constexpr int kQ4K = 64, kQ4N = 16;
+
+__device__ __forceinline__ int64_t code_block(int nt, int kb, int kb_all)        // in 512 bytes
+{
+    return (static_cast<int64_t>(nt >> 2) * kb_all + kb) * 4 + (nt & 3);
+}
+__device__ __forceinline__ int64_t par_block(int nt, int group, int groups)      // in 16 words
+{
+    return (static_cast<int64_t>(nt >> 2) * groups + group) * 4 + (nt & 3);
+}
 constexpr int kExpandThreads = 256;
 
 
@@ -33,8 +44,13 @@ __device__ __forceinline__ uint4 load_x8(const uint16_t* row, int k, int k_end)
     return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
-// 128 + c as bf16 pairs: a code is the low bits of the mantissa.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u; }
+// 128 + c as bf16 pairs: a code is the low bits of the mantissa.  One instruction, with both constants in registers.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j, uint32_t mask, uint32_t base)
+{
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w >> (4 * j)), "r"(mask), "r"(base));      // (w & mask) | base
+    return x;
+}
 
 // D = A B without an accumulator to add to.
 __device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -50,7 +66,7 @@ __device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, ui
 constexpr int kQ4Stages = 4, kQ4MaxWarps = 16;
 template <int NT, int MT, int SUB> struct Q4Stage {
     uint4 w[NT][32], x[MT][2][32];
-    uint32_t par[NT][SUB][16];
+    uint32_t par[SUB][NT][16];
 };
 template <int NT, int MT, int SUB> constexpr int kQ4Ring = kQ4Stages * static_cast<int>(sizeof(Q4Stage<NT, MT, SUB>));
 
@@ -70,7 +86,7 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, g = lane >> 2, t = lane & 3;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
-    const int nt_all = (p.n + kQ4N - 1) / kQ4N, nt0 = blockIdx.x * NT;
+    const int nt0 = blockIdx.x * NT;
     const int shift = p.group == 128 ? 1 : 0;
     const int row0 = blockIdx.y * 8 * MT, rows = min(8 * MT, p.m - row0);
     Stage* ring = reinterpret_cast<Stage*>(smem) + warp * kQ4Stages;
@@ -81,17 +97,16 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
         x[a] = static_cast<const uint16_t*>(p.x) + (row0 + min(8 * a + g, rows - 1)) * p.ld_x + 8 * t;
         live[a] = 8 * a + g < rows ? 16 : 0;
     }
-    // what a lane copies: its codes of every tile, its x, and (the first 4 NT SUB lanes) 16 bytes of one tile's parameters
-    const uint4* codes[NT];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) codes[b] = p.codes + static_cast<int64_t>(min(nt0 + b, nt_all - 1)) * kb_all * 32 + lane;
-    const int par_tile = lane / (4 * SUB), par_sub = lane / 4 % SUB;
-    const uint32_t* par = p.par + static_cast<int64_t>(min(nt0 + par_tile, nt_all - 1)) * groups * 16 + 4 * t;
-    const uint32_t at = smem_u32(ring) + 16 * lane, par_at = smem_u32(&ring[0].par[0][0][0]) + 16 * lane;
+    // what a lane copies: its codes of every tile (NT tiles lie in one block of four), its x, and (the first 4 NT SUB lanes) 16
+    // bytes of one tile's parameters
+    const uint4* codes = p.codes + code_block(nt0, 0, kb_all) * 32 + lane;
+    const int par_tile = lane / 4 % NT, par_sub = lane / (4 * NT);
+    const uint32_t* par = p.par + par_block(nt0 + par_tile, 0, groups) * 16 + 4 * t;
+    const uint32_t at = smem_u32(ring) + 16 * lane, par_at = smem_u32(&ring[0].par[0][0][0]) + 16 * lane;    // (par: [SUB][NT][16])
     auto load = [&](int kb, int stage) {
         const uint32_t dst = at + stage * static_cast<int>(sizeof(Stage));
 #pragma unroll
-        for (int b = 0; b < NT; ++b) copy16(dst + 512 * b, codes[b] + kb * 32, 16);
+        for (int b = 0; b < NT; ++b) copy16(dst + 512 * b, codes + kb * 128 + 32 * b, 16);
         const int k = kb * kQ4K;
 #pragma unroll
         for (int a = 0; a < MT; ++a)
@@ -107,11 +122,14 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
                     ring[stage].x[a][h][lane] = load_x8(x[a], k + 32 * h, p.k - 8 * t);
                 }
             }
-        if (par_tile < NT)
-            copy16(par_at + stage * static_cast<int>(sizeof(Stage)), par + (SUB == 2 ? min(2 * kb + par_sub, groups - 1) : kb >> shift) * 16, 16);
+        if (par_sub < SUB)
+            copy16(par_at + stage * static_cast<int>(sizeof(Stage)), par + (SUB == 2 ? min(2 * kb + par_sub, groups - 1) : kb >> shift) * 64, 16);
     };
     float tot[NT][MT][4] = {};
     constexpr uint32_t kOnes = 0x3f803f80u;
+    uint32_t mask, base;
+    asm volatile("mov.u32 %0, 0x000f000f;" : "=r"(mask));
+    asm volatile("mov.u32 %0, 0x43004300;" : "=r"(base));
     auto multiply = [&](const Stage& q) {
         uint4 wv[NT], xv[MT][2];
 #pragma unroll
@@ -136,7 +154,8 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
                     const uint32_t w = step == 0 ? wv[b].x : step == 1 ? wv[b].y : step == 2 ? wv[b].z : wv[b].w;
-                    const uint32_t a0 = code_pair(w, 0), a1 = code_pair(w, 1), a2 = code_pair(w, 2), a3 = code_pair(w, 3);
+                    const uint32_t a0 = code_pair(w, 0, mask, base), a1 = code_pair(w, 1, mask, base),
+                                   a2 = code_pair(w, 2, mask, base), a3 = code_pair(w, 3, mask, base);
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
                         if (i == 0) mma_first(c[b][a], a0, a1, a2, a3, b0[a], b1[a]);
@@ -148,7 +167,7 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t both = q.par[b][s][g + 8 * r];
+                    const uint32_t both = q.par[s][b][g + 8 * r];
                     const float step = mma::bf16_lo(both), lo = fmaf(-128.f, step, mma::bf16_hi(both));
 #pragma unroll
                     for (int a = 0; a < MT; ++a)
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
         if (bad || !isfinite(s)) s = a = __uint_as_float(0x7fc00000u);
         step[gr][c] = s;
         lo[gr][c] = a;
-        p.par[(static_cast<int64_t>(nt) * groups + k0 / p.group + gr) * 16 + c] = __float_as_uint(s) >> 16 | (__float_as_uint(a) & 0xffff0000u);
+        p.par[par_block(nt, k0 / p.group + gr, groups) * 16 + c] = __float_as_uint(s) >> 16 | (__float_as_uint(a) & 0xffff0000u);
     }
     __syncthreads();
     for (int i = tid; i < kWK / kQ4K * 128; i += kWThreads) {
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
             const float q = (x[k][c] - a) / d, half = fabsf(q - floorf(q) - 0.5f);
             w |= static_cast<uint32_t>(half > 0x1p-17f ? rintf(q) : static_cast<float>(rint((static_cast<double>(x[k][c]) - a) / d))) << (4 * j);
         }
-        reinterpret_cast<uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + k0 / kQ4K + kb) * 32 + lane)[s] = w;
+        reinterpret_cast<uint32_t*>(p.codes + code_block(nt, k0 / kQ4K + kb, kb_all) * 32 + lane)[s] = w;
     }
 }
 
@@ -263,9 +282,9 @@ __global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_
     for (int i = tid; i < 4 * 128; i += kExpandThreads) {
         const int nt = n0 / kQ4N + i / 128, lane = i % 128 / 4, s = i % 4, g = lane >> 2, t = lane & 3;
         if (nt * kQ4N >= p.n) continue;
-        const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + (static_cast<int64_t>(nt) * kb_all + kb) * 32 + lane)[s];
+        const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + code_block(nt, kb, kb_all) * 32 + lane)[s];
         const int k = 32 * (s >> 1) + 8 * t + 4 * (s & 1), gr = min((kb * kQ4K + k) / p.group, groups - 1);
-        const uint32_t* q = p.par + (static_cast<int64_t>(nt) * groups + gr) * 16 + g;
+        const uint32_t* q = p.par + par_block(nt, gr, groups) * 16 + g;
         const uint32_t par[2] = {q[0], q[8]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -318,7 +337,8 @@ cudaError_t launch_linear_q4(const LinearQ4Params& p, int sm_count, cudaStream_t
 
 cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s)
 {
-    return launch_dependent(q4_quantise_kernel, dim3((p.n + kQ4N - 1) / kQ4N, (p.k + kWK - 1) / kWK), dim3(kWThreads), 0, s, p);
+    // (tiles past n fill the last block of four)
+    return launch_dependent(q4_quantise_kernel, dim3((p.n + 63) / 64 * 4, (p.k + kWK - 1) / kWK), dim3(kWThreads), 0, s, p);
 }
 
 cudaError_t launch_q4_expand(const Q4WeightParams& p, cudaStream_t s)
