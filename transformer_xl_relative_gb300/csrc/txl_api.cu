@@ -1432,7 +1432,7 @@ txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* a)
     const bool pushes = a->k_new.ptr || a->v_new.ptr;
     if (a->T < 0 || a->clamp_len < 0 || a->n_rows < 1 || !a->u || !a->v_bias || !a->r || a->ld_r < m->D) return TXL_ERR_INVALID_ARG;
     if (pushes && (!a->k_new.ptr || !a->v_new.ptr)) return TXL_ERR_INVALID_ARG;
-    if (a->T > kDecodeMaxL) return TXL_ERR_UNSUPPORTED;
+    if (a->T > kDecodeMaxL || a->ld_r > INT32_MAX / m->H) return TXL_ERR_UNSUPPORTED;
     if (m->B == 0 || a->T == 0) return TXL_OK;
     if (!a->q.ptr || !a->out.ptr) return TXL_ERR_INVALID_ARG;
     const int elem = m->dtype == TXL_F32 ? 4 : 2;

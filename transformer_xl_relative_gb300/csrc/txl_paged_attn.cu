@@ -218,22 +218,32 @@ struct Part {
     bool own;                      // the pair has a new key that is not among the slots (k_new, position `first`)
 };
 
-// Page of the tiles that a warp will come to: lane x knows that of the warp's x-th tile from `base` on.
-struct Pages {
-    int base, mine;
+// Where the tiles that a warp will come to lie: lane x knows that of the warp's x-th tile from `base` on (a page's number
+// and the row in it take divisions, which are made once in 32 tiles).
+struct Tiles {
+    int base, mine;                // first position of the tile in m.pos, or -1 where there is no page
+    int64_t mine_kv;               // and its first element of the part's head in m.k and m.v
+
     __device__ __forceinline__ void look(const PagedParams& m, const Part& a, int tile, int lane)
     {
         base = tile;
         const int at = tile + kWarps * lane;
         const bool used = at < a.t1 && at * kPageUnit < a.len;
-        mine = used ? page_of(m, a.b, at * kPageUnit) : -1;
-        if (used && mine < 0) page_error(m);
+        const int page = used ? page_of(m, a.b, at * kPageUnit) : -1, row = at * kPageUnit % m.page_len;
+        if (used && page < 0) page_error(m);
+        mine = page < 0 ? -1 : page * m.page_len + row;
+        mine_kv = page < 0 ? -1 : page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld;
     }
-    // page of `tile` (a warp's own, at or after base)
-    __device__ __forceinline__ int get(const PagedParams& m, const Part& a, int tile, int lane)
+    // of `tile` (a warp's own; no later one was asked for)
+    __device__ __forceinline__ int pos(const PagedParams& m, const Part& a, int tile, int lane)
     {
         if (tile - base >= 32 * kWarps) look(m, a, tile, lane);
         return __shfl_sync(0xffffffffu, mine, (tile - base) / kWarps);
+    }
+    __device__ __forceinline__ int64_t kv(const PagedParams& m, const Part& a, int tile, int lane)
+    {
+        if (tile - base >= 32 * kWarps) look(m, a, tile, lane);
+        return __shfl_sync(0xffffffffu, mine_kv, (tile - base) / kWarps);
     }
 };
 
@@ -392,24 +402,35 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     const int T = p.n.T;
     const uint32_t stage0 = smem_u32(ring);
 
-    // a lane's pieces of a tile: of the rows of K and V, units of 16 bytes (a unit wholly past D is never copied, and zero
-    // from the start)
-    constexpr int kUnits = 4 * NC, kPieces = kPageUnit * kUnits / 32;
-    const int units = (m.D + 7) / 8;
-    auto copy = [&](int page, int tile, int stage) {
-        const int row0 = tile * kPageUnit % m.page_len;
-        const int64_t at = page < 0 ? 0 : page_row0(m, page, a.h) + static_cast<int64_t>(row0) * m.ld;
-        const uint16_t* k = static_cast<const uint16_t*>(m.k) + at;
-        const uint16_t* v = static_cast<const uint16_t*>(m.v) + at;
-        const int rows = page < 0 ? 0 : a.len - tile * kPageUnit;          // that hold something
-        const uint32_t dst = stage0 + stage * kStage<NC>;
+    // a lane's pieces of a tile: a unit of 16 bytes of every kSide-th row of K and of V (a unit wholly past D is never copied, and
+    // zero from the start)
+    constexpr int kUnits = 4 * NC, kSide = 32 / kUnits, kPieces = kPageUnit / kSide;
+    const int units = (m.D + 7) / 8, my_row = lane / kUnits, my_unit = lane % kUnits;
+    const bool copies = my_row < kSide && my_unit < units;
+    const int bytes = min(16, 2 * (m.D - 8 * my_unit)), from = 2 * (my_row * m.ld + 8 * my_unit), step = 2 * kSide * m.ld;
+    const uint32_t into = stage0 + my_row * kPitch<NC> + 16 * my_unit;
+    auto copy = [&](int64_t at, int tile, int stage) {
+        if (!copies) return;
+        const int rows = at < 0 ? 0 : a.len - tile * kPageUnit;            // that hold something
+        const int64_t off = 2 * max(at, static_cast<int64_t>(0));
+        const char* k = static_cast<const char*>(m.k) + off;
+        const char* v = static_cast<const char*>(m.v) + off;
+        const uint32_t dst = into + stage * kStage<NC>;
+        if (rows >= kPageUnit) {
+            k += from;
+            v += from;
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-            const int x = lane + 32 * j, row = x / kUnits, c = x % kUnits;
-            if (c >= units) continue;
-            const int bytes = row < rows ? min(16, 2 * (m.D - 8 * c)) : 0, off = row < rows ? row * m.ld + 8 * c : 0;
-            copy16(dst + row * kPitch<NC> + 16 * c, k + off, bytes);
-            copy16(dst + (kPageUnit + row) * kPitch<NC> + 16 * c, v + off, bytes);
+            for (int j = 0; j < kPieces; ++j) {
+                copy16(dst + j * kSide * kPitch<NC>, k + j * step, bytes);
+                copy16(dst + (kPageUnit + j * kSide) * kPitch<NC>, v + j * step, bytes);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const bool held = my_row + j * kSide < rows;
+                copy16(dst + j * kSide * kPitch<NC>, held ? k + from + j * step : k, held ? bytes : 0);
+                copy16(dst + (kPageUnit + j * kSide) * kPitch<NC>, held ? v + from + j * step : v, held ? bytes : 0);
+            }
         }
     };
     // what hangs on nothing is loaded first, then the pages, then what they lead to
@@ -419,8 +440,8 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     const bool owner = ONE && a.own && a.t1 == a.tiles && warp == kWarps - 1;
     if constexpr (ONE)
         if (owner) own_key.load(p, a, lane);
-    Pages pages;
-    pages.look(m, a, a.t0 + warp, lane);
+    Tiles tiles;
+    tiles.look(m, a, a.t0 + warp, lane);
     if (units < kUnits) {
         for (int x = lane; x < kStages<NC> * 2 * kPageUnit * (kUnits - units); x += 32) {
             const int row = x / (kUnits - units), c = units + x % (kUnits - units);
@@ -431,18 +452,18 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
 #pragma unroll
     for (int x = 0; x < kStages<NC> - 1; ++x) {
         const int tile = first + x * kWarps;
-        if (tile < a.t1) copy(pages.get(m, a, tile, lane), tile, x);
+        if (tile < a.t1) copy(tiles.kv(m, a, tile, lane), tile, x);
         mma::cp_async_commit();
     }
     // positions of keys g and g + 8, two tiles ahead (a slot that holds nothing is ahead of every query)
     constexpr int kAhead = 0x7fffffff;
     int pos[2];
-    auto load_pos = [&](int page, int tile) {
-        const int* at = m.pos + static_cast<int64_t>(max(page, 0)) * m.page_len + tile * kPageUnit % m.page_len + g;
+    auto load_pos = [&](int tile) {
+        const int at = tiles.pos(m, a, tile, lane);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) pos[y] = page >= 0 && tile * kPageUnit + 8 * y + g < a.len ? at[8 * y] : kAhead;
+        for (int y = 0; y < 2; ++y) pos[y] = at >= 0 && tile * kPageUnit + 8 * y + g < a.len ? m.pos[at + 8 * y + g] : kAhead;
     };
-    if (first < a.t1) load_pos(pages.get(m, a, first, lane), first);
+    if (first < a.t1) load_pos(first);
     queries.store(qs);
     if constexpr (ONE)
         if (owner) own_key.store(p, a, lane, own, bml + 2 * kWarps);
@@ -458,10 +479,17 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         E[x] = ONE ? nullptr : p.E + ((static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1)) * p.e_pitch;
     }
     const uint16_t* r = static_cast<const uint16_t*>(p.r) + a.h * p.r_head;
+    const int r_row = static_cast<int>(p.r_row);
+    const bool whole_rows = p.vec_r && m.D == 32 * NC;
     auto load_row = [&](int distance, uint4* w) {
-        const uint16_t* row = r + static_cast<int64_t>(distance) * p.r_row;
+        const uint16_t* row = r + static_cast<int64_t>(distance) * r_row;
+        if (whole_rows) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) w[j] = row_unit(row, 8 * (t + 4 * j), m.D, p.vec_r);
+            for (int j = 0; j < NC; ++j) w[j] = *reinterpret_cast<const uint4*>(row + 8 * t + 32 * j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) w[j] = row_unit(row, 8 * (t + 4 * j), m.D, p.vec_r);
+        }
     };
     auto load_terms = [&]() {
 #pragma unroll
@@ -480,7 +508,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     };
     if (first < a.t1) {
         load_terms();
-        if (first + kWarps < a.t1) load_pos(pages.get(m, a, first + kWarps, lane), first + kWarps);
+        if (first + kWarps < a.t1) load_pos(first + kWarps);
     }
     __syncthreads();
 
@@ -510,7 +538,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         __syncwarp();                                          // everyone's pieces are here, and the last stage is read
         if (tile + (kStages<NC> - 1) * kWarps < a.t1) {
             const int to = tile + (kStages<NC> - 1) * kWarps;
-            copy(pages.get(m, a, to, lane), to, ahead);
+            copy(tiles.kv(m, a, to, lane), to, ahead);
         }
         mma::cp_async_commit();
         ahead = stage;
@@ -539,7 +567,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
             for (int y = 0; y < 2; ++y) s[x][y] = e[x][y] == kNone ? kNone : c[x][2 * y] + c[x][2 * y + 1] + e[x][y];
         if (tile + kWarps < a.t1) {
             load_terms();
-            if (tile + 2 * kWarps < a.t1) load_pos(pages.get(m, a, tile + 2 * kWarps, lane), tile + 2 * kWarps);
+            if (tile + 2 * kWarps < a.t1) load_pos(tile + 2 * kWarps);
         }
         // the maximum follows only where a score is far above it: a weight may be up to 2^kSlack
         constexpr float kSlack = 8.f;
@@ -632,15 +660,16 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
         }
         // half a tile at a time: u / 2 is the warp's tile, u % 2 its half.  Keys, values and position terms are loaded one half
         // ahead, positions two.
-        Pages pages;
-        pages.look(m, a, a.t0 + warp, lane);
+        Tiles tiles;
+        tiles.look(m, a, a.t0 + warp, lane);
         const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + kWarps - 1) / kWarps) : 0;
         constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
         auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * kWarps; };
         auto load_kv = [&](int u, float4* k, float4* v) {
-            const int page = pages.get(m, a, tile_of(u), lane), slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
-            const bool held = page >= 0 && slot < a.len;
-            const int64_t at = held ? page_row0(m, page, a.h) + static_cast<int64_t>(slot % m.page_len) * m.ld : 0;
+            const int row = u % 2 * 8 + g, slot = tile_of(u) * kPageUnit + row;
+            const int64_t tile_at = tiles.kv(m, a, tile_of(u), lane);
+            const bool held = tile_at >= 0 && slot < a.len;
+            const int64_t at = held ? tile_at + row * m.ld : 0;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const int d = 4 * (t + 4 * j);
@@ -652,8 +681,8 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
             }
         };
         auto load_pos = [&](int u) {
-            const int page = pages.get(m, a, tile_of(u), lane), slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
-            return page >= 0 && slot < a.len ? m.pos[static_cast<int64_t>(page) * m.page_len + slot % m.page_len] : kAhead;
+            const int at = tiles.pos(m, a, tile_of(u), lane), row = u % 2 * 8 + g;
+            return at >= 0 && tile_of(u) * kPageUnit + row < a.len ? m.pos[at + row] : kAhead;
         };
         const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i0;
         auto load_e = [&](int pos, float* e) {
