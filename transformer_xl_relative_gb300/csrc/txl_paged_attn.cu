@@ -220,14 +220,14 @@ struct Part {
 
 // Where the tiles that a warp will come to lie: lane x knows that of the warp's x-th tile from `base` on (a page's number
 // and the row in it take divisions, which are made once in 32 tiles).
-struct Tiles {
+template <int NW> struct Tiles {
     int base, mine;                // first position of the tile in m.pos, or -1 where there is no page
     int64_t mine_kv;               // and its first element of the part's head in m.k and m.v
 
     __device__ __forceinline__ void look(const PagedParams& m, const Part& a, int tile, int lane)
     {
         base = tile;
-        const int at = tile + kWarps * lane;
+        const int at = tile + NW * lane;
         const bool used = at < a.t1 && at * kPageUnit < a.len;
         const int page = used ? page_of(m, a.b, at * kPageUnit) : -1, row = at * kPageUnit % m.page_len;
         if (used && page < 0) page_error(m);
@@ -237,13 +237,13 @@ struct Tiles {
     // of `tile` (a warp's own; no later one was asked for)
     __device__ __forceinline__ int pos(const PagedParams& m, const Part& a, int tile, int lane)
     {
-        if (tile - base >= 32 * kWarps) look(m, a, tile, lane);
-        return __shfl_sync(0xffffffffu, mine, (tile - base) / kWarps);
+        if (tile - base >= 32 * NW) look(m, a, tile, lane);
+        return __shfl_sync(0xffffffffu, mine, (tile - base) / NW);
     }
     __device__ __forceinline__ int64_t kv(const PagedParams& m, const Part& a, int tile, int lane)
     {
-        if (tile - base >= 32 * kWarps) look(m, a, tile, lane);
-        return __shfl_sync(0xffffffffu, mine_kv, (tile - base) / kWarps);
+        if (tile - base >= 32 * NW) look(m, a, tile, lane);
+        return __shfl_sync(0xffffffffu, mine_kv, (tile - base) / NW);
     }
 };
 
@@ -255,10 +255,10 @@ __device__ __forceinline__ int term(const PagedAttnParams& p, int at, int pos)
 
 __device__ __forceinline__ float finite_or_0(float m) { return m == kNone ? 0.f : m; }
 
-// bf16.  A warp takes every fourth tile of 16 keys through its own ring of stages in shared memory: asynchronous copies
+// bf16.  A warp takes every NW-th tile of 16 keys through its own ring of stages in shared memory: asynchronous copies
 // of 16 bytes, one or two tiles ahead.  What lies past a sequence's last slot, or past D, arrives as zeros.  Rows are an odd
 // number of 16-byte units apart, so that the eight rows of an ldmatrix lie in different banks.
-template <int NC> constexpr int kStages = NC == 2 ? 2 : 3;              // (four blocks of two stages on an SM, not three of three)
+template <int NC> constexpr int kStages = NC == 1 ? 3 : 2;              // (a third stage gains nothing: 16 warps of an SM copy)
 template <int NC> constexpr int kPitch = (4 * NC + 1) * 16;               // bytes
 template <int NC> constexpr int kStage = 2 * kPageUnit * kPitch<NC>;      // K and V of a tile
 template <int NC> constexpr int kWarpBytes = kStages<NC> * kStage<NC>;
@@ -291,8 +291,8 @@ template <int NC> constexpr int kQPitch = 32 * NC + 8;
 template <int NC, int NQ, bool ONE> constexpr int kQRows = ONE ? 16 : 8 * NQ;
 
 // The elements that a thread puts there: loaded before anything that waits, stored later.
-template <int NC, int NQ, bool ONE> struct Queries {
-    static constexpr int kWidth = 32 * NC, kRows = ONE ? 2 : 4 * NQ, kEach = (kRows * kWidth + kThreads - 1) / kThreads;
+template <int NC, int NQ, bool ONE, int NW> struct Queries {
+    static constexpr int kWidth = 32 * NC, kRows = ONE ? 2 : 4 * NQ, kEach = (kRows * kWidth + 32 * NW - 1) / (32 * NW);
     float y[kEach];
 
     __device__ __forceinline__ void load(const PagedAttnParams& p, const Part& a)
@@ -300,7 +300,7 @@ template <int NC, int NQ, bool ONE> struct Queries {
         const PagedParams& m = p.n.m;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int x = threadIdx.x + e * kThreads, row = x / kWidth, d = x % kWidth, i = ONE ? 0 : row;
+            const int x = threadIdx.x + e * (32 * NW), row = x / kWidth, d = x % kWidth, i = ONE ? 0 : row;
             y[e] = 0.f;
             if (row < kRows && i < a.n && d < m.D)
                 y[e] = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d]) +
@@ -311,7 +311,7 @@ template <int NC, int NQ, bool ONE> struct Queries {
     {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int x = threadIdx.x + e * kThreads, row = ONE ? x / kWidth * 8 : x / kWidth * 2, d = x % kWidth;
+            const int x = threadIdx.x + e * (32 * NW), row = ONE ? x / kWidth * 8 : x / kWidth * 2, d = x % kWidth;
             if (x >= kRows * kWidth) continue;
             const __nv_bfloat16 hi = __float2bfloat16_rn(y[e]);
             qs[row * kQPitch<NC> + d] = __bfloat16_as_ushort(hi);
@@ -394,7 +394,7 @@ template <int NC, bool W> struct OwnKey {
     }
 };
 
-template <int NC, int NQ, bool ONE, bool W>
+template <int NC, int NQ, bool ONE, bool W, int NW>
 __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& a, char* ring, float* bml, float* own, uint16_t* qs)
 {
     const PagedParams& m = p.n.m;
@@ -434,13 +434,13 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         }
     };
     // what hangs on nothing is loaded first, then the pages, then what they lead to
-    Queries<NC, NQ, ONE> queries;
+    Queries<NC, NQ, ONE, NW> queries;
     queries.load(p, a);
     OwnKey<NC, W> own_key;
-    const bool owner = ONE && a.own && a.t1 == a.tiles && warp == kWarps - 1;
+    const bool owner = ONE && a.own && a.t1 == a.tiles && warp == NW - 1;
     if constexpr (ONE)
         if (owner) own_key.load(p, a, lane);
-    Tiles tiles;
+    Tiles<NW> tiles;
     tiles.look(m, a, a.t0 + warp, lane);
     if (units < kUnits) {
         for (int x = lane; x < kStages<NC> * 2 * kPageUnit * (kUnits - units); x += 32) {
@@ -451,7 +451,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     const int first = a.t0 + warp;
 #pragma unroll
     for (int x = 0; x < kStages<NC> - 1; ++x) {
-        const int tile = first + x * kWarps;
+        const int tile = first + x * NW;
         if (tile < a.t1) copy(tiles.kv(m, a, tile, lane), tile, x);
         mma::cp_async_commit();
     }
@@ -466,7 +466,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     if (first < a.t1) load_pos(first);
     queries.store(qs);
     if constexpr (ONE)
-        if (owner) own_key.store(p, a, lane, own, bml + 2 * kWarps);
+        if (owner) own_key.store(p, a, lane, own, bml + 2 * NW);
 
     // what a tile's position terms come from, one tile ahead: which keys a lane's query sees, E's terms (e) or r's rows (rw)
     float e[NQ][2];
@@ -508,7 +508,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     };
     if (first < a.t1) {
         load_terms();
-        if (first + kWarps < a.t1) load_pos(first + kWarps);
+        if (first + NW < a.t1) load_pos(first + NW);
     }
     __syncthreads();
 
@@ -533,11 +533,11 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     const uint32_t k_at = stage0 + (lane & 15) * kPitch<NC> + (lane >> 4) * 16;
     const uint32_t v_at = stage0 + (kPageUnit + (lane & 7) + (lane >> 4) * 8) * kPitch<NC> + ((lane >> 3) & 1) * 16;
     int stage = 0, ahead = kStages<NC> - 1;
-    for (int tile = first; tile < a.t1; tile += kWarps) {
+    for (int tile = first; tile < a.t1; tile += NW) {
         copies_wait<kStages<NC> - 2>();
         __syncwarp();                                          // everyone's pieces are here, and the last stage is read
-        if (tile + (kStages<NC> - 1) * kWarps < a.t1) {
-            const int to = tile + (kStages<NC> - 1) * kWarps;
+        if (tile + (kStages<NC> - 1) * NW < a.t1) {
+            const int to = tile + (kStages<NC> - 1) * NW;
             copy(tiles.kv(m, a, to, lane), to, ahead);
         }
         mma::cp_async_commit();
@@ -565,9 +565,9 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         for (int x = 0; x < NQ; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) s[x][y] = e[x][y] == kNone ? kNone : c[x][2 * y] + c[x][2 * y + 1] + e[x][y];
-        if (tile + kWarps < a.t1) {
+        if (tile + NW < a.t1) {
             load_terms();
-            if (tile + 2 * kWarps < a.t1) load_pos(tile + 2 * kWarps);
+            if (tile + 2 * NW < a.t1) load_pos(tile + 2 * NW);
         }
         // the maximum follows only where a score is far above it: a weight may be up to 2^kSlack
         constexpr float kSlack = 8.f;
@@ -636,7 +636,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
 
 // fp32, CUDA cores.  Lane (g, t) takes keys g and g + 8 of a tile and channels 4 (t + 4 j) .. + 3; each of the eight g keeps
 // maximum and sums of its own, which meet at the end.  NQ queries at a time: their sums stay in registers.
-template <int NC, int NQ, bool W>
+template <int NC, int NQ, bool W, int NW>
 __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a, float* buf, int share, float* bml, float* qs)
 {
     constexpr int NJ = 2 * NC;             // chunks of four channels of a lane
@@ -645,7 +645,7 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
     const int T = p.n.T, D = m.D;
     for (int i0 = 0; i0 < a.n; i0 += NQ) {
         __syncthreads();
-        for (int x = threadIdx.x; x < NQ * p.Dp; x += kThreads) {
+        for (int x = threadIdx.x; x < NQ * p.Dp; x += (32 * NW)) {
             const int i = i0 + x / p.Dp, d = x % p.Dp;
             qs[x] = i < a.n && d < D ? (static_cast<const float*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d] + p.u[a.h * D + d]) * p.qscale : 0.f;
         }
@@ -660,11 +660,11 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
         }
         // half a tile at a time: u / 2 is the warp's tile, u % 2 its half.  Keys, values and position terms are loaded one half
         // ahead, positions two.
-        Tiles tiles;
+        Tiles<NW> tiles;
         tiles.look(m, a, a.t0 + warp, lane);
-        const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + kWarps - 1) / kWarps) : 0;
+        const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + NW - 1) / NW) : 0;
         constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
-        auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * kWarps; };
+        auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * NW; };
         auto load_kv = [&](int u, float4* k, float4* v) {
             const int row = u % 2 * 8 + g, slot = tile_of(u) * kPageUnit + row;
             const int64_t tile_at = tiles.kv(m, a, tile_of(u), lane);
@@ -795,8 +795,8 @@ template <typename T> __device__ __forceinline__ T* out_row(const PagedAttnParam
 }
 
 // One query's row again, key by key on the CUDA cores: its sums are not finite, and a value that is not finite at a key
-// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: kThreads floats.
-template <typename T>
+// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: (32 * NW) floats.
+template <typename T, int NW>
 __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, bool terms, float* tot)
 {
     const PagedParams& m = p.n.m;
@@ -828,7 +828,7 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     };
     float top = kNone;
     bool nan = false;
-    for (int s = threadIdx.x; s < keys; s += kThreads) {
+    for (int s = threadIdx.x; s < keys; s += (32 * NW)) {
         const float x = score(s);
         nan |= x != x;
         top = fmaxf(top, x);
@@ -836,13 +836,13 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     nan = __syncthreads_or(nan);
     tot[threadIdx.x] = top;
     __syncthreads();
-    for (int x = 0; x < kThreads; ++x) top = fmaxf(top, tot[x]);
+    for (int x = 0; x < (32 * NW); ++x) top = fmaxf(top, tot[x]);
     nan |= top == INFINITY;                                   // (infinity less itself)
     top = finite_or_0(top);
     float sum = nan ? __int_as_float(0x7fc00000) : 0.f, o = sum;
     const int d = threadIdx.x;                                // D <= 128: a channel a thread
-    __shared__ const T* values[kThreads];
-    for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += kThreads) {
+    __shared__ const T* values[(32 * NW)];
+    for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += (32 * NW)) {
         const int s = s0 + threadIdx.x;
         const float x = score(s);
         __syncthreads();
@@ -851,7 +851,7 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
         values[threadIdx.x] = x == kNone ? nullptr : row(s, true);
         __syncthreads();
 #pragma unroll 8
-        for (int y = 0; y < kThreads; ++y) {
+        for (int y = 0; y < (32 * NW); ++y) {
             const T* v = values[y];
             const float w = tot[y];
             sum += w;
@@ -862,10 +862,10 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     __syncthreads();
 }
 
-// The four warps' shares of a part joined: into the output where the part is the whole pair, else into the workspace;
+// The warps' shares of a part joined: into the output where the part is the whole pair, else into the workspace;
 // the last block of a pair joins the parts.  buf: the warps' sums [T][Dp], `pitch` apart, and (a new key's) own[D]; bml:
-// their maxima and weights [kWarps + 1][T][2].  The tickets are zero before and after the call.
-template <typename T, bool ONE, bool W>
+// their maxima and weights [NW + 1][T][2].  The tickets are zero before and after the call.
+template <typename T, bool ONE, bool W, int NW>
 __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, float* buf, int pitch, const float* own, float* bml)
 {
     __shared__ int last, again;
@@ -877,24 +877,24 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
     const bool whole = a.t0 == 0 && a.t1 == a.tiles;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (a.t0 == 0 ? 1 : 0);
     // (unused rows of buf hold what was there; only queries i < n are touched)
-    for (int x = tid; x < a.n * D; x += kThreads) {
+    for (int x = tid; x < a.n * D; x += (32 * NW)) {
         const int i = x / D, d = x - i * D;
         float top = kNone;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, bml[(w * Tq + i) * 2]);
-        if (with_own) top = fmaxf(top, bml[2 * kWarps]);
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, bml[(w * Tq + i) * 2]);
+        if (with_own) top = fmaxf(top, bml[2 * NW]);
         const float base = finite_or_0(top);
         float y = 0.f, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = exp2f(bml[(w * Tq + i) * 2] - base);
             y = fmaf(f, buf[w * pitch + i * p.Dp + d], y);
             l = fmaf(f, bml[(w * Tq + i) * 2 + 1], l);
         }
-        if (with_own && bml[2 * kWarps] != kNone) {
-            const float f = exp2f(bml[2 * kWarps] - base);
+        if (with_own && bml[2 * NW] != kNone) {
+            const float f = exp2f(bml[2 * NW] - base);
             y = fmaf(f, own[d], y);
-            l = fmaf(f, bml[2 * kWarps + 1], l);
+            l = fmaf(f, bml[2 * NW + 1], l);
         }
         if (whole && room) {
             const float v = l == 0.f ? 0.f : y / l;
@@ -922,9 +922,9 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
         if (last && room) {
             const int warp = tid >> 5, lane = tid & 31;
             auto slot_of = [&](int c) { return 2 * (a.first_block + c) + (c == 0 ? 1 : 0); };
-            // one query: every warp takes each fourth part; more: a warp takes a query
-            const int step = a.n == 1 ? kWarps : 1;
-            for (int i = a.n == 1 ? 0 : warp; i < a.n; i += kWarps) {
+            // one query: the warps share the parts; more: a warp takes a query
+            const int step = a.n == 1 ? NW : 1;
+            for (int i = a.n == 1 ? 0 : warp; i < a.n; i += NW) {
                 // the maximum of all parts first
                 float top = kNone;
                 for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(p.ml + (slot_of(c) * Tq + i) * 2));
@@ -958,12 +958,15 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
                         if (32 * k + lane < D) buf[warp * p.Dp + 32 * k + lane] = y[k];
                     if (lane == 0) bml[warp] = l;
                     __syncthreads();
-                    l = bml[0] + bml[1] + bml[2] + bml[3];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (32 * k + lane < D)
-                            y[k] = buf[32 * k + lane] + buf[p.Dp + 32 * k + lane] + buf[2 * p.Dp + 32 * k + lane] + buf[3 * p.Dp + 32 * k + lane];
                     if (warp) break;
+                    l = 0.f;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        l += bml[w];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (32 * k + lane < D) y[k] = w ? y[k] + buf[w * p.Dp + 32 * k + lane] : buf[32 * k + lane];
+                    }
                 }
                 bool finite = isfinite(l);
 #pragma unroll
@@ -978,12 +981,16 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
         }
     }
     __syncthreads();
-    for (int bits = again; bits; bits &= bits - 1) row_again<T>(p, a, __ffs(bits) - 1, !ONE, buf);
+    for (int bits = again; bits; bits &= bits - 1) row_again<T, NW>(p, a, __ffs(bits) - 1, !ONE, buf);
     __syncthreads();
 }
 
+// Warps of a block: four, or eight where registers leave room for two blocks of four at most (five drafted tokens of d_head 128:
+// 24.9 us against 28.5 with two blocks of four; one token of d_head 64: 31.9 against 30.6 with four blocks).
+template <typename T, int NC, int NQ> constexpr int kWarpsOf = sizeof(T) == 2 && (NC > 2 || NQ > 2) ? 8 : 4;
 // Blocks of the attention that an SM holds: what registers (bf16: the rings) of the variants leave room for.
-template <typename T, int NC, int NQ> constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2) : NC <= 2 && NQ <= 2 ? 4 : NC <= 2 ? 3 : 2;
+template <typename T, int NC, int NQ>
+constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2) : kWarpsOf<T, NC, NQ> == 8 ? 1 : 4;
 
 // Floats between the warps' sums in shared memory (bf16: in their rings).
 template <typename T, int NC>
@@ -1007,31 +1014,32 @@ __device__ __forceinline__ int4 now_of(const PagedAttnParams& p, int b)
 }
 
 // Shared memory: the warps' rings or sums; a new key's values; queries; maxima and weights; where the
-// sequences' pairs begin [B + 1] (64 bits, padded to an even number); what the sequences' entries of p.now are [B].
+// sequences' pairs begin [B + 1] (64 bits); the sequences' lengths and first positions [B].
 template <typename T, int NC, int NQ, bool ONE, bool W>
-__global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
+__global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ>)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
 {
+    constexpr int NW = kWarpsOf<T, NC, NQ>;
     extern __shared__ __align__(16) float buf[];
-    __shared__ int64_t scan[kWarps];
+    __shared__ int64_t scan[NW];
     const PagedParams& m = p.n.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pitch = warp_floats<T, NC>(p.n.T, p.Dp);
-    float* beside = buf + kWarps * pitch;
+    float* beside = buf + NW * pitch;
     float* bml = beside + beside_floats<T, NC, NQ, ONE>(p.Dp);
-    int64_t* start = reinterpret_cast<int64_t*>(bml + ((kWarps + 1) * p.n.T * 2 + 3) / 4 * 4);
-    int4* info = reinterpret_cast<int4*>(start + m.B + 2 - m.B % 2);
+    int64_t* start = reinterpret_cast<int64_t*>(bml + ((NW + 1) * p.n.T * 2 + 3) / 4 * 4);
+    int2* info = reinterpret_cast<int2*>(start + m.B + 1);
     // (no early launch of the next grid: blocks of the weights' kernel that wait would take the place of later blocks)
     pdl_wait();
 
     // start[b]: the work of all pairs of the sequences before b (an empty memory counts as a tile)
     int64_t done = 0;
-    for (int b0 = 0; b0 < m.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < m.B; b0 += (32 * NW)) {
         const int b = b0 + tid;
         int64_t x = 0;
         if (b < m.B) {
             const int4 now = ONE ? now_of(p, b) : p.now[b];
             x = now.z > 0 ? static_cast<int64_t>(kHead + max(1, (now.x + kPageUnit - 1) / kPageUnit)) * m.H : 0;
-            info[b] = now;
+            info[b] = make_int2(now.x, now.y);
             // prepared: the new positions count from now on (nothing here reads the memory's own numbers)
             if (!ONE && blockIdx.x == 0 && p.n.xk && now.z > 0) {
                 m.length[b] = now.x;
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
         int64_t before = done;
         for (int w = 0; w < warp; ++w) before += scan[w];
         if (b < m.B) start[b] = before + s - x;
-        for (int w = 0; w < kWarps; ++w) done += scan[w];
+        for (int w = 0; w < NW; ++w) done += scan[w];
         __syncthreads();
     }
     if (tid == 0) start[m.B] = done;
@@ -1057,15 +1065,15 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
     // ONE: the last block that has read the lengths advances them at its end (the ticket's answer is not waited for before)
     const bool counts = ONE && (p.n.xk || W);
     int ticket = -1;
-    if (counts && tid == kThreads - 1)
+    if (counts && tid == 32 * NW - 1)
         asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;" : "=r"(ticket) : "l"(m.scratch + m.B) : "memory");
     auto advance = [&] {
-        if (!counts || warp != kWarps - 1) return;
+        if (!counts || warp != NW - 1) return;
         const bool last = ticket == static_cast<int>(gridDim.x) - 1;
         if (!__any_sync(0xffffffffu, last)) return;
         if (last) m.scratch[m.B] = 0;
         for (int b = lane; b < m.B; b += 32) {
-            int4 now = info[b];
+            int4 now = make_int4(info[b].x, info[b].y, start[b + 1] > start[b] ? 1 : 0, 0);
             if (p.n.xk && now.z > 0) {
                 if (page_of(m, b, now.x) < 0) {
                     now.z = 0;
@@ -1080,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
     if constexpr (ONE) {
         // (the rows of queries that one token does not have)
         uint32_t* rows = reinterpret_cast<uint32_t*>(beside + p.Dp);
-        for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += kThreads) rows[x] = 0;
+        for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += (32 * NW)) rows[x] = 0;
     }
     __syncthreads();
     const int share = max(kMinTiles, quotient(done + gridDim.x - 1, gridDim.x));
@@ -1101,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
         a.b = b;
         a.len = info[b].x;
         a.first = info[b].y;
-        a.n = info[b].z;
+        a.n = ONE ? 1 : p.now[b].z;
         a.own = ONE && p.n.xk;
         a.room = !a.own || page_of(m, b, a.len) >= 0;
         a.tiles = max(1, (a.len + kPageUnit - 1) / kPageUnit);
@@ -1121,10 +1129,10 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, NC, NQ>)) paged_attn_ker
         }
         at = min(end, begin + size);
         if (a.t0 >= a.t1) continue;
-        if constexpr (sizeof(T) == 4) part_f32<NC, NQ, W>(p, a, buf, pitch, bml, beside);
-        else part_bf16<NC, NQ, ONE, W>(p, a, reinterpret_cast<char*>(buf + warp * pitch), bml, beside,
+        if constexpr (sizeof(T) == 4) part_f32<NC, NQ, W, NW>(p, a, buf, pitch, bml, beside);
+        else part_bf16<NC, NQ, ONE, W, NW>(p, a, reinterpret_cast<char*>(buf + warp * pitch), bml, beside,
                                        reinterpret_cast<uint16_t*>(beside + (ONE ? p.Dp : 0)));
-        join<T, ONE, W>(p, a, buf, pitch, beside, bml);
+        join<T, ONE, W, NW>(p, a, buf, pitch, beside, bml);
     }
     advance();
 }
@@ -1186,10 +1194,11 @@ cudaError_t launch_weights(const PagedAttnParams& p, int sm_count, cudaStream_t 
 template <typename T, int NC, int NQ, bool ONE>
 cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
+    constexpr int NW = kWarpsOf<T, NC, NQ>;
     static OncePerDevice once;
     const PagedParams& m = p.n.m;
-    const size_t smem = 4 * (static_cast<size_t>(kWarps) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
-                             static_cast<size_t>(kWarps + 1) * 2 * p.n.T + 2) + 8 * (3 * static_cast<size_t>(m.B) + 2);
+    const size_t smem = 4 * (static_cast<size_t>(NW) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
+                             static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1);
     cudaError_t e = allow_smem(once, 224 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
     if (e != cudaSuccess) return e;
     if (!ONE) {
@@ -1205,8 +1214,8 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
     // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its static part besides
     const int per_sm = max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (smem + 1024 + 64))));
     const int blocks = min(per_sm * sm_count, kPagedMaxCtas);
-    if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, false>, dim3(blocks), dim3(kThreads), smem, s, p);
-    e = launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, true>, dim3(blocks), dim3(kThreads), smem, s, p);
+    if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, false>, dim3(blocks), dim3(32 * NW), smem, s, p);
+    e = launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, true>, dim3(blocks), dim3(32 * NW), smem, s, p);
     if (e != cudaSuccess) return e;
     // four slots a lane where that leaves every SM two blocks (32 sequences of up to 4096 slots: 5.6 us a call less), else one (four
     // sequences of up to 2048, 80 rows each: 2.2 us less)
