@@ -62,6 +62,24 @@ constexpr int kEvictHeld = 8192;           // keys of a block that shared memory
 constexpr int kEvictRanks = 8;             // blocks of a sequence, at most
 constexpr int kEvictEach = 2048;           // slots that are worth a block
 
+// Integers of another block of the cluster.
+__device__ __forceinline__ int4 ld_rank4(const int* p, uint32_t rank)
+{
+    uint32_t a;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ int2 ld_rank2(const int* p, uint32_t rank)
+{
+    uint32_t a;
+    int2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
 // Exclusive sum over the block, and the total (every thread calls; 1024 threads).
 __device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total)
 {
@@ -89,13 +107,13 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total)
 // A cluster of blocks per sequence, each with a range of its slots: which slots leave (a selection by digits of the key,
 // from the top, over the sum of the blocks' histograms), then which survivors behind slot `keep` fill which holes in front.
 // Shared memory: the histograms of this digit and the next, the keys.
-__global__ void __launch_bounds__(kEvictThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p, int held)
+__global__ void __launch_bounds__(kEvictThreads, 1) paged_select_kernel(const __grid_constant__ PagedEvictParams p, int held)
 {
     extern __shared__ __align__(16) uint64_t keys[];
     int* bins = reinterpret_cast<int*>(keys + held);                          // [2][kBins]
     __shared__ int sums[32];
     __shared__ int found[3];
-    __shared__ int counts[2];                                                 // holes, movers of this block
+    __shared__ __align__(8) int counts[2];                                    // holes, movers of this block
     pdl_wait();
     pdl_launch_dependents();
     const PagedParams& m = p.m;
@@ -150,15 +168,24 @@ __global__ void __launch_bounds__(kEvictThreads) paged_select_kernel(const __gri
         if (ranks > 1) cluster_sync_all();
         else __syncthreads();
         turn ^= 1;
-        constexpr int kPer = kBins / kEvictThreads;
-        int c[kPer], sum = 0, total;
+        // four bins a thread, of all blocks' histograms (loaded together)
+        constexpr int kPer = 4;
+        static_assert(kBins == kPer * kEvictThreads / 2, "the first half of the threads takes the bins");
+        int c[kPer] = {}, sum = 0, total;
+        if (tid < kBins / kPer) {
+            int4 other[kEvictRanks];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            c[i] = 0;
-            for (int r = 0; r < ranks; ++r)
-                c[i] += ranks > 1 ? __float_as_int(ld_rank(reinterpret_cast<const float*>(own + tid * kPer + i), r)) : own[tid * kPer + i];
-            sum += c[i];
-            if (shift != 64) bins[turn * kBins + tid * kPer + i] = 0;          // (all blocks have read that one)
+            for (int r = 0; r < kEvictRanks; ++r)
+                other[r] = r >= ranks ? make_int4(0, 0, 0, 0) : ranks > 1 ? ld_rank4(own + tid * kPer, r) : reinterpret_cast<const int4*>(own)[tid];
+#pragma unroll
+            for (int r = 0; r < kEvictRanks; ++r) {
+                c[0] += other[r].x;
+                c[1] += other[r].y;
+                c[2] += other[r].z;
+                c[3] += other[r].w;
+            }
+            sum = c[0] + c[1] + c[2] + c[3];
+            if (shift != 64) reinterpret_cast<int4*>(bins + turn * kBins)[tid] = make_int4(0, 0, 0, 0);      // (all blocks have read that one)
         }
         int below = block_scan(sum, sums, total);
         if (total < want) want = total;                                       // (positions that are not distinct)
@@ -197,10 +224,12 @@ __global__ void __launch_bounds__(kEvictThreads) paged_select_kernel(const __gri
     int total_holes = all_holes, total_movers = all_movers;
     if (ranks > 1) {
         cluster_sync_all();
+        const int lane = tid & 31;
+        const int2 theirs = lane < ranks ? ld_rank2(counts, lane) : make_int2(0, 0);
         total_holes = total_movers = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const int h = __float_as_int(ld_rank(reinterpret_cast<const float*>(counts), r));
-            const int v = __float_as_int(ld_rank(reinterpret_cast<const float*>(counts + 1), r));
+#pragma unroll
+        for (int r = 0; r < kEvictRanks; ++r) {
+            const int h = __shfl_sync(0xffffffffu, theirs.x, r), v = __shfl_sync(0xffffffffu, theirs.y, r);
             if (r < rank) { holes += h; movers += v; }
             total_holes += h;
             total_movers += v;
