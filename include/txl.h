@@ -586,7 +586,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
  *              positions of a sequence leaves that sequence as it was, and its queries' outputs too.
  * Calls on one memory must not overlap on the GPU (one stream, or ordered streams), and no tensor that a call writes may
  * overlap one that it reads.
- * Limits (TXL_ERR_UNSUPPORTED): D <= 128; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
+ * Limits (TXL_ERR_UNSUPPORTED): D <= 128; ld <= 65536; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
  * max_pages * page_len below 2^31.  Positions are ints.
  */
 typedef struct {
@@ -632,7 +632,7 @@ txl_status txl_paged_push_call(const txl_paged_push_args* args);
  *   s_ij  = scale * ( q_i.k_j + q_i.r[delta] + u_h.k_j + v_h.r[delta] )
  *   out_i = sum_j softmax_j(s_ij over visible j) * v_j       (0 where nothing is visible)
  * Rows i >= counts[b] of out are left as they were (and those of q not read).
- *   u, v_bias, r, ld_r, scale : as txl_rel_attn_fwd;  n_rows >= 1 rows of r.
+ *   u, v_bias, r, ld_r, scale : as txl_rel_attn_fwd;  n_rows >= 1 rows of r (no more than 2^30 distances, H * ld_r below 2^31).
  *   accumulate : not 0: weight[j] += sum over heads and queries of softmax_j(s_ij), for txl_paged_evict (a slot's weight
  *              is the sum over the calls since it entered).
  *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_paged_workspace_size bytes (TXL_ERR_WORKSPACE).

@@ -180,6 +180,30 @@ def test_captured_on_another_stream_with_a_workspace(txl):
     assert torch.equal(all_, check_product(txl, 150, 128, 64, 64, x=x, W=W)[5:])
 
 
+def test_the_readmes_token_step(txl):
+    """The README's step runs over many tokens, and its memory stays within its bound."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md"), encoding="utf-8").read()
+    code = [c for c in re.findall(r"```python\n(.*?)```", text, re.S) if "def token_step" in c]
+    assert len(code) == 1
+    scope = {}
+    exec(code[0], scope)
+    B, H, D, d_model, keep = 3, 2, 32, 64, 40
+    g = torch.Generator().manual_seed(0)
+    w_qkv, w_o = (txl.QuantWeight.quantise(torch.randn(*s, generator=g).mul(0.1).to(BF).cuda()) for s in ((d_model, 3 * H * D), (H * D, d_model)))
+    u, vb = torch.zeros(H, D, device="cuda"), torch.zeros(H, D, device="cuda")
+    r = torch.randn(200, H, D, generator=g).to(BF).cuda()
+    mem = txl.PagedMemory.empty(B, 30, 16, H, D)
+    for t in range(150):
+        h = torch.randn(B, d_model, generator=g).to(BF).cuda()
+        y = scope["token_step"](h, mem, w_qkv, w_o, u, vb, r, 199, keep)
+        assert y.shape == h.shape
+    mem.check()
+    assert torch.isfinite(y.float()).all() and mem.next_pos.tolist() == [150] * B and max(mem.reserved) < keep + 64
+    assert mem.length.tolist() == mem.reserved
+
+
 def test_a_generated_tokens_layer_step(txl):
     """4-bit projections around the paged attention, against the same in 64 bits from the layer's rounded parts."""
     B, H, D, d_model, n_rows = 3, 4, 32, 128, 80

@@ -131,6 +131,25 @@ def test_push_without_room_leaves_the_sequence(txl):
     check_memory(mem, ref)
 
 
+@pytest.mark.parametrize("T", [1, 2])
+def test_every_bit_enters(txl, T):
+    """A push copies bits: the payloads of NaN and the sign of zero too, and rows end in zeros."""
+    ref = Pages(1, 2, 41, [20], 16, BF, room=T)
+    mem = ref.to_gpu(txl)
+    bits = (torch.arange(T * 2 * 41, dtype=torch.int32) * 37 % 65536 - 32768).to(torch.int16)
+    bits[::3] = torch.tensor([0x7fc1, 0x7f81, -1, -32768] * 100, dtype=torch.int16)[: len(bits[::3])]
+    k = bits.view(BF).view(1, T, 2, 41).cuda()
+    q, _, v, u, vb, r = new(1, T, 2, 41, BF, 1, 30)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 30, 29, out)
+    for t in range(T):
+        p, row = ref.at(0, 20 + t)
+        assert torch.equal(mem.k[p, :, row].cpu().view(torch.int16), k[0, t].cpu().view(torch.int16))
+        assert torch.equal(mem.v[p, :, row].cpu().view(torch.int16), v[0, t].cpu().view(torch.int16))
+        whole = torch.as_strided(mem.k, (*mem.k.shape[:3], 48), mem.k.stride())
+        assert (whole[p, :, row, 41:] == 0).all()
+
+
 # ------------------------------------------------------------------------------------ attention
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("D", [1, 8, 31, 32, 41, 64, 80, 96, 128])

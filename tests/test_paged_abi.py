@@ -35,7 +35,7 @@ BAD_MEMORIES = [
     (dict(dtype=2), "INVALID_ARG"), (dict(k=None), "INVALID_ARG"), (dict(weight=None), "INVALID_ARG"),
     (dict(table=None), "INVALID_ARG"), (dict(length=None), "INVALID_ARG"), (dict(scratch=None), "INVALID_ARG"),
     (dict(D=129, ld=136), "UNSUPPORTED"), (dict(page_len=24), "UNSUPPORTED"), (dict(B=4097), "UNSUPPORTED"),
-    (dict(H=65536), "UNSUPPORTED"), (dict(n_pages=1 << 28), "UNSUPPORTED"), (dict(max_pages=1 << 28), "UNSUPPORTED"),
+    (dict(H=65536), "UNSUPPORTED"), (dict(ld=65544), "UNSUPPORTED"), (dict(n_pages=1 << 28), "UNSUPPORTED"), (dict(max_pages=1 << 28), "UNSUPPORTED"),
     (dict(ld=44), "ALIGNMENT"), (dict(k=FAKE + 8), "ALIGNMENT"), (dict(pos=FAKE + 4), "ALIGNMENT"),
     (dict(length=FAKE + 2), "ALIGNMENT"), (dict(err_flag=FAKE + 1), "ALIGNMENT"),
 ]
@@ -82,12 +82,14 @@ def test_calls_that_are_refused(native):
     invalid, unsupported, alignment, workspace = (status(native, n) for n in ("INVALID_ARG", "UNSUPPORTED", "ALIGNMENT",
                                                                               "WORKSPACE"))
     assert push(native, None) == invalid and push(native, mem, T=-1) == invalid and push(native, mem, k=None) == invalid
-    assert push(native, mem, counts=FAKE + 2) == alignment
+    assert push(native, mem, counts=FAKE + 2) == alignment and push(native, mem, k=FAKE + 1) == alignment
+    assert push(native, paged(native, dtype=0, ld=44), v=FAKE + 2) == alignment
     for kw in (dict(T=-1), dict(clamp=-1), dict(n_rows=0), dict(q=0), dict(out=0), dict(k=0), dict(v=0), dict(u=0),
                dict(vb=0), dict(r=0), dict(ld_r=40)):
         assert attn(native, mem, **kw) == invalid, kw
     assert attn(native, None) == invalid
-    assert attn(native, mem, T=17) == unsupported
+    assert attn(native, mem, T=17) == unsupported and attn(native, mem, ld_r=1 << 30) == unsupported
+    assert attn(native, mem, n_rows=(1 << 31) - 1, clamp=(1 << 31) - 1) == unsupported
     for kw in (dict(q=FAKE + 1), dict(r=FAKE + 1), dict(u=FAKE + 2), dict(counts=FAKE + 1), dict(ws=FAKE + 8)):
         assert attn(native, mem, **kw) == alignment, kw
     need = native.load().txl_rel_attn_paged_workspace_size(ctypes.byref(mem), 2, 6, 0)
@@ -147,3 +149,12 @@ def test_the_binding_refuses_what_is_not_on_a_device(native):
         txl.QuantWeight.quantise(torch.zeros(64, 64, dtype=torch.bfloat16))
     with pytest.raises(TypeError):
         txl.QuantWeight.quantise(torch.zeros(64, 64))
+
+
+def test_what_an_earlier_kernel_may_write_is_not_read_through_the_read_only_path():
+    """The kernels may start before those in front of them have ended: nothing they read is read-only while they run."""
+    import re
+    csrc = os.path.join(ROOT, "transformer_xl_relative_gb300", "csrc")
+    for name in ("txl_paged.cu", "txl_paged.cuh", "txl_paged_attn.cu", "txl_linear_q4.cu"):
+        text = re.sub(r"//.*", "", open(os.path.join(csrc, name), encoding="utf-8").read())
+        assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", text), name

@@ -52,7 +52,7 @@ def _raw_stream(stream, device: int) -> int:
 
 def _on_device(device: int, call, args):
     """call(args) with CUDA device `device` current (the library launches on the current device)."""
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         return call(args)
     with torch.cuda.device(device):
         return call(args)
@@ -629,6 +629,11 @@ class PagedMemory:
         return self._c.page_len
 
     @property
+    def reserved(self) -> list:
+        """Positions that every sequence has room for: its length, and what was reserved and not pushed."""
+        return list(self._room)
+
+    @property
     def free_pages(self) -> int:
         """Pages that no sequence has."""
         return len(self._free)
@@ -864,34 +869,42 @@ def linear_q4(X: torch.Tensor, w: QuantWeight, Y: torch.Tensor | None = None, wo
               err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X W for bf16 X [m, k] and 4-bit W [k, n] (txl_linear_q4); Y [m, n] is allocated if not given, and so is the
     workspace where many rows need one."""
-    dev, (k, n) = w.device, w.shape
-    px, ldx = _rows2d(X, "X")
-    m = X.shape[0]
-    if X.shape[1] != k:
-        raise ValueError("inner dimensions differ")
-    if X.dtype != torch.bfloat16:
-        raise TypeError("linear_q4 computes in bfloat16, got %s" % X.dtype)
-    need = linear_q4_workspace_size(m, w) if workspace is None else 0
+    dev, (k, n), shape = w.device, w.shape, X.shape
+    if len(shape) != 2 or shape[1] != k or X.dtype != torch.bfloat16 or X.get_device() != dev:
+        _q4_refusal(X, w)
+    m, (ldx, x1) = shape[0], X.stride()
+    need = linear_q4_workspace_size(m, w) if m > 16 and workspace is None else 0
     if Y is None or need:
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
             if Y is None:
                 Y = torch.empty(m, n, dtype=X.dtype, device=X.device)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
-    py, ldy = _rows2d(Y, "Y")
-    if Y.shape != (m, n) or Y.dtype != torch.bfloat16:
-        raise ValueError("Y must be bfloat16 [%d, %d]" % (m, n))
-    if X.get_device() != dev or Y.get_device() != dev:
-        raise ValueError("tensors must live on the weights' device")
+    if Y.shape != (m, n) or Y.dtype != torch.bfloat16 or Y.get_device() != dev:
+        raise ValueError("Y must be bfloat16 [%d, %d] on the weights' device" % (m, n))
+    ldy, y1 = Y.stride()
+    if (x1 != 1 and k > 1) or (y1 != 1 and n > 1):
+        raise ValueError("X and Y must have unit column stride")
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and live on the weights' device")
     if err_flag is not None and (err_flag.get_device() != dev or err_flag.dtype != torch.int32 or err_flag.numel() < 1):
         raise ValueError("err_flag must be an int32 on the weights' device")
     pw, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
-    args = native.Q4_ARGS.pack(w.address, px, ldx if m > 1 else (k + 7) // 8 * 8, py, ldy if m > 1 else n, pw, size,
-                               err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev), m)
+    args = native.Q4_ARGS.pack(w.address, X.data_ptr(), ldx if m > 1 else (k + 7) // 8 * 8, Y.data_ptr(), ldy if m > 1 else n,
+                               pw, size, err_flag.data_ptr() if err_flag is not None else 0, _raw_stream(stream, dev), m)
     check(_on_device(dev, _lib().txl_linear_q4_call, args), "txl_linear_q4")
     return Y
+
+
+def _q4_refusal(X, w):
+    """Raises what is wrong with X of linear_q4 (called when something is)."""
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor with unit column stride")
+    if X.shape[1] != w.shape[0]:
+        raise ValueError("inner dimensions differ")
+    if X.dtype != torch.bfloat16:
+        raise TypeError("linear_q4 computes in bfloat16, got %s" % X.dtype)
+    raise ValueError("tensors must live on the weights' device")
 
 
 def selftest_wait_timeout(err_flag: torch.Tensor, timeout_us: int, stream=None) -> None:

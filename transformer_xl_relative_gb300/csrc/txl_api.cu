@@ -1301,7 +1301,7 @@ txl_status check_paged(const txl_paged* m)
     if (!m || m->B < 0 || m->H <= 0 || m->D <= 0 || m->n_pages < 0 || m->page_len <= 0 || m->max_pages < 0 || m->ld < m->D)
         return TXL_ERR_INVALID_ARG;
     if (m->dtype != TXL_F32 && m->dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
-    if (m->D > 128 || m->page_len % kPageUnit || m->B > kPagedMaxB || m->H > 65535) return TXL_ERR_UNSUPPORTED;
+    if (m->D > 128 || m->ld > 65536 || m->page_len % kPageUnit || m->B > kPagedMaxB || m->H > 65535) return TXL_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(m->n_pages) * m->page_len > INT32_MAX || static_cast<int64_t>(m->max_pages) * m->page_len > INT32_MAX)
         return TXL_ERR_UNSUPPORTED;
     if (m->B == 0) return TXL_OK;
@@ -1402,8 +1402,9 @@ txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl
     const txl_status st = check_paged(mem);
     if (st != TXL_OK) return st;
     if (T < 0 || (T > 0 && (!view_ok(k_new) || !view_ok(v_new)))) return TXL_ERR_INVALID_ARG;
-    if (!a4(counts)) return TXL_ERR_ALIGNMENT;
     if (T == 0 || mem->B == 0) return TXL_OK;
+    const uintptr_t odd = reinterpret_cast<uintptr_t>(k_new->ptr) | reinterpret_cast<uintptr_t>(v_new->ptr);
+    if (!a4(counts) || (odd & (mem->dtype == TXL_F32 ? 3u : 1u))) return TXL_ERR_ALIGNMENT;
     const PagedPushParams p = paged_push_params(mem, k_new, v_new, T, counts);
     return launch_paged_push(p, static_cast<txl_dtype>(mem->dtype), static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TXL_OK : TXL_ERR_CUDA;
@@ -1417,7 +1418,7 @@ txl_status txl_paged_push_call(const txl_paged_push_args* a)
 
 size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate)
 {
-    if (!mem || mem->B <= 0 || mem->H <= 0 || mem->D <= 0 || mem->D > 128 || T <= 0 || T > kDecodeMaxL || n_rows <= 0 ||
+    if (!mem || mem->B <= 0 || mem->H <= 0 || mem->D <= 0 || mem->D > 128 || T <= 0 || T > kDecodeMaxL || n_rows <= 0 || n_rows > (1 << 30) ||
         mem->max_pages < 0 || mem->page_len <= 0)
         return 0;
     return paged_workspace(mem, T, n_rows, accumulate, nullptr, nullptr);
@@ -1441,6 +1442,7 @@ txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* a)
                           reinterpret_cast<uintptr_t>(a->r);
     if (!a4(a->u) || !a4(a->v_bias) || !a4(a->counts) || (odd & (elem - 1))) return TXL_ERR_ALIGNMENT;
     const int n_e = static_cast<int>(std::min<int64_t>(a->n_rows, static_cast<int64_t>(a->clamp_len) + 1));
+    if (n_e > (1 << 30)) return TXL_ERR_UNSUPPORTED;
     PagedAttnParams p{};
     const size_t need = paged_workspace(m, a->T, n_e, a->accumulate, nullptr, nullptr);
     if (!a->workspace || a->workspace_bytes < need) return TXL_ERR_WORKSPACE;

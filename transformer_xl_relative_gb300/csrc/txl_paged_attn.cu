@@ -11,6 +11,12 @@
 //                        takes a share, and the last block of a pair joins its parts.  One bf16 token a sequence needs no
 //                        preparation: each key's row of r is multiplied beside the key, the new key is a part of its own
 //   paged_weight_kernel  (accumulate) 2^(score - log-sum-exp) summed over heads and queries
+//
+// Bound by HBM: K, V and a row of r once a key.  One query over 4096 positions of 8 sequences (H16 D64, 137 MB): 30.9 us, of which
+// 21 are the 6.3 TB/s of what further keys add (4096 -> 16384 positions: 403 MB in 64 us) and 9 the schedule (1.5), a part's
+// first tile (4.5: table, positions, rows, one after another) and the join (2.5).  32 ragged sequences with summed weights
+// (232 MB) 46.2 + 5.7 us, one of 65536 positions with a row of r for each (403 MB) 76.6, 16 queries 55, five of d_head 128 over
+// up to 2048 positions 26.
 #include <cuda_bf16.h>
 
 #include "txl_mma.cuh"
@@ -336,27 +342,28 @@ __device__ __forceinline__ void load_b(BFrag<NC>& f, const uint16_t* row, int t)
 // ONE: a pair's new key, by one warp: its score, its values as a part of one key, and its row into the page (which the
 // sequence may lack: then nothing is written).  Loaded before anything that waits, worked on later.
 template <int NC, bool W> struct OwnKey {
-    float s, k[NC], v[NC];
+    float s;
+    uint16_t k[NC], v[NC];
     int page;
 
     __device__ __forceinline__ void load(const PagedAttnParams& p, const Part& a, int lane)
     {
         const PagedParams& m = p.n.m;
         const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + a.b * p.q_sb + a.h * p.q_sh;
-        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
-        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
+        const uint16_t* kr = static_cast<const uint16_t*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
+        const uint16_t* vr = static_cast<const uint16_t*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
         const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.r) + a.h * p.r_head;
         page = page_of(m, a.b, a.len);
         s = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int d = lane + 32 * j;
-            k[j] = v[j] = 0.f;
+            k[j] = v[j] = 0;
             if (d < m.D) {
                 const float x = __bfloat162float(qr[d]);
-                k[j] = __bfloat162float(kr[d]);
-                v[j] = __bfloat162float(vr[d]);
-                s = fmaf((x + p.u[a.h * m.D + d]) * p.qscale, k[j], s);
+                k[j] = kr[d];
+                v[j] = vr[d];
+                s = fmaf((x + p.u[a.h * m.D + d]) * p.qscale, mma::bf16_lo(k[j]), s);
                 s = fmaf((x + p.vb[a.h * m.D + d]) * p.qscale, __bfloat162float(r[d]), s);
             }
         }
@@ -369,10 +376,10 @@ template <int NC, bool W> struct OwnKey {
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int d = lane + 32 * j;
-            if (d < m.D) values[d] = v[j];
+            if (d < m.D) values[d] = mma::bf16_lo(v[j]);
             if (page >= 0 && d < m.ld) {
-                static_cast<__nv_bfloat16*>(m.k)[at + d] = __float2bfloat16_rn(k[j]);
-                static_cast<__nv_bfloat16*>(m.v)[at + d] = __float2bfloat16_rn(v[j]);
+                static_cast<uint16_t*>(m.k)[at + d] = k[j];
+                static_cast<uint16_t*>(m.v)[at + d] = v[j];
             }
         }
         for (int d = lane + 32 * NC; page >= 0 && d < m.ld; d += 32)
