@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_select_kernel(const __
     int* bins = reinterpret_cast<int*>(keys + held);                          // [2][kBins]
     __shared__ int sums[32];
     __shared__ int found[3];
+    __shared__ __align__(16) unsigned long long ends[2];                      // least and largest key left
     __shared__ __align__(8) int counts[2];                                    // holes, movers of this block
     pdl_wait();
     pdl_launch_dependents();
@@ -144,10 +145,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_select_kernel(const __
     };
     for (int i = tid; i < min(mine, held); i += kEvictThreads) keys[i] = make(i);
     for (int i = tid; i < 2 * kBins; i += kEvictThreads) bins[i] = 0;
+    if (tid == 0) ends[0] = kStays, ends[1] = 0;
     auto key_of = [&](int i) { return i < held ? keys[i] : make(i); };
 
     // the least (n - keep) keys: those whose bits above `shift` are at most `limit`
-    int want = n - keep, shift = 64, turn = 0;
+    int want = n - keep, shift = 64, turn = 0, digits = 0;
     uint64_t limit = 0;
     while (shift > 0) {
         const int width = min(kDigit, shift);
@@ -206,6 +208,38 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_select_kernel(const __
         shift -= width;
         limit = (limit << width) | static_cast<uint64_t>(digit);
         if (all) break;
+        if (++digits != 2) continue;
+        // Two digits that did not do: as a rule many slots of one weight.  The digits that all the keys left share are skipped.
+        uint64_t least = kStays, most = 0;
+        for (int i = tid; i < mine; i += kEvictThreads) {
+            const uint64_t key = key_of(i);
+            if (key != kStays && key >> shift == limit) {
+                least = min(least, key);
+                most = max(most, key);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+        }
+        if ((tid & 31) == 0) {
+            atomicMin(&ends[0], least);
+            atomicMax(&ends[1], most);
+        }
+        if (ranks > 1) cluster_sync_all();
+        else __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kEvictRanks; ++r)
+            if (r < ranks) {
+                const int4 e = ranks > 1 ? ld_rank4(reinterpret_cast<const int*>(ends), r) : *reinterpret_cast<const int4*>(ends);
+                least = min(least, static_cast<uint64_t>(static_cast<uint32_t>(e.y)) << 32 | static_cast<uint32_t>(e.x));
+                most = max(most, static_cast<uint64_t>(static_cast<uint32_t>(e.w)) << 32 | static_cast<uint32_t>(e.z));
+            }
+        if (least < most) {
+            shift = 64 - __clzll(least ^ most);
+            limit = shift == 64 ? 0 : least >> shift;
+        }
     }
     // a thread's slots are neighbours: one sum over the threads each orders its holes and its movers
     auto leaves = [&](int i) {
