@@ -405,7 +405,9 @@ struct PagedEvictParams {
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sm_count, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights
-constexpr int kQ4MaxRows = 128;     // rows of X up to which they are multiplied with the codes as they are
+// Rows of X up to which they are multiplied with the codes as they are: at 128 rows 31 us against 44 through bf16 weights (k = n =
+// 4096), 111 against 128 (8192), 5.6 against 11.5 (1024); the former grows by 0.29, 0.87 and 0.03 us a row.
+constexpr int kQ4MaxRows = 128;
 
 struct LinearQ4Params {
     const void* x; int64_t ld_x;                // bf16 [m][ld_x]
