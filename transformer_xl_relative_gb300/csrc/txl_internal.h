@@ -405,8 +405,8 @@ struct PagedEvictParams {
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sm_count, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights
-// Rows of X up to which they are multiplied with the codes as they are: at 128 rows 31 us against 44 through bf16 weights (k = n =
-// 4096), 111 against 128 (8192), 5.6 against 11.5 (1024); the former grows by 0.29, 0.87 and 0.03 us a row.
+// Rows of X up to which they are multiplied with the codes as they are: at 128 rows 31 us against 38 through bf16 weights (k = n =
+// 4096), 92 against 106 (8192), 4.1 against 10.5 (1024), 14.1 against 14.0 (k = 1024, n = 4096).
 constexpr int kQ4MaxRows = 128;
 
 struct LinearQ4Params {

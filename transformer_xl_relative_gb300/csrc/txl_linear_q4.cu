@@ -274,25 +274,35 @@ __global__ void __launch_bounds__(kWThreads) q4_quantise_kernel(const __grid_con
     }
 }
 
-// 64 columns by 64 k of W from the codes: one fp32 multiply-add, rounded to bf16.
+// 64 columns by 64 k of W from the codes: one fp32 multiply-add, rounded to bf16.  A thread's word holds four k of columns g and
+// g + 8; it trades two of the k with the thread of column g ^ 1, so that pairs of columns go into a row of shared memory
+// (33 words a row: the rows of a warp in different banks).  4096 x 4096: 12.4 us (43 MB, 3.4 TB/s; single 16-bit stores into shared
+// memory took 18.0).
 __global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_constant__ Q4WeightParams p)
 {
-    __shared__ __align__(16) uint16_t x[kQ4K][72];
+    __shared__ uint32_t x[kQ4K][33];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, kb = blockIdx.y, n0 = blockIdx.x * 64;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+#pragma unroll
     for (int i = tid; i < 4 * 128; i += kExpandThreads) {
         const int nt = n0 / kQ4N + i / 128, lane = i % 128 / 4, s = i % 4, g = lane >> 2, t = lane & 3;
-        if (nt * kQ4N >= p.n) continue;
         const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + code_block(nt, kb, kb_all) * 32 + lane)[s];
         const int k = 32 * (s >> 1) + 8 * t + 4 * (s & 1), gr = min((kb * kQ4K + k) / p.group, groups - 1);
         const uint32_t* q = p.par + par_block(nt, gr, groups) * 16 + g;
         const uint32_t par[2] = {q[0], q[8]};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = fmaf(mma::bf16_lo(par[j & 1]), static_cast<float>((w >> (4 * j)) & 15u), mma::bf16_hi(par[j & 1]));
-            x[k + (j & 2) + (j >> 2)][i / 128 * kQ4N + g + 8 * (j & 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        for (int c = 0; c < 2; ++c) {
+            const float step = mma::bf16_lo(par[c]), lo = mma::bf16_hi(par[c]);
+            // a code as the low bits of 2^23 + c
+            auto value = [&](int j) { return fmaf(step, __uint_as_float((w >> (4 * j) & 15u) | 0x4B000000u) - 8388608.f, lo); };
+            const uint32_t front = mma::pack2(value(c), value(4 + c)), back = mma::pack2(value(2 + c), value(6 + c));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, g & 1 ? front : back, 16);
+            const uint32_t left = g & 1 ? other : front, right = g & 1 ? back : other;      // columns g & ~1, g | 1
+            uint32_t* row = &x[k + 2 * (g & 1)][(i / 128 * kQ4N + (g & 6) + 8 * c) / 2];
+            row[0] = __byte_perm(left, right, 0x5410);
+            row[33] = __byte_perm(left, right, 0x7632);
         }
     }
     __syncthreads();
@@ -302,10 +312,10 @@ __global__ void __launch_bounds__(kExpandThreads) q4_expand_kernel(const __grid_
         const int k = kb * kQ4K + i / 8, n = n0 + i % 8 * 8;
         if (k >= p.k || n >= p.n) continue;
         uint16_t* row = static_cast<uint16_t*>(p.w) + static_cast<int64_t>(k) * p.ld_w + n;
-        const uint16_t* from = &x[i / 8][i % 8 * 8];
-        if (vec && n + 8 <= p.n) *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(from);
+        const uint32_t* from = &x[i / 8][i % 8 * 4];
+        if (vec && n + 8 <= p.n) *reinterpret_cast<uint4*>(row) = make_uint4(from[0], from[1], from[2], from[3]);
         else
-            for (int e = 0; e < min(8, p.n - n); ++e) row[e] = from[e];
+            for (int e = 0; e < min(8, p.n - n); ++e) row[e] = static_cast<uint16_t>(from[e >> 1] >> (16 * (e & 1)));
     }
 }
 
@@ -313,7 +323,9 @@ template <int NT, int MT, int SUB, bool VEC>
 cudaError_t launch_variant(const LinearQ4Params& p, int warps, cudaStream_t s)
 {
     static OncePerDevice once;
-    const cudaError_t e = allow_smem(once, kQ4MaxWarps * kQ4Ring<NT, MT, SUB>, linear_q4_kernel<NT, MT, SUB, VEC>);
+    constexpr int most = 226 * 1024 / kQ4Ring<NT, MT, SUB> < kQ4MaxWarps ? 226 * 1024 / kQ4Ring<NT, MT, SUB> : kQ4MaxWarps;
+    warps = min(warps, most);
+    const cudaError_t e = allow_smem(once, most * kQ4Ring<NT, MT, SUB>, linear_q4_kernel<NT, MT, SUB, VEC>);
     if (e != cudaSuccess) return e;
     const dim3 grid((p.n + kQ4N * NT - 1) / (kQ4N * NT), (p.m + 8 * MT - 1) / (8 * MT));
     return launch_dependent(linear_q4_kernel<NT, MT, SUB, VEC>, grid, dim3(32 * warps), warps * kQ4Ring<NT, MT, SUB>, s, p);
@@ -335,10 +347,12 @@ cudaError_t launch_linear_q4(const LinearQ4Params& p, int sm_count, cudaStream_t
     // measured: n = 8192, k = 8192: 18.3, 14.5, 13.2; n = 4096, k = 1024: 2.44, 2.18, 2.73; n = 1024, k = 1024: 1.79, 1.91, 2.66).
     // Warps: a few blocks of k each (8 and 16 warps: k = 1024 1.79 and 1.89, k = 4096, n = 1024 3.82 and 3.43).  Rows: 8, or 16 at
     // once where there are more than 8 (the same codes serve both).
-    const int tiles = (p.n + kQ4N - 1) / kQ4N, kb = (p.k + kQ4K - 1) / kQ4K;
-    const int nt = tiles >= 3 * sm_count && p.m <= 8 ? 4 : tiles >= 3 * sm_count / 2 ? 2 : 1, warps = kb >= 48 && p.m <= 8 ? 16 : 8;
+    // 16 rows, 8 warps: k = n = 8192 25.4, 18.6, 14.7; 4096 8.5, 6.7, 8.5; 64 rows by 4096 x 4096 23.8, 18.5, 16.2.
+    const int kb = (p.k + kQ4K - 1) / kQ4K, at_once = p.m <= 8 ? 8 : 16;
+    const int64_t blocks = static_cast<int64_t>((p.n + kQ4N - 1) / kQ4N) * ((p.m + at_once - 1) / at_once);
+    const int nt = blocks >= 3 * sm_count ? 4 : blocks >= 3 * sm_count / 2 ? 2 : 1, warps = kb >= 48 && p.m <= 8 ? 16 : 8;
     if (p.m <= 8) return nt == 4 ? launch_rows<4, 1>(p, warps, s) : nt == 2 ? launch_rows<2, 1>(p, warps, s) : launch_rows<1, 1>(p, warps, s);
-    return nt == 2 ? launch_rows<2, 2>(p, warps, s) : launch_rows<1, 2>(p, warps, s);
+    return nt == 4 ? launch_rows<4, 2>(p, warps, s) : nt == 2 ? launch_rows<2, 2>(p, warps, s) : launch_rows<1, 2>(p, warps, s);
 }
 
 cudaError_t launch_q4_quantise(const Q4WeightParams& p, cudaStream_t s)
