@@ -641,7 +641,8 @@ class PagedMemory:
     def reserve(self, positions) -> None:
         """Pages for `positions` more positions of every sequence (an int, or one of each).  A pushed position must
         have been reserved; one that was reserved and then not pushed keeps its room until trim.  Raises, and changes
-        nothing, when the pool or a sequence's row of the table is too small."""
+        nothing, when the pool or a sequence's row of the table is too small.  The table changes on the current stream
+        (as it does in release and trim)."""
         B = self._shape[0]
         more = [positions] * B if isinstance(positions, int) else [int(x) for x in positions]
         if len(more) != B or min(more, default=0) < 0:

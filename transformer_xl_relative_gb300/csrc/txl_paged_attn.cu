@@ -221,9 +221,19 @@ struct Part {
     int b, h, len, first, n;       // slots, position of the first query, queries
     int t0, t1, tiles;             // its tiles, of the pair's
     int parts, first_block;        // the pair's parts, and the block of the first
+    const int* table;              // the sequence's row of the page table, in shared memory where that holds it
     bool room;                     // the new key has a page (else the sequence is left as it was)
     bool own;                      // the pair has a new key that is not among the slots (k_new, position `first`)
 };
+
+// The page of a slot of the part's sequence, or -1.
+__device__ __forceinline__ int page_at(const PagedParams& m, const Part& a, int s)
+{
+    const int i = s / m.page_len;
+    if (i >= m.max_pages) return -1;
+    const int page = a.table[i];
+    return static_cast<unsigned>(page) < static_cast<unsigned>(m.n_pages) ? page : -1;
+}
 
 // Where the tiles that a warp will come to lie: lane x knows that of the warp's x-th tile from `base` on (a page's number
 // and the row in it take divisions, which are made once in 32 tiles).
@@ -236,7 +246,7 @@ template <int NW> struct Tiles {
         base = tile;
         const int at = tile + NW * lane;
         const bool used = at < a.t1 && at * kPageUnit < a.len;
-        const int page = used ? page_of(m, a.b, at * kPageUnit) : -1, row = at * kPageUnit % m.page_len;
+        const int page = used ? page_at(m, a, at * kPageUnit) : -1, row = at * kPageUnit % m.page_len;
         if (used && page < 0) page_error(m);
         mine = page < 0 ? -1 : page * m.page_len + row;
         mine_kv = page < 0 ? -1 : page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld;
@@ -354,7 +364,7 @@ template <int NC, bool W> struct OwnKey {
         const uint16_t* kr = static_cast<const uint16_t*>(p.n.xk) + a.b * p.n.xk_sb + a.h * p.n.xk_sh;
         const uint16_t* vr = static_cast<const uint16_t*>(p.n.xv) + a.b * p.n.xv_sb + a.h * p.n.xv_sh;
         const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.r) + a.h * p.r_head;
-        page = page_of(m, a.b, a.len);
+        page = page_at(m, a, a.len);
         s = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -1011,6 +1021,13 @@ __host__ __device__ __forceinline__ int beside_floats(int Dp)
     return sizeof(T) == 4 ? NQ * Dp : (ONE ? Dp : 0) + kQRows<NC, NQ, ONE> * kQPitch<NC> / 2;
 }
 
+// Entries of a page table that the blocks keep in shared memory: none of a larger one.
+__host__ __device__ __forceinline__ int small_table(const PagedParams& m)
+{
+    const int64_t n = static_cast<int64_t>(m.B) * m.max_pages;
+    return n <= 2048 ? static_cast<int>(n) : 0;
+}
+
 // Length and position of the first query of sequence b, for a call that needed no preparation (ONE).
 __device__ __forceinline__ int4 now_of(const PagedAttnParams& p, int b)
 {
@@ -1022,7 +1039,7 @@ __device__ __forceinline__ int4 now_of(const PagedAttnParams& p, int b)
 }
 
 // Shared memory: the warps' rings or sums; a new key's values; queries; maxima and weights; where the
-// sequences' pairs begin [B + 1] (64 bits); the sequences' lengths and first positions [B].
+// sequences' pairs begin [B + 1] (64 bits); the sequences' lengths and first positions [B]; a small page table.
 template <typename T, int NC, int NQ, bool ONE, bool W>
 __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ>)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
 {
@@ -1036,9 +1053,21 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
     float* bml = beside + beside_floats<T, NC, NQ, ONE>(p.Dp);
     int64_t* start = reinterpret_cast<int64_t*>(bml + ((NW + 1) * p.n.T * 2 + 3) / 4 * 4);
     int2* info = reinterpret_cast<int2*>(start + m.B + 1);
+    int* small = reinterpret_cast<int*>(info + m.B);
+    if constexpr (ONE) {
+        // (the rows of queries that one token does not have)
+        uint32_t* rows = reinterpret_cast<uint32_t*>(beside + p.Dp);
+        for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += (32 * NW)) rows[x] = 0;
+    }
     // (no early launch of the next grid: blocks of the weights' kernel that wait would take the place of later blocks)
     pdl_wait();
 
+    // a small page table comes into shared memory beside the lengths: a part's first look then does not wait for one
+    const int entries = small_table(m);
+    for (int x = tid; x < entries; x += (32 * NW))
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(small + x)), "l"(m.table + x) : "memory");
+    mma::cp_async_commit();
+    const int* held = entries ? small : m.table;
     // start[b]: the work of all pairs of the sequences before b (an empty memory counts as a tile)
     int64_t done = 0;
     for (int b0 = 0; b0 < m.B; b0 += (32 * NW)) {
@@ -1069,7 +1098,6 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         __syncthreads();
     }
     if (tid == 0) start[m.B] = done;
-    __syncthreads();
     // ONE: the last block that has read the lengths advances them at its end (the ticket's answer is not waited for before)
     const bool counts = ONE && (p.n.xk || W);
     int ticket = -1;
@@ -1093,11 +1121,7 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
             if (W) p.now[b] = now;
         }
     };
-    if constexpr (ONE) {
-        // (the rows of queries that one token does not have)
-        uint32_t* rows = reinterpret_cast<uint32_t*>(beside + p.Dp);
-        for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += (32 * NW)) rows[x] = 0;
-    }
+    copies_wait<0>();
     __syncthreads();
     const int share = max(kMinTiles, quotient(done + gridDim.x - 1, gridDim.x));
     int64_t at = static_cast<int64_t>(blockIdx.x) * share;
@@ -1119,7 +1143,8 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         a.first = info[b].y;
         a.n = ONE ? 1 : p.now[b].z;
         a.own = ONE && p.n.xk;
-        a.room = !a.own || page_of(m, b, a.len) >= 0;
+        a.table = held + static_cast<int64_t>(b) * m.max_pages;
+        a.room = !a.own || page_at(m, a, a.len) >= 0;
         a.tiles = max(1, (a.len + kPageUnit - 1) / kPageUnit);
         const int size = kHead + a.tiles;
         a.h = quotient(at - start[b], size);
@@ -1206,7 +1231,7 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
     static OncePerDevice once;
     const PagedParams& m = p.n.m;
     const size_t smem = 4 * (static_cast<size_t>(NW) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
-                             static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1);
+                             static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1) + 4 * static_cast<size_t>(small_table(m));
     cudaError_t e = allow_smem(once, 224 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
     if (e != cudaSuccess) return e;
     if (!ONE) {
