@@ -467,6 +467,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
         }
     }
     const int first = a.t0 + warp;
+    if (!ONE && p.n.xk && a.t1 * kPageUnit > a.len - a.n) pdl_wait();      // new keys are among them
 #pragma unroll
     for (int x = 0; x < kStages<NC> - 1; ++x) {
         const int tile = first + x * NW;
@@ -483,6 +484,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     };
     if (first < a.t1) load_pos(first);
     queries.store(qs);
+    if (!ONE) pdl_wait();                                      // E is there
     if constexpr (ONE)
         if (owner) own_key.store(p, a, lane, own, bml + 2 * NW);
 
@@ -661,6 +663,7 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
     const PagedParams& m = p.n.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int T = p.n.T, D = m.D;
+    pdl_wait();
     for (int i0 = 0; i0 < a.n; i0 += NQ) {
         __syncthreads();
         for (int x = threadIdx.x; x < NQ * p.Dp; x += (32 * NW)) {
@@ -1021,21 +1024,29 @@ __host__ __device__ __forceinline__ int beside_floats(int Dp)
     return sizeof(T) == 4 ? NQ * Dp : (ONE ? Dp : 0) + kQRows<NC, NQ, ONE> * kQPitch<NC> / 2;
 }
 
-// Entries of a page table that the blocks keep in shared memory: none of a larger one.
+// Entries of a page table that the blocks keep in shared memory (8 KB, with which as many blocks fit an SM): none of a larger one,
+// whose first looks take 0.1 to 0.4 us more (one query over 64 positions 6.25 against 6.14, five of d_head 128 25.8 and 25.5).
 __host__ __device__ __forceinline__ int small_table(const PagedParams& m)
 {
     const int64_t n = static_cast<int64_t>(m.B) * m.max_pages;
     return n <= 2048 ? static_cast<int>(n) : 0;
 }
 
-// Length and position of the first query of sequence b, for a call that needed no preparation (ONE).
-__device__ __forceinline__ int4 now_of(const PagedAttnParams& p, int b)
+// Length, position of the first query and queries of sequence b, as the memory stands before the call: with ONE the length
+// without the new key, else with the keys that the preparation puts there (its rule; up to 16 of them lie in two pages at
+// most).
+template <bool ONE>
+__device__ __forceinline__ int3 now_of(const PagedAttnParams& p, int b)
 {
     const PagedParams& m = p.n.m;
-    const int len = m.length[b], next = m.next_pos[b], n = paged_count(p.n.counts, b, 1);
-    const bool ok = len >= 0 && len <= p.cap;
-    if (!ok && n > 0) page_error(m);
-    return make_int4(len, p.n.xk ? next : next - n, ok ? n : 0, 0);
+    const int len = m.length[b], next = m.next_pos[b], n = paged_count(p.n.counts, b, ONE ? 1 : p.n.T);
+    bool ok = len >= 0 && len <= p.cap;
+    if (ONE || !p.n.xk) {
+        if (ONE && !ok && n > 0) page_error(m);
+        return make_int3(len, p.n.xk ? next : next - n, ok ? n : 0);
+    }
+    ok = ok && n > 0 && len <= p.cap - n && page_of(m, b, len) >= 0 && page_of(m, b, len + n - 1) >= 0;
+    return make_int3(ok ? len + n : len, next, ok ? n : 0);
 }
 
 // Shared memory: the warps' rings or sums; a new key's values; queries; maxima and weights; where the
@@ -1060,7 +1071,10 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         for (int x = tid; x < kQRows<NC, NQ, ONE> * kQPitch<NC> / 2; x += (32 * NW)) rows[x] = 0;
     }
     // (no early launch of the next grid: blocks of the weights' kernel that wait would take the place of later blocks)
-    pdl_wait();
+    // The preparation began when all before it had ended, and this grid when all of that had begun: what the preparation does not
+    // write, which is all but the new positions and the workspace, is read while it still runs (four queries over 4096
+    // positions 35.3 us, after a wait for all of it 36.2; fp32 45.4 and 46.9).
+    if (ONE) pdl_wait();
 
     // a small page table comes into shared memory beside the lengths: a part's first look then does not wait for one
     const int entries = small_table(m);
@@ -1074,14 +1088,9 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         const int b = b0 + tid;
         int64_t x = 0;
         if (b < m.B) {
-            const int4 now = ONE ? now_of(p, b) : p.now[b];
+            const int3 now = now_of<ONE>(p, b);
             x = now.z > 0 ? static_cast<int64_t>(kHead + max(1, (now.x + kPageUnit - 1) / kPageUnit)) * m.H : 0;
             info[b] = make_int2(now.x, now.y);
-            // prepared: the new positions count from now on (nothing here reads the memory's own numbers)
-            if (!ONE && blockIdx.x == 0 && p.n.xk && now.z > 0) {
-                m.length[b] = now.x;
-                m.next_pos[b] = now.y + now.z;
-            }
         }
         int64_t s = x;
 #pragma unroll
@@ -1098,17 +1107,24 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         __syncthreads();
     }
     if (tid == 0) start[m.B] = done;
-    // ONE: the last block that has read the lengths advances them at its end (the ticket's answer is not waited for before)
-    const bool counts = ONE && (p.n.xk || W);
+    // the last block that has read the lengths advances them at its end (the ticket's answer is not waited for before)
+    const bool counts = p.n.xk || (ONE && W);
     int ticket = -1;
     if (counts && tid == 32 * NW - 1)
         asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;" : "=r"(ticket) : "l"(m.scratch + m.B) : "memory");
     auto advance = [&] {
+        if (!ONE) pdl_wait();                                  // (the preparation reads them too, and ends before this grid does)
         if (!counts || warp != NW - 1) return;
         const bool last = ticket == static_cast<int>(gridDim.x) - 1;
         if (!__any_sync(0xffffffffu, last)) return;
         if (last) m.scratch[m.B] = 0;
         for (int b = lane; b < m.B; b += 32) {
+            if (!ONE) {
+                if (start[b + 1] == start[b]) continue;
+                m.length[b] = info[b].x;
+                m.next_pos[b] = info[b].y + paged_count(p.n.counts, b, p.n.T);
+                continue;
+            }
             int4 now = make_int4(info[b].x, info[b].y, start[b + 1] > start[b] ? 1 : 0, 0);
             if (p.n.xk && now.z > 0) {
                 if (page_of(m, b, now.x) < 0) {
@@ -1141,7 +1157,7 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
         a.b = b;
         a.len = info[b].x;
         a.first = info[b].y;
-        a.n = ONE ? 1 : p.now[b].z;
+        a.n = ONE ? 1 : paged_count(p.n.counts, b, p.n.T);
         a.own = ONE && p.n.xk;
         a.table = held + static_cast<int64_t>(b) * m.max_pages;
         a.room = !a.own || page_at(m, a, a.len) >= 0;
@@ -1245,7 +1261,7 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
         if (e != cudaSuccess) return e;
     }
     // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its static part besides
-    const int per_sm = max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (smem + 1024 + 64))));
+    const int per_sm = max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (smem + 1024 + 32 * NW * 8 + 128))));
     const int blocks = min(per_sm * sm_count, kPagedMaxCtas);
     if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, false>, dim3(blocks), dim3(32 * NW), smem, s, p);
     e = launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, true>, dim3(blocks), dim3(32 * NW), smem, s, p);
