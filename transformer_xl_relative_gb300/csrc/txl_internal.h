@@ -392,8 +392,9 @@ struct PagedAttnParams {
     float* lse;                                 // [B][H][T] their log-sum-exp (accumulate)
     float* part; float* ml;                     // [2 kPagedMaxCtas][T][Dp], [..][T][2]: sums, maximum and weight
     int Dp;                                     // D rounded up to 32
+    int held;                                   // entries of the page table in the blocks' shared memory (set by the launch)
 };
-cudaError_t launch_paged_attn(const PagedAttnParams& p, txl_dtype dtype, int sm_count, cudaStream_t s);
+cudaError_t launch_paged_attn(PagedAttnParams& p, txl_dtype dtype, int sm_count, cudaStream_t s);
 
 struct PagedEvictParams {
     PagedParams m;

@@ -816,7 +816,8 @@ template <typename T> __device__ __forceinline__ T* out_row(const PagedAttnParam
 }
 
 // One query's row again, key by key on the CUDA cores: its sums are not finite, and a value that is not finite at a key
-// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: (32 * NW) floats.
+// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: a float and a pointer for each
+// of its threads.
 template <typename T, int NW>
 __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, bool terms, float* tot)
 {
@@ -862,7 +863,7 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     top = finite_or_0(top);
     float sum = nan ? __int_as_float(0x7fc00000) : 0.f, o = sum;
     const int d = threadIdx.x;                                // D <= 128: a channel a thread
-    __shared__ const T* values[(32 * NW)];
+    const T** values = reinterpret_cast<const T**>(tot + 32 * NW);
     for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += (32 * NW)) {
         const int s = s0 + threadIdx.x;
         const float x = score(s);
@@ -1006,30 +1007,26 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
     __syncthreads();
 }
 
-// Warps of a block: four, or eight where registers leave room for two blocks of four at most (five drafted tokens of d_head 128:
-// 24.9 us against 28.5 with two blocks of four; one token of d_head 64: 31.9 against 30.6 with four blocks).
-template <typename T, int NC, int NQ> constexpr int kWarpsOf = sizeof(T) == 2 && (NC > 2 || NQ > 2) ? 8 : 4;
-// Blocks of the attention that an SM holds: what registers (bf16: the rings) of the variants leave room for.
+// Warps of a block: four; eight, in one block, for more than eight queries or more than four of d_head above 64 (five drafted tokens
+// of d_head 128: 25.5 us, against 28.5 with three blocks of four; 16 queries of d_head 64 53.8 and 56.2; but one query of d_head 96
+// over 4096 positions 44.9 and 42.7, of d_head 128 over up to 2048 18.6 and 17.7; of d_head 64 31.9 and, with four blocks, 30.6).
+template <typename T, int NC, int NQ> constexpr int kWarpsOf = sizeof(T) == 2 && (NQ > 2 || (NC > 2 && NQ > 1)) ? 8 : 4;
+// Blocks of the attention that an SM holds: what registers (bf16: and the rings) of the variants leave room for.
 template <typename T, int NC, int NQ>
-constexpr int kBlocks = sizeof(T) == 4 ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2) : kWarpsOf<T, NC, NQ> == 8 ? 1 : 4;
+constexpr int kBlocks = sizeof(T) == 4             ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2)
+                        : kWarpsOf<T, NC, NQ> == 8 ? 1
+                        : NC <= 2                  ? 4
+                                                   : 3;
 
-// Floats between the warps' sums in shared memory (bf16: in their rings).
+// Floats between the warps' sums in shared memory (bf16: in their rings); row_again takes three a lane.
 template <typename T, int NC>
-__host__ __device__ __forceinline__ int warp_floats(int queries, int Dp) { return sizeof(T) == 4 ? queries * Dp : kWarpBytes<NC> / 4; }
+__host__ __device__ __forceinline__ int warp_floats(int queries, int Dp) { return sizeof(T) == 4 ? max(queries * Dp, 96) : kWarpBytes<NC> / 4; }
 
 // Floats of a new key's values (ONE) and the queries.
 template <typename T, int NC, int NQ, bool ONE>
 __host__ __device__ __forceinline__ int beside_floats(int Dp)
 {
     return sizeof(T) == 4 ? NQ * Dp : (ONE ? Dp : 0) + kQRows<NC, NQ, ONE> * kQPitch<NC> / 2;
-}
-
-// Entries of a page table that the blocks keep in shared memory (8 KB, with which as many blocks fit an SM): none of a larger one,
-// whose first looks take 0.1 to 0.4 us more (one query over 64 positions 6.25 against 6.14, five of d_head 128 25.8 and 25.5).
-__host__ __device__ __forceinline__ int small_table(const PagedParams& m)
-{
-    const int64_t n = static_cast<int64_t>(m.B) * m.max_pages;
-    return n <= 2048 ? static_cast<int>(n) : 0;
 }
 
 // Length, position of the first query and queries of sequence b, as the memory stands before the call: with ONE the length
@@ -1077,7 +1074,7 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
     if (ONE) pdl_wait();
 
     // a small page table comes into shared memory beside the lengths: a part's first look then does not wait for one
-    const int entries = small_table(m);
+    const int entries = p.held;
     for (int x = tid; x < entries; x += (32 * NW))
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(small + x)), "l"(m.table + x) : "memory");
     mma::cp_async_commit();
@@ -1241,13 +1238,21 @@ cudaError_t launch_weights(const PagedAttnParams& p, int sm_count, cudaStream_t 
 }
 
 template <typename T, int NC, int NQ, bool ONE>
-cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
+cudaError_t launch(PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
     constexpr int NW = kWarpsOf<T, NC, NQ>;
     static OncePerDevice once;
     const PagedParams& m = p.n.m;
-    const size_t smem = 4 * (static_cast<size_t>(NW) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
-                             static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1) + 4 * static_cast<size_t>(small_table(m));
+    size_t smem = 4 * (static_cast<size_t>(NW) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
+                       static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1);
+    // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its few static bytes besides
+    auto fit = [&](size_t bytes) { return max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (bytes + 1024 + 128)))); };
+    const int per_sm = fit(smem);
+    // A page table of up to 8 KB that takes no block's place stands in shared memory: first looks then take 0.1 to 0.4 us less (one
+    // query over 64 positions 6.14 against 6.25, five of d_head 128 25.5 and 25.8).
+    const int64_t entries = static_cast<int64_t>(m.B) * m.max_pages;
+    p.held = entries <= 2048 && smem + 4 * entries <= 224 * 1024 && fit(smem + 4 * entries) == per_sm ? static_cast<int>(entries) : 0;
+    smem += 4 * static_cast<size_t>(p.held);
     cudaError_t e = allow_smem(once, 224 * 1024, paged_attn_kernel<T, NC, NQ, ONE, false>, paged_attn_kernel<T, NC, NQ, ONE, true>);
     if (e != cudaSuccess) return e;
     if (!ONE) {
@@ -1260,8 +1265,6 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
                              copies, share);
         if (e != cudaSuccess) return e;
     }
-    // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its static part besides
-    const int per_sm = max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (smem + 1024 + 32 * NW * 8 + 128))));
     const int blocks = min(per_sm * sm_count, kPagedMaxCtas);
     if (!p.accumulate) return launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, false>, dim3(blocks), dim3(32 * NW), smem, s, p);
     e = launch_dependent(paged_attn_kernel<T, NC, NQ, ONE, true>, dim3(blocks), dim3(32 * NW), smem, s, p);
@@ -1272,7 +1275,7 @@ cudaError_t launch(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 }
 
 template <typename T, int NC>
-cudaError_t by_queries(const PagedAttnParams& p, int sm_count, cudaStream_t s)
+cudaError_t by_queries(PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
     // fp32: queries whose sums fit the registers; bf16: groups of four queries, and one token without preparation (B8 H16 D64 over
     // 4096 positions 38.6 us where two launches took 44.1, one sequence of 65536 with its own distances 84 and 115, when this was
@@ -1287,7 +1290,7 @@ cudaError_t by_queries(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 }
 
 template <typename T>
-cudaError_t by_channels(const PagedAttnParams& p, int sm_count, cudaStream_t s)
+cudaError_t by_channels(PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
     switch (p.Dp / 32) {
     case 1: return by_queries<T, 1>(p, sm_count, s);
@@ -1299,7 +1302,7 @@ cudaError_t by_channels(const PagedAttnParams& p, int sm_count, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_paged_attn(const PagedAttnParams& p, txl_dtype dtype, int sm_count, cudaStream_t s)
+cudaError_t launch_paged_attn(PagedAttnParams& p, txl_dtype dtype, int sm_count, cudaStream_t s)
 {
     return dtype == TXL_F32 ? by_channels<float>(p, sm_count, s) : by_channels<__nv_bfloat16>(p, sm_count, s);
 }
