@@ -587,7 +587,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
  * Calls on one memory must not overlap on the GPU (one stream, or ordered streams), and no tensor that a call writes may
  * overlap one that it reads.
  * Limits (TXL_ERR_UNSUPPORTED): D <= 128; ld <= 65536; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
- * max_pages * page_len below 2^31.  Positions are ints.
+ * max_pages * page_len below 2^31.  Positions are 0 .. 2^31 - 33.
  */
 typedef struct {
     void* k;
@@ -708,8 +708,8 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
  * txl_linear_q4 -- Y = X W' for bf16 X [m][ld_x] (columns 0 .. k-1 are read) and 4-bit weights: txl_linear with a quarter
  * of the weights' bytes, for the projections of a generated token.  Y bf16 [m][ld_y], columns 0 .. n-1 are written.
  * Up to 128 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
- * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry of x that is not finite makes its row of
- * Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
+ * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry of x that is not finite, or above 2^112,
+ * may make its row of Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
  *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
  *            may be NULL when that is 0).  Calls that share a workspace must not overlap on the GPU.
  * Limits: m >= 0 (0: nothing to do), m <= 2^19; ld_x >= k, ld_y >= n.  err_flag as txl_linear.

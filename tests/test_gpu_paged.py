@@ -313,6 +313,49 @@ def test_a_token_without_room_leaves_the_sequence(txl):
         assert torch.equal(mem.weight[others.cuda()], before[others.cuda()])
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_tokens_whose_second_page_is_missing(txl, dtype):
+    """Sixteen tokens that begin in a page the sequence has and end in one it lacks: it is left as it was."""
+    from transformer_xl_relative_gb300 import native
+    ref = Pages(3, 2, 64, [25, 25, 16], 16, dtype, room=16)
+    q, k, v, u, vb, r = new(3, 16, 2, 64, dtype, 4, 60)
+    mem = ref.to_gpu(txl)
+    mem.table[1, 2] = -1
+    out = torch.full_like(q, 5.0)
+    txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 60, 59, out)
+    with pytest.raises(txl.TxlError) as e:
+        mem.check()
+    assert e.value.status == native.TXL_ERR_PAGE
+    counts = torch.tensor([16, 0, 16], dtype=torch.int32)
+    ref.push(k.cpu(), v.cpu(), counts)
+    check_memory(mem, ref, weight=False)
+    assert (out[1] == 5).all()
+    want, tol, *_ = attend(ref, q.cpu(), u, vb, r, 59, counts)
+    assert ((out.cpu().double() - want).abs() <= tol)[[0, 2]].all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_calls_one_after_another(txl, dtype):
+    """Calls of different sizes queued without a pause leave what they leave with a pause after each."""
+    T = [4, 1, 16, 2, 1, 1, 8, 3, 16, 1, 5, 4]
+    ref = Pages(5, 4, 64, [700, 33, 0, 250, 1400], 16, dtype, room=sum(T))
+    args = [new(5, t, 4, 64, dtype, 7 + i, 300) for i, t in enumerate(T)]
+    dev = [[x.cuda() for x in a] for a in args]
+    left = []
+    for pause in (True, False):
+        mem = ref.to_gpu(txl)
+        outs = [torch.full_like(a[0], 5.0) for a in dev]
+        ws = torch.empty(txl.rel_attn_paged_workspace_size(dev[2][0], mem, 300, True), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for (q, k, v, u, vb, r), out in zip(dev, outs):
+            txl.rel_attn_paged(q, mem, k, v, u, vb, r, 300, 299, out, accumulate=True, workspace=ws)
+            if pause:
+                torch.cuda.synchronize()
+        mem.check()
+        left.append([x.clone() for x in (mem.k, mem.v, mem.pos, mem.weight, mem.length, mem.next_pos, *outs)])
+    assert all(same(a, b) for a, b in zip(*left))
+
+
 def test_as_many_sequences_as_a_memory_holds(txl):
     """B = 4096 at the widest head and most tokens: the blocks' shared memory at its largest."""
     B, T = 4096, 16
@@ -459,6 +502,24 @@ def test_evict_again_and_missing_pages(txl):
         mem.check()
     assert e.value.status == native.TXL_ERR_PAGE
     assert mem.length.tolist() == [10, kept]
+
+
+def test_room_after_an_eviction(txl):
+    """No sequence has room for more than it kept; what was reserved and not pushed is reserved again."""
+    mem = txl.PagedMemory.empty(1, 8, 16, 2, 64)
+    x = torch.randn(1, 60, 2, 64, device="cuda").to(BF)
+    mem.reserve(70)
+    txl.paged_push(mem, x, x)
+    txl.paged_evict(mem, 64, 8)
+    assert mem.reserved == [64] and mem.length.tolist() == [60] and mem.free_pages == 3
+    txl.paged_evict(mem, 20, 8)
+    assert mem.reserved == [20] and mem.length.tolist() == [20] and mem.free_pages == 3
+    mem.trim()
+    assert mem.reserved == [20] and mem.free_pages == 6
+    mem.reserve(60)
+    txl.paged_push(mem, x, x)
+    assert mem.length.tolist() == [80] and mem.next_pos.tolist() == [120]
+    mem.check()
 
 
 # ------------------------------------------------------------------------------------ a run of them

@@ -804,7 +804,8 @@ def paged_evict_workspace_size(mem: PagedMemory) -> int:
 def paged_evict(mem: PagedMemory, keep: int, recent: int = 0, workspace: torch.Tensor | None = None,
                 stream=None) -> PagedMemory:
     """Cut every sequence to `keep` positions (txl_paged_evict): the last `recent` ones and those of the largest
-    weight stay.  The pages stay with their sequences (PagedMemory.trim frees them)."""
+    weight stay.  The pages stay with their sequences (PagedMemory.trim frees them), and no sequence counts as having
+    room reserved for more than `keep` positions: reserve again what was reserved and is not pushed yet."""
     dev = mem.device
     if workspace is None:
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
