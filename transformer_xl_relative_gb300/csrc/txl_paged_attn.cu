@@ -654,8 +654,17 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     }
 }
 
-// fp32, CUDA cores.  Lane (g, t) takes keys g and g + 8 of a tile and channels 4 (t + 4 j) .. + 3; each of the eight g keeps
-// maximum and sums of its own, which meet at the end.  NQ queries at a time: their sums stay in registers.
+// fp32, CUDA cores.  A warp takes its tiles by halves of 8 keys through a ring of its own; lane (g, t) takes key g and channels
+// 4 (t + 4 j) .. + 3; each of the eight g keeps maximum and sums of its own, which meet at the end.  NQ queries at a time: their
+// sums stay in registers, and their chains of instructions run beside one another.  Rows are 16 floats more than their
+// channels apart: two rows' units of four lanes lie in different banks.  A key that a query does not see has weight 0; if its
+// value is not finite, row_again computes the row.  Bound by shared memory and the chains of a half (B8 H16 D64 over 2048
+// positions: one query 44 us, 4 queries 52, 16 queries 173; with rows loaded into registers one half ahead, query after query, 45,
+// 62 and 226).
+constexpr int kHalf = kPageUnit / 2;
+template <int NC> constexpr int kHalfStages = NC <= 2 ? 3 : 2;
+template <int NC> constexpr int kHalfPitch = 32 * NC + 16;                // floats
+template <int NC> constexpr int kHalfStage = 2 * kHalf * kHalfPitch<NC>;  // K and V of half a tile
 template <int NC, int NQ, bool W, int NW>
 __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a, float* buf, int share, float* bml, float* qs)
 {
@@ -663,12 +672,63 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
     const PagedParams& m = p.n.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int T = p.n.T, D = m.D;
+    float* ring = buf + NW * share + warp * (kHalfStages<NC> * kHalfStage<NC>);
+    // units of 16 bytes that lie past D wholly are never copied
+    constexpr int kUnits = 8 * NC, kPieces = kHalf * kUnits / 32;
+    for (int x = lane; x < kHalfStages<NC> * 2 * kHalf * kUnits; x += 32)
+        if (x % kUnits * 4 >= D) *reinterpret_cast<float4*>(ring + x / kUnits * kHalfPitch<NC> + x % kUnits * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
     pdl_wait();
     for (int i0 = 0; i0 < a.n; i0 += NQ) {
         __syncthreads();
         for (int x = threadIdx.x; x < NQ * p.Dp; x += (32 * NW)) {
             const int i = i0 + x / p.Dp, d = x % p.Dp;
             qs[x] = i < a.n && d < D ? (static_cast<const float*>(p.q)[a.b * p.q_sb + i * p.q_st + a.h * p.q_sh + d] + p.u[a.h * D + d]) * p.qscale : 0.f;
+        }
+        // u / 2 is the warp's tile, u % 2 its half.  Keys and values are copied two halves ahead, positions loaded two, position
+        // terms one.
+        Tiles<NW> tiles;
+        tiles.look(m, a, a.t0 + warp, lane);
+        const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + NW - 1) / NW) : 0;
+        constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
+        auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * NW; };
+        auto copy = [&](int u, int stage) {
+            const int64_t at = tiles.kv(m, a, tile_of(u), lane);
+            const int rows = at < 0 ? 0 : a.len - tile_of(u) * kPageUnit - u % 2 * kHalf;      // that hold something
+            const int64_t off = max(at, static_cast<int64_t>(0));
+            const float* k = static_cast<const float*>(m.k) + off;
+            const float* v = static_cast<const float*>(m.v) + off;
+            float* to = ring + stage * kHalfStage<NC>;
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int x = lane + 32 * j, row = x / kUnits, d = x % kUnits * 4;
+                if (d >= D) continue;
+                const bool held = row < rows;
+                const int from = held ? (u % 2 * kHalf + row) * m.ld + d : 0, bytes = held ? min(16, 4 * (D - d)) : 0;
+                const uint32_t dst = smem_u32(to + row * kHalfPitch<NC> + d);
+                copy16(dst, k + from, bytes);
+                copy16(dst + kHalf * kHalfPitch<NC> * 4, v + from, bytes);
+            }
+        };
+        auto load_pos = [&](int u) {
+            const int at = tiles.pos(m, a, tile_of(u), lane), row = u % 2 * kHalf + g;
+            return at >= 0 && tile_of(u) * kPageUnit + row < a.len ? m.pos[at + row] : kAhead;
+        };
+        const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i0;
+        float e[NQ];
+        auto load_e = [&](int pos) {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                e[x] = i0 + x < a.n && pos <= a.first + i0 + x ? p.E[(er + x) * p.e_pitch + term(p, a.first + i0 + x, pos)] : kNone;
+        };
+#pragma unroll
+        for (int u = 0; u < kHalfStages<NC> - 1; ++u) {
+            if (u < halves) copy(u, u);
+            mma::cp_async_commit();
+        }
+        int pos = kAhead;
+        if (halves) {
+            load_e(load_pos(0));
+            pos = load_pos(1);
         }
         __syncthreads();
         float o[NQ][NJ][4], mx[NQ], sum[NQ];
@@ -679,100 +739,72 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
 #pragma unroll
             for (int j = 0; j < NJ; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
         }
-        // half a tile at a time: u / 2 is the warp's tile, u % 2 its half.  Keys, values and position terms are loaded one half
-        // ahead, positions two.
-        Tiles<NW> tiles;
-        tiles.look(m, a, a.t0 + warp, lane);
-        const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + NW - 1) / NW) : 0;
-        constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
-        auto tile_of = [&](int u) { return a.t0 + warp + u / 2 * NW; };
-        auto load_kv = [&](int u, float4* k, float4* v) {
-            const int row = u % 2 * 8 + g, slot = tile_of(u) * kPageUnit + row;
-            const int64_t tile_at = tiles.kv(m, a, tile_of(u), lane);
-            const bool held = tile_at >= 0 && slot < a.len;
-            const int64_t at = held ? tile_at + row * m.ld : 0;
+        int stage = 0, ahead = kHalfStages<NC> - 1;
+        for (int u = 0; u < halves; ++u) {
+            copies_wait<kHalfStages<NC> - 2>();
+            __syncwarp();                                      // everyone's pieces are here, and the last stage is read
+            if (u + kHalfStages<NC> - 1 < halves) copy(u + kHalfStages<NC> - 1, ahead);
+            mma::cp_async_commit();
+            ahead = stage;
+            const float* k = ring + stage * kHalfStage<NC> + g * kHalfPitch<NC> + 4 * t;
+            stage = stage + 1 == kHalfStages<NC> ? 0 : stage + 1;
+            float s[NQ] = {};
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const int d = 4 * (t + 4 * j);
-                k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (held && d < D) {
-                    k[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.k) + at + d);
-                    v[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(m.v) + at + d);
+                const float4 y = *reinterpret_cast<const float4*>(k + 16 * j);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const float4 w = *reinterpret_cast<const float4*>(qs + x * p.Dp + 4 * (t + 4 * j));
+                    s[x] = fmaf(w.w, y.w, fmaf(w.z, y.z, fmaf(w.y, y.y, fmaf(w.x, y.x, s[x]))));
                 }
             }
-        };
-        auto load_pos = [&](int u) {
-            const int at = tiles.pos(m, a, tile_of(u), lane), row = u % 2 * 8 + g;
-            return at >= 0 && tile_of(u) * kPageUnit + row < a.len ? m.pos[at + row] : kAhead;
-        };
-        const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i0;
-        auto load_e = [&](int pos, float* e) {
 #pragma unroll
-            for (int x = 0; x < NQ; ++x)
-                e[x] = i0 + x < a.n && pos <= a.first + i0 + x ? p.E[(er + x) * p.e_pitch + term(p, a.first + i0 + x, pos)] : kNone;
-        };
-        float4 k[NJ], v[NJ];
-        float e[NQ];
-        int pos = kAhead;
-        if (halves) {
-            load_kv(0, k, v);
-            load_e(load_pos(0), e);
-            pos = load_pos(1);
-        }
-        for (int u = 0; u < halves; ++u) {
-            float4 kn[NJ], vn[NJ];
-            float en[NQ];
+            for (int x = 0; x < NQ; ++x) s[x] += __shfl_xor_sync(0xffffffffu, s[x], 1);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) s[x] += __shfl_xor_sync(0xffffffffu, s[x], 2);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) s[x] = e[x] == kNone ? kNone : s[x] + e[x];
             if (u + 1 < halves) {
-                load_kv(u + 1, kn, vn);
-                load_e(pos, en);
+                load_e(pos);
                 if (u + 2 < halves) pos = load_pos(u + 2);
             }
+            if (W && t == 0) {
+                const int slot = tile_of(u) * kPageUnit + u % 2 * kHalf + g;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int d = 4 * (t + 4 * j);
-                if (d + 1 >= D) k[j].y = 0.f;                  // a row's padding is anything
-                if (d + 2 >= D) k[j].z = 0.f;
-                if (d + 3 >= D) k[j].w = 0.f;
+                for (int x = 0; x < NQ; ++x)
+                    if (i0 + x < a.n && slot < a.len) p.S[(er + x) * p.cap + slot] = s[x];
+            }
+            // the maximum follows only where a score is far above it: a weight may be up to 2^kSlack
+            constexpr float kSlack = 8.f;
+            bool grows = false;
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) grows |= s[x] > mx[x] + kSlack;
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const float now = fmaxf(mx[x], s[x]), f = exp2f(mx[x] - finite_or_0(now));
+                    mx[x] = now;
+                    sum[x] *= f;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) { o[x][j][0] *= f; o[x][j][1] *= f; o[x][j][2] *= f; o[x][j][3] *= f; }
+                }
             }
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const float4 w = *reinterpret_cast<const float4*>(qs + x * p.Dp + 4 * (t + 4 * j));
-                    s = fmaf(w.w, k[j].w, fmaf(w.z, k[j].z, fmaf(w.y, k[j].y, fmaf(w.x, k[j].x, s))));
-                }
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                const bool seen = e[x] != kNone;
-                s = seen ? s + e[x] : kNone;
-                if (W && t == 0 && i0 + x < a.n) {
-                    const int slot = tile_of(u) * kPageUnit + u % 2 * 8 + g;
-                    if (slot < a.len) p.S[(er + x) * p.cap + slot] = s;
-                }
-                if (seen) {
-                    if (!(s <= mx[x])) {
-                        const float now = fmaxf(mx[x], s), f = exp2f(mx[x] - finite_or_0(now));
-                        mx[x] = now;
-                        sum[x] *= f;
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j) { o[x][j][0] *= f; o[x][j][1] *= f; o[x][j][2] *= f; o[x][j][3] *= f; }
-                    }
-                    const float pr = exp2f(s - finite_or_0(mx[x]));
-                    sum[x] += pr;
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        o[x][j][0] = fmaf(pr, v[j].x, o[x][j][0]);
-                        o[x][j][1] = fmaf(pr, v[j].y, o[x][j][1]);
-                        o[x][j][2] = fmaf(pr, v[j].z, o[x][j][2]);
-                        o[x][j][3] = fmaf(pr, v[j].w, o[x][j][3]);
-                    }
-                }
+                s[x] = exp2f(s[x] - finite_or_0(mx[x]));
+                sum[x] += s[x];
             }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) { k[j] = kn[j]; v[j] = vn[j]; }
+            for (int j = 0; j < NJ; ++j) {
+                const float4 y = *reinterpret_cast<const float4*>(k + kHalf * kHalfPitch<NC> + 16 * j);
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) e[x] = en[x];
+                for (int x = 0; x < NQ; ++x) {
+                    o[x][j][0] = fmaf(s[x], y.x, o[x][j][0]);
+                    o[x][j][1] = fmaf(s[x], y.y, o[x][j][1]);
+                    o[x][j][2] = fmaf(s[x], y.z, o[x][j][2]);
+                    o[x][j][3] = fmaf(s[x], y.w, o[x][j][3]);
+                }
+            }
         }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
@@ -1013,7 +1045,7 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
 template <typename T, int NC, int NQ> constexpr int kWarpsOf = sizeof(T) == 2 && (NQ > 2 || (NC > 2 && NQ > 1)) ? 8 : 4;
 // Blocks of the attention that an SM holds: what registers (bf16: and the rings) of the variants leave room for.
 template <typename T, int NC, int NQ>
-constexpr int kBlocks = sizeof(T) == 4             ? (NQ == 1 && NC == 1 ? 4 : NQ == 1 && NC == 2 ? 3 : 2)
+constexpr int kBlocks = sizeof(T) == 4             ? (NQ > 4 ? 4 - NC : NC == 1 ? 4 : NC == 2 || NQ == 1 ? 3 : 2)
                         : kWarpsOf<T, NC, NQ> == 8 ? 1
                         : NC <= 2                  ? 4
                                                    : 3;
@@ -1021,6 +1053,9 @@ constexpr int kBlocks = sizeof(T) == 4             ? (NQ == 1 && NC == 1 ? 4 : N
 // Floats between the warps' sums in shared memory (bf16: in their rings); row_again takes three a lane.
 template <typename T, int NC>
 __host__ __device__ __forceinline__ int warp_floats(int queries, int Dp) { return sizeof(T) == 4 ? max(queries * Dp, 96) : kWarpBytes<NC> / 4; }
+
+// Floats of a warp's ring that lie behind all warps' sums (bf16: none, the sums are in the ring).
+template <typename T, int NC> constexpr int kOwnRing = sizeof(T) == 4 ? kHalfStages<NC> * kHalfStage<NC> : 0;
 
 // Floats of a new key's values (ONE) and the queries.
 template <typename T, int NC, int NQ, bool ONE>
@@ -1046,7 +1081,7 @@ __device__ __forceinline__ int3 now_of(const PagedAttnParams& p, int b)
     return make_int3(ok ? len + n : len, next, ok ? n : 0);
 }
 
-// Shared memory: the warps' rings or sums; a new key's values; queries; maxima and weights; where the
+// Shared memory: the warps' rings (fp32: their sums, then their rings); a new key's values; queries; maxima and weights; where the
 // sequences' pairs begin [B + 1] (64 bits); the sequences' lengths and first positions [B]; a small page table.
 template <typename T, int NC, int NQ, bool ONE, bool W>
 __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ>)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
@@ -1057,7 +1092,7 @@ __global__ void __launch_bounds__((32 * kWarpsOf<T, NC, NQ>), (kBlocks<T, NC, NQ
     const PagedParams& m = p.n.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pitch = warp_floats<T, NC>(p.n.T, p.Dp);
-    float* beside = buf + NW * pitch;
+    float* beside = buf + NW * (pitch + kOwnRing<T, NC>);
     float* bml = beside + beside_floats<T, NC, NQ, ONE>(p.Dp);
     int64_t* start = reinterpret_cast<int64_t*>(bml + ((NW + 1) * p.n.T * 2 + 3) / 4 * 4);
     int2* info = reinterpret_cast<int2*>(start + m.B + 1);
@@ -1243,8 +1278,9 @@ cudaError_t launch(PagedAttnParams& p, int sm_count, cudaStream_t s)
     constexpr int NW = kWarpsOf<T, NC, NQ>;
     static OncePerDevice once;
     const PagedParams& m = p.n.m;
-    size_t smem = 4 * (static_cast<size_t>(NW) * warp_floats<T, NC>(p.n.T, p.Dp) + beside_floats<T, NC, NQ, ONE>(p.Dp) +
-                       static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) + 8 * (2 * static_cast<size_t>(m.B) + 1);
+    size_t smem = 4 * (static_cast<size_t>(NW) * (warp_floats<T, NC>(p.n.T, p.Dp) + kOwnRing<T, NC>) +
+                       beside_floats<T, NC, NQ, ONE>(p.Dp) + static_cast<size_t>(NW + 1) * 2 * p.n.T + 2) +
+                  8 * (2 * static_cast<size_t>(m.B) + 1);
     // all blocks at once: 228 KB of an SM, of which each block takes 1 KB and its few static bytes besides
     auto fit = [&](size_t bytes) { return max(1, min(kBlocks<T, NC, NQ>, static_cast<int>(228 * 1024 / (bytes + 1024 + 128)))); };
     const int per_sm = fit(smem);
@@ -1277,11 +1313,13 @@ cudaError_t launch(PagedAttnParams& p, int sm_count, cudaStream_t s)
 template <typename T, int NC>
 cudaError_t by_queries(PagedAttnParams& p, int sm_count, cudaStream_t s)
 {
-    // fp32: queries whose sums fit the registers; bf16: groups of four queries, and one token without preparation (B8 H16 D64 over
+    // fp32: as many queries at a time as the registers hold sums of (d_head 64, 16 queries: 173 us, by fours 226 when loads were
+    // into registers; d_head 128, 4 queries: 85 us, by twos 127); bf16: groups of four queries, and one token without preparation (B8 H16 D64 over
     // 4096 positions 38.6 us where two launches took 44.1, one sequence of 65536 with its own distances 84 and 115, when this was
     // measured)
     if constexpr (sizeof(T) == 4) {
-        return p.n.T == 1 ? launch<T, NC, 1, false>(p, sm_count, s) : launch<T, NC, NC <= 2 ? 4 : 2, false>(p, sm_count, s);
+        if (p.n.T == 1) return launch<T, NC, 1, false>(p, sm_count, s);
+        return p.n.T <= 4 ? launch<T, NC, 4, false>(p, sm_count, s) : launch<T, NC, (NC <= 2 ? 8 : 4), false>(p, sm_count, s);
     } else {
         if (p.n.T == 1) return launch<T, NC, 1, true>(p, sm_count, s);
         if (p.n.T <= 4) return launch<T, NC, 1, false>(p, sm_count, s);
