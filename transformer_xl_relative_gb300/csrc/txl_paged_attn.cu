@@ -848,14 +848,16 @@ template <typename T> __device__ __forceinline__ T* out_row(const PagedAttnParam
 }
 
 // One query's row again, key by key on the CUDA cores: its sums are not finite, and a value that is not finite at a key
-// that the query does not see must not reach it (0 times infinity).  The whole block calls; tot: a float and a pointer for each
-// of its threads.
+// that the query does not see must not reach it (0 times infinity).  A score of -inf comes of the tensor cores as NaN where the
+// lower one of the query's two bf16 parts is zero or has the other sign, so the scores and their log-sum-exp, of which the
+// weights are made, are written again too.  The whole block calls; tot: a float and a pointer for each of its threads.
 template <typename T, int NW>
 __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, bool terms, float* tot)
 {
     const PagedParams& m = p.n.m;
     const T* q = static_cast<const T*>(p.q) + a.b * p.q_sb + i * p.q_st + a.h * p.q_sh;
-    const float* E = p.E + ((static_cast<int64_t>(a.b) * m.H + a.h) * p.n.T + i) * p.e_pitch;
+    const int64_t row0 = (static_cast<int64_t>(a.b) * m.H + a.h) * p.n.T + i;
+    const float* E = p.E + row0 * p.e_pitch;
     const int at = a.first + i, keys = a.len + (a.own ? 1 : 0);
     // slot s, or the new key behind the last; null where there is none
     auto row = [&](int s, bool value) -> const T* {
@@ -899,6 +901,7 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += (32 * NW)) {
         const int s = s0 + threadIdx.x;
         const float x = score(s);
+        if (p.accumulate && s < keys) p.S[row0 * p.cap + s] = x;
         __syncthreads();
         // (a key that is seen and scores -inf weighs 0 as well; its values count as unseen)
         tot[threadIdx.x] = x == kNone ? 0.f : exp2f(x - top);
@@ -913,6 +916,7 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
         }
     }
     if (d < m.D) out_row<T>(p, a, i)[d] = from_f<T>(sum == 0.f ? 0.f : o / sum);
+    if (p.accumulate && d == 0) p.lse[row0] = top + log2f(sum);
     __syncthreads();
 }
 
