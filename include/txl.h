@@ -708,8 +708,8 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
  * txl_linear_q4 -- Y = X W' for bf16 X [m][ld_x] (columns 0 .. k-1 are read) and 4-bit weights: txl_linear with a quarter
  * of the weights' bytes, for the projections of a generated token.  Y bf16 [m][ld_y], columns 0 .. n-1 are written.
  * Up to 128 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
- * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry of x that is not finite, or above 2^112,
- * may make its row of Y NaN).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
+ * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry whose fp32 sums are not finite is computed
+ * again in double precision, so that any finite X and weights give the product, slower).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
  *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
  *            may be NULL when that is 0).  Calls that share a workspace must not overlap on the GPU.
  * Limits: m >= 0 (0: nothing to do), m <= 2^19; ld_x >= k, ld_y >= n.  err_flag as txl_linear.

@@ -73,6 +73,33 @@ template <int NT, int MT, int SUB> struct Q4Stage {
 };
 template <int NT, int MT, int SUB> constexpr int kQ4Ring = kQ4Stages * static_cast<int>(sizeof(Q4Stage<NT, MT, SUB>));
 
+// One entry of Y again, by a warp, as the sum of x times what the codes stand for in double precision: its fp32 sums are not
+// finite, which 128 step sum x and step sum x c (beyond fp32 from steps of 2.6e36 or x of 2^112 on) may be where Y is.  A lane
+// takes the four k of a word.
+__device__ __noinline__ float entry_again(const LinearQ4Params& p, int row, int n)
+{
+    const int lane = threadIdx.x & 31, t = lane >> 2 & 3, s = lane & 3, nt = n / kQ4N, c = n % kQ4N, high = c >> 3;
+    const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+    const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ld_x;
+    double y = 0.0;
+#pragma unroll 4
+    for (int kb = lane >> 4; kb < kb_all; kb += 2) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + code_block(nt, kb, kb_all) * 32 + (c & 7) * 4 + t)[s];
+        const int k = kb * kQ4K + 32 * (s >> 1) + 8 * t + 4 * (s & 1);
+        const uint32_t both = p.par[par_block(nt, min(k / p.group, groups - 1), groups) * 16 + c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i < p.k) {
+                const int j = (i & 2) + 4 * (i & 1) + high;
+                y += static_cast<double>(mma::bf16_lo(x[k + i])) *
+                     fma(static_cast<double>(mma::bf16_lo(both)), static_cast<double>(w >> (4 * j) & 15u), static_cast<double>(mma::bf16_hi(both)));
+            }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+    return static_cast<float>(y);
+}
+
 // A block of threads computes 16 NT columns of Y for 8 MT rows: its warps take turns over the blocks of k, three ahead, and
 // their sums meet in shared memory.
 // The products see 128 + c; what that adds, 128 step sum x, leaves with the minimum: lo - 128 step times sum x, which an mma
@@ -204,13 +231,20 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[warp][16 * b + g + 8 * (e >> 1)][8 * a + 2 * t + (e & 1)] = tot[b][a][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * NT * rows; i += blockDim.x) {
-        const int row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
-        if (n >= p.n) continue;
+    for (int i0 = 32 * warp; i0 < 16 * NT * rows; i0 += blockDim.x) {
+        const int i = i0 + lane, row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
+        const bool mine = i < 16 * NT * rows && n < p.n;
         float s = 0.f;
+        if (mine) {
 #pragma unroll 4
-        for (int w = 0; w < warps; ++w) s += red[w][col][row];
-        static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
+            for (int w = 0; w < warps; ++w) s += red[w][col][row];
+        }
+        for (uint32_t again = __ballot_sync(0xffffffffu, !isfinite(s)); again; again &= again - 1) {
+            const int z = __ffs(again) - 1;
+            const float y = entry_again(p, row0 + (i0 + z) / (16 * NT), nt0 * kQ4N + (i0 + z) % (16 * NT));
+            if (lane == z) s = y;
+        }
+        if (mine) static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
     }
 }
 
