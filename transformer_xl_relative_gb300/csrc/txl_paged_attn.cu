@@ -852,12 +852,11 @@ template <typename T> __device__ __forceinline__ T* out_row(const PagedAttnParam
 // lower one of the query's two bf16 parts is zero or has the other sign, so the scores and their log-sum-exp, of which the
 // weights are made, are written again too.  The whole block calls; tot: a float and a pointer for each of its threads.
 template <typename T, int NW>
-__device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, bool terms, float* tot)
+__device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, int i, float* tot)
 {
     const PagedParams& m = p.n.m;
     const T* q = static_cast<const T*>(p.q) + a.b * p.q_sb + i * p.q_st + a.h * p.q_sh;
     const int64_t row0 = (static_cast<int64_t>(a.b) * m.H + a.h) * p.n.T + i;
-    const float* E = p.E + row0 * p.e_pitch;
     const int at = a.first + i, keys = a.len + (a.own ? 1 : 0);
     // slot s, or the new key behind the last; null where there is none
     auto row = [&](int s, bool value) -> const T* {
@@ -873,14 +872,14 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
         if (!k) return kNone;
         const int pos = s == a.len ? at : m.pos[static_cast<int64_t>(page_of(m, a.b, s)) * m.page_len + s % m.page_len];
         if (pos > at) return kNone;
-        const int distance = term(p, at, pos);
-        const T* r = static_cast<const T*>(p.r) + a.h * p.r_head + distance * p.r_row;
+        // (E would not do: it comes of two bf16 parts as well)
+        const T* r = static_cast<const T*>(p.r) + a.h * p.r_head + term(p, at, pos) * p.r_row;
         float x = 0.f;
         for (int d = 0; d < m.D; ++d) {
             x = fmaf((to_f(q[d]) + p.u[a.h * m.D + d]) * p.qscale, to_f(k[d]), x);
-            if (!terms) x = fmaf((to_f(q[d]) + p.vb[a.h * m.D + d]) * p.qscale, to_f(r[d]), x);
+            x = fmaf((to_f(q[d]) + p.vb[a.h * m.D + d]) * p.qscale, to_f(r[d]), x);
         }
-        return terms ? x + E[distance] : x;
+        return x;
     };
     float top = kNone;
     bool nan = false;
@@ -1039,7 +1038,7 @@ __device__ __forceinline__ void join(const PagedAttnParams& p, const Part& a, fl
         }
     }
     __syncthreads();
-    for (int bits = again; bits; bits &= bits - 1) row_again<T, NW>(p, a, __ffs(bits) - 1, !ONE, buf);
+    for (int bits = again; bits; bits &= bits - 1) row_again<T, NW>(p, a, __ffs(bits) - 1, buf);
     __syncthreads();
 }
 
