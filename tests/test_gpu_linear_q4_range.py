@@ -88,3 +88,11 @@ def test_not_a_number_stays_in_its_row_and_column(txl):
     assert torch.equal(torch.isnan(y), torch.isnan(want))
     inf = torch.isinf(want)
     assert bool(inf[2].any()) and torch.equal(y[inf], want[inf])
+
+
+def test_no_rows(txl):
+    """A step with no sequence in it."""
+    w = txl.QuantWeight.quantise(weights(64, 24).cuda())
+    assert txl.linear_q4(torch.empty(0, 64, dtype=BF, device="cuda"), w).shape == (0, 24)
+    y = torch.empty(0, 24, dtype=BF, device="cuda")
+    assert txl.linear_q4(torch.empty(0, 64, dtype=BF, device="cuda"), w, y) is y

@@ -1,0 +1,17 @@
+"""CPU tests of the paged memory's and the 4-bit weights' entry points at the ends of their ranges: empty batches, the most
+slots, and workspaces against what a memory holds."""
+import ctypes
+
+from test_paged_abi import FAKE, native  # noqa: F401  (`native` is the fixture)
+
+
+def test_no_rows_through_the_codes(native):  # noqa: F811
+    """An empty tensor has no address: a product of no rows is done all the same, and the shape is still checked."""
+    lib = native.load()
+    w = native.TxlQ4(FAKE, 64, 32, 64)
+    call = lambda **kw: lib.txl_linear_q4(*{**dict(m=0, w=ctypes.byref(w), X=None, ldx=64, Y=None, ldy=32, ws=None, size=0,
+                                                   err=None, stream=None), **kw}.values())
+    assert call() == native.TXL_OK
+    assert call(ldx=63) == native.TXL_ERR_INVALID_ARG and call(ldy=31) == native.TXL_ERR_INVALID_ARG
+    assert call(m=1) == native.TXL_ERR_INVALID_ARG and call(m=1, X=FAKE) == native.TXL_ERR_INVALID_ARG
+    assert call(w=ctypes.byref(native.TxlQ4(None, 64, 32, 64))) == native.TXL_ERR_INVALID_ARG

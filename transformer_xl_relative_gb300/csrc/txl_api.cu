@@ -1534,10 +1534,11 @@ txl_status txl_linear_q4(int m, const txl_q4* w, const void* X, int64_t ld_x, vo
 {
     txl_status st = check_q4(w);
     if (st != TXL_OK) return st;
-    if (m < 0 || !X || !Y || ld_x < w->k || ld_y < w->n) return TXL_ERR_INVALID_ARG;
+    if (m < 0 || ld_x < w->k || ld_y < w->n) return TXL_ERR_INVALID_ARG;
+    if (m == 0) return TXL_OK;                                 // (X and Y are empty then, and may have no address)
+    if (!X || !Y) return TXL_ERR_INVALID_ARG;
     if (m > (1 << 19)) return TXL_ERR_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y)) & 1u) return TXL_ERR_ALIGNMENT;
-    if (m == 0) return TXL_OK;
     const bool rows16 = a16(X) && s16(ld_x, 2);
     const size_t need = txl_linear_q4_workspace_size(m, w);
     if (need && (!workspace || workspace_bytes < need)) return TXL_ERR_WORKSPACE;
