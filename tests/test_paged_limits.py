@@ -2,7 +2,7 @@
 slots, and workspaces against what a memory holds."""
 import ctypes
 
-from test_paged_abi import FAKE, native  # noqa: F401  (`native` is the fixture)
+from test_paged_abi import FAKE, attn, native, paged, push  # noqa: F401  (`native` is the fixture)
 
 
 def test_no_rows_through_the_codes(native):  # noqa: F811
@@ -15,3 +15,11 @@ def test_no_rows_through_the_codes(native):  # noqa: F811
     assert call(ldx=63) == native.TXL_ERR_INVALID_ARG and call(ldy=31) == native.TXL_ERR_INVALID_ARG
     assert call(m=1) == native.TXL_ERR_INVALID_ARG and call(m=1, X=FAKE) == native.TXL_ERR_INVALID_ARG
     assert call(w=ctypes.byref(native.TxlQ4(None, 64, 32, 64))) == native.TXL_ERR_INVALID_ARG
+
+
+def test_no_sequences(native):  # noqa: F811
+    """A memory of no sequences, whose tensors have no addresses."""
+    mem = paged(native, B=0, table=None, length=None, next_pos=None)
+    assert push(native, mem, T=3, k=None, v=None) == native.TXL_OK
+    assert attn(native, mem, q=0, k=0, v=0, out=0) == native.TXL_OK
+    assert push(native, mem, T=-1, k=None, v=None) == native.TXL_ERR_INVALID_ARG

@@ -1401,8 +1401,9 @@ txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl
 {
     const txl_status st = check_paged(mem);
     if (st != TXL_OK) return st;
-    if (T < 0 || (T > 0 && (!view_ok(k_new) || !view_ok(v_new)))) return TXL_ERR_INVALID_ARG;
-    if (T == 0 || mem->B == 0) return TXL_OK;
+    if (T < 0) return TXL_ERR_INVALID_ARG;
+    if (T == 0 || mem->B == 0) return TXL_OK;                  // (k_new and v_new are empty then, and may have no address)
+    if (!view_ok(k_new) || !view_ok(v_new)) return TXL_ERR_INVALID_ARG;
     const uintptr_t odd = reinterpret_cast<uintptr_t>(k_new->ptr) | reinterpret_cast<uintptr_t>(v_new->ptr);
     if (!a4(counts) || (odd & (mem->dtype == TXL_F32 ? 3u : 1u))) return TXL_ERR_ALIGNMENT;
     const PagedPushParams p = paged_push_params(mem, k_new, v_new, T, counts);
