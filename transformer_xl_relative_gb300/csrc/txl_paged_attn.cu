@@ -87,7 +87,7 @@ __device__ __forceinline__ void prep_sequence(const PagedAttnParams& p, int b, i
 // the sum of the two rows' products has 16 bits of the query.  Lane (g, t) loads units t + 4 j of 16 bytes of r's row g as they
 // are; the channels' order in A follows.
 template <int NC>
-__device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h, int f0, int d0, uint16_t* qs)
+__device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h, int f0, int d0, const bool* live, uint16_t* qs)
 {
     constexpr int kWidth = 32 * NC, kRow = kWidth + 8, kEach = kPrepRows / (8 * kWarps);
     const PagedParams& m = p.n.m;
@@ -105,7 +105,7 @@ __device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h,
     for (int e = 0; e < 8 * kWidth / kThreads; ++e) {
         const int x = threadIdx.x + e * kThreads, i = x / kWidth, d = x % kWidth, f = f0 + i, b = f / T;
         float y = 0.f;
-        if (f < m.B * T && d < m.D)
+        if (live[i] && d < m.D)
             y = (__bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[b * p.q_sb + (f - b * T) * p.q_st + h * p.q_sh + d]) + p.vb[h * m.D + d]) * p.qscale;
         const __nv_bfloat16 hi = __float2bfloat16_rn(y);
         qs[i * kRow + d] = __bfloat16_as_ushort(hi);
@@ -135,7 +135,7 @@ __device__ __forceinline__ void prep_terms_bf16(const PagedAttnParams& p, int h,
 // fp32: a warp takes eight distances at a time; lane (g, t) channels 4 (t + 4 j) .. + 3 of distance g, for eight queries
 // whose rows lie in shared memory.
 template <int NC>
-__device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, int f0, int d0, float* q)
+__device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, int f0, int d0, const bool* live, float* q)
 {
     constexpr int NJ = 2 * NC, kWidth = 32 * NC;
     const PagedParams& m = p.n.m;
@@ -143,7 +143,7 @@ __device__ __forceinline__ void prep_terms_f32(const PagedAttnParams& p, int h, 
     const int T = p.n.T, D = m.D, n = min(8, m.B * T - f0);
     for (int x = threadIdx.x; x < 8 * kWidth; x += kThreads) {
         const int e = x / kWidth, d = x % kWidth, f = f0 + e, b = f / T, i = f - b * T;
-        q[x] = e < n && d < D ? (static_cast<const float*>(p.q)[b * p.q_sb + i * p.q_st + h * p.q_sh + d] + p.vb[h * D + d]) * p.qscale : 0.f;
+        q[x] = live[e] && d < D ? (static_cast<const float*>(p.q)[b * p.q_sb + i * p.q_st + h * p.q_sh + d] + p.vb[h * D + d]) * p.qscale : 0.f;
     }
     __syncthreads();
     const float* r = static_cast<const float*>(p.r) + h * p.r_head;
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_const
 {
     __shared__ __align__(16) float qs[sizeof(T) == 4 ? 8 * 32 * NC : 8 * (32 * NC + 8)];
     __shared__ int far;
+    __shared__ bool live[8];                                   // queries that a sequence has (no others are read)
     pdl_wait();
     pdl_launch_dependents();
     const PagedParams& m = p.n.m;
@@ -198,14 +199,15 @@ __global__ void __launch_bounds__(kThreads) paged_prep_kernel(const __grid_const
     // distances beyond the start of all of these sequences are not met (next_pos changes in the attention's kernel)
     if (threadIdx.x == 0) far = 0;
     __syncthreads();
-    const int b0 = f0 / p.n.T, b1 = min(m.B - 1, (f0 + 7) / p.n.T);
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    if (b <= b1 && paged_count(p.n.counts, b, p.n.T) > 0)
-        atomicMax(&far, m.next_pos[b] + (p.n.xk ? p.n.T : 0));
+    if (threadIdx.x < 8) {
+        const int f = f0 + static_cast<int>(threadIdx.x), b = f / p.n.T;
+        live[threadIdx.x] = f < m.B * p.n.T && f - b * p.n.T < paged_count(p.n.counts, b, p.n.T);
+        if (live[threadIdx.x]) atomicMax(&far, m.next_pos[b] + (p.n.xk ? p.n.T : 0));
+    }
     __syncthreads();
     if (d0 >= far) return;
-    if constexpr (sizeof(T) == 4) prep_terms_f32<NC>(p, h, f0, d0, qs);
-    else prep_terms_bf16<NC>(p, h, f0, d0, reinterpret_cast<uint16_t*>(qs));
+    if constexpr (sizeof(T) == 4) prep_terms_f32<NC>(p, h, f0, d0, live, qs);
+    else prep_terms_bf16<NC>(p, h, f0, d0, live, reinterpret_cast<uint16_t*>(qs));
 }
 
 // ---------------------------------------------------------------- attention
