@@ -51,6 +51,69 @@ def test_a_memory_of_no_sequences(txl, dtype):
     assert mem.reserved == [] and mem.free_pages == 4
 
 
+# ------------------------------------------------------------------------------------ gaps
+def test_a_gap_in_a_row_stays_where_it_is(txl):
+    """A page that a table lacks in front of others: what the host writes for any sequence leaves the others' slots alone."""
+    from transformer_xl_relative_gb300 import native
+    L, n = 16, 12
+    mem = txl.PagedMemory.empty(1, n, L, 2, 64)
+    _, k, v, u, vb, r = new(2, 60, 2, 64, BF, 1, 80)
+    table = torch.full((2, 6), -1, dtype=torch.int32)
+    table[0, :3] = torch.tensor([5, 3, 7])
+    table[1, :1] = 2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    whole = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table.cuda(), torch.zeros(2, **i32), torch.zeros(2, **i32))
+    txl.paged_push(whole, k[:, :48], v[:, :48], counts=torch.tensor([48, 9], **i32))
+    table[0, 1] = -1                                           # positions 16 .. 31 are lost
+    mem = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table.cuda(), whole.length.clone(), whole.next_pos.clone())
+    assert mem.free_pages == n - 3 and mem.reserved == [48, 9]
+    mem.reserve([0, 20])
+    assert mem.table[0].tolist() == [5, -1, 7, -1, -1, -1] and mem.table[1, :2].min() >= 0
+    mem.reserve([1, 0])
+    row = mem.table[0].tolist()
+    assert row[:3] == [5, -1, 7] and row[3] >= 0 and row[4:] == [-1, -1] and mem.free_pages == n - 5
+    q, kn, vn, *_ = new(2, 1, 2, 64, BF, 2, 1)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, mem, kn, vn, u.cuda(), vb.cuda(), r.cuda(), 80, 79, out)
+    with pytest.raises(txl.TxlError) as e:
+        mem.check()
+    assert e.value.status == native.TXL_ERR_PAGE
+    ref = Pages(2, 2, 64, [48, 9], L, BF, room=48)
+    for b, m in ((0, 48), (1, 9)):
+        for s in range(m):
+            p, at = ref.at(b, s)
+            ref.k[p, :, at], ref.v[p, :, at], ref.pos[p, at] = k[b, s].cpu(), v[b, s].cpu(), s
+    ref.push(kn.cpu(), vn.cpu())
+    for s in range(16, 32):
+        p, at = ref.at(0, s)
+        ref.pos[p, at] = 1 << 30                               # seen by nobody
+    want, tol, *_ = attend(ref, q.cpu(), u, vb, r, 79)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+    # neither eviction (which leaves a sequence with a gap as it is), nor trim, nor release moves or frees what is not there
+    txl.paged_evict(mem, 20)
+    assert mem.length.tolist() == [49, 10] and mem.reserved[0] == 49
+    mem.trim()
+    assert mem.table[0].tolist() == row and mem.reserved == [49, 10]
+    mem.release(0)
+    assert (mem.table[0] == -1).all() and mem.free_pages == n - 1 and sorted(mem._free) == sorted(set(range(n)) - {int(mem.table[1, 0])})
+
+
+def test_a_gap_behind_the_length_is_filled(txl):
+    """No position is lost there: the next pages of the sequence come from the pool, those behind the gap are free."""
+    mem = txl.PagedMemory.empty(1, 8, 16, 2, 64)
+    table = torch.tensor([[6, -1, 3, 99]], dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    mem = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table, torch.tensor([10], **i32), torch.tensor([10], **i32))
+    assert mem.free_pages == 7 and mem.reserved == [10]
+    mem.reserve(30)
+    row = mem.table[0].tolist()
+    assert row[0] == 6 and len({*row[:3]}) == 3 and min(row[:3]) >= 0 and row[3] == -1 and mem.free_pages == 5
+    _, k, v, *_ = new(1, 30, 2, 64, BF, 1, 1)
+    txl.paged_push(mem, k, v)
+    mem.check()
+    assert mem.length.tolist() == [40]
+
+
 # ------------------------------------------------------------------------------------ what is not read
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("T", [1, 2, 5, 16])

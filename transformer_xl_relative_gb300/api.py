@@ -574,7 +574,10 @@ class PagedMemory:
     page_len], ``table`` int32 [B, max_pages], ``length`` and ``next_pos`` int32 [B], all on one device: slot s of
     sequence b is row s % page_len of page table[b, s // page_len].  Filled by paged_push and rel_attn_paged, cut by
     paged_evict.  The host gives pages to sequences: reserve before positions are pushed, release for a sequence that has
-    ended, trim for pages that an eviction left empty."""
+    ended, trim for pages that an eviction left empty.
+
+    A table may lack pages that a sequence's length spans: those slots count as not there, and their entries stay as they
+    are (-1) when pages are reserved or freed.  Behind the length a sequence has the pages up to the first missing one."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, table: torch.Tensor,
                  length: torch.Tensor, next_pos: torch.Tensor):
@@ -603,11 +606,16 @@ class PagedMemory:
                            length.data_ptr(), next_pos.data_ptr(), at, at + 4 * (B * (H + 1) + 1), B, H, D, ld, n, page_len, most, dtype_code(k))
         self.address = ctypes.addressof(self._c)
         self._shape, self._dtype = (B, H, D), k.dtype
-        rows = table.tolist()
-        used = {p for row in rows for p in row if 0 <= p < n}
-        self._rows = [[p for p in row if 0 <= p < n] for row in rows]              # pages of every sequence
-        self._free = [p for p in range(n - 1, -1, -1) if p not in used]
         self._room = length.tolist()                                               # positions that room was asked for
+        self._rows = []                                                            # pages of every sequence, -1: missing
+        for row, room in zip(table.tolist(), self._room):
+            row = [p if 0 <= p < n else -1 for p in row]
+            end = min(most, (max(room, 0) + page_len - 1) // page_len)
+            while end < most and row[end] >= 0:
+                end += 1
+            self._rows.append(row[:end])
+        used = {p for row in self._rows for p in row}
+        self._free = [p for p in range(n - 1, -1, -1) if p not in used]
 
     @classmethod
     def empty(cls, B, n_pages, page_len, H, D, max_pages=None, dtype=torch.bfloat16, device="cuda"):
@@ -663,7 +671,7 @@ class PagedMemory:
         """Sequence b keeps its first `kept` pages; the others are free (but for those it shares)."""
         gone, self._rows[b] = self._rows[b][kept:], self._rows[b][:kept]
         used = {p for row in self._rows for p in row} if gone else ()
-        self._free.extend(p for p in reversed(gone) if p not in used)
+        self._free.extend(p for p in reversed(gone) if p >= 0 and p not in used)
 
     def release(self, b: int) -> None:
         """Sequence b has ended: it is empty, and its pages are free."""
@@ -805,7 +813,8 @@ def paged_evict(mem: PagedMemory, keep: int, recent: int = 0, workspace: torch.T
                 stream=None) -> PagedMemory:
     """Cut every sequence to `keep` positions (txl_paged_evict): the last `recent` ones and those of the largest
     weight stay.  The pages stay with their sequences (PagedMemory.trim frees them), and no sequence counts as having
-    room reserved for more than `keep` positions: reserve again what was reserved and is not pushed yet."""
+    room reserved for more than `keep` positions: reserve again what was reserved and is not pushed yet.  A sequence that
+    lacks a page is left as it is."""
     dev = mem.device
     if workspace is None:
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
@@ -816,7 +825,7 @@ def paged_evict(mem: PagedMemory, keep: int, recent: int = 0, workspace: torch.T
     st = _on_device(dev, lambda _: _lib().txl_paged_evict(ctypes.byref(mem._c), int(keep), int(recent), workspace.data_ptr(),
                                                           size, raw), None)
     check(st, "txl_paged_evict")
-    mem._room = [min(x, int(keep)) for x in mem._room]
+    mem._room = [x if -1 in row else min(x, int(keep)) for x, row in zip(mem._room, mem._rows)]
     return mem
 
 
