@@ -587,7 +587,7 @@ int txl_rel_attn_qmem_path(int B, int L, int H, int D, const txl_view* q, const 
  * Calls on one memory must not overlap on the GPU (one stream, or ordered streams), and no tensor that a call writes may
  * overlap one that it reads.
  * Limits (TXL_ERR_UNSUPPORTED): D <= 128; ld <= 65536; page_len a multiple of 16; B <= 4096; H <= 65535; n_pages * page_len and
- * max_pages * page_len below 2^31.  Positions are 0 .. 2^31 - 33.
+ * max_pages * page_len, and the T of a push, below 2^31 - 2^20.  Positions are 0 .. 2^31 - 33.
  */
 typedef struct {
     void* k;

@@ -2,6 +2,8 @@
 slots, and workspaces against what a memory holds."""
 import ctypes
 
+import pytest
+
 from test_paged_abi import FAKE, attn, native, paged, push  # noqa: F401  (`native` is the fixture)
 
 
@@ -23,3 +25,16 @@ def test_no_sequences(native):  # noqa: F811
     assert push(native, mem, T=3, k=None, v=None) == native.TXL_OK
     assert attn(native, mem, q=0, k=0, v=0, out=0) == native.TXL_OK
     assert push(native, mem, T=-1, k=None, v=None) == native.TXL_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["n_pages", "max_pages"])
+def test_the_most_slots(native, name):  # noqa: F811
+    """Slots are counted in 32 bits, ahead of the last one too: the last 2^20 below 2^31 are refused, before any launch."""
+    mem = paged(native, page_len=1 << 20, **{name: (1 << 11) - 1})
+    for st in (push(native, mem), attn(native, mem),
+               native.load().txl_paged_evict(ctypes.byref(mem), 4, 0, FAKE, 1 << 40, None)):
+        assert st == native.TXL_ERR_UNSUPPORTED
+    # one page less is taken: the call ends at the workspace, which is the next thing that it looks at
+    mem = paged(native, page_len=1 << 20, **{name: (1 << 11) - 2})
+    assert attn(native, mem, ws=0) == native.TXL_ERR_WORKSPACE
+    assert push(native, paged(native), T=(1 << 31) - (1 << 20)) == native.TXL_ERR_UNSUPPORTED

@@ -1302,7 +1302,7 @@ txl_status check_paged(const txl_paged* m)
         return TXL_ERR_INVALID_ARG;
     if (m->dtype != TXL_F32 && m->dtype != TXL_BF16) return TXL_ERR_INVALID_ARG;
     if (m->D > 128 || m->ld > 65536 || m->page_len % kPageUnit || m->B > kPagedMaxB || m->H > 65535) return TXL_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(m->n_pages) * m->page_len > INT32_MAX || static_cast<int64_t>(m->max_pages) * m->page_len > INT32_MAX)
+    if (static_cast<int64_t>(m->n_pages) * m->page_len > kPagedMaxSlots || static_cast<int64_t>(m->max_pages) * m->page_len > kPagedMaxSlots)
         return TXL_ERR_UNSUPPORTED;
     if (m->B == 0) return TXL_OK;
     if (!m->length || !m->next_pos || !m->scratch || (m->max_pages && !m->table)) return TXL_ERR_INVALID_ARG;
@@ -1404,6 +1404,7 @@ txl_status txl_paged_push(const txl_paged* mem, const txl_view* k_new, const txl
     if (T < 0) return TXL_ERR_INVALID_ARG;
     if (T == 0 || mem->B == 0) return TXL_OK;                  // (k_new and v_new are empty then, and may have no address)
     if (!view_ok(k_new) || !view_ok(v_new)) return TXL_ERR_INVALID_ARG;
+    if (T > kPagedMaxSlots) return TXL_ERR_UNSUPPORTED;
     const uintptr_t odd = reinterpret_cast<uintptr_t>(k_new->ptr) | reinterpret_cast<uintptr_t>(v_new->ptr);
     if (!a4(counts) || (odd & (mem->dtype == TXL_F32 ? 3u : 1u))) return TXL_ERR_ALIGNMENT;
     const PagedPushParams p = paged_push_params(mem, k_new, v_new, T, counts);

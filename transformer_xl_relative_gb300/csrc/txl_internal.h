@@ -351,6 +351,9 @@ cudaError_t launch_qseg_f32(const QattnParams& p, int sm_count, cudaStream_t s);
 // ---------------------------------------------------------------- paged memory
 constexpr int kPageUnit = 16;       // a page holds a multiple of this many positions: the tile of the attention
 constexpr int kPagedMaxB = 4096;    // sequences of a paged memory
+// Slots of a paged memory's pool, of a row of its table, and positions of a call: kernels count them in 32 bits and step past
+// the last one by up to a grid's stride (16 blocks of 128 slots on each SM).
+constexpr int64_t kPagedMaxSlots = (int64_t{1} << 31) - (1 << 20) - 1;
 constexpr int kPagedMaxCtas = 640;  // blocks of the attention over a paged memory, at most (4 on each of 160 SMs)
 
 struct PagedParams {
