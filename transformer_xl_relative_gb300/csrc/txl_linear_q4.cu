@@ -3,7 +3,7 @@
 //
 //     y = sum over groups ( step sum_k x_k c_k + lo sum_k x_k ),     c exact in bf16, sums in fp32
 //
-// 8 rows by 8192 x 8192 (36 MB): 11.4 us, 3.1 TB/s; bound by the ALU that makes operands of the codes (59 of its instructions for 16 columns
+// 8 rows by 8192 x 8192 (36 MB): 10.9 us, 3.3 TB/s; bound by the ALU that makes operands of the codes (59 of its instructions for 16 columns
 // by 64 k; 75 % of its cycles on an SM that has a block).  4096 x 4096 4.7 us; 1024 x 1024 1.8 us, a launch.
 #include <cuda_bf16.h>
 
@@ -66,38 +66,46 @@ __device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, ui
 
 // A stage of a warp's ring in shared memory: codes of NT tiles of columns for one block of k, x of 8 MT rows (each lane copies
 // and reads its own 16 bytes of both), and the tiles' parameters.
-constexpr int kQ4Stages = 4, kQ4MaxWarps = 16;
+constexpr int kQ4Stages = 4;
+template <int MT> constexpr int kQ4MaxWarps = MT == 1 ? 16 : 8;
 template <int NT, int MT, int SUB> struct Q4Stage {
     uint4 w[NT][32], x[MT][2][32];
     uint32_t par[SUB][NT][16];
 };
 template <int NT, int MT, int SUB> constexpr int kQ4Ring = kQ4Stages * static_cast<int>(sizeof(Q4Stage<NT, MT, SUB>));
 
-// One entry of Y again, by a warp, as the sum of x times what the codes stand for in double precision: its fp32 sums are not
-// finite, which 128 step sum x and step sum x c (beyond fp32 from steps of 2.6e36 or x of 2^112 on) may be where Y is.  A lane
-// takes the four k of a word.
-__device__ __noinline__ float entry_again(const LinearQ4Params& p, int row, int n)
+// A warp's entries of a block's `cols` columns and `rows` rows of Y that are not finite again, one after another, as the sum of x times
+// what the codes stand for in double precision: fp32 sums of 128 step x and of step x c (beyond fp32 from steps of 2.6e36 or x of
+// 2^112 on) may be infinite where Y is not.  A lane takes the four k of a word.
+__device__ __noinline__ void entries_again(const LinearQ4Params& p, int row0, int rows, int n0, int cols)
 {
-    const int lane = threadIdx.x & 31, t = lane >> 2 & 3, s = lane & 3, nt = n / kQ4N, c = n % kQ4N, high = c >> 3;
+    const int lane = threadIdx.x & 31, t = lane >> 2 & 3, s = lane & 3;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
-    const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ld_x;
-    double y = 0.0;
-#pragma unroll 4
-    for (int kb = lane >> 4; kb < kb_all; kb += 2) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + code_block(nt, kb, kb_all) * 32 + (c & 7) * 4 + t)[s];
-        const int k = kb * kQ4K + 32 * (s >> 1) + 8 * t + 4 * (s & 1);
-        const uint32_t both = p.par[par_block(nt, min(k / p.group, groups - 1), groups) * 16 + c];
+    for (int i0 = threadIdx.x & ~31; i0 < rows * cols; i0 += blockDim.x)
+        for (int i = i0; i < min(i0 + 32, rows * cols); ++i) {
+            const int n = n0 + i % cols, nt = n / kQ4N, c = n % kQ4N, row = row0 + i / cols;
+            if (n >= p.n) continue;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.y) + row * p.ld_y + n;
+            if (isfinite(__bfloat162float(*out))) continue;
+            const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ld_x;
+            double y = 0.0;
+#pragma unroll 1
+            for (int kb = lane >> 4; kb < kb_all; kb += 2) {
+                const uint32_t w = reinterpret_cast<const uint32_t*>(p.codes + code_block(nt, kb, kb_all) * 32 + (c & 7) * 4 + t)[s];
+                const int k = kb * kQ4K + 32 * (s >> 1) + 8 * t + 4 * (s & 1);
+                const uint32_t both = p.par[par_block(nt, min(k / p.group, groups - 1), groups) * 16 + c];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (k + i < p.k) {
-                const int j = (i & 2) + 4 * (i & 1) + high;
-                y += static_cast<double>(mma::bf16_lo(x[k + i])) *
-                     fma(static_cast<double>(mma::bf16_lo(both)), static_cast<double>(w >> (4 * j) & 15u), static_cast<double>(mma::bf16_hi(both)));
+                for (int e = 0; e < 4; ++e)
+                    if (k + e < p.k) {
+                        const uint32_t code = w >> (4 * ((e & 2) + 4 * (e & 1) + (c >> 3))) & 15u;
+                        y += static_cast<double>(mma::bf16_lo(x[k + e])) *
+                             fma(static_cast<double>(mma::bf16_lo(both)), static_cast<double>(code), static_cast<double>(mma::bf16_hi(both)));
+                    }
             }
-    }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-    return static_cast<float>(y);
+            for (int d = 16; d; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+            if (lane == 0) *out = __float2bfloat16_rn(static_cast<float>(y));
+        }
 }
 
 // A block of threads computes 16 NT columns of Y for 8 MT rows: its warps take turns over the blocks of k, three ahead, and
@@ -106,7 +114,7 @@ __device__ __noinline__ float entry_again(const LinearQ4Params& p, int row, int 
 // with a matrix of ones gives in the same lanes.  Both cost 2^-24 of 128 step sum |x| (2^-16 of a step for each x).
 // VEC: rows of x start on 16-byte boundaries.
 template <int NT, int MT, int SUB, bool VEC>
-__global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __grid_constant__ LinearQ4Params p)
+__global__ void __launch_bounds__(32 * kQ4MaxWarps<MT>) linear_q4_kernel(const __grid_constant__ LinearQ4Params p)
 {
     using Stage = Q4Stage<NT, MT, SUB>;
     extern __shared__ __align__(16) char smem[];
@@ -213,6 +221,8 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
         mma::cp_async_commit();
     }
     int stage = 0;
+    // (rolled up, and with room for 16 warps of 16 rows, the compiler interleaves less: 8 rows by 8192 x 8192 11.5 us, 16 rows 15.9)
+#pragma unroll 8
     for (int kb = warp; kb < kb_all; kb += warps) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kQ4Stages - 2) : "memory");
         __syncwarp();                                          // the parameters are other lanes' copies
@@ -231,21 +241,17 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps) linear_q4_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[warp][16 * b + g + 8 * (e >> 1)][8 * a + 2 * t + (e & 1)] = tot[b][a][e];
     __syncthreads();
-    for (int i0 = 32 * warp; i0 < 16 * NT * rows; i0 += blockDim.x) {
-        const int i = i0 + lane, row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
-        const bool mine = i < 16 * NT * rows && n < p.n;
+    bool again = false;
+    for (int i = threadIdx.x; i < 16 * NT * rows; i += blockDim.x) {
+        const int row = i / (16 * NT), col = i % (16 * NT), n = nt0 * kQ4N + col;
+        if (n >= p.n) continue;
         float s = 0.f;
-        if (mine) {
 #pragma unroll 4
-            for (int w = 0; w < warps; ++w) s += red[w][col][row];
-        }
-        for (uint32_t again = __ballot_sync(0xffffffffu, !isfinite(s)); again; again &= again - 1) {
-            const int z = __ffs(again) - 1;
-            const float y = entry_again(p, row0 + (i0 + z) / (16 * NT), nt0 * kQ4N + (i0 + z) % (16 * NT));
-            if (lane == z) s = y;
-        }
-        if (mine) static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
+        for (int w = 0; w < warps; ++w) s += red[w][col][row];
+        static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
+        again |= !isfinite(s);
     }
+    if (__any_sync(0xffffffffu, again)) entries_again(p, row0, rows, nt0 * kQ4N, 16 * NT);
 }
 
 // ---------------------------------------------------------------- weights
@@ -357,7 +363,7 @@ template <int NT, int MT, int SUB, bool VEC>
 cudaError_t launch_variant(const LinearQ4Params& p, int warps, cudaStream_t s)
 {
     static OncePerDevice once;
-    constexpr int most = 226 * 1024 / kQ4Ring<NT, MT, SUB> < kQ4MaxWarps ? 226 * 1024 / kQ4Ring<NT, MT, SUB> : kQ4MaxWarps;
+    constexpr int most = 226 * 1024 / kQ4Ring<NT, MT, SUB> < kQ4MaxWarps<MT> ? 226 * 1024 / kQ4Ring<NT, MT, SUB> : kQ4MaxWarps<MT>;
     warps = min(warps, most);
     const cudaError_t e = allow_smem(once, most * kQ4Ring<NT, MT, SUB>, linear_q4_kernel<NT, MT, SUB, VEC>);
     if (e != cudaSuccess) return e;
