@@ -659,8 +659,8 @@ typedef struct {
 txl_status txl_rel_attn_paged(const txl_rel_attn_paged_args* args);
 
 /* Bytes of device workspace txl_rel_attn_paged needs for n_rows distances (min(n_rows, clamp_len + 1) are enough): mostly
- * B*H*T floats a distance (not for one bf16 token), with accumulate as many a slot of max_pages pages, and parts of the
- * sums (1280 T rows of D floats).  0 for an invalid shape. */
+ * B*H*T floats a distance (not for one bf16 token), with accumulate H*T floats a slot of the pool (of B * max_pages pages, where those
+ * are fewer), and parts of the sums (1280 T rows of D floats).  0 for an invalid shape. */
 size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate);
 
 /*
@@ -675,7 +675,8 @@ size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows
 txl_status txl_paged_evict(const txl_paged* mem, int keep, int recent, void* workspace, size_t workspace_bytes,
                            void* stream);
 
-/* Bytes of device workspace txl_paged_evict needs: two ints a sequence and slot of half the sequence's capacity. */
+/* Bytes of device workspace txl_paged_evict needs: two ints a sequence and slot of half the sequence's capacity (max_pages * page_len,
+ * which the number of blocks that a sequence is given follows too: a table no wider than the sequences need serves both). */
 size_t txl_paged_evict_workspace_size(const txl_paged* mem);
 
 /*

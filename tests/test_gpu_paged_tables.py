@@ -114,6 +114,58 @@ def test_a_gap_behind_the_length_is_filled(txl):
     assert mem.length.tolist() == [40]
 
 
+# ------------------------------------------------------------------------------------ tables wider than the pool
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T", [1, 3, 9])
+@pytest.mark.parametrize("D,page_len", [(64, 16), (41, 48), (128, 64)])
+def test_weights_over_a_wide_table(txl, dtype, T, D, page_len):
+    """Every row of the table could hold the pool: what scores take follows the pool, and weights are what they were."""
+    ref = Pages(4, 3, D, [300, 0, 70, 16], page_len, dtype, room=T, spare=5, first=[400, 0, 71, 16])
+    n = ref.k.shape[0]
+    narrow = ref.table.clone()
+    ref.table = torch.cat((narrow, torch.full((4, n - narrow.shape[1]), -1, dtype=torch.int32)), 1)
+    q, k, v, u, vb, r = new(4, T, 3, D, dtype, 3, 120)
+    counts = torch.tensor([T, max(1, T - 1), 0, T], dtype=torch.int32)
+    wide = ref.to_gpu(txl)
+    ref.table = narrow
+    slim = ref.to_gpu(txl)
+    outs, before = [], None
+    ref.push(k.cpu(), v.cpu(), counts)
+    before = ref.weight.clone()
+    for mem in (wide, slim):
+        out = torch.full(q.shape, 5.0, dtype=dtype, device="cuda")
+        txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 120, 119, out, counts=counts.cuda(), accumulate=True)
+        outs.append(out)
+        check_against(mem, ref, out, before, q, u, vb, r, 119, counts)
+    assert torch.equal(*outs) and torch.equal(wide.weight, slim.weight)
+    need = txl.rel_attn_paged_workspace_size(q, wide, 120, True) - txl.rel_attn_paged_workspace_size(q, wide, 120, False)
+    assert need <= (n * page_len + 4) * 3 * T * 4 + 64
+
+
+def test_a_missing_page_in_a_wide_table(txl):
+    """A slot without a page has no score: the others' weights are right, and nothing is written for it."""
+    ref = Pages(2, 2, 64, [100, 60], 16, BF, room=3, spare=5)
+    n = ref.k.shape[0]
+    narrow = ref.table.clone()
+    ref.table = torch.cat((narrow, torch.full((2, n - narrow.shape[1]), -1, dtype=torch.int32)), 1)
+    q, k, v, u, vb, r = new(2, 3, 2, 64, BF, 3, 120)
+    mem = ref.to_gpu(txl)
+    mem.table[0, 2] = -7
+    ref.table = narrow
+    out = torch.empty_like(q)
+    ws = torch.zeros(txl.rel_attn_paged_workspace_size(q, mem, 120, True) + 64, dtype=torch.uint8, device="cuda")
+    txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 120, 119, out, accumulate=True, workspace=ws)
+    with pytest.raises(txl.TxlError):
+        mem.check()
+    assert (ws[-64:] == 0).all()
+    ref.push(k.cpu(), v.cpu())
+    before = ref.weight.clone()
+    for s in range(32, 48):
+        p, row = ref.at(0, s)
+        ref.pos[p, row] = 1 << 30
+    check_against(mem, ref, out, before, q, u, vb, r, 119)
+
+
 # ------------------------------------------------------------------------------------ what is not read
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("T", [1, 2, 5, 16])

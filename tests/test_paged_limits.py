@@ -38,3 +38,15 @@ def test_the_most_slots(native, name):  # noqa: F811
     mem = paged(native, page_len=1 << 20, **{name: (1 << 11) - 2})
     assert attn(native, mem, ws=0) == native.TXL_ERR_WORKSPACE
     assert push(native, paged(native), T=(1 << 31) - (1 << 20)) == native.TXL_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [1, 2, 16])
+@pytest.mark.parametrize("B,n_pages,page_len,max_pages", [(32, 2112, 64, 2112), (8, 10, 16, 10), (4096, 5000, 16, 300), (3, 100, 32, 4)])
+def test_scores_take_no_more_than_the_memory_has_slots(native, T, B, n_pages, page_len, max_pages):  # noqa: F811
+    """The scores that `accumulate` keeps: one for each head, query and slot, of the pool or of all rows of the table, whichever
+    are fewer (a wide table, as an empty memory has by default, does not multiply the pool by the batch)."""
+    mem = paged(native, B=B, n_pages=n_pages, page_len=page_len, max_pages=max_pages)
+    size = native.load().txl_rel_attn_paged_workspace_size
+    scores = size(ctypes.byref(mem), T, 6, 1) - size(ctypes.byref(mem), T, 6, 0)
+    slots = min(n_pages, B * max_pages) * page_len
+    assert 0 <= scores - (slots + B) * 4 * T * 4 < 64            # (a log-sum-exp for each head and query of a sequence)

@@ -619,7 +619,8 @@ class PagedMemory:
 
     @classmethod
     def empty(cls, B, n_pages, page_len, H, D, max_pages=None, dtype=torch.bfloat16, device="cuda"):
-        """An empty memory; a sequence may hold up to max_pages pages (all of them by default)."""
+        """An empty memory; a sequence may hold up to max_pages pages (all of them by default).  paged_evict's workspace
+        is four bytes for each position that the B rows of the table could hold: give max_pages where sequences are bounded."""
         unit = 16 // torch.empty(0, dtype=dtype).element_size()
         ld = (D + unit - 1) // unit * unit
         k, v = (torch.zeros(n_pages, H, page_len, ld, dtype=dtype, device=device)[..., :D] for _ in range(2))

@@ -1344,7 +1344,8 @@ PagedPushParams paged_push_params(const txl_paged* m, const txl_view* k, const t
 size_t paged_workspace(const txl_paged* m, int T, int n_e, int accumulate, char* base, PagedAttnParams* p)
 {
     const size_t pairs = static_cast<size_t>(m->B) * m->H, rows = pairs * T;
-    const size_t cap = static_cast<size_t>(m->max_pages) * m->page_len;
+    // scores of the pool's slots, or of all rows of the table, whichever are fewer
+    const size_t in_rows = static_cast<size_t>(m->B) * m->max_pages, pages = std::min(in_rows, static_cast<size_t>(m->n_pages));
     const int Dp = (m->D + 31) / 32 * 32, e_pitch = (n_e + 7) / 8 * 8;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -1358,7 +1359,7 @@ size_t paged_workspace(const txl_paged* m, int T, int n_e, int accumulate, char*
     // one bf16 token a sequence multiplies r beside the keys
     char* E = take(m->dtype == TXL_BF16 && T == 1 ? 0 : rows * e_pitch * 4);
     char* lse = accumulate ? take(rows * 4) : nullptr;
-    char* S = accumulate ? take(rows * cap * 4) : nullptr;
+    char* S = accumulate ? take(pages * m->page_len * m->H * T * 4) : nullptr;
     if (p) {
         p->now = reinterpret_cast<int4*>(now);
         p->part = reinterpret_cast<float*>(part);
@@ -1366,6 +1367,8 @@ size_t paged_workspace(const txl_paged* m, int T, int n_e, int accumulate, char*
         p->E = reinterpret_cast<float*>(E);
         p->lse = reinterpret_cast<float*>(lse);
         p->S = reinterpret_cast<float*>(S);
+        p->s_slots = static_cast<int>(pages) * m->page_len;
+        p->s_pool = pages < in_rows;
         p->Dp = Dp;
         p->n_e = n_e;
         p->e_pitch = e_pitch;
@@ -1421,7 +1424,7 @@ txl_status txl_paged_push_call(const txl_paged_push_args* a)
 size_t txl_rel_attn_paged_workspace_size(const txl_paged* mem, int T, int n_rows, int accumulate)
 {
     if (!mem || mem->B <= 0 || mem->H <= 0 || mem->D <= 0 || mem->D > 128 || T <= 0 || T > kDecodeMaxL || n_rows <= 0 || n_rows > (1 << 30) ||
-        mem->max_pages < 0 || mem->page_len <= 0)
+        mem->n_pages < 0 || mem->max_pages < 0 || mem->page_len <= 0)
         return 0;
     return paged_workspace(mem, T, n_rows, accumulate, nullptr, nullptr);
 }

@@ -391,7 +391,8 @@ struct PagedAttnParams {
     // workspace
     int4* now;                                  // [B] length, first query's position, queries
     float* E;                                   // [B][H][T][e_pitch] position terms, log2 domain
-    float* S;                                   // [B][H][T][cap] scores, log2 domain (accumulate)
+    float* S;                                   // [H][T][s_slots] scores, log2 domain (accumulate)
+    int s_slots, s_pool;                        // the pool's slots (s_pool), or those of all rows of the table in turn
     float* lse;                                 // [B][H][T] their log-sum-exp (accumulate)
     float* part; float* ml;                     // [2 kPagedMaxCtas][T][Dp], [..][T][2]: sums, maximum and weight
     int Dp;                                     // D rounded up to 32

@@ -238,8 +238,9 @@ __device__ __forceinline__ int page_at(const PagedParams& m, const Part& a, int 
 }
 
 // Where the tiles that a warp will come to lie: lane x knows that of the warp's x-th tile from `base` on (a page's number
-// and the row in it take divisions, which are made once in 32 tiles).
-template <int NW> struct Tiles {
+// and the row in it take divisions, which are made once in 32 - BACK tiles).  Asked for a tile further on, the lanes look again,
+// from BACK tiles of the warp before it on: those stay known.
+template <int NW, int BACK> struct Tiles {
     int base, mine;                // first position of the tile in m.pos, or -1 where there is no page
     int64_t mine_kv;               // and its first element of the part's head in m.k and m.v
 
@@ -253,15 +254,15 @@ template <int NW> struct Tiles {
         mine = page < 0 ? -1 : page * m.page_len + row;
         mine_kv = page < 0 ? -1 : page_row0(m, page, a.h) + static_cast<int64_t>(row) * m.ld;
     }
-    // of `tile` (a warp's own; no later one was asked for)
+    // of `tile` (a warp's own; none later than BACK behind it was asked for)
     __device__ __forceinline__ int pos(const PagedParams& m, const Part& a, int tile, int lane)
     {
-        if (tile - base >= 32 * NW) look(m, a, tile, lane);
+        if (tile - base >= 32 * NW) look(m, a, tile - BACK * NW, lane);
         return __shfl_sync(0xffffffffu, mine, (tile - base) / NW);
     }
     __device__ __forceinline__ int64_t kv(const PagedParams& m, const Part& a, int tile, int lane)
     {
-        if (tile - base >= 32 * NW) look(m, a, tile, lane);
+        if (tile - base >= 32 * NW) look(m, a, tile - BACK * NW, lane);
         return __shfl_sync(0xffffffffu, mine_kv, (tile - base) / NW);
     }
 };
@@ -271,6 +272,14 @@ __device__ __forceinline__ int term(const PagedAttnParams& p, int at, int pos)
 {
     return static_cast<int>(min(static_cast<unsigned>(at) - static_cast<unsigned>(pos), static_cast<unsigned>(p.n_e - 1)));
 }
+
+// The scores of a query of a sequence and head, and the place in them of slot s, which lies at `at` in m.pos.  (All sequences' slots
+// are the pool's: a table whose rows could each hold the pool takes no more room for scores than the pool has slots.)
+__device__ __forceinline__ float* score_row(const PagedAttnParams& p, int b, int h, int i)
+{
+    return p.S + (static_cast<int64_t>(h) * p.n.T + i) * p.s_slots + (p.s_pool ? 0 : b * p.cap);
+}
+__device__ __forceinline__ int score_slot(const PagedAttnParams& p, int s, int at) { return p.s_pool ? at : s; }
 
 __device__ __forceinline__ float finite_or_0(float m) { return m == kNone ? 0.f : m; }
 
@@ -406,7 +415,7 @@ template <int NC, bool W> struct OwnKey {
             page_error(m);
             return;
         }
-        if (W) p.S[(static_cast<int64_t>(a.b) * m.H + a.h) * p.cap + a.len] = s;
+        if (W) score_row(p, a.b, a.h, 0)[score_slot(p, a.len, page * m.page_len + row)] = s;
         if (a.h == 0) {
             m.pos[static_cast<int64_t>(page) * m.page_len + row] = a.first;
             m.weight[static_cast<int64_t>(page) * m.page_len + row] = 0.f;
@@ -460,7 +469,7 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     const bool owner = ONE && a.own && a.t1 == a.tiles && warp == NW - 1;
     if constexpr (ONE)
         if (owner) own_key.load(p, a, lane);
-    Tiles<NW> tiles;
+    Tiles<NW, W ? 2 : 0> tiles;                                // (two tiles ahead of the one whose scores are written)
     tiles.look(m, a, a.t0 + warp, lane);
     if (units < kUnits) {
         for (int x = lane; x < kStages<NC> * 2 * kPageUnit * (kUnits - units); x += 32) {
@@ -535,12 +544,9 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
     __syncthreads();
 
     BFrag<NC> q[NQ], qv;
-    float* S[NQ];
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        load_b<NC, false>(q[x], qs + (8 * x + g) * kQPitch<NC>, t);
-        S[x] = W ? p.S + ((static_cast<int64_t>(a.b) * m.H + a.h) * T + min(4 * x + t, T - 1)) * p.cap : nullptr;
-    }
+    for (int x = 0; x < NQ; ++x) load_b<NC, false>(q[x], qs + (8 * x + g) * kQPitch<NC>, t);
+    float* S = W ? score_row(p, a.b, a.h, t) + g : nullptr;    // (of query t, if there is one)
     if (ONE) load_b<NC, true>(qv, qs + (8 + g) * kQPitch<NC>, t);
     float o[NQ][2 * NC][4];
     float mx[NQ], sum[NQ];
@@ -611,14 +617,20 @@ __device__ __forceinline__ void part_bf16(const PagedAttnParams& p, const Part& 
                     for (int y = 0; y < 4; ++y) o[x][z][y] *= f;
             }
         }
+        if constexpr (W) {
+            const int slot = p.s_pool ? tiles.pos(m, a, tile, lane) : tile * kPageUnit;
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                if (live[x] && slot >= 0) {
+                    // (not behind the last slot: that is the new key's)
+                    float* to = S + static_cast<int64_t>(4 * x) * p.s_slots + slot;
+                    if (tile * kPageUnit + g < a.len) to[0] = s[x][0];
+                    if (tile * kPageUnit + 8 + g < a.len) to[8] = s[x][1];
+                }
+        }
         uint32_t b0[NQ], b1[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-            if (W && live[x]) {
-                // (not behind the last slot: that is the new key's)
-                if (tile * kPageUnit + g < a.len) S[x][tile * kPageUnit + g] = s[x][0];
-                if (tile * kPageUnit + 8 + g < a.len) S[x][tile * kPageUnit + 8 + g] = s[x][1];
-            }
             const float base = finite_or_0(mx[x]);
             const float p0 = mma::ex2(s[x][0] - base), p1 = mma::ex2(s[x][1] - base);
             sum[x] += p0 + p1;
@@ -688,7 +700,7 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
         }
         // u / 2 is the warp's tile, u % 2 its half.  Keys and values are copied two halves ahead, positions loaded two, position
         // terms one.
-        Tiles<NW> tiles;
+        Tiles<NW, 0> tiles;
         tiles.look(m, a, a.t0 + warp, lane);
         const int halves = a.t0 + warp < a.t1 ? 2 * ((a.t1 - a.t0 - warp + NW - 1) / NW) : 0;
         constexpr int kAhead = 0x7fffffff;                     // a slot that holds nothing is ahead of every query
@@ -711,8 +723,10 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
                 copy16(dst + kHalf * kHalfPitch<NC> * 4, v + from, bytes);
             }
         };
+        int place = 0;                                         // of the half whose positions were loaded last
         auto load_pos = [&](int u) {
             const int at = tiles.pos(m, a, tile_of(u), lane), row = u % 2 * kHalf + g;
+            place = at;
             return at >= 0 && tile_of(u) * kPageUnit + row < a.len ? m.pos[at + row] : kAhead;
         };
         const int64_t er = (static_cast<int64_t>(a.b) * m.H + a.h) * T + i0;
@@ -727,10 +741,11 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
             if (u < halves) copy(u, u);
             mma::cp_async_commit();
         }
-        int pos = kAhead;
+        int pos = kAhead, place0 = 0;                          // (place0: of the half at work; a tile has two halves)
         if (halves) {
             load_e(load_pos(0));
             pos = load_pos(1);
+            place0 = place;
         }
         __syncthreads();
         float o[NQ][NJ][4], mx[NQ], sum[NQ];
@@ -770,11 +785,15 @@ __device__ __forceinline__ void part_f32(const PagedAttnParams& p, const Part& a
                 load_e(pos);
                 if (u + 2 < halves) pos = load_pos(u + 2);
             }
-            if (W && t == 0) {
-                const int slot = tile_of(u) * kPageUnit + u % 2 * kHalf + g;
+            if constexpr (W) {
+                const int at = p.s_pool ? place0 : tile_of(u) * kPageUnit, row = u % 2 * kHalf + g;
+                if (u % 2) place0 = place;
+                if (t == 0 && at >= 0 && tile_of(u) * kPageUnit + row < a.len) {
+                    float* S = score_row(p, a.b, a.h, i0) + at + row;
 #pragma unroll
-                for (int x = 0; x < NQ; ++x)
-                    if (i0 + x < a.n && slot < a.len) p.S[(er + x) * p.cap + slot] = s[x];
+                    for (int x = 0; x < NQ; ++x)
+                        if (i0 + x < a.n) S[static_cast<int64_t>(x) * p.s_slots] = s[x];
+                }
             }
             // the maximum follows only where a score is far above it: a weight may be up to 2^kSlack
             constexpr float kSlack = 8.f;
@@ -902,7 +921,8 @@ __device__ __noinline__ void row_again(const PagedAttnParams& p, const Part& a, 
     for (int s0 = 0; s0 < (nan ? 0 : keys); s0 += (32 * NW)) {
         const int s = s0 + threadIdx.x;
         const float x = score(s);
-        if (p.accumulate && s < keys) p.S[row0 * p.cap + s] = x;
+        const int page = p.accumulate && s < keys ? page_of(m, a.b, s) : -1;
+        if (page >= 0) score_row(p, a.b, a.h, i)[score_slot(p, s, page * m.page_len + s % m.page_len)] = x;
         __syncthreads();
         // (a key that is seen and scores -inf weighs 0 as well; its values count as unseen)
         tot[threadIdx.x] = x == kNone ? 0.f : exp2f(x - top);
@@ -1241,15 +1261,16 @@ __global__ void __launch_bounds__(32 * kWeightWarps<V>) paged_weight_kernel(cons
     for (int s0 = blockIdx.x * kSlots; s0 < now.x; s0 += gridDim.x * kSlots) {
         const int s = s0 + V * lane;                           // (a lane's slots lie in one unit of 16, all of them in S)
         float sum[V] = {};
-        if (s < now.x)
+        const int page = s < now.x && p.s_pool ? page_of(m, b, s) : 0;
+        if (s < now.x && page >= 0)
             for (int h = warp; h < m.H; h += kWeightWarps<V>) {
                 const int64_t row = (static_cast<int64_t>(b) * m.H + h) * p.n.T;
-                const float* S = p.S + row * p.cap + s;
+                const float* S = score_row(p, b, h, 0) + score_slot(p, s, page * m.page_len + s % m.page_len);
 #pragma unroll 4
                 for (int i = 0; i < now.z; ++i) {
                     float y[V];
-                    if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(S + static_cast<int64_t>(i) * p.cap);
-                    else y[0] = S[static_cast<int64_t>(i) * p.cap];
+                    if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(S + static_cast<int64_t>(i) * p.s_slots);
+                    else y[0] = S[static_cast<int64_t>(i) * p.s_slots];
                     const float l = p.lse[row + i];
 #pragma unroll
                     for (int e = 0; e < V; ++e) sum[e] += y[e] == kNone ? 0.f : exp2f(y[e] - l);
