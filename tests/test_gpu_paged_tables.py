@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from paged_common import Pages, attend
-from test_gpu_paged import new
+from test_gpu_paged import check_memory, new
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,51 @@ def test_queries_past_a_sequences_count_are_not_read(txl, dtype, T):
     assert not torch.isnan(ws).any()
     ref.push(k.cpu(), v.cpu(), counts)
     check_against(mem, ref, out, ref.weight.clone(), torch.nan_to_num(q), u, vb, r, 59, counts)
+
+
+# ------------------------------------------------------------------------------------ long memories
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype,T,D", [(BF, 1, 8), (BF, 2, 8), (BF, 16, 8), (F, 1, 8), (F, 3, 8)])
+def test_shares_of_many_tiles_of_a_pair(txl, dtype, T, D, wide):
+    """Pairs enough that a block takes more than 32 tiles a warp of one pair: a warp looks for its pages again and again."""
+    B, H, n = 16, 16, 6016
+    ref = Pages(B, H, D, [n - b % 3 for b in range(B)], 64, dtype, room=T, order=True)
+    q, k, v, u, vb, r = new(B, T, H, D, dtype, 4, 400)
+    if wide:                                                   # (rows that could hold the pool: scores by the pool's slots)
+        ref.table = torch.cat((ref.table, torch.full((B, ref.k.shape[0] - ref.table.shape[1]), -1, dtype=torch.int32)), 1)
+    mem = ref.to_gpu(txl)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, mem, k, v, u.cuda(), vb.cuda(), r.cuda(), 400, 399, out, accumulate=True)
+    ref.push(k.cpu(), v.cpu())
+    check_against(mem, ref, out, ref.weight.clone(), q, u, vb, r, 399)
+
+
+@pytest.mark.parametrize("D,T", [(64, 1), (64, 4), (64, 6), (64, 16), (128, 1), (128, 5)])
+def test_shares_of_many_tiles_of_shared_pages(txl, D, T):
+    """The same for rings of other depths and blocks of other sizes: many sequences read one sequence's pages, of which each
+    attends with queries of its own."""
+    B, H, n = 48, 16, 6016
+    ref = Pages(1, H, D, [n], 64, BF, order=True)
+    mem1 = ref.to_gpu(txl)
+    wide = lambda x: x.cuda().expand(B, *x.shape[1:]).contiguous()
+    mem = txl.PagedMemory(mem1.k, mem1.v, mem1.pos, mem1.weight, wide(ref.table), wide(ref.length[None])[:, 0].contiguous(),
+                          wide(ref.next_pos[None])[:, 0].contiguous())
+    q, _, _, u, vb, r = new(B, T, H, D, BF, 4, 400)
+    out = torch.empty_like(q)
+    txl.rel_attn_paged(q, mem, None, None, u.cuda(), vb.cuda(), r.cuda(), 400, 399, out)
+    for b in (0, 17, B - 1):
+        want, tol, *_ = attend(ref, q[b:b + 1].cpu(), u, vb, r, 399)
+        assert ((out[b:b + 1].cpu().double() - want).abs() <= tol).all(), b
+    mem.check()
+
+
+def test_evict_more_than_shared_memory_holds(txl):
+    """70000 slots of a sequence: a block of the cluster makes keys anew that its shared memory has no room for."""
+    for recent, kind in ((1000, "random"), (0, "few")):
+        ref = Pages(2, 1, 8, [70001, 300], 64, BF, first=[80000, 300], seed=recent)
+        if kind == "few":
+            ref.weight.copy_((ref.weight * 3).floor())
+        mem = ref.to_gpu(txl)
+        txl.paged_evict(mem, 30011, recent)
+        ref.evict(30011, recent)
+        check_memory(mem, ref)
