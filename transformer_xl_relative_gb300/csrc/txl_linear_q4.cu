@@ -74,19 +74,20 @@ template <int NT, int MT, int SUB> struct Q4Stage {
 };
 template <int NT, int MT, int SUB> constexpr int kQ4Ring = kQ4Stages * static_cast<int>(sizeof(Q4Stage<NT, MT, SUB>));
 
-// A warp's entries of a block's `cols` columns and `rows` rows of Y that are not finite again, one after another, as the sum of x times
-// what the codes stand for in double precision: fp32 sums of 128 step x and of step x c (beyond fp32 from steps of 2.6e36 or x of
-// 2^112 on) may be infinite where Y is not.  A lane takes the four k of a word.
+// A warp's entries of a block's `cols` columns and `rows` rows of Y whose fp32 sums are not finite (they hold NaN) again, one after
+// another, as the sum of x times what the codes stand for in double precision: sums of 128 step x and of step x c (beyond fp32 from
+// steps of 2.6e36 or x of 2^112 on) may be infinite where Y is not.  A lane takes the four k of a word.
 __device__ __noinline__ void entries_again(const LinearQ4Params& p, int row0, int rows, int n0, int cols)
 {
     const int lane = threadIdx.x & 31, t = lane >> 2 & 3, s = lane & 3;
     const int kb_all = (p.k + kQ4K - 1) / kQ4K, groups = (p.k + p.group - 1) / p.group;
+    __syncwarp();                                              // the entries are the lanes' stores
     for (int i0 = threadIdx.x & ~31; i0 < rows * cols; i0 += blockDim.x)
         for (int i = i0; i < min(i0 + 32, rows * cols); ++i) {
             const int n = n0 + i % cols, nt = n / kQ4N, c = n % kQ4N, row = row0 + i / cols;
             if (n >= p.n) continue;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.y) + row * p.ld_y + n;
-            if (isfinite(__bfloat162float(*out))) continue;
+            if (!__hisnan(*out)) continue;
             const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ld_x;
             double y = 0.0;
 #pragma unroll 1
@@ -248,8 +249,8 @@ __global__ void __launch_bounds__(32 * kQ4MaxWarps<MT>) linear_q4_kernel(const _
         float s = 0.f;
 #pragma unroll 4
         for (int w = 0; w < warps; ++w) s += red[w][col][row];
+        if (!isfinite(s)) again = true, s = __int_as_float(0x7fc00000);        // (marks the entry)
         static_cast<__nv_bfloat16*>(p.y)[(row0 + row) * p.ld_y + n] = __float2bfloat16_rn(s);
-        again |= !isfinite(s);
     }
     if (__any_sync(0xffffffffu, again)) entries_again(p, row0, rows, nt0 * kQ4N, 16 * NT);
 }
