@@ -614,6 +614,7 @@ class PagedMemory:
             while end < most and row[end] >= 0:
                 end += 1
             self._rows.append(row[:end])
+        self._gaps = [-1 in row for row in self._rows]
         used = {p for row in self._rows for p in row}
         self._free = [p for p in range(n - 1, -1, -1) if p not in used]
 
@@ -671,6 +672,7 @@ class PagedMemory:
     def _give_back(self, b: int, kept: int) -> None:
         """Sequence b keeps its first `kept` pages; the others are free (but for those it shares)."""
         gone, self._rows[b] = self._rows[b][kept:], self._rows[b][:kept]
+        self._gaps[b] = self._gaps[b] and -1 in self._rows[b]
         used = {p for row in self._rows for p in row} if gone else ()
         self._free.extend(p for p in reversed(gone) if p >= 0 and p not in used)
 
@@ -826,7 +828,8 @@ def paged_evict(mem: PagedMemory, keep: int, recent: int = 0, workspace: torch.T
     st = _on_device(dev, lambda _: _lib().txl_paged_evict(ctypes.byref(mem._c), int(keep), int(recent), workspace.data_ptr(),
                                                           size, raw), None)
     check(st, "txl_paged_evict")
-    mem._room = [x if -1 in row else min(x, int(keep)) for x, row in zip(mem._room, mem._rows)]
+    keep = int(keep)
+    mem._room = [x if x < keep or gap else keep for x, gap in zip(mem._room, mem._gaps)]
     return mem
 
 
