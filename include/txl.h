@@ -637,6 +637,8 @@ txl_status txl_paged_push_call(const txl_paged_push_args* args);
  *              is the sum over the calls since it entered).
  *   workspace : device scratch, 16-byte aligned, of at least txl_rel_attn_paged_workspace_size bytes (TXL_ERR_WORKSPACE).
  *              Calls that share a workspace must not overlap on the GPU.
+ * T > 16: TXL_ERR_UNSUPPORTED.  More tokens over a memory that a sequence already has go through calls of 16; a first prompt takes
+ * txl_rel_attn_fwd and txl_paged_push.
  * The slots of all (sequence, head) pairs are cut into equal shares for the blocks, whatever the lengths.  bf16: mma.sync
  * products; scale log2(e) (q + u), scale log2(e) (q + v) and the weights of the softmax are held to 16 bits (two bf16
  * each).  f32: fp32 arithmetic on the CUDA cores.  The result does not depend on the order in which blocks run.  A key or value
@@ -710,7 +712,8 @@ txl_status txl_q4_expand(const txl_q4* w, void* W, int64_t ld_w, void* stream);
  * of the weights' bytes, for the projections of a generated token.  Y bf16 [m][ld_y], columns 0 .. n-1 are written.
  * Up to 128 rows, and more of an X that txl_linear does not take (misaligned): 16 rows at a time straight from the codes
  * (products of the bf16 x and the exact codes, fp32 sums, one rounding; an entry whose fp32 sums are not finite is computed
- * again in double precision, so that any finite X and weights give the product, slower).  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
+ * again in double precision, so that any finite X and weights give the product, slower).  Every 16 rows expand the codes anew: from
+ * about a hundred rows on txl_linear with the bf16 weights is faster.  Otherwise the weights are expanded to bf16 in the workspace and txl_linear's kernel runs.
  *   workspace : device scratch, 16-byte aligned, of at least txl_linear_q4_workspace_size(m, w) bytes (TXL_ERR_WORKSPACE;
  *            may be NULL when that is 0).  Calls that share a workspace must not overlap on the GPU.
  * Limits: m >= 0 (0: nothing to do), m <= 2^19; ld_x >= k, ld_y >= n.  err_flag as txl_linear.

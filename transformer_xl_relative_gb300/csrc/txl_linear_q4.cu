@@ -3,8 +3,8 @@
 //
 //     y = sum over groups ( step sum_k x_k c_k + lo sum_k x_k ),     c exact in bf16, sums in fp32
 //
-// 8 rows by 8192 x 8192 (36 MB): 10.9 us, 3.3 TB/s; bound by the ALU that makes operands of the codes (59 of its instructions for 16 columns
-// by 64 k; 75 % of its cycles on an SM that has a block).  4096 x 4096 4.7 us; 1024 x 1024 1.8 us, a launch.
+// 8 rows by 8192 x 8192 (36 MB): 10.9 us, 3.3 TB/s; bound by the ALU that makes operands of the codes (28 instructions for 16 columns by 64 k; 57 % of the
+// pipe's cycles over all SMs, 67 % on those that have a block).  4096 x 4096 4.9 us; one row by 1024 x 1024 2.1 us, a launch.
 #include <cuda_bf16.h>
 
 #include "txl_mma.cuh"

@@ -12,10 +12,10 @@
 //                        preparation: each key's row of r is multiplied beside the key, the new key is a part of its own
 //   paged_weight_kernel  (accumulate) 2^(score - log-sum-exp) summed over heads and queries
 //
-// Bound by HBM: K, V and a row of r once a key.  One query over 4096 positions of 8 sequences (H16 D64, 137 MB): 30.3 us, of which
+// Bound by HBM: K, V and a row of r once a key.  One query over 4096 positions of 8 sequences (H16 D64, 137 MB): 30.5 us, of which
 // 21 are the 6.3 TB/s of what further keys add (4096 -> 16384 positions: 403 MB in 64 us) and 9 the schedule (1.5), a part's
-// first tile (4.5: positions, then rows) and the join (2.5).  32 ragged sequences with summed weights (232 MB) 45.7 + 5.8 us, one
-// of 65536 positions with a row of r for each (403 MB) 76.4, 4 queries 35.3, 16 queries 53.8, five of d_head 128 over up to 2048
+// first tile (4.5: positions, then rows) and the join (2.5).  32 ragged sequences with summed weights (232 MB) 46 + 6 us, one
+// of 65536 positions with a row of r for each (403 MB) 76, 4 queries 35.8, 16 queries 54, five of d_head 128 over up to 2048
 // positions, with summed weights, 25.5.
 #include <cuda_bf16.h>
 
