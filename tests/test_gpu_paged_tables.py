@@ -114,6 +114,20 @@ def test_a_gap_behind_the_length_is_filled(txl):
     assert mem.length.tolist() == [40]
 
 
+def test_a_page_listed_twice_is_free_once(txl):
+    """Behind the length a row may list a page that it has already: the pool gets it back once."""
+    mem = txl.PagedMemory.empty(1, 4, 16, 2, 64)
+    table = torch.tensor([[2, 2, 1], [0, -1, -1]], dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    mem = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table, torch.tensor([9, 9], **i32), torch.tensor([9, 9], **i32))
+    assert mem.free_pages == 1
+    mem.trim()
+    assert mem.table[0].tolist() == [2, -1, -1] and mem.free_pages == 2
+    mem = txl.PagedMemory(mem.k, mem.v, mem.pos, mem.weight, table.copy_(torch.tensor([[2, 2, 1], [0, -1, -1]])), mem.length, mem.next_pos)
+    mem.release(0)
+    assert mem.free_pages == 3 and sorted(mem._free) == [1, 2, 3]
+
+
 # ------------------------------------------------------------------------------------ tables wider than the pool
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("T", [1, 3, 9])

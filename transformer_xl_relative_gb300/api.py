@@ -674,7 +674,7 @@ class PagedMemory:
         gone, self._rows[b] = self._rows[b][kept:], self._rows[b][:kept]
         self._gaps[b] = self._gaps[b] and -1 in self._rows[b]
         used = {p for row in self._rows for p in row} if gone else ()
-        self._free.extend(p for p in reversed(gone) if p >= 0 and p not in used)
+        self._free.extend(p for p in dict.fromkeys(reversed(gone)) if p >= 0 and p not in used)
 
     def release(self, b: int) -> None:
         """Sequence b has ended: it is empty, and its pages are free."""
